@@ -32,6 +32,7 @@ EXPORTED = (
     "cb_dw_separable_block_static", "cb_conv_path", "cb_debug_timeout_probe", "cb_autotune_conv",
     "cb_autotune_clear", "cb_autotune_entries", "cb_preprocess_stem_u8", "cb_dw_separable_block_fused",
     "cb_set_tuning", "cb_last_launch", "cb_debug_sample_coords", "cb_convert_weights_bf16", "cb_stage_body",
+    "cb_attention", "cb_cache_append", "cb_attention_decode", "cb_attention_decode_workspace",
 )
 STATIC_SCRATCH_BYTES = 16 * 1024 * 1024  # CB_STATIC_SCRATCH_BYTES
 
@@ -43,6 +44,36 @@ class CbTensor(ctypes.Structure):
         ("stride_n", ctypes.c_longlong), ("stride_h", ctypes.c_longlong),
         ("stride_w", ctypes.c_longlong), ("stride_c", ctypes.c_longlong),
         ("layout", ctypes.c_int), ("dtype", ctypes.c_int),
+    ]
+
+
+class CbHeads(ctypes.Structure):
+    _fields_ = [
+        ("data", ctypes.c_void_p),
+        ("batch", ctypes.c_int), ("len", ctypes.c_int), ("heads", ctypes.c_int), ("dim", ctypes.c_int),
+        ("stride_b", ctypes.c_longlong), ("stride_l", ctypes.c_longlong), ("stride_h", ctypes.c_longlong),
+        ("dtype", ctypes.c_int),
+    ]
+
+
+class CbScore(ctypes.Structure):
+    _fields_ = [
+        ("scale", ctypes.c_float), ("softcap", ctypes.c_float), ("slopes", ctypes.c_void_p),
+        ("causal", ctypes.c_int), ("q_offset", ctypes.c_int),
+        ("prefix_len", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
+        ("doc_q", ctypes.c_void_p), ("doc_k", ctypes.c_void_p),
+    ]
+
+
+class CbPagedCache(ctypes.Structure):
+    _fields_ = [
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+        ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int), ("heads", ctypes.c_int),
+        ("dim_k", ctypes.c_int), ("dim_v", ctypes.c_int),
+        ("k_stride_page", ctypes.c_longlong), ("k_stride_slot", ctypes.c_longlong), ("k_stride_head", ctypes.c_longlong),
+        ("v_stride_page", ctypes.c_longlong), ("v_stride_slot", ctypes.c_longlong), ("v_stride_head", ctypes.c_longlong),
+        ("table", ctypes.c_void_p), ("batch", ctypes.c_int), ("max_pages", ctypes.c_int),
+        ("table_stride", ctypes.c_longlong), ("dtype", ctypes.c_int),
     ]
 
 
@@ -72,6 +103,7 @@ def load():
             lib = ctypes.CDLL(_LIB_PATH)
             P, I, F, LL, S = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_longlong, ctypes.c_size_t
             T = ctypes.POINTER(CbTensor)
+            H, SC, PC = ctypes.POINTER(CbHeads), ctypes.POINTER(CbScore), ctypes.POINTER(CbPagedCache)
             sig = {
                 "cb_fold_bn": [P, P, P, P, F, I, P, P],
                 "cb_repack_weights": [P, I, I, I, I, I, P],
@@ -83,6 +115,10 @@ def load():
                 "cb_avgpool_linear": [T, P, P, I, P, P],
                 "cb_preprocess_u8": [P, I, I, I, LL, P, I, I, P],
                 "cb_preprocess_u8_three_pass": [P, I, I, I, LL, P, P, P, I, I, P],
+                "cb_attention": [H, H, H, SC, H, P],
+                "cb_cache_append": [H, H, P, P, PC, P],
+                "cb_attention_decode_workspace": [H, PC, ctypes.POINTER(S)],
+                "cb_attention_decode": [H, PC, P, P, F, F, P, H, P, S, P],
                 "cb_get_device_error": [P],
                 "cb_last_cuda_error": [],
                 "cb_set_kernel_policy": [I],
@@ -151,6 +187,77 @@ def nchw(t) -> CbTensor:
     N, C, H, W = t.shape
     sn, sc, sh, sw = t.stride()
     return CbTensor(t.data_ptr(), N, H, W, C, sn, sh, sw, sc, LAYOUT_NCHW, dtype_code(t))
+
+
+def heads(t) -> CbHeads:
+    """View of a torch tensor indexed [B, L, H, D] (any strides, unit stride along D)."""
+    B, L, H, D = t.shape
+    sb, sl, sh, sd = t.stride()
+    if sd != 1 and D > 1:
+        raise ValueError("the last dim of a [B, L, H, D] view is contiguous")
+    return CbHeads(t.data_ptr(), B, L, H, D, sb, sl, sh, dtype_code(t))
+
+
+def _heads1(t) -> CbHeads:
+    """View of a torch tensor indexed [B, H, D]: one token per sequence."""
+    B, H, D = t.shape
+    sb, sh, sd = t.stride()
+    if sd != 1 and D > 1:
+        raise ValueError("the last dim of a [B, H, D] view is contiguous")
+    return CbHeads(t.data_ptr(), B, 1, H, D, sb, 0, sh, dtype_code(t))
+
+
+def _device_array(t, name, dtype, shape):
+    """Pointer of a contiguous device tensor of this dtype and shape (None stays None)."""
+    if t is None:
+        return None
+    if not t.is_cuda or str(t.dtype) != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous {dtype} device tensor of shape {shape}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+class Score:
+    """The score rule of `attention` (cb_score): how q.k becomes a score and which keys a query sees.
+
+    softcap > 0 caps scores by softcap * tanh(s / softcap); slopes: float32 [Hq], the bias
+    -slopes[h] * |i + q_offset - j|; causal, with prefix_len (int32 [B]) keys that every query sees;
+    kv_len: int32 [B]; doc_q / doc_k: int32 [B, Lq] / [B, Lk], negative = padding.  Keeps the tensors."""
+
+    def __init__(self, scale, softcap=0.0, slopes=None, causal=False, q_offset=0, prefix_len=None, kv_len=None,
+                 doc_q=None, doc_k=None):
+        self.scale, self.softcap, self.causal, self.q_offset = float(scale), float(softcap), bool(causal), int(q_offset)
+        self.slopes, self.prefix_len, self.kv_len, self.doc_q, self.doc_k = slopes, prefix_len, kv_len, doc_q, doc_k
+
+    def view(self, batch, lq, lk, hq) -> CbScore:
+        """The rule for [batch, lq, hq, .] queries over lk keys; checks the arrays' shapes."""
+        return CbScore(self.scale, self.softcap, _device_array(self.slopes, "slopes", "torch.float32", (hq,)),
+                       int(self.causal), self.q_offset,
+                       _device_array(self.prefix_len, "prefix_len", "torch.int32", (batch,)),
+                       _device_array(self.kv_len, "kv_len", "torch.int32", (batch,)),
+                       _device_array(self.doc_q, "doc_q", "torch.int32", (batch, lq)),
+                       _device_array(self.doc_k, "doc_k", "torch.int32", (batch, lk)))
+
+
+class PagedCache:
+    """A paged key-value cache (cb_paged_cache): k_pages [P, page, H, Dk] and v_pages [P, page, H, Dv]
+    (any strides, the last dim contiguous), table int32 [B, max_pages] (rows contiguous): token j of
+    sequence b lies in page table[b, j // page], slot j % page.  Holds the tensors; the table's
+    contents may change between calls."""
+
+    def __init__(self, k_pages, v_pages, table):
+        if k_pages.shape[:3] != v_pages.shape[:3] or k_pages.dtype != v_pages.dtype:
+            raise ValueError("k_pages and v_pages: the same pages, slots, heads and dtype")
+        if k_pages.stride(3) != 1 or v_pages.stride(3) != 1:
+            raise ValueError("the last dim of the pages is contiguous")
+        if str(table.dtype) != "torch.int32" or table.dim() != 2 or not table.is_cuda or \
+                (table.shape[1] > 1 and table.stride(1) != 1):
+            raise ValueError("table: an int32 device tensor [B, max_pages] with contiguous rows")
+        self.k_pages, self.v_pages, self.table = k_pages, v_pages, table
+        P, page, H, Dk = k_pages.shape
+        self.view = CbPagedCache(k_pages.data_ptr(), v_pages.data_ptr(), P, page, H, Dk, v_pages.shape[3],
+                                 *k_pages.stride()[:3], *v_pages.stride()[:3], table.data_ptr(), table.shape[0],
+                                 table.shape[1], table.stride(0), dtype_code(k_pages))
 
 
 # ----------------------------------------------------------- host helpers
@@ -353,6 +460,51 @@ def avgpool_linear(x, fc_w, fc_b, out, stream=None):
     xv = nhwc(x)
     _check(load().cb_avgpool_linear(ctypes.byref(xv), fc_w.data_ptr(), fc_b.data_ptr(), fc_w.shape[0],
                                     out.data_ptr(), _stream_ptr(stream)), "cb_avgpool_linear")
+    return out
+
+
+def attention(q, k, v, out, score, stream=None):
+    """cb_attention on torch CUDA tensors: q [B, Lq, Hq, Dk], k [B, Lk, Hkv, Dk], v [B, Lk, Hkv, Dv],
+    out [B, Lq, Hq, Dv] (any strides, the last dim contiguous; all float32 or all bfloat16); score: a
+    Score.  Slices of a projection's output are read in place."""
+    qv, kv, vv, ov = heads(q), heads(k), heads(v), heads(out)
+    sv = score.view(qv.batch, qv.len, kv.len, qv.heads)
+    _check(load().cb_attention(ctypes.byref(qv), ctypes.byref(kv), ctypes.byref(vv), ctypes.byref(sv),
+                               ctypes.byref(ov), _stream_ptr(stream)), "cb_attention")
+    return out
+
+
+def cache_append(k_new, v_new, cache, pos, count=None, stream=None):
+    """cb_cache_append: tokens t < count[b] of k_new [B, T, H, Dk] and v_new [B, T, H, Dv] become tokens
+    pos[b] + t of the cache's sequences.  pos, count: int32 [B] (count None: all T)."""
+    kv, vv = heads(k_new), heads(v_new)
+    B = kv.batch
+    _check(load().cb_cache_append(ctypes.byref(kv), ctypes.byref(vv), _device_array(pos, "pos", "torch.int32", (B,)),
+                                  _device_array(count, "count", "torch.int32", (B,)), ctypes.byref(cache.view),
+                                  _stream_ptr(stream)), "cb_cache_append")
+
+
+def attention_decode_workspace(q, cache) -> int:
+    """cb_attention_decode_workspace: bytes of scratch for q [B, Hq, Dk] over this cache."""
+    qv = _heads1(q)
+    n = ctypes.c_size_t(0)
+    _check(load().cb_attention_decode_workspace(ctypes.byref(qv), ctypes.byref(cache.view), ctypes.byref(n)),
+           "cb_attention_decode_workspace")
+    return n.value
+
+
+def attention_decode(q, cache, length, out, workspace, scale, softcap=0.0, slopes=None, first=None, stream=None):
+    """cb_attention_decode: one new token per sequence, q [B, Hq, Dk] and out [B, Hq, Dv], over the cache's
+    tokens first[b] <= j < length[b] (int32 [B]; first None: 0), the query at position length[b] - 1.
+    workspace: a uint8 device tensor of attention_decode_workspace bytes."""
+    qv, ov = _heads1(q), _heads1(out)
+    B = qv.batch
+    _check(load().cb_attention_decode(ctypes.byref(qv), ctypes.byref(cache.view),
+                                      _device_array(length, "length", "torch.int32", (B,)),
+                                      _device_array(first, "first", "torch.int32", (B,)), scale, softcap,
+                                      _device_array(slopes, "slopes", "torch.float32", (qv.heads,)), ctypes.byref(ov),
+                                      workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                      _stream_ptr(stream)), "cb_attention_decode")
     return out
 
 

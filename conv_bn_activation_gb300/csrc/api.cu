@@ -17,6 +17,7 @@
 #include <vector>
 
 #include "cb.h"
+#include "host_util.h"
 #include "internal.h"
 #include "launch_util.h"
 
@@ -1205,6 +1206,32 @@ cb_status run_direct(const cb_tensor* x, const float* w, const Epilogue& ep, int
 }  // namespace
 
 // =============================================================================
+namespace cb {
+
+cb_status host_device(int* sms, int** err) {
+  DeviceInfo* dev = nullptr;
+  const cb_status st = current_device(&dev);
+  if (st != CB_OK) return st;
+  *sms = dev->sms;
+  *err = dev->err;
+  return CB_OK;
+}
+
+cb_status host_cuda_fail(cudaError_t e) { return cuda_fail(e); }
+
+uint64_t host_timeout_ns() { return timeout_ns(); }
+
+bool host_map_bf16(CUtensorMap* out, const void* ptr, const cuuint64_t* dims, const cuuint64_t* strides_bytes,
+                   const cuuint32_t* box) {
+  const cuuint32_t ones[4] = {1, 1, 1, 1};
+  return encode_tiled() != nullptr &&
+         encode_tiled()(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides_bytes, box, ones,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace cb
+
 extern "C" {
 
 cb_status cb_fold_bn(const float* gamma, const float* beta, const float* mean, const float* var, float eps, int C,

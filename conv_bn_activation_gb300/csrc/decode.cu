@@ -1,0 +1,305 @@
+// Attention of one new token per sequence over a paged cache (cb_attention_decode):
+// the CUDA-core kernel and the join of split sequences.
+//
+// Bound by HBM: every key and value of the batch is read once, and one
+// query's 4 FLOP per element are far below the FMA rate until many heads
+// share a key head.  decode_common.cuh says how tokens are dealt.
+#include "decode_common.cuh"
+#include "launch_util.h"
+#include "ptx.cuh"
+
+namespace cb {
+
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kHeads = kDecodeSimtHeads;
+
+// Piece of a run: sequence, item within it, tiles, and how it relates to its item.
+struct Piece {
+  int b, item;           // item = key head * chunks + chunk
+  int tile0, tiles;      // absolute tile of the sequence
+  bool starts, ends;     // holds the item's first / last tile
+};
+
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kThreads) decode_simt_kernel(DecodeArgs a) {
+  extern __shared__ __align__(16) float smem[];
+  const int ldk = (a.dk + 3) / 4 * 4 + 4;
+  float* Ks = smem;                           // [64][ldk]
+  float* Qs = Ks + kDecodeTile * ldk;         // [kHeads][ldk]
+  float* Ps = Qs + kHeads * ldk;              // [64][kHeads]
+  float* red = Ps + kDecodeTile * kHeads;     // [kHeads][dv] at the end of a piece
+  unsigned* prefix = reinterpret_cast<unsigned*>(red + kHeads * a.dv);
+  __shared__ float ms[kHeads], ls[kHeads], corr_s[kHeads];
+  __shared__ int page_s[kDecodeTile], slot_s[kDecodeTile];
+
+  pdl_wait();
+  pdl_launch_dependents();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  tile_prefix(a, prefix);
+  const int per_seq = a.Hkv * a.chunks;
+  const long long total = static_cast<long long>(prefix[a.B]) * per_seq;
+  const Run run{total, min(static_cast<long long>(gridDim.x), max(total, 1LL))};
+  const long long cta = blockIdx.x;
+  if (tid == 0) a.record[2 * cta] = -1;
+  // Sequences without a visible token: zeros, dealt over the CTAs.
+  for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+    if (prefix[b + 1] != prefix[b]) continue;
+    T* o = static_cast<T*>(a.o) + b * a.os_b;
+    for (int e = tid; e < a.Hq * a.dv; e += kThreads) o[e / a.dv * a.os_h + e % a.dv] = from_f32<T>(0.f);
+  }
+  if (cta >= run.ctas || total == 0) return;
+  const long long end = run.begin(cta + 1);
+  long long at = run.begin(cta);
+  int b = 0;
+  {  // the sequence that holds tile `at`
+    int hi = a.B;
+    while (hi - b > 1) {
+      const int mid = (b + hi) >> 1;
+      if (static_cast<long long>(prefix[mid]) * per_seq <= at) b = mid;
+      else hi = mid;
+    }
+  }
+  // threads of one value row: lanes_v of 4 values each
+  int lanes_v = 1;
+  while (lanes_v * 4 < a.dv) lanes_v <<= 1;
+  const int slots = kThreads / lanes_v, vs = tid / lanes_v, vd = (tid % lanes_v) * 4;
+
+  while (at < end) {
+    while (static_cast<long long>(prefix[b + 1]) * per_seq <= at) ++b;
+    const SeqSpan sp = seq_span(a, b);
+    const long long in_seq = at - static_cast<long long>(prefix[b]) * per_seq;
+    const int item = static_cast<int>(in_seq / sp.tiles), off = static_cast<int>(in_seq - static_cast<long long>(item) * sp.tiles);
+    const int tiles = static_cast<int>(min(static_cast<long long>(sp.tiles - off), end - at));
+    const bool starts = off == 0, ends = off + tiles == sp.tiles;
+    const int hk = item / a.chunks, h0 = hk * a.group + (item % a.chunks) * kHeads;
+    const int heads = min(kHeads, (hk + 1) * a.group - h0);
+
+    __syncthreads();
+    for (int e = tid; e < kHeads * ldk; e += kThreads) {
+      const int g = e / ldk, d = e - g * ldk;
+      Qs[e] = g < heads && d < a.dk ? to_f32(static_cast<const T*>(a.q)[b * a.qs_b + (h0 + g) * a.qs_h + d]) : 0.f;
+    }
+    if (tid < kHeads) ms[tid] = kNegInf, ls[tid] = 0.f;
+    float acc[kHeads][4];
+#pragma unroll
+    for (int g = 0; g < kHeads; ++g)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) acc[g][c] = 0.f;
+
+    for (int t = 0; t < tiles; ++t) {
+      const int j0 = (sp.t0 + off + t) * kDecodeTile;
+      __syncthreads();
+      if (tid < kDecodeTile) {
+        const int j = j0 + tid;
+        page_s[tid] = j >= sp.lo && j < sp.hi ? token_page(a, b, j, &slot_s[tid]) : -1;
+      }
+      __syncthreads();
+      {  // keys
+        const int per = VEC ? static_cast<int>(16 / sizeof(T)) : 1;
+        const int pieces = VEC ? a.dk / per : ldk - 4;
+        for (int e = tid; e < kDecodeTile * pieces; e += kThreads) {
+          const int r = e / pieces, d = (e - r * pieces) * per;
+          const int page = page_s[r];
+          const T* src = static_cast<const T*>(a.cache.k) + page * a.cache.ks_p + slot_s[r] * a.cache.ks_t + hk * a.cache.ks_h + d;
+          if constexpr (VEC && sizeof(T) == 4) {
+            *reinterpret_cast<float4*>(Ks + r * ldk + d) = page < 0 ? make_float4(0.f, 0.f, 0.f, 0.f) : *reinterpret_cast<const float4*>(src);
+          } else if constexpr (VEC) {
+            const uint4 w = page < 0 ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4*>(src);
+            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              Ks[r * ldk + d + 2 * i] = __uint_as_float(u[i] << 16);
+              Ks[r * ldk + d + 2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+            }
+          } else {
+            Ks[r * ldk + d] = page < 0 || d >= a.dk ? 0.f : to_f32(*src);
+          }
+        }
+      }
+      __syncthreads();
+      {  // scores: thread = (key, every second head)
+        const int key = tid & (kDecodeTile - 1), half = tid >> 6;
+        float dot[kHeads / 2];
+#pragma unroll
+        for (int g = 0; g < kHeads / 2; ++g) dot[g] = 0.f;
+        for (int d = 0; d < ldk - 4; d += 4) {
+          const float4 kv = *reinterpret_cast<const float4*>(Ks + key * ldk + d);
+#pragma unroll
+          for (int g = 0; g < kHeads / 2; ++g) {
+            const float4 qv = *reinterpret_cast<const float4*>(Qs + (2 * g + half) * ldk + d);
+            dot[g] = fmaf(qv.x, kv.x, fmaf(qv.y, kv.y, fmaf(qv.z, kv.z, fmaf(qv.w, kv.w, dot[g]))));
+          }
+        }
+        const int dist = sp.len - 1 - (j0 + key);
+#pragma unroll
+        for (int g = 0; g < kHeads / 2; ++g) {
+          const int hd = 2 * g + half;
+          float x = dot[g] * a.scale;
+          if (a.softcap > 0.f) x = a.softcap * tanhf(x / a.softcap);
+          const float slope = a.slopes && hd < heads ? a.slopes[h0 + hd] * kLog2e : 0.f;
+          Ps[key * kHeads + hd] = page_s[key] < 0 ? kNegInf : fmaf(-slope, static_cast<float>(dist), x * kLog2e);
+        }
+      }
+      __syncthreads();
+      for (int g = warp; g < heads; g += kThreads / 32) {
+        const float x0 = Ps[lane * kHeads + g], x1 = Ps[(lane + 32) * kHeads + g];
+        float mx = fmaxf(x0, x1);
+        for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o));
+        const float m = ms[g], mn = fmaxf(m, mx), mu = mn == kNegInf ? 0.f : mn;
+        const float p0 = exp2_approx(x0 - mu), p1 = exp2_approx(x1 - mu);
+        float sum = p0 + p1;
+        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+        Ps[lane * kHeads + g] = p0;
+        Ps[(lane + 32) * kHeads + g] = p1;
+        __syncwarp();
+        if (lane == 0) {
+          const float corr = exp2_approx(m - mu);
+          corr_s[g] = corr;
+          ms[g] = mn;
+          ls[g] = ls[g] * corr + sum;
+        }
+      }
+      __syncthreads();
+#pragma unroll
+      for (int g = 0; g < kHeads; ++g) {
+        const float corr = g < heads ? corr_s[g] : 1.f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[g][c] *= corr;
+      }
+      if (vd < a.dv) {
+        for (int key = vs; key < kDecodeTile; key += slots) {
+          const int page = page_s[key];
+          if (page < 0) continue;
+          const T* src = static_cast<const T*>(a.cache.v) + page * a.cache.vs_p + slot_s[key] * a.cache.vs_t + hk * a.cache.vs_h + vd;
+          float v[4];
+          if constexpr (VEC && sizeof(T) == 4) {
+            const float4 w = *reinterpret_cast<const float4*>(src);
+            v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
+          } else if constexpr (VEC) {
+            const uint2 w = *reinterpret_cast<const uint2*>(src);
+            v[0] = __uint_as_float(w.x << 16), v[1] = __uint_as_float(w.x & 0xffff0000u);
+            v[2] = __uint_as_float(w.y << 16), v[3] = __uint_as_float(w.y & 0xffff0000u);
+          } else {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) v[c] = vd + c < a.dv ? to_f32(src[c]) : 0.f;
+          }
+          const float4 pa = *reinterpret_cast<const float4*>(Ps + key * kHeads);
+          const float4 pb = *reinterpret_cast<const float4*>(Ps + key * kHeads + 4);
+          const float p[kHeads] = {pa.x, pa.y, pa.z, pa.w, pb.x, pb.y, pb.z, pb.w};
+#pragma unroll
+          for (int g = 0; g < kHeads; ++g)
+            if (g < heads)
+#pragma unroll
+              for (int c = 0; c < 4; ++c) acc[g][c] = fmaf(p[g], v[c], acc[g][c]);
+        }
+      }
+    }
+    // The value slots' sums, in slot order.
+    for (int s = 0; s < slots; ++s) {
+      __syncthreads();
+      if (vs == s) {
+#pragma unroll
+        for (int g = 0; g < kHeads; ++g)
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (vd + c < a.dv) red[g * a.dv + vd + c] = (s ? red[g * a.dv + vd + c] : 0.f) + acc[g][c];
+      }
+    }
+    __syncthreads();
+    if (starts && ends) {
+      for (int e = tid; e < heads * a.dv; e += kThreads) {
+        const int g = e / a.dv, d = e - g * a.dv;
+        static_cast<T*>(a.o)[b * a.os_b + (h0 + g) * a.os_h + d] = from_f32<T>(ls[g] == 0.f ? 0.f : red[e] / ls[g]);
+      }
+    } else {
+      float* part = a.part + (2 * cta + (starts ? 1 : 0)) * part_floats(kHeads, a.dv);
+      for (int e = tid; e < heads * a.dv; e += kThreads) part[2 * kHeads + e] = red[e];
+      if (tid < heads) part[tid] = ms[tid], part[kHeads + tid] = ls[tid];
+      if (starts && tid == 0) {
+        const long long last = at - off + sp.tiles - 1;  // the item's last tile
+        a.record[2 * cta] = b * per_seq + item;
+        a.record[2 * cta + 1] = static_cast<int>(run.owner(last) - cta + 1);
+      }
+    }
+    at += tiles;
+  }
+}
+
+// One item that several CTAs shared: the CTA that holds its start (slot 1)
+// and the ones after it (slot 0).  out = sum w o / sum w l, w = 2^(m - max m).
+template <typename T>
+__global__ void __launch_bounds__(256) decode_join_kernel(DecodeArgs a, int part_heads) {
+  __shared__ __align__(16) float sum_s[8][128];
+  __shared__ float l_s[8];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int cta = blockIdx.x;
+  const int rec = a.record[2 * cta], pieces = a.record[2 * cta + 1];
+  if (rec < 0) return;
+  const int per_seq = a.Hkv * a.chunks;
+  const int b = rec / per_seq, item = rec - b * per_seq;
+  const int hk = item / a.chunks, h0 = hk * a.group + (item % a.chunks) * part_heads;
+  const int heads = min(part_heads, (hk + 1) * a.group - h0), g = blockIdx.y;
+  if (g >= heads) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const size_t pf = part_floats(part_heads, a.dv);
+  auto part = [&](int i) { return a.part + (i == 0 ? 2 * static_cast<size_t>(cta) + 1 : 2 * (static_cast<size_t>(cta) + i)) * pf; };
+  float m = kNegInf;
+  for (int i = lane; i < pieces; i += 32) m = fmaxf(m, part(i)[g]);
+  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+  const float mu = m == kNegInf ? 0.f : m;
+  float l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int i = warp; i < pieces; i += 8) {
+    const float* p = part(i);
+    const float w = exp2_approx(p[g] - mu);
+    l = fmaf(w, p[part_heads + g], l);
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if (lane + 32 * c < a.dv) acc[c] = fmaf(w, p[2 * part_heads + g * a.dv + lane + 32 * c], acc[c]);
+  }
+  for (int c = 0; c < 4; ++c) sum_s[warp][lane + 32 * c] = acc[c];
+  if (lane == 0) l_s[warp] = l;
+  __syncthreads();
+  if (threadIdx.x < a.dv) {
+    float o = 0.f, ll = 0.f;
+    for (int w = 0; w < 8; ++w) o += sum_s[w][threadIdx.x], ll += l_s[w];
+    static_cast<T*>(a.o)[b * a.os_b + (h0 + g) * a.os_h + threadIdx.x] = from_f32<T>(ll == 0.f ? 0.f : o / ll);
+  }
+}
+
+size_t simt_smem(int dk, int dv, int B) {
+  const size_t ldk = (dk + 3) / 4 * 4 + 4;
+  return sizeof(float) * ((kDecodeTile + kHeads) * ldk + kDecodeTile * kHeads + static_cast<size_t>(kHeads) * dv) +
+         sizeof(unsigned) * (B + 1);
+}
+
+template <typename T, bool VEC>
+cudaError_t launch_simt(const DecodeArgs& a, cudaStream_t s) {
+  const size_t smem = simt_smem(a.dk, a.dv, a.B);
+  cudaError_t e = smem_attr_once<decode_simt_kernel<T, VEC>>(smem);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(decode_simt_kernel<T, VEC>, dim3(a.ctas), dim3(kThreads), smem, s, a);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(decode_join_kernel<T>, dim3(a.ctas, a.group < kHeads ? a.group : kHeads), dim3(256), 0, s, a, kHeads);
+}
+
+}  // namespace
+
+size_t decode_workspace_bytes(int ctas, int heads, int dv) {
+  return sizeof(float) * 2 * ctas * part_floats(heads, dv) + sizeof(int) * 2 * ctas;
+}
+
+int decode_ctas(bool bf16, bool vec, int sms, int dk, int dv) {
+  (void)bf16, (void)vec, (void)dk, (void)dv;
+  return 4 * sms;
+}
+
+cudaError_t launch_decode(const DecodeArgs& a, bool bf16, bool vec, cudaStream_t s) {
+  if (bf16) return vec ? launch_simt<__nv_bfloat16, true>(a, s) : launch_simt<__nv_bfloat16, false>(a, s);
+  return vec ? launch_simt<float, true>(a, s) : launch_simt<float, false>(a, s);
+}
+
+}  // namespace cb

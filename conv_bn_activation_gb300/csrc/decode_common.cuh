@@ -1,0 +1,89 @@
+// How the decode kernels deal the cache's tokens over the GPU.
+//
+// An item is one sequence's tokens [first, length) for the query heads of one
+// key head (at most a kernel's head count of them).  Items are cut at
+// absolute multiples of kDecodeTile tokens, and the tiles of all items, in
+// order of (sequence, item), are dealt to the CTAs in equal runs: a CTA walks
+// the end of one item, whole items, and the start of another.  Whatever the
+// lengths, every CTA reads the same share of the cache, and only the item a
+// run starts or ends inside needs joining: two partial results per CTA.
+#pragma once
+
+#include "attention_common.cuh"
+
+namespace cb {
+
+constexpr int kDecodeTile = 64;
+constexpr int kDecodeMaxBatch = 4096;
+
+struct SeqSpan {
+  int lo, hi;      // visible tokens
+  int t0, tiles;   // first tile, tiles
+  int len;         // query at position len - 1
+};
+__device__ __forceinline__ SeqSpan seq_span(const DecodeArgs& a, int b) {
+  SeqSpan s;
+  const long long room = static_cast<long long>(a.cache.max_pages) * a.cache.page_size;
+  s.len = static_cast<int>(min(static_cast<long long>(max(a.length[b], 0)), room));
+  s.lo = a.first ? max(a.first[b], 0) : 0;
+  s.hi = s.len;
+  s.t0 = s.lo / kDecodeTile;
+  s.tiles = s.lo < s.hi ? (s.hi + kDecodeTile - 1) / kDecodeTile - s.t0 : 0;
+  return s;
+}
+
+// Exclusive prefix sums of the sequences' tiles into prefix[0..B] (shared
+// memory), by every thread of the CTA; ends with a barrier.
+__device__ __forceinline__ void tile_prefix(const DecodeArgs& a, unsigned* prefix) {
+  __shared__ unsigned warp_sum[32];
+  const int tid = threadIdx.x, n = blockDim.x, lane = tid & 31, warp = tid >> 5, warps = n >> 5;
+  const int per = (a.B + n - 1) / n, b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
+  unsigned sum = 0;
+  for (int b = b0; b < b1; ++b) sum += seq_span(a, b).tiles;
+  unsigned inc = sum;
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned up = __shfl_up_sync(~0u, inc, o);
+    if (lane >= o) inc += up;
+  }
+  if (lane == 31) warp_sum[warp] = inc;
+  __syncthreads();
+  unsigned base = inc - sum;
+  for (int w = 0; w < warps; ++w)
+    if (w < warp) base += warp_sum[w];
+  for (int b = b0; b < b1; ++b) {
+    prefix[b] = base;
+    base += seq_span(a, b).tiles;
+  }
+  if (b1 == a.B && b0 < b1) prefix[a.B] = base;
+  __syncthreads();
+}
+
+// The run of CTA c: tiles [begin, end) of the `total` dealt ones.
+struct Run {
+  long long total, ctas;
+  __device__ __forceinline__ long long begin(long long c) const { return c * total / ctas; }
+  // the CTA whose run holds tile x
+  __device__ __forceinline__ long long owner(long long x) const {
+    long long c = x * ctas / total;
+    while (c + 1 < ctas && begin(c + 1) <= x) ++c;
+    while (begin(c) > x) --c;
+    return c;
+  }
+};
+
+// Floats of one partial result: per head m, l, then dv unnormalised sums.
+__host__ __device__ inline size_t part_floats(int heads, int dv) { return static_cast<size_t>(heads) * (dv + 2); }
+
+// Where token j of sequence b lies: its page, or -1 (and the error recorded).
+__device__ __forceinline__ int token_page(const DecodeArgs& a, int b, int j, int* slot) {
+  const int pg = j / a.cache.page_size;
+  *slot = j - pg * a.cache.page_size;
+  const int page = a.cache.table[b * a.cache.table_stride + pg];
+  if (page < 0 || page >= a.cache.num_pages) {
+    atomicCAS(a.err, 0, 1);  // CB_ERR_INVALID_ARG
+    return -1;
+  }
+  return page;
+}
+
+}  // namespace cb

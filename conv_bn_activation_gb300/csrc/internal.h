@@ -300,6 +300,78 @@ cudaError_t launch_preprocess_resize(const uint8_t* src, int n, int hs, int ws, 
 cudaError_t launch_preprocess_normalize(const uint8_t* in, long long count, float* out, cudaStream_t s);
 cudaError_t launch_preprocess_layout(const float* in, int n, int h, int w, float* out, cudaStream_t s);
 
+// ---------------------------------------------------------------- attention
+// cb_attention's views and score rule (cb.h), strides in elements, last dim contiguous.
+struct AttnArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  void* o;
+  long long qs_b, qs_l, qs_h;
+  long long ks_b, ks_l, ks_h;
+  long long vs_b, vs_l, vs_h;
+  long long os_b, os_l, os_h;
+  int B, Lq, Lk, Hq, group, dk, dv;  // group = Hq / Hkv
+  float scale, softcap;
+  const float* slopes;
+  int causal, q_offset;
+  const int* prefix_len;
+  const int* kv_len;
+  const int* doc_q;
+  const int* doc_k;
+  int* err;
+  uint64_t timeout_ns;
+};
+// CUDA cores, fp32 arithmetic, any strides (attention_simt.cu).  vec: every
+// row of q, k, v and out is made of whole 16-byte pieces.
+cudaError_t launch_attn_simt(const AttnArgs& a, bool bf16, bool vec, int sms, cudaStream_t s);
+
+// The paged cache as the kernels read it (cb_paged_cache); page_div divides by page_size.
+struct PagedArgs {
+  void* k;
+  void* v;
+  long long ks_p, ks_t, ks_h;
+  long long vs_p, vs_t, vs_h;
+  const int* table;
+  long long table_stride;
+  int num_pages, page_size, max_pages;
+};
+struct AppendArgs {
+  const void* k;
+  const void* v;
+  long long ks_b, ks_l, ks_h;
+  long long vs_b, vs_l, vs_h;
+  const int* pos;
+  const int* count;
+  PagedArgs cache;
+  int B, T, H, dk, dv;
+  int* err;
+};
+// piece: bytes moved per access (16, or the element's size where a view is not made of 16-byte pieces).
+cudaError_t launch_cache_append(const AppendArgs& a, int elem_bytes, int piece, int sms, cudaStream_t s);
+
+struct DecodeArgs {
+  const void* q;
+  void* o;
+  long long qs_b, qs_h, os_b, os_h;
+  PagedArgs cache;
+  const int* length;
+  const int* first;
+  const float* slopes;
+  float scale, softcap;
+  int B, Hq, Hkv, group, dk, dv;
+  int chunks;           // items per key head: ceil(group / heads per item)
+  float* part;          // workspace: partial results, two per CTA
+  int* record;          // workspace: per CTA {item, pieces} of the item it starts and does not finish
+  int ctas;             // grid of the main kernel
+  int* err;
+};
+constexpr int kDecodeSimtHeads = 8;  // query heads of one item, CUDA-core kernel
+// Workspace: `ctas` records of two ints, then 2 * ctas partials of `heads` x (dv + 2) floats.
+size_t decode_workspace_bytes(int ctas, int heads, int dv);
+int decode_ctas(bool bf16, bool vec, int sms, int dk, int dv);
+cudaError_t launch_decode(const DecodeArgs& a, bool bf16, bool vec, cudaStream_t s);
+
 // ------------------------------------------------------------ watchdog hook
 cudaError_t launch_timeout_probe(int* err, uint64_t limit_ns, cudaStream_t s);
 

@@ -368,10 +368,137 @@ cb_status cb_preprocess_u8_three_pass(const unsigned char* src, int n, int src_h
                                       long long src_pitch, unsigned char* tmp_u8, float* tmp_f32,
                                       float* dst, int dst_h, int dst_w, void* stream);
 
+/* ------------------------------------------------------------------ attention
+ *
+ * Attention over the tokens of feature maps and over a decoder's cache: the
+ * operator that the network of "YOLO26N Inference Optimisation" runs beside
+ * its convolutions (nsys breakdown: flash_attention2 and the psa_* glue
+ * around it), with the forms a decoder of image tokens needs.  Projections
+ * are 1x1 layers (cb_conv_bn_act); their outputs are read in place.
+ *
+ * A batch of token rows split in heads: element (b, i, h, d) lives at
+ * data + b*stride_b + i*stride_l + h*stride_h + d (strides in ELEMENTS,
+ * non-negative, d contiguous).  A projection's NHWC output [N, H, W, C] with
+ * packed rows is a view with len = H*W, stride_l = the pixel stride and heads
+ * as channel slices: no glue kernel packs or splits them.
+ */
+typedef struct {
+  void* data;
+  int batch, len, heads, dim;
+  long long stride_b, stride_l, stride_h;
+  cb_dtype dtype;
+} cb_heads;
+
+/*
+ * How cb_attention turns q.k into a score, and which keys a query sees:
+ *   s = scale * q_i.k_j;   softcap > 0:  s = softcap * tanh(s / softcap);
+ *   slopes != NULL:  s -= slopes[h] * |i + q_offset - j|
+ *   key j is visible to query i of sequence b if
+ *     j < kv_len[b]                     (kv_len NULL: j < k->len), and
+ *     causal == 0, or j <= i + q_offset, or j < prefix_len[b]  (NULL: 0), and
+ *     doc_q[b*q->len + i] == doc_k[b*k->len + j] >= 0          (NULL: no documents).
+ * scale > 0 and softcap >= 0 are finite; |q_offset| <= 2^29; prefix_len
+ * needs causal; doc_q and doc_k come together.  slopes: DEVICE fp32
+ * [q->heads]; kv_len, prefix_len: DEVICE int [batch], clamped to
+ * [0, k->len]; doc_q, doc_k: DEVICE int [batch, len], contiguous, negative =
+ * padding that sees and is seen by nothing.
+ */
+typedef struct {
+  float scale, softcap;
+  const float* slopes;
+  int causal, q_offset;
+  const int* prefix_len;
+  const int* kv_len;
+  const int* doc_q;
+  const int* doc_k;
+} cb_score;
+
+/*
+ * out[b, i, h] = sum_j p_ij v[b, j, h'] with p_i the softmax of the scores of
+ * the visible keys and h' = h / (q->heads / k->heads) (grouped heads); a
+ * query that sees no key gets zeros.  What is not visible never reaches the
+ * output, whatever it holds (infinities and NaN included).
+ * q: [batch, Lq, Hq, Dk]; k: [batch, Lk, Hkv, Dk]; v: [batch, Lk, Hkv, Dv];
+ * out: [batch, Lq, Hq, Dv], overlapping none of them; Hq a multiple of Hkv;
+ * Dk and Dv at most 128 (else CB_ERR_UNSUPPORTED), all of one dtype, data
+ * aligned to its elements (else CB_ERR_ALIGNMENT).  Lq, Lk, batch may be 0.
+ * bf16 views whose data is 16-byte aligned with strides and head sizes that
+ * are multiples of 8 elements, at most 2^20 keys long, run on the tensor
+ * cores: scores and the sums over keys in fp32, the weights p rounded to bf16
+ * as the second product's operand.  fp32, and every other bf16 view, runs in
+ * fp32 on the CUDA cores.  Softmax statistics are fp32 throughout.  One
+ * kernel, no workspace; asynchronous on `stream`; bounded waits
+ * (CB_ERR_TIMEOUT through cb_get_device_error).
+ */
+cb_status cb_attention(const cb_heads* q, const cb_heads* k, const cb_heads* v, const cb_score* score, cb_heads* out,
+                       void* stream);
+
+/*
+ * A paged key-value cache: `num_pages` pages of `page_size` slots; slot t of
+ * page p holds a token's keys at k + p*k_stride_page + t*k_stride_slot +
+ * h*k_stride_head + d (d < dim_k; elements, non-negative) and its values
+ * likewise.  Token j of sequence b lies in page table[b*table_stride + j /
+ * page_size], slot j % page_size; table: DEVICE int [batch, max_pages].
+ * Table entries past a sequence's last token are never read.  An entry
+ * outside [0, num_pages) that is read, or a token past max_pages pages, is
+ * not followed: the kernel records CB_ERR_INVALID_ARG for
+ * cb_get_device_error and treats the token as absent.
+ */
+typedef struct {
+  void* k;
+  void* v;
+  int num_pages, page_size, heads, dim_k, dim_v;
+  long long k_stride_page, k_stride_slot, k_stride_head;
+  long long v_stride_page, v_stride_slot, v_stride_head;
+  const int* table;
+  int batch, max_pages;
+  long long table_stride;
+  cb_dtype dtype;
+} cb_paged_cache;
+
+/*
+ * Writes new tokens into the cache: token t of sequence b, for t < count[b]
+ * (DEVICE int [batch], clamped to [0, len]; NULL: every token of k_new),
+ * becomes token pos[b] + t.  pos: DEVICE int [batch]; a negative position is
+ * refused like a bad table entry.  k_new: [batch, T, heads, dim_k], v_new:
+ * [batch, T, heads, dim_v], of the cache's dtype.  Two tokens of one call
+ * must not share a slot.
+ */
+cb_status cb_cache_append(const cb_heads* k_new, const cb_heads* v_new, const int* pos, const int* count,
+                          const cb_paged_cache* cache, void* stream);
+
+/*
+ * Workspace bytes cb_attention_decode needs for these views (written to
+ * *bytes): room for the partial results of sequences that several CTAs
+ * share.  Depends on the shapes and the GPU, not on the lengths.
+ */
+cb_status cb_attention_decode_workspace(const cb_heads* q, const cb_paged_cache* cache, size_t* bytes);
+
+/*
+ * Attention of one new token per sequence over the paged cache: q and out
+ * are views with len 1, [batch, 1, Hq, dim_k] and [batch, 1, Hq, dim_v], and
+ * sequence b's query attends to cache tokens first[b] <= j < length[b]
+ * (DEVICE int [batch]; first NULL: 0; length clamped to what max_pages
+ * pages hold; an empty range gives zeros).  Scores as in cb_score with the
+ * query at position length[b] - 1: scale, softcap, and slopes (NULL or
+ * DEVICE fp32 [Hq]) times length[b] - 1 - j.  The new token's own key and
+ * value are in the cache already (cb_cache_append).  Hq a multiple of the
+ * cache's heads; dim_k and dim_v at most 128, batch at most 4096 (else
+ * CB_ERR_UNSUPPORTED).  The tokens of all sequences are dealt evenly over
+ * the GPU, a long sequence over many CTAs, and joined in a fixed order: the
+ * same inputs give the same bits.  workspace: DEVICE scratch of at least
+ * cb_attention_decode_workspace() bytes, 256-byte aligned, overwritten;
+ * calls that may overlap need one each.  CB_ERR_WORKSPACE if too small.
+ */
+cb_status cb_attention_decode(const cb_heads* q, const cb_paged_cache* cache, const int* length, const int* first,
+                              float scale, float softcap, const float* slopes, cb_heads* out, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
 /*
  * Synchronises `stream`, then reads and clears the library's device error
  * word: CB_ERR_TIMEOUT if a kernel gave up waiting on a barrier since the
- * last call, CB_ERR_CUDA if the stream reported an error, else CB_OK.
+ * last call, CB_ERR_INVALID_ARG if one met a bad page-table entry or cache
+ * position, CB_ERR_CUDA if the stream reported an error, else CB_OK.
  * The pages have no counterpart: this is the host end of the library's
  * bounded waits.  The word's device address is looked up once per device
  * and kept for the life of the process, like the scratch array of

@@ -1,0 +1,135 @@
+"""Refusals of the attention entry points, on the host: nothing is launched (no GPU)."""
+import ctypes
+
+import pytest
+
+DATA = 1 << 20  # never dereferenced
+
+
+def heads(cblib, b=2, l=8, h=4, d=64, data=DATA, dtype=1, sb=None, sl=None, sh=None):
+    sh = d if sh is None else sh
+    sl = h * d if sl is None else sl
+    return cblib.CbHeads(data, b, l, h, d, l * sl if sb is None else sb, sl, sh, dtype)
+
+
+def score(cblib, scale=0.125, softcap=0.0, **kw):
+    s = cblib.CbScore(scale, softcap)
+    for k, v in kw.items():
+        setattr(s, k, v)
+    return s
+
+
+def attention(cblib, **kw):
+    far = 1 << 24
+    a = {"q": heads(cblib), "k": heads(cblib, h=2, data=DATA + far), "v": heads(cblib, h=2, data=DATA + 2 * far),
+         "out": heads(cblib, data=DATA + 3 * far), "score": score(cblib)}
+    a.update(kw)
+    r = ctypes.byref
+    null = lambda x: r(x) if x is not None else None  # noqa: E731
+    return cblib.load().cb_attention(null(a["q"]), null(a["k"]), null(a["v"]), null(a["score"]), null(a["out"]), None)
+
+
+@pytest.mark.parametrize("name", ["q", "k", "v", "out", "score"])
+def test_attention_null(cblib, name):
+    assert attention(cblib, **{name: None}) == cblib.ERR_INVALID_ARG
+
+
+def test_attention_shapes(cblib):
+    far = 1 << 24
+    bad = [{"k": heads(cblib, h=3, data=DATA + far), "v": heads(cblib, h=3, data=DATA + far)},  # 4 % 3
+           {"k": heads(cblib, b=1, h=2, data=DATA + far)}, {"v": heads(cblib, l=7, h=2, data=DATA + far)},
+           {"k": heads(cblib, h=2, d=32, data=DATA + far)}, {"out": heads(cblib, d=32, data=DATA + 3 * far)},
+           {"out": heads(cblib, l=9, data=DATA + 3 * far)}, {"k": heads(cblib, h=2, dtype=0, data=DATA + far)},
+           {"q": heads(cblib, dtype=7)}, {"q": heads(cblib, data=0)}, {"q": heads(cblib, sl=-1, sb=0)},
+           {"q": heads(cblib, h=0)}, {"out": heads(cblib, data=DATA + 128)}]  # the last overlaps q
+    for kw in bad:
+        assert attention(cblib, **kw) == cblib.ERR_INVALID_ARG, kw
+
+
+def test_attention_scores(cblib):
+    inf, nan = float("inf"), float("nan")
+    for kw in ({"scale": 0.0}, {"scale": -1.0}, {"scale": nan}, {"scale": inf}, {"softcap": -1.0}, {"softcap": nan},
+               {"prefix_len": DATA}, {"doc_q": DATA}, {"doc_k": DATA}, {"q_offset": 1 << 30}):
+        assert attention(cblib, score=score(cblib, **kw)) == cblib.ERR_INVALID_ARG, kw
+
+
+def test_attention_unsupported_and_alignment(cblib):
+    far = 1 << 24
+    q, o = heads(cblib, d=136), heads(cblib, d=64, data=DATA + 3 * far)
+    assert attention(cblib, q=q, k=heads(cblib, h=2, d=136, data=DATA + far), out=o) == cblib.ERR_UNSUPPORTED
+    v, o = heads(cblib, h=2, d=129, data=DATA + far), heads(cblib, d=129, data=DATA + 3 * far)
+    assert attention(cblib, v=v, out=o) == cblib.ERR_UNSUPPORTED
+    assert attention(cblib, q=heads(cblib, data=DATA + 1)) == cblib.ERR_ALIGNMENT
+
+
+def test_attention_nothing_to_do(cblib):
+    e = {n: heads(cblib, b=0, h=2 if n in "kv" else 4, data=0) for n in ("q", "k", "v", "out")}
+    assert attention(cblib, **e) == cblib.OK
+
+
+def cache(cblib, P=10, page=16, H=2, dk=64, dv=64, batch=2, width=5, dtype=1, k=DATA, table=DATA, **kw):
+    c = cblib.CbPagedCache(k, DATA + (1 << 24), P, page, H, dk, dv, page * H * dk, H * dk, dk, page * H * dv, H * dv, dv, table,
+                           batch, width, width, dtype)
+    for n, v in kw.items():
+        setattr(c, n, v)
+    return c
+
+
+def append(cblib, k=None, v=None, pos=DATA, c=None):
+    k = heads(cblib, h=2) if k is None else k
+    v = heads(cblib, h=2) if v is None else v
+    c = cache(cblib) if c is None else c
+    return cblib.load().cb_cache_append(ctypes.byref(k), ctypes.byref(v), pos, None, ctypes.byref(c), None)
+
+
+def test_append_refusals(cblib):
+    I = cblib.ERR_INVALID_ARG
+    assert append(cblib, pos=None) == I
+    assert append(cblib, k=heads(cblib, h=4)) == I and append(cblib, v=heads(cblib, h=2, d=32)) == I
+    assert append(cblib, k=heads(cblib, h=2, l=3)) == I and append(cblib, c=cache(cblib, batch=3)) == I
+    assert append(cblib, c=cache(cblib, dtype=0)) == I and append(cblib, c=cache(cblib, page=0)) == I
+    assert append(cblib, c=cache(cblib, k=0)) == I and append(cblib, c=cache(cblib, table=0)) == I
+    assert append(cblib, c=cache(cblib, page=1 << 20, width=1 << 12)) == I
+    assert append(cblib, c=cache(cblib, k_stride_page=-1)) == I
+    assert append(cblib, c=cache(cblib, k=DATA + 1)) == cblib.ERR_ALIGNMENT
+    lib = cblib.load()
+    assert lib.cb_cache_append(None, None, DATA, None, None, None) == I
+    empty = heads(cblib, h=2, l=0)
+    assert append(cblib, k=empty, v=empty) == cblib.OK
+
+
+def decode(cblib, q=None, c=None, length=DATA, out=None, scale=0.125, cap=0.0, ws=DATA, size=1 << 40):
+    q = heads(cblib, l=1) if q is None else q
+    out = heads(cblib, l=1, data=DATA + (1 << 25)) if out is None else out
+    c = cache(cblib) if c is None else c
+    return cblib.load().cb_attention_decode(ctypes.byref(q), ctypes.byref(c), length, None, scale, cap, None,
+                                            ctypes.byref(out), ws, size, None)
+
+
+def test_decode_refusals(cblib):
+    I = cblib.ERR_INVALID_ARG
+    assert decode(cblib, length=None) == I and decode(cblib, ws=None) == I
+    assert decode(cblib, q=heads(cblib, l=2)) == I and decode(cblib, q=heads(cblib, l=1, d=32)) == I
+    assert decode(cblib, q=heads(cblib, l=1, h=3)) == I and decode(cblib, q=heads(cblib, l=1, b=3)) == I
+    assert decode(cblib, out=heads(cblib, l=1, h=2)) == I and decode(cblib, out=heads(cblib, l=1)) == I  # the last overlaps q
+    assert decode(cblib, scale=0.0) == I and decode(cblib, cap=-1.0) == I
+    assert decode(cblib, ws=DATA + 16) == cblib.ERR_ALIGNMENT
+    assert decode(cblib, q=heads(cblib, l=1, data=DATA + 1)) == cblib.ERR_ALIGNMENT
+    wide = dict(d=136, l=1)
+    assert decode(cblib, q=heads(cblib, **wide), c=cache(cblib, dk=136)) == cblib.ERR_UNSUPPORTED
+    n = ctypes.c_size_t(0)
+    lib = cblib.load()
+    assert lib.cb_attention_decode_workspace(None, None, ctypes.byref(n)) == I
+    q, c = heads(cblib, l=1), cache(cblib)
+    assert lib.cb_attention_decode_workspace(ctypes.byref(q), ctypes.byref(c), None) == I
+
+
+def test_binding_checks_index_tensors(cblib):
+    import torch
+    s = cblib.Score(0.1, kv_len=torch.zeros(2, dtype=torch.int64))
+    with pytest.raises(ValueError):
+        s.view(2, 4, 4, 4)
+    with pytest.raises(ValueError):
+        cblib.heads(torch.zeros(1, 2, 3, 8).transpose(2, 3))
+    with pytest.raises(ValueError):
+        cblib.PagedCache(torch.zeros(2, 4, 1, 8), torch.zeros(2, 4, 2, 8), torch.zeros(1, 1, dtype=torch.int32))

@@ -1,0 +1,190 @@
+"""cb_attention on the GPU against the definition in 64 bits: head layouts, lengths from one token on, odd sizes,
+strides, every mask, masks that leave a row empty, and what lies in masked places."""
+import pytest
+import torch
+
+import attention_ref as ref
+from conv_bn_activation_gb300 import binding as cb
+from gpu_util import sync_check
+
+pytestmark = pytest.mark.gpu
+BF16, F32 = torch.bfloat16, torch.float32
+
+# B, Lq, Lk, Hq, Hkv, Dk, Dv
+SHAPES = [(1, 1, 1, 1, 1, 8, 8), (2, 49, 49, 3, 3, 64, 64), (1, 130, 257, 4, 2, 32, 64), (2, 128, 128, 2, 1, 128, 128),
+          (1, 1, 1000, 8, 1, 128, 128), (1, 300, 300, 2, 2, 40, 72), (3, 127, 129, 5, 1, 96, 96), (1, 513, 640, 2, 2, 64, 128),
+          (1, 260, 70, 2, 1, 128, 64), (2, 400, 400, 4, 4, 32, 64), (1, 16, 2049, 6, 2, 64, 64), (1, 5, 0, 2, 1, 64, 64)]
+RULES = ["full", "causal", "prefix", "kv_len", "docs", "cap", "bias", "all"]
+
+
+def make(shape, dtype, seed=0, spread=3.0, device="cuda"):
+    B, Lq, Lk, Hq, Hkv, Dk, Dv = shape
+    q = ref.randn(B, Lq, Hq, Dk, seed=seed, dtype=torch.float32, device=device) * spread
+    return (q.to(dtype), ref.randn(B, Lk, Hkv, Dk, seed=seed + 1, dtype=dtype, device=device),
+            ref.randn(B, Lk, Hkv, Dv, seed=seed + 2, dtype=dtype, device=device))
+
+
+def rule(name, shape, device="cuda"):
+    B, Lq, Lk, Hq, Hkv, Dk, Dv = shape
+    kw = {"scale": Dk ** -0.5}
+    every = name == "all"
+    if name in ("causal", "prefix") or every:
+        kw.update(causal=True, q_offset=Lk - Lq)
+    if name == "prefix" or every:
+        kw["prefix_len"] = torch.tensor([(Lk // 3 + 37 * b) for b in range(B)], dtype=torch.int32, device=device)
+    if name == "kv_len" or every:  # the first sequence of several has no key at all
+        kw["kv_len"] = torch.tensor([Lk * (b if B > 1 else 2) // max(B, 3) for b in range(B)], dtype=torch.int32, device=device)
+    if name == "docs" or every:  # unsorted ids, padding, documents without a key
+        g = torch.Generator().manual_seed(Lq + Lk)
+        kw["doc_q"] = (torch.randint(-1, 4, (B, Lq), generator=g).repeat_interleave(37, 1)[:, :Lq]).to(torch.int32).to(device)
+        kw["doc_k"] = (torch.randint(-1, 3, (B, Lk), generator=g).repeat_interleave(61, 1)[:, :Lk]).to(torch.int32).to(device)
+        kw["doc_q"], kw["doc_k"] = kw["doc_q"].contiguous(), kw["doc_k"].contiguous()
+    if name == "cap" or every:
+        kw["softcap"] = 5.0
+    if name == "bias" or every:
+        kw["slopes"] = ref.alibi_slopes(Hq, device)
+    return kw
+
+
+def run(q, k, v, kw, out=None, stream=None):
+    if out is None:
+        out = torch.full((*q.shape[:3], v.shape[3]), float("nan"), dtype=q.dtype, device=q.device)
+    cb.attention(q, k, v, out, cb.Score(**kw), stream=stream)
+    return out
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("name", RULES)
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "x".join(map(str, s)))
+def test_against_definition(gpu, shape, name, dtype):
+    q, k, v = make(shape, dtype)
+    kw = rule(name, shape)
+    out = run(q, k, v, kw)
+    sync_check()
+    ref.check(out, ref.attention(q, k, v, **kw), v, dtype)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("dims", [(7, 5), (64, 64), (1, 1), (33, 128)], ids=str)
+def test_odd_dims_and_strides(gpu, dims, dtype):
+    """Head-major storage, rows with gaps, data off 16-byte boundaries; what lies around the output stays."""
+    B, Lq, Lk, Hq, Hkv = 2, 70, 131, 4, 2
+    dk, dv = dims
+    q, k, v = make((B, Lq, Lk, Hq, Hkv, dk, dv), dtype, seed=5)
+    qs = torch.zeros(B, Hq, Lq + 1, dk + 3, dtype=dtype, device="cuda")[:, :, 1:, 1:dk + 1].transpose(1, 2)
+    ks = torch.zeros(B, Hkv, Lk, dk + 1, dtype=dtype, device="cuda")[..., 1:].transpose(1, 2)
+    vs = torch.zeros(B, Lk, Hkv, 2 * dv + 1, dtype=dtype, device="cuda")[..., dv + 1:]
+    qs.copy_(q), ks.copy_(k), vs.copy_(v)
+    buf = torch.full((B, Lq, Hq + 1, dv + 2), 77.0, dtype=dtype, device="cuda")
+    out = buf[:, :, 1:, 1:dv + 1]
+    kw = {"scale": dk ** -0.5, "causal": True, "q_offset": Lk - Lq}
+    run(qs, ks, vs, kw, out=out)
+    sync_check()
+    ref.check(out, ref.attention(q, k, v, **kw), v, dtype)
+    assert (buf[:, :, 0] == 77).all() and (buf[..., 0] == 77).all() and (buf[..., -1] == 77).all()
+
+
+def test_slices_of_one_projection(gpu):
+    """q, k, v as channel slices of a projection's output, the output a slice beside them."""
+    B, L, Hq, Hkv, D = 2, 200, 8, 2, 64
+    row = ref.randn(B, L, (2 * Hq + 2 * Hkv) * D, seed=3, dtype=BF16, device="cuda")
+    q, k, v, o = (t.unflatten(-1, (-1, D)) for t in torch.split(row, [Hq * D, Hkv * D, Hkv * D, Hq * D], dim=-1))
+    want = ref.attention(q, k, v, 0.125)
+    cb.attention(q, k, v, o, cb.Score(0.125))
+    sync_check()
+    ref.check(o, want, v, BF16)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("poison", [float("nan"), float("inf"), -float("inf")], ids=str)
+def test_masked_places_do_not_matter(gpu, poison, dtype):
+    """Infinities and NaN in keys and values that a query does not see leave its row as it is: past kv_len,
+    in the future, in another document, in padding."""
+    shape = (2, 300, 300, 4, 2, 64, 64)
+    q, k, v = make(shape, dtype, seed=9)
+    doc = (torch.arange(300) // 90).to(torch.int32)
+    doc[280:] = -1
+    doc = doc[None].expand(2, 300).contiguous().cuda()
+    kw = {"scale": 0.125, "causal": True, "doc_q": doc, "doc_k": doc,
+          "kv_len": torch.tensor([300, 250], dtype=torch.int32, device="cuda")}
+    clean = ref.attention(q, k, v, **kw)
+    k[:, 285:] = poison
+    v[:, 285:] = poison
+    k[1, 250:] = poison
+    v[1, 250:] = poison
+    v[:, 150] = poison   # seen by queries 150..179 (its document, not before it) alone
+    out = run(q, k, v, kw)
+    sync_check()
+    got = out.cpu().double()
+    seen = torch.zeros(2, 300, dtype=torch.bool)
+    seen[:, 150:180] = True
+    assert torch.isfinite(got[~seen]).all()
+    assert not torch.isfinite(got[seen]).any()
+    got[seen] = clean[seen]
+    ref.check(got, clean, torch.where(torch.isfinite(v), v, torch.zeros_like(v)), dtype)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_large_scores_and_late_maximum(gpu, dtype):
+    """Scores of hundreds, the largest among the last keys: the running maximum moves far, exponentials of
+    the first tiles vanish, and nothing overflows."""
+    B, L, H, D = 1, 1024, 2, 64
+    q, k, v = make((B, L, L, H, H, D, D), dtype, seed=2, spread=1.0)
+    k = (k.float() * torch.linspace(0.5, 30.0, L, device="cuda")[None, :, None, None]).to(dtype)
+    out = run(q, k, v, {"scale": 1.0})
+    sync_check()
+    got, want = out.cpu().double(), ref.attention(q, k, v, 1.0)
+    # scores up to ~1000: their fp32 rounding (2^-24 * 1000 a few times) moves a weight by ~1e-3 of itself
+    err = (got - want).abs().max()
+    assert float(err) <= (3e-3 if dtype == F32 else 3e-3 + 2.0 ** -7) * float(v.abs().max())
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_same_bits_twice_and_on_another_stream(gpu, dtype):
+    shape = (2, 333, 777, 4, 2, 128, 128)
+    q, k, v = make(shape, dtype, seed=4)
+    kw = rule("all", shape)
+    a = run(q, k, v, kw)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    b = torch.empty_like(a)
+    run(q, k, v, kw, out=b, stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+def test_graph_capture(gpu):
+    shape = (1, 200, 200, 4, 4, 64, 64)
+    q, k, v = make(shape, BF16, seed=8)
+    kw = rule("causal", shape)
+    out = torch.zeros(1, 200, 4, 64, dtype=BF16, device="cuda")
+    run(q, k, v, kw, out=out)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run(q, k, v, kw, out=out)
+    q.copy_(ref.randn(*q.shape, seed=77, dtype=BF16, device="cuda"))
+    out.zero_()
+    g.replay()
+    sync_check()
+    ref.check(out, ref.attention(q, k, v, **kw), v, BF16)
+
+
+def test_empty_batch_and_rows(gpu):
+    for shape in ((0, 4, 4, 2, 2, 64, 64), (2, 0, 4, 2, 2, 64, 64)):
+        q, k, v = make(shape, BF16)
+        assert run(q, k, v, {"scale": 1.0}).numel() == 0
+    sync_check()
+
+
+def test_wide_offsets(gpu):
+    """Rows of one sequence more than 2^31 elements apart from the data pointer."""
+    stride = (1 << 30) + 64
+    flat = torch.empty(3 * stride + 4096, dtype=BF16, device="cuda")
+    k = flat.as_strided((1, 4, 1, 64), (0, stride, 64, 1))
+    v = flat.as_strided((1, 4, 1, 64), (0, stride, 64, 1), 64)
+    q, k0, v0 = make((1, 4, 4, 1, 1, 64, 64), BF16, seed=1)
+    k.copy_(k0), v.copy_(v0)
+    out = run(q, k, v, {"scale": 0.125})
+    sync_check()
+    ref.check(out, ref.attention(q, k0, v0, 0.125), v0, BF16)

@@ -92,6 +92,18 @@ bool score_ok(float scale, float softcap) {
   return std::isfinite(scale) && scale > 0.f && std::isfinite(softcap) && softcap >= 0.f;
 }
 
+// The tensor-core kernel's map of a view: (dim, heads, len, batch).
+bool tc_map(CUtensorMap* m, const cb_heads* t) {
+  int box_d = 0, box_l = 0;
+  attn_tc_box(&box_d, &box_l);
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(t->dim), static_cast<cuuint64_t>(t->heads),
+                              static_cast<cuuint64_t>(t->len), static_cast<cuuint64_t>(t->batch)};
+  const cuuint64_t strides[3] = {2 * static_cast<cuuint64_t>(t->stride_h), 2 * static_cast<cuuint64_t>(t->stride_l),
+                                 2 * static_cast<cuuint64_t>(t->stride_b)};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(box_d), 1, static_cast<cuuint32_t>(box_l), 1};
+  return host_map_bf16(m, t->data, dims, strides, box);
+}
+
 // Shapes of a decode call; fills nothing it refuses.
 cb_status check_decode(const cb_heads* q, const cb_paged_cache* cache) {
   if (!heads_ok(q) || !cache_ok(cache)) return CB_ERR_INVALID_ARG;
@@ -154,6 +166,10 @@ cb_status cb_attention(const cb_heads* q, const cb_heads* k, const cb_heads* v, 
   if (k->len > 0) a.doc_q = score->doc_q, a.doc_k = score->doc_k;
   a.timeout_ns = host_timeout_ns();
   const bool vec = pieces16(q) && pieces16(k) && pieces16(v) && pieces16(out);
+  CUtensorMap qm, km, vm;
+  if (q->dtype == CB_DTYPE_BF16 && vec && k->len >= 1 && k->len <= kAttnTcMaxKeys && tc_map(&qm, q) && tc_map(&km, k) &&
+      tc_map(&vm, v))
+    return done(launch_attn_tc(qm, km, vm, a, static_cast<cudaStream_t>(stream)));
   return done(launch_attn_simt(a, q->dtype == CB_DTYPE_BF16, vec, sms, static_cast<cudaStream_t>(stream)));
 }
 

@@ -115,7 +115,7 @@ cb_status check_decode(const cb_heads* q, const cb_paged_cache* cache) {
 }
 
 struct DecodePlan {
-  int sms = 0, ctas = 0, heads = 0;
+  int sms = 0, ctas = 0, chunks = 0, heads = 0;
   int* err = nullptr;
   bool vec = false;
 };
@@ -123,8 +123,12 @@ cb_status plan_decode(const cb_heads* q, const cb_paged_cache* cache, DecodePlan
   const cb_status st = host_device(&p->sms, &p->err);
   if (st != CB_OK) return st;
   p->vec = pieces16(cache);
-  p->ctas = decode_ctas(q->dtype == CB_DTYPE_BF16, p->vec, p->sms, cache->dim_k, cache->dim_v);
-  p->heads = kDecodeSimtHeads;
+  // One wave of resident CTAs: their runs are equal, so a second wave would only add pieces to join.
+  const bool mma = q->dtype == CB_DTYPE_BF16 && p->vec;
+  p->ctas = p->sms * (mma ? 2 : 4);
+  const int group = q->heads / cache->heads, most = mma ? kDecodeMmaHeads : kDecodeSimtHeads;
+  p->chunks = (group + most - 1) / most;
+  p->heads = (group + p->chunks - 1) / p->chunks;
   return CB_OK;
 }
 
@@ -238,7 +242,7 @@ cb_status cb_attention_decode(const cb_heads* q, const cb_paged_cache* cache, co
   a.scale = scale, a.softcap = softcap;
   a.B = q->batch, a.Hq = q->heads, a.Hkv = cache->heads, a.group = q->heads / cache->heads;
   a.dk = cache->dim_k, a.dv = cache->dim_v;
-  a.chunks = (a.group + p.heads - 1) / p.heads;
+  a.chunks = p.chunks, a.item_heads = p.heads;
   a.record = static_cast<int*>(workspace);
   a.part = reinterpret_cast<float*>(a.record + 2 * p.ctas);
   a.ctas = p.ctas;

@@ -1,5 +1,6 @@
 // Attention of one new token per sequence over a paged cache (cb_attention_decode):
-// the CUDA-core kernel and the join of split sequences.
+// the CUDA-core kernel (fp32 caches, and bf16 ones whose rows are not whole
+// 16-byte pieces; the others take decode_mma.cu) and the join of split sequences.
 //
 // Bound by HBM: every key and value of the batch is read once, and one
 // query's 4 FLOP per element are far below the FMA rate until many heads
@@ -14,13 +15,6 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kHeads = kDecodeSimtHeads;
-
-// Piece of a run: sequence, item within it, tiles, and how it relates to its item.
-struct Piece {
-  int b, item;           // item = key head * chunks + chunk
-  int tile0, tiles;      // absolute tile of the sequence
-  bool starts, ends;     // holds the item's first / last tile
-};
 
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads) decode_simt_kernel(DecodeArgs a) {
@@ -43,38 +37,19 @@ __global__ void __launch_bounds__(kThreads) decode_simt_kernel(DecodeArgs a) {
   const Run run{total, min(static_cast<long long>(gridDim.x), max(total, 1LL))};
   const long long cta = blockIdx.x;
   if (tid == 0) a.record[2 * cta] = -1;
-  // Sequences without a visible token: zeros, dealt over the CTAs.
-  for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-    if (prefix[b + 1] != prefix[b]) continue;
-    T* o = static_cast<T*>(a.o) + b * a.os_b;
-    for (int e = tid; e < a.Hq * a.dv; e += kThreads) o[e / a.dv * a.os_h + e % a.dv] = from_f32<T>(0.f);
-  }
+  zero_empty(a, prefix, [&](long long i) { static_cast<T*>(a.o)[i] = from_f32<T>(0.f); });
   if (cta >= run.ctas || total == 0) return;
   const long long end = run.begin(cta + 1);
   long long at = run.begin(cta);
-  int b = 0;
-  {  // the sequence that holds tile `at`
-    int hi = a.B;
-    while (hi - b > 1) {
-      const int mid = (b + hi) >> 1;
-      if (static_cast<long long>(prefix[mid]) * per_seq <= at) b = mid;
-      else hi = mid;
-    }
-  }
+  int b = find_seq(a, prefix, per_seq, at);
   // threads of one value row: lanes_v of 4 values each
   int lanes_v = 1;
   while (lanes_v * 4 < a.dv) lanes_v <<= 1;
   const int slots = kThreads / lanes_v, vs = tid / lanes_v, vd = (tid % lanes_v) * 4;
 
   while (at < end) {
-    while (static_cast<long long>(prefix[b + 1]) * per_seq <= at) ++b;
-    const SeqSpan sp = seq_span(a, b);
-    const long long in_seq = at - static_cast<long long>(prefix[b]) * per_seq;
-    const int item = static_cast<int>(in_seq / sp.tiles), off = static_cast<int>(in_seq - static_cast<long long>(item) * sp.tiles);
-    const int tiles = static_cast<int>(min(static_cast<long long>(sp.tiles - off), end - at));
-    const bool starts = off == 0, ends = off + tiles == sp.tiles;
-    const int hk = item / a.chunks, h0 = hk * a.group + (item % a.chunks) * kHeads;
-    const int heads = min(kHeads, (hk + 1) * a.group - h0);
+    const Piece pc = next_piece(a, prefix, per_seq, at, end, &b);
+    const int hk = pc.hk, h0 = pc.h0, heads = pc.heads;
 
     __syncthreads();
     for (int e = tid; e < kHeads * ldk; e += kThreads) {
@@ -88,12 +63,12 @@ __global__ void __launch_bounds__(kThreads) decode_simt_kernel(DecodeArgs a) {
 #pragma unroll
       for (int c = 0; c < 4; ++c) acc[g][c] = 0.f;
 
-    for (int t = 0; t < tiles; ++t) {
-      const int j0 = (sp.t0 + off + t) * kDecodeTile;
+    for (int t = 0; t < pc.tiles; ++t) {
+      const int j0 = (pc.tile0 + t) * kDecodeTile;
       __syncthreads();
       if (tid < kDecodeTile) {
         const int j = j0 + tid;
-        page_s[tid] = j >= sp.lo && j < sp.hi ? token_page(a, b, j, &slot_s[tid]) : -1;
+        page_s[tid] = j >= pc.lo && j < pc.hi ? token_page(a, b, j, &slot_s[tid]) : -1;
       }
       __syncthreads();
       {  // keys
@@ -103,16 +78,8 @@ __global__ void __launch_bounds__(kThreads) decode_simt_kernel(DecodeArgs a) {
           const int r = e / pieces, d = (e - r * pieces) * per;
           const int page = page_s[r];
           const T* src = static_cast<const T*>(a.cache.k) + page * a.cache.ks_p + slot_s[r] * a.cache.ks_t + hk * a.cache.ks_h + d;
-          if constexpr (VEC && sizeof(T) == 4) {
+          if constexpr (VEC) {
             *reinterpret_cast<float4*>(Ks + r * ldk + d) = page < 0 ? make_float4(0.f, 0.f, 0.f, 0.f) : *reinterpret_cast<const float4*>(src);
-          } else if constexpr (VEC) {
-            const uint4 w = page < 0 ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4*>(src);
-            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              Ks[r * ldk + d + 2 * i] = __uint_as_float(u[i] << 16);
-              Ks[r * ldk + d + 2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-            }
           } else {
             Ks[r * ldk + d] = page < 0 || d >= a.dk ? 0.f : to_f32(*src);
           }
@@ -132,7 +99,7 @@ __global__ void __launch_bounds__(kThreads) decode_simt_kernel(DecodeArgs a) {
             dot[g] = fmaf(qv.x, kv.x, fmaf(qv.y, kv.y, fmaf(qv.z, kv.z, fmaf(qv.w, kv.w, dot[g]))));
           }
         }
-        const int dist = sp.len - 1 - (j0 + key);
+        const int dist = pc.len - 1 - (j0 + key);
 #pragma unroll
         for (int g = 0; g < kHeads / 2; ++g) {
           const int hd = 2 * g + half;
@@ -174,13 +141,9 @@ __global__ void __launch_bounds__(kThreads) decode_simt_kernel(DecodeArgs a) {
           if (page < 0) continue;
           const T* src = static_cast<const T*>(a.cache.v) + page * a.cache.vs_p + slot_s[key] * a.cache.vs_t + hk * a.cache.vs_h + vd;
           float v[4];
-          if constexpr (VEC && sizeof(T) == 4) {
+          if constexpr (VEC) {
             const float4 w = *reinterpret_cast<const float4*>(src);
             v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
-          } else if constexpr (VEC) {
-            const uint2 w = *reinterpret_cast<const uint2*>(src);
-            v[0] = __uint_as_float(w.x << 16), v[1] = __uint_as_float(w.x & 0xffff0000u);
-            v[2] = __uint_as_float(w.y << 16), v[3] = __uint_as_float(w.y & 0xffff0000u);
           } else {
 #pragma unroll
             for (int c = 0; c < 4; ++c) v[c] = vd + c < a.dv ? to_f32(src[c]) : 0.f;
@@ -208,29 +171,25 @@ __global__ void __launch_bounds__(kThreads) decode_simt_kernel(DecodeArgs a) {
       }
     }
     __syncthreads();
-    if (starts && ends) {
+    if (pc.starts && pc.ends) {
       for (int e = tid; e < heads * a.dv; e += kThreads) {
         const int g = e / a.dv, d = e - g * a.dv;
         static_cast<T*>(a.o)[b * a.os_b + (h0 + g) * a.os_h + d] = from_f32<T>(ls[g] == 0.f ? 0.f : red[e] / ls[g]);
       }
     } else {
-      float* part = a.part + (2 * cta + (starts ? 1 : 0)) * part_floats(kHeads, a.dv);
-      for (int e = tid; e < heads * a.dv; e += kThreads) part[2 * kHeads + e] = red[e];
-      if (tid < heads) part[tid] = ms[tid], part[kHeads + tid] = ls[tid];
-      if (starts && tid == 0) {
-        const long long last = at - off + sp.tiles - 1;  // the item's last tile
-        a.record[2 * cta] = b * per_seq + item;
-        a.record[2 * cta + 1] = static_cast<int>(run.owner(last) - cta + 1);
-      }
+      float* part = a.part + (2 * cta + (pc.starts ? 1 : 0)) * part_floats(a.item_heads, a.dv);
+      for (int e = tid; e < heads * a.dv; e += kThreads) part[2 * a.item_heads + e] = red[e];
+      if (tid < heads) part[tid] = ms[tid], part[a.item_heads + tid] = ls[tid];
+      if (pc.starts && tid == 0) note_item(a, run, pc, per_seq, cta);
     }
-    at += tiles;
+    at += pc.tiles;
   }
 }
 
 // One item that several CTAs shared: the CTA that holds its start (slot 1)
 // and the ones after it (slot 0).  out = sum w o / sum w l, w = 2^(m - max m).
 template <typename T>
-__global__ void __launch_bounds__(256) decode_join_kernel(DecodeArgs a, int part_heads) {
+__global__ void __launch_bounds__(256) decode_join_kernel(DecodeArgs a) {
   __shared__ __align__(16) float sum_s[8][128];
   __shared__ float l_s[8];
   pdl_wait();
@@ -240,11 +199,11 @@ __global__ void __launch_bounds__(256) decode_join_kernel(DecodeArgs a, int part
   if (rec < 0) return;
   const int per_seq = a.Hkv * a.chunks;
   const int b = rec / per_seq, item = rec - b * per_seq;
-  const int hk = item / a.chunks, h0 = hk * a.group + (item % a.chunks) * part_heads;
-  const int heads = min(part_heads, (hk + 1) * a.group - h0), g = blockIdx.y;
+  const int hk = item / a.chunks, h0 = hk * a.group + (item % a.chunks) * a.item_heads;
+  const int heads = min(a.item_heads, (hk + 1) * a.group - h0), g = blockIdx.y;
   if (g >= heads) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const size_t pf = part_floats(part_heads, a.dv);
+  const size_t pf = part_floats(a.item_heads, a.dv);
   auto part = [&](int i) { return a.part + (i == 0 ? 2 * static_cast<size_t>(cta) + 1 : 2 * (static_cast<size_t>(cta) + i)) * pf; };
   float m = kNegInf;
   for (int i = lane; i < pieces; i += 32) m = fmaxf(m, part(i)[g]);
@@ -255,10 +214,10 @@ __global__ void __launch_bounds__(256) decode_join_kernel(DecodeArgs a, int part
   for (int i = warp; i < pieces; i += 8) {
     const float* p = part(i);
     const float w = exp2_approx(p[g] - mu);
-    l = fmaf(w, p[part_heads + g], l);
+    l = fmaf(w, p[a.item_heads + g], l);
 #pragma unroll
     for (int c = 0; c < 4; ++c)
-      if (lane + 32 * c < a.dv) acc[c] = fmaf(w, p[2 * part_heads + g * a.dv + lane + 32 * c], acc[c]);
+      if (lane + 32 * c < a.dv) acc[c] = fmaf(w, p[2 * a.item_heads + g * a.dv + lane + 32 * c], acc[c]);
   }
   for (int c = 0; c < 4; ++c) sum_s[warp][lane + 32 * c] = acc[c];
   if (lane == 0) l_s[warp] = l;
@@ -279,11 +238,14 @@ size_t simt_smem(int dk, int dv, int B) {
 template <typename T, bool VEC>
 cudaError_t launch_simt(const DecodeArgs& a, cudaStream_t s) {
   const size_t smem = simt_smem(a.dk, a.dv, a.B);
-  cudaError_t e = smem_attr_once<decode_simt_kernel<T, VEC>>(smem);
+  const cudaError_t e = smem_attr_once<decode_simt_kernel<T, VEC>>(smem);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(decode_simt_kernel<T, VEC>, dim3(a.ctas), dim3(kThreads), smem, s, a);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(decode_join_kernel<T>, dim3(a.ctas, a.group < kHeads ? a.group : kHeads), dim3(256), 0, s, a, kHeads);
+  return launch_pdl(decode_simt_kernel<T, VEC>, dim3(a.ctas), dim3(kThreads), smem, s, a);
+}
+
+template <typename T>
+cudaError_t launch_join(const DecodeArgs& a, cudaStream_t s) {
+  return launch_pdl(decode_join_kernel<T>, dim3(a.ctas, a.item_heads), dim3(256), 0, s, a);
 }
 
 }  // namespace
@@ -292,14 +254,14 @@ size_t decode_workspace_bytes(int ctas, int heads, int dv) {
   return sizeof(float) * 2 * ctas * part_floats(heads, dv) + sizeof(int) * 2 * ctas;
 }
 
-int decode_ctas(bool bf16, bool vec, int sms, int dk, int dv) {
-  (void)bf16, (void)vec, (void)dk, (void)dv;
-  return 4 * sms;
-}
-
 cudaError_t launch_decode(const DecodeArgs& a, bool bf16, bool vec, cudaStream_t s) {
-  if (bf16) return vec ? launch_simt<__nv_bfloat16, true>(a, s) : launch_simt<__nv_bfloat16, false>(a, s);
-  return vec ? launch_simt<float, true>(a, s) : launch_simt<float, false>(a, s);
+  cudaError_t e;
+  if (bf16)
+    e = vec ? launch_decode_mma(a, s) : launch_simt<__nv_bfloat16, false>(a, s);
+  else
+    e = vec ? launch_simt<float, true>(a, s) : launch_simt<float, false>(a, s);
+  if (e != cudaSuccess) return e;
+  return bf16 ? launch_join<__nv_bfloat16>(a, s) : launch_join<float>(a, s);
 }
 
 }  // namespace cb

@@ -71,6 +71,61 @@ struct Run {
   }
 };
 
+// The sequence whose tiles hold dealt tile `at`.
+__device__ __forceinline__ int find_seq(const DecodeArgs& a, const unsigned* prefix, int per_seq, long long at) {
+  int lo = 0, hi = a.B;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (static_cast<long long>(prefix[mid]) * per_seq <= at) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// A piece of a run: part or all of one item.
+struct Piece {
+  int b, item, hk, h0, heads;  // item = key head * chunks + chunk; query heads [h0, h0 + heads)
+  int lo, hi, len;             // the sequence's visible tokens; query at position len - 1
+  int tile0, tiles;            // absolute tiles of the sequence
+  bool starts, ends;           // holds the item's first / last tile
+  long long last;              // dealt index of the item's last tile
+};
+__device__ __forceinline__ Piece next_piece(const DecodeArgs& a, const unsigned* prefix, int per_seq, long long at,
+                                            long long end, int* b) {
+  while (static_cast<long long>(prefix[*b + 1]) * per_seq <= at) ++*b;
+  const SeqSpan sp = seq_span(a, *b);
+  const long long in_seq = at - static_cast<long long>(prefix[*b]) * per_seq;
+  Piece p;
+  p.b = *b;
+  p.item = static_cast<int>(in_seq / sp.tiles);
+  const int off = static_cast<int>(in_seq - static_cast<long long>(p.item) * sp.tiles);
+  p.tiles = static_cast<int>(min(static_cast<long long>(sp.tiles - off), end - at));
+  p.tile0 = sp.t0 + off;
+  p.starts = off == 0;
+  p.ends = off + p.tiles == sp.tiles;
+  p.last = at - off + sp.tiles - 1;
+  p.hk = p.item / a.chunks;
+  p.h0 = p.hk * a.group + (p.item % a.chunks) * a.item_heads;
+  p.heads = min(a.item_heads, (p.hk + 1) * a.group - p.h0);
+  p.lo = sp.lo, p.hi = sp.hi, p.len = sp.len;
+  return p;
+}
+
+// Sequences without a visible token: zeros, dealt over the CTAs.
+template <typename Store>
+__device__ __forceinline__ void zero_empty(const DecodeArgs& a, const unsigned* prefix, Store store) {
+  for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+    if (prefix[b + 1] != prefix[b]) continue;
+    for (int e = threadIdx.x; e < a.Hq * a.dv; e += blockDim.x) store(b * a.os_b + e / a.dv * a.os_h + e % a.dv);
+  }
+}
+
+// The CTA that starts an item it does not finish says so, for the join.
+__device__ __forceinline__ void note_item(const DecodeArgs& a, const Run& run, const Piece& p, int per_seq, long long cta) {
+  a.record[2 * cta] = p.b * per_seq + p.item;
+  a.record[2 * cta + 1] = static_cast<int>(run.owner(p.last) - cta + 1);
+}
+
 // Floats of one partial result: per head m, l, then dv unnormalised sums.
 __host__ __device__ inline size_t part_floats(int heads, int dv) { return static_cast<size_t>(heads) * (dv + 2); }
 

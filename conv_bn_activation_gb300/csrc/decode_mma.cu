@@ -1,0 +1,335 @@
+// Attention of one new token per sequence over a paged bf16 cache whose rows
+// are whole 16-byte pieces (cb_attention_decode; decode_common.cuh says how
+// tokens are dealt to the CTAs).
+//
+// Bound by HBM: 2 (dk + dv) bytes per cached token and key head, read once.
+// Up to 16 query heads that share a key head ride along: with 8 of them the
+// products are 8 FLOP per byte, too much conversion and FMA work for the CUDA
+// cores at the memory's rate (a bf16 value feeds 8 FMAs after one conversion;
+// measured 5.6x slower), and too little for tcgen05, whose 128 query rows
+// would be 8 used ones and whose operands would cross shared memory no
+// faster. So the products are warp-level MMAs with the heads as their 16 rows:
+//   S[16 heads x 16 keys] = Q K^T,  P = 2^(x - m),  O[16 heads x dv] += P V.
+// Each warp walks its own 16 keys of every 64-token tile with its own ring of
+// cp.async copies and its own maximum, sum and O, so nothing synchronises
+// inside a run; the four warps are joined when an item's piece ends. O is
+// rescaled only when a maximum grows by more than 2^8. l sums the weights as
+// rounded to bf16 for the second product, so their rounding largely cancels.
+#include "decode_common.cuh"
+#include "launch_util.h"
+#include "ptx.cuh"
+
+namespace cb {
+
+namespace {
+
+constexpr int kWarps = 4, kThreads = kWarps * 32;
+constexpr int kStep = 16;      // keys per warp and step
+constexpr int kStages = 3;
+constexpr float kGrowth = 8.f;
+static_assert(kWarps * kStep == kDecodeTile, "a tile is one step of every warp");
+
+template <int DK, int DV>
+constexpr int stage_bytes() { return kStep * (DK + DV) * 2; }
+template <int DK, int DV>
+constexpr int ring_bytes() {  // also holds the warps' results when a piece ends
+  return kWarps * kStages * stage_bytes<DK, DV>();
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+// d (16 x 8, fp32) += a (16 x 16, bf16) * b (16 x 8, bf16)
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <int DK, int DV>
+__global__ void __launch_bounds__(kThreads, 2) decode_mma_kernel(const DecodeArgs a) {
+  constexpr int kKeyBytes = DK * 2, kValBytes = DV * 2, kStageBytes = stage_bytes<DK, DV>();
+  constexpr int CK = DK / 8, CV = DV / 8;  // 16-byte pieces per row
+  extern __shared__ __align__(128) uint8_t smem[];
+  unsigned* prefix = reinterpret_cast<unsigned*>(smem + ring_bytes<DK, DV>());
+  __shared__ float ms[kWarps][16], ls[kWarps][16];
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // Pieces past dk / dv are never copied: they stay zero.
+  for (int e = tid; e < ring_bytes<DK, DV>() / 16; e += kThreads) reinterpret_cast<uint4*>(smem)[e] = make_uint4(0, 0, 0, 0);
+  pdl_wait();
+  pdl_launch_dependents();
+  tile_prefix(a, prefix);
+  const int per_seq = a.Hkv * a.chunks;
+  const long long total = static_cast<long long>(prefix[a.B]) * per_seq;
+  const Run run{total, min(static_cast<long long>(gridDim.x), max(total, 1LL))};
+  const long long cta = blockIdx.x;
+  if (tid == 0) a.record[2 * cta] = -1;
+  zero_empty(a, prefix, [&](long long at) { static_cast<__nv_bfloat16*>(a.o)[at] = __float2bfloat16_rn(0.f); });
+  if (cta >= run.ctas || total == 0) return;
+  const long long end = run.begin(cta + 1);
+  long long at = run.begin(cta);
+  int b = find_seq(a, prefix, per_seq, at);
+
+  uint8_t* ring = smem + warp * kStages * kStageBytes;
+  const uint32_t ring_addr = smem_u32(ring);
+  const int kq = a.dk / 8, vq = a.dv / 8;  // real pieces per row
+  const float c_scale = a.scale * kLog2e;
+  const bool cap = a.softcap > 0.f, bias = a.slopes != nullptr;
+  const float cap_a = a.softcap * kLog2e, cap_k = cap ? 2.f * c_scale / a.softcap : 0.f;
+  const int g = lane >> 2, t4 = lane & 3;
+
+  while (at < end) {
+    const Piece pc = next_piece(a, prefix, per_seq, at, end, &b);
+    const __nv_bfloat16* kbase = static_cast<const __nv_bfloat16*>(a.cache.k) + pc.hk * a.cache.ks_h;
+    const __nv_bfloat16* vbase = static_cast<const __nv_bfloat16*>(a.cache.v) + pc.hk * a.cache.vs_h;
+
+    // Q as the MMA's A operand: rows g and g + 8, elements 2 t4 and 2 t4 + 8 of each 16
+    uint32_t qf[DK / 16][4];
+#pragma unroll
+    for (int s = 0; s < DK / 16; ++s)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int hd = g + 8 * (r & 1), d = 16 * s + 2 * t4 + 8 * (r >> 1);
+        uint32_t w = 0;
+        if (hd < pc.heads && d < a.dk) {  // dk is even
+          const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + pc.b * a.qs_b + (pc.h0 + hd) * a.qs_h + d;
+          w = static_cast<uint32_t>(__bfloat16_as_ushort(q[0])) | (static_cast<uint32_t>(__bfloat16_as_ushort(q[1])) << 16);
+        }
+        qf[s][r] = w;
+      }
+    float slope[2] = {0.f, 0.f};
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+      if (bias && g + 8 * r < pc.heads) slope[r] = a.slopes[pc.h0 + g + 8 * r] * kLog2e;
+
+    float o[DV / 8][4], m[2] = {kNegInf, kNegInf}, l[2] = {0.f, 0.f};
+#pragma unroll
+    for (int n = 0; n < DV / 8; ++n)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) o[n][r] = 0.f;
+
+    // Lane x < 16 looks token x of a step up, one step before its copies are issued.
+    const int base = pc.tile0 * kDecodeTile + warp * kStep;
+    auto lookup = [&](int step, int* page, int* slot) {
+      const int j = base + step * kDecodeTile + (lane & 15);
+      *page = -1;
+      *slot = 0;
+      if (step < pc.tiles && j >= pc.lo && j < pc.hi) *page = token_page(a, pc.b, j, slot);
+    };
+    unsigned live[kStages];  // bit x: token x of the stage's step exists
+    auto issue = [&](int step, int stage, int page, int slot) {
+      if (step < pc.tiles) {
+        const uint32_t dst = ring_addr + stage * kStageBytes;
+#pragma unroll
+        for (int i = 0; i < kStep * CK / 32; ++i) {
+          const int r = i * (32 / CK) + lane / CK, c = lane % CK;
+          const int pg = __shfl_sync(~0u, page, r), sl = __shfl_sync(~0u, slot, r);
+          if (c < kq)
+            cp_async16(dst + r * kKeyBytes + ((c ^ (r & 7)) * 16), kbase + (pg < 0 ? 0 : pg * a.cache.ks_p + sl * a.cache.ks_t + c * 8), pg >= 0);
+        }
+#pragma unroll
+        for (int i = 0; i < kStep * CV / 32; ++i) {
+          const int r = i * (32 / CV) + lane / CV, c = lane % CV;
+          const int pg = __shfl_sync(~0u, page, r), sl = __shfl_sync(~0u, slot, r);
+          if (c < vq)
+            cp_async16(dst + kStep * kKeyBytes + r * kValBytes + ((c ^ (r & 7)) * 16),
+                       vbase + (pg < 0 ? 0 : pg * a.cache.vs_p + sl * a.cache.vs_t + c * 8), pg >= 0);
+        }
+      }
+      cp_async_commit();
+      return __ballot_sync(~0u, page >= 0) & 0xffffu;
+    };
+
+    int page, slot;
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s) {
+      lookup(s, &page, &slot);
+      live[s] = issue(s, s, page, slot);
+    }
+    lookup(kStages - 1, &page, &slot);
+    int stage = 0;
+    for (int step = 0; step < pc.tiles; ++step) {
+      const int fill = stage == 0 ? kStages - 1 : stage - 1;  // the stage read in the last step
+      __syncwarp();
+      {
+        const unsigned lv = issue(step + kStages - 1, fill, page, slot);
+#pragma unroll
+        for (int s = 0; s < kStages; ++s)
+          if (s == fill) live[s] = lv;
+      }
+      lookup(step + kStages, &page, &slot);
+      cp_async_wait<kStages - 1>();
+      __syncwarp();
+      unsigned lv = 0;
+#pragma unroll
+      for (int s = 0; s < kStages; ++s)
+        if (s == stage) lv = live[s];
+      const uint32_t ks = ring_addr + stage * kStageBytes, vs = ks + kStep * kKeyBytes;
+      float s[2][4];
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) s[n][r] = 0.f;
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int d = 0; d < DK / 32; ++d) {  // keys 8 n .. + 8, dims 32 d .. + 32
+          const int r = 8 * n + (lane & 7), c = 4 * d + (lane >> 3);
+          uint32_t f[4];
+          ldsm4(ks + r * kKeyBytes + ((c ^ (r & 7)) * 16), f);
+          mma16816(s[n], qf[2 * d], f[0], f[1]);
+          mma16816(s[n], qf[2 * d + 1], f[2], f[3]);
+        }
+      // x = log2(e) * score; element (n, r): head g + 8 (r >> 1), key 8 n + 2 t4 + (r & 1)
+      const int j0 = base + step * kDecodeTile;
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          float x = s[n][r];
+          if (cap) {
+            // cap * tanh(s / cap) = cap - 2 cap / (1 + e^(2 s / cap))
+            float den;
+            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(den) : "f"(1.f + exp2_approx(x * cap_k)));
+            x = fmaf(-2.f * cap_a, den, cap_a);
+          } else {
+            x *= c_scale;
+          }
+          const int key = 8 * n + 2 * t4 + (r & 1);
+          if (bias) x = fmaf(-slope[r >> 1], static_cast<float>(pc.len - 1 - j0 - key), x);
+          s[n][r] = x;
+        }
+      if (lv != 0xffffu) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (!((lv >> (8 * n + 2 * t4 + (r & 1))) & 1)) s[n][r] = kNegInf;
+      }
+      bool grow = false;
+      float mx[2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        mx[r] = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
+        mx[r] = fmaxf(mx[r], __shfl_xor_sync(~0u, mx[r], 1));
+        mx[r] = fmaxf(mx[r], __shfl_xor_sync(~0u, mx[r], 2));
+        grow |= mx[r] > m[r] + kGrowth;
+      }
+      if (__any_sync(~0u, grow)) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float mn = fmaxf(m[r], mx[r]);
+          const float f = mn == kNegInf ? 1.f : exp2_approx(m[r] - mn);
+          m[r] = mn;
+          l[r] *= f;
+#pragma unroll
+          for (int n = 0; n < DV / 8; ++n) o[n][2 * r] *= f, o[n][2 * r + 1] *= f;
+        }
+      }
+      uint32_t p[4];
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float mu = m[r] == kNegInf ? 0.f : m[r];
+          const __nv_bfloat162 w = __floats2bfloat162_rn(exp2_approx(s[n][2 * r] - mu), exp2_approx(s[n][2 * r + 1] - mu));
+          l[r] += __low2float(w) + __high2float(w);
+          p[2 * n + r] = *reinterpret_cast<const uint32_t*>(&w);
+        }
+#pragma unroll
+      for (int d = 0; d < DV / 16; ++d) {  // values 16 d .. + 16 of the 16 keys
+        const int r = (lane & 7) + 8 * ((lane >> 3) & 1), c = 2 * d + (lane >> 4);
+        uint32_t f[4];
+        ldsm4_t(vs + r * kValBytes + ((c ^ (r & 7)) * 16), f);
+        mma16816(o[2 * d], p, f[0], f[1]);
+        mma16816(o[2 * d + 1], p, f[2], f[3]);
+      }
+      stage = stage + 1 == kStages ? 0 : stage + 1;
+    }
+    cp_async_wait<0>();
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      l[r] += __shfl_xor_sync(~0u, l[r], 1);
+      l[r] += __shfl_xor_sync(~0u, l[r], 2);
+    }
+    __syncthreads();  // every warp is through with its ring: it now takes the results [warp][heads][DV]
+    float* res = reinterpret_cast<float*>(smem);
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int hd = g + 8 * r;
+      if (t4 == 0) ms[warp][hd] = m[r], ls[warp][hd] = l[r];
+      if (hd < pc.heads)
+#pragma unroll
+        for (int n = 0; n < DV / 8; ++n)
+          *reinterpret_cast<float2*>(res + (warp * pc.heads + hd) * DV + 8 * n + 2 * t4) = make_float2(o[n][2 * r], o[n][2 * r + 1]);
+    }
+    __syncthreads();
+    float* part = a.part + (2 * cta + (pc.starts ? 1 : 0)) * part_floats(a.item_heads, a.dv);
+    const bool whole = pc.starts && pc.ends;
+    for (int e = tid; e < pc.heads * DV; e += kThreads) {
+      const int hd = e / DV, d = e % DV;
+      if (d >= a.dv) continue;
+      float mm = kNegInf;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, ms[w][hd]);
+      const float mu = mm == kNegInf ? 0.f : mm;
+      float sum = 0.f, ll = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float f = exp2_approx(ms[w][hd] - mu);
+        sum = fmaf(f, res[(w * pc.heads + hd) * DV + d], sum);
+        ll = fmaf(f, ls[w][hd], ll);
+      }
+      if (whole) {
+        static_cast<__nv_bfloat16*>(a.o)[pc.b * a.os_b + (pc.h0 + hd) * a.os_h + d] = __float2bfloat16_rn(ll == 0.f ? 0.f : sum / ll);
+      } else {
+        part[2 * a.item_heads + hd * a.dv + d] = sum;
+        if (d == 0) part[hd] = mm, part[a.item_heads + hd] = ll;
+      }
+    }
+    if (!whole && pc.starts && tid == 0) note_item(a, run, pc, per_seq, cta);
+    at += pc.tiles;
+    __syncthreads();
+    // the pieces past dk / dv are zero again
+    if (at < end && (kq < CK || vq < CV)) {
+      for (int e = tid; e < ring_bytes<DK, DV>() / 16; e += kThreads) reinterpret_cast<uint4*>(smem)[e] = make_uint4(0, 0, 0, 0);
+      __syncthreads();
+    }
+  }
+}
+
+template <int DK, int DV>
+cudaError_t launch_dims(const DecodeArgs& a, cudaStream_t s) {
+  const size_t smem = ring_bytes<DK, DV>() + sizeof(unsigned) * (a.B + 1);
+  const cudaError_t e = smem_attr_once<decode_mma_kernel<DK, DV>>(smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(decode_mma_kernel<DK, DV>, dim3(a.ctas), dim3(kThreads), smem, s, a);
+}
+
+}  // namespace
+
+cudaError_t launch_decode_mma(const DecodeArgs& a, cudaStream_t s) {
+  if (a.dk <= 64) return a.dv <= 64 ? launch_dims<64, 64>(a, s) : launch_dims<64, 128>(a, s);
+  return a.dv <= 64 ? launch_dims<128, 64>(a, s) : launch_dims<128, 128>(a, s);
+}
+
+}  // namespace cb

@@ -367,16 +367,17 @@ struct DecodeArgs {
   const float* slopes;
   float scale, softcap;
   int B, Hq, Hkv, group, dk, dv;
-  int chunks;           // items per key head: ceil(group / heads per item)
+  int chunks;           // items per key head
+  int item_heads;       // query heads of one item: ceil(group / chunks)
   float* part;          // workspace: partial results, two per CTA
   int* record;          // workspace: per CTA {item, pieces} of the item it starts and does not finish
   int ctas;             // grid of the main kernel
   int* err;
 };
-constexpr int kDecodeSimtHeads = 8;  // query heads of one item, CUDA-core kernel
+constexpr int kDecodeSimtHeads = 8, kDecodeMmaHeads = 16;  // most query heads of one item
 // Workspace: `ctas` records of two ints, then 2 * ctas partials of `heads` x (dv + 2) floats.
 size_t decode_workspace_bytes(int ctas, int heads, int dv);
-int decode_ctas(bool bf16, bool vec, int sms, int dk, int dv);
+cudaError_t launch_decode_mma(const DecodeArgs& a, cudaStream_t s);  // bf16, rows of whole 16-byte pieces
 cudaError_t launch_decode(const DecodeArgs& a, bool bf16, bool vec, cudaStream_t s);
 
 // ------------------------------------------------------------ watchdog hook

@@ -173,7 +173,7 @@ cb_status cb_attention(const cb_heads* q, const cb_heads* k, const cb_heads* v, 
   CUtensorMap qm, km, vm;
   if (q->dtype == CB_DTYPE_BF16 && vec && k->len >= 1 && k->len <= kAttnTcMaxKeys && tc_map(&qm, q) && tc_map(&km, k) &&
       tc_map(&vm, v))
-    return done(launch_attn_tc(qm, km, vm, a, static_cast<cudaStream_t>(stream)));
+    return done(launch_attn_tc(qm, km, vm, a, sms, static_cast<cudaStream_t>(stream)));
   return done(launch_attn_simt(a, q->dtype == CB_DTYPE_BF16, vec, sms, static_cast<cudaStream_t>(stream)));
 }
 

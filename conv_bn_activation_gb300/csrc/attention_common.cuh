@@ -66,7 +66,7 @@ __device__ __forceinline__ float score_log2(const AttnArgs& a, float dot, float 
 // Here a key that is not visible is never touched, so the row comes out as
 // defined: finite where the visible data is, and infinite or NaN where that is.
 template <typename T>
-__device__ __noinline__ void attn_row(const AttnArgs& a, int b, int h, int i) {
+__device__ __forceinline__ void attn_row_inline(const AttnArgs& a, int b, int h, int i) {
   const int lane = threadIdx.x & 31;
   const T* q = static_cast<const T*>(a.q) + b * a.qs_b + static_cast<long long>(i) * a.qs_l + h * a.qs_h;
   const T* k = static_cast<const T*>(a.k) + b * a.ks_b + (h / a.group) * a.ks_h;
@@ -108,6 +108,12 @@ __device__ __noinline__ void attn_row(const AttnArgs& a, int b, int h, int i) {
   for (int s = 16; s; s >>= 1) l += __shfl_xor_sync(~0u, l, s);
   for (int c = 0; c < 4; ++c)
     if (lane + 32 * c < a.dv) o[lane + 32 * c] = from_f32<T>(l == 0.f ? 0.f : acc[c] / l);
+}
+
+// The same as a call, for kernels whose registers the cold path would burden.
+template <typename T>
+__device__ __noinline__ void attn_row(const AttnArgs& a, int b, int h, int i) {
+  attn_row_inline<T>(a, b, h, i);
 }
 
 }  // namespace cb

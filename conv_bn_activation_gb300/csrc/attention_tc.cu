@@ -1,28 +1,41 @@
 // Attention on the tensor cores: bf16 views of whole 16-byte pieces.
 //
-// One CTA owns 256 queries of one head as two tiles t of 128 and walks the
-// visible key tiles of 128 with a running maximum and sum per query:
+// Persistent CTAs, one per SM. An item is 256 queries of one head, as two
+// tiles t of 128, which walks the visible key tiles of 128 with a running
+// maximum and sum per query:
 //   S_t = Q_t K^T        tcgen05.mma, both operands in shared memory (TMA, 128-byte swizzle),
 //                        fp32 accumulator in 128 TMEM columns
-//   P_t = 2^(x - m)      x = log2(e) * score, by one warpgroup per tile, a thread per query:
-//                        tcgen05.ld of its 128 scores, P rounded to bf16 and stored over S_t
+//   P_t = 2^(x - m)      x = log2(e) * score, rounded to bf16 and stored over S_t
 //   O_t += P_t V         tcgen05.mma with A = P_t from TMEM and B = V as it lies (rows of keys:
 //                        the MN-major operand), O_t in up to 128 further columns
-// The tiles take turns: while one warpgroup computes P of tile 0, the tensor
-// cores work on tile 1.  One thread issues, in the order
+// Per pair of 128 x 128 tiles and 128 dims the MMAs take 2048 cycles of an SM
+// and the softmax about 900 issue slots of each scheduler; what decides is the
+// chain S -> P -> next S of one tile. So the two tiles take turns (the tensor
+// cores work on one while the other's weights are computed), a thread holds a
+// query's 128 scores in packed fp32 pairs, the first 64 weights are handed to
+// the MMAs while the other 64 are computed, and nothing waits between items:
+// copies run ahead through a ring that items share, a scheduler warp lists the
+// next item's key tiles, and the first MMAs of an item run under the output of
+// the one before.
+//
+// One thread issues all MMAs, in the order
 //   PV_0(n), QK_0(n+1), PV_1(n), QK_1(n+1),
 // so S_t is overwritten only by an MMA issued after the one that reads P_t, and
-// the commit after QK_t(n+1) also covers PV_t(n): once a warpgroup sees S_t(n+1)
-// it may rescale O_t without another barrier.
+// the commit after QK_t(n+1) also covers PV_t(n): once the softmax warps see
+// S_t(n+1) they may rescale O_t without another barrier.
 //
-// O is rescaled only when a query's maximum has grown by more than 2^8 since
-// the last time; until then weights are relative to the older maximum (at most
-// 2^8, exact in fp32 and of the same relative precision in bf16) and l and O
-// agree on it.  P is rounded to bf16 for the second product (2^-9 relative at
-// most to nearest, independent from key to key); l sums the unrounded weights.
+// Weights are relative to m_ref, the maximum of a query's first visible tile,
+// and stay so until a score exceeds it by 2^64: fp32 sums and bf16 weights keep
+// their relative precision at any such scale, so the running maximum is needed
+// only against overflow. A tile's weights therefore do not wait for its
+// maximum; it is found beside the first 64 exponentials, and only if it grew
+// that far are l, O and those weights redone. P is rounded to bf16 for the
+// second product (each weight to nearest, independent from key to key); l sums
+// the unrounded weights.
 //
-// Key tiles no query of the CTA sees are never loaded: a list of the tiles to
-// visit, with each query tile's state (skip, full, masked), is made first.
+// Key tiles no query of the item sees are never loaded: the list of the tiles
+// to visit holds each query tile's state (skip, full, masked), nearest keys
+// first: a bias by distance then has its largest scores in the first tile.
 #include "attention_common.cuh"
 #include "launch_util.h"
 #include "ptx.cuh"
@@ -33,15 +46,11 @@ namespace {
 
 constexpr int kTile = 128;          // queries per tile, keys per tile
 constexpr int kSlab = 128 * 128;    // bytes of 128 rows x 64 bf16
-// Two softmax warpgroups and a third with the copy warp, the MMA warp and two
-// idle ones: at launch every thread holds 168 registers (the most for 12
-// warps), then the third warpgroup hands its own to the other two, whose
-// threads keep 128 scores each: 2 * 128 * 224 + 128 * 56 = 384 * 168.
-constexpr int kThreads = 384;
-constexpr int kSoftmaxRegs = 224, kOtherRegs = 56;
-static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * 168, "registers of the launch");
-constexpr int kCopyWarp = 8, kMmaWarp = 9;
-constexpr float kGrowth = 8.f;      // rescale when the maximum grew by more (log2)
+constexpr int kSoftmaxWarps = 8;    // two warpgroups, one per tile
+constexpr int kCopyWarp = 8, kMmaWarp = 9, kListWarp = 10, kTailWarp = 11;
+constexpr int kThreads = 384;       // 168 registers per thread
+constexpr float kGrowth = 64.f;     // rescale when the maximum grew by more (log2)
+constexpr int kListReaders = kSoftmaxWarps + 3;
 
 __device__ __forceinline__ void tmem_ld_x32f(uint32_t taddr, float* r) {
   asm volatile(
@@ -53,14 +62,11 @@ __device__ __forceinline__ void tmem_ld_x32f(uint32_t taddr, float* r) {
         "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
       : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t* r) {
+__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t* r) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
@@ -94,53 +100,135 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
+
+// Packed pairs of fp32 (fma.rn.f32x2: each lane an fmaf): half the issue slots.
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 pack2(float a, float b) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(f2 v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// tanh(y) = y Q(y^2) for |y| <= 1, |error| <= 2.8e-6 (a minimax fit of degree 4
+// in y^2): 3.5 packed operations per score on the FMA pipe, where
+// 1 - 2 / (1 + e^(2 y)) takes two of the exponential unit's, which has none to
+// spare. Scores rarely pass their cap; a warp that holds one that does takes
+// the exact form for its tile.
+__device__ __forceinline__ f2 tanh2(f2 y) {
+  const f2 z = mul2(y, y);
+  f2 q = fma2(z, pack2(0.008365880697965622f, 0.008365880697965622f), pack2(-0.043299853801727295f, -0.043299853801727295f));
+  q = fma2(z, q, pack2(0.12922066450119019f, 0.12922066450119019f));
+  q = fma2(z, q, pack2(-0.33265823125839233f, -0.33265823125839233f));
+  q = fma2(z, q, pack2(0.9999684691429138f, 0.9999684691429138f));
+  return mul2(y, q);
+}
+
 enum : uint32_t { kSkip = 0, kFull = 1, kMasked = 2 };
+
+// What the scheduler warp says about an item.
+struct ItemInfo {
+  int n;       // tiles in the list
+  int kv;      // keys of the sequence
+  int prefix;
+  int tail;    // 1: the tile of key kv, if listed, holds rows past it, whose values must become zero
+};
 
 template <int SK, int SV>
 struct Shape {
   static constexpr int kSlot = (SK > SV ? SK : SV) * kSlab;  // one ring slot: a K or a V tile
   static constexpr int kStages = SK == 2 || SV == 2 ? 4 : 8;
   static constexpr int kQ = 2 * SK * kSlab;
-  static constexpr int kFixed = kQ + kStages * kSlot + 8 * kTile * 4 /* doc ids */ + 512 /* barriers */ + 1024 /* alignment */;
+  static constexpr int kFixed = kQ + kStages * kSlot + kSoftmaxWarps * kTile * 4 /* doc ids */ +
+                                4 * kTile * 4 /* bias by key */ + 1024 /* barriers, item infos */ + 1024 /* alignment */;
 };
+
+// Work items of the launch, longest first (under a causal mask the last query
+// tiles).  CTA c takes items c, 2 g - 1 - c, 2 g + c, ... of g CTAs: turning
+// round after each row evens long and short ones out.
+__device__ __forceinline__ int item_of(int k) {
+  return k * gridDim.x + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+}
+struct Item {
+  int b, h, i0;
+};
+__device__ __forceinline__ Item item_at(const AttnArgs& a, int q_tiles, int item) {
+  const int heads = a.B * a.Hq, bh = item % heads;
+  return {bh / a.Hq, bh % a.Hq, (q_tiles - 1 - item / heads) * 2 * kTile};
+}
 
 template <int SK, int SV>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
-               const __grid_constant__ CUtensorMap vmap, const AttnArgs a, int q_tiles) {
+               const __grid_constant__ CUtensorMap vmap, const AttnArgs a, int q_tiles, int items, int list_len) {
   using SH = Shape<SK, SV>;
   constexpr int NS = SH::kStages;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem;
   uint8_t* sKV = smem + SH::kQ;
-  int* doc_buf = reinterpret_cast<int*>(sKV + NS * SH::kSlot);  // [8 warps][128]
-  uint64_t* q_full = reinterpret_cast<uint64_t*>(doc_buf + 8 * kTile);
-  uint64_t* kv_full = q_full + 2;
+  int* doc_buf = reinterpret_cast<int*>(sKV + NS * SH::kSlot);                // [8 warps][128]
+  float* bias_buf = reinterpret_cast<float*>(doc_buf + kSoftmaxWarps * kTile);  // [2 lists][2 signs][128]: +-log2(e) slope * key
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(bias_buf + 4 * kTile);
+  uint64_t* q_empty = q_full + 2;
+  uint64_t* kv_full = q_empty + 2;
   uint64_t* kv_empty = kv_full + NS;
   uint64_t* s_full = kv_empty + NS;
-  uint64_t* p_ready = s_full + 2;
-  uint64_t* o_full = p_ready + 2;
-  uint64_t* v_tail = o_full + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(v_tail + 1);
+  uint64_t* p_ready = s_full + 2;  // [2 tiles][2 halves of the keys]
+  uint64_t* o_full = p_ready + 4;
+  uint64_t* o_free = o_full + 2;
+  uint64_t* list_full = o_free + 2;
+  uint64_t* list_free = list_full + 2;
+  uint64_t* tail_go = list_free + 2;  // the MMA thread has seen the values of a tail tile arrive
+  uint64_t* v_tail = tail_go + 1;  // their rows past the end are zero
+  ItemInfo* info = reinterpret_cast<ItemInfo*>(v_tail + 1);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(info + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int* shared_n = reinterpret_cast<int*>(tmem_slot + 2);  // tiles in the list
-  int* doc_range = shared_n + 1;                          // per query tile: min, max, any padding
-  uint32_t* list = reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(q_full) + 512);
+  uint32_t* lists = reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(q_full) + 1024);  // [2][list_len]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int t = 0; t < 2; ++t) {
       mbar_init(&q_full[t], 1);
+      mbar_init(&q_empty[t], 1);
       mbar_init(&s_full[t], 1);
-      mbar_init(&p_ready[t], 4);
+      mbar_init(&p_ready[2 * t], 4);
+      mbar_init(&p_ready[2 * t + 1], 4);
       mbar_init(&o_full[t], 1);
-      doc_range[3 * t] = 0x7fffffff, doc_range[3 * t + 1] = -1, doc_range[3 * t + 2] = 0;
+      mbar_init(&o_free[t], 4);
+      mbar_init(&list_full[t], 1);
+      mbar_init(&list_free[t], kListReaders);
     }
     for (int s = 0; s < NS; ++s) {
       mbar_init(&kv_full[s], 1);
       mbar_init(&kv_empty[s], 1);
     }
+    mbar_init(tail_go, 1);
     mbar_init(v_tail, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -156,339 +244,536 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
   pdl_wait();
   const uint32_t tmem = *tmem_slot;
   const Watchdog wd{a.err, abort_flag, a.timeout_ns};
+  const int rounds = (items + gridDim.x - 1) / gridDim.x;
 
-  // Last query tiles first: under a causal mask they are the longest.
-  const int heads = a.B * a.Hq;
-  const int qt = q_tiles - 1 - static_cast<int>(blockIdx.x / heads);
-  const int bh = blockIdx.x % heads, b = bh / a.Hq, h = bh % a.Hq, hk = h / a.group;
-  const int i0 = qt * 2 * kTile;
-  const SeqRule rule = seq_rule(a, b);
-  const bool docs = a.doc_k != nullptr;
-  const int* doc_k = docs ? a.doc_k + static_cast<long long>(b) * a.Lk : nullptr;
-
-  // ------------------------------------------------------------ the list
-  int my_row = 0, my_doc = 0, my_hi = 0;  // warpgroups: this thread's query
-  if (warp < 8) {
-    my_row = i0 + threadIdx.x;
-    if (my_row < a.Lq) {
-      my_hi = row_end(a, rule, my_row);
-      if (docs) my_doc = a.doc_q[static_cast<long long>(b) * a.Lq + my_row];
-      if (my_doc < 0) my_hi = 0;
-    }
-    if (docs) {
-      const int t = warp >> 2;
-      const bool row = my_row < a.Lq;
-      const int lo = __reduce_min_sync(~0u, row && my_doc >= 0 ? my_doc : 0x7fffffff);
-      const int hi = __reduce_max_sync(~0u, row && my_doc >= 0 ? my_doc : -1);
-      const bool pad = __any_sync(~0u, row && my_doc < 0);
-      if (lane == 0) {
-        atomicMin(&doc_range[3 * t], lo);
-        atomicMax(&doc_range[3 * t + 1], hi);
-        if (pad) doc_range[3 * t + 2] = 1;
-      }
-    }
-  }
-  int hi_lo[2], hi_hi[2];  // per query tile: keys that all / some of its queries see, before documents
-  for (int t = 0; t < 2; ++t) {
-    const int r0 = i0 + t * kTile, r1 = min(a.Lq, r0 + kTile) - 1;
-    hi_lo[t] = r0 <= r1 ? row_end(a, rule, r0) : 0;
-    hi_hi[t] = r0 <= r1 ? row_end(a, rule, r1) : 0;
-  }
-  const int all_tiles = (max(hi_hi[0], hi_hi[1]) + kTile - 1) / kTile;
-  if (docs) __syncthreads();
-  if (!docs) {
-    for (int n = threadIdx.x; n < all_tiles; n += kThreads) {
-      uint32_t e = n << 4;
-      for (int t = 0; t < 2; ++t)
-        e |= (n * kTile >= hi_hi[t] ? kSkip : (n + 1) * kTile <= hi_lo[t] ? kFull : kMasked) << (2 * t);
-      list[n] = e;
-    }
-    if (threadIdx.x == 0) *shared_n = all_tiles;
-  } else {
-    for (int n = warp; n < all_tiles; n += kThreads / 32) {
-      int lo = 0x7fffffff, hi = -0x7fffffff;
-      for (int c = lane; c < kTile; c += 32) {
-        const int j = n * kTile + c;
-        if (j < rule.kv) lo = min(lo, doc_k[j]), hi = max(hi, doc_k[j]);
-      }
-      lo = __reduce_min_sync(~0u, lo);
-      hi = __reduce_max_sync(~0u, hi);
-      uint32_t e = n << 4;
-      for (int t = 0; t < 2; ++t) {
-        const int dlo = doc_range[3 * t], dhi = doc_range[3 * t + 1];
-        uint32_t st = n * kTile >= hi_hi[t] || hi < dlo || lo > dhi ? kSkip : kMasked;
-        if (st == kMasked && lo == hi && dlo == dhi && lo == dlo && !doc_range[3 * t + 2] && (n + 1) * kTile <= hi_lo[t])
-          st = kFull;
-        e |= st << (2 * t);
-      }
-      if (lane == 0) list[n] = e;
-    }
-    __syncthreads();
-    if (warp == 0) {  // drop the tiles no query sees
-      int kept = 0;
-      for (int n0 = 0; n0 < all_tiles; n0 += 32) {
-        const uint32_t e = n0 + lane < all_tiles ? list[n0 + lane] : 0;
-        const unsigned keep = __ballot_sync(~0u, (e & 15u) != 0);
-        __syncwarp();
-        if (e & 15u) list[kept + __popc(keep & ((1u << lane) - 1))] = e;
-        kept += __popc(keep);
-        __syncwarp();
-      }
-      if (lane == 0) *shared_n = kept;
-    }
-  }
-  __syncthreads();
-  const int N = *shared_n;
-  // A last tile that holds keys past kv_len: their values, whatever they are, become zero.
-  const bool tail = N > 0 && static_cast<int>(list[N - 1] >> 4) * kTile + kTile > rule.kv && rule.kv < a.Lk;
-
-  if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp == kCopyWarp) {
-      // ---------------------------------------------------------- copies
-      // Lane s owns ring slot s (copies of one thread complete one after
-      // another, copies of several overlap); sequence K0, V0, K1, V1, ...
+  if (warp >= kSoftmaxWarps) {
+    if (warp == kListWarp) {
+      // ------------------------------------------------------------ lists
       bool ok = true;
-      if (lane == 0 && N > 0) {
+      for (int k = 0, item; ok && k < rounds; ++k) {
+        if ((item = item_of(k)) >= items) break;
+        const int buf = k & 1;
+        if (k >= 2) ok = mbar_wait(&list_free[buf], ((k >> 1) - 1) & 1u, wd);
+        ok = __all_sync(~0u, ok);
+        if (!ok) break;
+        const Item it = item_at(a, q_tiles, item);
+        const SeqRule rule = seq_rule(a, it.b);
+        uint32_t* list = lists + buf * list_len;
+        int hi_lo[2], hi_hi[2];  // per query tile: keys that all / some of its queries see, before documents
+        for (int t = 0; t < 2; ++t) {
+          const int r0 = it.i0 + t * kTile, r1 = min(a.Lq, r0 + kTile) - 1;
+          hi_lo[t] = r0 <= r1 ? row_end(a, rule, r0) : 0;
+          hi_hi[t] = r0 <= r1 ? row_end(a, rule, r1) : 0;
+        }
+        const int all = (max(hi_hi[0], hi_hi[1]) + kTile - 1) / kTile;
+        int kept = 0;
+        if (!a.doc_k) {
+          // from the tile of the item's last query down to the first, then the ones past it
+          const int near = min(all, max(0, (min(a.Lq, it.i0 + 2 * kTile) - 1 + a.q_offset) / kTile + 1));
+          for (int x = lane; x < all; x += 32) {
+            const int n = x < near ? near - 1 - x : x;
+            uint32_t e = n << 4;
+            for (int t = 0; t < 2; ++t)
+              e |= (n * kTile >= hi_hi[t] ? kSkip : (n + 1) * kTile <= hi_lo[t] ? kFull : kMasked) << (2 * t);
+            list[x] = e;
+          }
+          kept = all;
+        } else {
+          int dlo[2], dhi[2];  // documents of each tile's queries; hi_lo = 0 where one is padding
+          for (int t = 0; t < 2; ++t) {
+            int lo = 0x7fffffff, hi = -1, pad = 0;
+            for (int c = lane; c < kTile; c += 32) {
+              const int i = it.i0 + t * kTile + c;
+              const int d = i < a.Lq ? a.doc_q[static_cast<long long>(it.b) * a.Lq + i] : -1;
+              if (d >= 0) lo = min(lo, d), hi = max(hi, d);
+              pad |= i < a.Lq && d < 0;
+            }
+            dlo[t] = __reduce_min_sync(~0u, lo);
+            dhi[t] = __reduce_max_sync(~0u, hi);
+            if (__any_sync(~0u, pad)) hi_lo[t] = 0;
+          }
+          const int* doc_k = a.doc_k + static_cast<long long>(it.b) * a.Lk;
+          constexpr int kBatch = 4;  // tiles whose ids are in flight together
+          const int first = all - 1;  // last tile first
+          for (int n0 = 0; n0 < all; n0 += kBatch) {
+            int lo[kBatch], hi[kBatch];
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+              int d[4];
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                const int j = (first - n0 - u) * kTile + c * 32 + lane;
+                d[c] = j >= 0 && j < rule.kv ? __ldg(doc_k + j) : -1;
+              }
+              // the tile's ids; a key past the end counts as padding
+              lo[u] = min(min(d[0], d[1]), min(d[2], d[3]));
+              hi[u] = max(max(d[0], d[1]), max(d[2], d[3]));
+            }
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+              const int n = first - n0 - u;
+              const int l = __reduce_min_sync(~0u, lo[u]), h = __reduce_max_sync(~0u, hi[u]);
+              uint32_t e = 0;
+              for (int t = 0; t < 2; ++t) {
+                uint32_t st = n * kTile >= hi_hi[t] || h < dlo[t] || l > dhi[t] ? kSkip : kMasked;
+                if (st == kMasked && l == h && dlo[t] == dhi[t] && l == dlo[t] && (n + 1) * kTile <= hi_lo[t]) st = kFull;
+                e |= st << (2 * t);
+              }
+              if (e && n >= 0) {
+                if (lane == 0) list[kept] = e | (n << 4);
+                ++kept;
+              }
+            }
+          }
+        }
+        if (a.slopes) {
+          const float slope = a.slopes[it.h] * kLog2e;
+          for (int c = lane; c < kTile; c += 32) {
+            bias_buf[buf * 2 * kTile + c] = slope * static_cast<float>(c);
+            bias_buf[buf * 2 * kTile + kTile + c] = -slope * static_cast<float>(c);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) {
+          info[buf] = {kept, rule.kv, rule.prefix, rule.kv < a.Lk && rule.kv % kTile != 0};
+          mbar_arrive(&list_full[buf]);
+        }
+      }
+    } else if (warp == kCopyWarp) {
+      // ----------------------------------------------------------- copies
+      // Lane s owns ring slot s (copies of one thread complete one after
+      // another, copies of several overlap) of the sequence K0, V0, K1, V1,
+      // ... that runs on from item to item; two further lanes own Q_0, Q_1.
+      if (lane == 0) {
         tma_prefetch_desc(&qmap);
         tma_prefetch_desc(&kmap);
         tma_prefetch_desc(&vmap);
       }
-      if (lane >= NS && lane < NS + 2 && N > 0) {
-        const int t = lane - NS;
-        mbar_arrive_expect_tx(&q_full[t], SK * kSlab);
-        for (int s = 0; s < SK; ++s)
-          tma_load_4d(sQ + (t * SK + s) * kSlab, &qmap, &q_full[t], s * 64, h, i0 + t * kTile, b);
-      }
-      uint32_t use = 0;  // fills of this lane's slot so far
-      if (lane < NS) {
-        for (int q = lane; ok && q < 2 * N; q += NS, ++use) {
-          if (use && !mbar_wait(&kv_empty[lane], (use - 1) & 1u, wd)) {
-            ok = false;
-            break;
+      bool ok = true;
+      uint32_t use = 0;  // fills of this lane's slot or Q tile so far
+      long long base = 0;
+      for (int k = 0, item; ok && k < rounds; ++k) {
+        if ((item = item_of(k)) >= items) break;
+        const int buf = k & 1;
+        ok = mbar_wait(&list_full[buf], (k >> 1) & 1u, wd);
+        ok = __all_sync(~0u, ok);
+        if (!ok) break;
+        const int n = info[buf].n;
+        const Item it = item_at(a, q_tiles, item);
+        const uint32_t* list = lists + buf * list_len;
+        if (n > 0 && lane >= NS && lane < NS + 2) {
+          const int t = lane - NS;
+          ok = use == 0 || mbar_wait(&q_empty[t], (use - 1) & 1u, wd);
+          if (ok) {
+            mbar_arrive_expect_tx(&q_full[t], SK * kSlab);
+            for (int s = 0; s < SK; ++s)
+              tma_load_4d(sQ + (t * SK + s) * kSlab, &qmap, &q_full[t], s * 64, it.h, it.i0 + t * kTile, it.b);
+            ++use;
           }
-          const int j0 = static_cast<int>(list[q >> 1] >> 4) * kTile;
-          const bool is_v = q & 1;
-          mbar_arrive_expect_tx(&kv_full[lane], (is_v ? SV : SK) * kSlab);
-          for (int s = 0; s < (is_v ? SV : SK); ++s)
-            tma_load_4d(sKV + lane * SH::kSlot + s * kSlab, is_v ? &vmap : &kmap, &kv_full[lane], s * 64, hk, j0, b);
         }
-      }
-      __syncwarp();
-      if (tail) {
-        const int q = 2 * N - 1, slot = q % NS;
-        const bool got = mbar_wait(&kv_full[slot], (q / NS) & 1u, wd);
-        if (got) {
-          const int r0 = rule.kv % kTile;
-          for (int s = 0; s < SV; ++s)
-            for (int e = r0 * 8 + lane; e < kTile * 8; e += 32)
-              *reinterpret_cast<uint4*>(sKV + slot * SH::kSlot + s * kSlab + e * 16) = make_uint4(0, 0, 0, 0);
-          fence_async_shared();
+        if (lane < NS) {
+          const int hk = it.h / a.group;
+          // this lane's first place in the item: base + q == lane mod NS
+          for (int q = (lane - static_cast<int>(base % NS) + NS) % NS; q < 2 * n; q += NS) {
+            ok = use == 0 || mbar_wait(&kv_empty[lane], (use - 1) & 1u, wd);
+            if (!ok) break;
+            const int j0 = static_cast<int>(list[q >> 1] >> 4) * kTile;
+            const bool is_v = q & 1;
+            mbar_arrive_expect_tx(&kv_full[lane], (is_v ? SV : SK) * kSlab);
+            for (int s = 0; s < (is_v ? SV : SK); ++s)
+              tma_load_4d(sKV + lane * SH::kSlot + s * kSlab, is_v ? &vmap : &kmap, &kv_full[lane], s * 64, hk, j0, it.b);
+            ++use;
+          }
         }
-        __syncwarp();
-        if (lane == 0 && got) mbar_arrive(v_tail);
+        base += 2 * n;
+        ok = __all_sync(~0u, ok);
+        if (lane == 0) mbar_arrive(&list_free[buf]);
       }
       // Every copy lands before the CTA can exit.
-      if (lane < NS && use) mbar_wait_drain(&kv_full[lane], (use - 1) & 1u, 20000000ull);
-      if (lane >= NS && lane < NS + 2 && N > 0) mbar_wait_drain(&q_full[lane - NS], 0, 20000000ull);
-    } else if (warp == kMmaWarp) {
+      if (use && lane < NS) mbar_wait_drain(&kv_full[lane], (use - 1) & 1u, 20000000ull);
+      if (use && lane >= NS && lane < NS + 2) mbar_wait_drain(&q_full[lane - NS], (use - 1) & 1u, 20000000ull);
+    } else if (warp == kTailWarp) {
+      // --------------------------------- values past a sequence's end: zero
+      bool ok = true;
+      uint32_t base = 0, tails = 0;
+      for (int k = 0, item; ok && k < rounds; ++k) {
+        if ((item = item_of(k)) >= items) break;
+        const int buf = k & 1;
+        ok = __all_sync(~0u, mbar_wait(&list_full[buf], (k >> 1) & 1u, wd));
+        if (!ok) break;
+        const ItemInfo inf = info[buf];
+        int slot_of = -1;  // ring slot of the values of the tile that holds key kv
+        if (inf.tail)
+          for (int n = lane; n < inf.n; n += 32)
+            if (static_cast<int>(lists[buf * list_len + n] >> 4) == inf.kv / kTile)
+              slot_of = static_cast<int>((base + 2 * n + 1) % NS);
+        slot_of = __reduce_max_sync(~0u, slot_of);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&list_free[buf]);
+        base += 2 * inf.n;
+        if (slot_of < 0) continue;
+        ok = __all_sync(~0u, mbar_wait(tail_go, tails++ & 1u, wd));
+        if (!ok) break;
+        uint8_t* values = sKV + slot_of * SH::kSlot;
+        for (int s = 0; s < SV; ++s)
+          for (int e = (inf.kv % kTile) * 8 + lane; e < kTile * 8; e += 32)
+            *reinterpret_cast<uint4*>(values + s * kSlab + e * 16) = make_uint4(0, 0, 0, 0);
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(v_tail);
+      }
+    } else {
       // ------------------------------------------------------------- MMAs
-      if (lane == 0 && N > 0) {
-        const uint32_t idesc_s = idesc_bf16(kTile, kTile);
-        const int dvn = (a.dv + 15) & ~15;
-        const uint32_t idesc_o = idesc_bf16(kTile, dvn) | (1u << 16);  // B is MN-major
-        const int ksteps = (a.dk + 15) / 16;
-        const uint32_t q_addr = smem_u32(sQ), kv_addr = smem_u32(sKV);
-        uint32_t done[2] = {0, 0};  // tiles whose P was consumed
-        auto qk = [&](int t, int slot) {
-          for (int s = 0; s < ksteps; ++s)
-            mma_bf16(tmem + t * kTile, kmajor_swizzled_desc(q_addr + (t * SK + (s >> 2)) * kSlab + (s & 3) * 32, 128),
-                     kmajor_swizzled_desc(kv_addr + slot * SH::kSlot + (s >> 2) * kSlab + (s & 3) * 32, 128), idesc_s, s > 0);
-          mma_commit(&s_full[t]);
-        };
-        bool ok = mbar_wait(&kv_full[0], 0, wd);
-        for (int t = 0; ok && t < 2; ++t) {
-          ok = mbar_wait(&q_full[t], 0, wd);
+      // The whole warp walks the steps together and one elected lane issues,
+      // so that descriptors stay in uniform registers.  They advance by
+      // 16-byte units in their low word; the high word is a constant.
+      // (Built anew by a lone lane, each took longer than its MMA: 75 to 150
+      // cycles against 64.)
+      const uint32_t idesc_s = idesc_bf16(kTile, kTile);
+      const uint32_t idesc_o = idesc_bf16(kTile, (a.dv + 15) & ~15) | (1u << 16);  // B is MN-major
+      const uint32_t q_lo = static_cast<uint32_t>(kmajor_swizzled_desc(smem_u32(sQ), 128));
+      const uint32_t k_lo = static_cast<uint32_t>(kmajor_swizzled_desc(smem_u32(sKV), 128));
+      const uint32_t v_lo = static_cast<uint32_t>(mnmajor_desc(smem_u32(sKV)));
+      constexpr uint64_t kHi = (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
+      const bool leader = elect_one();
+      bool ok = true;
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        ok = __all_sync(~0u, ok && mbar_wait(bar, parity & 1u, wd));
+        return ok;
+      };
+      // One key tile of one item; `seq`: its K's place in the ring's sequence.
+      struct Step {
+        uint32_t e;
+        bool first, last, tail;
+        uint32_t seq;
+      };
+      int k = -1, n = 0, count = 0, tail_tile = -1;
+      uint32_t seq = 0, tails = 0;
+      auto fetch = [&](Step* s) {  // false: no further step (or a wait gave up)
+        while (n == count) {
+          ++k;
+          if (k >= rounds || item_of(k) >= items) return false;
+          if (!wait(&list_full[k & 1], k >> 1)) return false;
+          n = 0;
+          count = __shfl_sync(~0u, info[k & 1].n, 0);
+          tail_tile = __shfl_sync(~0u, info[k & 1].tail ? info[k & 1].kv / kTile : -1, 0);
+          if (count == 0 && leader) mbar_arrive(&list_free[k & 1]);
+        }
+        s->e = __shfl_sync(~0u, lists[(k & 1) * list_len + n], 0);
+        s->first = n == 0;
+        s->last = ++n == count;
+        s->tail = static_cast<int>(s->e >> 4) == tail_tile;
+        s->seq = seq;
+        seq += 2;
+        if (s->last && leader) mbar_arrive(&list_free[k & 1]);
+        return true;
+      };
+      uint32_t q_items = 0;  // items with keys so far
+      uint32_t q_have[2] = {0, 0}, p_seen[2] = {0, 0}, o_items[2] = {0, 0}, in_item[2] = {0, 0};
+      auto state = [](const Step& s, int t) { return (s.e >> (2 * t)) & 3u; };
+      auto qk = [&](const Step& s, int t) {
+        if (!state(s, t)) return;
+        if (q_have[t] != q_items) {  // the item's Q_t
+          q_have[t] = q_items;
+          if (!wait(&q_full[t], q_items - 1)) return;
           tc_fence_after_sync();
-          if (ok && ((list[0] >> (2 * t)) & 3u)) qk(t, 0);
         }
-        if (ok) mma_commit(&kv_empty[0]);
-        for (int n = 0; ok && n < N; ++n) {
-          const uint32_t e = list[n], en = n + 1 < N ? list[n + 1] : 0;
-          const int vq = 2 * n + 1, vs = vq % NS, kq = 2 * n + 2, ks = kq % NS;
-          ok = mbar_wait(&kv_full[vs], (vq / NS) & 1u, wd);
-          if (ok && tail && n + 1 == N) ok = mbar_wait(v_tail, 0, wd);
-          for (int t = 0; ok && t < 2; ++t) {
-            if ((e >> (2 * t)) & 3u) {
-              ok = mbar_wait(&p_ready[t], done[t] & 1u, wd);
-              if (!ok) break;
+        const uint32_t ql = q_lo + t * (SK * kSlab >> 4), kl = k_lo + s.seq % NS * (SH::kSlot >> 4);
+        if (leader) {
+#pragma unroll
+          for (int x = 0; x < 4 * SK; ++x) {  // dims past dk are zero in both operands
+            const uint32_t off = ((x >> 2) * kSlab + (x & 3) * 32) >> 4;
+            mma_bf16(tmem + t * kTile, kHi | (ql + off), kHi | (kl + off), idesc_s, x > 0);
+          }
+          mma_commit(&s_full[t]);
+        }
+        __syncwarp();
+      };
+      auto k_wait = [&](const Step& s) {
+        if (s.first) ++q_items;
+        wait(&kv_full[s.seq % NS], s.seq / NS);
+        tc_fence_after_sync();
+      };
+      auto k_done = [&](const Step& s) {
+        if (leader) {
+          mma_commit(&kv_empty[s.seq % NS]);
+          if (s.last) {
+            mma_commit(&q_empty[0]);
+            mma_commit(&q_empty[1]);
+          }
+        }
+        __syncwarp();
+      };
+      Step cur, nxt;
+      bool have = fetch(&cur);
+      if (have) {
+        k_wait(cur);
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          if (ok) qk(cur, t);
+        if (ok) k_done(cur);
+      }
+      while (ok && have) {
+        const bool more = fetch(&nxt);
+        if (!ok) break;
+        const uint32_t vq = cur.seq + 1, vs = vq % NS, vl = v_lo + vs * (SH::kSlot >> 4);
+        wait(&kv_full[vs], vq / NS);
+        if (ok && cur.tail) {
+          if (leader) mbar_arrive(tail_go);
+          wait(v_tail, tails++);
+        }
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (!ok) break;
+          if (state(cur, t)) {
+            if (in_item[t] == 0 && o_items[t] > 0) wait(&o_free[t], o_items[t] - 1);
+            const uint32_t fresh = in_item[t] == 0;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {  // 64 keys' weights each
+              if (!ok || !wait(&p_ready[2 * t + half], p_seen[t])) break;
               tc_fence_after_sync();
-              for (int s = 0; s < kTile / 16; ++s)
-                mma_bf16_ts(tmem + 2 * kTile + t * SV * 64, tmem + t * kTile + s * 8,
-                            mnmajor_desc(kv_addr + vs * SH::kSlot + s * 2048), idesc_o, done[t] > 0 || s > 0);
-              ++done[t];
-            }
-            if (n + 1 < N) {
-              if (t == 0) {
-                ok = mbar_wait(&kv_full[ks], (kq / NS) & 1u, wd);
-                if (!ok) break;
-                tc_fence_after_sync();
+              if (leader) {
+#pragma unroll
+                for (int x = 4 * half; x < 4 * half + 4; ++x)
+                  mma_bf16_ts(tmem + 2 * kTile + t * SV * 64, tmem + t * kTile + x * 8, kHi | (vl + x * (2048 >> 4)), idesc_o,
+                              x > 0 ? 1u : 1u - fresh);
               }
-              if ((en >> (2 * t)) & 3u) qk(t, ks);
+              __syncwarp();
             }
+            if (!ok) break;
+            ++p_seen[t];
+            ++in_item[t];
           }
-          if (ok) {
-            mma_commit(&kv_empty[vs]);
-            if (n + 1 < N) mma_commit(&kv_empty[ks]);
+          if (cur.last && in_item[t]) {
+            if (leader) mma_commit(&o_full[t]);
+            ++o_items[t];
+            in_item[t] = 0;
+          }
+          if (more) {
+            if (t == 0) k_wait(nxt);
+            if (ok) qk(nxt, t);
           }
         }
-        // The MMAs issued so far end before TMEM and shared memory are given back.
-        mma_commit(&o_full[0]);
-        mma_commit(&o_full[1]);
-        if (!ok) mbar_wait_drain(&o_full[0], 0, 20000000ull);
+        if (!ok) break;
+        if (leader) mma_commit(&kv_empty[vs]);
+        if (more) k_done(nxt);
+        have = more;
+        cur = nxt;
+      }
+      __syncwarp();
+      if (!ok && leader) {  // the MMAs issued so far end before TMEM and shared memory are given back
+        mma_commit(&q_empty[0]);
+        mbar_wait_drain(&q_empty[0], 0, 20000000ull);
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-    // ---------------------------------------------- softmax, one query per thread
-    const int t = warp >> 2;
+    // ---------------------------------------- softmax, one query per thread
+    const int t = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // this warp's 32 TMEM lanes
     const uint32_t s_col = tmem + lanes + t * kTile, o_col = tmem + lanes + 2 * kTile + t * SV * 64;
     int* my_docs = doc_buf + warp * kTile;
     const float c_scale = a.scale * kLog2e;
     const bool cap = a.softcap > 0.f, bias = a.slopes != nullptr;
-    const float mult = cap || bias ? 1.f : c_scale;                     // x = mult * value kept
-    const float cap_a = a.softcap * kLog2e, cap_k = cap ? 2.f * c_scale / a.softcap : 0.f;
-    const float slope = bias ? a.slopes[h] * kLog2e : 0.f;
-    const int at = my_row + a.q_offset;
-    float m_ref = kNegInf, l = 0.f;
-    uint32_t seen = 0;
+    const float gain = cap ? a.softcap * kLog2e : c_scale;  // x = gain * (the score, or its tanh) + bias
+    const float cap_in = cap ? a.scale / a.softcap : 0.f;
+    uint32_t s_seen = 0, o_seen = 0;
     bool ok = true;
-    for (int n = 0; n < N; ++n) {
-      const uint32_t e = list[n];
-      const uint32_t st = (e >> (2 * t)) & 3u;
-      if (st == kSkip) continue;
-      const int j0 = static_cast<int>(e >> 4) * kTile;
-      if (st == kMasked && docs) {
-        __syncwarp();
-        for (int c = lane; c < kTile; c += 32) my_docs[c] = j0 + c < rule.kv ? doc_k[j0 + c] : -1;
-        __syncwarp();
-      }
-      ok = mbar_wait(&s_full[t], seen & 1u, wd);
-      ok = __all_sync(~0u, ok);
+    for (int k = 0, item; ok && k < rounds; ++k) {
+        if ((item = item_of(k)) >= items) break;
+      const int buf = k & 1;
+      const Item it = item_at(a, q_tiles, item);
+      const int i = it.i0 + t * kTile + row;
+      const int doc = a.doc_q && i < a.Lq ? a.doc_q[static_cast<long long>(it.b) * a.Lq + i] : 0;
+      ok = __all_sync(~0u, mbar_wait(&list_full[buf], (k >> 1) & 1u, wd));
       if (!ok) break;
-      tc_fence_after_sync();
-      float s[kTile];
-#pragma unroll
-      for (int c = 0; c < kTile; c += 32) tmem_ld_x32f(s_col + c, s + c);
-      tmem_wait_ld();
-      if (cap) {
-        // cap * tanh(s / cap) = cap - 2 cap / (1 + e^(2 s / cap)), in log2 units
-#pragma unroll
-        for (int c = 0; c < kTile; ++c)
-          s[c] = fmaf(-2.f * cap_a, rcp_approx(1.f + exp2_approx(s[c] * cap_k)), cap_a);
-      }
-      if (bias) {
-        const float f = static_cast<float>(at - j0), k = cap ? 1.f : c_scale;
-#pragma unroll
-        for (int c = 0; c < kTile; ++c) s[c] = fmaf(-slope, fabsf(f - static_cast<float>(c)), s[c] * k);
-      }
-      if (st == kMasked) {
-        const int lim = my_hi - j0;
-        if (docs) {
-#pragma unroll
-          for (int c = 0; c < kTile; c += 4) {
-            const int4 d = *reinterpret_cast<const int4*>(my_docs + c);
-            s[c] = c < lim && d.x == my_doc ? s[c] : kNegInf;
-            s[c + 1] = c + 1 < lim && d.y == my_doc ? s[c + 1] : kNegInf;
-            s[c + 2] = c + 2 < lim && d.z == my_doc ? s[c + 2] : kNegInf;
-            s[c + 3] = c + 3 < lim && d.w == my_doc ? s[c + 3] : kNegInf;
-          }
-        } else {
-#pragma unroll
-          for (int c = 0; c < kTile; ++c) s[c] = c < lim ? s[c] : kNegInf;
+      const ItemInfo inf = info[buf];
+      const int hi = i < a.Lq && doc >= 0 ? row_end(a, SeqRule{inf.kv, inf.prefix}, i) : 0;
+      const int at = i + a.q_offset;
+      const uint32_t* list = lists + buf * list_len;
+      const float* by_key = bias_buf + buf * 2 * kTile;
+      const float slope = bias ? by_key[1] : 0.f;
+      float m_ref = kNegInf, l = 0.f;
+      bool any = false;
+      for (int n = 0; n < inf.n; ++n) {
+        const uint32_t e = list[n], st = (e >> (2 * t)) & 3u;
+        if (st == kSkip) continue;
+        const int j0 = static_cast<int>(e >> 4) * kTile;
+        if (st == kMasked && a.doc_k) {
+          __syncwarp();
+          for (int c = lane; c < kTile; c += 32)
+            my_docs[c] = j0 + c < inf.kv ? a.doc_k[static_cast<long long>(it.b) * a.Lk + j0 + c] : -1;
+          __syncwarp();
         }
-      }
-      float mx[4] = {s[0], s[1], s[2], s[3]};
+        ok = __all_sync(~0u, mbar_wait(&s_full[t], s_seen & 1u, wd));
+        if (!ok) break;
+        ++s_seen;
+        tc_fence_after_sync();
+        float s[kTile];
 #pragma unroll
-      for (int c = 4; c < kTile; c += 4) {
-        mx[0] = fmaxf(mx[0], s[c]);
-        mx[1] = fmaxf(mx[1], s[c + 1]);
-        mx[2] = fmaxf(mx[2], s[c + 2]);
-        mx[3] = fmaxf(mx[3], s[c + 3]);
-      }
-      const float m_new = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * mult;
-      const bool grow = m_new > m_ref + kGrowth;  // also: the first visible key (m_ref = -inf)
-      if (__any_sync(~0u, grow)) {
-        const float f = grow ? exp2_approx(m_ref - m_new) : 1.f;
-        if (grow) m_ref = m_new;
-        l *= f;
-        if (seen) {
-          for (int c = 0; c < SV * 64; c += 32) {
-            float o[32];
-            tmem_ld_x32f(o_col + c, o);
-            tmem_wait_ld();
+        for (int c = 0; c < kTile; c += 32) tmem_ld_x32f(s_col + c, s + c);
+        tmem_wait_ld();
+        if (cap) {
+          float big = 0.f;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] *= f;
-            tmem_st_x32(o_col + c, reinterpret_cast<uint32_t*>(o));
+          for (int c = 0; c < kTile; c += 2) big = max3(big, fabsf(s[c]), fabsf(s[c + 1]));
+          if (__all_sync(~0u, big * cap_in <= 1.f)) {
+            const f2 in = pack2(cap_in, cap_in);
+#pragma unroll
+            for (int c = 0; c < kTile; c += 2) unpack2(tanh2(mul2(pack2(s[c], s[c + 1]), in)), s[c], s[c + 1]);
+          } else {
+            const float k2 = 2.f * kLog2e * cap_in;
+#pragma unroll
+            for (int c = 0; c < kTile; ++c) s[c] = fmaf(-2.f, rcp_approx(1.f + exp2_approx(s[c] * k2)), 1.f);
           }
         }
-      }
-      const float mu = m_ref == kNegInf ? 0.f : m_ref;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        // x = mult * s + shift
+        float mult = gain, shift = 0.f;
+        if (bias) {
+          // -slope |at - j| = +-(slope (key in tile) - slope (at - j0)) where the rows lie on one side of the tile
+          const float f = static_cast<float>(at - j0);
+          const f2 g2 = pack2(gain, gain);
+          const bool after = __all_sync(~0u, at >= j0 + kTile - 1 || i >= a.Lq), before = __all_sync(~0u, at <= j0 || i >= a.Lq);
+          if (after || before) {
+            const float* y_at = by_key + (after ? 0 : kTile);
 #pragma unroll
-      for (int c = 0; c < kTile; c += 64) {
-        uint32_t p[32];
+            for (int c = 0; c < kTile; c += 4) {
+              const float4 y = *reinterpret_cast<const float4*>(y_at + c);
+              unpack2(fma2(pack2(s[c], s[c + 1]), g2, pack2(y.x, y.y)), s[c], s[c + 1]);
+              unpack2(fma2(pack2(s[c + 2], s[c + 3]), g2, pack2(y.z, y.w)), s[c + 2], s[c + 3]);
+            }
+            shift = after ? -slope * f : slope * f;
+          } else {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const float p0 = exp2_approx(fmaf(s[c + 2 * i], mult, -mu));
-          const float p1 = exp2_approx(fmaf(s[c + 2 * i + 1], mult, -mu));
-          sum[2 * (i & 1)] += p0;
-          sum[2 * (i & 1) + 1] += p1;
-          const __nv_bfloat162 w = __floats2bfloat162_rn(p0, p1);
-          p[i] = *reinterpret_cast<const uint32_t*>(&w);
+            for (int c = 0; c < kTile; ++c) s[c] = fmaf(-slope, fabsf(f - static_cast<float>(c)), s[c] * gain);
+          }
+          mult = 1.f;
         }
-        tmem_st_x32(s_col + c / 2, p);
+        if (st == kMasked) {
+          const int lim = hi - j0;
+          if (a.doc_k) {
+#pragma unroll
+            for (int c = 0; c < kTile; c += 4) {
+              const int4 d = *reinterpret_cast<const int4*>(my_docs + c);
+              s[c] = c < lim && d.x == doc ? s[c] : kNegInf;
+              s[c + 1] = c + 1 < lim && d.y == doc ? s[c + 1] : kNegInf;
+              s[c + 2] = c + 2 < lim && d.z == doc ? s[c + 2] : kNegInf;
+              s[c + 3] = c + 3 < lim && d.w == doc ? s[c + 3] : kNegInf;
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < kTile; ++c) s[c] = c < lim ? s[c] : kNegInf;
+          }
+        }
+        const f2 mult2 = pack2(mult, mult);
+        f2 sum[2] = {0, 0};
+        // Weights of keys [c0, c0 + 64) relative to m_ref, into TMEM.
+        auto weights = [&](int c0) {
+          const float mu = (m_ref == kNegInf ? 0.f : m_ref) - shift;
+          const f2 mu2 = pack2(-mu, -mu);
+          sum[0] = sum[1] = 0;
+#pragma unroll
+          for (int c = c0; c < c0 + 64; c += 32) {
+            uint32_t p[16];
+#pragma unroll
+            for (int u = 0; u < 16; ++u) {
+              float p0, p1;
+              unpack2(fma2(pack2(s[c + 2 * u], s[c + 2 * u + 1]), mult2, mu2), p0, p1);
+              p0 = exp2_approx(p0);
+              p1 = exp2_approx(p1);
+              sum[u & 1] = add2(sum[u & 1], pack2(p0, p1));
+              const __nv_bfloat162 w = __floats2bfloat162_rn(p0, p1);
+              p[u] = *reinterpret_cast<const uint32_t*>(&w);
+            }
+            tmem_st_x16(s_col + c / 2, p);
+          }
+        };
+        auto hand_over = [&](int half) {
+          float s0, s1;
+          unpack2(add2(sum[0], sum[1]), s0, s1);
+          l += s0 + s1;
+          tmem_wait_st();
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_ready[2 * t + half]);
+        };
+        if (any) weights(0);
+        float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+        for (int c = 4; c + 8 <= kTile; c += 8)
+#pragma unroll
+          for (int u = 0; u < 4; ++u) mx[u] = max3(mx[u], s[c + 2 * u], s[c + 2 * u + 1]);
+        const float rest = fmaxf(max3(s[kTile - 4], s[kTile - 3], s[kTile - 2]), s[kTile - 1]);
+        const float m_new = fmaf(max3(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]), rest), mult, shift);
+        const bool grow = m_new > m_ref + kGrowth;  // also: the first visible key (m_ref = -inf)
+        if (!any || __any_sync(~0u, grow)) {
+          const float f = grow ? exp2_approx(m_ref - m_new) : 1.f;
+          if (grow) m_ref = m_new;
+          l *= f;
+          if (any) {
+#pragma unroll 1
+            for (int c = 0; c < SV * 64; c += 32) {
+              float o[32];
+              tmem_ld_x32f(o_col + c, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int u = 0; u < 32; ++u) o[u] *= f;
+              tmem_st_x16(o_col + c, reinterpret_cast<uint32_t*>(o));
+              tmem_st_x16(o_col + c + 16, reinterpret_cast<uint32_t*>(o) + 16);
+            }
+          }
+          weights(0);
+        }
+        any = true;
+        hand_over(0);
+        weights(64);
+        hand_over(1);
       }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-      tmem_wait_st();
-      tc_fence_before_sync();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&p_ready[t]);
-      ++seen;
-    }
-    // ------------------------------------------------------------ output
-    if (ok && seen) ok = __all_sync(~0u, mbar_wait(&o_full[t], 0, wd));
-    if (ok) {
-      tc_fence_after_sync();
+      if (lane == 0) mbar_arrive(&list_free[buf]);
+      if (!ok) break;
+      // ---------------------------------------------------------- output
+      if (any) {
+        ok = __all_sync(~0u, mbar_wait(&o_full[t], o_seen & 1u, wd));
+        if (!ok) break;
+        ++o_seen;
+        tc_fence_after_sync();
+      }
       const float inv = l == 0.f ? 0.f : 1.f / l;
       float probe = inv * 0.f;
-      __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.o) + b * a.os_b + static_cast<long long>(my_row) * a.os_l + h * a.os_h;
-      for (int c = 0; c < a.dv; c += 32) {
-        float v[32];
-        if (seen) {
-          tmem_ld_x32f(o_col + c, v);
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.o) + it.b * a.os_b + static_cast<long long>(i) * a.os_l + it.h * a.os_h;
+#pragma unroll
+      for (int d0 = 0; d0 < SV * 64; d0 += 16) {
+        if (d0 >= a.dv) break;
+        uint32_t v[16];
+        if (any) {
+          tmem_ld_x16(o_col + d0, v);
           tmem_wait_ld();
         }
 #pragma unroll
-        for (int i = 0; i < 32; i += 8) {
+        for (int u = 0; u < 16; u += 8) {
           uint32_t w[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float x = seen ? v[i + 2 * k] * inv : 0.f, y = seen ? v[i + 2 * k + 1] * inv : 0.f;
-            if (c + i < a.dv) probe += x * 0.f + y * 0.f;
-            const __nv_bfloat162 xy = __floats2bfloat162_rn(x, y);
-            w[k] = *reinterpret_cast<const uint32_t*>(&xy);
+          for (int x = 0; x < 4; ++x) {
+            const float y = any ? __uint_as_float(v[u + 2 * x]) * inv : 0.f;
+            const float z = any ? __uint_as_float(v[u + 2 * x + 1]) * inv : 0.f;
+            if (d0 + u < a.dv) probe = fmaf(y, 0.f, fmaf(z, 0.f, probe));
+            const __nv_bfloat162 yz = __floats2bfloat162_rn(y, z);
+            w[x] = *reinterpret_cast<const uint32_t*>(&yz);
           }
-          if (my_row < a.Lq && c + i < a.dv) *reinterpret_cast<uint4*>(o + c + i) = make_uint4(w[0], w[1], w[2], w[3]);
+          if (i < a.Lq && d0 + u < a.dv) *reinterpret_cast<uint4*>(out + d0 + u) = make_uint4(w[0], w[1], w[2], w[3]);
         }
       }
+      if (any) {
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&o_free[t]);
+      }
       // Rows that met a non-finite value: again, key by key (attn_row).
-      unsigned bad = __ballot_sync(~0u, my_row < a.Lq && !(probe == 0.f));
+      unsigned bad = __ballot_sync(~0u, i < a.Lq && !(probe == 0.f));
       while (bad) {
         const int r = __ffs(bad) - 1;
         bad &= bad - 1;
-        attn_row<__nv_bfloat16>(a, b, h, i0 + warp * 32 + r);
+        attn_row_inline<__nv_bfloat16>(a, it.b, it.h, it.i0 + t * kTile + (warp & 3) * 32 + r);
       }
     }
     tc_fence_before_sync();
@@ -500,26 +785,29 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
   }
 }
 
-size_t list_bytes(int Lk) { return (static_cast<size_t>(Lk + kTile - 1) / kTile) * sizeof(uint32_t); }
+size_t list_len(int Lk) { return static_cast<size_t>(Lk + kTile - 1) / kTile; }
 
 template <int SK, int SV>
-cudaError_t launch_shape(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const AttnArgs& a, cudaStream_t s) {
-  const size_t smem = Shape<SK, SV>::kFixed + list_bytes(a.Lk);
+cudaError_t launch_shape(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const AttnArgs& a, int sms, cudaStream_t s) {
+  const size_t smem = Shape<SK, SV>::kFixed + 2 * list_len(a.Lk) * sizeof(uint32_t);
   const cudaError_t e = smem_attr_once<attn_tc_kernel<SK, SV>>(smem);
   if (e != cudaSuccess) return e;
   const int tiles = (a.Lq + 2 * kTile - 1) / (2 * kTile);
-  const long long ctas = static_cast<long long>(tiles) * a.B * a.Hq;
-  if (ctas >= (1LL << 31)) return cudaErrorInvalidConfiguration;
-  return launch_pdl(attn_tc_kernel<SK, SV>, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), smem, s, q, k, v, a, tiles);
+  const long long items = static_cast<long long>(tiles) * a.B * a.Hq;
+  if (items >= (1LL << 30)) return cudaErrorInvalidConfiguration;
+  const int grid = static_cast<int>(items < sms ? items : sms);
+  return launch_pdl(attn_tc_kernel<SK, SV>, dim3(grid), dim3(kThreads), smem, s, q, k, v, a, tiles, static_cast<int>(items),
+                    static_cast<int>(list_len(a.Lk)));
 }
 
 }  // namespace
 
 void attn_tc_box(int* box_d, int* box_l) { *box_d = 64, *box_l = kTile; }
 
-cudaError_t launch_attn_tc(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const AttnArgs& a, cudaStream_t s) {
-  if (a.dk <= 64) return a.dv <= 64 ? launch_shape<1, 1>(q, k, v, a, s) : launch_shape<1, 2>(q, k, v, a, s);
-  return a.dv <= 64 ? launch_shape<2, 1>(q, k, v, a, s) : launch_shape<2, 2>(q, k, v, a, s);
+cudaError_t launch_attn_tc(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const AttnArgs& a, int sms,
+                           cudaStream_t s) {
+  if (a.dk <= 64) return a.dv <= 64 ? launch_shape<1, 1>(q, k, v, a, sms, s) : launch_shape<1, 2>(q, k, v, a, sms, s);
+  return a.dv <= 64 ? launch_shape<2, 1>(q, k, v, a, sms, s) : launch_shape<2, 2>(q, k, v, a, sms, s);
 }
 
 }  // namespace cb

@@ -329,9 +329,10 @@ cudaError_t launch_attn_simt(const AttnArgs& a, bool bf16, bool vec, int sms, cu
 // Tensor cores, bf16 views of whole 16-byte pieces, 1 <= Lk <= kAttnTcMaxKeys
 // (attention_tc.cu).  The maps: q, k, v as 4-D bf16 tensors (dim, heads, len,
 // batch) with the box attn_tc_box gives, 128-byte swizzle, zero fill.
-constexpr int kAttnTcMaxKeys = 1 << 19;
+constexpr int kAttnTcMaxKeys = 1 << 18;
 void attn_tc_box(int* box_d, int* box_l);
-cudaError_t launch_attn_tc(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const AttnArgs& a, cudaStream_t s);
+cudaError_t launch_attn_tc(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const AttnArgs& a, int sms,
+                           cudaStream_t s);
 
 // The paged cache as the kernels read it (cb_paged_cache); page_div divides by page_size.
 struct PagedArgs {

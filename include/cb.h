@@ -423,7 +423,7 @@ typedef struct {
  * Dk and Dv at most 128 (else CB_ERR_UNSUPPORTED), all of one dtype, data
  * aligned to its elements (else CB_ERR_ALIGNMENT).  Lq, Lk, batch may be 0.
  * bf16 views whose data is 16-byte aligned with strides and head sizes that
- * are multiples of 8 elements, at most 2^19 keys long, run on the tensor
+ * are multiples of 8 elements, at most 2^18 keys long, run on the tensor
  * cores: scores and the sums over keys in fp32, the weights p rounded to bf16
  * as the second product's operand.  fp32, and every other bf16 view, runs in
  * fp32 on the CUDA cores.  Softmax statistics are fp32 throughout.  One

@@ -48,7 +48,12 @@ constexpr int kTile = 128;          // queries per tile, keys per tile
 constexpr int kSlab = 128 * 128;    // bytes of 128 rows x 64 bf16
 constexpr int kSoftmaxWarps = 8;    // two warpgroups, one per tile
 constexpr int kCopyWarp = 8, kMmaWarp = 9, kListWarp = 10, kTailWarp = 11;
-constexpr int kThreads = 384;       // 168 registers per thread
+// At launch every thread holds 168 registers (the most for 12 warps); the last
+// warpgroup hands some of its own to the softmax threads, which keep 128
+// scores each: 256 * 216 + 128 * 72 = 384 * 168.
+constexpr int kThreads = 384;
+constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
+static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * 168, "registers of the launch");
 constexpr float kGrowth = 64.f;     // rescale when the maximum grew by more (log2)
 constexpr int kListReaders = kSoftmaxWarps + 3;
 
@@ -182,7 +187,9 @@ __device__ __forceinline__ Item item_at(const AttnArgs& a, int q_tiles, int item
   return {bh / a.Hq, bh % a.Hq, (q_tiles - 1 - item / heads) * 2 * kTile};
 }
 
-template <int SK, int SV>
+// CAP, BIAS: whether scores are capped / biased (a branch per tile would make
+// every path keep the 128 scores in the same registers).
+template <int SK, int SV, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                const __grid_constant__ CUtensorMap vmap, const AttnArgs a, int q_tiles, int items, int list_len) {
@@ -247,6 +254,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
   const int rounds = (items + gridDim.x - 1) / gridDim.x;
 
   if (warp >= kSoftmaxWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kListWarp) {
       // ------------------------------------------------------------ lists
       bool ok = true;
@@ -567,15 +575,15 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
       }
     }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     // ---------------------------------------- softmax, one query per thread
     const int t = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // this warp's 32 TMEM lanes
     const uint32_t s_col = tmem + lanes + t * kTile, o_col = tmem + lanes + 2 * kTile + t * SV * 64;
     int* my_docs = doc_buf + warp * kTile;
     const float c_scale = a.scale * kLog2e;
-    const bool cap = a.softcap > 0.f, bias = a.slopes != nullptr;
-    const float gain = cap ? a.softcap * kLog2e : c_scale;  // x = gain * (the score, or its tanh) + bias
-    const float cap_in = cap ? a.scale / a.softcap : 0.f;
+    const float gain = CAP ? a.softcap * kLog2e : c_scale;  // x = gain * (the score, or its tanh) + bias
+    const float cap_in = CAP ? a.scale / a.softcap : 0.f;
     uint32_t s_seen = 0, o_seen = 0;
     bool ok = true;
     for (int k = 0, item; ok && k < rounds; ++k) {
@@ -591,7 +599,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
       const int at = i + a.q_offset;
       const uint32_t* list = lists + buf * list_len;
       const float* by_key = bias_buf + buf * 2 * kTile;
-      const float slope = bias ? by_key[1] : 0.f;
+      const float slope = BIAS ? by_key[1] : 0.f;
       float m_ref = kNegInf, l = 0.f;
       bool any = false;
       for (int n = 0; n < inf.n; ++n) {
@@ -612,7 +620,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
 #pragma unroll
         for (int c = 0; c < kTile; c += 32) tmem_ld_x32f(s_col + c, s + c);
         tmem_wait_ld();
-        if (cap) {
+        if constexpr (CAP) {
           float big = 0.f;
 #pragma unroll
           for (int c = 0; c < kTile; c += 2) big = max3(big, fabsf(s[c]), fabsf(s[c + 1]));
@@ -628,7 +636,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
         }
         // x = mult * s + shift
         float mult = gain, shift = 0.f;
-        if (bias) {
+        if constexpr (BIAS) {
           // -slope |at - j| = +-(slope (key in tile) - slope (at - j0)) where the rows lie on one side of the tile
           const float f = static_cast<float>(at - j0);
           const f2 g2 = pack2(gain, gain);
@@ -787,17 +795,24 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
 
 size_t list_len(int Lk) { return static_cast<size_t>(Lk + kTile - 1) / kTile; }
 
-template <int SK, int SV>
-cudaError_t launch_shape(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const AttnArgs& a, int sms, cudaStream_t s) {
+template <int SK, int SV, bool CAP, bool BIAS>
+cudaError_t launch_one(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const AttnArgs& a, int sms, cudaStream_t s) {
   const size_t smem = Shape<SK, SV>::kFixed + 2 * list_len(a.Lk) * sizeof(uint32_t);
-  const cudaError_t e = smem_attr_once<attn_tc_kernel<SK, SV>>(smem);
+  const cudaError_t e = smem_attr_once<attn_tc_kernel<SK, SV, CAP, BIAS>>(smem);
   if (e != cudaSuccess) return e;
   const int tiles = (a.Lq + 2 * kTile - 1) / (2 * kTile);
   const long long items = static_cast<long long>(tiles) * a.B * a.Hq;
   if (items >= (1LL << 30)) return cudaErrorInvalidConfiguration;
   const int grid = static_cast<int>(items < sms ? items : sms);
-  return launch_pdl(attn_tc_kernel<SK, SV>, dim3(grid), dim3(kThreads), smem, s, q, k, v, a, tiles, static_cast<int>(items),
-                    static_cast<int>(list_len(a.Lk)));
+  return launch_pdl(attn_tc_kernel<SK, SV, CAP, BIAS>, dim3(grid), dim3(kThreads), smem, s, q, k, v, a, tiles,
+                    static_cast<int>(items), static_cast<int>(list_len(a.Lk)));
+}
+
+template <int SK, int SV>
+cudaError_t launch_shape(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const AttnArgs& a, int sms, cudaStream_t s) {
+  if (a.softcap > 0.f)
+    return a.slopes ? launch_one<SK, SV, true, true>(q, k, v, a, sms, s) : launch_one<SK, SV, true, false>(q, k, v, a, sms, s);
+  return a.slopes ? launch_one<SK, SV, false, true>(q, k, v, a, sms, s) : launch_one<SK, SV, false, false>(q, k, v, a, sms, s);
 }
 
 }  // namespace

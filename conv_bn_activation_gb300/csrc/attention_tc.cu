@@ -18,11 +18,12 @@
 // next item's key tiles, and the first MMAs of an item run under the output of
 // the one before.
 //
-// One thread issues all MMAs, in the order
-//   PV_0(n), QK_0(n+1), PV_1(n), QK_1(n+1),
-// so S_t is overwritten only by an MMA issued after the one that reads P_t, and
-// the commit after QK_t(n+1) also covers PV_t(n): once the softmax warps see
-// S_t(n+1) they may rescale O_t without another barrier.
+// Each tile has its own MMA warp, which issues PV_t(n), then QK_t(n+1): S_t is
+// overwritten only by an MMA issued after the one that reads P_t, and the
+// commit after QK_t(n+1) also covers PV_t(n), so once the softmax warps see
+// S_t(n+1) they may rescale O_t without another barrier. (One warp for both
+// tiles was late by 2000 of 4000 cycles per pair: every wait, commit and list
+// read of one tile delayed the other's MMAs.)
 //
 // Weights are relative to m_ref, the maximum of a query's first visible tile,
 // and stay so until a score exceeds it by 2^64: fp32 sums and bf16 weights keep
@@ -47,7 +48,7 @@ namespace {
 constexpr int kTile = 128;          // queries per tile, keys per tile
 constexpr int kSlab = 128 * 128;    // bytes of 128 rows x 64 bf16
 constexpr int kSoftmaxWarps = 8;    // two warpgroups, one per tile
-constexpr int kCopyWarp = 8, kMmaWarp = 9, kListWarp = 10, kTailWarp = 11;
+constexpr int kCopyWarp = 8, kMmaWarp = 9, kListWarp = 11;  // MMA warps 9 and 10: tiles 0 and 1
 // At launch every thread holds 168 registers (the most for 12 warps); the last
 // warpgroup hands some of its own to the softmax threads, which keep 128
 // scores each: 256 * 216 + 128 * 72 = 384 * 168.
@@ -211,9 +212,10 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
   uint64_t* o_free = o_full + 2;
   uint64_t* list_full = o_free + 2;
   uint64_t* list_free = list_full + 2;
-  uint64_t* tail_go = list_free + 2;  // the MMA thread has seen the values of a tail tile arrive
-  uint64_t* v_tail = tail_go + 1;  // their rows past the end are zero
-  ItemInfo* info = reinterpret_cast<ItemInfo*>(v_tail + 1);
+  uint64_t* drain = list_free + 2;  // given-up launches only
+  uint64_t* v_tail = drain + 2;  // the values past the end of a tail tile are zero
+  int* turn = reinterpret_cast<int*>(v_tail + 1);  // 1 while an MMA warp issues a tile's MMAs
+  ItemInfo* info = reinterpret_cast<ItemInfo*>(v_tail + 2);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(info + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   uint32_t* lists = reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(q_full) + 1024);  // [2][list_len]
@@ -229,15 +231,16 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
       mbar_init(&o_full[t], 1);
       mbar_init(&o_free[t], 4);
       mbar_init(&list_full[t], 1);
+      mbar_init(&drain[t], 1);
       mbar_init(&list_free[t], kListReaders);
     }
     for (int s = 0; s < NS; ++s) {
       mbar_init(&kv_full[s], 1);
-      mbar_init(&kv_empty[s], 1);
+      mbar_init(&kv_empty[s], 2);
     }
-    mbar_init(tail_go, 1);
     mbar_init(v_tail, 1);
     *abort_flag = 0;
+    *turn = 0;
     fence_mbar_init();
   }
   if (warp == kMmaWarp) {
@@ -400,36 +403,6 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
       // Every copy lands before the CTA can exit.
       if (use && lane < NS) mbar_wait_drain(&kv_full[lane], (use - 1) & 1u, 20000000ull);
       if (use && lane >= NS && lane < NS + 2) mbar_wait_drain(&q_full[lane - NS], (use - 1) & 1u, 20000000ull);
-    } else if (warp == kTailWarp) {
-      // --------------------------------- values past a sequence's end: zero
-      bool ok = true;
-      uint32_t base = 0, tails = 0;
-      for (int k = 0, item; ok && k < rounds; ++k) {
-        if ((item = item_of(k)) >= items) break;
-        const int buf = k & 1;
-        ok = __all_sync(~0u, mbar_wait(&list_full[buf], (k >> 1) & 1u, wd));
-        if (!ok) break;
-        const ItemInfo inf = info[buf];
-        int slot_of = -1;  // ring slot of the values of the tile that holds key kv
-        if (inf.tail)
-          for (int n = lane; n < inf.n; n += 32)
-            if (static_cast<int>(lists[buf * list_len + n] >> 4) == inf.kv / kTile)
-              slot_of = static_cast<int>((base + 2 * n + 1) % NS);
-        slot_of = __reduce_max_sync(~0u, slot_of);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&list_free[buf]);
-        base += 2 * inf.n;
-        if (slot_of < 0) continue;
-        ok = __all_sync(~0u, mbar_wait(tail_go, tails++ & 1u, wd));
-        if (!ok) break;
-        uint8_t* values = sKV + slot_of * SH::kSlot;
-        for (int s = 0; s < SV; ++s)
-          for (int e = (inf.kv % kTile) * 8 + lane; e < kTile * 8; e += 32)
-            *reinterpret_cast<uint4*>(values + s * kSlab + e * 16) = make_uint4(0, 0, 0, 0);
-        fence_async_shared();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(v_tail);
-      }
     } else {
       // ------------------------------------------------------------- MMAs
       // The whole warp walks the steps together and one elected lane issues,
@@ -437,25 +410,42 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
       // 16-byte units in their low word; the high word is a constant.
       // (Built anew by a lone lane, each took longer than its MMA: 75 to 150
       // cycles against 64.)
+      const int t = warp - kMmaWarp;
       const uint32_t idesc_s = idesc_bf16(kTile, kTile);
       const uint32_t idesc_o = idesc_bf16(kTile, (a.dv + 15) & ~15) | (1u << 16);  // B is MN-major
-      const uint32_t q_lo = static_cast<uint32_t>(kmajor_swizzled_desc(smem_u32(sQ), 128));
+      const uint32_t q_lo = static_cast<uint32_t>(kmajor_swizzled_desc(smem_u32(sQ), 128)) + t * (SK * kSlab >> 4);
       const uint32_t k_lo = static_cast<uint32_t>(kmajor_swizzled_desc(smem_u32(sKV), 128));
       const uint32_t v_lo = static_cast<uint32_t>(mnmajor_desc(smem_u32(sKV)));
       constexpr uint64_t kHi = (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
+      const uint32_t s_tmem = tmem + t * kTile, o_tmem = tmem + 2 * kTile + t * SV * 64;
       const bool leader = elect_one();
       bool ok = true;
       auto wait = [&](uint64_t* bar, uint32_t parity) {
         ok = __all_sync(~0u, ok && mbar_wait(bar, parity & 1u, wd));
         return ok;
       };
+      // The tensor pipe for one tile's PV and QK at a time: interleaved with the
+      // other tile's they would take twice as long each, and the two tiles'
+      // softmax would then run side by side instead of under those MMAs.
+      auto take = [&] {
+        if (leader) {
+          const uint64_t t0 = global_timer_ns();
+          for (int spins = 1; atomicCAS_block(turn, 0, 1) != 0; ++spins)
+            if ((spins & 63) == 0 && (*abort_flag || global_timer_ns() - t0 > a.timeout_ns)) break;
+        }
+        __syncwarp();
+      };
+      auto give = [&] {
+        if (leader) atomicExch_block(turn, 0);
+        __syncwarp();
+      };
       // One key tile of one item; `seq`: its K's place in the ring's sequence.
       struct Step {
-        uint32_t e;
+        uint32_t state, seq;
         bool first, last, tail;
-        uint32_t seq;
+        int kv;
       };
-      int k = -1, n = 0, count = 0, tail_tile = -1;
+      int k = -1, n = 0, count = 0, kv = 0, tail_tile = -1;
       uint32_t seq = 0, tails = 0;
       auto fetch = [&](Step* s) {  // false: no further step (or a wait gave up)
         while (n == count) {
@@ -464,51 +454,45 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
           if (!wait(&list_full[k & 1], k >> 1)) return false;
           n = 0;
           count = __shfl_sync(~0u, info[k & 1].n, 0);
-          tail_tile = __shfl_sync(~0u, info[k & 1].tail ? info[k & 1].kv / kTile : -1, 0);
+          kv = __shfl_sync(~0u, info[k & 1].kv, 0);
+          tail_tile = __shfl_sync(~0u, info[k & 1].tail, 0) ? kv / kTile : -1;
           if (count == 0 && leader) mbar_arrive(&list_free[k & 1]);
         }
-        s->e = __shfl_sync(~0u, lists[(k & 1) * list_len + n], 0);
+        const uint32_t e = __shfl_sync(~0u, lists[(k & 1) * list_len + n], 0);
+        s->state = (e >> (2 * t)) & 3u;
+        s->seq = seq;
         s->first = n == 0;
         s->last = ++n == count;
-        s->tail = static_cast<int>(s->e >> 4) == tail_tile;
-        s->seq = seq;
+        s->tail = static_cast<int>(e >> 4) == tail_tile;
+        s->kv = kv;
         seq += 2;
         if (s->last && leader) mbar_arrive(&list_free[k & 1]);
         return true;
       };
-      uint32_t q_items = 0;  // items with keys so far
-      uint32_t q_have[2] = {0, 0}, p_seen[2] = {0, 0}, o_items[2] = {0, 0}, in_item[2] = {0, 0};
-      auto state = [](const Step& s, int t) { return (s.e >> (2 * t)) & 3u; };
-      auto qk = [&](const Step& s, int t) {
-        if (!state(s, t)) return;
-        if (q_have[t] != q_items) {  // the item's Q_t
-          q_have[t] = q_items;
-          if (!wait(&q_full[t], q_items - 1)) return;
-          tc_fence_after_sync();
-        }
-        const uint32_t ql = q_lo + t * (SK * kSlab >> 4), kl = k_lo + s.seq % NS * (SH::kSlot >> 4);
-        if (leader) {
-#pragma unroll
-          for (int x = 0; x < 4 * SK; ++x) {  // dims past dk are zero in both operands
-            const uint32_t off = ((x >> 2) * kSlab + (x & 3) * 32) >> 4;
-            mma_bf16(tmem + t * kTile, kHi | (ql + off), kHi | (kl + off), idesc_s, x > 0);
-          }
-          mma_commit(&s_full[t]);
-        }
-        __syncwarp();
-      };
+      uint32_t q_items = 0, q_have = 0;  // items with keys so far; the one whose Q was waited for
+      uint32_t p_seen = 0, o_items = 0, in_item = 0;
       auto k_wait = [&](const Step& s) {
         if (s.first) ++q_items;
         wait(&kv_full[s.seq % NS], s.seq / NS);
-        tc_fence_after_sync();
+        if (s.state && q_have != q_items) {
+          q_have = q_items;
+          wait(&q_full[t], q_items - 1);
+        }
       };
-      auto k_done = [&](const Step& s) {
+      auto qk = [&](const Step& s) {
+        tc_fence_after_sync();
+        const uint32_t kl = k_lo + s.seq % NS * (SH::kSlot >> 4);
         if (leader) {
-          mma_commit(&kv_empty[s.seq % NS]);
-          if (s.last) {
-            mma_commit(&q_empty[0]);
-            mma_commit(&q_empty[1]);
+          if (s.state) {
+#pragma unroll
+            for (int x = 0; x < 4 * SK; ++x) {  // dims past dk are zero in both operands
+              const uint32_t off = ((x >> 2) * kSlab + (x & 3) * 32) >> 4;
+              mma_bf16(s_tmem, kHi | (q_lo + off), kHi | (kl + off), idesc_s, x > 0);
+            }
+            mma_commit(&s_full[t]);
           }
+          mma_commit(&kv_empty[s.seq % NS]);
+          if (s.last) mma_commit(&q_empty[t]);
         }
         __syncwarp();
       };
@@ -516,62 +500,62 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
       bool have = fetch(&cur);
       if (have) {
         k_wait(cur);
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-          if (ok) qk(cur, t);
-        if (ok) k_done(cur);
+        if (ok) qk(cur);
       }
       while (ok && have) {
         const bool more = fetch(&nxt);
         if (!ok) break;
         const uint32_t vq = cur.seq + 1, vs = vq % NS, vl = v_lo + vs * (SH::kSlot >> 4);
         wait(&kv_full[vs], vq / NS);
-        if (ok && cur.tail) {
-          if (leader) mbar_arrive(tail_go);
+        if (ok && cur.tail) {  // values past the sequence's end, whatever they are, become zero
+          if (t == 0) {
+            for (int s = 0; s < SV; ++s)
+              for (int e = (cur.kv % kTile) * 8 + lane; e < kTile * 8; e += 32)
+                *reinterpret_cast<uint4*>(sKV + vs * SH::kSlot + s * kSlab + e * 16) = make_uint4(0, 0, 0, 0);
+            fence_async_shared();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(v_tail);
+          }
           wait(v_tail, tails++);
         }
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (!ok) break;
-          if (state(cur, t)) {
-            if (in_item[t] == 0 && o_items[t] > 0) wait(&o_free[t], o_items[t] - 1);
-            const uint32_t fresh = in_item[t] == 0;
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {  // 64 keys' weights each
-              if (!ok || !wait(&p_ready[2 * t + half], p_seen[t])) break;
-              tc_fence_after_sync();
-              if (leader) {
-#pragma unroll
-                for (int x = 4 * half; x < 4 * half + 4; ++x)
-                  mma_bf16_ts(tmem + 2 * kTile + t * SV * 64, tmem + t * kTile + x * 8, kHi | (vl + x * (2048 >> 4)), idesc_o,
-                              x > 0 ? 1u : 1u - fresh);
-              }
-              __syncwarp();
-            }
-            if (!ok) break;
-            ++p_seen[t];
-            ++in_item[t];
-          }
-          if (cur.last && in_item[t]) {
-            if (leader) mma_commit(&o_full[t]);
-            ++o_items[t];
-            in_item[t] = 0;
-          }
-          if (more) {
-            if (t == 0) k_wait(nxt);
-            if (ok) qk(nxt, t);
-          }
-        }
+        if (ok && more) k_wait(nxt);
         if (!ok) break;
+        if (cur.state) {
+          if (in_item == 0 && o_items > 0) wait(&o_free[t], o_items - 1);
+          const uint32_t fresh = in_item == 0;
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {  // 64 keys' weights each
+            if (!ok || !wait(&p_ready[2 * t + half], p_seen)) break;
+            if (half == 1) take();
+            tc_fence_after_sync();
+            if (leader) {
+#pragma unroll
+              for (int x = 4 * half; x < 4 * half + 4; ++x)
+                mma_bf16_ts(o_tmem, s_tmem + x * 8, kHi | (vl + x * (2048 >> 4)), idesc_o, x > 0 ? 1u : 1u - fresh);
+            }
+            __syncwarp();
+          }
+          if (!ok) break;
+          ++p_seen;
+          ++in_item;
+        }
+        if (cur.last && in_item) {
+          if (leader) mma_commit(&o_full[t]);
+          __syncwarp();
+          ++o_items;
+          in_item = 0;
+        }
+        if (more) qk(nxt);
+        if (cur.state) give();
         if (leader) mma_commit(&kv_empty[vs]);
-        if (more) k_done(nxt);
+        __syncwarp();
         have = more;
         cur = nxt;
       }
       __syncwarp();
       if (!ok && leader) {  // the MMAs issued so far end before TMEM and shared memory are given back
-        mma_commit(&q_empty[0]);
-        mbar_wait_drain(&q_empty[0], 0, 20000000ull);
+        mma_commit(&drain[t]);
+        mbar_wait_drain(&drain[t], 0, 20000000ull);
       }
     }
   } else {

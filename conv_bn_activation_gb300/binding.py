@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 import numpy as np
@@ -103,7 +104,7 @@ def load():
             lib = ctypes.CDLL(_LIB_PATH)
             P, I, F, LL, S = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_longlong, ctypes.c_size_t
             T = ctypes.POINTER(CbTensor)
-            H, SC, PC = ctypes.POINTER(CbHeads), ctypes.POINTER(CbScore), ctypes.POINTER(CbPagedCache)
+            H = SC = PC = P  # cb_heads, cb_score, cb_paged_cache: packed bytes, or a pointer to the structure
             sig = {
                 "cb_fold_bn": [P, P, P, P, F, I, P, P],
                 "cb_repack_weights": [P, I, I, I, I, I, P],
@@ -189,30 +190,68 @@ def nchw(t) -> CbTensor:
     return CbTensor(t.data_ptr(), N, H, W, C, sn, sh, sw, sc, LAYOUT_NCHW, dtype_code(t))
 
 
-def heads(t) -> CbHeads:
-    """View of a torch tensor indexed [B, L, H, D] (any strides, unit stride along D)."""
+# The attention calls are small (a decode step's kernels take microseconds), so their views are
+# packed by struct, in the layout of the ctypes structures: a ctypes structure takes several times
+# as long to build.
+_HEADS = struct.Struct("P4i3qi4x")   # CbHeads
+_SCORE = struct.Struct("2fP2i4P")    # CbScore
+_raw_stream = None
+_codes = None
+
+
+def _init_codes():
+    global _codes, _raw_stream
+    import torch
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+        (lambda device: torch.cuda.current_stream(device).cuda_stream)
+    _codes = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16, "i32": torch.int32, "f32": torch.float32}
+
+
+def _stream_of(t, stream):
+    """The stream's handle: `stream`, or the current one of t's device."""
+    if stream is not None:
+        return stream.cuda_stream
+    if not t.is_cuda:
+        raise ValueError("the tensors of a GPU call are on a CUDA device")
+    return _raw_stream(t.get_device())
+
+
+def heads(t) -> bytes:
+    """cb_heads of a torch tensor indexed [B, L, H, D] (any strides, D contiguous), packed."""
+    if _codes is None:
+        _init_codes()
     B, L, H, D = t.shape
     sb, sl, sh, sd = t.stride()
     if sd != 1 and D > 1:
         raise ValueError("the last dim of a [B, L, H, D] view is contiguous")
-    return CbHeads(t.data_ptr(), B, L, H, D, sb, sl, sh, dtype_code(t))
+    code = _codes.get(t.dtype)
+    if code is None:
+        raise TypeError(f"activation tensors are float32 or bfloat16, got {t.dtype}")
+    return _HEADS.pack(t.data_ptr(), B, L, H, D, sb, sl, sh, code)
 
 
-def _heads1(t) -> CbHeads:
-    """View of a torch tensor indexed [B, H, D]: one token per sequence."""
+def _heads1(t) -> bytes:
+    """cb_heads of a torch tensor indexed [B, H, D], one token per sequence, packed."""
+    if _codes is None:
+        _init_codes()
     B, H, D = t.shape
     sb, sh, sd = t.stride()
     if sd != 1 and D > 1:
         raise ValueError("the last dim of a [B, H, D] view is contiguous")
-    return CbHeads(t.data_ptr(), B, 1, H, D, sb, 0, sh, dtype_code(t))
+    code = _codes.get(t.dtype)
+    if code is None:
+        raise TypeError(f"activation tensors are float32 or bfloat16, got {t.dtype}")
+    return _HEADS.pack(t.data_ptr(), B, 1, H, D, sb, 0, sh, code)
 
 
 def _device_array(t, name, dtype, shape):
-    """Pointer of a contiguous device tensor of this dtype and shape (None stays None)."""
+    """Pointer of a contiguous device tensor ("i32" or "f32") of this shape; None is the null pointer."""
     if t is None:
-        return None
-    if not t.is_cuda or str(t.dtype) != dtype or tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError(f"{name}: a contiguous {dtype} device tensor of shape {shape}, got {t.dtype} "
+        return 0
+    if _codes is None:
+        _init_codes()
+    if t.dtype != _codes[dtype] or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous {_codes[dtype]} device tensor of shape {shape}, got {t.dtype} "
                          f"{tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
@@ -229,14 +268,16 @@ class Score:
         self.scale, self.softcap, self.causal, self.q_offset = float(scale), float(softcap), bool(causal), int(q_offset)
         self.slopes, self.prefix_len, self.kv_len, self.doc_q, self.doc_k = slopes, prefix_len, kv_len, doc_q, doc_k
 
-    def view(self, batch, lq, lk, hq) -> CbScore:
-        """The rule for [batch, lq, hq, .] queries over lk keys; checks the arrays' shapes."""
-        return CbScore(self.scale, self.softcap, _device_array(self.slopes, "slopes", "torch.float32", (hq,)),
-                       int(self.causal), self.q_offset,
-                       _device_array(self.prefix_len, "prefix_len", "torch.int32", (batch,)),
-                       _device_array(self.kv_len, "kv_len", "torch.int32", (batch,)),
-                       _device_array(self.doc_q, "doc_q", "torch.int32", (batch, lq)),
-                       _device_array(self.doc_k, "doc_k", "torch.int32", (batch, lk)))
+    def view(self, batch, lq, lk, hq) -> bytes:
+        """cb_score for [batch, lq, hq, .] queries over lk keys, packed; checks the arrays' shapes."""
+        slopes, prefix, kv, dq, dk = self.slopes, self.prefix_len, self.kv_len, self.doc_q, self.doc_k
+        return _SCORE.pack(self.scale, self.softcap,
+                           0 if slopes is None else _device_array(slopes, "slopes", "f32", (hq,)),
+                           self.causal, self.q_offset,
+                           0 if prefix is None else _device_array(prefix, "prefix_len", "i32", (batch,)),
+                           0 if kv is None else _device_array(kv, "kv_len", "i32", (batch,)),
+                           0 if dq is None else _device_array(dq, "doc_q", "i32", (batch, lq)),
+                           0 if dk is None else _device_array(dk, "doc_k", "i32", (batch, lk)))
 
 
 class PagedCache:
@@ -258,6 +299,7 @@ class PagedCache:
         self.view = CbPagedCache(k_pages.data_ptr(), v_pages.data_ptr(), P, page, H, Dk, v_pages.shape[3],
                                  *k_pages.stride()[:3], *v_pages.stride()[:3], table.data_ptr(), table.shape[0],
                                  table.shape[1], table.stride(0), dtype_code(k_pages))
+        self.ref = ctypes.byref(self.view)
 
 
 # ----------------------------------------------------------- host helpers
@@ -467,29 +509,28 @@ def attention(q, k, v, out, score, stream=None):
     """cb_attention on torch CUDA tensors: q [B, Lq, Hq, Dk], k [B, Lk, Hkv, Dk], v [B, Lk, Hkv, Dv],
     out [B, Lq, Hq, Dv] (any strides, the last dim contiguous; all float32 or all bfloat16); score: a
     Score.  Slices of a projection's output are read in place."""
-    qv, kv, vv, ov = heads(q), heads(k), heads(v), heads(out)
-    sv = score.view(qv.batch, qv.len, kv.len, qv.heads)
-    _check(load().cb_attention(ctypes.byref(qv), ctypes.byref(kv), ctypes.byref(vv), ctypes.byref(sv),
-                               ctypes.byref(ov), _stream_ptr(stream)), "cb_attention")
+    B, lq, hq, _ = q.shape
+    st = (_lib or load()).cb_attention(heads(q), heads(k), heads(v), score.view(B, lq, k.shape[1], hq), heads(out),
+                                       _stream_of(q, stream))
+    if st:
+        _check(st, "cb_attention")
     return out
 
 
 def cache_append(k_new, v_new, cache, pos, count=None, stream=None):
     """cb_cache_append: tokens t < count[b] of k_new [B, T, H, Dk] and v_new [B, T, H, Dv] become tokens
     pos[b] + t of the cache's sequences.  pos, count: int32 [B] (count None: all T)."""
-    kv, vv = heads(k_new), heads(v_new)
-    B = kv.batch
-    _check(load().cb_cache_append(ctypes.byref(kv), ctypes.byref(vv), _device_array(pos, "pos", "torch.int32", (B,)),
-                                  _device_array(count, "count", "torch.int32", (B,)), ctypes.byref(cache.view),
-                                  _stream_ptr(stream)), "cb_cache_append")
+    kv, vv, B = heads(k_new), heads(v_new), k_new.shape[0]
+    st = (_lib or load()).cb_cache_append(kv, vv, _device_array(pos, "pos", "i32", (B,)),
+                                          _device_array(count, "count", "i32", (B,)), cache.ref, _stream_of(k_new, stream))
+    if st:
+        _check(st, "cb_cache_append")
 
 
 def attention_decode_workspace(q, cache) -> int:
     """cb_attention_decode_workspace: bytes of scratch for q [B, Hq, Dk] over this cache."""
-    qv = _heads1(q)
     n = ctypes.c_size_t(0)
-    _check(load().cb_attention_decode_workspace(ctypes.byref(qv), ctypes.byref(cache.view), ctypes.byref(n)),
-           "cb_attention_decode_workspace")
+    _check(load().cb_attention_decode_workspace(_heads1(q), cache.ref, ctypes.byref(n)), "cb_attention_decode_workspace")
     return n.value
 
 
@@ -498,13 +539,13 @@ def attention_decode(q, cache, length, out, workspace, scale, softcap=0.0, slope
     tokens first[b] <= j < length[b] (int32 [B]; first None: 0), the query at position length[b] - 1.
     workspace: a uint8 device tensor of attention_decode_workspace bytes."""
     qv, ov = _heads1(q), _heads1(out)
-    B = qv.batch
-    _check(load().cb_attention_decode(ctypes.byref(qv), ctypes.byref(cache.view),
-                                      _device_array(length, "length", "torch.int32", (B,)),
-                                      _device_array(first, "first", "torch.int32", (B,)), scale, softcap,
-                                      _device_array(slopes, "slopes", "torch.float32", (qv.heads,)), ctypes.byref(ov),
-                                      workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                                      _stream_ptr(stream)), "cb_attention_decode")
+    B, hq, _ = q.shape
+    st = (_lib or load()).cb_attention_decode(
+        qv, cache.ref, _device_array(length, "length", "i32", (B,)), _device_array(first, "first", "i32", (B,)), scale,
+        softcap, _device_array(slopes, "slopes", "f32", (hq,)), ov, workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _stream_of(q, stream))
+    if st:
+        _check(st, "cb_attention_decode")
     return out
 
 

@@ -124,6 +124,19 @@ def test_decode_refusals(cblib):
     assert lib.cb_attention_decode_workspace(ctypes.byref(q), ctypes.byref(c), None) == I
 
 
+def test_packed_views_have_the_structures_layout(cblib):
+    import torch
+    t = torch.zeros(3, 5, 4, 16, dtype=torch.bfloat16)[:, 1:, ::2, 8:]
+    want = cblib.CbHeads(t.data_ptr(), 3, 4, 2, 8, *t.stride()[:3], cblib.DTYPE_BF16)
+    got = cblib.CbHeads.from_buffer_copy(cblib.heads(t))
+    assert all(getattr(got, n) == getattr(want, n) for n, _ in cblib.CbHeads._fields_)
+    assert len(cblib.heads(t)) == ctypes.sizeof(cblib.CbHeads)
+    packed = cblib.Score(0.5, 2.0, causal=True, q_offset=-3).view(1, 2, 3, 4)
+    assert len(packed) == ctypes.sizeof(cblib.CbScore)
+    got = cblib.CbScore.from_buffer_copy(packed)
+    assert (got.scale, got.softcap, got.causal, got.q_offset, got.slopes, got.doc_k) == (0.5, 2.0, 1, -3, None, None)
+
+
 def test_binding_checks_index_tensors(cblib):
     import torch
     s = cblib.Score(0.1, kv_len=torch.zeros(2, dtype=torch.int64))

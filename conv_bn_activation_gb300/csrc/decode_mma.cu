@@ -96,11 +96,19 @@ __global__ void __launch_bounds__(kThreads, 2) decode_mma_kernel(const DecodeArg
   const bool cap = a.softcap > 0.f, bias = a.slopes != nullptr;
   const float cap_a = a.softcap * kLog2e, cap_k = cap ? 2.f * c_scale / a.softcap : 0.f;
   const int g = lane >> 2, t4 = lane & 3;
+  // Within a stage: this lane's first copy targets and its rows' addresses for
+  // ldmatrix.  Stages and rows are multiples of 128 bytes, so the swizzle of a
+  // later row or piece is an exclusive or on the address.
+  const uint32_t k_dst = (lane / CK) * kKeyBytes + (((lane % CK) ^ (lane / CK)) * 16);
+  const uint32_t v_dst = kStep * kKeyBytes + (lane / CV) * kValBytes + (((lane % CV) ^ (lane / CV)) * 16);
+  const uint32_t k_src = (lane & 7) * kKeyBytes + (((lane >> 3) ^ (lane & 7)) * 16);
+  const uint32_t v_src = ((lane & 7) + 8 * ((lane >> 3) & 1)) * kValBytes + (((lane >> 4) ^ (lane & 7)) * 16);
+  const bool same = a.cache.ks_p == a.cache.vs_p && a.cache.ks_t == a.cache.vs_t;  // one offset serves both
 
   while (at < end) {
     const Piece pc = next_piece(a, prefix, per_seq, at, end, &b);
-    const __nv_bfloat16* kbase = static_cast<const __nv_bfloat16*>(a.cache.k) + pc.hk * a.cache.ks_h;
-    const __nv_bfloat16* vbase = static_cast<const __nv_bfloat16*>(a.cache.v) + pc.hk * a.cache.vs_h;
+    const char* kbase = static_cast<const char*>(a.cache.k) + pc.hk * a.cache.ks_h * 2 + (lane % CK) * 16;
+    const char* vbase = static_cast<const char*>(a.cache.v) + pc.hk * a.cache.vs_h * 2 + (lane % CV) * 16;
 
     // Q as the MMA's A operand: rows g and g + 8, elements 2 t4 and 2 t4 + 8 of each 16
     uint32_t qf[DK / 16][4];
@@ -127,56 +135,70 @@ __global__ void __launch_bounds__(kThreads, 2) decode_mma_kernel(const DecodeArg
 #pragma unroll
       for (int r = 0; r < 4; ++r) o[n][r] = 0.f;
 
-    // Lane x < 16 looks token x of a step up, one step before its copies are issued.
+    // Lane x < 16 looks token x of a step up, one step before its copies are
+    // issued: the byte offsets of its rows, or -1.
     const int base = pc.tile0 * kDecodeTile + warp * kStep;
-    auto lookup = [&](int step, int* page, int* slot) {
+    struct Rows {
+      long long k, v;
+    };
+    auto lookup = [&](int step) {
       const int j = base + step * kDecodeTile + (lane & 15);
-      *page = -1;
-      *slot = 0;
-      if (step < pc.tiles && j >= pc.lo && j < pc.hi) *page = token_page(a, pc.b, j, slot);
+      Rows r{-1, -1};
+      if (step < pc.tiles && j >= pc.lo && j < pc.hi) {
+        int slot;
+        const long long page = token_page(a, pc.b, j, &slot);
+        if (page >= 0) {
+          r.k = (page * a.cache.ks_p + slot * a.cache.ks_t) * 2;
+          r.v = same ? r.k : (page * a.cache.vs_p + slot * a.cache.vs_t) * 2;
+        }
+      }
+      return r;
     };
     unsigned live[kStages];  // bit x: token x of the stage's step exists
-    auto issue = [&](int step, int stage, int page, int slot) {
+    auto issue = [&](int step, int stage, const Rows& rows) {
+      const unsigned have = __ballot_sync(~0u, rows.k >= 0) & 0xffffu;
       if (step < pc.tiles) {
-        const uint32_t dst = ring_addr + stage * kStageBytes;
+        const uint32_t kd = ring_addr + stage * kStageBytes + k_dst, vd = ring_addr + stage * kStageBytes + v_dst;
 #pragma unroll
-        for (int i = 0; i < kStep * CK / 32; ++i) {
-          const int r = i * (32 / CK) + lane / CK, c = lane % CK;
-          const int pg = __shfl_sync(~0u, page, r), sl = __shfl_sync(~0u, slot, r);
-          if (c < kq)
-            cp_async16(dst + r * kKeyBytes + ((c ^ (r & 7)) * 16), kbase + (pg < 0 ? 0 : pg * a.cache.ks_p + sl * a.cache.ks_t + c * 8), pg >= 0);
+        for (int i = 0; i < kStep * CK / 32; ++i) {  // 32 / CK rows at a time
+          const int r = i * (32 / CK) + lane / CK;
+          const long long at = __shfl_sync(~0u, rows.k, r);
+          const bool ok = (have >> r) & 1;
+          // row r's pieces lie at piece ^ (r % 8)
+          if (lane % CK < kq) cp_async16((kd + i * (32 / CK) * kKeyBytes) ^ ((i * (32 / CK) & 7) * 16), ok ? kbase + at : kbase, ok);
+          if (CK == CV) {
+            const long long to = same ? at : __shfl_sync(~0u, rows.v, r);
+            if (lane % CV < vq) cp_async16((vd + i * (32 / CV) * kValBytes) ^ ((i * (32 / CV) & 7) * 16), ok ? vbase + to : vbase, ok);
+          }
         }
+        if (CK != CV) {
 #pragma unroll
-        for (int i = 0; i < kStep * CV / 32; ++i) {
-          const int r = i * (32 / CV) + lane / CV, c = lane % CV;
-          const int pg = __shfl_sync(~0u, page, r), sl = __shfl_sync(~0u, slot, r);
-          if (c < vq)
-            cp_async16(dst + kStep * kKeyBytes + r * kValBytes + ((c ^ (r & 7)) * 16),
-                       vbase + (pg < 0 ? 0 : pg * a.cache.vs_p + sl * a.cache.vs_t + c * 8), pg >= 0);
+          for (int i = 0; i < kStep * CV / 32; ++i) {
+            const int r = i * (32 / CV) + lane / CV;
+            const long long to = __shfl_sync(~0u, rows.v, r);
+            const bool ok = (have >> r) & 1;
+            if (lane % CV < vq) cp_async16((vd + i * (32 / CV) * kValBytes) ^ ((i * (32 / CV) & 7) * 16), ok ? vbase + to : vbase, ok);
+          }
         }
       }
       cp_async_commit();
-      return __ballot_sync(~0u, page >= 0) & 0xffffu;
+      return have;
     };
 
-    int page, slot;
 #pragma unroll
-    for (int s = 0; s < kStages - 1; ++s) {
-      lookup(s, &page, &slot);
-      live[s] = issue(s, s, page, slot);
-    }
-    lookup(kStages - 1, &page, &slot);
+    for (int s = 0; s < kStages - 1; ++s) live[s] = issue(s, s, lookup(s));
+    Rows rows = lookup(kStages - 1);
     int stage = 0;
     for (int step = 0; step < pc.tiles; ++step) {
       const int fill = stage == 0 ? kStages - 1 : stage - 1;  // the stage read in the last step
       __syncwarp();
       {
-        const unsigned lv = issue(step + kStages - 1, fill, page, slot);
+        const unsigned lv = issue(step + kStages - 1, fill, rows);
 #pragma unroll
         for (int s = 0; s < kStages; ++s)
           if (s == fill) live[s] = lv;
       }
-      lookup(step + kStages, &page, &slot);
+      rows = lookup(step + kStages);
       cp_async_wait<kStages - 1>();
       __syncwarp();
       unsigned lv = 0;
@@ -193,9 +215,8 @@ __global__ void __launch_bounds__(kThreads, 2) decode_mma_kernel(const DecodeArg
       for (int n = 0; n < 2; ++n)
 #pragma unroll
         for (int d = 0; d < DK / 32; ++d) {  // keys 8 n .. + 8, dims 32 d .. + 32
-          const int r = 8 * n + (lane & 7), c = 4 * d + (lane >> 3);
           uint32_t f[4];
-          ldsm4(ks + r * kKeyBytes + ((c ^ (r & 7)) * 16), f);
+          ldsm4((ks + k_src + 8 * n * kKeyBytes + (d >> 1) * 128) ^ ((d & 1) * 64), f);
           mma16816(s[n], qf[2 * d], f[0], f[1]);
           mma16816(s[n], qf[2 * d + 1], f[2], f[3]);
         }
@@ -257,9 +278,8 @@ __global__ void __launch_bounds__(kThreads, 2) decode_mma_kernel(const DecodeArg
         }
 #pragma unroll
       for (int d = 0; d < DV / 16; ++d) {  // values 16 d .. + 16 of the 16 keys
-        const int r = (lane & 7) + 8 * ((lane >> 3) & 1), c = 2 * d + (lane >> 4);
         uint32_t f[4];
-        ldsm4_t(vs + r * kValBytes + ((c ^ (r & 7)) * 16), f);
+        ldsm4_t((vs + v_src + (d >> 2) * 128) ^ ((d & 3) * 32), f);
         mma16816(o[2 * d], p, f[0], f[1]);
         mma16816(o[2 * d + 1], p, f[2], f[3]);
       }

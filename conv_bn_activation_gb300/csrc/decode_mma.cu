@@ -3,13 +3,14 @@
 // tokens are dealt to the CTAs).
 //
 // Bound by HBM: 2 (dk + dv) bytes per cached token and key head, read once.
-// Up to 16 query heads that share a key head ride along: with 8 of them the
+// The query heads that share a key head ride along: with 8 of them the
 // products are 8 FLOP per byte, too much conversion and FMA work for the CUDA
 // cores at the memory's rate (a bf16 value feeds 8 FMAs after one conversion;
-// measured 5.6x slower), and too little for tcgen05, whose 128 query rows
-// would be 8 used ones and whose operands would cross shared memory no
-// faster. So the products are warp-level MMAs with the heads as their 16 rows:
-//   S[16 heads x 16 keys] = Q K^T,  P = 2^(x - m),  O[16 heads x dv] += P V.
+// measured 5.6x slower), and too little for tcgen05, whose 128 rows would hold
+// 8 queries and whose operands would cross shared memory no faster. So the
+// products are warp-level MMAs with the keys (then the values' dims) as their
+// 16 rows and 8 heads as their columns, NB of them per item:
+//   S^T[16 keys x 8 heads] = K Q^T,  P = 2^(x - m),  O^T[dv x 8 heads] += V^T P^T.
 // Each warp walks its own 16 keys of every 64-token tile with its own ring of
 // cp.async copies and its own maximum, sum and O, so nothing synchronises
 // inside a run; the four warps are joined when an item's piece ends. O is
@@ -56,6 +57,12 @@ __device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
                : "r"(addr)
                : "memory");
 }
+// The transpose of an 8 x 8 matrix of 16-bit elements held as an MMA fragment.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
 // d (16 x 8, fp32) += a (16 x 16, bf16) * b (16 x 8, bf16)
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t* a, uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -64,13 +71,13 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t* a, uint3
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <int DK, int DV>
+template <int DK, int DV, int NB>
 __global__ void __launch_bounds__(kThreads, 2) decode_mma_kernel(const DecodeArgs a) {
   constexpr int kKeyBytes = DK * 2, kValBytes = DV * 2, kStageBytes = stage_bytes<DK, DV>();
   constexpr int CK = DK / 8, CV = DV / 8;  // 16-byte pieces per row
   extern __shared__ __align__(128) uint8_t smem[];
   unsigned* prefix = reinterpret_cast<unsigned*>(smem + ring_bytes<DK, DV>());
-  __shared__ float ms[kWarps][16], ls[kWarps][16];
+  __shared__ float ms[kWarps][8 * NB], ls[kWarps][8 * NB];
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   // Pieces past dk / dv are never copied: they stay zero.
@@ -101,8 +108,8 @@ __global__ void __launch_bounds__(kThreads, 2) decode_mma_kernel(const DecodeArg
   // later row or piece is an exclusive or on the address.
   const uint32_t k_dst = (lane / CK) * kKeyBytes + (((lane % CK) ^ (lane / CK)) * 16);
   const uint32_t v_dst = kStep * kKeyBytes + (lane / CV) * kValBytes + (((lane % CV) ^ (lane / CV)) * 16);
-  const uint32_t k_src = (lane & 7) * kKeyBytes + (((lane >> 3) ^ (lane & 7)) * 16);
-  const uint32_t v_src = ((lane & 7) + 8 * ((lane >> 3) & 1)) * kValBytes + (((lane >> 4) ^ (lane & 7)) * 16);
+  const uint32_t k_src = ((lane & 7) + 8 * ((lane >> 3) & 1)) * kKeyBytes + (((lane >> 4) ^ (lane & 7)) * 16);
+  const uint32_t v_src = ((lane & 7) + 8 * (lane >> 4)) * kValBytes + ((((lane >> 3) & 1) ^ (lane & 7)) * 16);
   const bool same = a.cache.ks_p == a.cache.vs_p && a.cache.ks_t == a.cache.vs_t;  // one offset serves both
 
   while (at < end) {
@@ -110,30 +117,38 @@ __global__ void __launch_bounds__(kThreads, 2) decode_mma_kernel(const DecodeArg
     const char* kbase = static_cast<const char*>(a.cache.k) + pc.hk * a.cache.ks_h * 2 + (lane % CK) * 16;
     const char* vbase = static_cast<const char*>(a.cache.v) + pc.hk * a.cache.vs_h * 2 + (lane % CV) * 16;
 
-    // Q as the MMA's A operand: rows g and g + 8, elements 2 t4 and 2 t4 + 8 of each 16
-    uint32_t qf[DK / 16][4];
+    // Q^T as the MMA's B operand: head g of each 8, elements 2 t4 and 2 t4 + 8 of each 16
+    uint32_t qf[DK / 16][NB][2];
 #pragma unroll
     for (int s = 0; s < DK / 16; ++s)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int hd = g + 8 * (r & 1), d = 16 * s + 2 * t4 + 8 * (r >> 1);
-        uint32_t w = 0;
-        if (hd < pc.heads && d < a.dk) {  // dk is even
-          const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + pc.b * a.qs_b + (pc.h0 + hd) * a.qs_h + d;
-          w = static_cast<uint32_t>(__bfloat16_as_ushort(q[0])) | (static_cast<uint32_t>(__bfloat16_as_ushort(q[1])) << 16);
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int hd = g + 8 * nb, d = 16 * s + 2 * t4 + 8 * r;
+          uint32_t w = 0;
+          if (hd < pc.heads && d < a.dk) {  // dk is even
+            const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + pc.b * a.qs_b + (pc.h0 + hd) * a.qs_h + d;
+            w = static_cast<uint32_t>(__bfloat16_as_ushort(q[0])) | (static_cast<uint32_t>(__bfloat16_as_ushort(q[1])) << 16);
+          }
+          qf[s][nb][r] = w;
         }
-        qf[s][r] = w;
+    // This thread's heads are 8 nb + 2 t4 and the one after.
+    float slope[NB][2], m[NB][2], l[NB][2], o[DV / 16][NB][4];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int hd = 8 * nb + 2 * t4 + e;
+        slope[nb][e] = bias && hd < pc.heads ? a.slopes[pc.h0 + hd] * kLog2e : 0.f;
+        m[nb][e] = kNegInf;
+        l[nb][e] = 0.f;
       }
-    float slope[2] = {0.f, 0.f};
 #pragma unroll
-    for (int r = 0; r < 2; ++r)
-      if (bias && g + 8 * r < pc.heads) slope[r] = a.slopes[pc.h0 + g + 8 * r] * kLog2e;
-
-    float o[DV / 8][4], m[2] = {kNegInf, kNegInf}, l[2] = {0.f, 0.f};
+      for (int d = 0; d < DV / 16; ++d)
 #pragma unroll
-    for (int n = 0; n < DV / 8; ++n)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) o[n][r] = 0.f;
+        for (int r = 0; r < 4; ++r) o[d][nb][r] = 0.f;
+    }
 
     // Lane x < 16 looks token x of a step up, one step before its copies are
     // issued: the byte offsets of its rows, or -1.
@@ -206,27 +221,28 @@ __global__ void __launch_bounds__(kThreads, 2) decode_mma_kernel(const DecodeArg
       for (int s = 0; s < kStages; ++s)
         if (s == stage) lv = live[s];
       const uint32_t ks = ring_addr + stage * kStageBytes, vs = ks + kStep * kKeyBytes;
-      float s[2][4];
+      float s[NB][4];  // element r: key g + 8 (r >> 1), head 8 nb + 2 t4 + (r & 1)
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
+      for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) s[n][r] = 0.f;
+        for (int r = 0; r < 4; ++r) s[nb][r] = 0.f;
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
+      for (int d = 0; d < DK / 16; ++d) {
+        uint32_t f[4];
+        ldsm4((ks + k_src + (d >> 2) * 128) ^ ((d & 3) * 32), f);
 #pragma unroll
-        for (int d = 0; d < DK / 32; ++d) {  // keys 8 n .. + 8, dims 32 d .. + 32
-          uint32_t f[4];
-          ldsm4((ks + k_src + 8 * n * kKeyBytes + (d >> 1) * 128) ^ ((d & 1) * 64), f);
-          mma16816(s[n], qf[2 * d], f[0], f[1]);
-          mma16816(s[n], qf[2 * d + 1], f[2], f[3]);
-        }
-      // x = log2(e) * score; element (n, r): head g + 8 (r >> 1), key 8 n + 2 t4 + (r & 1)
+        for (int nb = 0; nb < NB; ++nb) mma16816(s[nb], f, qf[d][nb][0], qf[d][nb][1]);
+      }
+      // x = log2(e) * score
       const int j0 = base + step * kDecodeTile;
+      const float dist = static_cast<float>(pc.len - 1 - j0 - g);
+      bool grow = false;
+      float mx[NB][2];
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
+      for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          float x = s[n][r];
+          float x = s[nb][r];
           if (cap) {
             // cap * tanh(s / cap) = cap - 2 cap / (1 + e^(2 s / cap))
             float den;
@@ -235,73 +251,74 @@ __global__ void __launch_bounds__(kThreads, 2) decode_mma_kernel(const DecodeArg
           } else {
             x *= c_scale;
           }
-          const int key = 8 * n + 2 * t4 + (r & 1);
-          if (bias) x = fmaf(-slope[r >> 1], static_cast<float>(pc.len - 1 - j0 - key), x);
-          s[n][r] = x;
+          if (bias) x = fmaf(-slope[nb][r & 1], dist - 8.f * (r >> 1), x);
+          if (lv != 0xffffu && !((lv >> (g + 8 * (r >> 1))) & 1)) x = kNegInf;
+          s[nb][r] = x;
         }
-      if (lv != 0xffffu) {
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            if (!((lv >> (8 * n + 2 * t4 + (r & 1))) & 1)) s[n][r] = kNegInf;
-      }
-      bool grow = false;
-      float mx[2];
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        mx[r] = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
-        mx[r] = fmaxf(mx[r], __shfl_xor_sync(~0u, mx[r], 1));
-        mx[r] = fmaxf(mx[r], __shfl_xor_sync(~0u, mx[r], 2));
-        grow |= mx[r] > m[r] + kGrowth;
+        for (int e = 0; e < 2; ++e) {
+          float y = fmaxf(s[nb][e], s[nb][2 + e]);
+          y = fmaxf(y, __shfl_xor_sync(~0u, y, 4));
+          y = fmaxf(y, __shfl_xor_sync(~0u, y, 8));
+          y = fmaxf(y, __shfl_xor_sync(~0u, y, 16));
+          mx[nb][e] = y;
+          grow |= y > m[nb][e] + kGrowth;
+        }
       }
       if (__any_sync(~0u, grow)) {
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const float mn = fmaxf(m[r], mx[r]);
-          const float f = mn == kNegInf ? 1.f : exp2_approx(m[r] - mn);
-          m[r] = mn;
-          l[r] *= f;
+        for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-          for (int n = 0; n < DV / 8; ++n) o[n][2 * r] *= f, o[n][2 * r + 1] *= f;
+          for (int e = 0; e < 2; ++e) {
+            const float mn = fmaxf(m[nb][e], mx[nb][e]);
+            const float f = mn == kNegInf ? 1.f : exp2_approx(m[nb][e] - mn);
+            m[nb][e] = mn;
+            l[nb][e] *= f;
+#pragma unroll
+            for (int d = 0; d < DV / 16; ++d) o[d][nb][e] *= f, o[d][nb][2 + e] *= f;
+          }
+      }
+      uint32_t p[NB][2];
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        const float mu0 = m[nb][0] == kNegInf ? 0.f : m[nb][0], mu1 = m[nb][1] == kNegInf ? 0.f : m[nb][1];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {  // keys 8 r .. + 8
+          const __nv_bfloat162 w = __floats2bfloat162_rn(exp2_approx(s[nb][2 * r] - mu0), exp2_approx(s[nb][2 * r + 1] - mu1));
+          l[nb][0] += __low2float(w);
+          l[nb][1] += __high2float(w);
+          p[nb][r] = transpose8(*reinterpret_cast<const uint32_t*>(&w));
         }
       }
-      uint32_t p[4];
-#pragma unroll
-      for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const float mu = m[r] == kNegInf ? 0.f : m[r];
-          const __nv_bfloat162 w = __floats2bfloat162_rn(exp2_approx(s[n][2 * r] - mu), exp2_approx(s[n][2 * r + 1] - mu));
-          l[r] += __low2float(w) + __high2float(w);
-          p[2 * n + r] = *reinterpret_cast<const uint32_t*>(&w);
-        }
 #pragma unroll
       for (int d = 0; d < DV / 16; ++d) {  // values 16 d .. + 16 of the 16 keys
         uint32_t f[4];
         ldsm4_t((vs + v_src + (d >> 2) * 128) ^ ((d & 3) * 32), f);
-        mma16816(o[2 * d], p, f[0], f[1]);
-        mma16816(o[2 * d + 1], p, f[2], f[3]);
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) mma16816(o[d][nb], f, p[nb][0], p[nb][1]);
       }
       stage = stage + 1 == kStages ? 0 : stage + 1;
     }
     cp_async_wait<0>();
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      l[r] += __shfl_xor_sync(~0u, l[r], 1);
-      l[r] += __shfl_xor_sync(~0u, l[r], 2);
-    }
     __syncthreads();  // every warp is through with its ring: it now takes the results [warp][heads][DV]
     float* res = reinterpret_cast<float*>(smem);
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int hd = g + 8 * r;
-      if (t4 == 0) ms[warp][hd] = m[r], ls[warp][hd] = l[r];
-      if (hd < pc.heads)
+    for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-        for (int n = 0; n < DV / 8; ++n)
-          *reinterpret_cast<float2*>(res + (warp * pc.heads + hd) * DV + 8 * n + 2 * t4) = make_float2(o[n][2 * r], o[n][2 * r + 1]);
-    }
+      for (int e = 0; e < 2; ++e) {
+        float y = l[nb][e];
+        y += __shfl_xor_sync(~0u, y, 4);
+        y += __shfl_xor_sync(~0u, y, 8);
+        y += __shfl_xor_sync(~0u, y, 16);
+        const int hd = 8 * nb + 2 * t4 + e;
+        if (g == 0) ms[warp][hd] = m[nb][e], ls[warp][hd] = y;
+        if (hd < pc.heads)
+#pragma unroll
+          for (int d = 0; d < DV / 16; ++d) {
+            res[(warp * pc.heads + hd) * DV + 16 * d + g] = o[d][nb][e];
+            res[(warp * pc.heads + hd) * DV + 16 * d + g + 8] = o[d][nb][2 + e];
+          }
+      }
     __syncthreads();
     float* part = a.part + (2 * cta + (pc.starts ? 1 : 0)) * part_floats(a.item_heads, a.dv);
     const bool whole = pc.starts && pc.ends;
@@ -337,12 +354,17 @@ __global__ void __launch_bounds__(kThreads, 2) decode_mma_kernel(const DecodeArg
   }
 }
 
+template <int DK, int DV, int NB>
+cudaError_t launch_one(const DecodeArgs& a, cudaStream_t s) {
+  const size_t smem = ring_bytes<DK, DV>() + sizeof(unsigned) * (a.B + 1);
+  const cudaError_t e = smem_attr_once<decode_mma_kernel<DK, DV, NB>>(smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(decode_mma_kernel<DK, DV, NB>, dim3(a.ctas), dim3(kThreads), smem, s, a);
+}
+
 template <int DK, int DV>
 cudaError_t launch_dims(const DecodeArgs& a, cudaStream_t s) {
-  const size_t smem = ring_bytes<DK, DV>() + sizeof(unsigned) * (a.B + 1);
-  const cudaError_t e = smem_attr_once<decode_mma_kernel<DK, DV>>(smem);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(decode_mma_kernel<DK, DV>, dim3(a.ctas), dim3(kThreads), smem, s, a);
+  return a.item_heads <= 8 ? launch_one<DK, DV, 1>(a, s) : launch_one<DK, DV, 2>(a, s);
 }
 
 }  // namespace

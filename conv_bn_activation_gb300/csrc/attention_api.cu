@@ -115,7 +115,7 @@ cb_status check_decode(const cb_heads* q, const cb_paged_cache* cache) {
 }
 
 struct DecodePlan {
-  int sms = 0, ctas = 0, chunks = 0, heads = 0;
+  int sms = 0, ctas = 0, chunks = 0, heads = 0, split = 0;
   int* err = nullptr;
   bool vec = false;
 };
@@ -125,10 +125,18 @@ cb_status plan_decode(const cb_heads* q, const cb_paged_cache* cache, DecodePlan
   p->vec = pieces16(cache);
   // One wave of resident CTAs: their runs are equal, so a second wave would only add pieces to join.
   const bool mma = q->dtype == CB_DTYPE_BF16 && p->vec;
-  p->ctas = p->sms * (mma ? 2 : 4);
+  p->ctas = p->sms * (p->vec ? decode_ctas_per_sm(cache->dim_k, cache->dim_v) : 4);
   const int group = q->heads / cache->heads, most = mma ? kDecodeMmaHeads : kDecodeSimtHeads;
   p->chunks = (group + most - 1) / most;
   p->heads = (group + p->chunks - 1) / p->chunks;
+  // Whole items on clusters where that leaves a CTA at most eight tiles of 64
+  // tokens of the largest cache the table can name: no join then, and no CTA
+  // walks much longer than another.  Else runs.
+  const long long items = static_cast<long long>(q->batch) * cache->heads * p->chunks;
+  const long long tiles = (static_cast<long long>(cache->max_pages) * cache->page_size + 63) / 64;
+  p->split = 1;
+  while (p->split < 8 && items * p->split * 2 <= p->ctas && p->split < tiles) p->split *= 2;
+  if (!p->vec || tiles > 8LL * p->split) p->split = 0;
   return CB_OK;
 }
 
@@ -242,7 +250,7 @@ cb_status cb_attention_decode(const cb_heads* q, const cb_paged_cache* cache, co
   a.scale = scale, a.softcap = softcap;
   a.B = q->batch, a.Hq = q->heads, a.Hkv = cache->heads, a.group = q->heads / cache->heads;
   a.dk = cache->dim_k, a.dv = cache->dim_v;
-  a.chunks = p.chunks, a.item_heads = p.heads;
+  a.chunks = p.chunks, a.item_heads = p.heads, a.split = p.split;
   a.record = static_cast<int*>(workspace);
   a.part = reinterpret_cast<float*>(a.record + 2 * p.ctas);
   a.ctas = p.ctas;

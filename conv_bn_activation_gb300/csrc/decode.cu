@@ -1,6 +1,6 @@
 // Attention of one new token per sequence over a paged cache (cb_attention_decode):
-// the CUDA-core kernel (fp32 caches, and bf16 ones whose rows are not whole
-// 16-byte pieces; the others take decode_mma.cu) and the join of split sequences.
+// the kernel for caches whose rows are not whole 16-byte pieces (the others take
+// decode_stream.cuh) and the join of split sequences.
 //
 // Bound by HBM: every key and value of the batch is read once, and one
 // query's 4 FLOP per element are far below the FMA rate until many heads
@@ -16,7 +16,7 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kHeads = kDecodeSimtHeads;
 
-template <typename T, bool VEC>
+template <typename T>
 __global__ void __launch_bounds__(kThreads) decode_simt_kernel(DecodeArgs a) {
   extern __shared__ __align__(16) float smem[];
   const int ldk = (a.dk + 3) / 4 * 4 + 4;
@@ -72,17 +72,12 @@ __global__ void __launch_bounds__(kThreads) decode_simt_kernel(DecodeArgs a) {
       }
       __syncthreads();
       {  // keys
-        const int per = VEC ? static_cast<int>(16 / sizeof(T)) : 1;
-        const int pieces = VEC ? a.dk / per : ldk - 4;
-        for (int e = tid; e < kDecodeTile * pieces; e += kThreads) {
-          const int r = e / pieces, d = (e - r * pieces) * per;
+        const int width = ldk - 4;
+        for (int e = tid; e < kDecodeTile * width; e += kThreads) {
+          const int r = e / width, d = e - r * width;
           const int page = page_s[r];
-          const T* src = static_cast<const T*>(a.cache.k) + page * a.cache.ks_p + slot_s[r] * a.cache.ks_t + hk * a.cache.ks_h + d;
-          if constexpr (VEC) {
-            *reinterpret_cast<float4*>(Ks + r * ldk + d) = page < 0 ? make_float4(0.f, 0.f, 0.f, 0.f) : *reinterpret_cast<const float4*>(src);
-          } else {
-            Ks[r * ldk + d] = page < 0 || d >= a.dk ? 0.f : to_f32(*src);
-          }
+          Ks[r * ldk + d] = page < 0 || d >= a.dk ? 0.f
+                                                  : to_f32(static_cast<const T*>(a.cache.k)[page * a.cache.ks_p + slot_s[r] * a.cache.ks_t + hk * a.cache.ks_h + d]);
         }
       }
       __syncthreads();
@@ -141,13 +136,8 @@ __global__ void __launch_bounds__(kThreads) decode_simt_kernel(DecodeArgs a) {
           if (page < 0) continue;
           const T* src = static_cast<const T*>(a.cache.v) + page * a.cache.vs_p + slot_s[key] * a.cache.vs_t + hk * a.cache.vs_h + vd;
           float v[4];
-          if constexpr (VEC) {
-            const float4 w = *reinterpret_cast<const float4*>(src);
-            v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
-          } else {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) v[c] = vd + c < a.dv ? to_f32(src[c]) : 0.f;
-          }
+          for (int c = 0; c < 4; ++c) v[c] = vd + c < a.dv ? to_f32(src[c]) : 0.f;
           const float4 pa = *reinterpret_cast<const float4*>(Ps + key * kHeads);
           const float4 pb = *reinterpret_cast<const float4*>(Ps + key * kHeads + 4);
           const float p[kHeads] = {pa.x, pa.y, pa.z, pa.w, pb.x, pb.y, pb.z, pb.w};
@@ -235,12 +225,12 @@ size_t simt_smem(int dk, int dv, int B) {
          sizeof(unsigned) * (B + 1);
 }
 
-template <typename T, bool VEC>
+template <typename T>
 cudaError_t launch_simt(const DecodeArgs& a, cudaStream_t s) {
   const size_t smem = simt_smem(a.dk, a.dv, a.B);
-  const cudaError_t e = smem_attr_once<decode_simt_kernel<T, VEC>>(smem);
+  const cudaError_t e = smem_attr_once<decode_simt_kernel<T>>(smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(decode_simt_kernel<T, VEC>, dim3(a.ctas), dim3(kThreads), smem, s, a);
+  return launch_pdl(decode_simt_kernel<T>, dim3(a.ctas), dim3(kThreads), smem, s, a);
 }
 
 template <typename T>
@@ -256,11 +246,11 @@ size_t decode_workspace_bytes(int ctas, int heads, int dv) {
 
 cudaError_t launch_decode(const DecodeArgs& a, bool bf16, bool vec, cudaStream_t s) {
   cudaError_t e;
-  if (bf16)
-    e = vec ? launch_decode_mma(a, s) : launch_simt<__nv_bfloat16, false>(a, s);
+  if (vec)
+    e = bf16 ? launch_decode_mma(a, s) : launch_decode_fma(a, s);
   else
-    e = vec ? launch_simt<float, true>(a, s) : launch_simt<float, false>(a, s);
-  if (e != cudaSuccess) return e;
+    e = bf16 ? launch_simt<__nv_bfloat16>(a, s) : launch_simt<float>(a, s);
+  if (e != cudaSuccess || a.split) return e;
   return bf16 ? launch_join<__nv_bfloat16>(a, s) : launch_join<float>(a, s);
 }
 

@@ -111,6 +111,25 @@ __device__ __forceinline__ Piece next_piece(const DecodeArgs& a, const unsigned*
   return p;
 }
 
+// The piece of a CTA that belongs to a cluster of a.split CTAs per item.
+__device__ __forceinline__ Piece whole_piece(const DecodeArgs& a, int per_seq) {
+  const int all = blockIdx.x / a.split, rank = blockIdx.x % a.split;
+  Piece p;
+  p.b = all / per_seq;
+  p.item = all % per_seq;
+  const SeqSpan sp = seq_span(a, p.b);
+  const int begin = static_cast<int>(static_cast<long long>(sp.tiles) * rank / a.split);
+  p.tiles = static_cast<int>(static_cast<long long>(sp.tiles) * (rank + 1) / a.split) - begin;
+  p.tile0 = sp.t0 + begin;
+  p.starts = p.ends = a.split == 1;
+  p.last = 0;
+  p.hk = p.item / a.chunks;
+  p.h0 = p.hk * a.group + (p.item % a.chunks) * a.item_heads;
+  p.heads = min(a.item_heads, (p.hk + 1) * a.group - p.h0);
+  p.lo = sp.lo, p.hi = sp.hi, p.len = sp.len;
+  return p;
+}
+
 // Sequences without a visible token: zeros, dealt over the CTAs.
 template <typename Store>
 __device__ __forceinline__ void zero_empty(const DecodeArgs& a, const unsigned* prefix, Store store) {

@@ -1,0 +1,288 @@
+// The streaming decode kernel: one new token's attention over a paged cache
+// whose rows are whole 16-byte pieces.  A policy C does the arithmetic
+// (decode_mma.cu: bf16 by warp-level MMAs; decode_fma.cu: fp32 by FMAs).
+//
+// Bound by HBM: (dk + dv) * sizeof(element) bytes per cached token and key
+// head, read once.  A CTA's four warps walk a piece of one item together: each
+// takes its own kStep tokens of every kWarps * kStep through its own ring of
+// cp.async copies and keeps its own maximum, sum and O, so nothing synchronises
+// inside a piece; the four are joined when it ends.
+//
+// Two ways to deal items (decode_common.cuh):
+//  - Runs: equal runs of tiles over one wave of CTAs; items cut by a run's end
+//    go through the workspace and a join kernel.
+//  - Whole items, for caches small enough that a CTA walks at most eight tiles:
+//    a cluster of a.split CTAs per item, joined through distributed shared
+//    memory.  One launch, no prefix over the lengths: one sequence of 421
+//    tokens takes 5.6 us where runs and their join take 7.7.
+#pragma once
+
+#include "decode_common.cuh"
+#include "launch_util.h"
+#include "ptx.cuh"
+
+namespace cb {
+
+constexpr int kDecodeWarps = 4, kDecodeThreads = kDecodeWarps * 32;
+constexpr float kDecodeGrowth = 8.f;  // rescale O when a maximum grew by more (log2)
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// log2(e) * score of a dot product, as the decode kernels evaluate it.
+struct DecodeScore {
+  float c_scale, cap_a, cap_k;
+  bool cap;
+  __device__ __forceinline__ explicit DecodeScore(const DecodeArgs& a) {
+    c_scale = a.scale * kLog2e;
+    cap = a.softcap > 0.f;
+    cap_a = a.softcap * kLog2e;
+    cap_k = cap ? 2.f * c_scale / a.softcap : 0.f;
+  }
+  // cap * tanh(s / cap) = cap - 2 cap / (1 + e^(2 s / cap))
+  __device__ __forceinline__ float operator()(float dot) const {
+    if (!cap) return dot * c_scale;
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + exp2_approx(dot * cap_k)));
+    return fmaf(-2.f * cap_a, r, cap_a);
+  }
+};
+
+template <class C>
+constexpr int decode_ring_bytes() {  // also holds the results when a piece ends
+  return kDecodeWarps * C::kStages * C::kStep * (C::DK + C::DV) * static_cast<int>(sizeof(typename C::T));
+}
+template <class C>
+constexpr int decode_part_offset() {  // floats: the four warps' results, then the CTA's
+  return kDecodeWarps * C::kHeads * C::DV;
+}
+
+template <class C, bool WHOLE>
+__global__ void __launch_bounds__(kDecodeThreads, decode_ctas_per_sm(C::DK, C::DV)) decode_stream_kernel(const DecodeArgs a) {
+  using T = typename C::T;
+  constexpr int DK = C::DK, DV = C::DV, kStep = C::kStep, kStages = C::kStages, kEl = static_cast<int>(sizeof(T));
+  constexpr int kKeyBytes = DK * kEl, kValBytes = DV * kEl, kStageBytes = kStep * (kKeyBytes + kValBytes);
+  constexpr int CK = kKeyBytes / 16, CV = kValBytes / 16;  // 16-byte pieces per row
+  constexpr int RK = 32 / CK, RV = 32 / CV;                // rows per warp-wide copy
+  static_assert(decode_ring_bytes<C>() >= 4 * (decode_part_offset<C>() + C::kHeads * DV), "results fit the ring");
+  extern __shared__ __align__(128) uint8_t smem[];
+  uint8_t* after = smem + decode_ring_bytes<C>();
+  __shared__ float ms[kDecodeWarps][C::kHeads], ls[kDecodeWarps][C::kHeads];
+  __shared__ float part_m[C::kHeads], part_l[C::kHeads];
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int kq = a.dk * kEl / 16, vq = a.dv * kEl / 16;  // real pieces per row
+  const bool padded = kq < CK || vq < CV;
+  auto clear = [&] {  // pieces past dk / dv are never copied: they stay zero
+    for (int e = tid; e < decode_ring_bytes<C>() / 16; e += kDecodeThreads) reinterpret_cast<uint4*>(smem)[e] = make_uint4(0, 0, 0, 0);
+  };
+  if (padded) clear();
+  pdl_wait();
+  pdl_launch_dependents();
+  const int per_seq = a.Hkv * a.chunks;
+  unsigned* prefix = reinterpret_cast<unsigned*>(after + C::kExtra);
+  long long at = 0, end = 1, cta = blockIdx.x;
+  Run run{1, 1};
+  int b = 0;
+  if constexpr (!WHOLE) {
+    tile_prefix(a, prefix);
+    const long long total = static_cast<long long>(prefix[a.B]) * per_seq;
+    run = Run{total, min(static_cast<long long>(gridDim.x), max(total, 1LL))};
+    if (tid == 0) a.record[2 * cta] = -1;
+    zero_empty(a, prefix, [&](long long i) { static_cast<T*>(a.o)[i] = from_f32<T>(0.f); });
+    if (cta >= run.ctas || total == 0) return;
+    at = run.begin(cta);
+    end = run.begin(cta + 1);
+    b = find_seq(a, prefix, per_seq, at);
+  } else {
+    __syncthreads();
+  }
+
+  // Within a stage: this lane's first copy targets.  Row r's pieces lie at
+  // piece ^ swizzle(r), and swizzle is linear over exclusive or, so a later
+  // row's address differs by a constant and an exclusive or.
+  uint8_t* ring = smem + warp * kStages * kStageBytes;
+  const uint32_t ring_addr = smem_u32(ring);
+  const uint32_t k_dst = (lane / CK) * kKeyBytes + (((lane % CK) ^ C::swizzle(lane / CK)) * 16);
+  const uint32_t v_dst = kStep * kKeyBytes + (lane / CV) * kValBytes + (((lane % CV) ^ C::swizzle(lane / CV)) * 16);
+  const bool same = a.cache.ks_p == a.cache.vs_p && a.cache.ks_t == a.cache.vs_t;  // one offset serves both
+
+  while (at < end) {
+    const Piece pc = WHOLE ? whole_piece(a, per_seq) : next_piece(a, prefix, per_seq, at, end, &b);
+    const char* kbase = static_cast<const char*>(a.cache.k) + pc.hk * a.cache.ks_h * kEl + (lane % CK) * 16;
+    const char* vbase = static_cast<const char*>(a.cache.v) + pc.hk * a.cache.vs_h * kEl + (lane % CV) * 16;
+    C c(a, pc, after);
+
+    // Lanes below kStep look the step's tokens up, one step before their copies
+    // are issued: the byte offsets of the rows, or -1.
+    const int base = pc.tile0 * kDecodeTile + warp * kStep;
+    const int steps = pc.tiles * (kDecodeTile / (kDecodeWarps * kStep));
+    struct Rows {
+      long long k, v;
+    };
+    auto lookup = [&](int step) {
+      const int j = base + step * (kDecodeWarps * kStep) + lane % kStep;
+      Rows r{-1, -1};
+      if (step < steps && j >= pc.lo && j < pc.hi) {
+        int slot;
+        const long long page = token_page(a, pc.b, j, &slot);
+        if (page >= 0) {
+          r.k = (page * a.cache.ks_p + slot * a.cache.ks_t) * kEl;
+          r.v = same ? r.k : (page * a.cache.vs_p + slot * a.cache.vs_t) * kEl;
+        }
+      }
+      return r;
+    };
+    constexpr unsigned kAll = kStep == 32 ? ~0u : (1u << kStep) - 1;
+    unsigned live[kStages];  // bit x: token x of the stage's step exists
+    auto issue = [&](int step, int stage, const Rows& rows) {
+      const unsigned have = __ballot_sync(~0u, rows.k >= 0) & kAll;
+      if (step < steps) {
+        const uint32_t kd = ring_addr + stage * kStageBytes + k_dst, vd = ring_addr + stage * kStageBytes + v_dst;
+#pragma unroll
+        for (int i = 0; i < kStep / RK; ++i) {
+          const int r = i * RK + lane / CK;
+          const long long off = __shfl_sync(~0u, rows.k, r);
+          const bool ok = (have >> r) & 1;
+          if (lane % CK < kq) cp_async16((kd + i * RK * kKeyBytes) ^ (C::swizzle(i * RK) * 16), ok ? kbase + off : kbase, ok);
+          if (CK == CV) {
+            const long long to = same ? off : __shfl_sync(~0u, rows.v, r);
+            if (lane % CV < vq) cp_async16((vd + i * RV * kValBytes) ^ (C::swizzle(i * RV) * 16), ok ? vbase + to : vbase, ok);
+          }
+        }
+        if (CK != CV) {
+#pragma unroll
+          for (int i = 0; i < kStep / RV; ++i) {
+            const int r = i * RV + lane / CV;
+            const long long to = __shfl_sync(~0u, rows.v, r);
+            const bool ok = (have >> r) & 1;
+            if (lane % CV < vq) cp_async16((vd + i * RV * kValBytes) ^ (C::swizzle(i * RV) * 16), ok ? vbase + to : vbase, ok);
+          }
+        }
+      }
+      cp_async_commit();
+      return have;
+    };
+
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s) live[s] = issue(s, s, lookup(s));
+    Rows rows = lookup(kStages - 1);
+    int stage = 0;
+    for (int step = 0; step < steps; ++step) {
+      const int fill = stage == 0 ? kStages - 1 : stage - 1;  // the stage read in the last step
+      __syncwarp();
+      {
+        const unsigned lv = issue(step + kStages - 1, fill, rows);
+#pragma unroll
+        for (int s = 0; s < kStages; ++s)
+          if (s == fill) live[s] = lv;
+      }
+      rows = lookup(step + kStages);
+      cp_async_wait<kStages - 1>();
+      __syncwarp();
+      unsigned lv = 0;
+#pragma unroll
+      for (int s = 0; s < kStages; ++s)
+        if (s == stage) lv = live[s];
+      const uint32_t ks = ring_addr + stage * kStageBytes;
+      c.step(ks, ks + kStep * kKeyBytes, lv, pc.len - 1 - base - step * (kDecodeWarps * kStep));
+      stage = stage + 1 == kStages ? 0 : stage + 1;
+    }
+    cp_async_wait<0>();
+    __syncthreads();  // every warp is through with its ring: it now takes the results [warp][heads][DV]
+    float* res = reinterpret_cast<float*>(smem);
+    c.store(res + warp * pc.heads * DV, ms[warp], ls[warp]);
+    __syncthreads();
+    // The four warps' results as one: into the output, the workspace, or (whole
+    // items of a cluster) this CTA's part.
+    float* part_s = res + decode_part_offset<C>();
+    float* part = WHOLE ? nullptr : a.part + (2 * cta + (pc.starts ? 1 : 0)) * part_floats(a.item_heads, a.dv);
+    const bool out = pc.starts && pc.ends;
+    for (int e = tid; e < pc.heads * DV; e += kDecodeThreads) {
+      const int hd = e / DV, d = e % DV;
+      if (d >= a.dv) continue;
+      float mm = kNegInf;
+#pragma unroll
+      for (int w = 0; w < kDecodeWarps; ++w) mm = fmaxf(mm, ms[w][hd]);
+      const float mu = mm == kNegInf ? 0.f : mm;
+      float sum = 0.f, ll = 0.f;
+#pragma unroll
+      for (int w = 0; w < kDecodeWarps; ++w) {
+        const float f = exp2_approx(ms[w][hd] - mu);
+        sum = fmaf(f, res[(w * pc.heads + hd) * DV + d], sum);
+        ll = fmaf(f, ls[w][hd], ll);
+      }
+      if (out) {
+        static_cast<T*>(a.o)[pc.b * a.os_b + (pc.h0 + hd) * a.os_h + d] = from_f32<T>(ll == 0.f ? 0.f : sum / ll);
+      } else if constexpr (WHOLE) {
+        part_s[hd * DV + d] = sum;
+        if (d == 0) part_m[hd] = mm, part_l[hd] = ll;
+      } else {
+        part[2 * a.item_heads + hd * a.dv + d] = sum;
+        if (d == 0) part[hd] = mm, part[a.item_heads + hd] = ll;
+      }
+    }
+    if constexpr (WHOLE) {
+      if (a.split > 1) {  // the cluster's CTAs share the item: each joins every a.split-th value of all
+        cluster_sync();
+        for (int e = tid * a.split + static_cast<int>(cluster_ctarank()); e < pc.heads * DV; e += kDecodeThreads * a.split) {
+          const int hd = e / DV, d = e % DV;
+          if (d >= a.dv) continue;
+          float m[8], mm = kNegInf, sum = 0.f, ll = 0.f;
+#pragma unroll
+          for (int r = 0; r < 8; ++r) {
+            m[r] = r < a.split ? ld_cluster_f32(map_shared_rank(smem_u32(part_m + hd), r)) : kNegInf;
+            mm = fmaxf(mm, m[r]);
+          }
+          const float mu = mm == kNegInf ? 0.f : mm;
+#pragma unroll
+          for (int r = 0; r < 8; ++r)
+            if (r < a.split) {
+              const float f = exp2_approx(m[r] - mu);
+              sum = fmaf(f, ld_cluster_f32(map_shared_rank(smem_u32(part_s + e), r)), sum);
+              ll = fmaf(f, ld_cluster_f32(map_shared_rank(smem_u32(part_l + hd), r)), ll);
+            }
+          static_cast<T*>(a.o)[pc.b * a.os_b + (pc.h0 + hd) * a.os_h + d] = from_f32<T>(ll == 0.f ? 0.f : sum / ll);
+        }
+        cluster_sync();  // the parts are read before any CTA leaves
+      }
+      return;
+    }
+    if (!out && pc.starts && tid == 0) note_item(a, run, pc, per_seq, cta);
+    at += pc.tiles;
+    __syncthreads();
+    if (at < end && padded) {
+      clear();
+      __syncthreads();
+    }
+  }
+}
+
+template <class C>
+cudaError_t launch_decode_stream(const DecodeArgs& a, cudaStream_t s) {
+  const size_t fixed = decode_ring_bytes<C>() + C::kExtra;
+  if (a.split) {
+    const cudaError_t e = smem_attr_once<decode_stream_kernel<C, true>>(fixed);
+    if (e != cudaSuccess) return e;
+    const dim3 grid(static_cast<unsigned>(a.B * a.Hkv * a.chunks * a.split));
+    if (a.split == 1) return launch_pdl(decode_stream_kernel<C, true>, grid, dim3(kDecodeThreads), fixed, s, a);
+    return launch_pdl_cluster(decode_stream_kernel<C, true>, grid, dim3(kDecodeThreads), fixed, s, a.split, a);
+  }
+  const size_t smem = fixed + sizeof(unsigned) * (a.B + 1);
+  const cudaError_t e = smem_attr_once<decode_stream_kernel<C, false>>(smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(decode_stream_kernel<C, false>, dim3(a.ctas), dim3(kDecodeThreads), smem, s, a);
+}
+
+}  // namespace cb

@@ -370,15 +370,19 @@ struct DecodeArgs {
   int B, Hq, Hkv, group, dk, dv;
   int chunks;           // items per key head
   int item_heads;       // query heads of one item: ceil(group / chunks)
+  int split;            // CTAs of a cluster per item (1 to 8), or 0: runs of tiles over one wave of CTAs
   float* part;          // workspace: partial results, two per CTA
   int* record;          // workspace: per CTA {item, pieces} of the item it starts and does not finish
   int ctas;             // grid of the main kernel
   int* err;
 };
 constexpr int kDecodeSimtHeads = 8, kDecodeMmaHeads = 16;  // most query heads of one item
+// CTAs per SM of the streaming kernels: their rings take 48, 72 or 96 KB.
+constexpr int decode_ctas_per_sm(int dk, int dv) { return dk <= 64 && dv <= 64 ? 4 : dk <= 64 || dv <= 64 ? 3 : 2; }
 // Workspace: `ctas` records of two ints, then 2 * ctas partials of `heads` x (dv + 2) floats.
 size_t decode_workspace_bytes(int ctas, int heads, int dv);
 cudaError_t launch_decode_mma(const DecodeArgs& a, cudaStream_t s);  // bf16, rows of whole 16-byte pieces
+cudaError_t launch_decode_fma(const DecodeArgs& a, cudaStream_t s);  // fp32, rows of whole 16-byte pieces
 cudaError_t launch_decode(const DecodeArgs& a, bool bf16, bool vec, cudaStream_t s);
 
 // ------------------------------------------------------------ watchdog hook

@@ -104,6 +104,21 @@ bool tc_map(CUtensorMap* m, const cb_heads* t) {
   return host_map_bf16(m, t->data, dims, strides, box);
 }
 
+// Whether the streaming kernel (columns of at most 16 or 8 (query, head) pairs,
+// keys split over clusters) beats the tiled one of its dtype.
+// bf16: the tiled kernel walks pairs of 128-row tiles, mostly empty rows when
+// there are few queries, and cannot split the keys.  32 sequences, 4 key heads,
+// groups of 5, 2048 keys: 8 queries 54 against 78 us, 16 queries 90 against 78;
+// one sequence, 2 heads, 2048 keys, 64 queries: 11 against 22 us.
+// fp32: tiles of 32 rows at least: 8 sequences, 8 heads of 128, 2048 keys: 64
+// queries 271 against 353 us, 128 queries 524 against 357.
+bool few_queries(const AttnArgs& a, bool bf16, int sms) {
+  if (!bf16) return a.Lq <= 64;
+  const long long rows = static_cast<long long>(a.Lq) * a.group, chunks = (rows + kDecodeMmaHeads - 1) / kDecodeMmaHeads;
+  const long long pairs = (static_cast<long long>((a.Lq + 127) / 128) * a.group + 1) / 2;
+  return 2 * chunks <= 3 * pairs || (chunks <= 8 && a.Lk >= 256 && 4 * pairs * a.B * (a.Hq / a.group) <= sms);
+}
+
 // Shapes of a decode call; fills nothing it refuses.
 cb_status check_decode(const cb_heads* q, const cb_paged_cache* cache) {
   if (!heads_ok(q) || !cache_ok(cache)) return CB_ERR_INVALID_ARG;
@@ -178,6 +193,8 @@ cb_status cb_attention(const cb_heads* q, const cb_heads* k, const cb_heads* v, 
   if (k->len > 0) a.doc_q = score->doc_q, a.doc_k = score->doc_k;
   a.timeout_ns = host_timeout_ns();
   const bool vec = pieces16(q) && pieces16(k) && pieces16(v) && pieces16(out);
+  if (vec && few_queries(a, q->dtype == CB_DTYPE_BF16, sms))
+    return done(launch_attn_rows(a, q->dtype == CB_DTYPE_BF16, sms, static_cast<cudaStream_t>(stream)));
   CUtensorMap qm, km, vm;
   if (q->dtype == CB_DTYPE_BF16 && vec && k->len >= 1 && k->len <= kAttnTcMaxKeys && tc_map(&qm, q) && tc_map(&km, k) &&
       tc_map(&vm, v))

@@ -1,8 +1,9 @@
 // Attention on the tensor cores: bf16 views of whole 16-byte pieces.
 //
-// Persistent CTAs, one per SM. An item is 256 queries of one head, as two
-// tiles t of 128, which walks the visible key tiles of 128 with a running
-// maximum and sum per query:
+// Persistent CTAs, one per SM. The queries of the heads that share a key head
+// are cut into tiles of 128 of one head, heads fastest; an item is two
+// neighbouring tiles t (two heads of a group, or 256 queries of one), which
+// walk the visible key tiles of 128 with a running maximum and sum per query:
 //   S_t = Q_t K^T        tcgen05.mma, both operands in shared memory (TMA, 128-byte swizzle),
 //                        fp32 accumulator in 128 TMEM columns
 //   P_t = 2^(x - m)      x = log2(e) * score, rounded to bf16 and stored over S_t
@@ -171,7 +172,7 @@ struct Shape {
   static constexpr int kStages = SK == 2 || SV == 2 ? 4 : 8;
   static constexpr int kQ = 2 * SK * kSlab;
   static constexpr int kFixed = kQ + kStages * kSlot + kSoftmaxWarps * kTile * 4 /* doc ids */ +
-                                4 * kTile * 4 /* bias by key */ + 1024 /* barriers, item infos */ + 1024 /* alignment */;
+                                8 * kTile * 4 /* bias by key */ + 1024 /* barriers, item infos */ + 1024 /* alignment */;
 };
 
 // Work items of the launch, longest first (under a causal mask the last query
@@ -181,11 +182,21 @@ __device__ __forceinline__ int item_of(int k) {
   return k * gridDim.x + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
 }
 struct Item {
-  int b, h, i0;
+  int b, hk;
+  int h[2], i0[2];  // per tile; a tile past the last one starts at Lq: it has no query
 };
-__device__ __forceinline__ Item item_at(const AttnArgs& a, int q_tiles, int item) {
-  const int heads = a.B * a.Hq, bh = item % heads;
-  return {bh / a.Hq, bh % a.Hq, (q_tiles - 1 - item / heads) * 2 * kTile};
+__device__ __forceinline__ Item item_at(const AttnArgs& a, int pairs, int item) {
+  const int seqs = a.B * (a.Hq / a.group), bh = item % seqs, u = 2 * (pairs - 1 - item / seqs);
+  Item it;
+  it.b = bh / (a.Hq / a.group);
+  it.hk = bh % (a.Hq / a.group);
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int q = (u + t) / a.group;
+    it.h[t] = it.hk * a.group + (u + t) % a.group;
+    it.i0[t] = min(q * kTile, a.Lq);
+  }
+  return it;
 }
 
 // CAP, BIAS: whether scores are capped / biased (a branch per tile would make
@@ -193,7 +204,7 @@ __device__ __forceinline__ Item item_at(const AttnArgs& a, int q_tiles, int item
 template <int SK, int SV, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
-               const __grid_constant__ CUtensorMap vmap, const AttnArgs a, int q_tiles, int items, int list_len) {
+               const __grid_constant__ CUtensorMap vmap, const AttnArgs a, int pairs, int items, int list_len) {
   using SH = Shape<SK, SV>;
   constexpr int NS = SH::kStages;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -201,8 +212,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
   uint8_t* sQ = smem;
   uint8_t* sKV = smem + SH::kQ;
   int* doc_buf = reinterpret_cast<int*>(sKV + NS * SH::kSlot);                // [8 warps][128]
-  float* bias_buf = reinterpret_cast<float*>(doc_buf + kSoftmaxWarps * kTile);  // [2 lists][2 signs][128]: +-log2(e) slope * key
-  uint64_t* q_full = reinterpret_cast<uint64_t*>(bias_buf + 4 * kTile);
+  float* bias_buf = reinterpret_cast<float*>(doc_buf + kSoftmaxWarps * kTile);  // [2 lists][2 tiles][2 signs][128]: +-log2(e) slope * key
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(bias_buf + 8 * kTile);
   uint64_t* q_empty = q_full + 2;
   uint64_t* kv_full = q_empty + 2;
   uint64_t* kv_empty = kv_full + NS;
@@ -267,12 +278,12 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
         if (k >= 2) ok = mbar_wait(&list_free[buf], ((k >> 1) - 1) & 1u, wd);
         ok = __all_sync(~0u, ok);
         if (!ok) break;
-        const Item it = item_at(a, q_tiles, item);
+        const Item it = item_at(a, pairs, item);
         const SeqRule rule = seq_rule(a, it.b);
         uint32_t* list = lists + buf * list_len;
         int hi_lo[2], hi_hi[2];  // per query tile: keys that all / some of its queries see, before documents
         for (int t = 0; t < 2; ++t) {
-          const int r0 = it.i0 + t * kTile, r1 = min(a.Lq, r0 + kTile) - 1;
+          const int r0 = it.i0[t], r1 = min(a.Lq, r0 + kTile) - 1;
           hi_lo[t] = r0 <= r1 ? row_end(a, rule, r0) : 0;
           hi_hi[t] = r0 <= r1 ? row_end(a, rule, r1) : 0;
         }
@@ -280,7 +291,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
         int kept = 0;
         if (!a.doc_k) {
           // from the tile of the item's last query down to the first, then the ones past it
-          const int near = min(all, max(0, (min(a.Lq, it.i0 + 2 * kTile) - 1 + a.q_offset) / kTile + 1));
+          const int near = min(all, max(0, (min(a.Lq, max(it.i0[0] + (it.i0[0] < a.Lq) * kTile, it.i0[1] < a.Lq ? it.i0[1] + kTile : 0)) - 1 + a.q_offset) / kTile + 1));
           for (int x = lane; x < all; x += 32) {
             const int n = x < near ? near - 1 - x : x;
             uint32_t e = n << 4;
@@ -294,7 +305,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
           for (int t = 0; t < 2; ++t) {
             int lo = 0x7fffffff, hi = -1, pad = 0;
             for (int c = lane; c < kTile; c += 32) {
-              const int i = it.i0 + t * kTile + c;
+              const int i = it.i0[t] + c;
               const int d = i < a.Lq ? a.doc_q[static_cast<long long>(it.b) * a.Lq + i] : -1;
               if (d >= 0) lo = min(lo, d), hi = max(hi, d);
               pad |= i < a.Lq && d < 0;
@@ -338,10 +349,14 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
           }
         }
         if (a.slopes) {
-          const float slope = a.slopes[it.h] * kLog2e;
-          for (int c = lane; c < kTile; c += 32) {
-            bias_buf[buf * 2 * kTile + c] = slope * static_cast<float>(c);
-            bias_buf[buf * 2 * kTile + kTile + c] = -slope * static_cast<float>(c);
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const float slope = a.slopes[it.h[t]] * kLog2e;
+            float* y = bias_buf + (buf * 2 + t) * 2 * kTile;
+            for (int c = lane; c < kTile; c += 32) {
+              y[c] = slope * static_cast<float>(c);
+              y[kTile + c] = -slope * static_cast<float>(c);
+            }
           }
         }
         __syncwarp();
@@ -370,7 +385,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
         ok = __all_sync(~0u, ok);
         if (!ok) break;
         const int n = info[buf].n;
-        const Item it = item_at(a, q_tiles, item);
+        const Item it = item_at(a, pairs, item);
         const uint32_t* list = lists + buf * list_len;
         if (n > 0 && lane >= NS && lane < NS + 2) {
           const int t = lane - NS;
@@ -378,12 +393,11 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
           if (ok) {
             mbar_arrive_expect_tx(&q_full[t], SK * kSlab);
             for (int s = 0; s < SK; ++s)
-              tma_load_4d(sQ + (t * SK + s) * kSlab, &qmap, &q_full[t], s * 64, it.h, it.i0 + t * kTile, it.b);
+              tma_load_4d(sQ + (t * SK + s) * kSlab, &qmap, &q_full[t], s * 64, it.h[t], it.i0[t], it.b);
             ++use;
           }
         }
         if (lane < NS) {
-          const int hk = it.h / a.group;
           // this lane's first place in the item: base + q == lane mod NS
           for (int q = (lane - static_cast<int>(base % NS) + NS) % NS; q < 2 * n; q += NS) {
             ok = use == 0 || mbar_wait(&kv_empty[lane], (use - 1) & 1u, wd);
@@ -392,7 +406,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
             const bool is_v = q & 1;
             mbar_arrive_expect_tx(&kv_full[lane], (is_v ? SV : SK) * kSlab);
             for (int s = 0; s < (is_v ? SV : SK); ++s)
-              tma_load_4d(sKV + lane * SH::kSlot + s * kSlab, is_v ? &vmap : &kmap, &kv_full[lane], s * 64, hk, j0, it.b);
+              tma_load_4d(sKV + lane * SH::kSlot + s * kSlab, is_v ? &vmap : &kmap, &kv_full[lane], s * 64, it.hk, j0, it.b);
             ++use;
           }
         }
@@ -573,8 +587,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
     for (int k = 0, item; ok && k < rounds; ++k) {
         if ((item = item_of(k)) >= items) break;
       const int buf = k & 1;
-      const Item it = item_at(a, q_tiles, item);
-      const int i = it.i0 + t * kTile + row;
+      const Item it = item_at(a, pairs, item);
+      const int i = it.i0[t] + row, h = it.h[t];
       const int doc = a.doc_q && i < a.Lq ? a.doc_q[static_cast<long long>(it.b) * a.Lq + i] : 0;
       ok = __all_sync(~0u, mbar_wait(&list_full[buf], (k >> 1) & 1u, wd));
       if (!ok) break;
@@ -582,7 +596,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
       const int hi = i < a.Lq && doc >= 0 ? row_end(a, SeqRule{inf.kv, inf.prefix}, i) : 0;
       const int at = i + a.q_offset;
       const uint32_t* list = lists + buf * list_len;
-      const float* by_key = bias_buf + buf * 2 * kTile;
+      const float* by_key = bias_buf + (buf * 2 + t) * 2 * kTile;
       const float slope = BIAS ? by_key[1] : 0.f;
       float m_ref = kNegInf, l = 0.f;
       bool any = false;
@@ -732,7 +746,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
       }
       const float inv = l == 0.f ? 0.f : 1.f / l;
       float probe = inv * 0.f;
-      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.o) + it.b * a.os_b + static_cast<long long>(i) * a.os_l + it.h * a.os_h;
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.o) + it.b * a.os_b + static_cast<long long>(i) * a.os_l + h * a.os_h;
 #pragma unroll
       for (int d0 = 0; d0 < SV * 64; d0 += 16) {
         if (d0 >= a.dv) break;
@@ -765,7 +779,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
       while (bad) {
         const int r = __ffs(bad) - 1;
         bad &= bad - 1;
-        attn_row_inline<__nv_bfloat16>(a, it.b, it.h, it.i0 + t * kTile + (warp & 3) * 32 + r);
+        attn_row_inline<__nv_bfloat16>(a, it.b, h, it.i0[t] + (warp & 3) * 32 + r);
       }
     }
     tc_fence_before_sync();
@@ -784,11 +798,11 @@ cudaError_t launch_one(const CUtensorMap& q, const CUtensorMap& k, const CUtenso
   const size_t smem = Shape<SK, SV>::kFixed + 2 * list_len(a.Lk) * sizeof(uint32_t);
   const cudaError_t e = smem_attr_once<attn_tc_kernel<SK, SV, CAP, BIAS>>(smem);
   if (e != cudaSuccess) return e;
-  const int tiles = (a.Lq + 2 * kTile - 1) / (2 * kTile);
-  const long long items = static_cast<long long>(tiles) * a.B * a.Hq;
+  const long long tiles = static_cast<long long>((a.Lq + kTile - 1) / kTile) * a.group, pairs = (tiles + 1) / 2;
+  const long long items = pairs * a.B * (a.Hq / a.group);
   if (items >= (1LL << 30)) return cudaErrorInvalidConfiguration;
   const int grid = static_cast<int>(items < sms ? items : sms);
-  return launch_pdl(attn_tc_kernel<SK, SV, CAP, BIAS>, dim3(grid), dim3(kThreads), smem, s, q, k, v, a, tiles,
+  return launch_pdl(attn_tc_kernel<SK, SV, CAP, BIAS>, dim3(grid), dim3(kThreads), smem, s, q, k, v, a, static_cast<int>(pairs),
                     static_cast<int>(items), static_cast<int>(list_len(a.Lk)));
 }
 

@@ -244,6 +244,26 @@ size_t decode_workspace_bytes(int ctas, int heads, int dv) {
   return sizeof(float) * 2 * ctas * part_floats(heads, dv) + sizeof(int) * 2 * ctas;
 }
 
+cudaError_t launch_attn_rows(const AttnArgs& rw, bool bf16, int sms, cudaStream_t s) {
+  DecodeArgs a{};
+  a.scale = rw.scale, a.softcap = rw.softcap;
+  a.B = rw.B, a.Hq = rw.Hq, a.group = rw.group, a.Hkv = rw.Hq / rw.group;
+  a.dk = rw.dk, a.dv = rw.dv;
+  // a sequence is one page of Lk slots
+  a.cache.k = const_cast<void*>(rw.k), a.cache.v = const_cast<void*>(rw.v);
+  a.cache.ks_p = rw.ks_b, a.cache.ks_t = rw.ks_l, a.cache.ks_h = rw.ks_h;
+  a.cache.vs_p = rw.vs_b, a.cache.vs_t = rw.vs_l, a.cache.vs_h = rw.vs_h;
+  const int rows = rw.Lq * rw.group, most = bf16 ? kDecodeMmaHeads : kDecodeSimtHeads;
+  a.chunks = (rows + most - 1) / most;
+  a.item_heads = (rows + a.chunks - 1) / a.chunks;
+  // A cluster per item while that fills the GPU better and leaves every CTA a tile.
+  const long long items = static_cast<long long>(a.B) * a.Hkv * a.chunks, room = sms * decode_ctas_per_sm(a.dk, a.dv);
+  const int tiles = (rw.Lk + 63) / 64;
+  a.split = 1;
+  while (a.split < 8 && items * a.split * 2 <= room && a.split < tiles) a.split *= 2;
+  return bf16 ? launch_rows_mma(a, rw, s) : launch_rows_fma(a, rw, s);
+}
+
 cudaError_t launch_decode(const DecodeArgs& a, bool bf16, bool vec, cudaStream_t s) {
   cudaError_t e;
   if (vec)

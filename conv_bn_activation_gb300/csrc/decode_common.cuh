@@ -130,6 +130,28 @@ __device__ __forceinline__ Piece whole_piece(const DecodeArgs& a, int per_seq) {
   return p;
 }
 
+// The same for contiguous rows: columns are (query, head) pairs r = query *
+// group + head in the group, a.item_heads of them per item.
+__device__ __forceinline__ Piece rows_piece(const DecodeArgs& a, const AttnArgs& rw) {
+  const int all = blockIdx.x / a.split, rank = blockIdx.x % a.split;
+  const int rows = rw.Lq * a.group, per_seq = a.Hkv * a.chunks;
+  Piece p;
+  p.b = all / per_seq;
+  p.item = all % per_seq;
+  p.hk = p.item / a.chunks;
+  p.h0 = (p.item % a.chunks) * a.item_heads;
+  p.heads = min(a.item_heads, rows - p.h0);
+  p.lo = 0;
+  p.hi = row_end(rw, seq_rule(rw, p.b), (p.h0 + p.heads - 1) / a.group);
+  p.len = p.hi;
+  const int tiles = (p.hi + kDecodeTile - 1) / kDecodeTile;
+  p.tile0 = static_cast<int>(static_cast<long long>(tiles) * rank / a.split);
+  p.tiles = static_cast<int>(static_cast<long long>(tiles) * (rank + 1) / a.split) - p.tile0;
+  p.starts = p.ends = a.split == 1;
+  p.last = 0;
+  return p;
+}
+
 // Sequences without a visible token: zeros, dealt over the CTAs.
 template <typename Store>
 __device__ __forceinline__ void zero_empty(const DecodeArgs& a, const unsigned* prefix, Store store) {

@@ -16,10 +16,11 @@ __device__ __forceinline__ float4 lds4(uint32_t addr) {
   return v;
 }
 
-template <int DK_, int DV_, int NH>
+template <int DK_, int DV_, int NH, bool ROWS>
 struct FmaPolicy {
   using T = float;
   static constexpr int DK = DK_, DV = DV_, kStep = 8, kStages = 3, kHeads = NH;
+  static constexpr bool kRows = ROWS;
   static constexpr int kQBytes = NH * DK * 4;                          // q, one copy per CTA
   static constexpr int kPStride = NH < 4 ? 4 : NH;                     // weights [8 keys][heads] per warp
   static constexpr int kExtra = kQBytes + kDecodeWarps * 8 * kPStride * 4;
@@ -34,16 +35,17 @@ struct FmaPolicy {
   int key, sub, lane, heads;
   uint32_t q_addr, p_addr;
   float* p_mine;
+  RowRule rule[OWN];
   float slope[OWN], m[OWN], l[OWN], o[NH][EV];
 
-  __device__ __forceinline__ FmaPolicy(const DecodeArgs& a, const Piece& pc, uint8_t* after) : score(a) {
+  __device__ __forceinline__ FmaPolicy(const DecodeArgs& a, const AttnArgs& rw, const Piece& pc, uint8_t* after) : score(a) {
     lane = threadIdx.x & 31;
     const int warp = threadIdx.x >> 5;
     key = lane >> 2, sub = lane & 3, heads = pc.heads;
     float* q = reinterpret_cast<float*>(after);
     for (int e = threadIdx.x; e < NH * DK; e += kDecodeThreads) {
       const int h = e / DK, d = e % DK;
-      q[e] = h < heads && d < a.dk ? static_cast<const float*>(a.q)[pc.b * a.qs_b + (pc.h0 + h) * a.qs_h + d] : 0.f;
+      q[e] = h < heads && d < a.dk ? query_row<ROWS, float>(a, rw, pc, h)[d] : 0.f;
     }
     __syncthreads();
     q_addr = smem_u32(q);
@@ -52,7 +54,8 @@ struct FmaPolicy {
 #pragma unroll
     for (int i = 0; i < OWN; ++i) {
       const int h = sub + 4 * i;
-      slope[i] = a.slopes && h < heads ? a.slopes[pc.h0 + h] * kLog2e : 0.f;
+      slope[i] = slope_of(a, rw, pc, h, ROWS);
+      if constexpr (ROWS) rule[i] = row_rule(a, rw, pc, h);
       m[i] = kNegInf;
       l[i] = 0.f;
     }
@@ -62,7 +65,7 @@ struct FmaPolicy {
       for (int e = 0; e < EV; ++e) o[h][e] = 0.f;
   }
 
-  __device__ __forceinline__ void step(uint32_t ks, uint32_t vs, unsigned lv, int far) {
+  __device__ __forceinline__ void step(uint32_t ks, uint32_t vs, unsigned lv, int far, int doc) {
     float dot[NH];
 #pragma unroll
     for (int h = 0; h < NH; ++h) dot[h] = 0.f;
@@ -78,6 +81,7 @@ struct FmaPolicy {
     }
     // This lane's heads sub, sub + 4, ... of its key.
     const bool exists = (lv >> key) & 1;
+    const int my_doc = ROWS ? __shfl_sync(~0u, doc, key) : 0;
     float x[OWN], mx[OWN];
     bool grow = false;
 #pragma unroll
@@ -89,7 +93,13 @@ struct FmaPolicy {
       const float e0 = (hi ? d2 : d0) + __shfl_xor_sync(~0u, hi ? d0 : d2, 2);
       const float e1 = (hi ? d3 : d1) + __shfl_xor_sync(~0u, hi ? d1 : d3, 2);
       const float d = (odd ? e1 : e0) + __shfl_xor_sync(~0u, odd ? e0 : e1, 1);
-      x[i] = exists ? fmaf(-slope[i], static_cast<float>(far - key), score(d)) : kNegInf;
+      if constexpr (ROWS) {
+        const int j = far + key;
+        const bool seen = exists && j < rule[i].hi && my_doc == rule[i].doc;
+        x[i] = seen ? fmaf(-slope[i], static_cast<float>(abs(rule[i].at - j)), score(d)) : kNegInf;
+      } else {
+        x[i] = exists ? fmaf(-slope[i], static_cast<float>(far - key), score(d)) : kNegInf;
+      }
       float y = x[i];
       y = fmaxf(y, __shfl_xor_sync(~0u, y, 4));
       y = fmaxf(y, __shfl_xor_sync(~0u, y, 8));
@@ -166,10 +176,10 @@ struct FmaPolicy {
 
 template <int DK, int DV>
 cudaError_t launch_dims(const DecodeArgs& a, cudaStream_t s) {
-  if (a.item_heads <= 1) return launch_decode_stream<FmaPolicy<DK, DV, 1>>(a, s);
-  if (a.item_heads <= 2) return launch_decode_stream<FmaPolicy<DK, DV, 2>>(a, s);
-  if (a.item_heads <= 4) return launch_decode_stream<FmaPolicy<DK, DV, 4>>(a, s);
-  return launch_decode_stream<FmaPolicy<DK, DV, 8>>(a, s);
+  if (a.item_heads <= 1) return launch_decode_stream<FmaPolicy<DK, DV, 1, false>>(a, s);
+  if (a.item_heads <= 2) return launch_decode_stream<FmaPolicy<DK, DV, 2, false>>(a, s);
+  if (a.item_heads <= 4) return launch_decode_stream<FmaPolicy<DK, DV, 4, false>>(a, s);
+  return launch_decode_stream<FmaPolicy<DK, DV, 8, false>>(a, s);
 }
 
 }  // namespace
@@ -177,6 +187,13 @@ cudaError_t launch_dims(const DecodeArgs& a, cudaStream_t s) {
 cudaError_t launch_decode_fma(const DecodeArgs& a, cudaStream_t s) {
   if (a.dk <= 64) return a.dv <= 64 ? launch_dims<64, 64>(a, s) : launch_dims<64, 128>(a, s);
   return a.dv <= 64 ? launch_dims<128, 64>(a, s) : launch_dims<128, 128>(a, s);
+}
+
+cudaError_t launch_rows_fma(const DecodeArgs& a, const AttnArgs& rw, cudaStream_t s) {
+  const long long ctas = static_cast<long long>(a.B) * a.Hkv * a.chunks * a.split;
+  if (a.dk <= 64)
+    return a.dv <= 64 ? launch_whole<FmaPolicy<64, 64, 8, true>>(a, rw, ctas, s) : launch_whole<FmaPolicy<64, 128, 8, true>>(a, rw, ctas, s);
+  return a.dv <= 64 ? launch_whole<FmaPolicy<128, 64, 8, true>>(a, rw, ctas, s) : launch_whole<FmaPolicy<128, 128, 8, true>>(a, rw, ctas, s);
 }
 
 }  // namespace cb

@@ -41,10 +41,11 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t* a, uint3
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <int DK_, int DV_, int NB>
+template <int DK_, int DV_, int NB, bool ROWS>
 struct MmaPolicy {
   using T = __nv_bfloat16;
   static constexpr int DK = DK_, DV = DV_, kStep = 16, kStages = 3, kHeads = 8 * NB, kExtra = 0;
+  static constexpr bool kRows = ROWS;
   static constexpr int kKeyBytes = DK * 2, kValBytes = DV * 2;
   static __device__ __forceinline__ constexpr int swizzle(int row) { return row & 7; }
 
@@ -55,34 +56,38 @@ struct MmaPolicy {
   // Q^T as the MMA's B operand: head g of each 8, elements 2 t4 and 2 t4 + 8 of each 16.
   uint32_t qf[DK / 16][NB][2];
   // This thread's heads are 8 nb + 2 t4 and the one after.
+  RowRule rule[NB][2];
   float slope[NB][2], m[NB][2], l[NB][2], o[DV / 16][NB][4];
 
-  __device__ __forceinline__ MmaPolicy(const DecodeArgs& a, const Piece& pc, uint8_t*) : score(a) {
+  __device__ __forceinline__ MmaPolicy(const DecodeArgs& a, const AttnArgs& rw, const Piece& pc, uint8_t*) : score(a) {
     const int lane = threadIdx.x & 31;
     g = lane >> 2, t4 = lane & 3, heads = pc.heads;
-    bias = a.slopes != nullptr;
+    bias = ROWS ? rw.slopes != nullptr : a.slopes != nullptr;
     k_src = ((lane & 7) + 8 * ((lane >> 3) & 1)) * kKeyBytes + (((lane >> 4) ^ (lane & 7)) * 16);
     v_src = ((lane & 7) + 8 * (lane >> 4)) * kValBytes + ((((lane >> 3) & 1) ^ (lane & 7)) * 16);
 #pragma unroll
-    for (int s = 0; s < DK / 16; ++s)
+    for (int nb = 0; nb < NB; ++nb) {
+      const int hd = g + 8 * nb;
+      const T* q = query_row<ROWS, T>(a, rw, pc, hd < heads ? hd : 0);
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
+      for (int s = 0; s < DK / 16; ++s)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const int hd = g + 8 * nb, d = 16 * s + 2 * t4 + 8 * r;
+          const int d = 16 * s + 2 * t4 + 8 * r;
           uint32_t w = 0;
-          if (hd < heads && d < a.dk) {  // dk is even
-            const T* q = static_cast<const T*>(a.q) + pc.b * a.qs_b + (pc.h0 + hd) * a.qs_h + d;
-            w = static_cast<uint32_t>(__bfloat16_as_ushort(q[0])) | (static_cast<uint32_t>(__bfloat16_as_ushort(q[1])) << 16);
-          }
+          if (hd < heads && d < a.dk)  // dk is even; rows are 16-byte aligned, a decode query need not be
+            w = ROWS ? *reinterpret_cast<const uint32_t*>(q + d)
+                     : static_cast<uint32_t>(__bfloat16_as_ushort(q[d])) | (static_cast<uint32_t>(__bfloat16_as_ushort(q[d + 1])) << 16);
           qf[s][nb][r] = w;
         }
+    }
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int hd = 8 * nb + 2 * t4 + e;
-        slope[nb][e] = bias && hd < heads ? a.slopes[pc.h0 + hd] * kLog2e : 0.f;
+        slope[nb][e] = slope_of(a, rw, pc, hd, ROWS);
+        if constexpr (ROWS) rule[nb][e] = row_rule(a, rw, pc, hd);
         m[nb][e] = kNegInf;
         l[nb][e] = 0.f;
       }
@@ -93,8 +98,9 @@ struct MmaPolicy {
     }
   }
 
-  // 16 keys at ks / vs; bit x of lv: key x exists; far: distance of the first key.
-  __device__ __forceinline__ void step(uint32_t ks, uint32_t vs, unsigned lv, int far) {
+  // 16 keys at ks / vs; bit x of lv: key x exists; far: the first key's distance
+  // from the query (ROWS: its place); doc: the document of key lane % 16 (ROWS).
+  __device__ __forceinline__ void step(uint32_t ks, uint32_t vs, unsigned lv, int far, int doc) {
     float s[NB][4];  // element r: key g + 8 (r >> 1), head 8 nb + 2 t4 + (r & 1)
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
@@ -109,6 +115,7 @@ struct MmaPolicy {
     }
     // x = log2(e) * score
     const float dist = static_cast<float>(far - g);
+    const int doc0 = ROWS ? __shfl_sync(~0u, doc, g) : 0, doc1 = ROWS ? __shfl_sync(~0u, doc, g + 8) : 0;
     bool grow = false;
     float mx[NB][2];
 #pragma unroll
@@ -116,7 +123,14 @@ struct MmaPolicy {
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         float x = score(s[nb][r]);
-        if (bias) x = fmaf(-slope[nb][r & 1], dist - 8.f * (r >> 1), x);
+        if constexpr (ROWS) {
+          const RowRule& w = rule[nb][r & 1];
+          const int j = far + g + 8 * (r >> 1);
+          if (bias) x = fmaf(-slope[nb][r & 1], static_cast<float>(abs(w.at - j)), x);
+          if (j >= w.hi || (r < 2 ? doc0 : doc1) != w.doc) x = kNegInf;
+        } else {
+          if (bias) x = fmaf(-slope[nb][r & 1], dist - 8.f * (r >> 1), x);
+        }
         if (lv != 0xffffu && !((lv >> (g + 8 * (r >> 1))) & 1)) x = kNegInf;
         s[nb][r] = x;
       }
@@ -188,7 +202,8 @@ struct MmaPolicy {
 
 template <int DK, int DV>
 cudaError_t launch_dims(const DecodeArgs& a, cudaStream_t s) {
-  return a.item_heads <= 8 ? launch_decode_stream<MmaPolicy<DK, DV, 1>>(a, s) : launch_decode_stream<MmaPolicy<DK, DV, 2>>(a, s);
+  return a.item_heads <= 8 ? launch_decode_stream<MmaPolicy<DK, DV, 1, false>>(a, s)
+                           : launch_decode_stream<MmaPolicy<DK, DV, 2, false>>(a, s);
 }
 
 }  // namespace
@@ -196,6 +211,13 @@ cudaError_t launch_dims(const DecodeArgs& a, cudaStream_t s) {
 cudaError_t launch_decode_mma(const DecodeArgs& a, cudaStream_t s) {
   if (a.dk <= 64) return a.dv <= 64 ? launch_dims<64, 64>(a, s) : launch_dims<64, 128>(a, s);
   return a.dv <= 64 ? launch_dims<128, 64>(a, s) : launch_dims<128, 128>(a, s);
+}
+
+cudaError_t launch_rows_mma(const DecodeArgs& a, const AttnArgs& rw, cudaStream_t s) {
+  const long long ctas = static_cast<long long>(a.B) * a.Hkv * a.chunks * a.split;
+  if (a.dk <= 64)
+    return a.dv <= 64 ? launch_whole<MmaPolicy<64, 64, 2, true>>(a, rw, ctas, s) : launch_whole<MmaPolicy<64, 128, 2, true>>(a, rw, ctas, s);
+  return a.dv <= 64 ? launch_whole<MmaPolicy<128, 64, 2, true>>(a, rw, ctas, s) : launch_whole<MmaPolicy<128, 128, 2, true>>(a, rw, ctas, s);
 }
 
 }  // namespace cb

@@ -1,6 +1,12 @@
-// The streaming decode kernel: one new token's attention over a paged cache
-// whose rows are whole 16-byte pieces.  A policy C does the arithmetic
-// (decode_mma.cu: bf16 by warp-level MMAs; decode_fma.cu: fp32 by FMAs).
+// The streaming attention kernel for few queries per key head, over keys and
+// values whose rows are whole 16-byte pieces.  A policy C does the arithmetic
+// (decode_mma.cu: bf16 by warp-level MMAs; decode_fma.cu: fp32 by FMAs) for
+// one of two sources:
+//  - a paged cache and one new token per sequence (cb_attention_decode): an
+//    item's columns are query heads that share a key head;
+//  - contiguous rows and short query sequences (cb_attention, C::kRows): an
+//    item's columns are (query, head) pairs that share a key head, each with
+//    its own visible keys.
 //
 // Bound by HBM: (dk + dv) * sizeof(element) bytes per cached token and key
 // head, read once.  A CTA's four warps walk a piece of one item together: each
@@ -11,8 +17,8 @@
 // Two ways to deal items (decode_common.cuh):
 //  - Runs: equal runs of tiles over one wave of CTAs; items cut by a run's end
 //    go through the workspace and a join kernel.
-//  - Whole items, for caches small enough that a CTA walks at most eight tiles:
-//    a cluster of a.split CTAs per item, joined through distributed shared
+//  - Whole items, for caches small enough that a CTA walks at most eight tiles
+//    and for contiguous rows: a cluster of a.split CTAs per item, joined through distributed shared
 //    memory.  One launch, no prefix over the lengths: one sequence of 421
 //    tokens takes 5.6 us where runs and their join take 7.7.
 #pragma once
@@ -59,6 +65,43 @@ struct DecodeScore {
   }
 };
 
+// Where column hd of an item comes from and goes to.
+template <bool ROWS, typename T>
+__device__ __forceinline__ const T* query_row(const DecodeArgs& a, const AttnArgs& rw, const Piece& pc, int hd) {
+  if constexpr (ROWS) {
+    const int r = pc.h0 + hd;
+    return static_cast<const T*>(rw.q) + pc.b * rw.qs_b + r / a.group * rw.qs_l + (pc.hk * a.group + r % a.group) * rw.qs_h;
+  }
+  return static_cast<const T*>(a.q) + pc.b * a.qs_b + (pc.h0 + hd) * a.qs_h;
+}
+template <bool ROWS, typename T>
+__device__ __forceinline__ T* out_row(const DecodeArgs& a, const AttnArgs& rw, const Piece& pc, int hd) {
+  if constexpr (ROWS) {
+    const int r = pc.h0 + hd;
+    return static_cast<T*>(rw.o) + pc.b * rw.os_b + r / a.group * rw.os_l + (pc.hk * a.group + r % a.group) * rw.os_h;
+  }
+  return static_cast<T*>(a.o) + pc.b * a.os_b + (pc.h0 + hd) * a.os_h;
+}
+__device__ __forceinline__ float slope_of(const DecodeArgs& a, const AttnArgs& rw, const Piece& pc, int hd, bool rows) {
+  const float* slopes = rows ? rw.slopes : a.slopes;
+  if (!slopes || hd >= pc.heads) return 0.f;
+  return slopes[rows ? pc.hk * a.group + (pc.h0 + hd) % a.group : pc.h0 + hd] * kLog2e;
+}
+// What a row query sees: keys [0, hi) of its document; it stands at `at`.
+struct RowRule {
+  int hi, at, doc;
+};
+__device__ __forceinline__ RowRule row_rule(const DecodeArgs& a, const AttnArgs& rw, const Piece& pc, int hd) {
+  RowRule r{0, 0, -2};
+  if (hd >= pc.heads) return r;
+  const int i = (pc.h0 + hd) / a.group;
+  r.hi = row_end(rw, seq_rule(rw, pc.b), i);
+  r.at = i + rw.q_offset;
+  r.doc = rw.doc_q ? rw.doc_q[static_cast<long long>(pc.b) * rw.Lq + i] : -1;  // without documents a key's is -1 too
+  if (rw.doc_q && r.doc < 0) r.hi = 0;
+  return r;
+}
+
 template <class C>
 constexpr int decode_ring_bytes() {  // also holds the results when a piece ends
   return kDecodeWarps * C::kStages * C::kStep * (C::DK + C::DV) * static_cast<int>(sizeof(typename C::T));
@@ -69,7 +112,7 @@ constexpr int decode_part_offset() {  // floats: the four warps' results, then t
 }
 
 template <class C, bool WHOLE>
-__global__ void __launch_bounds__(kDecodeThreads, decode_ctas_per_sm(C::DK, C::DV)) decode_stream_kernel(const DecodeArgs a) {
+__global__ void __launch_bounds__(kDecodeThreads, decode_ctas_per_sm(C::DK, C::DV)) decode_stream_kernel(const DecodeArgs a, const AttnArgs rw) {
   using T = typename C::T;
   constexpr int DK = C::DK, DV = C::DV, kStep = C::kStep, kStages = C::kStages, kEl = static_cast<int>(sizeof(T));
   constexpr int kKeyBytes = DK * kEl, kValBytes = DV * kEl, kStageBytes = kStep * (kKeyBytes + kValBytes);
@@ -119,10 +162,14 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas_per_sm(C::DK, C::D
   const bool same = a.cache.ks_p == a.cache.vs_p && a.cache.ks_t == a.cache.vs_t;  // one offset serves both
 
   while (at < end) {
-    const Piece pc = WHOLE ? whole_piece(a, per_seq) : next_piece(a, prefix, per_seq, at, end, &b);
+    static_assert(WHOLE || !C::kRows, "contiguous rows are dealt as whole items");
+    Piece pc;
+    if constexpr (C::kRows) pc = rows_piece(a, rw);
+    else if constexpr (WHOLE) pc = whole_piece(a, per_seq);
+    else pc = next_piece(a, prefix, per_seq, at, end, &b);
     const char* kbase = static_cast<const char*>(a.cache.k) + pc.hk * a.cache.ks_h * kEl + (lane % CK) * 16;
     const char* vbase = static_cast<const char*>(a.cache.v) + pc.hk * a.cache.vs_h * kEl + (lane % CV) * 16;
-    C c(a, pc, after);
+    C c(a, rw, pc, after);
 
     // Lanes below kStep look the step's tokens up, one step before their copies
     // are issued: the byte offsets of the rows, or -1.
@@ -130,11 +177,18 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas_per_sm(C::DK, C::D
     const int steps = pc.tiles * (kDecodeTile / (kDecodeWarps * kStep));
     struct Rows {
       long long k, v;
+      int doc;  // contiguous rows: the key's document
     };
     auto lookup = [&](int step) {
       const int j = base + step * (kDecodeWarps * kStep) + lane % kStep;
-      Rows r{-1, -1};
+      Rows r{-1, -1, -1};
       if (step < steps && j >= pc.lo && j < pc.hi) {
+        if constexpr (C::kRows) {
+          r.k = (pc.b * a.cache.ks_p + j * a.cache.ks_t) * kEl;
+          r.v = (pc.b * a.cache.vs_p + j * a.cache.vs_t) * kEl;
+          if (rw.doc_k) r.doc = rw.doc_k[static_cast<long long>(pc.b) * rw.Lk + j];
+          return r;
+        }
         int slot;
         const long long page = token_page(a, pc.b, j, &slot);
         if (page >= 0) {
@@ -146,6 +200,7 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas_per_sm(C::DK, C::D
     };
     constexpr unsigned kAll = kStep == 32 ? ~0u : (1u << kStep) - 1;
     unsigned live[kStages];  // bit x: token x of the stage's step exists
+    int docs[kStages];
     auto issue = [&](int step, int stage, const Rows& rows) {
       const unsigned have = __ballot_sync(~0u, rows.k >= 0) & kAll;
       if (step < steps) {
@@ -176,7 +231,11 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas_per_sm(C::DK, C::D
     };
 
 #pragma unroll
-    for (int s = 0; s < kStages - 1; ++s) live[s] = issue(s, s, lookup(s));
+    for (int s = 0; s < kStages - 1; ++s) {
+      const Rows r = lookup(s);
+      live[s] = issue(s, s, r);
+      docs[s] = r.doc;
+    }
     Rows rows = lookup(kStages - 1);
     int stage = 0;
     for (int step = 0; step < steps; ++step) {
@@ -186,17 +245,20 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas_per_sm(C::DK, C::D
         const unsigned lv = issue(step + kStages - 1, fill, rows);
 #pragma unroll
         for (int s = 0; s < kStages; ++s)
-          if (s == fill) live[s] = lv;
+          if (s == fill) live[s] = lv, docs[s] = rows.doc;
       }
       rows = lookup(step + kStages);
       cp_async_wait<kStages - 1>();
       __syncwarp();
       unsigned lv = 0;
+      int doc = 0;
 #pragma unroll
       for (int s = 0; s < kStages; ++s)
-        if (s == stage) lv = live[s];
+        if (s == stage) lv = live[s], doc = docs[s];
       const uint32_t ks = ring_addr + stage * kStageBytes;
-      c.step(ks, ks + kStep * kKeyBytes, lv, pc.len - 1 - base - step * (kDecodeWarps * kStep));
+      // a decode query stands pc.len - 1 - j before key j; a row query knows its own place
+      const int j0 = base + step * (kDecodeWarps * kStep);
+      c.step(ks, ks + kStep * kKeyBytes, lv, C::kRows ? j0 : pc.len - 1 - j0, doc);
       stage = stage + 1 == kStages ? 0 : stage + 1;
     }
     cp_async_wait<0>();
@@ -209,29 +271,37 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas_per_sm(C::DK, C::D
     float* part_s = res + decode_part_offset<C>();
     float* part = WHOLE ? nullptr : a.part + (2 * cta + (pc.starts ? 1 : 0)) * part_floats(a.item_heads, a.dv);
     const bool out = pc.starts && pc.ends;
+    if (tid < pc.heads) {
+      float mm = kNegInf, ll = 0.f, f[kDecodeWarps];
+#pragma unroll
+      for (int w = 0; w < kDecodeWarps; ++w) mm = fmaxf(mm, ms[w][tid]);
+      const float mu = mm == kNegInf ? 0.f : mm;
+#pragma unroll
+      for (int w = 0; w < kDecodeWarps; ++w) {
+        f[w] = exp2_approx(ms[w][tid] - mu);
+        ll = fmaf(f[w], ls[w][tid], ll);
+      }
+      const float inv = !out ? 1.f : ll == 0.f ? 0.f : 1.f / ll;
+#pragma unroll
+      for (int w = 0; w < kDecodeWarps; ++w) ms[w][tid] = f[w] * inv;
+      if constexpr (WHOLE) part_m[tid] = mm, part_l[tid] = ll;
+      else if (!out) part[tid] = mm, part[a.item_heads + tid] = ll;
+    }
+    __syncthreads();
+    bool bad = false;  // contiguous rows: a result that is not finite
+    auto put = [&](int hd, int d, float y) {
+      out_row<C::kRows, T>(a, rw, pc, hd)[d] = from_f32<T>(y);
+      bad |= !(y * 0.f == 0.f);
+    };
     for (int e = tid; e < pc.heads * DV; e += kDecodeThreads) {
       const int hd = e / DV, d = e % DV;
       if (d >= a.dv) continue;
-      float mm = kNegInf;
+      float sum = 0.f;
 #pragma unroll
-      for (int w = 0; w < kDecodeWarps; ++w) mm = fmaxf(mm, ms[w][hd]);
-      const float mu = mm == kNegInf ? 0.f : mm;
-      float sum = 0.f, ll = 0.f;
-#pragma unroll
-      for (int w = 0; w < kDecodeWarps; ++w) {
-        const float f = exp2_approx(ms[w][hd] - mu);
-        sum = fmaf(f, res[(w * pc.heads + hd) * DV + d], sum);
-        ll = fmaf(f, ls[w][hd], ll);
-      }
-      if (out) {
-        static_cast<T*>(a.o)[pc.b * a.os_b + (pc.h0 + hd) * a.os_h + d] = from_f32<T>(ll == 0.f ? 0.f : sum / ll);
-      } else if constexpr (WHOLE) {
-        part_s[hd * DV + d] = sum;
-        if (d == 0) part_m[hd] = mm, part_l[hd] = ll;
-      } else {
-        part[2 * a.item_heads + hd * a.dv + d] = sum;
-        if (d == 0) part[hd] = mm, part[a.item_heads + hd] = ll;
-      }
+      for (int w = 0; w < kDecodeWarps; ++w) sum = fmaf(ms[w][hd], res[(w * pc.heads + hd) * DV + d], sum);
+      if (out) put(hd, d, sum);
+      else if constexpr (WHOLE) part_s[hd * DV + d] = sum;
+      else part[2 * a.item_heads + hd * a.dv + d] = sum;
     }
     if constexpr (WHOLE) {
       if (a.split > 1) {  // the cluster's CTAs share the item: each joins every a.split-th value of all
@@ -253,9 +323,19 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas_per_sm(C::DK, C::D
               sum = fmaf(f, ld_cluster_f32(map_shared_rank(smem_u32(part_s + e), r)), sum);
               ll = fmaf(f, ld_cluster_f32(map_shared_rank(smem_u32(part_l + hd), r)), ll);
             }
-          static_cast<T*>(a.o)[pc.b * a.os_b + (pc.h0 + hd) * a.os_h + d] = from_f32<T>(ll == 0.f ? 0.f : sum / ll);
+          put(hd, d, ll == 0.f ? 0.f : sum / ll);
         }
         cluster_sync();  // the parts are read before any CTA leaves
+      }
+      if constexpr (C::kRows) {
+        // A masked key's weight 0 times an infinite or NaN value: such rows again, key by key (attn_row).
+        if (__syncthreads_or(bad))
+          for (int hd = warp; hd < pc.heads; hd += kDecodeWarps) {
+            const T* o = out_row<true, T>(a, rw, pc, hd);
+            bool any = false;
+            for (int d = lane; d < a.dv; d += 32) any |= !(to_f32(o[d]) * 0.f == 0.f);
+            if (__any_sync(~0u, any)) attn_row<T>(rw, pc.b, pc.hk * a.group + (pc.h0 + hd) % a.group, (pc.h0 + hd) / a.group);
+          }
       }
       return;
     }
@@ -270,19 +350,24 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas_per_sm(C::DK, C::D
 }
 
 template <class C>
+cudaError_t launch_whole(const DecodeArgs& a, const AttnArgs& rw, long long ctas, cudaStream_t s) {
+  const size_t smem = decode_ring_bytes<C>() + C::kExtra;
+  const cudaError_t e = smem_attr_once<decode_stream_kernel<C, true>>(smem);
+  if (e != cudaSuccess) return e;
+  if (ctas >= (1LL << 31)) return cudaErrorInvalidConfiguration;
+  const dim3 grid(static_cast<unsigned>(ctas));
+  if (a.split == 1) return launch_pdl(decode_stream_kernel<C, true>, grid, dim3(kDecodeThreads), smem, s, a, rw);
+  return launch_pdl_cluster(decode_stream_kernel<C, true>, grid, dim3(kDecodeThreads), smem, s, a.split, a, rw);
+}
+
+template <class C>
 cudaError_t launch_decode_stream(const DecodeArgs& a, cudaStream_t s) {
-  const size_t fixed = decode_ring_bytes<C>() + C::kExtra;
-  if (a.split) {
-    const cudaError_t e = smem_attr_once<decode_stream_kernel<C, true>>(fixed);
-    if (e != cudaSuccess) return e;
-    const dim3 grid(static_cast<unsigned>(a.B * a.Hkv * a.chunks * a.split));
-    if (a.split == 1) return launch_pdl(decode_stream_kernel<C, true>, grid, dim3(kDecodeThreads), fixed, s, a);
-    return launch_pdl_cluster(decode_stream_kernel<C, true>, grid, dim3(kDecodeThreads), fixed, s, a.split, a);
-  }
-  const size_t smem = fixed + sizeof(unsigned) * (a.B + 1);
+  const AttnArgs none{};
+  if (a.split) return launch_whole<C>(a, none, static_cast<long long>(a.B) * a.Hkv * a.chunks * a.split, s);
+  const size_t smem = decode_ring_bytes<C>() + C::kExtra + sizeof(unsigned) * (a.B + 1);
   const cudaError_t e = smem_attr_once<decode_stream_kernel<C, false>>(smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(decode_stream_kernel<C, false>, dim3(a.ctas), dim3(kDecodeThreads), smem, s, a);
+  return launch_pdl(decode_stream_kernel<C, false>, dim3(a.ctas), dim3(kDecodeThreads), smem, s, a, none);
 }
 
 }  // namespace cb

@@ -384,6 +384,12 @@ size_t decode_workspace_bytes(int ctas, int heads, int dv);
 cudaError_t launch_decode_mma(const DecodeArgs& a, cudaStream_t s);  // bf16, rows of whole 16-byte pieces
 cudaError_t launch_decode_fma(const DecodeArgs& a, cudaStream_t s);  // fp32, rows of whole 16-byte pieces
 cudaError_t launch_decode(const DecodeArgs& a, bool bf16, bool vec, cudaStream_t s);
+// cb_attention with few queries per key head through the streaming kernel:
+// columns are (query, head) pairs, at most kDecodeMmaHeads (bf16) or
+// kDecodeSimtHeads (fp32) of them per item.  Fills a from rw.
+cudaError_t launch_attn_rows(const AttnArgs& rw, bool bf16, int sms, cudaStream_t s);
+cudaError_t launch_rows_mma(const DecodeArgs& a, const AttnArgs& rw, cudaStream_t s);
+cudaError_t launch_rows_fma(const DecodeArgs& a, const AttnArgs& rw, cudaStream_t s);
 
 // ------------------------------------------------------------ watchdog hook
 cudaError_t launch_timeout_probe(int* err, uint64_t limit_ns, cudaStream_t s);

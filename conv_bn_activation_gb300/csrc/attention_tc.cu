@@ -13,8 +13,7 @@
 // and the softmax about 900 issue slots of each scheduler; what decides is the
 // chain S -> P -> next S of one tile. So the two tiles take turns (the tensor
 // cores work on one while the other's weights are computed), a thread holds a
-// query's 128 scores in packed fp32 pairs, the first 64 weights are handed to
-// the MMAs while the other 64 are computed, and nothing waits between items:
+// query's 128 scores in packed fp32 pairs, and nothing waits between items:
 // copies run ahead through a ring that items share, a scheduler warp lists the
 // next item's key tiles, and the first MMAs of an item run under the output of
 // the one before.
@@ -27,13 +26,13 @@
 // read of one tile delayed the other's MMAs.)
 //
 // Weights are relative to m_ref, the maximum of a query's first visible tile,
-// and stay so until a score exceeds it by 2^64: fp32 sums and bf16 weights keep
-// their relative precision at any such scale, so the running maximum is needed
-// only against overflow. A tile's weights therefore do not wait for its
-// maximum; it is found beside the first 64 exponentials, and only if it grew
-// that far are l, O and those weights redone. P is rounded to bf16 for the
-// second product (each weight to nearest, independent from key to key); l sums
-// the unrounded weights.
+// and stay so until a tile's weights sum to more than 2^64: fp32 sums and bf16
+// weights keep their relative precision at any such scale, so the running
+// maximum is needed only against overflow, and an ordinary tile's maximum is
+// never taken. The first tile, masked ones and those that overflow take the
+// slow path: scores, mask, maximum, and l and O brought to the new one. P is
+// rounded to bf16 for the second product (each weight to nearest, independent
+// from key to key); l sums the unrounded weights.
 //
 // Key tiles no query of the item sees are never loaded: the list of the tiles
 // to visit holds each query tile's state (skip, full, masked), nearest keys
@@ -56,7 +55,7 @@ constexpr int kCopyWarp = 8, kMmaWarp = 9, kListWarp = 11;  // MMA warps 9 and 1
 constexpr int kThreads = 384;
 constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
 static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * 168, "registers of the launch");
-constexpr float kGrowth = 64.f;     // rescale when the maximum grew by more (log2)
+constexpr float kGrowth = 64.f;     // log2 of the largest weight sum of a tile before its maximum is taken anew
 constexpr int kListReaders = kSoftmaxWarps + 3;
 
 __device__ __forceinline__ void tmem_ld_x32f(uint32_t taddr, float* r) {
@@ -142,19 +141,13 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
-// tanh(y) = y Q(y^2) for |y| <= 1, |error| <= 2.8e-6 (a minimax fit of degree 4
-// in y^2): 3.5 packed operations per score on the FMA pipe, where
-// 1 - 2 / (1 + e^(2 y)) takes two of the exponential unit's, which has none to
-// spare. Scores rarely pass their cap; a warp that holds one that does takes
-// the exact form for its tile.
-__device__ __forceinline__ f2 tanh2(f2 y) {
-  const f2 z = mul2(y, y);
-  f2 q = fma2(z, pack2(0.008365880697965622f, 0.008365880697965622f), pack2(-0.043299853801727295f, -0.043299853801727295f));
-  q = fma2(z, q, pack2(0.12922066450119019f, 0.12922066450119019f));
-  q = fma2(z, q, pack2(-0.33265823125839233f, -0.33265823125839233f));
-  q = fma2(z, q, pack2(0.9999684691429138f, 0.9999684691429138f));
-  return mul2(y, q);
-}
+// Capped scores: cap tanh(y), y = s / cap, as s Q(s^2) with coefficients for
+// |y| <= 0.8, |error of tanh| <= 6.1e-6 (a minimax fit of degree 3 in y^2):
+// packed operations on the FMA pipe, where 1 - 2 / (1 + e^(2 y)) takes two of
+// the exponential unit's, which has none to spare. Scores rarely come near
+// their cap; a warp that holds one that does takes the exact form for its tile.
+constexpr float kTanhRange = 0.8f;
+constexpr float kTanh[4] = {0.9999305605888367f, -0.3318033516407013f, 0.1240561306476593f, -0.03185783699154854f};
 
 enum : uint32_t { kSkip = 0, kFull = 1, kMasked = 2 };
 
@@ -171,8 +164,7 @@ struct Shape {
   static constexpr int kSlot = (SK > SV ? SK : SV) * kSlab;  // one ring slot: a K or a V tile
   static constexpr int kStages = SK == 2 || SV == 2 ? 4 : 8;
   static constexpr int kQ = 2 * SK * kSlab;
-  static constexpr int kFixed = kQ + kStages * kSlot + kSoftmaxWarps * kTile * 4 /* doc ids */ +
-                                8 * kTile * 4 /* bias by key */ + 1024 /* barriers, item infos */ + 1024 /* alignment */;
+  static constexpr int kFixed = kQ + kStages * kSlot + 8 * kTile * 4 /* bias by key */ + 1024 /* barriers, item infos */ + 1024 /* alignment */;
 };
 
 // Work items of the launch, longest first (under a causal mask the last query
@@ -211,15 +203,14 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem;
   uint8_t* sKV = smem + SH::kQ;
-  int* doc_buf = reinterpret_cast<int*>(sKV + NS * SH::kSlot);                // [8 warps][128]
-  float* bias_buf = reinterpret_cast<float*>(doc_buf + kSoftmaxWarps * kTile);  // [2 lists][2 tiles][2 signs][128]: +-log2(e) slope * key
+  float* bias_buf = reinterpret_cast<float*>(sKV + NS * SH::kSlot);  // [2 lists][2 tiles][2 signs][128]: +-log2(e) slope * key
   uint64_t* q_full = reinterpret_cast<uint64_t*>(bias_buf + 8 * kTile);
   uint64_t* q_empty = q_full + 2;
   uint64_t* kv_full = q_empty + 2;
   uint64_t* kv_empty = kv_full + NS;
   uint64_t* s_full = kv_empty + NS;
-  uint64_t* p_ready = s_full + 2;  // [2 tiles][2 halves of the keys]
-  uint64_t* o_full = p_ready + 4;
+  uint64_t* p_ready = s_full + 2;
+  uint64_t* o_full = p_ready + 2;
   uint64_t* o_free = o_full + 2;
   uint64_t* list_full = o_free + 2;
   uint64_t* list_free = list_full + 2;
@@ -237,8 +228,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
       mbar_init(&q_full[t], 1);
       mbar_init(&q_empty[t], 1);
       mbar_init(&s_full[t], 1);
-      mbar_init(&p_ready[2 * t], 4);
-      mbar_init(&p_ready[2 * t + 1], 4);
+      mbar_init(&p_ready[t], 4);
       mbar_init(&o_full[t], 1);
       mbar_init(&o_free[t], 4);
       mbar_init(&list_full[t], 1);
@@ -315,21 +305,27 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
             if (__any_sync(~0u, pad)) hi_lo[t] = 0;
           }
           const int* doc_k = a.doc_k + static_cast<long long>(it.b) * a.Lk;
-          constexpr int kBatch = 4;  // tiles whose ids are in flight together
+          constexpr int kBatch = 8;  // tiles whose ids are in flight together
+          const bool vec = a.Lk % 4 == 0 && (reinterpret_cast<uintptr_t>(a.doc_k) & 15) == 0;
           const int first = all - 1;  // last tile first
           for (int n0 = 0; n0 < all; n0 += kBatch) {
             int lo[kBatch], hi[kBatch];
 #pragma unroll
-            for (int u = 0; u < kBatch; ++u) {
-              int d[4];
+            for (int u = 0; u < kBatch; ++u) {  // a key past the end counts as padding
+              const int j0 = (first - n0 - u) * kTile;
+              int4 d = make_int4(-1, -1, -1, -1);
+              if (vec && j0 >= 0 && j0 + kTile <= rule.kv) {
+                d = __ldg(reinterpret_cast<const int4*>(doc_k + j0) + lane);
+              } else {
+                int* x = reinterpret_cast<int*>(&d);
 #pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                const int j = (first - n0 - u) * kTile + c * 32 + lane;
-                d[c] = j >= 0 && j < rule.kv ? __ldg(doc_k + j) : -1;
+                for (int c = 0; c < 4; ++c) {
+                  const int j = j0 + c * 32 + lane;
+                  if (j >= 0 && j < rule.kv) x[c] = __ldg(doc_k + j);
+                }
               }
-              // the tile's ids; a key past the end counts as padding
-              lo[u] = min(min(d[0], d[1]), min(d[2], d[3]));
-              hi[u] = max(max(d[0], d[1]), max(d[2], d[3]));
+              lo[u] = min(min(d.x, d.y), min(d.z, d.w));
+              hi[u] = max(max(d.x, d.y), max(d.z, d.w));
             }
 #pragma unroll
             for (int u = 0; u < kBatch; ++u) {
@@ -537,19 +533,15 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
         if (cur.state) {
           if (in_item == 0 && o_items > 0) wait(&o_free[t], o_items - 1);
           const uint32_t fresh = in_item == 0;
+          if (!ok || !wait(&p_ready[t], p_seen)) break;
+          take();
+          tc_fence_after_sync();
+          if (leader) {
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {  // 64 keys' weights each
-            if (!ok || !wait(&p_ready[2 * t + half], p_seen)) break;
-            if (half == 1) take();
-            tc_fence_after_sync();
-            if (leader) {
-#pragma unroll
-              for (int x = 4 * half; x < 4 * half + 4; ++x)
-                mma_bf16_ts(o_tmem, s_tmem + x * 8, kHi | (vl + x * (2048 >> 4)), idesc_o, x > 0 ? 1u : 1u - fresh);
-            }
-            __syncwarp();
+            for (int x = 0; x < kTile / 16; ++x)
+              mma_bf16_ts(o_tmem, s_tmem + x * 8, kHi | (vl + x * (2048 >> 4)), idesc_o, x > 0 ? 1u : 1u - fresh);
           }
-          if (!ok) break;
+          __syncwarp();
           ++p_seen;
           ++in_item;
         }
@@ -578,10 +570,12 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
     const int t = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // this warp's 32 TMEM lanes
     const uint32_t s_col = tmem + lanes + t * kTile, o_col = tmem + lanes + 2 * kTile + t * SV * 64;
-    int* my_docs = doc_buf + warp * kTile;
     const float c_scale = a.scale * kLog2e;
-    const float gain = CAP ? a.softcap * kLog2e : c_scale;  // x = gain * (the score, or its tanh) + bias
-    const float cap_in = CAP ? a.scale / a.softcap : 0.f;
+    const float cap_in = CAP ? a.scale / a.softcap : 0.f, cap_out = a.softcap * kLog2e;  // x = cap_out tanh(cap_in s)
+    // x = s gain, or s Q(s^2) with the cap's scales in Q's coefficients
+    const float gain = c_scale;
+    const float q0 = kTanh[0] * cap_out * cap_in, q1 = kTanh[1] * cap_out * cap_in * cap_in * cap_in;
+    const float q2 = q1 / kTanh[1] * kTanh[2] * cap_in * cap_in, q3 = q1 / kTanh[1] * kTanh[3] * cap_in * cap_in * cap_in * cap_in;
     uint32_t s_seen = 0, o_seen = 0;
     bool ok = true;
     for (int k = 0, item; ok && k < rounds; ++k) {
@@ -593,6 +587,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
       ok = __all_sync(~0u, mbar_wait(&list_full[buf], (k >> 1) & 1u, wd));
       if (!ok) break;
       const ItemInfo inf = info[buf];
+      // a row that sees nothing (hi 0) is dead: whatever it computes is dropped
       const int hi = i < a.Lq && doc >= 0 ? row_end(a, SeqRule{inf.kv, inf.prefix}, i) : 0;
       const int at = i + a.q_offset;
       const uint32_t* list = lists + buf * list_len;
@@ -604,11 +599,13 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
         const uint32_t e = list[n], st = (e >> (2 * t)) & 3u;
         if (st == kSkip) continue;
         const int j0 = static_cast<int>(e >> 4) * kTile;
+        int key_doc[4] = {-1, -1, -1, -1};  // documents of keys lane + 32 x
         if (st == kMasked && a.doc_k) {
-          __syncwarp();
-          for (int c = lane; c < kTile; c += 32)
-            my_docs[c] = j0 + c < inf.kv ? a.doc_k[static_cast<long long>(it.b) * a.Lk + j0 + c] : -1;
-          __syncwarp();
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int j = j0 + lane + 32 * x;
+            if (j < inf.kv) key_doc[x] = a.doc_k[static_cast<long long>(it.b) * a.Lk + j];
+          }
         }
         ok = __all_sync(~0u, mbar_wait(&s_full[t], s_seen & 1u, wd));
         if (!ok) break;
@@ -618,72 +615,17 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
 #pragma unroll
         for (int c = 0; c < kTile; c += 32) tmem_ld_x32f(s_col + c, s + c);
         tmem_wait_ld();
-        if constexpr (CAP) {
-          float big = 0.f;
-#pragma unroll
-          for (int c = 0; c < kTile; c += 2) big = max3(big, fabsf(s[c]), fabsf(s[c + 1]));
-          if (__all_sync(~0u, big * cap_in <= 1.f)) {
-            const f2 in = pack2(cap_in, cap_in);
-#pragma unroll
-            for (int c = 0; c < kTile; c += 2) unpack2(tanh2(mul2(pack2(s[c], s[c + 1]), in)), s[c], s[c + 1]);
-          } else {
-            const float k2 = 2.f * kLog2e * cap_in;
-#pragma unroll
-            for (int c = 0; c < kTile; ++c) s[c] = fmaf(-2.f, rcp_approx(1.f + exp2_approx(s[c] * k2)), 1.f);
-          }
-        }
-        // x = mult * s + shift
-        float mult = gain, shift = 0.f;
-        if constexpr (BIAS) {
-          // -slope |at - j| = +-(slope (key in tile) - slope (at - j0)) where the rows lie on one side of the tile
-          const float f = static_cast<float>(at - j0);
-          const f2 g2 = pack2(gain, gain);
-          const bool after = __all_sync(~0u, at >= j0 + kTile - 1 || i >= a.Lq), before = __all_sync(~0u, at <= j0 || i >= a.Lq);
-          if (after || before) {
-            const float* y_at = by_key + (after ? 0 : kTile);
-#pragma unroll
-            for (int c = 0; c < kTile; c += 4) {
-              const float4 y = *reinterpret_cast<const float4*>(y_at + c);
-              unpack2(fma2(pack2(s[c], s[c + 1]), g2, pack2(y.x, y.y)), s[c], s[c + 1]);
-              unpack2(fma2(pack2(s[c + 2], s[c + 3]), g2, pack2(y.z, y.w)), s[c + 2], s[c + 3]);
-            }
-            shift = after ? -slope * f : slope * f;
-          } else {
-#pragma unroll
-            for (int c = 0; c < kTile; ++c) s[c] = fmaf(-slope, fabsf(f - static_cast<float>(c)), s[c] * gain);
-          }
-          mult = 1.f;
-        }
-        if (st == kMasked) {
-          const int lim = hi - j0;
-          if (a.doc_k) {
-#pragma unroll
-            for (int c = 0; c < kTile; c += 4) {
-              const int4 d = *reinterpret_cast<const int4*>(my_docs + c);
-              s[c] = c < lim && d.x == doc ? s[c] : kNegInf;
-              s[c + 1] = c + 1 < lim && d.y == doc ? s[c + 1] : kNegInf;
-              s[c + 2] = c + 2 < lim && d.z == doc ? s[c + 2] : kNegInf;
-              s[c + 3] = c + 3 < lim && d.w == doc ? s[c + 3] : kNegInf;
-            }
-          } else {
-#pragma unroll
-            for (int c = 0; c < kTile; ++c) s[c] = c < lim ? s[c] : kNegInf;
-          }
-        }
-        const f2 mult2 = pack2(mult, mult);
-        f2 sum[2] = {0, 0};
-        // Weights of keys [c0, c0 + 64) relative to m_ref, into TMEM.
-        auto weights = [&](int c0) {
-          const float mu = (m_ref == kNegInf ? 0.f : m_ref) - shift;
-          const f2 mu2 = pack2(-mu, -mu);
+        f2 sum[2];
+        // Thirty-two weights at a time, two per call of `pair`, into TMEM.
+        auto store_weights = [&](auto pair) {
           sum[0] = sum[1] = 0;
 #pragma unroll
-          for (int c = c0; c < c0 + 64; c += 32) {
+          for (int c = 0; c < kTile; c += 32) {
             uint32_t p[16];
 #pragma unroll
             for (int u = 0; u < 16; ++u) {
               float p0, p1;
-              unpack2(fma2(pack2(s[c + 2 * u], s[c + 2 * u + 1]), mult2, mu2), p0, p1);
+              unpack2(pair(c + 2 * u), p0, p1);
               p0 = exp2_approx(p0);
               p1 = exp2_approx(p1);
               sum[u & 1] = add2(sum[u & 1], pack2(p0, p1));
@@ -693,46 +635,123 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
             tmem_st_x16(s_col + c / 2, p);
           }
         };
-        auto hand_over = [&](int half) {
+        auto total = [&] {
           float s0, s1;
           unpack2(add2(sum[0], sum[1]), s0, s1);
-          l += s0 + s1;
-          tmem_wait_st();
-          tc_fence_before_sync();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&p_ready[2 * t + half]);
+          return s0 + s1;
         };
-        if (any) weights(0);
-        float mx[4] = {s[0], s[1], s[2], s[3]};
+        // ------------------------------------------------ an ordinary tile
+        bool fast = st == kFull && !__any_sync(~0u, hi > 0 && m_ref == kNegInf);
+        float shift = 0.f;
+        const float* table = nullptr;
+        const float f_at = static_cast<float>(at - j0);
+        if constexpr (BIAS) {
+          // -slope |at - j| = +-(slope (key in tile) - slope (at - j0)) where the rows lie on one side of the tile
+          const bool after = __all_sync(~0u, at >= j0 + kTile - 1 || i >= a.Lq), before = __all_sync(~0u, at <= j0 || i >= a.Lq);
+          fast = fast && (after || before);
+          table = by_key + (after ? 0 : kTile);
+          shift = after ? -slope * f_at : slope * f_at;
+        }
+        if constexpr (CAP) {
+          float big[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int c = 4; c + 8 <= kTile; c += 8)
+          for (int c = 0; c < kTile; c += 8)
 #pragma unroll
-          for (int u = 0; u < 4; ++u) mx[u] = max3(mx[u], s[c + 2 * u], s[c + 2 * u + 1]);
-        const float rest = fmaxf(max3(s[kTile - 4], s[kTile - 3], s[kTile - 2]), s[kTile - 1]);
-        const float m_new = fmaf(max3(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]), rest), mult, shift);
-        const bool grow = m_new > m_ref + kGrowth;  // also: the first visible key (m_ref = -inf)
-        if (!any || __any_sync(~0u, grow)) {
-          const float f = grow ? exp2_approx(m_ref - m_new) : 1.f;
-          if (grow) m_ref = m_new;
-          l *= f;
-          if (any) {
-#pragma unroll 1
-            for (int c = 0; c < SV * 64; c += 32) {
-              float o[32];
-              tmem_ld_x32f(o_col + c, o);
-              tmem_wait_ld();
+            for (int u = 0; u < 4; ++u) big[u] = max3(big[u], fabsf(s[c + 2 * u]), fabsf(s[c + 2 * u + 1]));
+          fast = fast && __all_sync(~0u, max3(fmaxf(big[0], big[1]), big[2], big[3]) * cap_in <= kTanhRange);
+        }
+        float tile_sum = 0.f;
+        if (fast) {
+          const float mu = shift - m_ref;
+          const f2 mu2 = pack2(mu, mu);
+          store_weights([&](int c) {
+            const f2 x = pack2(s[c], s[c + 1]);
+            f2 g = pack2(gain, gain);
+            if constexpr (CAP) {
+              const f2 z = mul2(x, x);
+              g = fma2(z, pack2(q3, q3), pack2(q2, q2));
+              g = fma2(z, g, pack2(q1, q1));
+              g = fma2(z, g, pack2(q0, q0));
+            }
+            if constexpr (BIAS) {
+              const float2 y = *reinterpret_cast<const float2*>(table + c);
+              return add2(fma2(x, g, pack2(y.x, y.y)), mu2);
+            } else {
+              return fma2(x, g, mu2);
+            }
+          });
+          tile_sum = total();
+          fast = !__any_sync(~0u, hi > 0 && !(tile_sum <= 0x1p64f));
+        }
+        if (!fast) {
+          // ------------------------- scores, mask, maximum; then the weights
 #pragma unroll
-              for (int u = 0; u < 32; ++u) o[u] *= f;
-              tmem_st_x16(o_col + c, reinterpret_cast<uint32_t*>(o));
-              tmem_st_x16(o_col + c + 16, reinterpret_cast<uint32_t*>(o) + 16);
+          for (int c = 0; c < kTile; ++c) {
+            if constexpr (CAP) s[c] = fmaf(-2.f * cap_out, rcp_approx(1.f + exp2_approx(s[c] * (2.f * kLog2e * cap_in))), cap_out);
+            else s[c] *= gain;
+            if constexpr (BIAS) s[c] = fmaf(-slope, fabsf(f_at - static_cast<float>(c)), s[c]);
+          }
+          if (st == kMasked) {
+            // Bit c of seen: this row sees key c. The documents of a warp's rows are few: one round each.
+            uint32_t seen[4] = {~0u, ~0u, ~0u, ~0u};
+            if (a.doc_k) {
+              unsigned rows = ~0u;
+              while (rows) {
+                const int d = __shfl_sync(~0u, doc, __ffs(rows) - 1);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                  const uint32_t same = __ballot_sync(~0u, key_doc[x] == d);
+                  if (doc == d) seen[x] = same;
+                }
+                rows &= ~__ballot_sync(~0u, doc == d);
+              }
+            }
+            const int lim = hi - j0;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const int n_seen = min(max(lim - 32 * x, 0), 32);
+              seen[x] &= n_seen == 32 ? ~0u : (1u << n_seen) - 1;
+              if (!__all_sync(~0u, seen[x] == ~0u)) {
+#pragma unroll
+                for (int c = 0; c < 32; ++c) s[32 * x + c] = (seen[x] >> c) & 1 ? s[32 * x + c] : kNegInf;
+              }
             }
           }
-          weights(0);
+          float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+          for (int c = 4; c + 8 <= kTile; c += 8)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) mx[u] = max3(mx[u], s[c + 2 * u], s[c + 2 * u + 1]);
+          const float rest = fmaxf(max3(s[kTile - 4], s[kTile - 3], s[kTile - 2]), s[kTile - 1]);
+          const float m_new = max3(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]), rest);
+          const bool grow = hi > 0 && m_new > m_ref + kGrowth;  // also: the first visible key (m_ref = -inf)
+          if (__any_sync(~0u, grow)) {
+            const float f = grow ? exp2_approx(m_ref - m_new) : 1.f;
+            if (grow) m_ref = m_new;
+            l *= f;
+            if (any) {
+#pragma unroll 1
+              for (int c = 0; c < SV * 64; c += 16) {
+                uint32_t o[16];
+                tmem_ld_x16(o_col + c, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int u = 0; u < 16; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * f);
+                tmem_st_x16(o_col + c, o);
+              }
+            }
+          }
+          const float mu = m_ref == kNegInf ? 0.f : -m_ref;
+          const f2 mu2 = pack2(mu, mu);
+          store_weights([&](int c) { return add2(pack2(s[c], s[c + 1]), mu2); });
+          tile_sum = total();
         }
         any = true;
-        hand_over(0);
-        weights(64);
-        hand_over(1);
+        l += tile_sum;
+        tmem_wait_st();
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_ready[t]);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&list_free[buf]);
@@ -744,8 +763,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
         ++o_seen;
         tc_fence_after_sync();
       }
+      const bool live = any && hi > 0;
       const float inv = l == 0.f ? 0.f : 1.f / l;
-      float probe = inv * 0.f;
+      float probe = live ? inv * 0.f : 0.f;
       __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.o) + it.b * a.os_b + static_cast<long long>(i) * a.os_l + h * a.os_h;
 #pragma unroll
       for (int d0 = 0; d0 < SV * 64; d0 += 16) {
@@ -760,8 +780,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
           uint32_t w[4];
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
-            const float y = any ? __uint_as_float(v[u + 2 * x]) * inv : 0.f;
-            const float z = any ? __uint_as_float(v[u + 2 * x + 1]) * inv : 0.f;
+            const float y = live ? __uint_as_float(v[u + 2 * x]) * inv : 0.f;
+            const float z = live ? __uint_as_float(v[u + 2 * x + 1]) * inv : 0.f;
             if (d0 + u < a.dv) probe = fmaf(y, 0.f, fmaf(z, 0.f, probe));
             const __nv_bfloat162 yz = __floats2bfloat162_rn(y, z);
             w[x] = *reinterpret_cast<const uint32_t*>(&yz);

@@ -51,9 +51,9 @@ constexpr int kSoftmaxWarps = 8;    // two warpgroups, one per tile
 constexpr int kCopyWarp = 8, kMmaWarp = 9, kListWarp = 11;  // MMA warps 9 and 10: tiles 0 and 1
 // At launch every thread holds 168 registers (the most for 12 warps); the last
 // warpgroup hands some of its own to the softmax threads, which keep 128
-// scores each: 256 * 216 + 128 * 72 = 384 * 168.
+// scores each: 256 * 224 + 128 * 56 = 384 * 168.
 constexpr int kThreads = 384;
-constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
+constexpr int kSoftmaxRegs = 224, kOtherRegs = 56;
 static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * 168, "registers of the launch");
 constexpr float kGrowth = 64.f;     // log2 of the largest weight sum of a tile before its maximum is taken anew
 constexpr int kListReaders = kSoftmaxWarps + 3;
@@ -75,8 +75,15 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t* r) {
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// These are .sync.aligned: the warp is converged explicitly before each group of
+// them (a lane back from a branch of its own is not otherwise sure to have rejoined).
+__device__ __forceinline__ void tmem_wait_ld() {
+  __syncwarp();
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // D[tmem] (+)= A[tmem] * B[smem], kind::f16 with bf16 operands: A row i in
@@ -157,14 +164,49 @@ struct ItemInfo {
   int kv;      // keys of the sequence
   int prefix;
   int tail;    // 1: the tile of key kv, if listed, holds rows past it, whose values must become zero
+  float slope[2];  // log2(e) times the slopes of the two tiles' heads
 };
+
+// Least and greatest document of key tiles [n0, n0 + count) of sequence b, into
+// cache[0 .. count), by `warps` warps.  A key past the end counts as padding.
+constexpr int kDocTiles = 512;  // tiles whose ranges are kept: 65536 keys
+__device__ __forceinline__ void scan_docs(const AttnArgs& a, int b, int kv, int2* cache, int n0, int count, int warp, int warps) {
+  constexpr int kBatch = 4;  // tiles whose ids are in flight together
+  const int lane = threadIdx.x & 31;
+  const int* doc_k = a.doc_k + static_cast<long long>(b) * a.Lk;
+  const bool vec = a.Lk % 4 == 0 && (reinterpret_cast<uintptr_t>(a.doc_k) & 15) == 0;
+  for (int x0 = warp * kBatch; x0 < count; x0 += warps * kBatch) {
+    int lo[kBatch], hi[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int j0 = (n0 + x0 + u) * kTile;
+      int4 d = make_int4(-1, -1, -1, -1);
+      if (vec && j0 + kTile <= kv) {
+        d = __ldg(reinterpret_cast<const int4*>(doc_k + j0) + lane);
+      } else {
+        if (j0 + lane < kv) d.x = __ldg(doc_k + j0 + lane);
+        if (j0 + lane + 32 < kv) d.y = __ldg(doc_k + j0 + lane + 32);
+        if (j0 + lane + 64 < kv) d.z = __ldg(doc_k + j0 + lane + 64);
+        if (j0 + lane + 96 < kv) d.w = __ldg(doc_k + j0 + lane + 96);
+      }
+      lo[u] = min(min(d.x, d.y), min(d.z, d.w));
+      hi[u] = max(max(d.x, d.y), max(d.z, d.w));
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int2 r = make_int2(__reduce_min_sync(~0u, lo[u]), __reduce_max_sync(~0u, hi[u]));
+      if (lane == u && x0 + u < count) cache[x0 + u] = r;
+    }
+  }
+  __syncwarp();
+}
 
 template <int SK, int SV>
 struct Shape {
   static constexpr int kSlot = (SK > SV ? SK : SV) * kSlab;  // one ring slot: a K or a V tile
   static constexpr int kStages = SK == 2 || SV == 2 ? 4 : 8;
   static constexpr int kQ = 2 * SK * kSlab;
-  static constexpr int kFixed = kQ + kStages * kSlot + 8 * kTile * 4 /* bias by key */ + 1024 /* barriers, item infos */ + 1024 /* alignment */;
+  static constexpr int kFixed = kQ + kStages * kSlot + 4 * kTile * 4 /* queries' documents */ + 1024 /* barriers, item infos */ + 1024 /* alignment */;
 };
 
 // Work items of the launch, longest first (under a causal mask the last query
@@ -203,8 +245,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem;
   uint8_t* sKV = smem + SH::kQ;
-  float* bias_buf = reinterpret_cast<float*>(sKV + NS * SH::kSlot);  // [2 lists][2 tiles][2 signs][128]: +-log2(e) slope * key
-  uint64_t* q_full = reinterpret_cast<uint64_t*>(bias_buf + 8 * kTile);
+  int* q_docs = reinterpret_cast<int*>(sKV + NS * SH::kSlot);  // [2 lists][2 tiles][128]: documents of the queries
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(q_docs + 4 * kTile);
   uint64_t* q_empty = q_full + 2;
   uint64_t* kv_full = q_empty + 2;
   uint64_t* kv_empty = kv_full + NS;
@@ -221,6 +263,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(info + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   uint32_t* lists = reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(q_full) + 1024);  // [2][list_len]
+  int2* doc_cache = reinterpret_cast<int2*>(lists + 2 * ((list_len + 1) & ~1));            // [2][kDocTiles] with documents
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -256,12 +299,24 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
   const uint32_t tmem = *tmem_slot;
   const Watchdog wd{a.err, abort_flag, a.timeout_ns};
   const int rounds = (items + gridDim.x - 1) / gridDim.x;
+  // The first two items' document ranges by every warp: nothing hides their latency yet.
+  const int key_tiles = (a.Lk + kTile - 1) / kTile;
+  if (a.doc_k && key_tiles <= kDocTiles) {
+    for (int k = 0; k < 2; ++k)
+      if (k < rounds && item_of(k) < items) {
+        const int b = item_at(a, pairs, item_of(k)).b;
+        scan_docs(a, b, seq_rule(a, b).kv, doc_cache + k * kDocTiles, 0, key_tiles, warp, kThreads / 32);
+      }
+    __syncthreads();
+  }
 
   if (warp >= kSoftmaxWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kListWarp) {
       // ------------------------------------------------------------ lists
       bool ok = true;
+      int cached0 = rounds > 0 && item_of(0) < items ? item_at(a, pairs, item_of(0)).b : -1;  // whose ranges the caches hold
+      int cached1 = rounds > 1 && item_of(1) < items ? item_at(a, pairs, item_of(1)).b : -1;
       for (int k = 0, item; ok && k < rounds; ++k) {
         if ((item = item_of(k)) >= items) break;
         const int buf = k & 1;
@@ -297,6 +352,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
             for (int c = lane; c < kTile; c += 32) {
               const int i = it.i0[t] + c;
               const int d = i < a.Lq ? a.doc_q[static_cast<long long>(it.b) * a.Lq + i] : -1;
+              q_docs[(buf * 2 + t) * kTile + c] = d;
               if (d >= 0) lo = min(lo, d), hi = max(hi, d);
               pad |= i < a.Lq && d < 0;
             }
@@ -304,60 +360,35 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
             dhi[t] = __reduce_max_sync(~0u, hi);
             if (__any_sync(~0u, pad)) hi_lo[t] = 0;
           }
-          const int* doc_k = a.doc_k + static_cast<long long>(it.b) * a.Lk;
-          constexpr int kBatch = 8;  // tiles whose ids are in flight together
-          const bool vec = a.Lk % 4 == 0 && (reinterpret_cast<uintptr_t>(a.doc_k) & 15) == 0;
-          const int first = all - 1;  // last tile first
-          for (int n0 = 0; n0 < all; n0 += kBatch) {
-            int lo[kBatch], hi[kBatch];
+          // from the last tile down; ranges of up to kDocTiles tiles at a time
+          for (int end = all; end > 0; end -= kDocTiles) {
+            const int n0 = key_tiles <= kDocTiles ? 0 : max(0, end - kDocTiles);
+            int2* cache = doc_cache + buf * kDocTiles;
+            if (key_tiles > kDocTiles) scan_docs(a, it.b, rule.kv, cache, n0, end - n0, 0, 1);
+            else if (k >= 2 && it.b != (buf ? cached1 : cached0)) scan_docs(a, it.b, rule.kv, cache, 0, key_tiles, 0, 1);
+            for (int x0 = end - 1; x0 >= n0; x0 -= 32) {
+              const int n = x0 - lane;
+              uint32_t e = 0;
+              if (n >= n0) {
+                const int l = cache[n - n0].x, h = cache[n - n0].y;
 #pragma unroll
-            for (int u = 0; u < kBatch; ++u) {  // a key past the end counts as padding
-              const int j0 = (first - n0 - u) * kTile;
-              int4 d = make_int4(-1, -1, -1, -1);
-              if (vec && j0 >= 0 && j0 + kTile <= rule.kv) {
-                d = __ldg(reinterpret_cast<const int4*>(doc_k + j0) + lane);
-              } else {
-                int* x = reinterpret_cast<int*>(&d);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                  const int j = j0 + c * 32 + lane;
-                  if (j >= 0 && j < rule.kv) x[c] = __ldg(doc_k + j);
+                for (int t = 0; t < 2; ++t) {
+                  uint32_t st = n * kTile >= hi_hi[t] || h < dlo[t] || l > dhi[t] ? kSkip : kMasked;
+                  if (st == kMasked && l == h && dlo[t] == dhi[t] && l == dlo[t] && (n + 1) * kTile <= hi_lo[t]) st = kFull;
+                  e |= st << (2 * t);
                 }
               }
-              lo[u] = min(min(d.x, d.y), min(d.z, d.w));
-              hi[u] = max(max(d.x, d.y), max(d.z, d.w));
-            }
-#pragma unroll
-            for (int u = 0; u < kBatch; ++u) {
-              const int n = first - n0 - u;
-              const int l = __reduce_min_sync(~0u, lo[u]), h = __reduce_max_sync(~0u, hi[u]);
-              uint32_t e = 0;
-              for (int t = 0; t < 2; ++t) {
-                uint32_t st = n * kTile >= hi_hi[t] || h < dlo[t] || l > dhi[t] ? kSkip : kMasked;
-                if (st == kMasked && l == h && dlo[t] == dhi[t] && l == dlo[t] && (n + 1) * kTile <= hi_lo[t]) st = kFull;
-                e |= st << (2 * t);
-              }
-              if (e && n >= 0) {
-                if (lane == 0) list[kept] = e | (n << 4);
-                ++kept;
-              }
+              const unsigned keep = __ballot_sync(~0u, e != 0);
+              if (e) list[kept + __popc(keep & ((1u << lane) - 1))] = e | (n << 4);
+              kept += __popc(keep);
             }
           }
-        }
-        if (a.slopes) {
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            const float slope = a.slopes[it.h[t]] * kLog2e;
-            float* y = bias_buf + (buf * 2 + t) * 2 * kTile;
-            for (int c = lane; c < kTile; c += 32) {
-              y[c] = slope * static_cast<float>(c);
-              y[kTile + c] = -slope * static_cast<float>(c);
-            }
-          }
+          (buf ? cached1 : cached0) = it.b;
         }
         __syncwarp();
         if (lane == 0) {
-          info[buf] = {kept, rule.kv, rule.prefix, rule.kv < a.Lk && rule.kv % kTile != 0};
+          info[buf] = {kept, rule.kv, rule.prefix, rule.kv < a.Lk && rule.kv % kTile != 0,
+                       {a.slopes ? a.slopes[it.h[0]] * kLog2e : 0.f, a.slopes ? a.slopes[it.h[1]] * kLog2e : 0.f}};
           mbar_arrive(&list_full[buf]);
         }
       }
@@ -583,16 +614,15 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
       const int buf = k & 1;
       const Item it = item_at(a, pairs, item);
       const int i = it.i0[t] + row, h = it.h[t];
-      const int doc = a.doc_q && i < a.Lq ? a.doc_q[static_cast<long long>(it.b) * a.Lq + i] : 0;
       ok = __all_sync(~0u, mbar_wait(&list_full[buf], (k >> 1) & 1u, wd));
       if (!ok) break;
       const ItemInfo inf = info[buf];
+      const int doc = a.doc_q ? q_docs[(buf * 2 + t) * kTile + row] : 0;
       // a row that sees nothing (hi 0) is dead: whatever it computes is dropped
       const int hi = i < a.Lq && doc >= 0 ? row_end(a, SeqRule{inf.kv, inf.prefix}, i) : 0;
       const int at = i + a.q_offset;
       const uint32_t* list = lists + buf * list_len;
-      const float* by_key = bias_buf + (buf * 2 + t) * 2 * kTile;
-      const float slope = BIAS ? by_key[1] : 0.f;
+      const float slope = t ? inf.slope[1] : inf.slope[0];
       float m_ref = kNegInf, l = 0.f;
       bool any = false;
       for (int n = 0; n < inf.n; ++n) {
@@ -612,6 +642,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
         ++s_seen;
         tc_fence_after_sync();
         float s[kTile];
+        __syncwarp();
 #pragma unroll
         for (int c = 0; c < kTile; c += 32) tmem_ld_x32f(s_col + c, s + c);
         tmem_wait_ld();
@@ -619,6 +650,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
         // Thirty-two weights at a time, two per call of `pair`, into TMEM.
         auto store_weights = [&](auto pair) {
           sum[0] = sum[1] = 0;
+          __syncwarp();
 #pragma unroll
           for (int c = 0; c < kTile; c += 32) {
             uint32_t p[16];
@@ -642,40 +674,49 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
         };
         // ------------------------------------------------ an ordinary tile
         bool fast = st == kFull && !__any_sync(~0u, hi > 0 && m_ref == kNegInf);
-        float shift = 0.f;
-        const float* table = nullptr;
+        // -slope |at - j| = +-slope (j - at) where a row's visible keys lie on one side of it: side * slope * (j - at)
         const float f_at = static_cast<float>(at - j0);
+        float side = 0.f;
         if constexpr (BIAS) {
-          // -slope |at - j| = +-(slope (key in tile) - slope (at - j0)) where the rows lie on one side of the tile
-          const bool after = __all_sync(~0u, at >= j0 + kTile - 1 || i >= a.Lq), before = __all_sync(~0u, at <= j0 || i >= a.Lq);
-          fast = fast && (after || before);
-          table = by_key + (after ? 0 : kTile);
-          shift = after ? -slope * f_at : slope * f_at;
+          if (__all_sync(~0u, min(hi, j0 + kTile) - 1 <= at || hi == 0)) side = slope;
+          else if (__all_sync(~0u, at <= j0 || hi == 0)) side = -slope;
+          fast = fast && side != 0.f;
         }
+        // The bias of keys c, c + 1 plus `more`, for c a multiple of 32; each next pair of keys adds 2 * side.
+        auto bias_at = [&](int c, float more) {
+          const float y = fmaf(side, static_cast<float>(c) - f_at, more);
+          return pack2(y, y + side);
+        };
+        const f2 bias_step = pack2(2.f * side, 2.f * side);
+        bool in_range = true;
         if constexpr (CAP) {
           float big[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int c = 0; c < kTile; c += 8)
 #pragma unroll
             for (int u = 0; u < 4; ++u) big[u] = max3(big[u], fabsf(s[c + 2 * u]), fabsf(s[c + 2 * u + 1]));
-          fast = fast && __all_sync(~0u, max3(fmaxf(big[0], big[1]), big[2], big[3]) * cap_in <= kTanhRange);
+          in_range = __all_sync(~0u, max3(fmaxf(big[0], big[1]), big[2], big[3]) * cap_in <= kTanhRange);
+          fast = fast && in_range;
         }
+        auto cap_gain = [&](f2 x) {  // Q(x^2) with the cap's scales: x times it is log2(e) cap tanh(x / cap)
+          const f2 z = mul2(x, x);
+          f2 g = fma2(z, pack2(q3, q3), pack2(q2, q2));
+          g = fma2(z, g, pack2(q1, q1));
+          return fma2(z, g, pack2(q0, q0));
+        };
         float tile_sum = 0.f;
+        f2 y2 = 0;
         if (fast) {
-          const float mu = shift - m_ref;
+          const float mu = -m_ref;
           const f2 mu2 = pack2(mu, mu);
           store_weights([&](int c) {
             const f2 x = pack2(s[c], s[c + 1]);
-            f2 g = pack2(gain, gain);
-            if constexpr (CAP) {
-              const f2 z = mul2(x, x);
-              g = fma2(z, pack2(q3, q3), pack2(q2, q2));
-              g = fma2(z, g, pack2(q1, q1));
-              g = fma2(z, g, pack2(q0, q0));
-            }
+            f2 g;
+            if constexpr (CAP) g = cap_gain(x);
+            else g = pack2(gain, gain);
             if constexpr (BIAS) {
-              const float2 y = *reinterpret_cast<const float2*>(table + c);
-              return add2(fma2(x, g, pack2(y.x, y.y)), mu2);
+              y2 = c % 32 == 0 ? bias_at(c, mu) : add2(y2, bias_step);
+              return fma2(x, g, y2);
             } else {
               return fma2(x, g, mu2);
             }
@@ -684,12 +725,37 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
           fast = !__any_sync(~0u, hi > 0 && !(tile_sum <= 0x1p64f));
         }
         if (!fast) {
+          tmem_wait_st();  // weights of an attempt that overflowed
           // ------------------------- scores, mask, maximum; then the weights
+          // x = mult * s from here on
+          float mult = gain;
+          if constexpr (CAP) {
+            if (in_range) {
 #pragma unroll
-          for (int c = 0; c < kTile; ++c) {
-            if constexpr (CAP) s[c] = fmaf(-2.f * cap_out, rcp_approx(1.f + exp2_approx(s[c] * (2.f * kLog2e * cap_in))), cap_out);
-            else s[c] *= gain;
-            if constexpr (BIAS) s[c] = fmaf(-slope, fabsf(f_at - static_cast<float>(c)), s[c]);
+              for (int c = 0; c < kTile; c += 2) {
+                const f2 x = pack2(s[c], s[c + 1]);
+                unpack2(mul2(x, cap_gain(x)), s[c], s[c + 1]);
+              }
+            } else {
+#pragma unroll
+              for (int c = 0; c < kTile; ++c)
+                s[c] = fmaf(-2.f * cap_out, rcp_approx(1.f + exp2_approx(s[c] * (2.f * kLog2e * cap_in))), cap_out);
+            }
+            mult = 1.f;
+          }
+          if constexpr (BIAS) {
+            if (side != 0.f) {
+              const f2 g2 = pack2(mult, mult);
+#pragma unroll
+              for (int c = 0; c < kTile; c += 2) {
+                y2 = c % 32 == 0 ? bias_at(c, 0.f) : add2(y2, bias_step);
+                unpack2(fma2(pack2(s[c], s[c + 1]), g2, y2), s[c], s[c + 1]);
+              }
+            } else {
+#pragma unroll
+              for (int c = 0; c < kTile; ++c) s[c] = fmaf(-slope, fabsf(f_at - static_cast<float>(c)), s[c] * mult);
+            }
+            mult = 1.f;
           }
           if (st == kMasked) {
             // Bit c of seen: this row sees key c. The documents of a warp's rows are few: one round each.
@@ -723,7 +789,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
 #pragma unroll
             for (int u = 0; u < 4; ++u) mx[u] = max3(mx[u], s[c + 2 * u], s[c + 2 * u + 1]);
           const float rest = fmaxf(max3(s[kTile - 4], s[kTile - 3], s[kTile - 2]), s[kTile - 1]);
-          const float m_new = max3(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]), rest);
+          const float m_new = max3(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]), rest) * mult;
           const bool grow = hi > 0 && m_new > m_ref + kGrowth;  // also: the first visible key (m_ref = -inf)
           if (__any_sync(~0u, grow)) {
             const float f = grow ? exp2_approx(m_ref - m_new) : 1.f;
@@ -737,13 +803,14 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                 tmem_wait_ld();
 #pragma unroll
                 for (int u = 0; u < 16; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * f);
+                __syncwarp();
                 tmem_st_x16(o_col + c, o);
               }
             }
           }
           const float mu = m_ref == kNegInf ? 0.f : -m_ref;
-          const f2 mu2 = pack2(mu, mu);
-          store_weights([&](int c) { return add2(pack2(s[c], s[c + 1]), mu2); });
+          const f2 mu2 = pack2(mu, mu), mult2 = pack2(mult, mult);
+          store_weights([&](int c) { return fma2(pack2(s[c], s[c + 1]), mult2, mu2); });
           tile_sum = total();
         }
         any = true;
@@ -815,7 +882,8 @@ size_t list_len(int Lk) { return static_cast<size_t>(Lk + kTile - 1) / kTile; }
 
 template <int SK, int SV, bool CAP, bool BIAS>
 cudaError_t launch_one(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const AttnArgs& a, int sms, cudaStream_t s) {
-  const size_t smem = Shape<SK, SV>::kFixed + 2 * list_len(a.Lk) * sizeof(uint32_t);
+  const size_t smem = Shape<SK, SV>::kFixed + 2 * ((list_len(a.Lk) + 1) & ~size_t(1)) * sizeof(uint32_t) +
+                      (a.doc_k ? 2 * kDocTiles * sizeof(int2) : 0);
   const cudaError_t e = smem_attr_once<attn_tc_kernel<SK, SV, CAP, BIAS>>(smem);
   if (e != cudaSuccess) return e;
   const long long tiles = static_cast<long long>((a.Lq + kTile - 1) / kTile) * a.group, pairs = (tiles + 1) / 2;

@@ -170,6 +170,19 @@ def test_graph_capture(gpu):
     ref.check(out, ref.attention(q, k, v, **kw), v, BF16)
 
 
+@pytest.mark.parametrize("name", RULES)
+def test_more_items_than_sms(gpu, name):
+    """Several rounds of work per CTA: lists, rings and accumulators pass from item to item."""
+    shape = (41, 300, 300, 6, 3, 64, 64)
+    q, k, v = make(shape, BF16, seed=12)
+    kw = rule(name, shape)
+    out = run(q, k, v, kw)
+    sync_check()
+    pick = [0, 1, 17, 40]
+    part = {n: (t[pick] if n in ("prefix_len", "kv_len", "doc_q", "doc_k") else t) for n, t in kw.items()}
+    ref.check(out[pick], ref.attention(q[pick], k[pick], v[pick], **part), v, BF16)
+
+
 def test_empty_batch_and_rows(gpu):
     for shape in ((0, 4, 4, 2, 2, 64, 64), (2, 0, 4, 2, 2, 64, 64)):
         q, k, v = make(shape, BF16)

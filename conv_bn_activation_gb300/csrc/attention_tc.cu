@@ -86,6 +86,12 @@ __device__ __forceinline__ void tmem_wait_st() {
 }
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
+__device__ __forceinline__ void st_global_x8(void* p, const uint32_t* r) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]),
+               "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
 // D[tmem] (+)= A[tmem] * B[smem], kind::f16 with bf16 operands: A row i in
 // lane i, two K elements per column.
 __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
@@ -158,8 +164,13 @@ constexpr float kTanh[4] = {0.9999305605888367f, -0.3318033516407013f, 0.1240561
 
 enum : uint32_t { kSkip = 0, kFull = 1, kMasked = 2 };
 
+struct Item {
+  int b, hk;
+  int h[2], i0[2];  // per tile; a tile past the last one starts at Lq: it has no query
+};
 // What the scheduler warp says about an item.
 struct ItemInfo {
+  Item it;     // worked out once: the divisions took a softmax thread about 1000 cycles per item
   int n;       // tiles in the list
   int kv;      // keys of the sequence
   int prefix;
@@ -215,10 +226,6 @@ struct Shape {
 __device__ __forceinline__ int item_of(int k) {
   return k * gridDim.x + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
 }
-struct Item {
-  int b, hk;
-  int h[2], i0[2];  // per tile; a tile past the last one starts at Lq: it has no query
-};
 __device__ __forceinline__ Item item_at(const AttnArgs& a, int pairs, int item) {
   const int seqs = a.B * (a.Hq / a.group), bh = item % seqs, u = 2 * (pairs - 1 - item / seqs);
   Item it;
@@ -387,7 +394,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
         }
         __syncwarp();
         if (lane == 0) {
-          info[buf] = {kept, rule.kv, rule.prefix, rule.kv < a.Lk && rule.kv % kTile != 0,
+          info[buf] = {it, kept, rule.kv, rule.prefix, rule.kv < a.Lk && rule.kv % kTile != 0,
                        {a.slopes ? a.slopes[it.h[0]] * kLog2e : 0.f, a.slopes ? a.slopes[it.h[1]] * kLog2e : 0.f}};
           mbar_arrive(&list_full[buf]);
         }
@@ -405,14 +412,14 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
       bool ok = true;
       uint32_t use = 0;  // fills of this lane's slot or Q tile so far
       long long base = 0;
-      for (int k = 0, item; ok && k < rounds; ++k) {
-        if ((item = item_of(k)) >= items) break;
+      for (int k = 0; ok && k < rounds; ++k) {
+        if (item_of(k) >= items) break;
         const int buf = k & 1;
         ok = mbar_wait(&list_full[buf], (k >> 1) & 1u, wd);
         ok = __all_sync(~0u, ok);
         if (!ok) break;
         const int n = info[buf].n;
-        const Item it = item_at(a, pairs, item);
+        const Item it = info[buf].it;
         const uint32_t* list = lists + buf * list_len;
         if (n > 0 && lane >= NS && lane < NS + 2) {
           const int t = lane - NS;
@@ -607,16 +614,18 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
     const float gain = c_scale;
     const float q0 = kTanh[0] * cap_out * cap_in, q1 = kTanh[1] * cap_out * cap_in * cap_in * cap_in;
     const float q2 = q1 / kTanh[1] * kTanh[2] * cap_in * cap_in, q3 = q1 / kTanh[1] * kTanh[3] * cap_in * cap_in * cap_in * cap_in;
+    // 32-byte stores of the output, where its rows allow them: a store instruction touches 32 rows, and costs
+    // by the row
+    const bool wide = ((reinterpret_cast<uintptr_t>(a.o) | (a.os_b * 2) | (a.os_l * 2) | (a.os_h * 2)) & 31) == 0 && a.dv % 16 == 0;
     uint32_t s_seen = 0, o_seen = 0;
     bool ok = true;
-    for (int k = 0, item; ok && k < rounds; ++k) {
-        if ((item = item_of(k)) >= items) break;
+    for (int k = 0; ok && k < rounds; ++k) {
+      if (item_of(k) >= items) break;
       const int buf = k & 1;
-      const Item it = item_at(a, pairs, item);
-      const int i = it.i0[t] + row, h = it.h[t];
       ok = __all_sync(~0u, mbar_wait(&list_full[buf], (k >> 1) & 1u, wd));
       if (!ok) break;
       const ItemInfo inf = info[buf];
+      const int b = inf.it.b, i0 = t ? inf.it.i0[1] : inf.it.i0[0], h = t ? inf.it.h[1] : inf.it.h[0], i = i0 + row;
       const int doc = a.doc_q ? q_docs[(buf * 2 + t) * kTile + row] : 0;
       // a row that sees nothing (hi 0) is dead: whatever it computes is dropped
       const int hi = i < a.Lq && doc >= 0 ? row_end(a, SeqRule{inf.kv, inf.prefix}, i) : 0;
@@ -629,12 +638,33 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
         const uint32_t e = list[n], st = (e >> (2 * t)) & 3u;
         if (st == kSkip) continue;
         const int j0 = static_cast<int>(e >> 4) * kTile;
-        int key_doc[4] = {-1, -1, -1, -1};  // documents of keys lane + 32 x
-        if (st == kMasked && a.doc_k) {
+        // Bit c of seen: this row sees key j0 + c. Found before the scores are waited for.
+        uint32_t seen[4] = {~0u, ~0u, ~0u, ~0u};
+        if (st == kMasked) {
+          if (a.doc_k) {
+            int key_doc[4];  // documents of keys lane + 32 x
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const int j = j0 + lane + 32 * x;
+              key_doc[x] = j < inf.kv ? a.doc_k[static_cast<long long>(b) * a.Lk + j] : -1;
+            }
+            // The documents of a warp's rows are few: one round each.
+            unsigned rows = ~0u;
+            while (rows) {
+              const int d = __shfl_sync(~0u, doc, __ffs(rows) - 1);
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                const uint32_t same = __ballot_sync(~0u, key_doc[x] == d);
+                if (doc == d) seen[x] = same;
+              }
+              rows &= ~__ballot_sync(~0u, doc == d);
+            }
+          }
+          const int lim = hi - j0;
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
-            const int j = j0 + lane + 32 * x;
-            if (j < inf.kv) key_doc[x] = a.doc_k[static_cast<long long>(it.b) * a.Lk + j];
+            const int n_seen = min(max(lim - 32 * x, 0), 32);
+            seen[x] &= n_seen == 32 ? ~0u : (1u << n_seen) - 1;
           }
         }
         ok = __all_sync(~0u, mbar_wait(&s_full[t], s_seen & 1u, wd));
@@ -758,25 +788,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
             mult = 1.f;
           }
           if (st == kMasked) {
-            // Bit c of seen: this row sees key c. The documents of a warp's rows are few: one round each.
-            uint32_t seen[4] = {~0u, ~0u, ~0u, ~0u};
-            if (a.doc_k) {
-              unsigned rows = ~0u;
-              while (rows) {
-                const int d = __shfl_sync(~0u, doc, __ffs(rows) - 1);
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                  const uint32_t same = __ballot_sync(~0u, key_doc[x] == d);
-                  if (doc == d) seen[x] = same;
-                }
-                rows &= ~__ballot_sync(~0u, doc == d);
-              }
-            }
-            const int lim = hi - j0;
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-              const int n_seen = min(max(lim - 32 * x, 0), 32);
-              seen[x] &= n_seen == 32 ? ~0u : (1u << n_seen) - 1;
               if (!__all_sync(~0u, seen[x] == ~0u)) {
 #pragma unroll
                 for (int c = 0; c < 32; ++c) s[32 * x + c] = (seen[x] >> c) & 1 ? s[32 * x + c] : kNegInf;
@@ -832,41 +845,49 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
       }
       const bool live = any && hi > 0;
       const float inv = l == 0.f ? 0.f : 1.f / l;
-      float probe = live ? inv * 0.f : 0.f;
-      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.o) + it.b * a.os_b + static_cast<long long>(i) * a.os_l + h * a.os_h;
+      const f2 inv2 = pack2(inv, inv);
+      f2 probe[2] = {mul2(inv2, 0), 0};  // 0 times every value: NaN where one is not finite
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.o) + b * a.os_b + static_cast<long long>(i) * a.os_l + h * a.os_h;
 #pragma unroll
       for (int d0 = 0; d0 < SV * 64; d0 += 16) {
         if (d0 >= a.dv) break;
-        uint32_t v[16];
+        uint32_t v[16], w[8];
         if (any) {
           tmem_ld_x16(o_col + d0, v);
           tmem_wait_ld();
         }
+        const bool second = d0 + 8 < a.dv;  // dims come in eights
 #pragma unroll
-        for (int u = 0; u < 16; u += 8) {
-          uint32_t w[4];
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const float y = live ? __uint_as_float(v[u + 2 * x]) * inv : 0.f;
-            const float z = live ? __uint_as_float(v[u + 2 * x + 1]) * inv : 0.f;
-            if (d0 + u < a.dv) probe = fmaf(y, 0.f, fmaf(z, 0.f, probe));
-            const __nv_bfloat162 yz = __floats2bfloat162_rn(y, z);
-            w[x] = *reinterpret_cast<const uint32_t*>(&yz);
+        for (int u = 0; u < 8; ++u) {
+          const f2 y = mul2(pack2(__uint_as_float(v[2 * u]), __uint_as_float(v[2 * u + 1])), inv2);
+          if (u < 4 || second) probe[u & 1] = fma2(y, 0, probe[u & 1]);
+          float y0, y1;
+          unpack2(y, y0, y1);
+          const __nv_bfloat162 yz = __floats2bfloat162_rn(y0, y1);
+          w[u] = live ? *reinterpret_cast<const uint32_t*>(&yz) : 0u;
+        }
+        if (i < a.Lq) {
+          if (wide) {
+            st_global_x8(out + d0, w);
+          } else {
+            *reinterpret_cast<uint4*>(out + d0) = make_uint4(w[0], w[1], w[2], w[3]);
+            if (second) *reinterpret_cast<uint4*>(out + d0 + 8) = make_uint4(w[4], w[5], w[6], w[7]);
           }
-          if (i < a.Lq && d0 + u < a.dv) *reinterpret_cast<uint4*>(out + d0 + u) = make_uint4(w[0], w[1], w[2], w[3]);
         }
       }
+      float probe0, probe1;
+      unpack2(add2(probe[0], probe[1]), probe0, probe1);
       if (any) {
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&o_free[t]);
       }
       // Rows that met a non-finite value: again, key by key (attn_row).
-      unsigned bad = __ballot_sync(~0u, i < a.Lq && !(probe == 0.f));
+      unsigned bad = __ballot_sync(~0u, i < a.Lq && live && !(probe0 + probe1 == 0.f));
       while (bad) {
         const int r = __ffs(bad) - 1;
         bad &= bad - 1;
-        attn_row_inline<__nv_bfloat16>(a, it.b, h, it.i0[t] + (warp & 3) * 32 + r);
+        attn_row_inline<__nv_bfloat16>(a, b, h, i0 + (warp & 3) * 32 + r);
       }
     }
     tc_fence_before_sync();

@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(kThreads) decode_simt_kernel(DecodeArgs a) {
       if (tid < heads) part[tid] = ms[tid], part[a.item_heads + tid] = ls[tid];
       if (pc.starts && tid == 0) note_item(a, run, pc, per_seq, cta);
     }
-    at += pc.tiles;
+    at += pc.dealt;
   }
 }
 

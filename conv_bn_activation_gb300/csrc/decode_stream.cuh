@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas_per_sm(C::DK, C::D
       return;
     }
     if (!out && pc.starts && tid == 0) note_item(a, run, pc, per_seq, cta);
-    at += pc.tiles;
+    at += pc.dealt;
     __syncthreads();
     if (at < end && padded) {
       clear();

@@ -370,6 +370,7 @@ struct DecodeArgs {
   int B, Hq, Hkv, group, dk, dv;
   int chunks;           // items per key head
   int item_heads;       // query heads of one item: ceil(group / chunks)
+  int item_cost;        // tiles that an item's start counts for when runs are cut
   int split;            // CTAs of a cluster per item (1 to 8), or 0: runs of tiles over one wave of CTAs
   float* part;          // workspace: partial results, two per CTA
   int* record;          // workspace: per CTA {item, pieces} of the item it starts and does not finish
@@ -379,6 +380,9 @@ struct DecodeArgs {
 constexpr int kDecodeSimtHeads = 8, kDecodeMmaHeads = 16;  // most query heads of one item
 // CTAs per SM of the streaming kernels: their rings take 48, 72 or 96 KB.
 constexpr int decode_ctas_per_sm(int dk, int dv) { return dk <= 64 && dv <= 64 ? 4 : dk <= 64 || dv <= 64 ? 3 : 2; }
+// What an item's start costs a CTA, in tiles of 64 tokens (decode_common.cuh). A tile of
+// fp32 takes a CTA twice as long as one of bf16, whatever the dims: fewer dims, more CTAs per SM.
+constexpr int decode_item_cost(bool bf16) { return bf16 ? 3 : 1; }
 // Workspace: `ctas` records of two ints, then 2 * ctas partials of `heads` x (dv + 2) floats.
 size_t decode_workspace_bytes(int ctas, int heads, int dv);
 cudaError_t launch_decode_mma(const DecodeArgs& a, cudaStream_t s);  // bf16, rows of whole 16-byte pieces

@@ -16,6 +16,10 @@ tiny MNIST layers are launch-bound without it).
     ("YOLO26N Inference Optimisation", improvement #6).
   * PreprocessStem -- fused u8 preprocess to planar fp32, then the stem conv
     3x3 s2 3->16 + BN + SiLU reading the planar tensor directly.
+  * MapReader -- an attention layer over a feature map's positions that then
+    answers token by token from a paged cache: 1x1 conv to queries, keys and
+    values, attention, 1x1 conv with the residual; cb_attention,
+    cb_cache_append and cb_attention_decode as they are used together.
 """
 from __future__ import annotations
 
@@ -223,3 +227,62 @@ class PreprocessStem:
             cb.preprocess_u8(frames, self.planar, stream=stream)
         self.stem(self.planar, self.out, stream=stream, x_layout=cb.LAYOUT_NCHW)
         return self.out
+
+
+class MapReader:
+    """One attention layer over feature maps [B, H, W, C], then over the maps and the tokens that follow.
+
+    read(x): every position of a map sees every other; their keys and values go to the cache.
+    step(tok): one further token [B, C] per sequence, which sees the map, the tokens before it and itself.
+    Both are qkv (1x1 conv + folded BN), attention, out (1x1 conv + folded BN) plus the input, on buffers
+    made here, and may be captured in a CUDA graph: the lengths live on the device.  `tokens`: how many
+    steps the cache has room for; a page holds `page` tokens."""
+
+    def __init__(self, params, batch, hw, tokens, page=16, device="cuda", dtype=torch.float32):
+        self.hq, self.hkv, self.dim = params["heads"], params["kv_heads"], params["dim"]
+        self.batch, self.hw, (H, W) = batch, hw, hw
+        kw = dict(device=device, dtype=dtype)
+        self.qkv = ConvBnAct(params["qkv_w"], params["qkv_bn"], 1, 0, cb.ACT_NONE, **kw)
+        self.out = ConvBnAct(params["out_w"], params["out_bn"], 1, 0, cb.ACT_NONE, **kw)
+        C, wide = self.qkv.cin, self.qkv.cout
+        self.map_qkv, self.tok_qkv = torch.empty(batch, H, W, wide, **kw), torch.empty(batch, 1, 1, wide, **kw)
+        self.map_ctx = torch.empty(batch, H, W, self.hq * self.dim, **kw)
+        self.tok_ctx = torch.empty(batch, 1, 1, self.hq * self.dim, **kw)
+        self.map_out, self.tok_out = torch.empty(batch, H, W, C, **kw), torch.empty(batch, 1, 1, C, **kw)
+        pages = -(-(H * W + tokens) // page)
+        self.pages = [torch.zeros(batch * pages, page, self.hkv, self.dim, **kw) for _ in range(2)]
+        self.table = torch.arange(batch * pages, dtype=torch.int32, device=device).view(batch, pages)
+        self.cache = cb.PagedCache(*self.pages, self.table)
+        self.start = torch.zeros(batch, dtype=torch.int32, device=device)
+        self.length = torch.zeros(batch, dtype=torch.int32, device=device)
+        self.score = cb.Score(self.dim ** -0.5)
+        q = self._split(self.tok_qkv)[0][:, 0]
+        self.workspace = torch.empty(cb.attention_decode_workspace(q, self.cache), dtype=torch.uint8, device=device)
+
+    def _split(self, qkv):
+        """Queries, keys and values [B, L, heads, dim]: slices of the projection, read in place."""
+        d, hq, hkv = self.dim, self.hq, self.hkv
+        rows = qkv.view(self.batch, -1, hq + 2 * hkv, d)
+        return rows[:, :, :hq], rows[:, :, hq:hq + hkv], rows[:, :, hq + hkv:]
+
+    def read(self, x, stream=None):
+        self.qkv(x, self.map_qkv, stream=stream)
+        q, k, v = self._split(self.map_qkv)
+        cb.attention(q, k, v, self.map_ctx.view(*q.shape), self.score, stream=stream)
+        cb.cache_append(k, v, self.cache, self.start, stream=stream)
+        self.out(self.map_ctx, self.map_out, residual=x, res_mode=cb.RES_POST_ACT, stream=stream)
+        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(x.device)):
+            self.length.fill_(self.hw[0] * self.hw[1])
+        return self.map_out
+
+    def step(self, tok, stream=None):
+        x = tok.view(self.batch, 1, 1, -1)
+        self.qkv(x, self.tok_qkv, stream=stream)
+        q, k, v = self._split(self.tok_qkv)
+        cb.cache_append(k, v, self.cache, self.length, stream=stream)
+        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(x.device)):
+            self.length.add_(1)
+        cb.attention_decode(q[:, 0], self.cache, self.length, self.tok_ctx.view(self.batch, self.hq, self.dim), self.workspace,
+                            self.score.scale, stream=stream)
+        self.out(self.tok_ctx, self.tok_out, residual=x, res_mode=cb.RES_POST_ACT, stream=stream)
+        return self.tok_out.view(self.batch, -1)

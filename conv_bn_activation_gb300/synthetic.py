@@ -138,3 +138,12 @@ def stem_params(seed: int = SEED_BASE + 4):
     """Stem conv 3->16, 3x3, stride 2, + BN (fed by the preprocess)."""
     g = rng(seed + 100)
     return kaiming(g, 16, 3, 3, 3), bn_params(g, 16)
+
+
+def map_reader_params(channels=64, heads=8, kv_heads=2, dim=32, seed: int = SEED_BASE + 5):
+    """An attention layer over feature maps: 1x1 conv to queries, keys and values, 1x1 conv back, each with BN."""
+    g = rng(seed)
+    wide = (heads + 2 * kv_heads) * dim
+    return {"heads": heads, "kv_heads": kv_heads, "dim": dim,
+            "qkv_w": kaiming(g, wide, channels, 1, 1), "qkv_bn": bn_params(g, wide),
+            "out_w": kaiming(g, channels, heads * dim, 1, 1), "out_bn": bn_params(g, channels)}

@@ -138,20 +138,21 @@ cb_status plan_decode(const cb_heads* q, const cb_paged_cache* cache, DecodePlan
   const cb_status st = host_device(&p->sms, &p->err);
   if (st != CB_OK) return st;
   p->vec = pieces16(cache);
-  // One wave of resident CTAs: their runs are equal, so a second wave would only add pieces to join.
   const bool mma = q->dtype == CB_DTYPE_BF16 && p->vec;
-  p->ctas = p->sms * (p->vec ? decode_ctas_per_sm(cache->dim_k, cache->dim_v) : 4);
+  // One wave of resident CTAs: their runs are equal, so a second wave would only add pieces to join.
   const int group = q->heads / cache->heads, most = mma ? kDecodeMmaHeads : kDecodeSimtHeads;
   p->chunks = (group + most - 1) / most;
   p->heads = (group + p->chunks - 1) / p->chunks;
-  // Whole items on clusters where that leaves a CTA at most eight tiles of 64
+  p->ctas = p->sms * (p->vec ? decode_ctas_per_sm(cache->dim_k, cache->dim_v, mma, p->heads, q->batch) : 4);
+  // Whole items on clusters where that leaves a CTA at most 16 tiles of 64
   // tokens of the largest cache the table can name: no join then, and no CTA
-  // walks much longer than another.  Else runs.
+  // walks much longer than another.  Else runs.  (61 sequences of 944 to 2729
+  // tokens, 2 key heads of 64: 17.5 us, as runs 22; for more tiles see decode_stream.cuh.)
   const long long items = static_cast<long long>(q->batch) * cache->heads * p->chunks;
   const long long tiles = (static_cast<long long>(cache->max_pages) * cache->page_size + 63) / 64;
   p->split = 1;
   while (p->split < 8 && items * p->split * 2 <= p->ctas && p->split < tiles) p->split *= 2;
-  if (!p->vec || tiles > 8LL * p->split) p->split = 0;
+  if (!p->vec || tiles > 16LL * p->split) p->split = 0;
   return CB_OK;
 }
 

@@ -257,7 +257,7 @@ cudaError_t launch_attn_rows(const AttnArgs& rw, bool bf16, int sms, cudaStream_
   a.chunks = (rows + most - 1) / most;
   a.item_heads = (rows + a.chunks - 1) / a.chunks;
   // A cluster per item while that fills the GPU better and leaves every CTA a tile.
-  const long long items = static_cast<long long>(a.B) * a.Hkv * a.chunks, room = sms * decode_ctas_per_sm(a.dk, a.dv);
+  const long long items = static_cast<long long>(a.B) * a.Hkv * a.chunks, room = sms * decode_ctas_per_sm(a.dk, a.dv, bf16, a.item_heads, 0);
   const int tiles = (rw.Lk + 63) / 64;
   a.split = 1;
   while (a.split < 8 && items * a.split * 2 <= room && a.split < tiles) a.split *= 2;

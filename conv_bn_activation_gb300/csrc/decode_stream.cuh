@@ -17,10 +17,13 @@
 // Two ways to deal items (decode_common.cuh):
 //  - Runs: equal runs of tiles over one wave of CTAs; items cut by a run's end
 //    go through the workspace and a join kernel.
-//  - Whole items, for caches small enough that a CTA walks at most eight tiles
-//    and for contiguous rows: a cluster of a.split CTAs per item, joined through distributed shared
-//    memory.  One launch, no prefix over the lengths: one sequence of 421
-//    tokens takes 5.6 us where runs and their join take 7.7.
+//  - Whole items, for caches small enough that a CTA walks at most 16 tiles
+//    and for contiguous rows: a cluster of a.split CTAs per item, joined
+//    through distributed shared memory.  One launch, no prefix over the
+//    lengths: one sequence of 421 tokens takes 4.8 us where runs and their join
+//    take 7.7, 64 of 200 to 500 tokens (8 key heads of 128) 26 and 33; from
+//    about 30 tiles per CTA on runs are faster (32 sequences of 100 to 2000
+//    tokens: 37, whole 41).
 #pragma once
 
 #include "decode_common.cuh"
@@ -112,7 +115,8 @@ constexpr int decode_part_offset() {  // floats: the four warps' results, then t
 }
 
 template <class C, bool WHOLE>
-__global__ void __launch_bounds__(kDecodeThreads, decode_ctas_per_sm(C::DK, C::DV)) decode_stream_kernel(const DecodeArgs a, const AttnArgs rw) {
+__global__ void __launch_bounds__(kDecodeThreads, decode_ctas_per_sm(C::DK, C::DV, sizeof(typename C::T) == 2, C::kHeads, 0))
+    decode_stream_kernel(const DecodeArgs a, const AttnArgs rw) {
   using T = typename C::T;
   constexpr int DK = C::DK, DV = C::DV, kStep = C::kStep, kStages = C::kStages, kEl = static_cast<int>(sizeof(T));
   constexpr int kKeyBytes = DK * kEl, kValBytes = DV * kEl, kStageBytes = kStep * (kKeyBytes + kValBytes);
@@ -367,7 +371,9 @@ cudaError_t launch_decode_stream(const DecodeArgs& a, cudaStream_t s) {
   const size_t smem = decode_ring_bytes<C>() + C::kExtra + sizeof(unsigned) * (a.B + 1);
   const cudaError_t e = smem_attr_once<decode_stream_kernel<C, false>>(smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(decode_stream_kernel<C, false>, dim3(a.ctas), dim3(kDecodeThreads), smem, s, a, none);
+  // After the kernel before it, not among its CTAs: this wave fills the SMs exactly, and CTAs that came while others
+  // still held some of them would be placed unevenly (104 sequences of about 2000 fp32 tokens, 2 heads: 65 us, so 45).
+  return launch_serial(decode_stream_kernel<C, false>, dim3(a.ctas), dim3(kDecodeThreads), smem, s, a, none);
 }
 
 }  // namespace cb

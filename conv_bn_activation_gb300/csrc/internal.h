@@ -378,8 +378,16 @@ struct DecodeArgs {
   int* err;
 };
 constexpr int kDecodeSimtHeads = 8, kDecodeMmaHeads = 16;  // most query heads of one item
-// CTAs per SM of the streaming kernels: their rings take 48, 72 or 96 KB.
-constexpr int decode_ctas_per_sm(int dk, int dv) { return dk <= 64 && dv <= 64 ? 4 : dk <= 64 || dv <= 64 ? 3 : 2; }
+// CTAs of a streaming kernel that an SM holds: by registers 4, 3 or 2 (rings of 48, 72 or 96 KB), and no more than
+// its 228 KB of shared memory do, with fp32 queries and weights, the prefix over `batch` lengths, the static arrays
+// and the system's 1 KB. (One CTA more than fit is a second wave: 331 us, with the count right 253, for two fp32
+// sequences of 93000 tokens, 8 key heads of 64 and 128, 8 query heads each.)
+constexpr int decode_ctas_per_sm(int dk, int dv, bool bf16, int heads, int batch) {
+  const int DK = dk <= 64 ? 64 : 128, DV = dv <= 64 ? 64 : 128, most = DK + DV == 128 ? 4 : DK + DV == 192 ? 3 : 2;
+  const int nh = heads <= 4 ? 4 : 8, bytes = 384 * (DK + DV) + (bf16 ? 0 : 4 * nh * (DK + 32)) + 4 * (batch + 1) + 1824;
+  const int fit = 233472 / bytes;
+  return fit < most ? fit : most;
+}
 // What an item's start costs a CTA, in tiles of 64 tokens (decode_common.cuh). A tile of
 // fp32 takes a CTA twice as long as one of bf16, whatever the dims: fewer dims, more CTAs per SM.
 constexpr int decode_item_cost(bool bf16) { return bf16 ? 3 : 1; }

@@ -194,3 +194,18 @@ def test_append_refuses_bad_places(gpu):
     changed = (k != before).any(-1).any(-1).nonzero().tolist()
     assert changed == [[int(table[0, 0]), 0]]  # position -1 + 1 is token 0; the table's last page is -1
     assert cb.get_device_error() == cb.OK
+
+
+@pytest.mark.parametrize("lens", [[40, 0, 129], [3000, 1, 2100, 777]], ids=["whole", "runs"])
+@pytest.mark.parametrize("Hq,Hkv", [(2, 2), (20, 2)], ids=["one_head", "ten_heads"])
+@pytest.mark.parametrize("dk,dv", [(96, 96), (72, 96), (88, 80), (96, 128), (128, 72), (96, 64)])
+def test_dims_between_64_and_128(gpu, dk, dv, Hq, Hkv, lens):
+    """The pads of rows shorter than the kernel's are zeros, whatever the pages hold beyond a sequence."""
+    k, v, table = paged(lens, 16, Hkv, dk, dv, BF16, seed=dk + dv)
+    if len(lens) == 4:  # a table that could name far more: too many tiles for whole items
+        table = torch.cat([table, torch.full((4, 3000), -1, dtype=torch.int32, device="cuda")], 1)
+    q = (ref.randn(len(lens), Hq, dk, seed=5, dtype=F32, device="cuda") * 2).to(BF16)
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    got = run(q, k, v, table, n, scale=dk ** -0.5)
+    sync_check()
+    ref.check(got, ref.decode(q, k, v, table, n, dk ** -0.5), finite(v), BF16)

@@ -110,11 +110,19 @@ bool tc_map(CUtensorMap* m, const cb_heads* t) {
 // there are few queries, and cannot split the keys.  32 sequences, 4 key heads,
 // groups of 5, 2048 keys: 8 queries 54 against 78 us, 16 queries 90 against 78;
 // one sequence, 2 heads, 2048 keys, 64 queries: 11 against 22 us.
-// fp32: tiles of 32 rows at least: 8 sequences, 8 heads of 128, 2048 keys: 64
-// queries 271 against 353 us, 128 queries 524 against 357.
+// fp32: an item of 8 columns reads all its keys anew, and costs the GPU about
+// 1.3e-4 us per key; a wave of tiles of 64 rows takes 0.12 us per key however
+// few they are: 900 items per wave (32 heads on 4, 512 keys: 64 queries of one
+// sequence 26 against 62 us, 16 of 8 sequences 41 and 63, 64 of 8 136 and 85).
+// An item's start counts as 120 keys, a tile's as 50 (7 sequences of 82 tokens,
+// 10 heads on 2: 33 against 23 us; 4 of 160, 8 on 2: 22 and 29).
 bool few_queries(const AttnArgs& a, bool bf16, int sms) {
-  if (!bf16) return a.Lq <= 64;
-  const long long rows = static_cast<long long>(a.Lq) * a.group, chunks = (rows + kDecodeMmaHeads - 1) / kDecodeMmaHeads;
+  const long long rows = static_cast<long long>(a.Lq) * a.group;
+  if (!bf16) {
+    const long long seqs = static_cast<long long>(a.B) * (a.Hq / a.group), waves = ((rows + 63) / 64 * seqs + 2 * sms - 1) / (2 * sms);
+    return (rows + kDecodeSimtHeads - 1) / kDecodeSimtHeads * seqs * (a.Lk + 120) <= 6 * sms * waves * (a.Lk + 50);
+  }
+  const long long chunks = (rows + kDecodeMmaHeads - 1) / kDecodeMmaHeads;
   const long long pairs = (static_cast<long long>((a.Lq + 127) / 128) * a.group + 1) / 2;
   return 2 * chunks <= 3 * pairs || (chunks <= 8 && a.Lk >= 256 && 4 * pairs * a.B * (a.Hq / a.group) <= sms);
 }
@@ -177,6 +185,7 @@ cb_status cb_attention(const cb_heads* q, const cb_heads* k, const cb_heads* v, 
     if (!elem_aligned(t->data, t->dtype)) return CB_ERR_ALIGNMENT;
   if (empty(q)) return CB_OK;
   if (static_cast<long long>(q->batch) * q->heads * ((q->len + 31) / 32) >= (1LL << 31)) return CB_ERR_UNSUPPORTED;
+  if (static_cast<long long>(q->len) * (q->heads / k->heads) > (1LL << 31) - 256) return CB_ERR_UNSUPPORTED;  // rows of a key head
   AttnArgs a{};
   int sms = 0;
   const cb_status st = host_device(&sms, &a.err);

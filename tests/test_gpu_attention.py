@@ -201,3 +201,35 @@ def test_wide_offsets(gpu):
     out = run(q, k, v, {"scale": 0.125})
     sync_check()
     ref.check(out, ref.attention(q, k0, v0, 0.125), v0, BF16)
+
+
+@pytest.mark.parametrize("poison", [False, True], ids=["clean", "poison"])
+@pytest.mark.parametrize("name", ["full", "all"])
+@pytest.mark.parametrize("shape", [(40, 70, 83, 10, 10, 64, 64), (24, 66, 90, 20, 4, 72, 96), (5, 201, 190, 40, 8, 128, 128),
+                                   (40, 33, 40, 24, 8, 96, 128), (9, 300, 300, 12, 4, 40, 72), (3, 700, 700, 8, 8, 124, 100)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_fp32_tiles(gpu, shape, name, poison):
+    """Enough work that fp32 takes the tiled kernel: rows of 32, 64 and 128, heads that share a key head in one
+    tile, 64, 96 and 128 values; with NaN and infinities among the values that lie past the sequences' ends."""
+    B, Lq, Lk, Hq, Hkv, Dk, Dv = shape
+    q, k, v = make(shape, F32, seed=8, spread=1.0)
+    kw = rule(name, shape)
+    kv = torch.tensor([Lk - 7 * b % Lk for b in range(B)], dtype=torch.int32, device="cuda")
+    kw["kv_len"] = kv
+    past = torch.arange(Lk, device="cuda")[None, :] >= kv[:, None]
+    if poison:
+        k[past], v[past] = float("nan"), float("inf")
+    out = run(q, k, v, kw)
+    sync_check()
+    kd, vd = (t.double().masked_fill(past[..., None, None], 0.).repeat_interleave(Hq // Hkv, 2) for t in (k, v))
+    s = torch.einsum("bihd,bjhd->bhij", q.double(), kd) * kw["scale"]
+    at, j = torch.arange(Lq, device="cuda")[:, None] + kw.get("q_offset", 0), torch.arange(Lk, device="cuda")[None, :]
+    if name == "all":
+        s = 5.0 * torch.tanh(s / 5.0) - kw["slopes"].double()[None, :, None, None] * (at - j).abs()
+    keep = ~past[:, None, None, :]
+    if name == "all":
+        keep = keep & ((j <= at) | (j < kw["prefix_len"][:, None, None]))[:, None]
+        keep = keep & ((kw["doc_q"][:, :, None] == kw["doc_k"][:, None, :]) & (kw["doc_q"] >= 0)[:, :, None])[:, None]
+    w = torch.exp((s - s.masked_fill(~keep, -1e30).amax(-1, keepdim=True)).masked_fill(~keep, float("-inf")))
+    want = torch.einsum("bhij,bjhd->bihd", w / w.sum(-1, keepdim=True).clamp(min=1e-300), vd).cpu()
+    ref.check(out, want, vd, F32)

@@ -239,7 +239,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
   uint64_t* o_free = o_full + 2;
   uint64_t* list_full = o_free + 2;
   uint64_t* list_free = list_full + 2;
-  uint64_t* drain = list_free + 2;  // given-up launches only
+  uint64_t* drain = list_free + 2;  // all MMAs of a tile's warp are over
   uint64_t* v_tail = drain + 2;  // the values past the end of a tail tile are zero
   int* turn = reinterpret_cast<int*>(v_tail + 1);  // 1 while an MMA warp issues a tile's MMAs
   ItemInfo* info = reinterpret_cast<ItemInfo*>(v_tail + 2);
@@ -265,7 +265,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
       mbar_init(&kv_full[s], 1);
       mbar_init(&kv_empty[s], 2);
     }
-    mbar_init(v_tail, 1);
+    mbar_init(v_tail, 2);
     *abort_flag = 0;
     *turn = 0;
     fence_mbar_init();
@@ -498,7 +498,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
       auto k_wait = [&](const Step& s) {
         if (s.first) ++q_items;
         wait(&kv_full[s.seq % NS], s.seq / NS);
-        if (s.state && q_have != q_items) {
+        // Q_t has landed before its buffer is given back, also where no key tile of the item used it: a second
+        // load into a barrier whose first is still under way would be one arrival too many.
+        if ((s.state || s.last) && q_have != q_items) {
           q_have = q_items;
           wait(&q_full[t], q_items - 1);
         }
@@ -538,8 +540,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                 *reinterpret_cast<uint4*>(sKV + vs * SH::kSlot + s * kSlab + e * 16) = make_uint4(0, 0, 0, 0);
             fence_async_shared();
             __syncwarp();
-            if (lane == 0) mbar_arrive(v_tail);
           }
+          if (lane == 0) mbar_arrive(v_tail);  // both warps: neither is ever two tails ahead of the other
           wait(v_tail, tails++);
         }
         if (ok && more) k_wait(nxt);
@@ -573,7 +575,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
         cur = nxt;
       }
       __syncwarp();
-      if (!ok && leader) {  // the MMAs issued so far end before TMEM and shared memory are given back
+      if (leader) {  // the MMAs and arrivals issued so far end before TMEM and shared memory are given back
         mma_commit(&drain[t]);
         mbar_wait_drain(&drain[t], 0, 20000000ull);
       }

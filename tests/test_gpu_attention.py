@@ -233,3 +233,23 @@ def test_fp32_tiles(gpu, shape, name, poison):
     w = torch.exp((s - s.masked_fill(~keep, -1e30).amax(-1, keepdim=True)).masked_fill(~keep, float("-inf")))
     want = torch.einsum("bhij,bjhd->bihd", w / w.sum(-1, keepdim=True).clamp(min=1e-300), vd).cpu()
     ref.check(out, want, vd, F32)
+
+
+@pytest.mark.parametrize("docs", [False, True], ids=["odd_tiles", "padded_tiles"])
+def test_items_whose_second_tile_sees_nothing(gpu, docs):
+    """Pairs of query tiles of which one has no key to visit, over one or two key tiles and many rounds: its
+    queries' load is waited for before the next one is issued.  The same bits every time."""
+    shape = (100, 300, 100, 4, 4, 64, 64) if not docs else (30, 500, 500, 8, 8, 64, 64)
+    q, k, v = make(shape, BF16, seed=4)
+    kw = {"scale": 0.125}
+    if docs:
+        d = torch.arange(500, device="cuda") // 130
+        d[384:] = -1
+        kw["doc_q"] = kw["doc_k"] = d.to(torch.int32).expand(shape[0], 500).contiguous()
+    first = run(q, k, v, kw)
+    for _ in range(100):
+        assert torch.equal(run(q, k, v, kw).view(torch.int16), first.view(torch.int16))
+    sync_check()
+    pick = [0, 1, shape[0] - 1]
+    part = {n: (t[pick] if n in ("doc_q", "doc_k") else t) for n, t in kw.items()}
+    ref.check(first[pick], ref.attention(q[pick], k[pick], v[pick], **part), v, BF16)

@@ -425,8 +425,10 @@ typedef struct {
  * bf16 views whose data is 16-byte aligned with strides and head sizes that
  * are multiples of 8 elements, at most 2^18 keys long, run on the tensor
  * cores: scores and the sums over keys in fp32, the weights p rounded to bf16
- * as the second product's operand.  fp32, and every other bf16 view, runs in
- * fp32 on the CUDA cores.  Softmax statistics are fp32 throughout.  One
+ * as the second product's operand; where few queries share a key head they
+ * stream the keys through warp-level MMAs, as cb_attention_decode does.  fp32,
+ * and every other bf16 view, runs in fp32 on the CUDA cores.  Softmax
+ * statistics are fp32 throughout.  One
  * kernel, no workspace; asynchronous on `stream`; bounded waits
  * (CB_ERR_TIMEOUT through cb_get_device_error).
  */

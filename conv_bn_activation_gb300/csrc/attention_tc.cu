@@ -34,12 +34,12 @@
 // rounded to bf16 for the second product (each weight to nearest, independent
 // from key to key); l sums the unrounded weights.
 //
-// 4096 tokens, 16 heads on 4 key heads of 128: 103 us, 1330 TFLOP/s (0.69 of
-// the measured bf16 rate); capped 144, biased 114, causal 54; 16 heads of 64:
-// 86. The rest is latency: a tile's scores wait for its own weights' product,
+// 4096 tokens, 16 heads on 4 key heads of 128: 101 us, 1360 TFLOP/s (0.71 of
+// the measured bf16 rate); capped 137, biased 115, causal 53; 16 heads of 64:
+// 85. The rest is latency: a tile's scores wait for its own weights' product,
 // and two warps per scheduler do not cover all of it. Measured and not kept: P in
 // columns of its own for narrow values, so that the next scores start earlier
-// (86 -> 90); one path for full and masked tiles (103 -> 109).
+// (86 -> 90); one path for full and masked tiles (104 -> 109).
 //
 // Key tiles no query of the item sees are never loaded: the list of the tiles
 // to visit holds each query tile's state (skip, full, masked), nearest keys
@@ -604,22 +604,33 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
     const bool wide = ((reinterpret_cast<uintptr_t>(a.o) | (a.os_b * 2) | (a.os_l * 2) | (a.os_h * 2)) & 31) == 0 && a.dv % 16 == 0;
     uint32_t s_seen = 0, o_seen = 0;
     bool ok = true;
-    for (int k = 0; ok && k < rounds; ++k) {
-      if (item_of(k) >= items) break;
+    // What a thread needs of an item. The next one's is read before an item's output: the wait for the last
+    // product covers it.
+    struct Mine {
+      int b, i0, h, n, kv, doc, hi;
+      float slope;
+    } me, next;
+    auto read = [&](int k, Mine* m) {  // false: no such item, or a wait gave up (ok)
+      if (k >= rounds || item_of(k) >= items) return false;
       const int buf = k & 1;
       ok = __all_sync(~0u, mbar_wait(&list_full[buf], (k >> 1) & 1u, wd));
-      if (!ok) break;
+      if (!ok) return false;
       const ItemInfo inf = info[buf];
-      const int b = inf.it.b, i0 = t ? inf.it.i0[1] : inf.it.i0[0], h = t ? inf.it.h[1] : inf.it.h[0], i = i0 + row;
-      const int doc = a.doc_q ? q_docs[(buf * 2 + t) * kTile + row] : 0;
+      m->b = inf.it.b, m->i0 = t ? inf.it.i0[1] : inf.it.i0[0], m->h = t ? inf.it.h[1] : inf.it.h[0];
+      m->n = inf.n, m->kv = inf.kv, m->slope = t ? inf.slope[1] : inf.slope[0];
+      m->doc = a.doc_q ? q_docs[(buf * 2 + t) * kTile + row] : 0;
       // a row that sees nothing (hi 0) is dead: whatever it computes is dropped
-      const int hi = i < a.Lq && doc >= 0 ? row_end(a, SeqRule{inf.kv, inf.prefix}, i) : 0;
-      const int at = i + a.q_offset;
+      m->hi = m->i0 + row < a.Lq && m->doc >= 0 ? row_end(a, SeqRule{inf.kv, inf.prefix}, m->i0 + row) : 0;
+      return true;
+    };
+    bool more = read(0, &me);
+    for (int k = 0; more; ++k, me = next) {
+      const int buf = k & 1, b = me.b, i0 = me.i0, h = me.h, i = i0 + row, doc = me.doc, hi = me.hi, at = i + a.q_offset;
       const uint32_t* list = lists + buf * list_len;
-      const float slope = t ? inf.slope[1] : inf.slope[0];
+      const float slope = me.slope;
       float m_ref = kNegInf, l = 0.f;
       bool any = false;
-      for (int n = 0; n < inf.n; ++n) {
+      for (int n = 0; n < me.n; ++n) {
         const uint32_t e = list[n], st = (e >> (2 * t)) & 3u;
         if (st == kSkip) continue;
         const int j0 = static_cast<int>(e >> 4) * kTile;
@@ -631,7 +642,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
               const int j = j0 + lane + 32 * x;
-              key_doc[x] = j < inf.kv ? a.doc_k[static_cast<long long>(b) * a.Lk + j] : -1;
+              key_doc[x] = j < me.kv ? a.doc_k[static_cast<long long>(b) * a.Lk + j] : -1;
             }
             // The documents of a warp's rows are few: one round each.
             unsigned rows = ~0u;
@@ -820,6 +831,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&list_free[buf]);
+      if (!ok) break;
+      more = read(k + 1, &next);
       if (!ok) break;
       // ---------------------------------------------------------- output
       if (any) {

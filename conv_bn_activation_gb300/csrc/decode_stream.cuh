@@ -173,7 +173,6 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas_per_sm(C::DK, C::D
     else pc = next_piece(a, prefix, per_seq, at, end, &b);
     const char* kbase = static_cast<const char*>(a.cache.k) + pc.hk * a.cache.ks_h * kEl + (lane % CK) * 16;
     const char* vbase = static_cast<const char*>(a.cache.v) + pc.hk * a.cache.vs_h * kEl + (lane % CV) * 16;
-    C c(a, rw, pc, after);
 
     // Lanes below kStep look the step's tokens up, one step before their copies
     // are issued: the byte offsets of the rows, or -1.
@@ -240,6 +239,7 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas_per_sm(C::DK, C::D
       live[s] = issue(s, s, r);
       docs[s] = r.doc;
     }
+    C c(a, rw, pc, after);  // the queries are read while the first tokens come
     Rows rows = lookup(kStages - 1);
     int stage = 0;
     for (int step = 0; step < steps; ++step) {

@@ -182,16 +182,20 @@ __device__ __forceinline__ void note_item(const DecodeArgs& a, const Run& run, c
 // Floats of one partial result: per head m, l, then dv unnormalised sums.
 __host__ __device__ inline size_t part_floats(int heads, int dv) { return static_cast<size_t>(heads) * (dv + 2); }
 
-// Where token j of sequence b lies: its page, or -1 (and the error recorded).
-__device__ __forceinline__ int token_page(const DecodeArgs& a, int b, int j, int* slot) {
-  const int pg = j / a.cache.page_size;
-  *slot = j - pg * a.cache.page_size;
+// The page that entry pg of sequence b names, or -1 (and the error recorded).
+__device__ __forceinline__ int checked_page(const DecodeArgs& a, int b, int pg) {
   const int page = a.cache.table[b * a.cache.table_stride + pg];
   if (page < 0 || page >= a.cache.num_pages) {
     atomicCAS(a.err, 0, 1);  // CB_ERR_INVALID_ARG
     return -1;
   }
   return page;
+}
+// Where token j of sequence b lies: its page, or -1 (and the error recorded).
+__device__ __forceinline__ int token_page(const DecodeArgs& a, int b, int j, int* slot) {
+  const int pg = j / a.cache.page_size;
+  *slot = j - pg * a.cache.page_size;
+  return checked_page(a, b, pg);
 }
 
 }  // namespace cb

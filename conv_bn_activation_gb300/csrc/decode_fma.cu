@@ -65,6 +65,7 @@ struct FmaPolicy {
       for (int e = 0; e < EV; ++e) o[h][e] = 0.f;
   }
 
+  template <bool>
   __device__ __forceinline__ void step(uint32_t ks, uint32_t vs, unsigned lv, int far, int doc) {
     float dot[NH];
 #pragma unroll
@@ -82,7 +83,7 @@ struct FmaPolicy {
     // This lane's heads sub, sub + 4, ... of its key.
     const bool exists = (lv >> key) & 1;
     const int my_doc = ROWS ? __shfl_sync(~0u, doc, key) : 0;
-    float x[OWN], mx[OWN];
+    float x[OWN];
     bool grow = false;
 #pragma unroll
     for (int i = 0; i < OWN; ++i) {
@@ -100,18 +101,17 @@ struct FmaPolicy {
       } else {
         x[i] = exists ? fmaf(-slope[i], static_cast<float>(far - key), score(d)) : kNegInf;
       }
-      float y = x[i];
-      y = fmaxf(y, __shfl_xor_sync(~0u, y, 4));
-      y = fmaxf(y, __shfl_xor_sync(~0u, y, 8));
-      y = fmaxf(y, __shfl_xor_sync(~0u, y, 16));
-      mx[i] = y;
-      grow |= y > m[i] + kDecodeGrowth;
+      grow |= x[i] > m[i] + kDecodeGrowth;
     }
-    if (__any_sync(~0u, grow)) {
+    if (__any_sync(~0u, grow)) {  // only then are the maxima taken
       float f[OWN];
 #pragma unroll
       for (int i = 0; i < OWN; ++i) {
-        const float mn = fmaxf(m[i], mx[i]);
+        float y = x[i];
+        y = fmaxf(y, __shfl_xor_sync(~0u, y, 4));
+        y = fmaxf(y, __shfl_xor_sync(~0u, y, 8));
+        y = fmaxf(y, __shfl_xor_sync(~0u, y, 16));
+        const float mn = fmaxf(m[i], y);
         f[i] = mn == kNegInf ? 1.f : exp2_approx(m[i] - mn);
         m[i] = mn;
         l[i] *= f[i];

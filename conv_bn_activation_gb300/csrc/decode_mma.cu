@@ -100,6 +100,8 @@ struct MmaPolicy {
 
   // 16 keys at ks / vs; bit x of lv: key x exists; far: the first key's distance
   // from the query (ROWS: its place); doc: the document of key lane % 16 (ROWS).
+  // EAGER: the maxima are taken only when a score passes the last ones by kDecodeGrowth.
+  template <bool EAGER>
   __device__ __forceinline__ void step(uint32_t ks, uint32_t vs, unsigned lv, int far, int doc) {
     float s[NB][4];  // element r: key g + 8 (r >> 1), head 8 nb + 2 t4 + (r & 1)
 #pragma unroll
@@ -117,7 +119,6 @@ struct MmaPolicy {
     const float dist = static_cast<float>(far - g);
     const int doc0 = ROWS ? __shfl_sync(~0u, doc, g) : 0, doc1 = ROWS ? __shfl_sync(~0u, doc, g + 8) : 0;
     bool grow = false;
-    float mx[NB][2];
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
@@ -133,18 +134,26 @@ struct MmaPolicy {
         }
         if (lv != 0xffffu && !((lv >> (g + 8 * (r >> 1))) & 1)) x = kNegInf;
         s[nb][r] = x;
-      }
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float y = fmaxf(s[nb][e], s[nb][2 + e]);
-        y = fmaxf(y, __shfl_xor_sync(~0u, y, 4));
-        y = fmaxf(y, __shfl_xor_sync(~0u, y, 8));
-        y = fmaxf(y, __shfl_xor_sync(~0u, y, 16));
-        mx[nb][e] = y;
-        grow |= y > m[nb][e] + kDecodeGrowth;
+        if (EAGER) grow |= x > m[nb][r & 1] + kDecodeGrowth;
       }
     }
+    float mx[NB][2];
+    auto maxima = [&] {
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float y = fmaxf(s[nb][e], s[nb][2 + e]);
+          y = fmaxf(y, __shfl_xor_sync(~0u, y, 4));
+          y = fmaxf(y, __shfl_xor_sync(~0u, y, 8));
+          y = fmaxf(y, __shfl_xor_sync(~0u, y, 16));
+          mx[nb][e] = y;
+          if (!EAGER) grow |= y > m[nb][e] + kDecodeGrowth;
+        }
+    };
+    if (!EAGER) maxima();
     if (__any_sync(~0u, grow)) {
+      if (EAGER) maxima();
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll

@@ -20,7 +20,7 @@
 //  - Whole items, for caches small enough that a CTA walks at most 16 tiles
 //    and for contiguous rows: a cluster of a.split CTAs per item, joined
 //    through distributed shared memory.  One launch, no prefix over the
-//    lengths: one sequence of 421 tokens takes 4.8 us where runs and their join
+//    lengths: one sequence of 421 tokens takes 4.7 us where runs and their join
 //    take 7.7, 64 of 200 to 500 tokens (8 key heads of 128) 26 and 33; from
 //    about 30 tiles per CTA on runs are faster (32 sequences of 100 to 2000
 //    tokens: 37, whole 41).
@@ -165,6 +165,13 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas_per_sm(C::DK, C::D
   const uint32_t v_dst = kStep * kKeyBytes + (lane / CV) * kValBytes + (((lane % CV) ^ C::swizzle(lane / CV)) * 16);
   const bool same = a.cache.ks_p == a.cache.vs_p && a.cache.ks_t == a.cache.vs_t;  // one offset serves both
 
+  // Steps as short as they can be, but for runs of bf16 tokens, which HBM bounds: there warps that wait less
+  // for themselves run further apart, and memory is the slower for it (8 sequences of up to 131072 tokens 483 us,
+  // with eager steps 510; 8 of 300 to 1700, whole: 13.7 and 13.2; two fp32 sequences of 93000: 249 and 222).
+  constexpr bool kEager = WHOLE || sizeof(T) == 4;
+  // from a lane's token to its next one, without a division per step
+  const int adv_pg = C::kRows ? 0 : kDecodeWarps * kStep / a.cache.page_size, adv_slot = kDecodeWarps * kStep - adv_pg * a.cache.page_size;
+
   while (at < end) {
     static_assert(WHOLE || !C::kRows, "contiguous rows are dealt as whole items");
     Piece pc;
@@ -182,22 +189,27 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas_per_sm(C::DK, C::D
       long long k, v;
       int doc;  // contiguous rows: the key's document
     };
-    auto lookup = [&](int step) {
-      const int j = base + step * (kDecodeWarps * kStep) + lane % kStep;
+    int j = base + lane % kStep, pg = C::kRows ? 0 : j / a.cache.page_size, slot = C::kRows ? 0 : j - pg * a.cache.page_size;
+    auto lookup = [&](int step) {  // once for each step, in order
       Rows r{-1, -1, -1};
       if (step < steps && j >= pc.lo && j < pc.hi) {
         if constexpr (C::kRows) {
           r.k = (pc.b * a.cache.ks_p + j * a.cache.ks_t) * kEl;
           r.v = (pc.b * a.cache.vs_p + j * a.cache.vs_t) * kEl;
           if (rw.doc_k) r.doc = rw.doc_k[static_cast<long long>(pc.b) * rw.Lk + j];
-          return r;
+        } else {
+          if (!kEager) pg = j / a.cache.page_size, slot = j - pg * a.cache.page_size;
+          const long long page = checked_page(a, pc.b, pg);
+          if (page >= 0) {
+            r.k = (page * a.cache.ks_p + slot * a.cache.ks_t) * kEl;
+            r.v = same ? r.k : (page * a.cache.vs_p + slot * a.cache.vs_t) * kEl;
+          }
         }
-        int slot;
-        const long long page = token_page(a, pc.b, j, &slot);
-        if (page >= 0) {
-          r.k = (page * a.cache.ks_p + slot * a.cache.ks_t) * kEl;
-          r.v = same ? r.k : (page * a.cache.vs_p + slot * a.cache.vs_t) * kEl;
-        }
+      }
+      j += kDecodeWarps * kStep;
+      if (kEager && !C::kRows) {
+        pg += adv_pg, slot += adv_slot;
+        if (slot >= a.cache.page_size) slot -= a.cache.page_size, ++pg;
       }
       return r;
     };
@@ -262,7 +274,7 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas_per_sm(C::DK, C::D
       const uint32_t ks = ring_addr + stage * kStageBytes;
       // a decode query stands pc.len - 1 - j before key j; a row query knows its own place
       const int j0 = base + step * (kDecodeWarps * kStep);
-      c.step(ks, ks + kStep * kKeyBytes, lv, C::kRows ? j0 : pc.len - 1 - j0, doc);
+      c.template step<kEager>(ks, ks + kStep * kKeyBytes, lv, C::kRows ? j0 : pc.len - 1 - j0, doc);
       stage = stage + 1 == kStages ? 0 : stage + 1;
     }
     cp_async_wait<0>();

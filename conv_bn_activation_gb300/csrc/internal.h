@@ -380,7 +380,7 @@ struct DecodeArgs {
 constexpr int kDecodeSimtHeads = 8, kDecodeMmaHeads = 16;  // most query heads of one item
 // CTAs of a streaming kernel that an SM holds: by registers 4, 3 or 2 (rings of 48, 72 or 96 KB), and no more than
 // its 228 KB of shared memory do, with fp32 queries and weights, the prefix over `batch` lengths, the static arrays
-// and the system's 1 KB. (One CTA more than fit is a second wave: 331 us, with the count right 253, for two fp32
+// and the system's 1 KB. (One CTA more than fit is a second wave: 331 us, with the count right 253 (now 222), for two fp32
 // sequences of 93000 tokens, 8 key heads of 64 and 128, 8 query heads each.)
 constexpr int decode_ctas_per_sm(int dk, int dv, bool bf16, int heads, int batch) {
   const int DK = dk <= 64 ? 64 : 128, DV = dv <= 64 ? 64 : 128, most = DK + DV == 128 ? 4 : DK + DV == 192 ? 3 : 2;

@@ -211,9 +211,10 @@ def _stream_of(t, stream):
     """The stream's handle: `stream`, or the current one of t's device."""
     if stream is not None:
         return stream.cuda_stream
-    if not t.is_cuda:
+    device = t.get_device()
+    if device < 0:
         raise ValueError("the tensors of a GPU call are on a CUDA device")
-    return _raw_stream(t.get_device())
+    return _raw_stream(device)
 
 
 def heads(t) -> bytes:
@@ -250,7 +251,7 @@ def _device_array(t, name, dtype, shape):
         return 0
     if _codes is None:
         _init_codes()
-    if t.dtype != _codes[dtype] or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+    if t.dtype is not _codes[dtype] or t.shape != shape or t.get_device() < 0 or not t.is_contiguous():
         raise ValueError(f"{name}: a contiguous {_codes[dtype]} device tensor of shape {shape}, got {t.dtype} "
                          f"{tuple(t.shape)} on {t.device}")
     return t.data_ptr()

@@ -83,8 +83,7 @@ struct FmaPolicy {
     // This lane's heads sub, sub + 4, ... of its key.
     const bool exists = (lv >> key) & 1;
     const int my_doc = ROWS ? __shfl_sync(~0u, doc, key) : 0;
-    float x[OWN];
-    bool grow = false;
+    float x[OWN], own[1][OWN];
 #pragma unroll
     for (int i = 0; i < OWN; ++i) {
       // The four lanes' sums of four heads, each lane left with its own head's.
@@ -93,13 +92,18 @@ struct FmaPolicy {
       const bool hi = sub & 2, odd = sub & 1;
       const float e0 = (hi ? d2 : d0) + __shfl_xor_sync(~0u, hi ? d0 : d2, 2);
       const float e1 = (hi ? d3 : d1) + __shfl_xor_sync(~0u, hi ? d1 : d3, 2);
-      const float d = (odd ? e1 : e0) + __shfl_xor_sync(~0u, odd ? e0 : e1, 1);
+      own[0][i] = (odd ? e1 : e0) + __shfl_xor_sync(~0u, odd ? e0 : e1, 1);
+    }
+    score(own);
+    bool grow = false;
+#pragma unroll
+    for (int i = 0; i < OWN; ++i) {
       if constexpr (ROWS) {
         const int j = far + key;
         const bool seen = exists && j < rule[i].hi && my_doc == rule[i].doc;
-        x[i] = seen ? fmaf(-slope[i], static_cast<float>(abs(rule[i].at - j)), score(d)) : kNegInf;
+        x[i] = seen ? fmaf(-slope[i], static_cast<float>(abs(rule[i].at - j)), own[0][i]) : kNegInf;
       } else {
-        x[i] = exists ? fmaf(-slope[i], static_cast<float>(far - key), score(d)) : kNegInf;
+        x[i] = exists ? fmaf(-slope[i], static_cast<float>(far - key), own[0][i]) : kNegInf;
       }
       grow |= x[i] > m[i] + kDecodeGrowth;
     }

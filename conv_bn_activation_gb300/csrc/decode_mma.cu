@@ -115,7 +115,7 @@ struct MmaPolicy {
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) mma16816(s[nb], f, qf[d][nb][0], qf[d][nb][1]);
     }
-    // x = log2(e) * score
+    score(s);  // x = log2(e) * score
     const float dist = static_cast<float>(far - g);
     const int doc0 = ROWS ? __shfl_sync(~0u, doc, g) : 0, doc1 = ROWS ? __shfl_sync(~0u, doc, g + 8) : 0;
     bool grow = false;
@@ -123,7 +123,7 @@ struct MmaPolicy {
     for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        float x = score(s[nb][r]);
+        float x = s[nb][r];
         if constexpr (ROWS) {
           const RowRule& w = rule[nb][r & 1];
           const int j = far + g + 8 * (r >> 1);

@@ -1,0 +1,79 @@
+"""Capped scores on every attention kernel, at caps far above, near and far below the scores, against the
+definition in 64 bits: scale, cap tanh(s / cap), softmax."""
+import pytest
+import torch
+
+import attention_ref as ref
+from conv_bn_activation_gb300 import binding as cb
+from gpu_util import sync_check
+from test_gpu_decode import finite, paged, run as run_decode
+
+pytestmark = pytest.mark.gpu
+BF16, F32 = torch.bfloat16, torch.float32
+TYPES = pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+
+
+def definition(q, k, v, scale, softcap, slopes=None, causal=False):
+    """attention_ref.attention for whole rows, on the GPU in 64 bits."""
+    group = q.shape[2] // k.shape[2]
+    q, k, v = q.double(), k.double().repeat_interleave(group, 2), v.double().repeat_interleave(group, 2)
+    s = torch.einsum("bihd,bjhd->bhij", q, k) * scale
+    if softcap:
+        s = softcap * torch.tanh(s / softcap)
+    i, j = torch.arange(s.shape[2], device="cuda")[:, None], torch.arange(s.shape[3], device="cuda")[None, :]
+    i = i + (s.shape[3] - s.shape[2] if causal else 0)
+    if slopes is not None:
+        s = s - slopes.double()[None, :, None, None] * (i - j).abs()
+    if causal:
+        s = s.masked_fill(j > i, float("-inf"))
+    return torch.einsum("bhij,bjhd->bihd", torch.softmax(s, -1), v).cpu()
+
+
+def tokens(shape, dtype, seed, spread=3.0):
+    B, Lq, Lk, Hq, Hkv, Dk, Dv = shape
+    return ((ref.randn(B, Lq, Hq, Dk, seed=seed, dtype=F32, device="cuda") * spread).to(dtype),
+            ref.randn(B, Lk, Hkv, Dk, seed=seed + 1, dtype=dtype, device="cuda"),
+            ref.randn(B, Lk, Hkv, Dv, seed=seed + 2, dtype=dtype, device="cuda"))
+
+
+def attend(q, k, v, **kw):
+    out = torch.full((*q.shape[:3], v.shape[3]), float("nan"), dtype=q.dtype, device="cuda")
+    if kw.get("causal"):
+        kw["q_offset"] = k.shape[1] - q.shape[1]
+    cb.attention(q, k, v, out, cb.Score(**kw))
+    sync_check()
+    return out
+
+
+# few queries per key head (the streaming kernel), then tiles (tensor cores; fp32 on the CUDA cores), then bf16
+# rows that are not whole 16-byte pieces
+ROWS = [(1, 1, 1000, 8, 1, 128, 128), (8, 2, 700, 6, 2, 64, 64), (4, 1, 300, 4, 4, 96, 64)]
+TILES = [(2, 400, 400, 4, 4, 32, 64), (16, 300, 300, 8, 2, 128, 128), (2, 150, 150, 2, 2, 33, 31)]
+CAPS = pytest.mark.parametrize("softcap", [50.0, 1e3, 1e6, 1e30], ids=str)
+
+
+@TYPES
+@CAPS
+@pytest.mark.parametrize("shape", ROWS + TILES, ids=lambda s: "x".join(map(str, s)))
+def test_attention_keeps_scores_far_below_their_cap(gpu, shape, softcap, dtype):
+    q, k, v = tokens(shape, dtype, seed=3)
+    kw = {"scale": shape[5] ** -0.5, "softcap": softcap}
+    ref.check(attend(q, k, v, **kw), definition(q, k, v, **kw), v, dtype)
+
+
+@TYPES
+@CAPS
+@pytest.mark.parametrize("dims", [(64, 64), (96, 128), (33, 31)], ids=str)
+@pytest.mark.parametrize("Hq,Hkv", [(2, 2), (16, 2)], ids=["one_head", "eight_heads"])
+@pytest.mark.parametrize("lens", [[421, 77], [3000, 1, 2100]], ids=["whole", "runs"])
+def test_decode_keeps_scores_far_below_their_cap(gpu, lens, Hq, Hkv, dims, softcap, dtype):
+    dk, dv = dims
+    k, v, table = paged(lens, 16, Hkv, dk, dv, dtype, seed=2)
+    if len(lens) == 3:  # a table that could name far more: too many tiles for whole items
+        table = torch.cat([table, torch.full((3, 3000), -1, dtype=torch.int32, device="cuda")], 1)
+    q = (ref.randn(len(lens), Hq, dk, seed=5, dtype=F32, device="cuda") * 3).to(dtype)
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    kw = {"scale": dk ** -0.5, "softcap": softcap}
+    got = run_decode(q, k, v, table, n, **kw)
+    sync_check()
+    ref.check(got, ref.decode(q, k, v, table, n, **kw), finite(v), dtype)

@@ -92,6 +92,14 @@ bool score_ok(float scale, float softcap) {
   return std::isfinite(scale) && scale > 0.f && std::isfinite(softcap) && softcap >= 0.f;
 }
 
+// The cap as the kernels take it (0: none), away from the ends of fp32's range, where scale / softcap or
+// softcap * log2(e) would be 0 or infinite. From 2^100 on a cap moves no score below 2^88 by a bit; below 2^-30
+// every weight e^(+-softcap) is 1 in 32 bits, as it is at 2^-30.
+float kernel_cap(float softcap) {
+  if (softcap == 0.f || softcap >= 0x1p100f) return 0.f;
+  return softcap < 0x1p-30f ? 0x1p-30f : softcap;
+}
+
 // The tensor-core kernel's map of a view: (dim, heads, len, batch).
 bool tc_map(CUtensorMap* m, const cb_heads* t) {
   int box_d = 0, box_l = 0;
@@ -197,7 +205,7 @@ cb_status cb_attention(const cb_heads* q, const cb_heads* k, const cb_heads* v, 
   a.os_b = out->stride_b, a.os_l = out->stride_l, a.os_h = out->stride_h;
   a.B = q->batch, a.Lq = q->len, a.Lk = k->len, a.Hq = q->heads, a.group = q->heads / k->heads;
   a.dk = q->dim, a.dv = v->dim;
-  a.scale = score->scale, a.softcap = score->softcap, a.slopes = score->slopes;
+  a.scale = score->scale, a.softcap = kernel_cap(score->softcap), a.slopes = score->slopes;
   a.causal = score->causal ? 1 : 0, a.q_offset = score->q_offset;
   a.prefix_len = score->prefix_len, a.kv_len = score->kv_len;
   if (k->len > 0) a.doc_q = score->doc_q, a.doc_k = score->doc_k;
@@ -274,7 +282,7 @@ cb_status cb_attention_decode(const cb_heads* q, const cb_paged_cache* cache, co
   a.qs_b = q->stride_b, a.qs_h = q->stride_h, a.os_b = out->stride_b, a.os_h = out->stride_h;
   a.cache = paged_args(cache);
   a.length = length, a.first = first, a.slopes = slopes;
-  a.scale = scale, a.softcap = softcap;
+  a.scale = scale, a.softcap = kernel_cap(softcap);
   a.B = q->batch, a.Hq = q->heads, a.Hkv = cache->heads, a.group = q->heads / cache->heads;
   a.dk = cache->dim_k, a.dv = cache->dim_v;
   a.chunks = p.chunks, a.item_heads = p.heads, a.split = p.split;

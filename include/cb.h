@@ -397,7 +397,8 @@ typedef struct {
  *     j < kv_len[b]                     (kv_len NULL: j < k->len), and
  *     causal == 0, or j <= i + q_offset, or j < prefix_len[b]  (NULL: 0), and
  *     doc_q[b*q->len + i] == doc_k[b*k->len + j] >= 0          (NULL: no documents).
- * scale > 0 and softcap >= 0 are finite; |q_offset| <= 2^29; prefix_len
+ * scale > 0 and softcap >= 0 are finite (a softcap from 2^100 on counts as
+ * none: it changes only scores past 2^88); |q_offset| <= 2^29; prefix_len
  * needs causal; doc_q and doc_k come together.  slopes: DEVICE fp32
  * [q->heads]; kv_len, prefix_len: DEVICE int [batch], clamped to
  * [0, k->len]; doc_q, doc_k: DEVICE int [batch, len], contiguous, negative =

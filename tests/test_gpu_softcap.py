@@ -77,3 +77,33 @@ def test_decode_keeps_scores_far_below_their_cap(gpu, lens, Hq, Hkv, dims, softc
     got = run_decode(q, k, v, table, n, **kw)
     sync_check()
     ref.check(got, ref.decode(q, k, v, table, n, **kw), finite(v), dtype)
+
+
+ENDS = pytest.mark.parametrize("softcap", [1e-45, 1e-40, 1e-30, 1e-9, 2e38, 3.4e38], ids=str)
+
+
+@TYPES
+@ENDS
+@pytest.mark.parametrize("shape", ROWS[:1] + TILES, ids=lambda s: "x".join(map(str, s)))
+def test_attention_with_caps_at_the_ends_of_fp32(gpu, shape, softcap, dtype):
+    """A cap as small as fp32 holds leaves the mean of the values, one as large caps nothing; a score of exactly
+    zero is neither's NaN."""
+    q, k, v = tokens(shape, dtype, seed=6)
+    q[:, 0] = 0
+    kw = {"scale": shape[5] ** -0.5, "softcap": softcap}
+    ref.check(attend(q, k, v, **kw), definition(q, k, v, **kw), v, dtype)
+
+
+@TYPES
+@ENDS
+@pytest.mark.parametrize("dims", [(64, 64), (33, 31)], ids=str)
+def test_decode_with_caps_at_the_ends_of_fp32(gpu, dims, softcap, dtype):
+    lens = [421, 77]
+    k, v, table = paged(lens, 16, 2, *dims, dtype, seed=2)
+    q = (ref.randn(2, 4, dims[0], seed=5, dtype=F32, device="cuda") * 3).to(dtype)
+    q[0, 0] = 0
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    kw = {"scale": dims[0] ** -0.5, "softcap": softcap}
+    got = run_decode(q, k, v, table, n, **kw)
+    sync_check()
+    ref.check(got, ref.decode(q, k, v, table, n, **kw), finite(v), dtype)

@@ -311,14 +311,26 @@ __global__ void __launch_bounds__(BM * 2, BM == 128 ? 1 : 2) attn_simt_kernel(At
       }
     }
   }
-  // Rows that met a non-finite value: again, key by key (attn_row).
+  // Rows that met a hidden value that is not finite: again, key by key. This warp's 16 rows, one per lane.
+  const int lane = tid & 31, row = r0 + (tid >> 5) * 16 + lane;
+  unsigned odd = 0;
+  float sum = 0.f;
 #pragma unroll
   for (int r = 0; r < 8; ++r) {
     const unsigned who = __ballot_sync(~0u, (bad >> r) & 1);
-    const int first = r0 + (tid >> 5) * 16 + r;
-    __syncwarp();
-    if (who & 0xffffu) attn_row<T>(a, b, hk * a.group + first % a.group, first / a.group);
-    if (who >> 16) attn_row<T>(a, b, hk * a.group + (first + 8) % a.group, (first + 8) / a.group);
+    odd |= (who & 0xffffu ? 1u << r : 0u) | (who >> 16 ? 256u << r : 0u);
+    const float x = __shfl_sync(~0u, l[r], lane & 8 ? 16 : 0);
+    if ((lane & 7) == r) sum = x;
+  }
+  if (odd) {
+    const bool mine = lane < 16 && (odd >> lane) & 1;
+    const int i = mine ? row / a.group : 0, my_doc = mine && a.doc_q ? a.doc_q[static_cast<long long>(b) * a.Lq + i] : 0;
+    const int end = min(rule.kv, (hi_max + kBN - 1) / kBN * kBN);
+    unsigned again = rows_to_redo<T, VEC>(a, b, hk, end, mine, mine && my_doc >= 0 ? row_end(a, rule, i) : 0, my_doc, sum);
+    for (; again; again &= again - 1) {
+      const int r = row - lane + __ffs(again) - 1;
+      attn_row<T, VEC>(a, b, hk * a.group + r % a.group, r / a.group);
+    }
   }
 }
 

@@ -880,12 +880,13 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
         __syncwarp();
         if (lane == 0) mbar_arrive(&o_free[t]);
       }
-      // Rows that met a non-finite value: again, key by key (attn_row).
+      // Rows that met a hidden value that is not finite: again, key by key.
       unsigned bad = __ballot_sync(~0u, i < a.Lq && live && !(probe0 + probe1 == 0.f));
-      while (bad) {
-        const int r = __ffs(bad) - 1;
-        bad &= bad - 1;
-        attn_row_inline<__nv_bfloat16>(a, b, h, i0 + (warp & 3) * 32 + r);
+      if (bad) {
+        const SeqRule rule = seq_rule(a, b);
+        const int end = min(rule.kv, (row_end(a, rule, min(a.Lq, i0 + kTile) - 1) + kTile - 1) / kTile * kTile);
+        bad = rows_to_redo<__nv_bfloat16, true>(a, b, h / a.group, end, (bad >> lane) & 1, hi, doc, l);
+        for (; bad; bad &= bad - 1) attn_row<__nv_bfloat16, true>(a, b, h, i0 + (warp & 3) * 32 + __ffs(bad) - 1);
       }
     }
     tc_fence_before_sync();

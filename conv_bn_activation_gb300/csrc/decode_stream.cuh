@@ -165,6 +165,7 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas_per_sm(C::DK, C::D
   uint8_t* after = smem + decode_ring_bytes<C>();
   __shared__ float ms[kDecodeWarps][C::kHeads], ls[kDecodeWarps][C::kHeads];
   __shared__ float part_m[C::kHeads], part_l[C::kHeads];
+  __shared__ int odd[C::kHeads];  // contiguous rows: columns with a result that is not finite
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int kq = a.dk * kEl / 16, vq = a.dv * kEl / 16;  // real pieces per row
@@ -325,6 +326,7 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas_per_sm(C::DK, C::D
     float* part_s = res + decode_part_offset<C>();
     float* part = WHOLE ? nullptr : a.part + (2 * cta + (pc.starts ? 1 : 0)) * part_floats(a.item_heads, a.dv);
     const bool out = pc.starts && pc.ends;
+    if (C::kRows && tid < C::kHeads) odd[tid] = 0;
     if (tid < pc.heads) {
       float mm = kNegInf, ll = 0.f, f[kDecodeWarps];
 #pragma unroll
@@ -342,10 +344,10 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas_per_sm(C::DK, C::D
       else if (!out) part[tid] = mm, part[a.item_heads + tid] = ll;
     }
     __syncthreads();
-    bool bad = false;  // contiguous rows: a result that is not finite
-    auto put = [&](int hd, int d, float y) {
+    bool bad = false;
+    auto put = [&](int hd, int d, float y, float sum) {
       out_row<C::kRows, T>(a, rw, pc, hd)[d] = from_f32<T>(y);
-      bad |= !(y * 0.f == 0.f);
+      if (C::kRows && !(y * 0.f == 0.f) && sum == sum) bad = true, odd[hd] = 1;
     };
     for (int e = tid; e < pc.heads * DV; e += kDecodeThreads) {
       const int hd = e / DV, d = e % DV;
@@ -353,7 +355,7 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas_per_sm(C::DK, C::D
       float sum = 0.f;
 #pragma unroll
       for (int w = 0; w < kDecodeWarps; ++w) sum = fmaf(ms[w][hd], res[(w * pc.heads + hd) * DV + d], sum);
-      if (out) put(hd, d, sum);
+      if (out) put(hd, d, sum, C::kRows ? part_l[hd] : 0.f);
       else if constexpr (WHOLE) part_s[hd * DV + d] = sum;
       else part[2 * a.item_heads + hd * a.dv + d] = sum;
     }
@@ -377,19 +379,19 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas_per_sm(C::DK, C::D
               sum = fmaf(f, ld_cluster_f32(map_shared_rank(smem_u32(part_s + e), r)), sum);
               ll = fmaf(f, ld_cluster_f32(map_shared_rank(smem_u32(part_l + hd), r)), ll);
             }
-          put(hd, d, ll == 0.f ? 0.f : sum / ll);
+          put(hd, d, ll == 0.f ? 0.f : sum / ll, ll);
         }
         cluster_sync();  // the parts are read before any CTA leaves
       }
       if constexpr (C::kRows) {
-        // A masked key's weight 0 times an infinite or NaN value: such rows again, key by key (attn_row).
-        if (__syncthreads_or(bad))
-          for (int hd = warp; hd < pc.heads; hd += kDecodeWarps) {
-            const T* o = out_row<true, T>(a, rw, pc, hd);
-            bool any = false;
-            for (int d = lane; d < a.dv; d += 32) any |= !(to_f32(o[d]) * 0.f == 0.f);
-            if (__any_sync(~0u, any)) attn_row<T>(rw, pc.b, pc.hk * a.group + (pc.h0 + hd) % a.group, (pc.h0 + hd) / a.group);
-          }
+        // Rows that met a hidden value that is not finite: again, key by key. A column per lane.
+        if (__syncthreads_or(bad)) {
+          const bool mine = lane < pc.heads && odd[lane];
+          const RowRule r = row_rule(a, rw, pc, lane);
+          const unsigned again = rows_to_redo<T, true>(rw, pc.b, pc.hk, pc.hi, mine, r.hi, r.doc, 1.f);
+          for (int hd = warp; hd < pc.heads; hd += kDecodeWarps)
+            if ((again >> hd) & 1) attn_row<T, true>(rw, pc.b, pc.hk * a.group + (pc.h0 + hd) % a.group, (pc.h0 + hd) / a.group);
+        }
       }
       return;
     }

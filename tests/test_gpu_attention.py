@@ -253,3 +253,92 @@ def test_items_whose_second_tile_sees_nothing(gpu, docs):
     pick = [0, 1, shape[0] - 1]
     part = {n: (t[pick] if n in ("doc_q", "doc_k") else t) for n, t in kw.items()}
     ref.check(first[pick], ref.attention(q[pick], k[pick], v[pick], **part), v, BF16)
+
+
+LONG = [(1, 4096, 4096, 4, 2, 64, 64), (1, 1500, 2000, 2, 1, 128, 128), (3, 2, 3000, 4, 2, 64, 96), (1, 700, 900, 2, 2, 20, 36)]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("poison", [float("nan"), float("inf")], ids=str)
+@pytest.mark.parametrize("where", ["key", "value"])
+@pytest.mark.parametrize("shape", LONG, ids=lambda s: "x".join(map(str, s)))
+def test_visible_infinities_and_nan_stay_in_their_rows_and_dims(gpu, shape, where, poison, dtype):
+    """A key that is not finite makes every row that sees it NaN; a value that is not finite only its own
+    dimension, in the rows that see it. Rows that share a tile with them are as ever."""
+    B, Lq, Lk, Hq, Hkv, Dk, Dv = shape
+    q, k, v = make(shape, dtype, seed=41, spread=1.0)
+    at, off, d = Lk - Lq + Lq // 3, Lk - Lq, 3
+    s = torch.einsum("bihd,bjhd->bhij", q.double(), k.double().repeat_interleave(Hq // Hkv, 2)) * Dk ** -0.5
+    i, j = torch.arange(Lq, device="cuda")[:, None] + off, torch.arange(Lk, device="cuda")[None, :]
+    w = torch.softmax(s.masked_fill(j > i, float("-inf")), -1)
+    want = torch.einsum("bhij,bjhd->bihd", w, v.double().repeat_interleave(Hq // Hkv, 2)).cpu()
+    hit = torch.zeros(B, Lq, Hq, Dv, dtype=torch.bool)
+    if where == "key":
+        k[:, at] = poison  # with queries of both signs in every dimension: a score of NaN
+        hit[:, at - off:] = True
+    else:
+        v[:, at, :, d] = poison
+        hit[:, at - off:, :, d] = True
+    got = run(q, k, v, {"scale": Dk ** -0.5, "causal": True, "q_offset": off}).cpu().double()
+    sync_check()
+    assert torch.isfinite(got[~hit]).all() and not torch.isfinite(got[hit]).any()
+    clean = torch.where(torch.isfinite(v), v, torch.zeros_like(v))
+    ref.check(torch.where(hit, want, got), want, clean, dtype)
+
+
+@pytest.mark.parametrize("where", ["key", "value"])
+def test_one_nan_holds_up_no_bounded_wait(gpu, where):
+    """16384 queries that all see one NaN, with waits bounded at 50 ms."""
+    shape = (1, 16384, 16384, 4, 1, 128, 128)
+    q, k, v = make(shape, BF16, seed=42)
+    kw = {"scale": 128 ** -0.5, "causal": True}
+    clean = run(q, k, v, kw)
+    (k if where == "key" else v)[:, 0, :, 5] = float("nan")
+    with cb.tuning("CB_TIMEOUT_MS", "50"):
+        got = run(q, k, v, kw)
+        sync_check()
+    if where == "key":
+        assert torch.isnan(got).all()
+    else:
+        assert torch.isnan(got[..., 5]).all()
+        rest = torch.arange(128, device="cuda") != 5
+        assert torch.equal(got[..., rest], clean[..., rest])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_padding_with_nan_in_every_tile(gpu, dtype):
+    """Padding tokens that hold NaN among every 32 keys: no row's tiled sum stands, and each comes out right."""
+    shape = (1, 600, 600, 2, 1, 64, 64)
+    q, k, v = make(shape, dtype, seed=43)
+    doc = (torch.arange(600, device="cuda") // 200).to(torch.int32)
+    doc[::32] = -1
+    doc = doc[None].contiguous()
+    kw = {"scale": 0.125, "doc_q": doc, "doc_k": doc}
+    want = ref.attention(q, k, v, **kw)
+    k[:, ::32], v[:, ::32] = float("nan"), float("nan")
+    out = run(q, k, v, kw)
+    sync_check()
+    ref.check(out, want, torch.where(torch.isfinite(v), v, torch.zeros_like(v)), dtype)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("nan", [False, True], ids=["finite", "one_nan"])
+def test_large_values_under_rising_scores(gpu, nan, dtype):
+    """Scores that rise by 2^40 from the first tiles to the last, over values of 1e30: sums relative to the first
+    tiles' maximum would overflow. With a visible NaN in one dimension the others stay finite all the same."""
+    L, D = 1024, 64
+    q = torch.zeros(1, L, 1, D, device="cuda", dtype=dtype)
+    k = torch.zeros(1, L, 1, D, device="cuda", dtype=dtype)
+    q[..., 0] = 8
+    k[..., 0] = (torch.linspace(0, 28, L, device="cuda") / 8)[None, :, None].to(dtype)
+    v = (ref.randn(1, L, 1, D, seed=44, dtype=F32, device="cuda") * 1e30).to(dtype)
+    want = ref.attention(q, k, v, 1.0)
+    big = v.clone()
+    if nan:
+        v[0, 900, 0, 7] = float("nan")
+    got = run(q, k, v, {"scale": 1.0}).cpu().double()
+    sync_check()
+    if nan:
+        assert torch.isnan(got[..., 7]).all()
+        got[..., 7] = want[..., 7]
+    ref.check(got, want, big, dtype)

@@ -207,13 +207,21 @@ def _init_codes():
     _codes = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16, "i32": torch.int32, "f32": torch.float32}
 
 
-def _stream_of(t, stream):
-    """The stream's handle: `stream`, or the current one of t's device."""
+def _device_of(*tensors):
+    """The CUDA device that the tensors of a call lie on, all of them."""
+    device = tensors[0].get_device()
+    for t in tensors:
+        if t.get_device() != device or device < 0:
+            raise ValueError("the tensors of a GPU call are on one CUDA device, got " + ", ".join(str(t.device) for t in tensors))
+    return device
+
+
+def _stream_of(device, stream):
+    """The stream's handle: `stream`, or the device's current one."""
     if stream is not None:
         return stream.cuda_stream
-    device = t.get_device()
-    if device < 0:
-        raise ValueError("the tensors of a GPU call are on a CUDA device")
+    if _codes is None:
+        _init_codes()
     return _raw_stream(device)
 
 
@@ -245,14 +253,16 @@ def _heads1(t) -> bytes:
     return _HEADS.pack(t.data_ptr(), B, 1, H, D, sb, 0, sh, code)
 
 
-def _device_array(t, name, dtype, shape):
-    """Pointer of a contiguous device tensor ("i32" or "f32") of this shape; None is the null pointer."""
+def _device_array(t, name, dtype, shape, device=None):
+    """Pointer of a contiguous device tensor ("i32" or "f32") of this shape, on `device` (None: any); None is the
+    null pointer."""
     if t is None:
         return 0
     if _codes is None:
         _init_codes()
-    if t.dtype is not _codes[dtype] or t.shape != shape or t.get_device() < 0 or not t.is_contiguous():
-        raise ValueError(f"{name}: a contiguous {_codes[dtype]} device tensor of shape {shape}, got {t.dtype} "
+    at = t.get_device()
+    if t.dtype is not _codes[dtype] or t.shape != shape or at < 0 or device not in (None, at) or not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous {_codes[dtype]} tensor of shape {shape} on the call's device, got {t.dtype} "
                          f"{tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
@@ -269,16 +279,16 @@ class Score:
         self.scale, self.softcap, self.causal, self.q_offset = float(scale), float(softcap), bool(causal), int(q_offset)
         self.slopes, self.prefix_len, self.kv_len, self.doc_q, self.doc_k = slopes, prefix_len, kv_len, doc_q, doc_k
 
-    def view(self, batch, lq, lk, hq) -> bytes:
-        """cb_score for [batch, lq, hq, .] queries over lk keys, packed; checks the arrays' shapes."""
+    def view(self, batch, lq, lk, hq, device=None) -> bytes:
+        """cb_score for [batch, lq, hq, .] queries over lk keys, packed; checks the arrays' shapes and device."""
         slopes, prefix, kv, dq, dk = self.slopes, self.prefix_len, self.kv_len, self.doc_q, self.doc_k
         return _SCORE.pack(self.scale, self.softcap,
-                           0 if slopes is None else _device_array(slopes, "slopes", "f32", (hq,)),
+                           0 if slopes is None else _device_array(slopes, "slopes", "f32", (hq,), device),
                            self.causal, self.q_offset,
-                           0 if prefix is None else _device_array(prefix, "prefix_len", "i32", (batch,)),
-                           0 if kv is None else _device_array(kv, "kv_len", "i32", (batch,)),
-                           0 if dq is None else _device_array(dq, "doc_q", "i32", (batch, lq)),
-                           0 if dk is None else _device_array(dk, "doc_k", "i32", (batch, lk)))
+                           0 if prefix is None else _device_array(prefix, "prefix_len", "i32", (batch,), device),
+                           0 if kv is None else _device_array(kv, "kv_len", "i32", (batch,), device),
+                           0 if dq is None else _device_array(dq, "doc_q", "i32", (batch, lq), device),
+                           0 if dk is None else _device_array(dk, "doc_k", "i32", (batch, lk), device))
 
 
 class PagedCache:
@@ -292,9 +302,9 @@ class PagedCache:
             raise ValueError("k_pages and v_pages: the same pages, slots, heads and dtype")
         if k_pages.stride(3) != 1 or v_pages.stride(3) != 1:
             raise ValueError("the last dim of the pages is contiguous")
-        if str(table.dtype) != "torch.int32" or table.dim() != 2 or not table.is_cuda or \
-                (table.shape[1] > 1 and table.stride(1) != 1):
+        if str(table.dtype) != "torch.int32" or table.dim() != 2 or (table.shape[1] > 1 and table.stride(1) != 1):
             raise ValueError("table: an int32 device tensor [B, max_pages] with contiguous rows")
+        _device_of(k_pages, v_pages, table)
         self.k_pages, self.v_pages, self.table = k_pages, v_pages, table
         P, page, H, Dk = k_pages.shape
         self.view = CbPagedCache(k_pages.data_ptr(), v_pages.data_ptr(), P, page, H, Dk, v_pages.shape[3],
@@ -511,8 +521,9 @@ def attention(q, k, v, out, score, stream=None):
     out [B, Lq, Hq, Dv] (any strides, the last dim contiguous; all float32 or all bfloat16); score: a
     Score.  Slices of a projection's output are read in place."""
     B, lq, hq, _ = q.shape
-    st = (_lib or load()).cb_attention(heads(q), heads(k), heads(v), score.view(B, lq, k.shape[1], hq), heads(out),
-                                       _stream_of(q, stream))
+    device = _device_of(q, k, v, out)
+    st = (_lib or load()).cb_attention(heads(q), heads(k), heads(v), score.view(B, lq, k.shape[1], hq, device), heads(out),
+                                       _stream_of(device, stream))
     if st:
         _check(st, "cb_attention")
     return out
@@ -522,8 +533,10 @@ def cache_append(k_new, v_new, cache, pos, count=None, stream=None):
     """cb_cache_append: tokens t < count[b] of k_new [B, T, H, Dk] and v_new [B, T, H, Dv] become tokens
     pos[b] + t of the cache's sequences.  pos, count: int32 [B] (count None: all T)."""
     kv, vv, B = heads(k_new), heads(v_new), k_new.shape[0]
-    st = (_lib or load()).cb_cache_append(kv, vv, _device_array(pos, "pos", "i32", (B,)),
-                                          _device_array(count, "count", "i32", (B,)), cache.ref, _stream_of(k_new, stream))
+    device = _device_of(k_new, v_new, cache.table)
+    st = (_lib or load()).cb_cache_append(kv, vv, _device_array(pos, "pos", "i32", (B,), device),
+                                          _device_array(count, "count", "i32", (B,), device), cache.ref,
+                                          _stream_of(device, stream))
     if st:
         _check(st, "cb_cache_append")
 
@@ -541,10 +554,11 @@ def attention_decode(q, cache, length, out, workspace, scale, softcap=0.0, slope
     workspace: a uint8 device tensor of attention_decode_workspace bytes."""
     qv, ov = _heads1(q), _heads1(out)
     B, hq, _ = q.shape
+    device = _device_of(q, out, cache.table, workspace)
     st = (_lib or load()).cb_attention_decode(
-        qv, cache.ref, _device_array(length, "length", "i32", (B,)), _device_array(first, "first", "i32", (B,)), scale,
-        softcap, _device_array(slopes, "slopes", "f32", (hq,)), ov, workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _stream_of(q, stream))
+        qv, cache.ref, _device_array(length, "length", "i32", (B,), device), _device_array(first, "first", "i32", (B,), device),
+        scale, softcap, _device_array(slopes, "slopes", "f32", (hq,), device), ov, workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _stream_of(device, stream))
     if st:
         _check(st, "cb_attention_decode")
     return out

@@ -146,3 +146,61 @@ def test_binding_checks_index_tensors(cblib):
         cblib.heads(torch.zeros(1, 2, 3, 8).transpose(2, 3))
     with pytest.raises(ValueError):
         cblib.PagedCache(torch.zeros(2, 4, 1, 8), torch.zeros(2, 4, 2, 8), torch.zeros(1, 1, dtype=torch.int32))
+
+
+class OnDevice:
+    """Host tensors that say they lie on a CUDA device, and a library that must not be reached."""
+
+    def __init__(self, monkeypatch, cblib):
+        import torch
+
+        class Claims(torch.Tensor):
+            def get_device(self):
+                return self.claimed
+
+        def make(*shape, dtype=torch.bfloat16, device=0):
+            t = torch.zeros(*shape, dtype=dtype).as_subclass(Claims)
+            t.claimed = device
+            return t
+
+        class Library:
+            def __getattr__(self, name):
+                def called(*args):
+                    raise AssertionError(f"{name} was called")
+                return called
+
+        class Stream:
+            cuda_stream = 0
+
+        self.make, self.i32, self.f32, self.stream = make, torch.int32, torch.float32, Stream()
+        monkeypatch.setattr(cblib, "_lib", Library())
+
+
+@pytest.mark.parametrize("device", [-1, 1], ids=["host", "another"])
+def test_binding_checks_every_tensors_device(cblib, monkeypatch, device):
+    """A tensor on the host, or on another device than the others, is refused before the library is called, also
+    where a stream is given."""
+    on = OnDevice(monkeypatch, cblib)
+    s = on.stream
+
+    def refused(call, shapes):
+        tensors = {n: on.make(*sh, dtype=dt) for n, (sh, dt) in shapes.items()}
+        with pytest.raises(AssertionError, match="was called"):
+            call(tensors)  # all on one device: the call goes on to the library
+        for n, (sh, dt) in shapes.items():
+            with pytest.raises(ValueError):
+                call({**tensors, n: on.make(*sh, dtype=dt, device=device)})
+
+    import torch
+    B, h = (2, 3, 4, 64), torch.bfloat16
+    refused(lambda t: cblib.attention(t["q"], t["k"], t["v"], t["out"],
+                                      cblib.Score(0.1, kv_len=t["kv"], slopes=t["slopes"]), stream=s),
+            {"q": (B, h), "k": (B, h), "v": (B, h), "out": (B, h), "kv": ((2,), on.i32), "slopes": ((4,), on.f32)})
+    pages, table = ((5, 16, 4, 64), h), ((2, 3), on.i32)
+    refused(lambda t: cblib.cache_append(t["k"], t["v"], cblib.PagedCache(t["kp"], t["vp"], t["table"]), t["pos"],
+                                         count=t["count"], stream=s),
+            {"k": (B, h), "v": (B, h), "kp": pages, "vp": pages, "table": table, "pos": ((2,), on.i32), "count": ((2,), on.i32)})
+    refused(lambda t: cblib.attention_decode(t["q"], cblib.PagedCache(t["kp"], t["vp"], t["table"]), t["n"], t["out"],
+                                             t["ws"], 0.1, slopes=t["slopes"], first=t["first"], stream=s),
+            {"q": ((2, 4, 64), h), "kp": pages, "vp": pages, "table": table, "n": ((2,), on.i32), "out": ((2, 4, 64), h),
+             "ws": ((4096,), torch.uint8), "slopes": ((4,), on.f32), "first": ((2,), on.i32)})

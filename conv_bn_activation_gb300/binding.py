@@ -551,10 +551,12 @@ def attention_decode_workspace(q, cache) -> int:
 def attention_decode(q, cache, length, out, workspace, scale, softcap=0.0, slopes=None, first=None, stream=None):
     """cb_attention_decode: one new token per sequence, q [B, Hq, Dk] and out [B, Hq, Dv], over the cache's
     tokens first[b] <= j < length[b] (int32 [B]; first None: 0), the query at position length[b] - 1.
-    workspace: a uint8 device tensor of attention_decode_workspace bytes."""
+    workspace: a contiguous uint8 device tensor of attention_decode_workspace bytes."""
     qv, ov = _heads1(q), _heads1(out)
     B, hq, _ = q.shape
     device = _device_of(q, out, cache.table, workspace)
+    if not workspace.is_contiguous():
+        raise ValueError("workspace: a contiguous device tensor")
     st = (_lib or load()).cb_attention_decode(
         qv, cache.ref, _device_array(length, "length", "i32", (B,), device), _device_array(first, "first", "i32", (B,), device),
         scale, softcap, _device_array(slopes, "slopes", "f32", (hq,), device), ov, workspace.data_ptr(),

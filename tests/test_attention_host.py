@@ -204,3 +204,13 @@ def test_binding_checks_every_tensors_device(cblib, monkeypatch, device):
                                              t["ws"], 0.1, slopes=t["slopes"], first=t["first"], stream=s),
             {"q": ((2, 4, 64), h), "kp": pages, "vp": pages, "table": table, "n": ((2,), on.i32), "out": ((2, 4, 64), h),
              "ws": ((4096,), torch.uint8), "slopes": ((4,), on.f32), "first": ((2,), on.i32)})
+
+
+def test_binding_wants_a_contiguous_workspace(cblib, monkeypatch):
+    import torch
+    on = OnDevice(monkeypatch, cblib)
+    cache = cblib.PagedCache(on.make(5, 16, 4, 64), on.make(5, 16, 4, 64), on.make(2, 3, dtype=on.i32))
+    q, n, ws = on.make(2, 4, 64), on.make(2, dtype=on.i32), on.make(4096, 2, dtype=torch.uint8)[:, 0]
+    ws.claimed = 0
+    with pytest.raises(ValueError):
+        cblib.attention_decode(q, cache, n, on.make(2, 4, 64), ws, 0.1, stream=on.stream)

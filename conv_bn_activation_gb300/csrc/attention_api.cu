@@ -33,30 +33,34 @@ bool pieces16(const void* data, cb_dtype dt, int dim, long long s0, long long s1
 }
 bool pieces16(const cb_heads* t) { return pieces16(t->data, t->dtype, t->dim, t->stride_b, t->stride_l, t->stride_h); }
 
-void range(const cb_heads* t, uintptr_t* lo, uintptr_t* hi) {
-  const long long last =
-      (t->batch - 1LL) * t->stride_b + (t->len - 1LL) * t->stride_l + (t->heads - 1LL) * t->stride_h + t->dim;
-  *lo = reinterpret_cast<uintptr_t>(t->data);
-  *hi = *lo + static_cast<uintptr_t>(last) * elem_bytes(t->dtype);
+// Elements from a row's, a sequence's and a view's first to one past its last.
+long long row_extent(const cb_heads* t) { return (t->heads - 1LL) * t->stride_h + t->dim; }
+long long seq_extent(const cb_heads* t) { return (t->len - 1LL) * t->stride_l + row_extent(t); }
+long long extent(const cb_heads* t) { return (t->batch - 1LL) * t->stride_b + seq_extent(t); }
+
+// Whether [0, a) and [d, d + b), both repeated every `period`, stay apart.
+bool apart(long long period, long long a, long long b, long long d) {
+  if (period <= 0 || a > period) return false;
+  const long long at = (d % period + period) % period;
+  return at >= a && at + b <= period;
 }
 
-// True if the views may share an element.  Two views with the same row and
-// sequence strides whose heads lie in disjoint parts of a row share none (a
-// slice of a wider buffer beside another), though their ranges interleave.
+// True if the views, of one dtype, may share an element. Views whose ranges
+// interleave share none if one's rows or sequences lie in the gaps between the
+// other's, at the same strides (slices of a wider buffer), or one lies in a
+// single gap.
 bool overlap(const cb_heads* a, const cb_heads* b) {
   if (empty(a) || empty(b)) return false;
-  uintptr_t alo, ahi, blo, bhi;
-  range(a, &alo, &ahi);
-  range(b, &blo, &bhi);
-  if (!(alo < bhi && blo < ahi)) return false;
-  if (a->dtype == b->dtype && a->stride_b == b->stride_b && a->stride_l == b->stride_l && a->stride_l > 0 &&
-      a->stride_b % a->stride_l == 0 && (a->batch == 1 || a->stride_b >= a->stride_l * a->len)) {
-    const uintptr_t base = alo < blo ? alo : blo, eb = elem_bytes(a->dtype);
-    const long long da = static_cast<long long>((alo - base) / eb), db = static_cast<long long>((blo - base) / eb);
-    const long long ea = da + (a->heads - 1LL) * a->stride_h + a->dim, ebd = db + (b->heads - 1LL) * b->stride_h + b->dim;
-    if (ea <= a->stride_l && ebd <= a->stride_l && (ea <= db || ebd <= da)) return false;
-  }
-  return true;
+  const long long eb = static_cast<long long>(elem_bytes(a->dtype));
+  const long long d = static_cast<long long>(reinterpret_cast<uintptr_t>(b->data) - reinterpret_cast<uintptr_t>(a->data));
+  if (d >= extent(a) * eb || -d >= extent(b) * eb) return false;
+  auto rows_repeat = [](const cb_heads* t) { return t->batch == 1 || (t->stride_l > 0 && t->stride_b % t->stride_l == 0); };
+  if (a->stride_l == b->stride_l && rows_repeat(a) && rows_repeat(b) &&
+      apart(a->stride_l * eb, row_extent(a) * eb, row_extent(b) * eb, d))
+    return false;
+  if (a->stride_b == b->stride_b && apart(a->stride_b * eb, seq_extent(a) * eb, seq_extent(b) * eb, d)) return false;
+  return !apart(a->stride_b * eb, seq_extent(a) * eb, extent(b) * eb, d) &&
+         !apart(b->stride_b * eb, seq_extent(b) * eb, extent(a) * eb, -d);
 }
 
 bool cache_ok(const cb_paged_cache* c) {
@@ -73,6 +77,13 @@ bool cache_ok(const cb_paged_cache* c) {
 bool pieces16(const cb_paged_cache* c) {
   return pieces16(c->k, c->dtype, c->dim_k, c->k_stride_page, c->k_stride_slot, c->k_stride_head) &&
          pieces16(c->v, c->dtype, c->dim_v, c->v_stride_page, c->v_stride_slot, c->v_stride_head);
+}
+
+// Whether a view may share an element with the cache's pages.
+bool overlap(const cb_heads* t, const cb_paged_cache* c) {
+  const cb_heads k{c->k, c->num_pages, c->page_size, c->heads, c->dim_k, c->k_stride_page, c->k_stride_slot, c->k_stride_head, c->dtype};
+  const cb_heads v{c->v, c->num_pages, c->page_size, c->heads, c->dim_v, c->v_stride_page, c->v_stride_slot, c->v_stride_head, c->dtype};
+  return overlap(&k, t) || overlap(&v, t);
 }
 
 PagedArgs paged_args(const cb_paged_cache* c) {
@@ -231,7 +242,7 @@ cb_status cb_cache_append(const cb_heads* k_new, const cb_heads* v_new, const in
                         static_cast<const void*>(cache->k), static_cast<const void*>(cache->v)})
     if (!elem_aligned(p, cache->dtype)) return CB_ERR_ALIGNMENT;
   if (empty(k_new)) return CB_OK;
-  if (!pos) return CB_ERR_INVALID_ARG;
+  if (!pos || overlap(k_new, cache) || overlap(v_new, cache)) return CB_ERR_INVALID_ARG;
   AppendArgs a{};
   int sms = 0;
   const cb_status st = host_device(&sms, &a.err);
@@ -271,7 +282,7 @@ cb_status cb_attention_decode(const cb_heads* q, const cb_paged_cache* cache, co
                         static_cast<const void*>(cache->k), static_cast<const void*>(cache->v)})
     if (!elem_aligned(p, q->dtype)) return CB_ERR_ALIGNMENT;
   if (q->batch == 0) return CB_OK;
-  if (!length || !workspace) return CB_ERR_INVALID_ARG;
+  if (!length || !workspace || overlap(out, cache)) return CB_ERR_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(workspace) % 256 != 0) return CB_ERR_ALIGNMENT;
   DecodePlan p;
   st = plan_decode(q, cache, &p);

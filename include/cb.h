@@ -464,8 +464,8 @@ typedef struct {
  * (DEVICE int [batch], clamped to [0, len]; NULL: every token of k_new),
  * becomes token pos[b] + t.  pos: DEVICE int [batch]; a negative position is
  * refused like a bad table entry.  k_new: [batch, T, heads, dim_k], v_new:
- * [batch, T, heads, dim_v], of the cache's dtype.  Two tokens of one call
- * must not share a slot.
+ * [batch, T, heads, dim_v], of the cache's dtype, overlapping no page.  Two
+ * tokens of one call must not share a slot.
  */
 cb_status cb_cache_append(const cb_heads* k_new, const cb_heads* v_new, const int* pos, const int* count,
                           const cb_paged_cache* cache, void* stream);
@@ -484,7 +484,8 @@ cb_status cb_attention_decode_workspace(const cb_heads* q, const cb_paged_cache*
  * (DEVICE int [batch]; first NULL: 0; length clamped to what max_pages
  * pages hold; an empty range gives zeros).  Scores as in cb_score with the
  * query at position length[b] - 1: scale, softcap, and slopes (NULL or
- * DEVICE fp32 [Hq]) times length[b] - 1 - j.  The new token's own key and
+ * DEVICE fp32 [Hq]) times length[b] - 1 - j.  out overlaps neither q nor a
+ * page.  The new token's own key and
  * value are in the cache already (cb_cache_append).  Hq a multiple of the
  * cache's heads; dim_k and dim_v at most 128, batch at most 4096 (else
  * CB_ERR_UNSUPPORTED).  The tokens of all sequences are dealt evenly over

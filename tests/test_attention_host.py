@@ -214,3 +214,30 @@ def test_binding_wants_a_contiguous_workspace(cblib, monkeypatch):
     ws.claimed = 0
     with pytest.raises(ValueError):
         cblib.attention_decode(q, cache, n, on.make(2, 4, 64), ws, 0.1, stream=on.stream)
+
+
+FAR, BYTES = 1 << 26, 10 * 16 * 2 * 64 * 2  # BYTES: of the cache's key or value pages
+
+
+def test_append_refuses_tokens_that_lie_in_the_pages(cblib):
+    k, v = heads(cblib, h=2, data=DATA + FAR), heads(cblib, h=2, data=DATA + 2 * FAR)
+    for at in (DATA, DATA + BYTES - 2, DATA - 2, DATA + (1 << 24) + 4096):
+        new = heads(cblib, h=2, data=at)
+        assert append(cblib, k=new, v=v) == cblib.ERR_INVALID_ARG, at
+        assert append(cblib, k=k, v=new) == cblib.ERR_INVALID_ARG, at
+
+
+def test_decode_refuses_an_output_in_the_pages(cblib):
+    """With no workspace: what is not refused for its place is refused for that, and nothing is launched."""
+    page = 16 * 2 * 64  # elements of a page; strided ones have the next three pages' room free
+    q, wide = heads(cblib, l=1, data=DATA + FAR), cache(cblib, k_stride_page=4 * page, v_stride_page=4 * page)
+    wide.v = DATA + 2 * page
+    behind = DATA + 2 * (5 * 4 * page + 2 * page)  # behind the values of page 5
+
+    def status(at, c=None):
+        return decode(cblib, q=q, c=c, out=heads(cblib, l=1, data=at), size=0)
+
+    for at in (DATA, DATA + BYTES - 2, DATA + (1 << 24) + 4096):
+        assert status(at) == cblib.ERR_INVALID_ARG, at
+    assert status(behind - 2, wide) == cblib.ERR_INVALID_ARG
+    assert status(DATA + BYTES) != cblib.ERR_INVALID_ARG and status(behind, wide) != cblib.ERR_INVALID_ARG

@@ -209,3 +209,18 @@ def test_dims_between_64_and_128(gpu, dk, dv, Hq, Hkv, lens):
     got = run(q, k, v, table, n, scale=dk ** -0.5)
     sync_check()
     ref.check(got, ref.decode(q, k, v, table, n, dk ** -0.5), finite(v), BF16)
+
+
+def test_append_from_another_layers_pages(gpu):
+    """Two layers' pages in turn in one buffer: one layer's tokens, as a view with the pages' strides, are appended
+    to the other's."""
+    P, page, H, D = 6, 16, 2, 64
+    g = torch.Generator().manual_seed(1)
+    buf = torch.randn(P, 4, page, H, D, generator=g).to("cuda", BF16)  # k and v of layer 0, then of layer 1
+    want = buf.clone()
+    want[[3, 1], :2] = buf[[0, 1], 2:]
+    table = torch.tensor([[3], [1]], dtype=torch.int32, device="cuda")
+    cb.cache_append(buf[:2, 2], buf[:2, 3], cb.PagedCache(buf[:, 0], buf[:, 1], table),
+                    torch.zeros(2, dtype=torch.int32, device="cuda"))
+    sync_check()
+    assert torch.equal(buf, want)

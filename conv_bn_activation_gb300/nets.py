@@ -236,7 +236,10 @@ class MapReader:
     step(tok): one further token [B, C] per sequence, which sees the map, the tokens before it and itself.
     Both are qkv (1x1 conv + folded BN), attention, out (1x1 conv + folded BN) plus the input, on buffers
     made here, and may be captured in a CUDA graph: the lengths live on the device.  `tokens`: how many
-    steps the cache has room for; a page holds `page` tokens."""
+    steps the cache has room for (at least: the last page is used up); a page holds `page` tokens.  A step
+    that the cache has no room for raises ValueError.  Replays of a captured step are not seen here: past
+    the room their token is not stored, and cb.get_device_error() says so; after a captured read no step is
+    refused here."""
 
     def __init__(self, params, batch, hw, tokens, page=16, device="cuda", dtype=torch.float32):
         self.hq, self.hkv, self.dim = params["heads"], params["kv_heads"], params["dim"]
@@ -251,6 +254,7 @@ class MapReader:
         self.map_out, self.tok_out = torch.empty(batch, H, W, C, **kw), torch.empty(batch, 1, 1, C, **kw)
         pages = -(-(H * W + tokens) // page)
         self.pages = [torch.zeros(batch * pages, page, self.hkv, self.dim, **kw) for _ in range(2)]
+        self.room, self.filled = pages * page, 0  # tokens per sequence; filled None: replays of `read` are not seen
         self.table = torch.arange(batch * pages, dtype=torch.int32, device=device).view(batch, pages)
         self.cache = cb.PagedCache(*self.pages, self.table)
         self.start = torch.zeros(batch, dtype=torch.int32, device=device)
@@ -265,7 +269,13 @@ class MapReader:
         rows = qkv.view(self.batch, -1, hq + 2 * hkv, d)
         return rows[:, :, :hq], rows[:, :, hq:hq + hkv], rows[:, :, hq + hkv:]
 
+    @staticmethod
+    def _capturing(stream):
+        with torch.cuda.stream(stream):  # None: the current one
+            return torch.cuda.is_current_stream_capturing()
+
     def read(self, x, stream=None):
+        self.filled = None if self.filled is None or self._capturing(stream) else self.hw[0] * self.hw[1]
         self.qkv(x, self.map_qkv, stream=stream)
         q, k, v = self._split(self.map_qkv)
         cb.attention(q, k, v, self.map_ctx.view(*q.shape), self.score, stream=stream)
@@ -276,6 +286,10 @@ class MapReader:
         return self.map_out
 
     def step(self, tok, stream=None):
+        if self.filled is not None and not self._capturing(stream):
+            if self.filled >= self.room:
+                raise ValueError(f"the cache has room for {self.room} tokens of a sequence, map included")
+            self.filled += 1
         x = tok.view(self.batch, 1, 1, -1)
         self.qkv(x, self.tok_qkv, stream=stream)
         q, k, v = self._split(self.tok_qkv)

@@ -88,3 +88,49 @@ def test_graph_and_stream_match_eager(gpu, dtype):
         got.append(net.tok_out.view(B, C).clone())
     sync_check()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("hw,steps,page", [((4, 4), 0, 16), ((3, 3), 3, 4), ((5, 7), 2, 16)], ids=str)
+def test_a_step_past_the_room_is_refused(gpu, hw, steps, page):
+    """As many steps as the pages hold, then ValueError and nothing changed; a new map starts over."""
+    net = MapReader(synthetic.map_reader_params(), 2, hw, steps, page=page, dtype=BF16)
+    x, tok = ref.randn(2, *hw, 64, seed=1, dtype=BF16, device="cuda"), ref.randn(2, 64, seed=2, dtype=BF16, device="cuda")
+    n = hw[0] * hw[1]
+    room = -(-(n + steps) // page) * page - n
+    assert room >= steps
+    for stream in (None, torch.cuda.Stream()):
+        torch.cuda.synchronize()
+        net.read(x, stream=stream)
+        for _ in range(room):
+            net.step(tok, stream=stream)
+        torch.cuda.synchronize()
+        before = net.tok_out.clone()
+        with pytest.raises(ValueError):
+            net.step(tok, stream=stream)
+        sync_check()
+        assert net.length.tolist() == [n + room] * 2 and torch.equal(net.tok_out, before)
+
+
+def test_the_room_leaves_captured_calls_alone(gpu):
+    """Capturing a step takes no room; after a captured read, whose replays start over, no step is refused."""
+    hw, page = (4, 4), 16
+    net = MapReader(synthetic.map_reader_params(), 2, hw, 16, page=page, dtype=BF16)
+    x, tok = ref.randn(2, *hw, 64, seed=1, dtype=BF16, device="cuda"), ref.randn(2, 64, seed=2, dtype=BF16, device="cuda")
+    net.read(x)
+    net.step(tok)
+    for _ in range(20):
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            net.step(tok)
+    for _ in range(15):
+        net.step(tok)
+    with pytest.raises(ValueError):
+        net.step(tok)
+    read = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(read):
+        net.read(x)
+    for _ in range(3):
+        read.replay()
+        for _ in range(16):
+            net.step(tok)
+    sync_check()
+    assert net.length.tolist() == [32, 32]

@@ -36,7 +36,7 @@ __device__ __forceinline__ SeqSpan seq_span(const DecodeArgs& a, int b) {
   s.lo = a.first ? max(a.first[b], 0) : 0;
   s.hi = s.len;
   s.t0 = s.lo / kDecodeTile;
-  s.tiles = s.lo < s.hi ? (s.hi + kDecodeTile - 1) / kDecodeTile - s.t0 : 0;
+  s.tiles = s.lo < s.hi ? (s.hi - 1) / kDecodeTile + 1 - s.t0 : 0;  // hi may be 2^31 - 1
   s.dealt = s.tiles > 0 ? s.tiles + a.item_cost : 0;
   return s;
 }

@@ -228,16 +228,18 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas_per_sm(C::DK, C::D
       long long k, v;
       int doc;  // contiguous rows: the key's document
     };
-    int j = base + lane % kStep, pg = C::kRows ? 0 : j / a.cache.page_size, slot = C::kRows ? 0 : j - pg * a.cache.page_size;
+    // j is unsigned: a token looked up past the piece's end may be past 2^31
+    unsigned j = base + lane % kStep;
+    int pg = C::kRows ? 0 : static_cast<int>(j) / a.cache.page_size, slot = C::kRows ? 0 : static_cast<int>(j) - pg * a.cache.page_size;
     auto lookup = [&](int step) {  // once for each step, in order
       Rows r{-1, -1, -1};
-      if (step < steps && j >= pc.lo && j < pc.hi) {
+      if (step < steps && j >= static_cast<unsigned>(pc.lo) && j < static_cast<unsigned>(pc.hi)) {
         if constexpr (C::kRows) {
           r.k = (pc.b * a.cache.ks_p + j * a.cache.ks_t) * kEl;
           r.v = (pc.b * a.cache.vs_p + j * a.cache.vs_t) * kEl;
           if (rw.doc_k) r.doc = rw.doc_k[static_cast<long long>(pc.b) * rw.Lk + j];
         } else {
-          if (!kEager) pg = j / a.cache.page_size, slot = j - pg * a.cache.page_size;
+          if (!kEager) pg = static_cast<int>(j) / a.cache.page_size, slot = static_cast<int>(j) - pg * a.cache.page_size;
           const long long page = checked_page(a, pc.b, pg);
           if (page >= 0) {
             r.k = (page * a.cache.ks_p + slot * a.cache.ks_t) * kEl;

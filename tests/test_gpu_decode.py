@@ -224,3 +224,23 @@ def test_append_from_another_layers_pages(gpu):
                     torch.zeros(2, dtype=torch.int32, device="cuda"))
     sync_check()
     assert torch.equal(buf, want)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("dims", [(64, 64), (7, 5)], ids=str)
+def test_lengths_near_the_largest_int(gpu, dims, dtype):
+    """A table of 2^31 - 2 tokens (one page, named everywhere), of which the query sees the last hundred."""
+    page, pages = 99962, 21483
+    room = page * pages
+    assert room == 2 ** 31 - 2
+    k = ref.randn(1, page, 1, dims[0], seed=1, dtype=dtype, device="cuda")
+    v = ref.randn(1, page, 1, dims[1], seed=2, dtype=dtype, device="cuda")
+    table = torch.zeros(1, pages, dtype=torch.int32, device="cuda")
+    q = ref.randn(1, 4, dims[0], seed=3, dtype=dtype, device="cuda")
+    kw = {"scale": dims[0] ** -0.5, "slopes": ref.alibi_slopes(4, "cuda")}
+    n = torch.tensor([room], dtype=torch.int32, device="cuda")
+    got = run(q, k, v, table, n, first=n - 100, **kw)
+    sync_check()
+    last = torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+    want = ref.decode(q, k[:, -100:], v[:, -100:], last, torch.tensor([100]), **kw)
+    ref.check(got, want, v, dtype)

@@ -342,3 +342,45 @@ def test_large_values_under_rising_scores(gpu, nan, dtype):
         assert torch.isnan(got[..., 7]).all()
         got[..., 7] = want[..., 7]
     ref.check(got, want, big, dtype)
+
+
+@pytest.mark.parametrize("sorted_ids", [True, False], ids=["sorted", "mixed"])
+def test_documents_over_more_keys_than_kept_ranges(gpu, sorted_ids):
+    """70000 keys: more key tiles than whose document ranges are kept at once."""
+    B, Lq, Lk, H, D = 1, 300, 70000, 2, 64
+    q, k, v = make((B, Lq, Lk, H, 1, D, D), BF16, seed=6, spread=1.0)
+    j = torch.arange(Lk, device="cuda")
+    doc_k = j // 997 if sorted_ids else (j // 128 * 7919) % 71
+    doc_k = torch.where(j % 1009 == 5, -1, doc_k).to(torch.int32)[None].contiguous()
+    doc_q = (torch.arange(Lq, device="cuda") // 50 * 11).to(torch.int32)[None].contiguous()
+    doc_q[0, 120:130] = -1
+    kw = {"scale": 0.125, "doc_q": doc_q, "doc_k": doc_k, "kv_len": torch.tensor([69990], dtype=torch.int32, device="cuda")}
+    out = run(q, k, v, kw)
+    sync_check()
+    s = torch.einsum("ihd,jd->hij", q[0].double(), k[0, :, 0].double()) * 0.125
+    keep = (doc_q[0][:, None] == doc_k[0][None, :]) & (doc_q[0] >= 0)[:, None] & (j < 69990)[None, :]
+    w = torch.exp(s - s.masked_fill(~keep, -1e30).amax(-1, keepdim=True)).masked_fill(~keep, 0.0)
+    want = torch.einsum("hij,jd->ihd", w / w.sum(-1, keepdim=True).clamp(min=1e-300), v[0, :, 0].double())
+    ref.check(out[0], want.cpu(), v, BF16)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(2, 400, 400, 4, 2, 64, 64), (2, 3, 500, 4, 2, 64, 128), (4, 260, 300, 4, 1, 128, 128)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_orders_and_broadcast_inputs(gpu, shape, dtype):
+    """Whole 16-byte pieces in other orders than [B, L, H, D]: head-major, sequence-major, keys and values that
+    all sequences or all key heads share (strides of zero)."""
+    B, Lq, Lk, Hq, Hkv, Dk, Dv = shape
+    q, k, v = make(shape, dtype, seed=31)
+    kw = {"scale": Dk ** -0.5, "causal": True, "q_offset": Lk - Lq}
+    want = run(q, k, v, kw)
+    heads_first = [t.transpose(1, 2).contiguous().transpose(1, 2) for t in (q, k, v)]
+    out = torch.full((B, Hq, Lq, Dv), float("nan"), dtype=dtype, device="cuda").transpose(1, 2)
+    assert torch.equal(run(*heads_first, kw, out=out), want)
+    rows_first = [t.transpose(0, 1).contiguous().transpose(0, 1) for t in (q, k, v)]
+    out = torch.full((Lq, B, Hq, Dv), float("nan"), dtype=dtype, device="cuda").transpose(0, 1)
+    assert torch.equal(run(*rows_first, kw, out=out), want)
+    for wide, narrow in (((B, Lk, Hkv), (1, Lk, Hkv)), ((B, Lk, Hkv), (B, Lk, 1))):
+        ke, ve = (t[:narrow[0], :, :narrow[2]].expand(*wide, -1) for t in (k, v))
+        assert torch.equal(run(q, ke, ve, kw), run(q, ke.contiguous(), ve.contiguous(), kw))
+    sync_check()

@@ -244,3 +244,35 @@ def test_lengths_near_the_largest_int(gpu, dims, dtype):
     last = torch.zeros(1, 1, dtype=torch.int32, device="cuda")
     want = ref.decode(q, k[:, -100:], v[:, -100:], last, torch.tensor([100]), **kw)
     ref.check(got, want, v, dtype)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("dims", [(64, 64), (7, 5)], ids=str)
+@pytest.mark.parametrize("wide", [False, True], ids=["tight_table", "wide_table"])
+@pytest.mark.parametrize("B", [129, 300, 1000])
+def test_more_sequences_than_threads(gpu, B, wide, dims, dtype):
+    """Several sequences per thread where the prefix over the lengths is taken; empty ones among them."""
+    lens = [(37 * b) % 150 if b % 5 else 0 for b in range(B)]
+    k, v, table = paged(lens, 16, 1, *dims, dtype, seed=7)
+    if wide:
+        table = torch.cat([table, torch.full((B, 3000), -1, dtype=torch.int32, device="cuda")], 1)
+    q = ref.randn(B, 2, dims[0], seed=8, dtype=dtype, device="cuda")
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    got = run(q, k, v, table, n, scale=dims[0] ** -0.5)
+    sync_check()
+    ref.check(got, ref.decode(q, k.cpu(), v.cpu(), table.cpu(), lens, dims[0] ** -0.5), finite(v), dtype)
+
+
+@pytest.mark.parametrize("lens", [[40, 0, 129], [3000, 1, 2100, 777]], ids=["whole", "runs"])
+@pytest.mark.parametrize("Hq,Hkv", [(2, 2), (6, 2), (20, 2)], ids=["one_head", "three_heads", "ten_heads"])
+@pytest.mark.parametrize("dk,dv", [(96, 96), (72, 100), (36, 40), (128, 72), (96, 64)])
+def test_fp32_dims_between_the_kernels(gpu, dk, dv, Hq, Hkv, lens):
+    """test_dims_between_64_and_128 for fp32, and for fewer than 64."""
+    k, v, table = paged(lens, 16, Hkv, dk, dv, F32, seed=dk + dv)
+    if len(lens) == 4:
+        table = torch.cat([table, torch.full((4, 3000), -1, dtype=torch.int32, device="cuda")], 1)
+    q = ref.randn(len(lens), Hq, dk, seed=5, dtype=F32, device="cuda") * 2
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    got = run(q, k, v, table, n, scale=dk ** -0.5)
+    sync_check()
+    ref.check(got, ref.decode(q, k, v, table, n, dk ** -0.5), finite(v), F32)

@@ -107,3 +107,34 @@ def test_decode_with_caps_at_the_ends_of_fp32(gpu, dims, softcap, dtype):
     got = run_decode(q, k, v, table, n, **kw)
     sync_check()
     ref.check(got, ref.decode(q, k, v, table, n, **kw), finite(v), dtype)
+
+
+@pytest.mark.parametrize("softcap", [30.0, 50.0])
+@pytest.mark.parametrize("causal", [False, True], ids=["full", "causal"])
+@pytest.mark.parametrize("bias", [False, True], ids=["flat", "bias"])
+@pytest.mark.parametrize("shape", [(1, 384, 640, 2, 1, 64, 64), (2, 512, 512, 4, 2, 128, 128), (1, 700, 700, 2, 2, 32, 128),
+                                   (1, 256, 900, 4, 4, 128, 64)], ids=lambda s: "x".join(map(str, s)))
+def test_whole_tiles_of_ordinary_caps(gpu, shape, bias, causal, softcap):
+    """Scores of standard deviation 3 under caps of 30 and 50: unmasked tiles of 128 keys in which every score is
+    far enough from the cap for the tensor-core kernel's polynomial, with and without a bias."""
+    q, k, v = tokens(shape, BF16, seed=11)
+    kw = {"scale": shape[5] ** -0.5, "softcap": softcap, "causal": causal}
+    if bias:
+        kw["slopes"] = ref.alibi_slopes(shape[3], "cuda")
+    ref.check(attend(q, k, v, **kw), definition(q, k, v, **kw), v, BF16)
+
+
+@pytest.mark.parametrize("bias", [False, True], ids=["flat", "bias"])
+@pytest.mark.parametrize("lead", [False, True], ids=["near_first", "far_first"])
+def test_rows_that_meet_both_forms_of_the_cap(gpu, lead, bias):
+    """Key tiles whose scores all stay below 0.8 of the cap beside tiles whose scores pass it."""
+    shape = (1, 256, 768, 2, 1, 64, 64)
+    q, k, v = tokens(shape, BF16, seed=21, spread=1.5)
+    big = torch.arange(768, device="cuda") // 128 % 2 == int(lead)
+    k[:, big] *= 4
+    kw = {"scale": 0.125, "softcap": 12.0}
+    y = torch.einsum("bihd,bjhd->bhij", q.double(), k.double().repeat_interleave(2, 2)).abs() * 0.125 / 12.0
+    assert float(y[..., ~big].max()) < 0.79 and float(y[..., big].max()) > 1.0
+    if bias:
+        kw["slopes"] = ref.alibi_slopes(2, "cuda") * 0.02
+    ref.check(attend(q, k, v, **kw), definition(q, k, v, **kw), v, BF16)

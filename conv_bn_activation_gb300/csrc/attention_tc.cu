@@ -478,11 +478,17 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
       };
       int k = -1, n = 0, count = 0, kv = 0, tail_tile = -1;
       uint32_t seq = 0, tails = 0;
-      auto fetch = [&](Step* s) {  // false: no further step (or a wait gave up)
+      // kNone: no further step (or a wait gave up). ahead: the last step's second product is still to be issued, and
+      // kLater says that two items after its own are empty: the third one's list comes only when the softmax warps
+      // have left the first, and so the output that waits for that product.
+      enum Fetched { kNone, kStep, kLater };
+      auto fetch = [&](Step* s, bool ahead) {
+        const int own = k;
         while (n == count) {
+          if (ahead && k - own == 2) return kLater;
           ++k;
-          if (k >= rounds || item_of(k) >= items) return false;
-          if (!wait(&list_full[k & 1], k >> 1)) return false;
+          if (k >= rounds || item_of(k) >= items) return kNone;
+          if (!wait(&list_full[k & 1], k >> 1)) return kNone;
           n = 0;
           count = __shfl_sync(~0u, info[k & 1].n, 0);
           kv = __shfl_sync(~0u, info[k & 1].kv, 0);
@@ -498,7 +504,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
         s->kv = kv;
         seq += 2;
         if (s->last && leader) mbar_arrive(&list_free[k & 1]);
-        return true;
+        return kStep;
       };
       uint32_t q_items = 0, q_have = 0;  // items with keys so far; the one whose Q was waited for
       uint32_t p_seen = 0, o_items = 0, in_item = 0;
@@ -530,56 +536,61 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
         __syncwarp();
       };
       Step cur, nxt;
-      bool have = fetch(&cur);
-      if (have) {
-        k_wait(cur);
-        if (ok) qk(cur);
-      }
-      while (ok && have) {
-        const bool more = fetch(&nxt);
-        if (!ok) break;
-        const uint32_t vq = cur.seq + 1, vs = vq % NS, vl = v_lo + vs * (SH::kSlot >> 4);
-        wait(&kv_full[vs], vq / NS);
-        if (ok && cur.tail) {  // values past the sequence's end, whatever they are, become zero
-          if (t == 0) {
-            for (int s = 0; s < SV; ++s)
-              for (int e = (cur.kv % kTile) * 8 + lane; e < kTile * 8; e += 32)
-                *reinterpret_cast<uint4*>(sKV + vs * SH::kSlot + s * kSlab + e * 16) = make_uint4(0, 0, 0, 0);
-            fence_async_shared();
-            __syncwarp();
-          }
-          if (lane == 0) mbar_arrive(v_tail);  // both warps: neither is ever two tails ahead of the other
-          wait(v_tail, tails++);
+      for (bool again = true; ok && again;) {  // again: after empty items, with no product held back
+        again = false;
+        bool have = fetch(&cur, false) == kStep;
+        if (have) {
+          k_wait(cur);
+          if (ok) qk(cur);
         }
-        if (ok && more) k_wait(nxt);
-        if (!ok) break;
-        if (cur.state) {
-          if (in_item == 0 && o_items > 0) wait(&o_free[t], o_items - 1);
-          const uint32_t fresh = in_item == 0;
-          if (!ok || !wait(&p_ready[t], p_seen)) break;
-          take();
-          tc_fence_after_sync();
-          if (leader) {
+        while (ok && have) {
+          const Fetched next = fetch(&nxt, true);
+          if (!ok) break;
+          const bool more = next == kStep;
+          again = next == kLater;
+          const uint32_t vq = cur.seq + 1, vs = vq % NS, vl = v_lo + vs * (SH::kSlot >> 4);
+          wait(&kv_full[vs], vq / NS);
+          if (ok && cur.tail) {  // values past the sequence's end, whatever they are, become zero
+            if (t == 0) {
+              for (int s = 0; s < SV; ++s)
+                for (int e = (cur.kv % kTile) * 8 + lane; e < kTile * 8; e += 32)
+                  *reinterpret_cast<uint4*>(sKV + vs * SH::kSlot + s * kSlab + e * 16) = make_uint4(0, 0, 0, 0);
+              fence_async_shared();
+              __syncwarp();
+            }
+            if (lane == 0) mbar_arrive(v_tail);  // both warps: neither is ever two tails ahead of the other
+            wait(v_tail, tails++);
+          }
+          if (ok && more) k_wait(nxt);
+          if (!ok) break;
+          if (cur.state) {
+            if (in_item == 0 && o_items > 0) wait(&o_free[t], o_items - 1);
+            const uint32_t fresh = in_item == 0;
+            if (!ok || !wait(&p_ready[t], p_seen)) break;
+            take();
+            tc_fence_after_sync();
+            if (leader) {
 #pragma unroll
-            for (int x = 0; x < kTile / 16; ++x)
-              mma_bf16_ts(o_tmem, s_tmem + x * 8, kHi | (vl + x * (2048 >> 4)), idesc_o, x > 0 ? 1u : 1u - fresh);
+              for (int x = 0; x < kTile / 16; ++x)
+                mma_bf16_ts(o_tmem, s_tmem + x * 8, kHi | (vl + x * (2048 >> 4)), idesc_o, x > 0 ? 1u : 1u - fresh);
+            }
+            __syncwarp();
+            ++p_seen;
+            ++in_item;
           }
+          if (cur.last && in_item) {
+            if (leader) mma_commit(&o_full[t]);
+            __syncwarp();
+            ++o_items;
+            in_item = 0;
+          }
+          if (more) qk(nxt);
+          if (cur.state) give();
+          if (leader) mma_commit(&kv_empty[vs]);
           __syncwarp();
-          ++p_seen;
-          ++in_item;
+          have = more;
+          cur = nxt;
         }
-        if (cur.last && in_item) {
-          if (leader) mma_commit(&o_full[t]);
-          __syncwarp();
-          ++o_items;
-          in_item = 0;
-        }
-        if (more) qk(nxt);
-        if (cur.state) give();
-        if (leader) mma_commit(&kv_empty[vs]);
-        __syncwarp();
-        have = more;
-        cur = nxt;
       }
       __syncwarp();
       if (leader) {  // the MMAs and arrivals issued so far end before TMEM and shared memory are given back

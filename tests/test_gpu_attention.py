@@ -384,3 +384,32 @@ def test_orders_and_broadcast_inputs(gpu, shape, dtype):
         ke, ve = (t[:narrow[0], :, :narrow[2]].expand(*wide, -1) for t in (k, v))
         assert torch.equal(run(q, ke, ve, kw), run(q, ke.contiguous(), ve.contiguous(), kw))
     sync_check()
+
+
+@pytest.mark.parametrize("Lk", [1, 130, 400])
+@pytest.mark.parametrize("case", ["offset", "lengths", "documents"])
+def test_runs_of_items_without_a_key(gpu, case, Lk):
+    """Many rounds of work per CTA in which most items see no key, several in a row: the next item's keys are not
+    waited for while the last one's output is still to come."""
+    shape = (45, 450, Lk, 16, 2, 64, 64)
+    B, Lq, _, Hq, Hkv, D, _ = shape
+    q, k, v = make(shape, BF16, seed=51)
+    kw = {"scale": 0.125}
+    i, j = torch.arange(Lq, device="cuda")[:, None], torch.arange(Lk, device="cuda")[None, :]
+    if case == "offset":  # the last queries alone see keys
+        kw.update(causal=True, q_offset=-(Lq - 3))
+        keep = (j <= i + kw["q_offset"]).expand(B, Lq, Lk)
+    elif case == "lengths":
+        kw["kv_len"] = torch.tensor([Lk if b % 7 in (0, 3) else 0 for b in range(B)], dtype=torch.int32, device="cuda")
+        keep = (j < kw["kv_len"][:, None, None]).expand(B, Lq, Lk)
+    else:
+        b = torch.arange(B, device="cuda")[:, None]
+        kw["doc_q"] = ((i[:, 0] // 150)[None] + 10 * b).to(torch.int32).contiguous()
+        kw["doc_k"] = torch.where(b % 5 == 2, 10 * b + j // 100, -1).to(torch.int32).contiguous()
+        keep = kw["doc_q"][:, :, None] == kw["doc_k"][:, None, :]
+    out = run(q, k, v, kw)
+    sync_check()
+    s = torch.einsum("bihd,bjhd->bhij", q.double(), k.double().repeat_interleave(Hq // Hkv, 2)) * 0.125
+    w = torch.exp(s - s.amax(-1, keepdim=True)).masked_fill(~keep[:, None], 0.0)
+    w = w / w.sum(-1, keepdim=True).clamp(min=1e-300)
+    ref.check(out, torch.einsum("bhij,bjhd->bihd", w, v.double().repeat_interleave(Hq // Hkv, 2)).cpu(), v, BF16)

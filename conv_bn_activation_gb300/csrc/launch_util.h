@@ -6,6 +6,7 @@
 #include <atomic>
 #include <cstddef>
 #include <cstdlib>
+#include <mutex>
 #include <utility>
 
 namespace cb {
@@ -23,12 +24,13 @@ cudaError_t smem_attr_once(size_t smem) {
   if (dev < 0 || dev >= kMaxDevices)
     return cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (raised[dev].load(std::memory_order_acquire) >= smem) return cudaSuccess;
+  // One thread at a time: the call sets the limit, so that a smaller one set last would lower it again.
+  static std::mutex raising;
+  const std::lock_guard<std::mutex> lock(raising);
+  if (raised[dev].load(std::memory_order_relaxed) >= smem) return cudaSuccess;
   e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-  if (e != cudaSuccess) return e;
-  size_t cur = raised[dev].load(std::memory_order_relaxed);
-  while (cur < smem && !raised[dev].compare_exchange_weak(cur, smem, std::memory_order_acq_rel)) {
-  }
-  return cudaSuccess;
+  if (e == cudaSuccess) raised[dev].store(smem, std::memory_order_release);
+  return e;
 }
 
 // Programmatic dependent launch is on unless CB_PDL=0 (read once).

@@ -413,3 +413,45 @@ def test_runs_of_items_without_a_key(gpu, case, Lk):
     w = torch.exp(s - s.amax(-1, keepdim=True)).masked_fill(~keep[:, None], 0.0)
     w = w / w.sum(-1, keepdim=True).clamp(min=1e-300)
     ref.check(out, torch.einsum("bhij,bjhd->bihd", w, v.double().repeat_interleave(Hq // Hkv, 2)).cpu(), v, BF16)
+
+
+THREADS = """
+import sys, threading
+sys.path.insert(0, {root!r})
+import torch
+from conv_bn_activation_gb300 import binding as cb
+
+cb.load()
+q = torch.randn(1, 256, 2, 64, device="cuda").to(torch.bfloat16)
+sizes = [1000, 30000, 60000, 120000, 90000, 45000, 200000, 150000]
+kv = [torch.randn(1, n, 2, 64, device="cuda").to(torch.bfloat16) for n in sizes]
+out = [torch.empty_like(q) for n in sizes]
+start = threading.Barrier(len(sizes))
+failed = []
+
+def call(i):
+    start.wait()
+    for x in (i, *range(len(sizes))):
+        try:
+            cb.attention(q, kv[x], kv[x], out[x] if x == i else torch.empty_like(q), cb.Score(0.125))
+        except cb.CbError as e:
+            failed.append((i, x, str(e)))
+
+threads = [threading.Thread(target=call, args=(i,)) for i in range(len(sizes))]
+[t.start() for t in threads]
+[t.join() for t in threads]
+torch.cuda.synchronize()
+assert not failed, failed
+assert cb.get_device_error() == cb.OK
+"""
+
+
+def test_first_calls_of_many_threads(gpu):
+    """Calls that need different amounts of shared memory, the first ones of a process at the same time."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    for _ in range(3):
+        r = subprocess.run([sys.executable, "-c", THREADS.format(root=root)], capture_output=True, text=True, timeout=240)
+        assert r.returncode == 0, r.stderr[-2000:]

@@ -228,7 +228,7 @@ __device__ __forceinline__ Item item_at(const AttnArgs& a, int pairs, int item) 
 template <int SK, int SV, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
-               const __grid_constant__ CUtensorMap vmap, const AttnArgs a, int pairs, int items, int list_len) {
+               const __grid_constant__ CUtensorMap vmap, const __grid_constant__ AttnArgs a, int pairs, int items, int list_len) {
   using SH = Shape<SK, SV>;
   constexpr int NS = SH::kStages;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -473,49 +473,51 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
       // One key tile of one item; `seq`: its K's place in the ring's sequence.
       struct Step {
         uint32_t state, seq;
-        bool first, last, tail;
-        int kv;
+        bool last;
+        int tail;  // rows of a tail tile that are keys, else 0
       };
-      int k = -1, n = 0, count = 0, kv = 0, tail_tile = -1;
-      uint32_t seq = 0, tails = 0;
+      int k = -1, n = 0, count = 0, tail_tile = -1, tail_rows = 0;
+      uint32_t seq = 0;
+      // Parities of the next waits (Q and o_free: of the phase before the next one), and two facts about the item at
+      // hand: its Q was waited for, its O was begun.
+      enum : uint32_t { kP = 1, kTail = 2, kQ = 4, kO = 8, kHaveQ = 16, kBegun = 32 };
+      uint32_t bits = kQ | kO;
       // kNone: no further step (or a wait gave up). ahead: the last step's second product is still to be issued, and
-      // kLater says that two items after its own are empty: the third one's list comes only when the softmax warps
-      // have left the first, and so the output that waits for that product.
+      // kLater says that the item after its own is empty. Past two such items the next list would come only when the
+      // softmax warps have left the first, and so the output that waits for that product.
       enum Fetched { kNone, kStep, kLater };
       auto fetch = [&](Step* s, bool ahead) {
-        const int own = k;
         while (n == count) {
-          if (ahead && k - own == 2) return kLater;
           ++k;
           if (k >= rounds || item_of(k) >= items) return kNone;
           if (!wait(&list_full[k & 1], k >> 1)) return kNone;
           n = 0;
           count = __shfl_sync(~0u, info[k & 1].n, 0);
-          kv = __shfl_sync(~0u, info[k & 1].kv, 0);
+          const int kv = __shfl_sync(~0u, info[k & 1].kv, 0);
           tail_tile = __shfl_sync(~0u, info[k & 1].tail, 0) ? kv / kTile : -1;
-          if (count == 0 && leader) mbar_arrive(&list_free[k & 1]);
+          tail_rows = kv % kTile;
+          if (count == 0) {
+            if (leader) mbar_arrive(&list_free[k & 1]);
+            if (ahead) return kLater;
+          }
         }
         const uint32_t e = __shfl_sync(~0u, lists[(k & 1) * list_len + n], 0);
         s->state = (e >> (2 * t)) & 3u;
         s->seq = seq;
-        s->first = n == 0;
+        if (n == 0) bits = (bits ^ kQ) & ~kHaveQ;
         s->last = ++n == count;
-        s->tail = static_cast<int>(e >> 4) == tail_tile;
-        s->kv = kv;
+        s->tail = static_cast<int>(e >> 4) == tail_tile ? tail_rows : 0;
         seq += 2;
         if (s->last && leader) mbar_arrive(&list_free[k & 1]);
         return kStep;
       };
-      uint32_t q_items = 0, q_have = 0;  // items with keys so far; the one whose Q was waited for
-      uint32_t p_seen = 0, o_items = 0, in_item = 0;
       auto k_wait = [&](const Step& s) {
-        if (s.first) ++q_items;
         wait(&kv_full[s.seq % NS], s.seq / NS);
         // Q_t has landed before its buffer is given back, also where no key tile of the item used it: a second
         // load into a barrier whose first is still under way would be one arrival too many.
-        if ((s.state || s.last) && q_have != q_items) {
-          q_have = q_items;
-          wait(&q_full[t], q_items - 1);
+        if ((s.state || s.last) && !(bits & kHaveQ)) {
+          bits |= kHaveQ;
+          wait(&q_full[t], (bits & kQ) != 0);
         }
       };
       auto qk = [&](const Step& s) {
@@ -536,61 +538,54 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
         __syncwarp();
       };
       Step cur, nxt;
-      for (bool again = true; ok && again;) {  // again: after empty items, with no product held back
-        again = false;
-        bool have = fetch(&cur, false) == kStep;
-        if (have) {
-          k_wait(cur);
-          if (ok) qk(cur);
+      bool held = false;  // cur is a step whose second product is still to be issued
+      for (;;) {
+        const Fetched next = fetch(&nxt, held);
+        const bool more = next == kStep;
+        if (!ok || !(held || more)) break;
+        const uint32_t vq = held ? cur.seq + 1 : 0, vs = vq % NS, vl = v_lo + vs * (SH::kSlot >> 4);
+        if (held) wait(&kv_full[vs], vq / NS);
+        if (ok && held && cur.tail) {  // values past the sequence's end, whatever they are, become zero
+          if (t == 0) {
+            for (int s = 0; s < SV; ++s)
+              for (int e = cur.tail * 8 + lane; e < kTile * 8; e += 32)
+                *reinterpret_cast<uint4*>(sKV + vs * SH::kSlot + s * kSlab + e * 16) = make_uint4(0, 0, 0, 0);
+            fence_async_shared();
+            __syncwarp();
+          }
+          if (lane == 0) mbar_arrive(v_tail);  // both warps: neither is ever two tails ahead of the other
+          wait(v_tail, (bits & kTail) != 0);
+          bits ^= kTail;
         }
-        while (ok && have) {
-          const Fetched next = fetch(&nxt, true);
-          if (!ok) break;
-          const bool more = next == kStep;
-          again = next == kLater;
-          const uint32_t vq = cur.seq + 1, vs = vq % NS, vl = v_lo + vs * (SH::kSlot >> 4);
-          wait(&kv_full[vs], vq / NS);
-          if (ok && cur.tail) {  // values past the sequence's end, whatever they are, become zero
-            if (t == 0) {
-              for (int s = 0; s < SV; ++s)
-                for (int e = (cur.kv % kTile) * 8 + lane; e < kTile * 8; e += 32)
-                  *reinterpret_cast<uint4*>(sKV + vs * SH::kSlot + s * kSlab + e * 16) = make_uint4(0, 0, 0, 0);
-              fence_async_shared();
-              __syncwarp();
-            }
-            if (lane == 0) mbar_arrive(v_tail);  // both warps: neither is ever two tails ahead of the other
-            wait(v_tail, tails++);
-          }
-          if (ok && more) k_wait(nxt);
-          if (!ok) break;
-          if (cur.state) {
-            if (in_item == 0 && o_items > 0) wait(&o_free[t], o_items - 1);
-            const uint32_t fresh = in_item == 0;
-            if (!ok || !wait(&p_ready[t], p_seen)) break;
-            take();
-            tc_fence_after_sync();
-            if (leader) {
+        if (ok && more) k_wait(nxt);
+        if (!ok) break;
+        if (held && cur.state) {
+          const uint32_t begun = (bits & kBegun) != 0;
+          if (!begun) wait(&o_free[t], (bits & kO) != 0);  // at once before the first item's
+          if (!ok || !wait(&p_ready[t], bits & kP)) break;
+          take();
+          tc_fence_after_sync();
+          if (leader) {
 #pragma unroll
-              for (int x = 0; x < kTile / 16; ++x)
-                mma_bf16_ts(o_tmem, s_tmem + x * 8, kHi | (vl + x * (2048 >> 4)), idesc_o, x > 0 ? 1u : 1u - fresh);
-            }
-            __syncwarp();
-            ++p_seen;
-            ++in_item;
+            for (int x = 0; x < kTile / 16; ++x)
+              mma_bf16_ts(o_tmem, s_tmem + x * 8, kHi | (vl + x * (2048 >> 4)), idesc_o, x > 0 ? 1u : begun);
           }
-          if (cur.last && in_item) {
-            if (leader) mma_commit(&o_full[t]);
-            __syncwarp();
-            ++o_items;
-            in_item = 0;
-          }
-          if (more) qk(nxt);
+          __syncwarp();
+          bits = (bits ^ kP) | kBegun;
+        }
+        if (held && cur.last && (bits & kBegun)) {
+          if (leader) mma_commit(&o_full[t]);
+          __syncwarp();
+          bits = (bits ^ kO) & ~kBegun;
+        }
+        if (more) qk(nxt);
+        if (held) {
           if (cur.state) give();
           if (leader) mma_commit(&kv_empty[vs]);
           __syncwarp();
-          have = more;
-          cur = nxt;
         }
+        held = more;
+        cur = nxt;
       }
       __syncwarp();
       if (leader) {  // the MMAs and arrivals issued so far end before TMEM and shared memory are given back
@@ -604,12 +599,6 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
     const int t = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // this warp's 32 TMEM lanes
     const uint32_t s_col = tmem + lanes + t * kTile, o_col = tmem + lanes + 2 * kTile + t * SV * 64;
-    const float c_scale = a.scale * kLog2e;
-    const float cap_in = CAP ? a.scale / a.softcap : 0.f, cap_out = a.softcap * kLog2e;  // x = cap_out tanh(cap_in s)
-    // x = s gain, or s Q(s^2) with the cap's scales in Q's coefficients
-    const float gain = c_scale;
-    const float q0 = kTanh[0] * cap_out * cap_in, q1 = kTanh[1] * cap_out * cap_in * cap_in * cap_in;
-    const float q2 = q1 / kTanh[1] * kTanh[2] * cap_in * cap_in, q3 = q1 / kTanh[1] * kTanh[3] * cap_in * cap_in * cap_in * cap_in;
     // 32-byte stores of the output, where its rows allow them: a store instruction touches 32 rows, and costs
     // by the row
     const bool wide = ((reinterpret_cast<uintptr_t>(a.o) | (a.os_b * 2) | (a.os_l * 2) | (a.os_h * 2)) & 31) == 0 && a.dv % 16 == 0;
@@ -732,14 +721,14 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
           for (int c = 0; c < kTile; c += 8)
 #pragma unroll
             for (int u = 0; u < 4; ++u) big[u] = max3(big[u], fabsf(s[c + 2 * u]), fabsf(s[c + 2 * u + 1]));
-          in_range = __all_sync(~0u, max3(fmaxf(big[0], big[1]), big[2], big[3]) * cap_in <= kTanhRange);
+          in_range = __all_sync(~0u, max3(fmaxf(big[0], big[1]), big[2], big[3]) * a.tc.cap_in <= kTanhRange);
           fast = fast && in_range;
         }
         auto cap_gain = [&](f2 x) {  // Q(x^2) with the cap's scales: x times it is log2(e) cap tanh(x / cap)
           const f2 z = mul2(x, x);
-          f2 g = fma2(z, pack2(q3, q3), pack2(q2, q2));
-          g = fma2(z, g, pack2(q1, q1));
-          return fma2(z, g, pack2(q0, q0));
+          f2 g = fma2(z, pack2(a.tc.poly[3], a.tc.poly[3]), pack2(a.tc.poly[2], a.tc.poly[2]));
+          g = fma2(z, g, pack2(a.tc.poly[1], a.tc.poly[1]));
+          return fma2(z, g, pack2(a.tc.poly[0], a.tc.poly[0]));
         };
         float tile_sum = 0.f;
         f2 y2 = 0;
@@ -750,7 +739,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
             const f2 x = pack2(s[c], s[c + 1]);
             f2 g;
             if constexpr (CAP) g = cap_gain(x);
-            else g = pack2(gain, gain);
+            else g = pack2(a.tc.gain, a.tc.gain);
             if constexpr (BIAS) {
               y2 = c % 32 == 0 ? bias_at(c, mu) : add2(y2, bias_step);
               return fma2(x, g, y2);
@@ -765,7 +754,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
           tmem_wait_st();  // weights of an attempt that overflowed
           // ------------------------- scores, mask, maximum; then the weights
           // x = mult * s from here on
-          float mult = gain;
+          float mult = a.tc.gain;
           if constexpr (CAP) {
             if (in_range) {
 #pragma unroll
@@ -776,7 +765,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
             } else {
 #pragma unroll
               for (int c = 0; c < kTile; ++c)
-                s[c] = fmaf(-2.f * cap_out, rcp_approx(1.f + exp2_approx(s[c] * (2.f * kLog2e * cap_in))), cap_out);
+                s[c] = fmaf(-2.f * a.tc.cap_out, rcp_approx(1.f + exp2_approx(s[c] * (2.f * kLog2e * a.tc.cap_in))), a.tc.cap_out);
             }
             mult = 1.f;
           }
@@ -936,8 +925,14 @@ cudaError_t launch_shape(const CUtensorMap& q, const CUtensorMap& k, const CUten
 
 void attn_tc_box(int* box_d, int* box_l) { *box_d = 64, *box_l = kTile; }
 
-cudaError_t launch_attn_tc(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const AttnArgs& a, int sms,
+cudaError_t launch_attn_tc(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const AttnArgs& given, int sms,
                            cudaStream_t s) {
+  AttnArgs a = given;
+  TcScore& x = a.tc;
+  x.gain = a.scale * kLog2e;
+  x.cap_in = a.softcap > 0.f ? a.scale / a.softcap : 0.f, x.cap_out = a.softcap * kLog2e;
+  float power = x.gain;
+  for (int i = 0; i < 4; ++i, power *= x.cap_in * x.cap_in) x.poly[i] = kTanh[i] * power;
   if (a.dk <= 64) return a.dv <= 64 ? launch_shape<1, 1>(q, k, v, a, sms, s) : launch_shape<1, 2>(q, k, v, a, sms, s);
   return a.dv <= 64 ? launch_shape<2, 1>(q, k, v, a, sms, s) : launch_shape<2, 2>(q, k, v, a, sms, s);
 }

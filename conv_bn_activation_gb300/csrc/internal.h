@@ -301,6 +301,11 @@ cudaError_t launch_preprocess_normalize(const uint8_t* in, long long count, floa
 cudaError_t launch_preprocess_layout(const float* in, int n, int h, int w, float* out, cudaStream_t s);
 
 // ---------------------------------------------------------------- attention
+// Scores as the tensor-core kernel evaluates them from a dot product s: gain s, or, capped, cap_out tanh(cap_in s),
+// which is s (poly[0] + poly[1] s^2 + ...) far enough below the cap. Read as parameters, they take no registers.
+struct TcScore {
+  float gain, cap_in, cap_out, poly[4];
+};
 // cb_attention's views and score rule (cb.h), strides in elements, last dim contiguous.
 struct AttnArgs {
   const void* q;
@@ -321,6 +326,7 @@ struct AttnArgs {
   const int* doc_k;
   int* err;
   uint64_t timeout_ns;
+  TcScore tc;
 };
 // CUDA cores, fp32 arithmetic, any strides (attention_simt.cu).  vec: every
 // row of q, k, v and out is made of whole 16-byte pieces.

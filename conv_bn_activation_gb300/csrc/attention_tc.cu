@@ -44,6 +44,8 @@
 // Key tiles no query of the item sees are never loaded: the list of the tiles
 // to visit holds each query tile's state (skip, full, masked), nearest keys
 // first: a bias by distance then has its largest scores in the first tile.
+#include <cmath>
+
 #include "attention_common.cuh"
 #include "launch_util.h"
 #include "ptx.cuh"
@@ -721,7 +723,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
           for (int c = 0; c < kTile; c += 8)
 #pragma unroll
             for (int u = 0; u < 4; ++u) big[u] = max3(big[u], fabsf(s[c + 2 * u]), fabsf(s[c + 2 * u + 1]));
-          in_range = __all_sync(~0u, max3(fmaxf(big[0], big[1]), big[2], big[3]) * a.tc.cap_in <= kTanhRange);
+          in_range = __all_sync(~0u, max3(fmaxf(big[0], big[1]), big[2], big[3]) * a.tc.reach <= kTanhRange);
           fast = fast && in_range;
         }
         auto cap_gain = [&](f2 x) {  // Q(x^2) with the cap's scales: x times it is log2(e) cap tanh(x / cap)
@@ -933,6 +935,9 @@ cudaError_t launch_attn_tc(const CUtensorMap& q, const CUtensorMap& k, const CUt
   x.cap_in = a.softcap > 0.f ? a.scale / a.softcap : 0.f, x.cap_out = a.softcap * kLog2e;
   float power = x.gain;
   for (int i = 0; i < 4; ++i, power *= x.cap_in * x.cap_in) x.poly[i] = kTanh[i] * power;
+  // The polynomial is for finite s^2 and coefficients. Where scale / softcap is so large that they are not, the exact
+  // form serves for all scores, those of 0 too: reach is NaN.
+  x.reach = std::isfinite(x.poly[3]) ? std::fmax(x.cap_in, kTanhRange * 0x1p-60f) : NAN;
   if (a.dk <= 64) return a.dv <= 64 ? launch_shape<1, 1>(q, k, v, a, sms, s) : launch_shape<1, 2>(q, k, v, a, sms, s);
   return a.dv <= 64 ? launch_shape<2, 1>(q, k, v, a, sms, s) : launch_shape<2, 2>(q, k, v, a, sms, s);
 }

@@ -302,9 +302,9 @@ cudaError_t launch_preprocess_layout(const float* in, int n, int h, int w, float
 
 // ---------------------------------------------------------------- attention
 // Scores as the tensor-core kernel evaluates them from a dot product s: gain s, or, capped, cap_out tanh(cap_in s),
-// which is s (poly[0] + poly[1] s^2 + ...) far enough below the cap. Read as parameters, they take no registers.
+// which is s (poly[0] + poly[1] s^2 + ...) while |s| * reach <= kTanhRange. Read as parameters, they take no registers.
 struct TcScore {
-  float gain, cap_in, cap_out, poly[4];
+  float gain, cap_in, cap_out, poly[4], reach;
 };
 // cb_attention's views and score rule (cb.h), strides in elements, last dim contiguous.
 struct AttnArgs {

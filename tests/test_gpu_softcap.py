@@ -138,3 +138,16 @@ def test_rows_that_meet_both_forms_of_the_cap(gpu, lead, bias):
     if bias:
         kw["slopes"] = ref.alibi_slopes(2, "cuda") * 0.02
     ref.check(attend(q, k, v, **kw), definition(q, k, v, **kw), v, BF16)
+
+
+@TYPES
+@pytest.mark.parametrize("softcap,scale", [(1e-40, 0.125), (1e-9, 0.125), (1e-6, 0.125), (1e-3, 1e3), (0.5, 1e6)], ids=str)
+@pytest.mark.parametrize("shape", ROWS[:1] + TILES, ids=lambda s: "x".join(map(str, s)))
+def test_scores_of_zero_under_any_cap(gpu, shape, softcap, scale, dtype):
+    """Queries of zeros see the mean of the values, however large scale / softcap is; so do, nearly, queries whose
+    scores stay a little below or above the cap."""
+    q, k, v = tokens(shape, dtype, seed=61)
+    kw = {"scale": scale, "softcap": softcap}
+    for factor in (0.0, softcap / scale * 0.05, softcap / scale * 0.5):
+        x = (q.float() * factor).to(dtype)
+        ref.check(attend(x, k, v, **kw), definition(x, k, v, **kw), v, dtype)

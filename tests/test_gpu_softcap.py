@@ -151,3 +151,15 @@ def test_scores_of_zero_under_any_cap(gpu, shape, softcap, scale, dtype):
     for factor in (0.0, softcap / scale * 0.05, softcap / scale * 0.5):
         x = (q.float() * factor).to(dtype)
         ref.check(attend(x, k, v, **kw), definition(x, k, v, **kw), v, dtype)
+
+
+@pytest.mark.parametrize("softcap", [1e4, 1e5, 1e6])
+@pytest.mark.parametrize("shape", [(1, 384, 384, 2, 2, 64, 64), (2, 300, 520, 4, 2, 128, 128)], ids=lambda s: "x".join(map(str, s)))
+def test_small_scores_beside_rows_at_their_cap(gpu, shape, softcap):
+    """Every other query's scores lie far above a large cap, its neighbours' far below: those keep their precision."""
+    q, k, v = tokens(shape, BF16, seed=71)
+    q[:, 1::2] = (q[:, 1::2].float() * softcap).to(BF16)
+    kw = {"scale": shape[5] ** -0.5, "softcap": softcap}
+    got, want = attend(q, k, v, **kw), definition(q, k, v, **kw)
+    assert torch.isfinite(got.float()).all()
+    ref.check(got[:, ::2], want[:, ::2], v, BF16)

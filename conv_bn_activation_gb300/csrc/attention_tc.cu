@@ -34,9 +34,9 @@
 // rounded to bf16 for the second product (each weight to nearest, independent
 // from key to key); l sums the unrounded weights.
 //
-// 4096 tokens, 16 heads on 4 key heads of 128: 101 us, 1360 TFLOP/s (0.71 of
-// the measured bf16 rate); capped 137, biased 115, causal 53; 16 heads of 64:
-// 85. The rest is latency: a tile's scores wait for its own weights' product,
+// 4096 tokens, 16 heads on 4 key heads of 128: 102 us, 1350 TFLOP/s (0.70 of
+// the measured bf16 rate); capped 137, biased 115, causal 54; 16 heads of 64:
+// 86. The rest is latency: a tile's scores wait for its own weights' product,
 // and two warps per scheduler do not cover all of it. Measured and not kept: P in
 // columns of its own for narrow values, so that the next scores start earlier
 // (86 -> 90); one path for full and masked tiles (104 -> 109).

@@ -21,7 +21,7 @@
 //    and for contiguous rows: a cluster of a.split CTAs per item, joined
 //    through distributed shared memory.  One launch, no prefix over the
 //    lengths: one sequence of 421 tokens takes 4.7 us where runs and their join
-//    take 7.7, 64 of 200 to 500 tokens (8 key heads of 128) 26 and 33; from
+//    take 9.4, 64 of 200 to 500 tokens (8 key heads of 128) 25 and 33; from
 //    about 30 tiles per CTA on runs are faster (32 sequences of 100 to 2000
 //    tokens: 37, whole 41).
 #pragma once

@@ -340,7 +340,7 @@ void attn_tc_box(int* box_d, int* box_l);
 cudaError_t launch_attn_tc(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const AttnArgs& a, int sms,
                            cudaStream_t s);
 
-// The paged cache as the kernels read it (cb_paged_cache); page_div divides by page_size.
+// The paged cache as the kernels read it (cb_paged_cache).
 struct PagedArgs {
   void* k;
   void* v;

@@ -426,10 +426,11 @@ typedef struct {
  * bf16 views whose data is 16-byte aligned with strides and head sizes that
  * are multiples of 8 elements, at most 2^18 keys long, run on the tensor
  * cores: scores and the sums over keys in fp32, the weights p rounded to bf16
- * as the second product's operand; where few queries share a key head they
- * stream the keys through warp-level MMAs, as cb_attention_decode does.  fp32,
- * and every other bf16 view, runs in fp32 on the CUDA cores.  Softmax
- * statistics are fp32 throughout.  One
+ * as the second product's operand (their own sum is of the unrounded ones),
+ * a cap's tanh to 7e-5 of its value and 6.1e-6; where few queries share a key
+ * head they stream the keys through warp-level MMAs, as cb_attention_decode
+ * does.  fp32, and every other bf16 view, runs in fp32 on the CUDA cores.
+ * Softmax statistics are fp32 throughout.  One
  * kernel, no workspace; asynchronous on `stream`; bounded waits
  * (CB_ERR_TIMEOUT through cb_get_device_error).
  */
@@ -485,10 +486,11 @@ cb_status cb_attention_decode_workspace(const cb_heads* q, const cb_paged_cache*
  * pages hold; an empty range gives zeros).  Scores as in cb_score with the
  * query at position length[b] - 1: scale, softcap, and slopes (NULL or
  * DEVICE fp32 [Hq]) times length[b] - 1 - j.  out overlaps neither q nor a
- * page.  The new token's own key and
- * value are in the cache already (cb_cache_append).  Hq a multiple of the
- * cache's heads; dim_k and dim_v at most 128, batch at most 4096 (else
- * CB_ERR_UNSUPPORTED).  The tokens of all sequences are dealt evenly over
+ * page.  The new token's own key and value are in the cache already
+ * (cb_cache_append).  Hq a multiple of the cache's heads; dim_k and dim_v at
+ * most 128, batch at most 4096 (else CB_ERR_UNSUPPORTED).  bf16 caches whose
+ * rows are whole 16-byte pieces round the weights to bf16 for the second
+ * product and sum them as rounded; all else is fp32.  The tokens of all sequences are dealt evenly over
  * the GPU, a long sequence over many CTAs, and joined in a fixed order: the
  * same inputs give the same bits.  workspace: DEVICE scratch of at least
  * cb_attention_decode_workspace() bytes, 256-byte aligned, overwritten;

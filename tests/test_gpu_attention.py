@@ -455,3 +455,22 @@ def test_first_calls_of_many_threads(gpu):
     for _ in range(3):
         r = subprocess.run([sys.executable, "-c", THREADS.format(root=root)], capture_output=True, text=True, timeout=240)
         assert r.returncode == 0, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("offset", [20000, 250000, -250000])
+def test_bias_over_long_distances(gpu, offset, dtype):
+    """Keys that all lie far from their queries: what a bias differs by from key to key is small beside it."""
+    shape = (2, 300, 384, 8, 8, 64, 64)
+    q, k, v = make(shape, dtype, seed=81)
+    kw = {"scale": 0.125, "slopes": ref.alibi_slopes(8, "cuda"), "q_offset": offset}
+    out = run(q, k, v, kw)
+    sync_check()
+    s = torch.einsum("bihd,bjhd->bhij", q.double(), k.double()) * 0.125
+    i, j = torch.arange(300, device="cuda")[:, None] + offset, torch.arange(384, device="cuda")[None, :]
+    w = torch.softmax(s - kw["slopes"].double()[None, :, None, None] * (i - j).abs(), -1)
+    want = torch.einsum("bhij,bjhd->bihd", w, v.double()).cpu()
+    # scores of up to 125000 hold no more than 2^-7 of themselves: the weights carry that, rounded once, at worst
+    worst = 2.0 ** -24 * 0.5 * abs(offset) * 1.4427
+    err = (out.cpu().double() - want).abs().max()
+    assert float(err) <= worst * float(v.abs().max()) + float(ref.bound(want, v.cpu().double(), dtype).max())

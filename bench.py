@@ -8,8 +8,9 @@ ranks).  A step is R passes of the chain over the batch, R chosen so that
 the timed region lasts at least --min-timed-s (the pass count is in
 ``config``); the R passes of a step are one CUDA graph.
 
-The same line carries, under ``configs``, the other configurations measured
-in the same run, each with its value, roofline and CPU baseline:
+The same line carries, under ``configs``, the values of the other
+configurations measured in the same run; standard error gets the line with
+the tables per launch and each configuration's roofline and CPU baseline:
   mnist       the DepthwiseMNIST forward at batch 64 (images/s)
   depthwise   the depthwise 3x3 + BN + ReLU layer [64,56,56,384], stride 1 and 2 (GB/s)
   dense       the dense 3x3 + BN + SiLU sweep at batch 16 and 1 (TFLOP/s, tensor cores)
@@ -1089,6 +1090,15 @@ EXTRA_CONFIGS = (("cfg0_mnist_b64", "mnist", 64), ("cfg1_depthwise_b64", "depthw
                  ("bf16_pointwise_b32", "pointwise_bf16", 32))
 
 
+def short_line(line):
+    """The line as standard output gets it: without the tables per launch, and the other configurations by their
+    values alone (all of it, some 47 KB, is longer than a reader of one line may take; it goes to standard error)."""
+    short = {k: v for k, v in line.items() if k not in ("launches", "kernel_shares", "timing", "configs")}
+    if "configs" in line:
+        short["configs"] = {k: [c["value"], c["unit"]] for k, c in line["configs"].items()}
+    return short
+
+
 def run_ours(args):
     import torch
     world, rank, local = dist_setup()
@@ -1155,7 +1165,8 @@ def run_ours(args):
     line.update({k: v for k, v in main.items() if k not in ("value", "unit", "steps", "ms_per_step", "config")})
     if extra:
         line["configs"] = extra
-    print(json.dumps(line), flush=True)
+    print("details: " + json.dumps(line), file=sys.stderr, flush=True)
+    print(json.dumps(short_line(line)), flush=True)
     if world > 1:
         torch.distributed.destroy_process_group()
 

@@ -52,3 +52,17 @@ def test_dist_setup_defaults_to_one_rank(monkeypatch):
     for k in ("WORLD_SIZE", "RANK", "LOCAL_RANK"):
         monkeypatch.delenv(k, raising=False)
     assert bench.dist_setup() == (1, 0, 0)
+
+
+def test_the_line_stays_short():
+    """Standard output gets every key of the contract and no table per launch."""
+    launch = {"name": "s0.down", "kernel": "cb::stem_tc_kernel", "us": 91.2, "roofline": {"frac": 0.5}}
+    keys = ("metric", "value", "unit", "n_gpus", "steps", "warmup", "ms_per_step", "higher_is_better", "scaling",
+            "vs_baseline", "dtype", "data", "config", "e2e", "gpu_launches", "clocks", "roofline")
+    line = {k: k for k in keys}
+    line.update(launches=[launch] * 40, kernel_shares={"k": launch}, timing={"launches": "x" * 200},
+                configs={f"cfg{i}": {"value": 711047.277, "unit": "images/s", "launches": [launch] * 40} for i in range(10)})
+    short = bench.short_line(line)
+    assert all(short[k] == k for k in keys)
+    assert short["configs"]["cfg3"] == [711047.277, "images/s"]
+    assert len(bench.json.dumps(short)) < 2000 and "launches" in line

@@ -1,67 +1,13 @@
 // Entry points of the attention operators: argument validation, kernel choice
 // and launches.  Host code only.
-#include <cmath>
-
 #include "cb.h"
 #include "host_util.h"
 #include "internal.h"
+#include "views.h"
 
 using namespace cb;
 
 namespace {
-
-constexpr int kMaxDim = 128;
-constexpr int kMaxBatch = 4096;
-
-size_t elem_bytes(cb_dtype t) { return t == CB_DTYPE_BF16 ? 2 : 4; }
-
-bool heads_ok(const cb_heads* t) {
-  if (!t || (t->dtype != CB_DTYPE_F32 && t->dtype != CB_DTYPE_BF16)) return false;
-  if (t->batch < 0 || t->len < 0 || t->heads < 1 || t->dim < 1) return false;
-  if (t->stride_b < 0 || t->stride_l < 0 || t->stride_h < 0) return false;
-  return t->data || t->batch == 0 || t->len == 0;
-}
-
-bool empty(const cb_heads* t) { return t->batch == 0 || t->len == 0; }
-
-bool elem_aligned(const void* p, cb_dtype t) { return reinterpret_cast<uintptr_t>(p) % elem_bytes(t) == 0; }
-
-// Every head's row is made of whole 16-byte pieces at 16-byte boundaries.
-bool pieces16(const void* data, cb_dtype dt, int dim, long long s0, long long s1, long long s2) {
-  const long long per = 16 / static_cast<long long>(elem_bytes(dt));
-  return reinterpret_cast<uintptr_t>(data) % 16 == 0 && dim % per == 0 && s0 % per == 0 && s1 % per == 0 && s2 % per == 0;
-}
-bool pieces16(const cb_heads* t) { return pieces16(t->data, t->dtype, t->dim, t->stride_b, t->stride_l, t->stride_h); }
-
-// Elements from a row's, a sequence's and a view's first to one past its last.
-long long row_extent(const cb_heads* t) { return (t->heads - 1LL) * t->stride_h + t->dim; }
-long long seq_extent(const cb_heads* t) { return (t->len - 1LL) * t->stride_l + row_extent(t); }
-long long extent(const cb_heads* t) { return (t->batch - 1LL) * t->stride_b + seq_extent(t); }
-
-// Whether [0, a) and [d, d + b), both repeated every `period`, stay apart.
-bool apart(long long period, long long a, long long b, long long d) {
-  if (period <= 0 || a > period) return false;
-  const long long at = (d % period + period) % period;
-  return at >= a && at + b <= period;
-}
-
-// True if the views, of one dtype, may share an element. Views whose ranges
-// interleave share none if one's rows or sequences lie in the gaps between the
-// other's, at the same strides (slices of a wider buffer), or one lies in a
-// single gap.
-bool overlap(const cb_heads* a, const cb_heads* b) {
-  if (empty(a) || empty(b)) return false;
-  const long long eb = static_cast<long long>(elem_bytes(a->dtype));
-  const long long d = static_cast<long long>(reinterpret_cast<uintptr_t>(b->data) - reinterpret_cast<uintptr_t>(a->data));
-  if (d >= extent(a) * eb || -d >= extent(b) * eb) return false;
-  auto rows_repeat = [](const cb_heads* t) { return t->batch == 1 || (t->stride_l > 0 && t->stride_b % t->stride_l == 0); };
-  if (a->stride_l == b->stride_l && rows_repeat(a) && rows_repeat(b) &&
-      apart(a->stride_l * eb, row_extent(a) * eb, row_extent(b) * eb, d))
-    return false;
-  if (a->stride_b == b->stride_b && apart(a->stride_b * eb, seq_extent(a) * eb, seq_extent(b) * eb, d)) return false;
-  return !apart(a->stride_b * eb, seq_extent(a) * eb, extent(b) * eb, d) &&
-         !apart(b->stride_b * eb, seq_extent(b) * eb, extent(a) * eb, -d);
-}
 
 bool cache_ok(const cb_paged_cache* c) {
   if (!c || (c->dtype != CB_DTYPE_F32 && c->dtype != CB_DTYPE_BF16)) return false;
@@ -75,15 +21,15 @@ bool cache_ok(const cb_paged_cache* c) {
 }
 
 bool pieces16(const cb_paged_cache* c) {
-  return pieces16(c->k, c->dtype, c->dim_k, c->k_stride_page, c->k_stride_slot, c->k_stride_head) &&
-         pieces16(c->v, c->dtype, c->dim_v, c->v_stride_page, c->v_stride_slot, c->v_stride_head);
+  return cb::pieces16(c->k, c->dtype, c->dim_k, c->k_stride_page, c->k_stride_slot, c->k_stride_head) &&
+         cb::pieces16(c->v, c->dtype, c->dim_v, c->v_stride_page, c->v_stride_slot, c->v_stride_head);
 }
 
 // Whether a view may share an element with the cache's pages.
 bool overlap(const cb_heads* t, const cb_paged_cache* c) {
   const cb_heads k{c->k, c->num_pages, c->page_size, c->heads, c->dim_k, c->k_stride_page, c->k_stride_slot, c->k_stride_head, c->dtype};
   const cb_heads v{c->v, c->num_pages, c->page_size, c->heads, c->dim_v, c->v_stride_page, c->v_stride_slot, c->v_stride_head, c->dtype};
-  return overlap(&k, t) || overlap(&v, t);
+  return cb::overlap(&k, t) || cb::overlap(&v, t);
 }
 
 PagedArgs paged_args(const cb_paged_cache* c) {
@@ -95,20 +41,6 @@ PagedArgs paged_args(const cb_paged_cache* c) {
   p.table_stride = c->table_stride;
   p.num_pages = c->num_pages, p.page_size = c->page_size, p.max_pages = c->max_pages;
   return p;
-}
-
-cb_status done(cudaError_t e) { return e == cudaSuccess ? CB_OK : host_cuda_fail(e); }
-
-bool score_ok(float scale, float softcap) {
-  return std::isfinite(scale) && scale > 0.f && std::isfinite(softcap) && softcap >= 0.f;
-}
-
-// The cap as the kernels take it (0: none), away from the ends of fp32's range, where scale / softcap or
-// softcap * log2(e) would be 0 or infinite. From 2^100 on a cap moves no score below 2^88 by a bit; below 2^-30
-// every weight e^(+-softcap) is 1 in 32 bits, as it is at 2^-30.
-float kernel_cap(float softcap) {
-  if (softcap == 0.f || softcap >= 0x1p100f) return 0.f;
-  return softcap < 0x1p-30f ? 0x1p-30f : softcap;
 }
 
 // The tensor-core kernel's map of a view: (dim, heads, len, batch).

@@ -34,6 +34,7 @@ EXPORTED = (
     "cb_autotune_clear", "cb_autotune_entries", "cb_preprocess_stem_u8", "cb_dw_separable_block_fused",
     "cb_set_tuning", "cb_last_launch", "cb_debug_sample_coords", "cb_convert_weights_bf16", "cb_stage_body",
     "cb_attention", "cb_cache_append", "cb_attention_decode", "cb_attention_decode_workspace",
+    "cb_norm_rotate", "cb_cache4_append", "cb_cache4_read", "cb_attention_decode4", "cb_attention_decode4_workspace",
 )
 STATIC_SCRATCH_BYTES = 16 * 1024 * 1024  # CB_STATIC_SCRATCH_BYTES
 
@@ -78,6 +79,29 @@ class CbPagedCache(ctypes.Structure):
     ]
 
 
+class CbHeadRule(ctypes.Structure):
+    _fields_ = [
+        ("norm", ctypes.c_int), ("eps", ctypes.c_float), ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+        ("rotary", ctypes.c_int), ("adjacent", ctypes.c_int), ("axes", ctypes.c_int),
+        ("freq", ctypes.c_void_p), ("axis", ctypes.c_void_p), ("pos", ctypes.c_void_p),
+        ("pos_stride_axis", ctypes.c_longlong), ("pos_stride_b", ctypes.c_longlong),
+    ]
+
+
+class CbPagedCache4(ctypes.Structure):
+    _fields_ = [
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+        ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int), ("heads", ctypes.c_int),
+        ("dim_k", ctypes.c_int), ("dim_v", ctypes.c_int),
+        ("k_stride_page", ctypes.c_longlong), ("k_stride_slot", ctypes.c_longlong), ("k_stride_head", ctypes.c_longlong),
+        ("v_stride_page", ctypes.c_longlong), ("v_stride_slot", ctypes.c_longlong), ("v_stride_head", ctypes.c_longlong),
+        ("ks_stride_page", ctypes.c_longlong), ("ks_stride_slot", ctypes.c_longlong), ("ks_stride_head", ctypes.c_longlong),
+        ("vs_stride_page", ctypes.c_longlong), ("vs_stride_slot", ctypes.c_longlong), ("vs_stride_head", ctypes.c_longlong),
+        ("table", ctypes.c_void_p), ("batch", ctypes.c_int), ("max_pages", ctypes.c_int),
+        ("table_stride", ctypes.c_longlong),
+    ]
+
+
 class CbLaunchInfo(ctypes.Structure):
     _fields_ = [("grid", ctypes.c_int), ("threads", ctypes.c_int), ("smem_bytes", ctypes.c_size_t),
                 ("cluster", ctypes.c_int), ("blocks_per_sm", ctypes.c_int), ("kernel", ctypes.c_char_p)]
@@ -104,7 +128,7 @@ def load():
             lib = ctypes.CDLL(_LIB_PATH)
             P, I, F, LL, S = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_longlong, ctypes.c_size_t
             T = ctypes.POINTER(CbTensor)
-            H = SC = PC = P  # cb_heads, cb_score, cb_paged_cache: packed bytes, or a pointer to the structure
+            H = SC = HR = PC = P  # cb_heads, cb_score, cb_head_rule, cb_paged_cache(4): packed bytes, or a pointer to the structure
             sig = {
                 "cb_fold_bn": [P, P, P, P, F, I, P, P],
                 "cb_repack_weights": [P, I, I, I, I, I, P],
@@ -120,6 +144,11 @@ def load():
                 "cb_cache_append": [H, H, P, P, PC, P],
                 "cb_attention_decode_workspace": [H, PC, ctypes.POINTER(S)],
                 "cb_attention_decode": [H, PC, P, P, F, F, P, H, P, S, P],
+                "cb_norm_rotate": [H, H, HR, H, H, P],
+                "cb_cache4_append": [H, H, P, P, PC, P],
+                "cb_cache4_read": [PC, P, P, H, H, P],
+                "cb_attention_decode4_workspace": [H, PC, ctypes.POINTER(S)],
+                "cb_attention_decode4": [H, PC, P, P, F, F, P, H, P, S, P],
                 "cb_get_device_error": [P],
                 "cb_last_cuda_error": [],
                 "cb_set_kernel_policy": [I],
@@ -195,6 +224,7 @@ def nchw(t) -> CbTensor:
 # as long to build.
 _HEADS = struct.Struct("P4i3qi4x")   # CbHeads
 _SCORE = struct.Struct("2fP2i4P")    # CbScore
+_RULE = struct.Struct("if2P3i4x3P2q")  # CbHeadRule
 _raw_stream = None
 _codes = None
 
@@ -311,6 +341,84 @@ class PagedCache:
                                  *k_pages.stride()[:3], *v_pages.stride()[:3], table.data_ptr(), table.shape[0],
                                  table.shape[1], table.stride(0), dtype_code(k_pages))
         self.ref = ctypes.byref(self.view)
+
+
+class Rotation:
+    """How `norm_rotate` treats the heads of a token (cb_head_rule).
+
+    norm: y = x / sqrt(mean x^2 + eps) * weight (q_weight, k_weight: float32 [dim], None: 1).
+    freq: float32 [pairs], radians per position (None: nothing turns); pair p is dims (p, p + pairs), or with
+    `adjacent` (2p, 2p + 1), and follows axis[p] of the `axes` positions of a token (int32 [pairs], None: the first).
+    Keeps the tensors."""
+
+    def __init__(self, freq=None, axis=None, axes=1, adjacent=False, norm=False, eps=1e-6, q_weight=None, k_weight=None):
+        self.freq, self.axis, self.axes, self.adjacent = freq, axis, int(axes), bool(adjacent)
+        self.norm, self.eps, self.q_weight, self.k_weight = bool(norm), float(eps), q_weight, k_weight
+        if not norm and (q_weight is not None or k_weight is not None):
+            raise ValueError("q_weight and k_weight are the norm's")
+        if axis is not None and freq is None:
+            raise ValueError("axis: the axes of freq's pairs")
+
+    def view(self, batch, length, dim, pos=None, device=None) -> bytes:
+        """cb_head_rule for [batch, length, ., dim] heads at `pos`, packed; checks the arrays."""
+        pairs = 0 if self.freq is None else self.freq.shape[0]
+        at = sa = sb = 0
+        if pairs:
+            if _codes is None:
+                _init_codes()
+            if pos is None or pos.dtype is not _codes["i32"] or pos.shape != (self.axes, batch, length) or \
+                    (length > 1 and pos.stride(2) != 1) or device not in (None, pos.get_device()):
+                raise ValueError(f"pos: an int32 tensor of shape {(self.axes, batch, length)} on the call's device, its last dim "
+                                 "contiguous")
+            at, (sa, sb, _) = pos.data_ptr(), pos.stride()
+        return _RULE.pack(self.norm, self.eps, _device_array(self.q_weight, "q_weight", "f32", (dim,), device),
+                          _device_array(self.k_weight, "k_weight", "f32", (dim,), device), 2 * pairs, self.adjacent, self.axes,
+                          _device_array(self.freq, "freq", "f32", (pairs,), device),
+                          _device_array(self.axis, "axis", "i32", (pairs,), device), at, sa, sb)
+
+
+class PagedCache4:
+    """A paged key-value cache in 4 bits (cb_paged_cache4): k_codes [P, page, H, (Dk + 1) // 2] uint8, k_scales
+    [P, page, H, scales_per_row(Dk)] bfloat16, v_codes and v_scales likewise (any strides, the last dim contiguous),
+    table as in PagedCache.  dim_k, dim_v: needed where odd.  Holds the tensors; the table's contents may change
+    between calls.  `PagedCache4.empty` makes the pages, each head's slots of a page side by side."""
+
+    def __init__(self, k_codes, k_scales, v_codes, v_scales, table, dim_k=None, dim_v=None):
+        dim_k = 2 * k_codes.shape[3] if dim_k is None else int(dim_k)
+        dim_v = 2 * v_codes.shape[3] if dim_v is None else int(dim_v)
+        for codes, scales, dim in ((k_codes, k_scales, dim_k), (v_codes, v_scales, dim_v)):
+            if str(codes.dtype) != "torch.uint8" or str(scales.dtype) != "torch.bfloat16":
+                raise ValueError("codes: uint8, scales: bfloat16")
+            if codes.shape[:3] != k_codes.shape[:3] or scales.shape[:3] != k_codes.shape[:3]:
+                raise ValueError("codes and scales of keys and values: the same pages, slots and heads")
+            if codes.shape[3] != (dim + 1) // 2 or scales.shape[3] != scales_per_row(dim):
+                raise ValueError(f"rows of {dim} dims: {(dim + 1) // 2} bytes of codes and {scales_per_row(dim)} scales")
+            if (codes.stride(3) != 1 and codes.shape[3] > 1) or scales.stride(3) != 1:
+                raise ValueError("the last dim of the pages is contiguous")
+        if str(table.dtype) != "torch.int32" or table.dim() != 2 or (table.shape[1] > 1 and table.stride(1) != 1):
+            raise ValueError("table: an int32 device tensor [B, max_pages] with contiguous rows")
+        _device_of(k_codes, k_scales, v_codes, v_scales, table)
+        self.k_codes, self.k_scales, self.v_codes, self.v_scales, self.table = k_codes, k_scales, v_codes, v_scales, table
+        P, page, H, _ = k_codes.shape
+        self.view = CbPagedCache4(k_codes.data_ptr(), v_codes.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), P, page, H,
+                                  dim_k, dim_v, *k_codes.stride()[:3], *v_codes.stride()[:3], *k_scales.stride()[:3],
+                                  *v_scales.stride()[:3], table.data_ptr(), table.shape[0], table.shape[1], table.stride(0))
+        self.ref = ctypes.byref(self.view)
+
+    @classmethod
+    def empty(cls, num_pages, page, heads, dim_k, dim_v, table):
+        """A cache with pages of zeros on the table's device."""
+        import torch
+        pages = []
+        for dim in (dim_k, dim_v):
+            for width, dtype in (((dim + 1) // 2, torch.uint8), (scales_per_row(dim), torch.bfloat16)):
+                pages.append(torch.zeros(num_pages, heads, page, width, dtype=dtype, device=table.device).transpose(1, 2))
+        return cls(*pages, table, dim_k=dim_k, dim_v=dim_v)
+
+
+def scales_per_row(dim) -> int:
+    """Scales that a 4-bit cache keeps for a token's head: one for 32 dims, an even number."""
+    return 2 * ((dim + 63) // 64)
 
 
 # ----------------------------------------------------------- host helpers
@@ -563,6 +671,70 @@ def attention_decode(q, cache, length, out, workspace, scale, softcap=0.0, slope
         workspace.numel() * workspace.element_size(), _stream_of(device, stream))
     if st:
         _check(st, "cb_attention_decode")
+    return out
+
+
+def norm_rotate(q, k, pos, rule, q_out=None, k_out=None, stream=None):
+    """cb_norm_rotate on torch CUDA tensors: q [B, L, Hq, D] and k [B, L, Hkv, D] (any strides, the last dim contiguous;
+    k None: queries alone) normed and turned as `rule` (a Rotation) says, at pos int32 [axes, B, L] (any strides over
+    axes and sequences; None where nothing turns).  q_out, k_out: the results, None: in place."""
+    q_out = q if q_out is None else q_out
+    k_out = k if k_out is None else k_out
+    if k is None and k_out is not None:
+        raise ValueError("k_out without k")
+    B, L, _, D = q.shape
+    device = _device_of(q, q_out) if k is None else _device_of(q, k, q_out, k_out)
+    st = (_lib or load()).cb_norm_rotate(heads(q), None if k is None else heads(k), rule.view(B, L, D, pos, device), heads(q_out),
+                                         None if k is None else heads(k_out), _stream_of(device, stream))
+    if st:
+        _check(st, "cb_norm_rotate")
+    return q_out, k_out
+
+
+def cache4_append(k_new, v_new, cache, pos, count=None, stream=None):
+    """cb_cache4_append: `cache_append` for a PagedCache4; k_new and v_new float32 or bfloat16."""
+    kv, vv, B = heads(k_new), heads(v_new), k_new.shape[0]
+    device = _device_of(k_new, v_new, cache.table)
+    st = (_lib or load()).cb_cache4_append(kv, vv, _device_array(pos, "pos", "i32", (B,), device),
+                                           _device_array(count, "count", "i32", (B,), device), cache.ref,
+                                           _stream_of(device, stream))
+    if st:
+        _check(st, "cb_cache4_append")
+
+
+def cache4_read(cache, k_out, v_out, first=None, count=None, stream=None):
+    """cb_cache4_read: the values of a PagedCache4's tokens first[b] + t, t < count[b], as rows t of k_out
+    [B, T, H, Dk] and v_out [B, T, H, Dv] (both float32 or both bfloat16).  first, count: int32 [B] (None: 0; all T)."""
+    kv, vv, B = heads(k_out), heads(v_out), k_out.shape[0]
+    device = _device_of(k_out, v_out, cache.table)
+    st = (_lib or load()).cb_cache4_read(cache.ref, _device_array(first, "first", "i32", (B,), device),
+                                         _device_array(count, "count", "i32", (B,), device), kv, vv, _stream_of(device, stream))
+    if st:
+        _check(st, "cb_cache4_read")
+    return k_out, v_out
+
+
+def attention_decode4_workspace(q, cache) -> int:
+    """cb_attention_decode4_workspace: bytes of scratch for q [B, Hq, Dk] over this PagedCache4."""
+    n = ctypes.c_size_t(0)
+    _check(load().cb_attention_decode4_workspace(_heads1(q), cache.ref, ctypes.byref(n)), "cb_attention_decode4_workspace")
+    return n.value
+
+
+def attention_decode4(q, cache, length, out, workspace, scale, softcap=0.0, slopes=None, first=None, stream=None):
+    """cb_attention_decode4: `attention_decode` over a PagedCache4; q and out both float32 or both bfloat16.
+    workspace: a contiguous uint8 device tensor of attention_decode4_workspace bytes."""
+    qv, ov = _heads1(q), _heads1(out)
+    B, hq, _ = q.shape
+    device = _device_of(q, out, cache.table, workspace)
+    if not workspace.is_contiguous():
+        raise ValueError("workspace: a contiguous device tensor")
+    st = (_lib or load()).cb_attention_decode4(
+        qv, cache.ref, _device_array(length, "length", "i32", (B,), device), _device_array(first, "first", "i32", (B,), device),
+        scale, softcap, _device_array(slopes, "slopes", "f32", (hq,), device), ov, workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _stream_of(device, stream))
+    if st:
+        _check(st, "cb_attention_decode4")
     return out
 
 

@@ -1,10 +1,11 @@
-// Attention of one new token per sequence over a paged cache (cb_attention_decode):
-// the kernel for caches whose rows are not whole 16-byte pieces (the others take
-// decode_stream.cuh) and the join of split sequences.
+// Attention of one new token per sequence over a paged cache (cb_attention_decode,
+// cb_attention_decode4): the kernel for caches whose rows are not whole 16-byte
+// pieces (the others take decode_stream.cuh) and the join of split sequences.
 //
 // Bound by HBM: every key and value of the batch is read once, and one
 // query's 4 FLOP per element are far below the FMA rate until many heads
 // share a key head.  decode_common.cuh says how tokens are dealt.
+#include "cache4.cuh"
 #include "decode_common.cuh"
 #include "launch_util.h"
 #include "ptx.cuh"
@@ -16,7 +17,26 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kHeads = kDecodeSimtHeads;
 
+// A cache's elements: as T, or 4-bit.
 template <typename T>
+struct Elements {
+  static __device__ __forceinline__ float key(const DecodeArgs& a, long long page, long long slot, int hk, int d) {
+    return to_f32(static_cast<const T*>(a.cache.k)[page * a.cache.ks_p + slot * a.cache.ks_t + hk * a.cache.ks_h + d]);
+  }
+  static __device__ __forceinline__ float value(const DecodeArgs& a, long long page, long long slot, int hk, int d) {
+    return to_f32(static_cast<const T*>(a.cache.v)[page * a.cache.vs_p + slot * a.cache.vs_t + hk * a.cache.vs_h + d]);
+  }
+};
+struct Elements4 {
+  static __device__ __forceinline__ float key(const DecodeArgs& a, long long page, long long slot, int hk, int d) {
+    return value4(key_codes4(a.cache, page, slot, hk), key_scales4(a.cache, page, slot, hk), d);
+  }
+  static __device__ __forceinline__ float value(const DecodeArgs& a, long long page, long long slot, int hk, int d) {
+    return value4(value_codes4(a.cache, page, slot, hk), value_scales4(a.cache, page, slot, hk), d);
+  }
+};
+
+template <typename T, class E>
 __global__ void __launch_bounds__(kThreads) decode_simt_kernel(DecodeArgs a) {
   extern __shared__ __align__(16) float smem[];
   const int ldk = (a.dk + 3) / 4 * 4 + 4;
@@ -76,8 +96,7 @@ __global__ void __launch_bounds__(kThreads) decode_simt_kernel(DecodeArgs a) {
         for (int e = tid; e < kDecodeTile * width; e += kThreads) {
           const int r = e / width, d = e - r * width;
           const int page = page_s[r];
-          Ks[r * ldk + d] = page < 0 || d >= a.dk ? 0.f
-                                                  : to_f32(static_cast<const T*>(a.cache.k)[page * a.cache.ks_p + slot_s[r] * a.cache.ks_t + hk * a.cache.ks_h + d]);
+          Ks[r * ldk + d] = page < 0 || d >= a.dk ? 0.f : E::key(a, page, slot_s[r], hk, d);
         }
       }
       __syncthreads();
@@ -134,10 +153,9 @@ __global__ void __launch_bounds__(kThreads) decode_simt_kernel(DecodeArgs a) {
         for (int key = vs; key < kDecodeTile; key += slots) {
           const int page = page_s[key];
           if (page < 0) continue;
-          const T* src = static_cast<const T*>(a.cache.v) + page * a.cache.vs_p + slot_s[key] * a.cache.vs_t + hk * a.cache.vs_h + vd;
           float v[4];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) v[c] = vd + c < a.dv ? to_f32(src[c]) : 0.f;
+          for (int c = 0; c < 4; ++c) v[c] = vd + c < a.dv ? E::value(a, page, slot_s[key], hk, vd + c) : 0.f;
           const float4 pa = *reinterpret_cast<const float4*>(Ps + key * kHeads);
           const float4 pb = *reinterpret_cast<const float4*>(Ps + key * kHeads + 4);
           const float p[kHeads] = {pa.x, pa.y, pa.z, pa.w, pb.x, pb.y, pb.z, pb.w};
@@ -225,12 +243,12 @@ size_t simt_smem(int dk, int dv, int B) {
          sizeof(unsigned) * (B + 1);
 }
 
-template <typename T>
+template <typename T, class E = Elements<T>>
 cudaError_t launch_simt(const DecodeArgs& a, cudaStream_t s) {
   const size_t smem = simt_smem(a.dk, a.dv, a.B);
-  const cudaError_t e = smem_attr_once<decode_simt_kernel<T>>(smem);
+  const cudaError_t e = smem_attr_once<decode_simt_kernel<T, E>>(smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(decode_simt_kernel<T>, dim3(a.ctas), dim3(kThreads), smem, s, a);
+  return launch_pdl(decode_simt_kernel<T, E>, dim3(a.ctas), dim3(kThreads), smem, s, a);
 }
 
 template <typename T>
@@ -271,6 +289,12 @@ cudaError_t launch_decode(const DecodeArgs& a, bool bf16, bool vec, cudaStream_t
   else
     e = bf16 ? launch_simt<__nv_bfloat16>(a, s) : launch_simt<float>(a, s);
   if (e != cudaSuccess || a.split) return e;
+  return bf16 ? launch_join<__nv_bfloat16>(a, s) : launch_join<float>(a, s);
+}
+
+cudaError_t launch_decode4(const DecodeArgs& a, bool bf16, bool vec, cudaStream_t s) {
+  const cudaError_t e = bf16 ? launch_simt<__nv_bfloat16, Elements4>(a, s) : launch_simt<float, Elements4>(a, s);
+  if (e != cudaSuccess) return e;
   return bf16 ? launch_join<__nv_bfloat16>(a, s) : launch_join<float>(a, s);
 }
 

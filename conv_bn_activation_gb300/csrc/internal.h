@@ -340,7 +340,8 @@ void attn_tc_box(int* box_d, int* box_l);
 cudaError_t launch_attn_tc(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const AttnArgs& a, int sms,
                            cudaStream_t s);
 
-// The paged cache as the kernels read it (cb_paged_cache).
+// The paged cache as the kernels read it (cb_paged_cache; cb_paged_cache4, whose
+// codes' strides are bytes and whose scales are bf16).
 struct PagedArgs {
   void* k;
   void* v;
@@ -349,6 +350,10 @@ struct PagedArgs {
   const int* table;
   long long table_stride;
   int num_pages, page_size, max_pages;
+  const uint16_t* k_scale;  // 4-bit caches only
+  const uint16_t* v_scale;
+  long long kx_p, kx_t, kx_h;
+  long long vx_p, vx_t, vx_h;
 };
 struct AppendArgs {
   const void* k;
@@ -363,6 +368,44 @@ struct AppendArgs {
 };
 // piece: bytes moved per access (16, or the element's size where a view is not made of 16-byte pieces).
 cudaError_t launch_cache_append(const AppendArgs& a, int elem_bytes, int piece, int sms, cudaStream_t s);
+
+// cb_cache4_append (AppendArgs: k, v fp32 or bf16 tokens) and cb_cache4_read
+// (cache4.cu).  vec: rows of 16-byte pieces on both sides.
+struct Read4Args {
+  void* k;
+  void* v;
+  long long ks_b, ks_l, ks_h;
+  long long vs_b, vs_l, vs_h;
+  const int* first;
+  const int* count;
+  PagedArgs cache;
+  int B, T, H, dk, dv;
+  int* err;
+};
+cudaError_t launch_cache4_append(const AppendArgs& a, bool bf16, bool vec, int sms, cudaStream_t s);
+cudaError_t launch_cache4_read(const Read4Args& a, bool bf16, bool vec, int sms, cudaStream_t s);
+
+// cb_norm_rotate (norm_rotate.cu): queries, then keys (no heads: none).  vec:
+// every view's rows are 16-byte pieces, and pairs lie in whole pieces.
+struct RotateView {
+  const void* x;
+  void* y;
+  long long xs_b, xs_l, xs_h;
+  long long ys_b, ys_l, ys_h;
+  const float* weight;
+  int heads;
+};
+struct RotateArgs {
+  RotateView v[2];
+  int B, L, dim, rotary, adjacent, norm, axes;
+  float eps;
+  const float* freq;
+  const int* axis;
+  const int* pos;
+  long long ps_a, ps_b;
+  int* err;
+};
+cudaError_t launch_norm_rotate(const RotateArgs& a, bool bf16, bool vec, int sms, cudaStream_t s);
 
 struct DecodeArgs {
   const void* q;
@@ -402,6 +445,7 @@ size_t decode_workspace_bytes(int ctas, int heads, int dv);
 cudaError_t launch_decode_mma(const DecodeArgs& a, cudaStream_t s);  // bf16, rows of whole 16-byte pieces
 cudaError_t launch_decode_fma(const DecodeArgs& a, cudaStream_t s);  // fp32, rows of whole 16-byte pieces
 cudaError_t launch_decode(const DecodeArgs& a, bool bf16, bool vec, cudaStream_t s);
+cudaError_t launch_decode4(const DecodeArgs& a, bool bf16, bool vec, cudaStream_t s);  // 4-bit caches
 // cb_attention with few queries per key head through the streaming kernel:
 // columns are (query, head) pairs, at most kDecodeMmaHeads (bf16) or
 // kDecodeSimtHeads (fp32) of them per item.  Fills a from rw.

@@ -501,6 +501,107 @@ cb_status cb_attention_decode(const cb_heads* q, const cb_paged_cache* cache, co
                               size_t workspace_bytes, void* stream);
 
 /*
+ * How cb_norm_rotate treats the heads of a token:
+ *   norm != 0:  y = x / sqrt(mean_d x^2 + eps) * weight  (weights DEVICE fp32
+ *               [dim], NULL: 1; squares are summed in fp32);  else y = x;
+ *   then pair p of the first `rotary` dims, (p, p + rotary/2) or, adjacent,
+ *   (2p, 2p + 1), turns by pos[axis[p], b, i] * freq[p] radians:
+ *               (y1 cos - y2 sin,  y2 cos + y1 sin);
+ *   the dims behind them stay y.
+ * freq: DEVICE fp32 [rotary/2], finite; axis: DEVICE int [rotary/2] in
+ * [0, axes) (NULL: 0), so that parts of the pairs, or pairs in turn, follow
+ * time, height and width (1 <= axes <= 8).  pos: DEVICE int, element
+ * (a, b, i) at a*pos_stride_axis + b*pos_stride_b + i (non-negative strides).
+ * Angles are reduced in 64-bit fixed point: with |freq| <= 1 the farthest
+ * position is off by 2^-32 of a turn.  A pair whose freq is not finite or
+ * whose axis is outside [0, axes) does not turn, and CB_ERR_INVALID_ARG is
+ * recorded for cb_get_device_error.
+ */
+typedef struct {
+  int norm;
+  float eps;
+  const float* q_weight;
+  const float* k_weight;
+  int rotary, adjacent, axes;
+  const float* freq;
+  const int* axis;
+  const int* pos;
+  long long pos_stride_axis, pos_stride_b;
+} cb_head_rule;
+
+/*
+ * Norms and rotary positions of queries [batch, L, Hq, dim] and keys [batch,
+ * L, Hkv, dim] (k and k_out NULL: queries alone) in one pass: q_out, k_out of
+ * the same shape, either the very same view (in place) or overlapping no view
+ * of the call; no two of an output's rows overlap (its strides nest).  All of
+ * one dtype, aligned to it; arithmetic in fp32, rounded once.  dim at most
+ * 128, rotary even, fewer than 2^31 tokens (else CB_ERR_UNSUPPORTED).  L and
+ * batch may be 0.  One kernel, no workspace.
+ */
+cb_status cb_norm_rotate(const cb_heads* q, const cb_heads* k, const cb_head_rule* rule, cb_heads* q_out,
+                         cb_heads* k_out, void* stream);
+
+/*
+ * A paged cache in 4 bits.  32 consecutive dims of a token's head are a group:
+ *   s = max|x| / 7, rounded to bf16;   c = x / s, rounded to the nearest whole
+ *   number (ties to even) within -7..7 (0 where s is 0);   value = c * s.
+ * Both roundings are exact: the same tokens give the same bits.  A group that
+ * holds an infinity or a NaN has the scale NaN, so its values are NaN.  Byte i
+ * of a row of (dim + 1) / 2 bytes holds c + 8 of dim 2i in its low and of dim
+ * 2i + 1 in its high half.  Row (page, slot, head) of the keys lies at k +
+ * page*k_stride_page + slot*k_stride_slot + head*k_stride_head (BYTES,
+ * non-negative), its scales (DEVICE bf16, one per group, then zeros up to an
+ * even number of them: 2 for dim <= 64, 4 for dim <= 128) at k_scale +
+ * page*ks_stride_page + ... (ELEMENTS, non-negative); the values' likewise.
+ * Pages, table and bad entries are as in cb_paged_cache.  Head-major pages
+ * (k_stride_head the largest in a page) are read in longer runs.
+ */
+typedef struct {
+  void* k;
+  void* v;
+  void* k_scale;
+  void* v_scale;
+  int num_pages, page_size, heads, dim_k, dim_v;
+  long long k_stride_page, k_stride_slot, k_stride_head;
+  long long v_stride_page, v_stride_slot, v_stride_head;
+  long long ks_stride_page, ks_stride_slot, ks_stride_head;
+  long long vs_stride_page, vs_stride_slot, vs_stride_head;
+  const int* table;
+  int batch, max_pages;
+  long long table_stride;
+} cb_paged_cache4;
+
+/*
+ * cb_cache_append for a 4-bit cache: k_new and v_new are fp32 or bf16 (both
+ * the same); dim_k and dim_v at most 128 (else CB_ERR_UNSUPPORTED).
+ */
+cb_status cb_cache4_append(const cb_heads* k_new, const cb_heads* v_new, const int* pos, const int* count,
+                           const cb_paged_cache4* cache, void* stream);
+
+/*
+ * The values that cached tokens stand for: token first[b] + t of sequence b
+ * becomes row t of k_out [batch, T, heads, dim_k] and v_out [batch, T, heads,
+ * dim_v] for t < count[b] (DEVICE int [batch], clamped to [0, T]; NULL: every
+ * t); first: DEVICE int [batch], NULL: 0.  Rows behind them keep what they
+ * hold.  fp32 (exact) or bf16 (rounded once), both outputs the same; what a
+ * prompt's further tokens attend to by cb_attention.  A token whose position
+ * or page is refused (as by cb_cache_append) reads as zeros.  The outputs
+ * overlap neither each other nor the pages, and their rows do not overlap
+ * (their strides nest).
+ */
+cb_status cb_cache4_read(const cb_paged_cache4* cache, const int* first, const int* count, cb_heads* k_out,
+                         cb_heads* v_out, void* stream);
+
+/*
+ * cb_attention_decode over a 4-bit cache: the same arguments and rule, on the
+ * values c * s.  q and out are both fp32 or both bf16.
+ */
+cb_status cb_attention_decode4_workspace(const cb_heads* q, const cb_paged_cache4* cache, size_t* bytes);
+cb_status cb_attention_decode4(const cb_heads* q, const cb_paged_cache4* cache, const int* length, const int* first,
+                               float scale, float softcap, const float* slopes, cb_heads* out, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/*
  * Synchronises `stream`, then reads and clears the library's device error
  * word: CB_ERR_TIMEOUT if a kernel gave up waiting on a barrier since the
  * last call, CB_ERR_INVALID_ARG if one met a bad page-table entry or cache

@@ -1,5 +1,7 @@
 // Entry points of the head norms and rotations and of the 4-bit cache: argument
 // validation, kernel choice and launches.  Host code only.
+#include <initializer_list>
+
 #include "cb.h"
 #include "host_util.h"
 #include "internal.h"
@@ -43,6 +45,24 @@ bool cache_ok(const cb_paged_cache4* c) {
 
 bool aligned(const cb_paged_cache4* c) {
   return reinterpret_cast<uintptr_t>(c->k_scale) % 2 == 0 && reinterpret_cast<uintptr_t>(c->v_scale) % 2 == 0;
+}
+
+// Rows of whole 16-byte pieces of codes, and a row's scales one word: what the streaming kernels copy.
+bool pieces(const void* codes, const void* scales, int dim, std::initializer_list<long long> code_strides,
+            std::initializer_list<long long> scale_strides) {
+  const int unit = dim <= 64 ? 2 : 4;
+  if (dim % 32 != 0 || reinterpret_cast<uintptr_t>(codes) % 16 != 0 || reinterpret_cast<uintptr_t>(scales) % (2 * unit) != 0) return false;
+  for (const long long s : code_strides)
+    if (s % 16 != 0) return false;
+  for (const long long s : scale_strides)
+    if (s % unit != 0) return false;
+  return true;
+}
+bool streams(const cb_paged_cache4* c) {
+  return pieces(c->k, c->k_scale, c->dim_k, {c->k_stride_page, c->k_stride_slot, c->k_stride_head},
+                {c->ks_stride_page, c->ks_stride_slot, c->ks_stride_head}) &&
+         pieces(c->v, c->v_scale, c->dim_v, {c->v_stride_page, c->v_stride_slot, c->v_stride_head},
+                {c->vs_stride_page, c->vs_stride_slot, c->vs_stride_head});
 }
 
 bool overlap(const cb_heads* t, const cb_paged_cache4* c) {
@@ -91,10 +111,18 @@ struct Decode4Plan {
 cb_status plan_decode(const cb_heads* q, const cb_paged_cache4* cache, Decode4Plan* p) {
   const cb_status st = host_device(&p->sms, &p->err);
   if (st != CB_OK) return st;
-  const int group = q->heads / cache->heads;
-  p->chunks = (group + kDecodeSimtHeads - 1) / kDecodeSimtHeads;
+  p->vec = streams(cache);
+  const bool bf16 = q->dtype == CB_DTYPE_BF16;
+  const int group = q->heads / cache->heads, most = !p->vec ? kDecodeSimtHeads : bf16 ? kDecode4Heads : kDecode4HeadsF32;
+  p->chunks = (group + most - 1) / most;
   p->heads = (group + p->chunks - 1) / p->chunks;
-  p->ctas = p->sms * 4;
+  p->ctas = p->sms * (p->vec ? decode4_ctas_per_sm(cache->dim_k, cache->dim_v, bf16, p->heads, q->batch) : 4);
+  // Whole items on clusters where a CTA then walks at most 16 tiles, as for other caches (cb_attention_decode).
+  const long long items = static_cast<long long>(q->batch) * cache->heads * p->chunks;
+  const long long tiles = (static_cast<long long>(cache->max_pages) * cache->page_size + 63) / 64;
+  p->split = 1;
+  while (p->split < 8 && items * p->split * 2 <= p->ctas && p->split < tiles) p->split *= 2;
+  if (!p->vec || tiles > 16LL * p->split) p->split = 0;
   return CB_OK;
 }
 

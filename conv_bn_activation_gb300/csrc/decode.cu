@@ -293,8 +293,12 @@ cudaError_t launch_decode(const DecodeArgs& a, bool bf16, bool vec, cudaStream_t
 }
 
 cudaError_t launch_decode4(const DecodeArgs& a, bool bf16, bool vec, cudaStream_t s) {
-  const cudaError_t e = bf16 ? launch_simt<__nv_bfloat16, Elements4>(a, s) : launch_simt<float, Elements4>(a, s);
-  if (e != cudaSuccess) return e;
+  cudaError_t e;
+  if (vec)
+    e = bf16 ? launch_decode4_bf16(a, s) : launch_decode4_f32(a, s);
+  else
+    e = bf16 ? launch_simt<__nv_bfloat16, Elements4>(a, s) : launch_simt<float, Elements4>(a, s);
+  if (e != cudaSuccess || a.split) return e;
   return bf16 ? launch_join<__nv_bfloat16>(a, s) : launch_join<float>(a, s);
 }
 

@@ -1,0 +1,12 @@
+// Attention over a 4-bit cache with fp32 queries (decode4.cuh).
+#include "decode4.cuh"
+
+namespace cb {
+
+cudaError_t launch_decode4_f32(const DecodeArgs& a, cudaStream_t s) {
+  if (a.dk <= 64)
+    return a.dv <= 64 ? launch_decode4_shape<Decode4Shape<64, 64, 1, float>>(a, s) : launch_decode4_shape<Decode4Shape<64, 128, 1, float>>(a, s);
+  return a.dv <= 64 ? launch_decode4_shape<Decode4Shape<128, 64, 1, float>>(a, s) : launch_decode4_shape<Decode4Shape<128, 128, 1, float>>(a, s);
+}
+
+}  // namespace cb

@@ -1,42 +1,47 @@
 // The streaming kernel of attention over a 4-bit cache (cb_attention_decode4),
 // for rows of whole 16-byte pieces (dims that are multiples of 32).  Tokens are
 // dealt as in decode_common.cuh; a CTA's four warps walk a piece together, each
-// its own kStep tokens of every 4 kStep through its own ring of cp.async copies,
-// as in decode_stream.cuh.
+// its own 32 tokens of every 128 through its own ring of cp.async copies, as in
+// decode_stream.cuh.
 //
-// 4.5 bits an element: at the memory's rate an SM has to turn 42 elements a
-// cycle into products, three lane-instructions each.  So codes go to the MMAs
-// (m16n8k16, f16 operands, fp32 sums) with one AND and half a shift a pair:
-// the bits of a nibble, alone in 16 bits, are the f16 number code * 2^-24, and
-// of the nibble above it code * 2^-20; ldmatrix hands each lane whole bytes of a
-// token (keys) or of two tokens' same dims (values, transposed).  What is left:
-//  - the nibbles hold c + 8.  Keys: 8 sum q of a group goes in as the
+// 4.5 bits an element: at the memory's rate an SM has 97 cycles for 16 tokens of
+// a key head with dims of 128, 388 issue slots and 194 of the integer pipe.  So
+// codes go to the MMAs (m16n8k16, f16 operands, fp32 sums) with one AND and half
+// a shift a pair: the bits of a nibble, alone in 16 bits, are the f16 number
+// code * 2^-24, and of the nibble above it code * 2^-20; ldmatrix hands each lane
+// whole bytes of a token (keys) or of two tokens' same dims (values, transposed).
+// What is left:
+//  - the nibbles hold c + 8.  Keys: -8 sum q of a group goes in as the
 //    accumulator's first value.  Values: one more MMA with -8 everywhere per
 //    tile, in the same step, so that no sum grows with the offset.
 //  - a group's scale: keys, one FMA per score and group on the group's sum;
 //    values, on the weights, a set of weights per group.
 //  - f16's range.  Queries are scaled by a power of two per head (2^15 above),
-//    weights times scales by one per warp, 2^7 below which the largest scale so
-//    far lies; O follows when it grows, as it does a maximum.  Weights below
+//    weights by 2^7 and the values' scales by the power of two above the largest
+//    so far, which O follows when it grows, as it does a maximum.  Weights below
 //    2^-31 of the largest are lost.
-// The MMAs cut what they add off at the largest term's last bits, toward zero.
-// For fp32 that would show, so there queries are two whole numbers of at most
-// 2^11 on a common grid per head (hi + lo 2^-12, 24 bits below the largest
-// element): every product and sum of theirs is exact.  Weights are sums of two
-// f16 numbers (22 bits), and a step's products are added to O by FADDs: cut off
-// at O's last bit in every step, they would lose 2^-23 of it each time.
+// The MMAs add 16 products and the sum so far with all that lies 25 bits below
+// the largest exponent cut off, toward zero, and a subnormal's exponent counts as
+// 2^-14: a step's sums keep 15 bits below their largest term, besides the 11 of a
+// weight.  For fp32 that would show, so there queries are two whole numbers of at
+// most 2^11 on a common grid per head (hi + lo 2^-12, 24 bits below the largest
+// element), whose products and sums are exact; weights are sums of two f16
+// numbers (22 bits), codes are made f16 numbers of their own size, and a step's
+// products are added to O by FADDs.
 #pragma once
 
 #include <cuda_fp16.h>
+
+#include <type_traits>
 
 #include "cache4.cuh"
 #include "decode_stream.cuh"
 
 namespace cb {
 
-__device__ __forceinline__ void cp_async_small(uint32_t dst, const void* src, bool valid, int bytes) {
-  if (bytes == 8) asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(valid ? 8 : 0) : "memory");
-  else asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(valid ? 4 : 0) : "memory");
+template <int BYTES>
+__device__ __forceinline__ void cp_async_small(uint32_t dst, const void* src, bool valid) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(valid ? BYTES : 0) : "memory");
 }
 __device__ __forceinline__ void ldsm4_4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -55,7 +60,14 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
 }
-// d (16 x 8, fp32) += a (16 x 16, f16) * b (16 x 8, f16)
+// d (16 x 8, fp32) = c + a (16 x 16, f16) * b (16 x 8, f16)
+__device__ __forceinline__ void mma_f16(float (&d)[4], float c0, float c1, float c2, float c3, uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+}
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -64,6 +76,11 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
 }
 __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t half2_times(uint32_t x, float bits) {  // bits: a pair of f16 numbers
+  const uint32_t y = __float_as_uint(bits);
+  const __half2 h = __hmul2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&y));
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 // What f16 rounding left of a pair: another pair of f16 numbers.
@@ -85,13 +102,13 @@ __device__ __forceinline__ uint32_t high_codes(uint32_t w) {
   const __half2 h = __hfma2(*reinterpret_cast<const __half2*>(&x), __float2half2_rn(0.0625f), __float2half2_rn(-72.f));
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-constexpr int kWeightBits = 7;  // weights times the largest scale: up to 2^(kDecodeGrowth + kWeightBits) = 2^15
-constexpr int kMinTopExp = -119;  // 2^(kWeightBits - top_exp) is an fp32 number
+constexpr int kWeightBits = 7;     // weights go up to 2^(kDecodeGrowth + kWeightBits) = 2^15
+constexpr int kMinTopExp = -119;  // 2^-top_exp is an fp32 number
 
 template <int DK_, int DV_, int NB_, typename T_>
 struct Decode4Shape {
   using T = T_;
-  static constexpr int DK = DK_, DV = DV_, NB = NB_, kStep = 16, kStages = 4, kHeads = 8 * NB_;
+  static constexpr int DK = DK_, DV = DV_, NB = NB_, kStep = 32, kStages = 2, kHeads = 8 * NB_;
   static constexpr int kParts = sizeof(T) == 4 ? 2 : 1;
   static constexpr int GK = DK / kGroup4, GV = DV / kGroup4;
   static constexpr int kKeyBytes = DK / 2, kValBytes = DV / 2;
@@ -100,7 +117,7 @@ struct Decode4Shape {
   static constexpr int kRing = kDecodeWarps * kStages * kStageBytes;
   static constexpr int kResults = 4 * (kDecodeWarps + 1) * kHeads * DV;  // the warps' and the CTA's, when a piece ends
   static constexpr int kMain = kRing > kResults ? kRing : kResults;
-  static constexpr int kScaleArea = 2 * kStep * 16;  // a step's scales as fp32, per warp
+  static constexpr int kScaleArea = kStep * 2 * 16;  // a step's scales, per warp: keys' fp32, values' fp32 or f16
   static constexpr int kSmem = kMain + kDecodeWarps * kScaleArea;
   static constexpr int kCtasPerSm = decode4_ctas_per_sm(DK, DV, sizeof(T) == 2, kHeads, 0);
 };
@@ -124,7 +141,8 @@ struct Decode4Math {
   uint32_t qf[S::kParts][GK][NB][4];
   float first[S::kParts][GK][NB][2];  // -8 sum q of this thread's heads 8 nb + 2 t4 and the one after
   float k_mul, head_mul[NB][2];
-  float slope[NB][2], m[NB][2], l[NB][2], o[2 * GV][NB][4];
+  // neg = kWeightBits - maximum (+infinity before the first token): weights are 2^(x + neg).
+  float slope[NB][2], neg[NB][2], l[NB][2], o[2 * GV][NB][4];
 
   __device__ __forceinline__ Decode4Math(const DecodeArgs& a, const Piece& pc) : score(a) {
     const int lane = threadIdx.x & 31;
@@ -196,7 +214,7 @@ struct Decode4Math {
 #pragma unroll
           for (int i = 0; i < GK; ++i) first[p][i][nb][e] = __shfl_sync(~0u, sums[p][i][nb], from);
         slope[nb][e] = a.slopes && hd < heads ? a.slopes[pc.h0 + hd] * kLog2e : 0.f;
-        m[nb][e] = kNegInf;
+        neg[nb][e] = __builtin_huge_valf();
         l[nb][e] = 0.f;
       }
 #pragma unroll
@@ -215,139 +233,68 @@ struct Decode4Math {
         for (int r = 0; r < 4; ++r) o[d][nb][r] *= f[nb][r & 1];
   }
 
-  // 16 tokens of a stage; bit x of lv: token x exists; far: the first one's distance from the query.  area: this
-  // warp's scales as fp32, [keys, values][token][group].
-  __device__ __forceinline__ void step(uint32_t st, unsigned lv, int far, const DecodeArgs& a, float4* area) {
-    const int lane = threadIdx.x & 31;
-    {  // lanes 0 to 15: the keys' scales of their token; 16 to 31: the values'
-      const bool is_v = lane >= 16;
-      const int groups = is_v ? GV : GK, real = is_v ? a.dv : a.dk;
-      const uint32_t at = st + (is_v ? S::kValScales + (lane - 16) * GV * 2 : S::kKeyScales + lane * GK * 2);
-      uint32_t w0, w1 = 0;
-      if (GK == GV ? GK == 4 : groups == 4) asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w0), "=r"(w1) : "r"(at) : "memory");
-      else asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w0) : "r"(at) : "memory");
-      const bool live = (lv >> (lane & 15)) & 1;
-      if (!live) w0 = w1 = 0;
-      if (real <= 32) w0 &= 0xffffu;
-      if (real <= 96) w1 &= 0xffffu;
-      float4 f = make_float4(__uint_as_float(w0 << 16), __uint_as_float(w0 & 0xffff0000u), __uint_as_float(w1 << 16),
-                             __uint_as_float(w1 & 0xffff0000u));
-      float big = is_v ? fmaxf(fmaxf(f.x, f.y), fmaxf(f.z, f.w)) : 0.f;  // NaN only where all are
-      if (!(big < __builtin_huge_valf())) big = 0.f;
-      const unsigned top = __reduce_max_sync(~0u, __float_as_uint(big));
-      const int e = static_cast<int>(top >> 23) - 126;  // below 2^e
-      if (e > top_exp) {
-        const float f2 = exp2_approx(static_cast<float>(top_exp - e));
-        top_exp = e;
-        float all[NB][2];
+  // Scores of 16 tokens before the heads' factors: element r is key g + 8 (r >> 1), head 8 nb + 2 t4 + (r & 1).
+  __device__ __forceinline__ void scores(float (&s)[NB][4], uint32_t keys, const float4* area) const {
+    const float4 x0 = area[g], x1 = area[g + 8];
+    const float k0[4] = {x0.x, x0.y, x0.z, x0.w}, k1[4] = {x1.x, x1.y, x1.z, x1.w};
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) all[nb][0] = all[nb][1] = f2;
-        rescale(all);
-      }
-      const float mul = is_v ? __uint_as_float(static_cast<unsigned>(127 + kWeightBits - top_exp) << 23) : k_mul;
-      f.x *= mul, f.y *= mul, f.z *= mul, f.w *= mul;
-      area[lane] = f;
-      __syncwarp();
-    }
-    float s[NB][4];  // element r: key g + 8 (r >> 1), head 8 nb + 2 t4 + (r & 1)
+    for (int i = 0; i < GK; i += 2) {
+      uint32_t w[4];  // groups i and i + 1: a word of key g and of key g + 8
+      ldsm4_4((keys + k_src) ^ (i * 16), w);
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
+      for (int j = 0; j < 2; ++j) {
+        const uint32_t u = w[2 * j], v = w[2 * j + 1], u8 = u >> 8, v8 = v >> 8;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) s[nb][r] = 0.f;
-    {
-      const float4 x0 = area[g], x1 = area[g + 8];
-      const float k0[4] = {x0.x, x0.y, x0.z, x0.w}, k1[4] = {x1.x, x1.y, x1.z, x1.w};
+        for (int nb = 0; nb < NB; ++nb) {
+          float acc[S::kParts][4];
 #pragma unroll
-      for (int i = 0; i < GK; i += 2) {
-        uint32_t w[4];  // groups i and i + 1: a word of key g and of key g + 8
-        ldsm4_4((st + k_src) ^ (i * 16), w);
+          for (int p = 0; p < S::kParts; ++p) {
+            const float f0 = first[p][i + j][nb][0], f1 = first[p][i + j][nb][1];
+            const uint32_t(&q)[4] = qf[p][i + j][nb];
+            mma_f16(acc[p], f0, f1, f0, f1, u & kLowNibble, v & kLowNibble, u & kHighNibble, v & kHighNibble, q[0], q[1]);
+            mma_f16(acc[p], u8 & kLowNibble, v8 & kLowNibble, u8 & kHighNibble, v8 & kHighNibble, q[2], q[3]);
+          }
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const uint32_t u = w[2 * j], v = w[2 * j + 1], u8 = u >> 8, v8 = v >> 8;
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb) {
-            float acc[S::kParts][4];
-#pragma unroll
-            for (int p = 0; p < S::kParts; ++p) {
-              const float(&f)[2] = first[p][i + j][nb];
-              acc[p][0] = acc[p][2] = f[0], acc[p][1] = acc[p][3] = f[1];
-              const uint32_t(&q)[4] = qf[p][i + j][nb];
-              mma_f16(acc[p], u & kLowNibble, v & kLowNibble, u & kHighNibble, v & kHighNibble, q[0], q[1]);
-              mma_f16(acc[p], u8 & kLowNibble, v8 & kLowNibble, u8 & kHighNibble, v8 & kHighNibble, q[2], q[3]);
-            }
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const float sum = S::kParts == 2 ? fmaf(acc[S::kParts - 1][r], 0x1p-12f, acc[0][r]) : acc[0][r];
-              s[nb][r] = fmaf(sum, r < 2 ? k0[i + j] : k1[i + j], s[nb][r]);
-            }
+          for (int r = 0; r < 4; ++r) {
+            const float sum = S::kParts == 2 ? fmaf(acc[S::kParts - 1][r], 0x1p-12f, acc[0][r]) : acc[0][r], k = r < 2 ? k0[i + j] : k1[i + j];
+            s[nb][r] = i + j == 0 ? sum * k : fmaf(sum, k, s[nb][r]);
           }
         }
       }
     }
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) s[nb][r] *= head_mul[nb][r & 1];
-    if (score.cap) score(s);  // x = log2(e) * score
-    const float dist = static_cast<float>(far - g);
-    bool grow = false;
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        float x = s[nb][r];
-        if (bias) x = fmaf(-slope[nb][r & 1], dist - 8.f * (r >> 1), x);
-        if (lv != 0xffffu && !((lv >> (g + 8 * (r >> 1))) & 1)) x = kNegInf;
-        s[nb][r] = x;
-        grow |= x > m[nb][r & 1] + kDecodeGrowth;
-      }
-    if (__any_sync(~0u, grow)) {
-      float f[NB][2];
+  }
+
+  // O += weights (of 16 tokens, in s) times values.  area: S::kParts == 1, [token pair][group] pairs of f16 scales;
+  // else [token] four fp32 scales.
+  __device__ __forceinline__ void outputs(const float (&s)[NB][4], uint32_t vals, const float4* area) {
+    constexpr bool kF16 = S::kParts == 1;
+    const float4 x0 = area[kF16 ? t4 : g], x1 = area[kF16 ? t4 + 4 : g + 8];
+    const float c0[4] = {x0.x, x0.y, x0.z, x0.w}, c1[4] = {x1.x, x1.y, x1.z, x1.w};
+    uint32_t b[NB][2];
+    if constexpr (kF16)
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float y = fmaxf(s[nb][e], s[nb][2 + e]);
-          y = fmaxf(y, __shfl_xor_sync(~0u, y, 4));
-          y = fmaxf(y, __shfl_xor_sync(~0u, y, 8));
-          y = fmaxf(y, __shfl_xor_sync(~0u, y, 16));
-          const float mn = fmaxf(m[nb][e], y);
-          f[nb][e] = mn == kNegInf ? 1.f : exp2_approx(m[nb][e] - mn);
-          m[nb][e] = mn;
-          l[nb][e] *= f[nb][e];
-        }
-      rescale(f);
-    }
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-      const float mu0 = m[nb][0] == kNegInf ? 0.f : m[nb][0], mu1 = m[nb][1] == kNegInf ? 0.f : m[nb][1];
-#pragma unroll
-      for (int r = 0; r < 4; ++r) s[nb][r] = exp2_approx(s[nb][r] - (r & 1 ? mu1 : mu0));
-      l[nb][0] += s[nb][0] + s[nb][2];
-      l[nb][1] += s[nb][1] + s[nb][3];
-    }
-    const float4 x0 = area[16 + g], x1 = area[24 + g];
-    const float v0[4] = {x0.x, x0.y, x0.z, x0.w}, v1[4] = {x1.x, x1.y, x1.z, x1.w};
+        for (int r = 0; r < 2; ++r) b[nb][r] = transpose8x8(half2_bits(s[nb][2 * r], s[nb][2 * r + 1]));
 #pragma unroll
     for (int i = 0; i < GV; i += 2) {
       uint32_t w[4];  // groups i and i + 1: dims 4 g .. + 4 of tokens 2 t4, 2 t4 + 1 and of those + 8
-      ldsm4_4t((st + S::kStep * S::kKeyBytes + v_src) ^ (i * 16), w);
+      ldsm4_4t((vals + v_src) ^ (i * 16), w);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const uint32_t u = w[2 * j], v = w[2 * j + 1], u8 = u >> 8, v8 = v >> 8;
-        const float c0 = v0[i + j], c1 = v1[i + j];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-          const float p0 = s[nb][0] * c0, p1 = s[nb][1] * c0, p2 = s[nb][2] * c1, p3 = s[nb][3] * c1;
-          uint32_t lo = half2_bits(p0, p1), hi = half2_bits(p2, p3);
-          if constexpr (S::kParts == 1) {
-            const uint32_t b0 = transpose8x8(lo), b1 = transpose8x8(hi);
-            float(&d0)[4] = o[2 * (i + j)][nb], (&d1)[4] = o[2 * (i + j) + 1][nb];
+          float(&d0)[4] = o[2 * (i + j)][nb], (&d1)[4] = o[2 * (i + j) + 1][nb];
+          if constexpr (kF16) {
+            const uint32_t b0 = half2_times(b[nb][0], c0[i + j]), b1 = half2_times(b[nb][1], c1[i + j]);
             mma_f16(d0, u & kLowNibble, u & kHighNibble, v & kLowNibble, v & kHighNibble, b0, b1);
             mma_f16(d1, u8 & kLowNibble, u8 & kHighNibble, v8 & kLowNibble, v8 & kHighNibble, b0, b1);
             mma_f16(d0, kLowMinus8, kHighMinus8, kLowMinus8, kHighMinus8, b0, b1);
             mma_f16(d1, kLowMinus8, kHighMinus8, kLowMinus8, kHighMinus8, b0, b1);
           } else {
+            const float p0 = s[nb][0] * c0[i + j], p1 = s[nb][1] * c0[i + j], p2 = s[nb][2] * c1[i + j], p3 = s[nb][3] * c1[i + j];
+            uint32_t lo = half2_bits(p0, p1), hi = half2_bits(p2, p3);
             float fresh[2][4] = {};
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
@@ -357,10 +304,134 @@ struct Decode4Math {
               mma_f16(fresh[1], low_codes(u8), high_codes(u8), low_codes(v8), high_codes(v8), b0, b1);
             }
 #pragma unroll
-            for (int r = 0; r < 4; ++r) o[2 * (i + j)][nb][r] += fresh[0][r], o[2 * (i + j) + 1][nb][r] += fresh[1][r];
+            for (int r = 0; r < 4; ++r) d0[r] += fresh[0][r], d1[r] += fresh[1][r];
           }
         }
       }
+    }
+  }
+
+  // The step's scales as the products take them, a token per lane: area [32] keys', then values'.
+  template <bool FULL>
+  __device__ __forceinline__ void scales(uint32_t st, unsigned lv, const DecodeArgs& a, float4* area) {
+    const int lane = threadIdx.x & 31;
+    const bool live = FULL || ((lv >> lane) & 1);
+    auto load = [&](uint32_t at, int groups, int dim) {
+      uint32_t w0, w1 = 0;
+      if (groups == 4) asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w0), "=r"(w1) : "r"(at) : "memory");
+      else asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w0) : "r"(at) : "memory");
+      if (!live) w0 = w1 = 0;
+      if (groups == 2 && dim <= 32) w0 &= 0xffffu;
+      if (groups == 4 && dim <= 96) w1 &= 0xffffu;
+      return make_float4(__uint_as_float(w0 << 16), __uint_as_float(w0 & 0xffff0000u), __uint_as_float(w1 << 16),
+                         __uint_as_float(w1 & 0xffff0000u));
+    };
+    float4 k = load(st + S::kKeyScales + lane * GK * 2, GK, a.dk), v = load(st + S::kValScales + lane * GV * 2, GV, a.dv);
+    k.x *= k_mul, k.y *= k_mul, k.z *= k_mul, k.w *= k_mul;
+    area[lane] = k;
+    float big = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w));  // NaN only where all are
+    if (!(big < __builtin_huge_valf())) big = 0.f;
+    const int e = static_cast<int>(__reduce_max_sync(~0u, __float_as_uint(big)) >> 23) - 126;  // below 2^e
+    if (e > top_exp) {
+      const float f2 = exp2_approx(static_cast<float>(top_exp - e));
+      top_exp = e;
+      float all[NB][2];
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) all[nb][0] = all[nb][1] = f2;
+      rescale(all);
+    }
+    const float mul = __uint_as_float(static_cast<unsigned>(127 - top_exp) << 23);
+    v.x *= mul, v.y *= mul, v.z *= mul, v.w *= mul;
+    if constexpr (S::kParts == 2) {
+      area[32 + lane] = v;
+    } else {
+      // Tokens' pairs side by side: an even lane takes groups 0 and 1 of the pair, an odd one 2 and 3.
+      const uint32_t h01 = half2_bits(v.x, v.y), h23 = half2_bits(v.z, v.w);
+      const bool odd = lane & 1;
+      const uint32_t own = odd ? h23 : h01, other = __shfl_xor_sync(~0u, odd ? h01 : h23, 1);
+      const uint32_t lo = odd ? other : own, hi = odd ? own : other;
+      reinterpret_cast<uint2*>(area + 32)[lane] = make_uint2(__byte_perm(lo, hi, 0x5410), __byte_perm(lo, hi, 0x7632));
+    }
+    __syncwarp();
+  }
+
+  // 32 tokens of a stage; bit x of lv: token x exists (FULL: all do); far: the first one's distance from the query.
+  template <bool FULL>
+  __device__ __forceinline__ void step(uint32_t st, unsigned lv, int far, const DecodeArgs& a, float4* area) {
+    scales<FULL>(st, lv, a, area);
+    const float dist = static_cast<float>(far - g);
+    float s[2][NB][4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) scores(s[h], st + h * 16 * S::kKeyBytes, area + 16 * h);
+    // What the exponential takes: x + neg, x = log2(e) * score.
+    const bool direct = !score.cap && !bias;
+    float y[2][NB][4];
+    if (!direct) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) s[h][nb][r] *= head_mul[nb][r & 1];
+        if (score.cap) score(s[h]);
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) s[h][nb][r] = fmaf(-slope[nb][r & 1], dist - 16.f * h - 8.f * (r >> 1), s[h][nb][r]);
+      }
+    }
+    auto exponents = [&](const float (&add)[NB][2]) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            y[h][nb][r] = direct ? fmaf(s[h][nb][r], head_mul[nb][r & 1], add[nb][r & 1]) : s[h][nb][r] + add[nb][r & 1];
+            if (!FULL && !((lv >> (g + 8 * (r >> 1) + 16 * h)) & 1)) y[h][nb][r] = kNegInf;
+          }
+    };
+    exponents(neg);
+    bool grow = false;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) grow |= !(y[h][nb][r] <= kDecodeGrowth + kWeightBits);
+    if (__any_sync(~0u, grow)) {
+      float zero[NB][2], f[NB][2], now[NB][2];
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) zero[nb][0] = zero[nb][1] = 0.f;
+      exponents(zero);
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float x = fmaxf(fmaxf(y[0][nb][e], y[0][nb][2 + e]), fmaxf(y[1][nb][e], y[1][nb][2 + e]));
+          x = fmaxf(x, __shfl_xor_sync(~0u, x, 4));
+          x = fmaxf(x, __shfl_xor_sync(~0u, x, 8));
+          x = fmaxf(x, __shfl_xor_sync(~0u, x, 16));
+          // Before the first token the maximum is -infinity: what is multiplied then is 0.
+          const float was = kWeightBits - neg[nb][e], mn = fmaxf(was, x);
+          f[nb][e] = was == kNegInf ? 1.f : exp2_approx(was - mn);
+          neg[nb][e] = kWeightBits - mn;
+          now[nb][e] = mn == kNegInf ? 0.f : neg[nb][e];
+          l[nb][e] *= f[nb][e];
+        }
+      rescale(f);
+      exponents(now);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) y[h][nb][r] = exp2_approx(y[h][nb][r]);
+        l[nb][0] += y[h][nb][0] + y[h][nb][2];
+        l[nb][1] += y[h][nb][1] + y[h][nb][3];
+      }
+      outputs(y[h], st + S::kStep * S::kKeyBytes + h * 16 * S::kValBytes, area + 32 + (S::kParts == 1 ? 8 : 16) * h);
     }
   }
 
@@ -376,14 +447,14 @@ struct Decode4Math {
         y += __shfl_xor_sync(~0u, y, 8);
         y += __shfl_xor_sync(~0u, y, 16);
         const int hd = 8 * nb + 2 * t4 + e;
-        if (g == 0) ms[hd] = y == 0.f ? kNegInf : m[nb][e] + log2f(y), ls[hd] = y == 0.f ? 0.f : y == y ? 1.f : y;
+        if (g == 0) ms[hd] = y == 0.f ? kNegInf : log2f(y) - neg[nb][e], ls[hd] = y == 0.f ? 0.f : y == y ? 1.f : y;
         const float inv = y == 0.f ? 0.f : 1.f / y;
         if (hd < heads)
 #pragma unroll
           for (int d = 0; d < 2 * GV; ++d)
             *reinterpret_cast<float2*>(res + hd * S::DV + 16 * (d & ~1) + 4 * g + 2 * (d & 1)) =
-                make_float2(ldexpf(o[d][nb][e] * inv, top_exp - kWeightBits + (S::kParts == 1 ? 24 : 0)),
-                            ldexpf(o[d][nb][2 + e] * inv, top_exp - kWeightBits + (S::kParts == 1 ? 20 : 0)));
+                make_float2(ldexpf(o[d][nb][e] * inv, top_exp + (S::kParts == 1 ? 24 : 0)),
+                            ldexpf(o[d][nb][2 + e] * inv, top_exp + (S::kParts == 1 ? 20 : 0)));
       }
   }
 };
@@ -421,9 +492,8 @@ __global__ void __launch_bounds__(kDecodeThreads, S::kCtasPerSm) decode4_stream_
   float4* area = reinterpret_cast<float4*>(smem + S::kMain + warp * S::kScaleArea);
   const uint32_t k_dst = (lane / CK) * S::kKeyBytes + (((lane % CK) ^ swizzle4<S::kKeyBytes>(lane / CK)) * 16);
   const uint32_t v_dst = kStep * S::kKeyBytes + (lane / CV) * S::kValBytes + (((lane % CV) ^ swizzle4<S::kValBytes>(lane / CV)) * 16);
-  const uint32_t x_dst = lane < 16 ? S::kKeyScales + lane * S::GK * 2 : S::kValScales + (lane - 16) * S::GV * 2;
-  const long long xs_p = lane < 16 ? a.cache.kx_p : a.cache.vx_p, xs_t = lane < 16 ? a.cache.kx_t : a.cache.vx_t;
   const bool same = a.cache.ks_p == a.cache.vs_p && a.cache.ks_t == a.cache.vs_t;  // one offset serves both
+  const bool same_x = a.cache.kx_p == a.cache.vx_p && a.cache.kx_t == a.cache.vx_t;
   // from a lane's token to its next one, without a division per step
   const int adv_pg = kDecodeWarps * kStep / a.cache.page_size, adv_slot = kDecodeWarps * kStep - adv_pg * a.cache.page_size;
 
@@ -433,25 +503,27 @@ __global__ void __launch_bounds__(kDecodeThreads, S::kCtasPerSm) decode4_stream_
     else pc = next_piece(a, prefix, per_seq, at, end, &b);
     const char* kbase = static_cast<const char*>(a.cache.k) + pc.hk * a.cache.ks_h + (lane % CK) * 16;
     const char* vbase = static_cast<const char*>(a.cache.v) + pc.hk * a.cache.vs_h + (lane % CV) * 16;
-    const uint16_t* xbase = lane < 16 ? a.cache.k_scale + pc.hk * a.cache.kx_h : a.cache.v_scale + pc.hk * a.cache.vx_h;
+    const uint16_t* kxbase = a.cache.k_scale + pc.hk * a.cache.kx_h;
+    const uint16_t* vxbase = a.cache.v_scale + pc.hk * a.cache.vx_h;
 
     const int base = pc.tile0 * kDecodeTile + warp * kStep;
-    const int steps = pc.tiles * (kDecodeTile / (kDecodeWarps * kStep));
-    // Lanes look the step's tokens up (lane and lane + 16 the same one), one step before their copies are issued:
-    // the byte offsets of the rows, or -1.
+    const int steps = (pc.tiles * kDecodeTile + kDecodeWarps * kStep - 1) / (kDecodeWarps * kStep);
+    const unsigned limit = static_cast<unsigned>(min(static_cast<long long>(pc.hi), (pc.tile0 + static_cast<long long>(pc.tiles)) * kDecodeTile));
+    // Lanes look the step's tokens up, one step before their copies are issued: the byte offsets of the rows, or -1.
     struct Rows {
-      long long k, v, x;
+      long long k, v, kx, vx;
     };
-    unsigned j = base + lane % kStep;  // unsigned: a token looked up past the piece's end may be past 2^31
+    unsigned j = base + lane;  // unsigned: a token looked up past the piece's end may be past 2^31
     int pg = static_cast<int>(j) / a.cache.page_size, slot = static_cast<int>(j) - pg * a.cache.page_size;
     auto lookup = [&](int step) {  // once for each step, in order
-      Rows r{-1, -1, 0};
-      if (step < steps && j >= static_cast<unsigned>(pc.lo) && j < static_cast<unsigned>(pc.hi)) {
+      Rows r{-1, -1, 0, 0};
+      if (step < steps && j >= static_cast<unsigned>(pc.lo) && j < limit) {
         const long long page = checked_page(a, pc.b, pg);
         if (page >= 0) {
           r.k = page * a.cache.ks_p + slot * a.cache.ks_t;
           r.v = same ? r.k : page * a.cache.vs_p + slot * a.cache.vs_t;
-          r.x = page * xs_p + slot * xs_t;
+          r.kx = page * a.cache.kx_p + slot * a.cache.kx_t;
+          r.vx = same_x ? r.kx : page * a.cache.vx_p + slot * a.cache.vx_t;
         }
       }
       j += kDecodeWarps * kStep;
@@ -459,39 +531,44 @@ __global__ void __launch_bounds__(kDecodeThreads, S::kCtasPerSm) decode4_stream_
       if (slot >= a.cache.page_size) slot -= a.cache.page_size, ++pg;
       return r;
     };
-    unsigned live[kStages];  // bit x: token x of the stage's step exists
     auto issue = [&](int step, int stage, const Rows& rows) {
-      const unsigned have = __ballot_sync(~0u, rows.k >= 0) & 0xffffu;
+      const unsigned have = __ballot_sync(~0u, rows.k >= 0);
       if (step < steps) {
         const uint32_t st = ring + stage * S::kStageBytes;
+        auto copies = [&](auto full) {
+          constexpr bool kFull = decltype(full)::value;
 #pragma unroll
-        for (int i = 0; i < kStep / RK; ++i) {
-          const int r = i * RK + lane / CK;
-          const long long off = __shfl_sync(~0u, rows.k, r);
-          const bool ok = (have >> r) & 1;
-          if (lane % CK < kq) cp_async16((st + k_dst + i * RK * S::kKeyBytes) ^ (swizzle4<S::kKeyBytes>(i * RK) * 16), ok ? kbase + off : kbase, ok);
-          if (CK == CV) {
-            const long long to = same ? off : __shfl_sync(~0u, rows.v, r);
-            if (lane % CV < vq) cp_async16((st + v_dst + i * RV * S::kValBytes) ^ (swizzle4<S::kValBytes>(i * RV) * 16), ok ? vbase + to : vbase, ok);
+          for (int i = 0; i < kStep / RK; ++i) {
+            const int r = i * RK + lane / CK;
+            const long long off = __shfl_sync(~0u, rows.k, r);
+            const bool ok = kFull || ((have >> r) & 1);
+            if (lane % CK < kq) cp_async16((st + k_dst + i * RK * S::kKeyBytes) ^ (swizzle4<S::kKeyBytes>(i * RK) * 16), ok ? kbase + off : kbase, ok);
+            if (CK == CV) {
+              const long long to = same ? off : __shfl_sync(~0u, rows.v, r);
+              if (lane % CV < vq) cp_async16((st + v_dst + i * RV * S::kValBytes) ^ (swizzle4<S::kValBytes>(i * RV) * 16), ok ? vbase + to : vbase, ok);
+            }
           }
-        }
-        if (CK != CV) {
+          if (CK != CV) {
 #pragma unroll
-          for (int i = 0; i < kStep / RV; ++i) {
-            const int r = i * RV + lane / CV;
-            const long long to = __shfl_sync(~0u, rows.v, r);
-            const bool ok = (have >> r) & 1;
-            if (lane % CV < vq) cp_async16((st + v_dst + i * RV * S::kValBytes) ^ (swizzle4<S::kValBytes>(i * RV) * 16), ok ? vbase + to : vbase, ok);
+            for (int i = 0; i < kStep / RV; ++i) {
+              const int r = i * RV + lane / CV;
+              const long long to = __shfl_sync(~0u, rows.v, r);
+              const bool ok = kFull || ((have >> r) & 1);
+              if (lane % CV < vq) cp_async16((st + v_dst + i * RV * S::kValBytes) ^ (swizzle4<S::kValBytes>(i * RV) * 16), ok ? vbase + to : vbase, ok);
+            }
           }
-        }
-        const bool ok = rows.k >= 0;
-        const int bytes = 2 * (S::GK == S::GV ? S::GK : lane < 16 ? S::GK : S::GV);
-        cp_async_small(st + x_dst, ok ? xbase + rows.x : xbase, ok, bytes);
+          const bool ok = kFull || rows.k >= 0;
+          cp_async_small<2 * S::GK>(st + S::kKeyScales + lane * S::GK * 2, ok ? kxbase + rows.kx : kxbase, ok);
+          cp_async_small<2 * S::GV>(st + S::kValScales + lane * S::GV * 2, ok ? vxbase + rows.vx : vxbase, ok);
+        };
+        if (have == ~0u) copies(std::true_type{});
+        else copies(std::false_type{});
       }
       cp_async_commit();
       return have;
     };
 
+    unsigned live[kStages - 1];  // of the next steps: bit x, token x exists
 #pragma unroll
     for (int s = 0; s < kStages - 1; ++s) live[s] = issue(s, s, lookup(s));
     Decode4Math<S> c(a, pc);  // the queries are read while the first tokens come
@@ -500,20 +577,16 @@ __global__ void __launch_bounds__(kDecodeThreads, S::kCtasPerSm) decode4_stream_
     for (int step = 0; step < steps; ++step) {
       const int fill = stage == 0 ? kStages - 1 : stage - 1;  // the stage read in the last step
       __syncwarp();
-      {
-        const unsigned lv = issue(step + kStages - 1, fill, rows);
+      const unsigned lv = live[0], next = issue(step + kStages - 1, fill, rows);
 #pragma unroll
-        for (int s = 0; s < kStages; ++s)
-          if (s == fill) live[s] = lv;
-      }
+      for (int s = 0; s + 1 < kStages - 1; ++s) live[s] = live[s + 1];
+      live[kStages - 2] = next;
       rows = lookup(step + kStages);
       cp_async_wait<kStages - 1>();
       __syncwarp();
-      unsigned lv = 0;
-#pragma unroll
-      for (int s = 0; s < kStages; ++s)
-        if (s == stage) lv = live[s];
-      c.step(ring + stage * S::kStageBytes, lv, pc.len - 1 - (base + step * (kDecodeWarps * kStep)), a, area);
+      const int far = pc.len - 1 - (base + step * (kDecodeWarps * kStep));
+      if (lv == ~0u) c.template step<true>(ring + stage * S::kStageBytes, lv, far, a, area);
+      else if (lv) c.template step<false>(ring + stage * S::kStageBytes, lv, far, a, area);
       stage = stage + 1 == kStages ? 0 : stage + 1;
     }
     cp_async_wait<0>();

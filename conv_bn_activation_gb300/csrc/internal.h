@@ -449,8 +449,8 @@ cudaError_t launch_decode(const DecodeArgs& a, bool bf16, bool vec, cudaStream_t
 // CTAs that an SM holds: by registers 4, 3 or 2, and no more than its shared memory does.
 constexpr int decode4_ctas_per_sm(int dk, int dv, bool bf16, int heads, int batch) {
   const int DK = dk <= 64 ? 64 : 128, DV = dv <= 64 ? 64 : 128, hd = heads <= 8 ? 8 : 16;
-  const int most = !bf16 || hd == 16 ? 2 : 4, ring = 4 * 4 * 16 * 9 * (DK + DV) / 16, results = 4 * 5 * hd * DV;
-  const int bytes = (ring > results ? ring : results) + 4 * 512 + 4 * (batch + 1) + 1824, fit = 233472 / bytes;
+  const int most = !bf16 || hd == 16 ? 2 : 4, ring = 4 * 2 * 32 * 9 * (DK + DV) / 16, results = 4 * 5 * hd * DV;
+  const int bytes = (ring > results ? ring : results) + 4 * 1024 + 4 * (batch + 1) + 1824, fit = 233472 / bytes;
   return fit < most ? fit : most;
 }
 constexpr int kDecode4Heads = 16, kDecode4HeadsF32 = 8;  // most query heads of one item

@@ -47,10 +47,16 @@ bool aligned(const cb_paged_cache4* c) {
   return reinterpret_cast<uintptr_t>(c->k_scale) % 2 == 0 && reinterpret_cast<uintptr_t>(c->v_scale) % 2 == 0;
 }
 
-// Rows of whole 16-byte pieces of codes, and a row's scales one word: what the streaming kernels copy.
-bool pieces(const void* codes, const void* scales, int dim, std::initializer_list<long long> code_strides,
+// Rows of whole 16-byte pieces of codes, and a row's scales one word: what the streaming kernels copy, at offsets of
+// 32 bits in those units.
+bool pieces(const cb_paged_cache4* c, const void* codes, const void* scales, int dim, std::initializer_list<long long> code_strides,
             std::initializer_list<long long> scale_strides) {
   const int unit = dim <= 64 ? 2 : 4;
+  auto reach = [&](const std::initializer_list<long long>& s, long long per) {  // of pages and slots
+    const double last = static_cast<double>(s.begin()[0]) * c->num_pages + static_cast<double>(s.begin()[1]) * c->page_size;
+    return last / static_cast<double>(per) < 4294967296.0;
+  };
+  if (!reach(code_strides, 16) || !reach(scale_strides, unit)) return false;
   if (dim % 32 != 0 || reinterpret_cast<uintptr_t>(codes) % 16 != 0 || reinterpret_cast<uintptr_t>(scales) % (2 * unit) != 0) return false;
   for (const long long s : code_strides)
     if (s % 16 != 0) return false;
@@ -59,9 +65,9 @@ bool pieces(const void* codes, const void* scales, int dim, std::initializer_lis
   return true;
 }
 bool streams(const cb_paged_cache4* c) {
-  return pieces(c->k, c->k_scale, c->dim_k, {c->k_stride_page, c->k_stride_slot, c->k_stride_head},
+  return pieces(c, c->k, c->k_scale, c->dim_k, {c->k_stride_page, c->k_stride_slot, c->k_stride_head},
                 {c->ks_stride_page, c->ks_stride_slot, c->ks_stride_head}) &&
-         pieces(c->v, c->v_scale, c->dim_v, {c->v_stride_page, c->v_stride_slot, c->v_stride_head},
+         pieces(c, c->v, c->v_scale, c->dim_v, {c->v_stride_page, c->v_stride_slot, c->v_stride_head},
                 {c->vs_stride_page, c->vs_stride_slot, c->vs_stride_head});
 }
 

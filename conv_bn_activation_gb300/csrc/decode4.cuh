@@ -57,22 +57,27 @@ __device__ __forceinline__ void ldsm4_4t(uint32_t addr, uint32_t (&r)[4]) {
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t r;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
 }
 // d (16 x 8, fp32) = c + a (16 x 16, f16) * b (16 x 8, f16)
 __device__ __forceinline__ void mma_f16(float (&d)[4], float c0, float c1, float c2, float c3, uint32_t a0, uint32_t a1, uint32_t a2,
                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// d (16 x 8, fp32) = a (16 x 8, tf32) * b (8 x 8, tf32)
+__device__ __forceinline__ void mma_tf32(float (&d)[4], float a0, float a1, float a2, float a3, float b0, float b1) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(__float_as_uint(a0)), "r"(__float_as_uint(a1)), "r"(__float_as_uint(a2)), "r"(__float_as_uint(a3)), "r"(__float_as_uint(b0)),
+        "r"(__float_as_uint(b1)), "f"(0.f));
 }
 __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
@@ -108,7 +113,7 @@ constexpr int kMinTopExp = -119;  // 2^-top_exp is an fp32 number
 template <int DK_, int DV_, int NB_, typename T_>
 struct Decode4Shape {
   using T = T_;
-  static constexpr int DK = DK_, DV = DV_, NB = NB_, kStep = 32, kStages = 2, kHeads = 8 * NB_;
+  static constexpr int DK = DK_, DV = DV_, NB = NB_, kStep = 32, kStages = 3, kHeads = 8 * NB_;
   static constexpr int kParts = sizeof(T) == 4 ? 2 : 1;
   static constexpr int GK = DK / kGroup4, GV = DV / kGroup4;
   static constexpr int kKeyBytes = DK / 2, kValBytes = DV / 2;
@@ -139,7 +144,9 @@ struct Decode4Math {
   // Queries as the MMAs' B operand, for each group and its two MMAs: head g, dims 8 t4 + (0, 4) and (1, 5) / 16, then
   // (2, 6) and (3, 7) / 16.
   uint32_t qf[S::kParts][GK][NB][4];
-  float first[S::kParts][GK][NB][2];  // -8 sum q of this thread's heads 8 nb + 2 t4 and the one after
+  // The offsets -8 sum q. bf16: of group t4 and head 8 nb + g, as two tf32 numbers: with a key's scales as A, one MMA
+  // makes a score's share of them. fp32: of every group and this thread's heads 8 nb + 2 t4 and the one after.
+  float offset[NB][2], first[S::kParts == 2 ? 2 : 1][S::kParts == 2 ? GK : 1][NB][2];
   float k_mul, head_mul[NB][2];
   // neg = kWeightBits - maximum (+infinity before the first token): weights are 2^(x + neg).
   float slope[NB][2], neg[NB][2], l[NB][2], o[2 * GV][NB][4];
@@ -210,7 +217,7 @@ struct Decode4Math {
         const int he = __shfl_sync(~0u, exponent[nb], from);
         head_mul[nb][e] = ldexpf(1.f, min(he + 24 - k_exp, 16)) * (score.cap ? 1.f : score.c_scale);
 #pragma unroll
-        for (int p = 0; p < S::kParts; ++p)
+        for (int p = 0; p < S::kParts && S::kParts == 2; ++p)
 #pragma unroll
           for (int i = 0; i < GK; ++i) first[p][i][nb][e] = __shfl_sync(~0u, sums[p][i][nb], from);
         slope[nb][e] = a.slopes && hd < heads ? a.slopes[pc.h0 + hd] * kLog2e : 0.f;
@@ -221,6 +228,11 @@ struct Decode4Math {
       for (int d = 0; d < 2 * GV; ++d)
 #pragma unroll
         for (int r = 0; r < 4; ++r) o[d][nb][r] = 0.f;
+      float f = 0.f;
+#pragma unroll
+      for (int i = 0; i < GK; ++i) f = t4 == i ? sums[0][i][nb] : f;
+      offset[nb][0] = __uint_as_float(__float_as_uint(f) & 0xffffe000u);  // tf32's bits; the rest, of 13, as another
+      offset[nb][1] = f - offset[nb][0];
     }
   }
 
@@ -237,6 +249,11 @@ struct Decode4Math {
   __device__ __forceinline__ void scores(float (&s)[NB][4], uint32_t keys, const float4* area) const {
     const float4 x0 = area[g], x1 = area[g + 8];
     const float k0[4] = {x0.x, x0.y, x0.z, x0.w}, k1[4] = {x1.x, x1.y, x1.z, x1.w};
+    if constexpr (S::kParts == 1) {  // a scale has bf16's 8 bits
+      const float a0 = reinterpret_cast<const float*>(area + g)[t4], a1 = reinterpret_cast<const float*>(area + g + 8)[t4];
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) mma_tf32(s[nb], a0, a1, a0, a1, offset[nb][0], offset[nb][1]);
+    }
 #pragma unroll
     for (int i = 0; i < GK; i += 2) {
       uint32_t w[4];  // groups i and i + 1: a word of key g and of key g + 8
@@ -246,18 +263,20 @@ struct Decode4Math {
         const uint32_t u = w[2 * j], v = w[2 * j + 1], u8 = u >> 8, v8 = v >> 8;
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
+          const float ks[4] = {k0[i + j], k0[i + j], k1[i + j], k1[i + j]};
           float acc[S::kParts][4];
 #pragma unroll
           for (int p = 0; p < S::kParts; ++p) {
-            const float f0 = first[p][i + j][nb][0], f1 = first[p][i + j][nb][1];
+            float f0 = 0.f, f1 = 0.f;
+            if constexpr (S::kParts == 2) f0 = first[p][i + j][nb][0], f1 = first[p][i + j][nb][1];
             const uint32_t(&q)[4] = qf[p][i + j][nb];
             mma_f16(acc[p], f0, f1, f0, f1, u & kLowNibble, v & kLowNibble, u & kHighNibble, v & kHighNibble, q[0], q[1]);
             mma_f16(acc[p], u8 & kLowNibble, v8 & kLowNibble, u8 & kHighNibble, v8 & kHighNibble, q[2], q[3]);
           }
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            const float sum = S::kParts == 2 ? fmaf(acc[S::kParts - 1][r], 0x1p-12f, acc[0][r]) : acc[0][r], k = r < 2 ? k0[i + j] : k1[i + j];
-            s[nb][r] = i + j == 0 ? sum * k : fmaf(sum, k, s[nb][r]);
+            const float sum = S::kParts == 2 ? fmaf(acc[S::kParts - 1][r], 0x1p-12f, acc[0][r]) : acc[0][r];
+            s[nb][r] = S::kParts == 2 && i + j == 0 ? sum * ks[r] : fmaf(sum, ks[r], s[nb][r]);
           }
         }
       }
@@ -460,7 +479,7 @@ struct Decode4Math {
 };
 
 template <class S, bool WHOLE>
-__global__ void __launch_bounds__(kDecodeThreads, S::kCtasPerSm) decode4_stream_kernel(const DecodeArgs a) {
+__global__ void __launch_bounds__(kDecodeThreads, S::kCtasPerSm) decode4_stream_kernel(const DecodeArgs a, const Units4 units) {
   using T = typename S::T;
   constexpr int DV = S::DV, kStep = S::kStep, kStages = S::kStages;
   constexpr int CK = S::kKeyBytes / 16, CV = S::kValBytes / 16, RK = 32 / CK, RV = 32 / CV;
@@ -492,8 +511,8 @@ __global__ void __launch_bounds__(kDecodeThreads, S::kCtasPerSm) decode4_stream_
   float4* area = reinterpret_cast<float4*>(smem + S::kMain + warp * S::kScaleArea);
   const uint32_t k_dst = (lane / CK) * S::kKeyBytes + (((lane % CK) ^ swizzle4<S::kKeyBytes>(lane / CK)) * 16);
   const uint32_t v_dst = kStep * S::kKeyBytes + (lane / CV) * S::kValBytes + (((lane % CV) ^ swizzle4<S::kValBytes>(lane / CV)) * 16);
-  const bool same = a.cache.ks_p == a.cache.vs_p && a.cache.ks_t == a.cache.vs_t;  // one offset serves both
-  const bool same_x = a.cache.kx_p == a.cache.vx_p && a.cache.kx_t == a.cache.vx_t;
+  const bool same = units.k_p == units.v_p && units.k_t == units.v_t;  // one offset serves both
+  const bool same_x = units.kx_p == units.vx_p && units.kx_t == units.vx_t;
   // from a lane's token to its next one, without a division per step
   const int adv_pg = kDecodeWarps * kStep / a.cache.page_size, adv_slot = kDecodeWarps * kStep - adv_pg * a.cache.page_size;
 
@@ -509,22 +528,25 @@ __global__ void __launch_bounds__(kDecodeThreads, S::kCtasPerSm) decode4_stream_
     const int base = pc.tile0 * kDecodeTile + warp * kStep;
     const int steps = (pc.tiles * kDecodeTile + kDecodeWarps * kStep - 1) / (kDecodeWarps * kStep);
     const unsigned limit = static_cast<unsigned>(min(static_cast<long long>(pc.hi), (pc.tile0 + static_cast<long long>(pc.tiles)) * kDecodeTile));
-    // Lanes look the step's tokens up, one step before their copies are issued: the byte offsets of the rows, or -1.
+    // Lanes look the step's tokens up, one step before their copies are issued: whether there is one, and its rows'
+    // offsets, of codes in 16 bytes, of scales in rows' scales.
     struct Rows {
-      long long k, v, kx, vx;
+      bool ok;
+      unsigned k, v, kx, vx;
     };
+    const int* table = a.cache.table + pc.b * a.cache.table_stride;
     unsigned j = base + lane;  // unsigned: a token looked up past the piece's end may be past 2^31
     int pg = static_cast<int>(j) / a.cache.page_size, slot = static_cast<int>(j) - pg * a.cache.page_size;
     auto lookup = [&](int step) {  // once for each step, in order
-      Rows r{-1, -1, 0, 0};
+      Rows r{false, 0, 0, 0, 0};
       if (step < steps && j >= static_cast<unsigned>(pc.lo) && j < limit) {
-        const long long page = checked_page(a, pc.b, pg);
-        if (page >= 0) {
-          r.k = page * a.cache.ks_p + slot * a.cache.ks_t;
-          r.v = same ? r.k : page * a.cache.vs_p + slot * a.cache.vs_t;
-          r.kx = page * a.cache.kx_p + slot * a.cache.kx_t;
-          r.vx = same_x ? r.kx : page * a.cache.vx_p + slot * a.cache.vx_t;
-        }
+        const unsigned page = table[pg];
+        r.ok = page < static_cast<unsigned>(a.cache.num_pages);
+        if (!r.ok) atomicCAS(a.err, 0, 1);  // CB_ERR_INVALID_ARG
+        r.k = page * units.k_p + slot * units.k_t;
+        r.v = same ? r.k : page * units.v_p + slot * units.v_t;
+        r.kx = page * units.kx_p + slot * units.kx_t;
+        r.vx = same_x ? r.kx : page * units.vx_p + slot * units.vx_t;
       }
       j += kDecodeWarps * kStep;
       pg += adv_pg, slot += adv_slot;
@@ -532,7 +554,7 @@ __global__ void __launch_bounds__(kDecodeThreads, S::kCtasPerSm) decode4_stream_
       return r;
     };
     auto issue = [&](int step, int stage, const Rows& rows) {
-      const unsigned have = __ballot_sync(~0u, rows.k >= 0);
+      const unsigned have = __ballot_sync(~0u, rows.ok);
       if (step < steps) {
         const uint32_t st = ring + stage * S::kStageBytes;
         auto copies = [&](auto full) {
@@ -540,11 +562,11 @@ __global__ void __launch_bounds__(kDecodeThreads, S::kCtasPerSm) decode4_stream_
 #pragma unroll
           for (int i = 0; i < kStep / RK; ++i) {
             const int r = i * RK + lane / CK;
-            const long long off = __shfl_sync(~0u, rows.k, r);
+            const long long off = 16ull * __shfl_sync(~0u, rows.k, r);
             const bool ok = kFull || ((have >> r) & 1);
             if (lane % CK < kq) cp_async16((st + k_dst + i * RK * S::kKeyBytes) ^ (swizzle4<S::kKeyBytes>(i * RK) * 16), ok ? kbase + off : kbase, ok);
             if (CK == CV) {
-              const long long to = same ? off : __shfl_sync(~0u, rows.v, r);
+              const long long to = same ? off : 16ull * __shfl_sync(~0u, rows.v, r);
               if (lane % CV < vq) cp_async16((st + v_dst + i * RV * S::kValBytes) ^ (swizzle4<S::kValBytes>(i * RV) * 16), ok ? vbase + to : vbase, ok);
             }
           }
@@ -552,14 +574,14 @@ __global__ void __launch_bounds__(kDecodeThreads, S::kCtasPerSm) decode4_stream_
 #pragma unroll
             for (int i = 0; i < kStep / RV; ++i) {
               const int r = i * RV + lane / CV;
-              const long long to = __shfl_sync(~0u, rows.v, r);
+              const long long to = 16ull * __shfl_sync(~0u, rows.v, r);
               const bool ok = kFull || ((have >> r) & 1);
               if (lane % CV < vq) cp_async16((st + v_dst + i * RV * S::kValBytes) ^ (swizzle4<S::kValBytes>(i * RV) * 16), ok ? vbase + to : vbase, ok);
             }
           }
-          const bool ok = kFull || rows.k >= 0;
-          cp_async_small<2 * S::GK>(st + S::kKeyScales + lane * S::GK * 2, ok ? kxbase + rows.kx : kxbase, ok);
-          cp_async_small<2 * S::GV>(st + S::kValScales + lane * S::GV * 2, ok ? vxbase + rows.vx : vxbase, ok);
+          const bool ok = kFull || rows.ok;
+          cp_async_small<2 * S::GK>(st + S::kKeyScales + lane * S::GK * 2, ok ? kxbase + static_cast<unsigned long long>(rows.kx) * S::GK : kxbase, ok);
+          cp_async_small<2 * S::GV>(st + S::kValScales + lane * S::GV * 2, ok ? vxbase + static_cast<unsigned long long>(rows.vx) * S::GV : vxbase, ok);
         };
         if (have == ~0u) copies(std::true_type{});
         else copies(std::false_type{});
@@ -662,21 +684,21 @@ __global__ void __launch_bounds__(kDecodeThreads, S::kCtasPerSm) decode4_stream_
 }
 
 template <class S>
-cudaError_t launch_decode4_shape(const DecodeArgs& a, cudaStream_t s) {
+cudaError_t launch_decode4_shape(const DecodeArgs& a, const Units4& u, cudaStream_t s) {
   if (a.split) {
     const long long ctas = static_cast<long long>(a.B) * a.Hkv * a.chunks * a.split;
     const cudaError_t e = smem_attr_once<decode4_stream_kernel<S, true>>(S::kSmem);
     if (e != cudaSuccess) return e;
     if (ctas >= (1LL << 31)) return cudaErrorInvalidConfiguration;
     const dim3 grid(static_cast<unsigned>(ctas));
-    if (a.split == 1) return launch_pdl(decode4_stream_kernel<S, true>, grid, dim3(kDecodeThreads), S::kSmem, s, a);
-    return launch_pdl_cluster(decode4_stream_kernel<S, true>, grid, dim3(kDecodeThreads), S::kSmem, s, a.split, a);
+    if (a.split == 1) return launch_pdl(decode4_stream_kernel<S, true>, grid, dim3(kDecodeThreads), S::kSmem, s, a, u);
+    return launch_pdl_cluster(decode4_stream_kernel<S, true>, grid, dim3(kDecodeThreads), S::kSmem, s, a.split, a, u);
   }
   const size_t smem = S::kSmem + sizeof(unsigned) * (a.B + 1);
   const cudaError_t e = smem_attr_once<decode4_stream_kernel<S, false>>(smem);
   if (e != cudaSuccess) return e;
   // After the kernel before it, not among its CTAs: this wave fills the SMs exactly (decode_stream.cuh).
-  return launch_serial(decode4_stream_kernel<S, false>, dim3(a.ctas), dim3(kDecodeThreads), smem, s, a);
+  return launch_serial(decode4_stream_kernel<S, false>, dim3(a.ctas), dim3(kDecodeThreads), smem, s, a, u);
 }
 
 }  // namespace cb

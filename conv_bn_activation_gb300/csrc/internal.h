@@ -446,16 +446,21 @@ cudaError_t launch_decode_mma(const DecodeArgs& a, cudaStream_t s);  // bf16, ro
 cudaError_t launch_decode_fma(const DecodeArgs& a, cudaStream_t s);  // fp32, rows of whole 16-byte pieces
 cudaError_t launch_decode(const DecodeArgs& a, bool bf16, bool vec, cudaStream_t s);
 // 4-bit caches (decode4.cuh: rows of whole 16-byte pieces; decode.cu: the others).
-// CTAs that an SM holds: by registers 4, 3 or 2, and no more than its shared memory does.
+// CTAs that an SM holds: by registers 3 or 2, and no more than its shared memory does.
 constexpr int decode4_ctas_per_sm(int dk, int dv, bool bf16, int heads, int batch) {
   const int DK = dk <= 64 ? 64 : 128, DV = dv <= 64 ? 64 : 128, hd = heads <= 8 ? 8 : 16;
-  const int most = !bf16 || hd == 16 ? 2 : 4, ring = 4 * 2 * 32 * 9 * (DK + DV) / 16, results = 4 * 5 * hd * DV;
+  const int most = !bf16 || hd == 16 ? 2 : 3, ring = 4 * 3 * 32 * 9 * (DK + DV) / 16, results = 4 * 5 * hd * DV;
   const int bytes = (ring > results ? ring : results) + 4 * 1024 + 4 * (batch + 1) + 1824, fit = 233472 / bytes;
   return fit < most ? fit : most;
 }
 constexpr int kDecode4Heads = 16, kDecode4HeadsF32 = 8;  // most query heads of one item
-cudaError_t launch_decode4_bf16(const DecodeArgs& a, cudaStream_t s);
-cudaError_t launch_decode4_f32(const DecodeArgs& a, cudaStream_t s);
+// The streaming kernels' strides of pages and slots, of codes in 16 bytes and of scales in rows' scales (2 for
+// dims up to 64, else 4): 32 bits reach 64 GB of codes.
+struct Units4 {
+  unsigned k_p, k_t, v_p, v_t, kx_p, kx_t, vx_p, vx_t;
+};
+cudaError_t launch_decode4_bf16(const DecodeArgs& a, const Units4& u, cudaStream_t s);
+cudaError_t launch_decode4_f32(const DecodeArgs& a, const Units4& u, cudaStream_t s);
 cudaError_t launch_decode4(const DecodeArgs& a, bool bf16, bool vec, cudaStream_t s);
 // cb_attention with few queries per key head through the streaming kernel:
 // columns are (query, head) pairs, at most kDecodeMmaHeads (bf16) or

@@ -71,6 +71,15 @@ bool streams(const cb_paged_cache4* c) {
                 {c->vs_stride_page, c->vs_stride_slot, c->vs_stride_head});
 }
 
+// The codes' pages as the streaming kernels' copies take them; false where they cannot.
+bool code_map(CUtensorMap* m, const void* codes, const cb_paged_cache4* c, int dim, long long page, long long slot, long long head) {
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(dim / 2), static_cast<cuuint64_t>(c->page_size), static_cast<cuuint64_t>(c->heads),
+                              static_cast<cuuint64_t>(c->num_pages)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(slot), static_cast<cuuint64_t>(head), static_cast<cuuint64_t>(page)};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(decode4_box(dim)), 16, 1, 1};
+  return host_map_u8(m, codes, dims, strides, box);
+}
+
 bool overlap(const cb_heads* t, const cb_paged_cache4* c) {
   for (const Region& r : pages(c).part)
     if (cb::overlap(r, region(t))) return true;
@@ -261,7 +270,12 @@ cb_status cb_attention_decode4(const cb_heads* q, const cb_paged_cache4* cache, 
   a.part = reinterpret_cast<float*>(a.record + 2 * p.ctas);
   a.ctas = p.ctas;
   a.err = p.err;
-  return done(launch_decode4(a, q->dtype == CB_DTYPE_BF16, p.vec, static_cast<cudaStream_t>(stream)));
+  a.timeout_ns = host_timeout_ns();
+  Maps4 maps;
+  const bool mapped = p.vec && !p.split && cache->num_pages > 0 && cache->page_size % 16 == 0 &&
+                      code_map(&maps.k, cache->k, cache, cache->dim_k, cache->k_stride_page, cache->k_stride_slot, cache->k_stride_head) &&
+                      code_map(&maps.v, cache->v, cache, cache->dim_v, cache->v_stride_page, cache->v_stride_slot, cache->v_stride_head);
+  return done(launch_decode4(a, q->dtype == CB_DTYPE_BF16, p.vec, mapped ? &maps : nullptr, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

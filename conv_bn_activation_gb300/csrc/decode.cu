@@ -292,7 +292,7 @@ cudaError_t launch_decode(const DecodeArgs& a, bool bf16, bool vec, cudaStream_t
   return bf16 ? launch_join<__nv_bfloat16>(a, s) : launch_join<float>(a, s);
 }
 
-cudaError_t launch_decode4(const DecodeArgs& a, bool bf16, bool vec, cudaStream_t s) {
+cudaError_t launch_decode4(const DecodeArgs& a, bool bf16, bool vec, const Maps4* maps, cudaStream_t s) {
   cudaError_t e;
   if (vec) {
     const PagedArgs& c = a.cache;
@@ -300,7 +300,7 @@ cudaError_t launch_decode4(const DecodeArgs& a, bool bf16, bool vec, cudaStream_
     const Units4 u{static_cast<unsigned>(c.ks_p / 16), static_cast<unsigned>(c.ks_t / 16), static_cast<unsigned>(c.vs_p / 16),
                    static_cast<unsigned>(c.vs_t / 16), static_cast<unsigned>(c.kx_p / gk), static_cast<unsigned>(c.kx_t / gk),
                    static_cast<unsigned>(c.vx_p / gv), static_cast<unsigned>(c.vx_t / gv)};
-    e = bf16 ? launch_decode4_bf16(a, u, s) : launch_decode4_f32(a, u, s);
+    e = bf16 ? launch_decode4_bf16(a, u, maps, s) : launch_decode4_f32(a, u, maps, s);
   } else
     e = bf16 ? launch_simt<__nv_bfloat16, Elements4>(a, s) : launch_simt<float, Elements4>(a, s);
   if (e != cudaSuccess || a.split) return e;

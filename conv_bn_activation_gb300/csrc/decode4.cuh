@@ -43,6 +43,13 @@ template <int BYTES>
 __device__ __forceinline__ void cp_async_small(uint32_t dst, const void* src, bool valid) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(valid ? BYTES : 0) : "memory");
 }
+__device__ __forceinline__ void tma_load_4d_at(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2, int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
 __device__ __forceinline__ void ldsm4_4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -107,23 +114,26 @@ __device__ __forceinline__ uint32_t high_codes(uint32_t w) {
   const __half2 h = __hfma2(*reinterpret_cast<const __half2*>(&x), __float2half2_rn(0.0625f), __float2half2_rn(-72.f));
   return *reinterpret_cast<const uint32_t*>(&h);
 }
+constexpr uint64_t kDrainNs = 20000000;
 constexpr int kWeightBits = 7;     // weights go up to 2^(kDecodeGrowth + kWeightBits) = 2^15
 constexpr int kMinTopExp = -119;  // 2^-top_exp is an fp32 number
 
 template <int DK_, int DV_, int NB_, typename T_>
 struct Decode4Shape {
   using T = T_;
-  static constexpr int DK = DK_, DV = DV_, NB = NB_, kStep = 32, kStages = 3, kHeads = 8 * NB_;
+  static constexpr int DK = DK_, DV = DV_, NB = NB_, kStep = 32, kStages = 2, kHeads = 8 * NB_;
   static constexpr int kParts = sizeof(T) == 4 ? 2 : 1;
   static constexpr int GK = DK / kGroup4, GV = DV / kGroup4;
   static constexpr int kKeyBytes = DK / 2, kValBytes = DV / 2;
-  static constexpr int kKeyScales = kStep * (kKeyBytes + kValBytes), kValScales = kKeyScales + kStep * GK * 2;  // in a stage
-  static constexpr int kStageBytes = kValScales + kStep * GV * 2;
+  static constexpr int kStageBytes = kStep * (kKeyBytes + kValBytes), kScaleBytes = kStep * (GK + GV) * 2;
   static constexpr int kRing = kDecodeWarps * kStages * kStageBytes;
   static constexpr int kResults = 4 * (kDecodeWarps + 1) * kHeads * DV;  // the warps' and the CTA's, when a piece ends
   static constexpr int kMain = kRing > kResults ? kRing : kResults;
-  static constexpr int kScaleArea = kStep * 2 * 16;  // a step's scales, per warp: keys' fp32, values' fp32 or f16
-  static constexpr int kSmem = kMain + kDecodeWarps * kScaleArea;
+  // Behind the ring of codes: a step's scales as the products take them, per warp (keys' fp32, values' fp32 or f16);
+  // the ring of scales; queries; barriers.
+  static constexpr int kArea = kStep * 2 * 16, kScales = kMain + kDecodeWarps * kArea;
+  static constexpr int kQueries = kScales + kDecodeWarps * kStages * kScaleBytes, kBars = kQueries + kParts * GK * NB * 512;
+  static constexpr int kSmem = kBars + kDecodeWarps * kStages * 8, kAlign = 512;  // of the copies' swizzle
   static constexpr int kCtasPerSm = decode4_ctas_per_sm(DK, DV, sizeof(T) == 2, kHeads, 0);
 };
 
@@ -138,12 +148,12 @@ struct Decode4Math {
   using T = typename S::T;
   static constexpr int GK = S::GK, GV = S::GV, NB = S::NB;
   DecodeScore score;
-  bool bias;
+
   int g, t4, heads, top_exp;
   uint32_t k_src, v_src;  // this lane's ldmatrix rows
-  // Queries as the MMAs' B operand, for each group and its two MMAs: head g, dims 8 t4 + (0, 4) and (1, 5) / 16, then
-  // (2, 6) and (3, 7) / 16.
-  uint32_t qf[S::kParts][GK][NB][4];
+  // Queries as the MMAs' B operand, for each part and group: head g, dims 8 t4 + (0, 4) and (1, 5) / 16, then (2, 6) and
+  // (3, 7) / 16.  In shared memory, one copy for the CTA: in registers they would cost it a neighbour.
+  const uint4* queries;
   // The offsets -8 sum q. bf16: of group t4 and head 8 nb + g, as two tf32 numbers: with a key's scales as A, one MMA
   // makes a score's share of them. fp32: of every group and this thread's heads 8 nb + 2 t4 and the one after.
   float offset[NB][2], first[S::kParts == 2 ? 2 : 1][S::kParts == 2 ? GK : 1][NB][2];
@@ -151,16 +161,17 @@ struct Decode4Math {
   // neg = kWeightBits - maximum (+infinity before the first token): weights are 2^(x + neg).
   float slope[NB][2], neg[NB][2], l[NB][2], o[2 * GV][NB][4];
 
-  __device__ __forceinline__ Decode4Math(const DecodeArgs& a, const Piece& pc) : score(a) {
+  __device__ __forceinline__ Decode4Math(const DecodeArgs& a, const Piece& pc, uint4* q_area) : score(a), queries(q_area + (threadIdx.x & 31)) {
     const int lane = threadIdx.x & 31;
     g = lane >> 2, t4 = lane & 3, heads = pc.heads, top_exp = kMinTopExp;
-    bias = a.slopes != nullptr;
+
     const int row = (lane & 7) + 8 * ((lane >> 3) & 1);
     k_src = row * S::kKeyBytes + (((lane >> 4) ^ swizzle4<S::kKeyBytes>(row)) * 16);
     v_src = row * S::kValBytes + (((lane >> 4) ^ swizzle4<S::kValBytes>(row)) * 16);
     int exponent[NB], top = -1000;
     float sums[S::kParts][GK][NB];
     constexpr int kBits = S::kParts == 2 ? 11 : 15;  // queries go up to 2^kBits
+    constexpr int kCodeBits = 24;                   // codes are c + 8 times 2^-kCodeBits
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
       const int hd = g + 8 * nb;
@@ -182,21 +193,33 @@ struct Decode4Math {
       if (big > 0.f) top = max(top, exponent[nb]);
 #pragma unroll
       for (int i = 0; i < GK; ++i) {
-        float sum[S::kParts] = {};
+        float y[8], sum[S::kParts] = {};
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {  // dims 8 t4 + r and r + 4; odd r: a sixteenth
-          const float lo = ldexpf(x[i][r], kBits - e2), hi = ldexpf(x[i][r + 4], kBits - e2), unit = r & 1 ? 0.0625f : 1.f;
-          if constexpr (S::kParts == 1) {
-            qf[0][i][nb][r] = half2_bits(lo * unit, hi * unit);
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&qf[0][i][nb][r]));
+        for (int e = 0; e < 8; ++e) y[e] = ldexpf(x[i][e], kBits - e2);
+        if constexpr (S::kParts == 1) {
+          uint32_t qf[4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {  // dims 8 t4 + r and r + 4; odd r: a sixteenth
+            const float unit = r & 1 ? 0.0625f : 1.f;
+            qf[r] = half2_bits(y[r] * unit, y[r + 4] * unit);
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&qf[r]));
             sum[0] += (f.x + f.y) / unit;
-          } else {
-            const float a0 = rintf(lo), a1 = rintf(hi), b0 = rintf((lo - a0) * 0x1p12f), b1 = rintf((hi - a1) * 0x1p12f);
-            qf[0][i][nb][r] = half2_bits(a0 * unit, a1 * unit);
-            qf[1][i][nb][r] = half2_bits(b0 * unit, b1 * unit);
+          }
+          if (threadIdx.x < 32) q_area[(i * NB + nb) * 32 + lane] = make_uint4(qf[0], qf[1], qf[2], qf[3]);
+        } else {
+          uint32_t qf[2][4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const float unit = r & 1 ? 0.0625f : 1.f;
+            const float a0 = rintf(y[r]), a1 = rintf(y[r + 4]), b0 = rintf((y[r] - a0) * 0x1p12f), b1 = rintf((y[r + 4] - a1) * 0x1p12f);
+            qf[0][r] = half2_bits(a0 * unit, a1 * unit);
+            qf[1][r] = half2_bits(b0 * unit, b1 * unit);
             sum[0] += a0 + a1;
             sum[1] += b0 + b1;
           }
+#pragma unroll
+          for (int p = 0; p < 2; ++p)
+            if (threadIdx.x < 32) q_area[((p * GK + i) * NB + nb) * 32 + lane] = make_uint4(qf[p][0], qf[p][1], qf[p][2], qf[p][3]);
         }
 #pragma unroll
         for (int p = 0; p < S::kParts; ++p) {
@@ -207,7 +230,7 @@ struct Decode4Math {
       }
     }
     for (int s = 4; s < 32; s <<= 1) top = max(top, __shfl_xor_sync(~0u, top, s));
-    const int k_exp = min(max(top + 24, -126), 127);
+    const int k_exp = min(max(top + kCodeBits, -126), 127);
     k_mul = ldexpf(1.f, k_exp);
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
@@ -215,7 +238,7 @@ struct Decode4Math {
       for (int e = 0; e < 2; ++e) {
         const int from = 4 * (2 * t4 + e), hd = 8 * nb + 2 * t4 + e;
         const int he = __shfl_sync(~0u, exponent[nb], from);
-        head_mul[nb][e] = ldexpf(1.f, min(he + 24 - k_exp, 16)) * (score.cap ? 1.f : score.c_scale);
+        head_mul[nb][e] = ldexpf(1.f, min(he + kCodeBits - k_exp, 16)) * (score.cap ? 1.f : score.c_scale);
 #pragma unroll
         for (int p = 0; p < S::kParts && S::kParts == 2; ++p)
 #pragma unroll
@@ -245,39 +268,53 @@ struct Decode4Math {
         for (int r = 0; r < 4; ++r) o[d][nb][r] *= f[nb][r & 1];
   }
 
-  // Scores of 16 tokens before the heads' factors: element r is key g + 8 (r >> 1), head 8 nb + 2 t4 + (r & 1).
-  __device__ __forceinline__ void scores(float (&s)[NB][4], uint32_t keys, const float4* area) const {
-    const float4 x0 = area[g], x1 = area[g + 8];
-    const float k0[4] = {x0.x, x0.y, x0.z, x0.w}, k1[4] = {x1.x, x1.y, x1.z, x1.w};
-    if constexpr (S::kParts == 1) {  // a scale has bf16's 8 bits
-      const float a0 = reinterpret_cast<const float*>(area + g)[t4], a1 = reinterpret_cast<const float*>(area + g + 8)[t4];
+  // Scores of 32 tokens before the heads' factors: element r of half h is key 16 h + g + 8 (r >> 1), head
+  // 8 nb + 2 t4 + (r & 1).
+  __device__ __forceinline__ void scores(float (&s)[2][NB][4], uint32_t keys, const float4* area) const {
+    float ks[2][2][4];
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb) mma_tf32(s[nb], a0, a1, a0, a1, offset[nb][0], offset[nb][1]);
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float4 x = area[16 * h + 8 * e + g];
+        ks[h][e][0] = x.x, ks[h][e][1] = x.y, ks[h][e][2] = x.z, ks[h][e][3] = x.w;
+      }
+      if constexpr (S::kParts == 1) {  // a scale has bf16's 8 bits
+        const float* x = reinterpret_cast<const float*>(area + 16 * h + g) + t4;
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) mma_tf32(s[h][nb], x[0], x[32], x[0], x[32], offset[nb][0], offset[nb][1]);
+      }
     }
 #pragma unroll
     for (int i = 0; i < GK; i += 2) {
-      uint32_t w[4];  // groups i and i + 1: a word of key g and of key g + 8
-      ldsm4_4((keys + k_src) ^ (i * 16), w);
+      uint32_t w[2][4];  // groups i and i + 1: a word of key g and of key g + 8
+#pragma unroll
+      for (int h = 0; h < 2; ++h) ldsm4_4((keys + 16 * h * S::kKeyBytes + k_src) ^ (i * 16), w[h]);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const uint32_t u = w[2 * j], v = w[2 * j + 1], u8 = u >> 8, v8 = v >> 8;
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-          const float ks[4] = {k0[i + j], k0[i + j], k1[i + j], k1[i + j]};
-          float acc[S::kParts][4];
+          float acc[S::kParts][2][4];
 #pragma unroll
           for (int p = 0; p < S::kParts; ++p) {
-            float f0 = 0.f, f1 = 0.f;
-            if constexpr (S::kParts == 2) f0 = first[p][i + j][nb][0], f1 = first[p][i + j][nb][1];
-            const uint32_t(&q)[4] = qf[p][i + j][nb];
-            mma_f16(acc[p], f0, f1, f0, f1, u & kLowNibble, v & kLowNibble, u & kHighNibble, v & kHighNibble, q[0], q[1]);
-            mma_f16(acc[p], u8 & kLowNibble, v8 & kLowNibble, u8 & kHighNibble, v8 & kHighNibble, q[2], q[3]);
+            const uint4 q = queries[((p * GK + i + j) * NB + nb) * 32];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t u = w[h][2 * j], v = w[h][2 * j + 1];
+              const uint32_t u8 = u >> 8, v8 = v >> 8;
+              float f0 = 0.f, f1 = 0.f;
+              if constexpr (S::kParts == 2) f0 = first[p][i + j][nb][0], f1 = first[p][i + j][nb][1];
+              mma_f16(acc[p][h], f0, f1, f0, f1, u & kLowNibble, v & kLowNibble, u & kHighNibble, v & kHighNibble, q.x, q.y);
+              mma_f16(acc[p][h], u8 & kLowNibble, v8 & kLowNibble, u8 & kHighNibble, v8 & kHighNibble, q.z, q.w);
+            }
           }
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const float sum = S::kParts == 2 ? fmaf(acc[S::kParts - 1][r], 0x1p-12f, acc[0][r]) : acc[0][r];
-            s[nb][r] = S::kParts == 2 && i + j == 0 ? sum * ks[r] : fmaf(sum, ks[r], s[nb][r]);
-          }
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const float k = ks[h][r >> 1][i + j], sum = S::kParts == 2 ? fmaf(acc[S::kParts - 1][h][r], 0x1p-12f, acc[0][h][r]) : acc[0][h][r];
+              s[h][nb][r] = S::kParts == 2 && i + j == 0 ? sum * k : fmaf(sum, k, s[h][nb][r]);
+            }
         }
       }
     }
@@ -332,7 +369,7 @@ struct Decode4Math {
 
   // The step's scales as the products take them, a token per lane: area [32] keys', then values'.
   template <bool FULL>
-  __device__ __forceinline__ void scales(uint32_t st, unsigned lv, const DecodeArgs& a, float4* area) {
+  __device__ __forceinline__ void scales(uint32_t raw, unsigned lv, const DecodeArgs& a, float4* area) {
     const int lane = threadIdx.x & 31;
     const bool live = FULL || ((lv >> lane) & 1);
     auto load = [&](uint32_t at, int groups, int dim) {
@@ -345,7 +382,7 @@ struct Decode4Math {
       return make_float4(__uint_as_float(w0 << 16), __uint_as_float(w0 & 0xffff0000u), __uint_as_float(w1 << 16),
                          __uint_as_float(w1 & 0xffff0000u));
     };
-    float4 k = load(st + S::kKeyScales + lane * GK * 2, GK, a.dk), v = load(st + S::kValScales + lane * GV * 2, GV, a.dv);
+    float4 k = load(raw + lane * GK * 2, GK, a.dk), v = load(raw + S::kStep * GK * 2 + lane * GV * 2, GV, a.dv);
     k.x *= k_mul, k.y *= k_mul, k.z *= k_mul, k.w *= k_mul;
     area[lane] = k;
     float big = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w));  // NaN only where all are
@@ -374,18 +411,18 @@ struct Decode4Math {
     __syncwarp();
   }
 
-  // 32 tokens of a stage; bit x of lv: token x exists (FULL: all do); far: the first one's distance from the query.
-  template <bool FULL>
-  __device__ __forceinline__ void step(uint32_t st, unsigned lv, int far, const DecodeArgs& a, float4* area) {
-    scales<FULL>(st, lv, a, area);
-    const float dist = static_cast<float>(far - g);
+  // 32 tokens of a stage, codes at st, scales at raw; bit x of lv: token x exists (FULL: all do); far: the first one's
+  // distance from the query.
+  // DIRECT: no cap and no bias.
+  template <bool FULL, bool DIRECT>
+  __device__ __forceinline__ void step(uint32_t st, uint32_t raw, unsigned lv, int far, const DecodeArgs& a, float4* area) {
+    scales<FULL>(raw, lv, a, area);
     float s[2][NB][4];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) scores(s[h], st + h * 16 * S::kKeyBytes, area + 16 * h);
+    scores(s, st, area);
     // What the exponential takes: x + neg, x = log2(e) * score.
-    const bool direct = !score.cap && !bias;
     float y[2][NB][4];
-    if (!direct) {
+    if constexpr (!DIRECT) {
+      const float dist = static_cast<float>(far - g);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
 #pragma unroll
@@ -406,7 +443,7 @@ struct Decode4Math {
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            y[h][nb][r] = direct ? fmaf(s[h][nb][r], head_mul[nb][r & 1], add[nb][r & 1]) : s[h][nb][r] + add[nb][r & 1];
+            y[h][nb][r] = DIRECT ? fmaf(s[h][nb][r], head_mul[nb][r & 1], add[nb][r & 1]) : s[h][nb][r] + add[nb][r & 1];
             if (!FULL && !((lv >> (g + 8 * (r >> 1) + 16 * h)) & 1)) y[h][nb][r] = kNegInf;
           }
     };
@@ -478,17 +515,32 @@ struct Decode4Math {
   }
 };
 
-template <class S, bool WHOLE>
-__global__ void __launch_bounds__(kDecodeThreads, S::kCtasPerSm) decode4_stream_kernel(const DecodeArgs a, const Units4 units) {
+// TMA: pages of a multiple of 16 slots, whose codes come in boxes of 16 rows (maps: bytes of a row, slots, heads,
+// pages; swizzled as swizzle4 says); else each lane copies 16-byte pieces.  Scales, a token per lane, come by
+// cp.async in either case.
+template <class S, bool WHOLE, bool TMA>
+__global__ void __launch_bounds__(kDecodeThreads, S::kCtasPerSm)
+    decode4_stream_kernel(const DecodeArgs a, const Units4 units, const __grid_constant__ Maps4 maps) {
   using T = typename S::T;
   constexpr int DV = S::DV, kStep = S::kStep, kStages = S::kStages;
   constexpr int CK = S::kKeyBytes / 16, CV = S::kValBytes / 16, RK = 32 / CK, RV = 32 / CV;
-  extern __shared__ __align__(128) uint8_t smem[];
+  extern __shared__ __align__(128) uint8_t smem_raw[];
   __shared__ float ms[kDecodeWarps][S::kHeads], ls[kDecodeWarps][S::kHeads];
   __shared__ float part_m[S::kHeads], part_l[S::kHeads];
+  __shared__ int abort_flag;
+  uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & (S::kAlign - 1));
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int kq = a.dk / kGroup4, vq = a.dv / kGroup4;  // real pieces per row; what the others hold meets queries of 0
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kBars) + warp * kStages;
+  if constexpr (TMA) {
+    if (tid == 0) abort_flag = 0;
+    if (lane == 0) {
+      for (int s = 0; s < kStages; ++s) mbar_init(bars + s, 2);  // the lanes that copy
+      fence_mbar_init();
+    }
+    __syncthreads();
+  }
   pdl_wait();
   pdl_launch_dependents();
   const int per_seq = a.Hkv * a.chunks;
@@ -508,13 +560,18 @@ __global__ void __launch_bounds__(kDecodeThreads, S::kCtasPerSm) decode4_stream_
     b = find_seq(a, prefix, per_seq, at);
   }
   const uint32_t ring = smem_u32(smem + warp * kStages * S::kStageBytes);
-  float4* area = reinterpret_cast<float4*>(smem + S::kMain + warp * S::kScaleArea);
+  const uint32_t raw_ring = smem_u32(smem + S::kScales + warp * kStages * S::kScaleBytes);
+  float4* area = reinterpret_cast<float4*>(smem + S::kMain + warp * S::kArea);
   const uint32_t k_dst = (lane / CK) * S::kKeyBytes + (((lane % CK) ^ swizzle4<S::kKeyBytes>(lane / CK)) * 16);
   const uint32_t v_dst = kStep * S::kKeyBytes + (lane / CV) * S::kValBytes + (((lane % CV) ^ swizzle4<S::kValBytes>(lane / CV)) * 16);
   const bool same = units.k_p == units.v_p && units.k_t == units.v_t;  // one offset serves both
   const bool same_x = units.kx_p == units.vx_p && units.kx_t == units.vx_t;
   // from a lane's token to its next one, without a division per step
   const int adv_pg = kDecodeWarps * kStep / a.cache.page_size, adv_slot = kDecodeWarps * kStep - adv_pg * a.cache.page_size;
+  const bool direct = a.softcap == 0.f && !a.slopes;
+  const Watchdog wd{a.err, &abort_flag, a.timeout_ns};
+  unsigned phases = 0;  // bit s: the parity that stage s's barrier is waited for with
+  bool alive = true;    // no wait has run out: else the warp copies and computes nothing more
 
   while (at < end) {
     Piece pc;
@@ -527,64 +584,78 @@ __global__ void __launch_bounds__(kDecodeThreads, S::kCtasPerSm) decode4_stream_
 
     const int base = pc.tile0 * kDecodeTile + warp * kStep;
     const int steps = (pc.tiles * kDecodeTile + kDecodeWarps * kStep - 1) / (kDecodeWarps * kStep);
-    const unsigned limit = static_cast<unsigned>(min(static_cast<long long>(pc.hi), (pc.tile0 + static_cast<long long>(pc.tiles)) * kDecodeTile));
-    // Lanes look the step's tokens up, one step before their copies are issued: whether there is one, and its rows'
-    // offsets, of codes in 16 bytes, of scales in rows' scales.
-    struct Rows {
-      bool ok;
-      unsigned k, v, kx, vx;
+    const unsigned first = pc.lo, limit = static_cast<unsigned>(min(static_cast<long long>(pc.hi), (pc.tile0 + static_cast<long long>(pc.tiles)) * kDecodeTile));
+    // Lanes look the step's tokens up, one step before their copies are issued: page (-1: none that the piece needs;
+    // TMA: none that the 16 tokens around need) and slot.
+    struct Place {
+      int page, slot;
     };
     const int* table = a.cache.table + pc.b * a.cache.table_stride;
     unsigned j = base + lane;  // unsigned: a token looked up past the piece's end may be past 2^31
     int pg = static_cast<int>(j) / a.cache.page_size, slot = static_cast<int>(j) - pg * a.cache.page_size;
     auto lookup = [&](int step) {  // once for each step, in order
-      Rows r{false, 0, 0, 0, 0};
-      if (step < steps && j >= static_cast<unsigned>(pc.lo) && j < limit) {
-        const unsigned page = table[pg];
-        r.ok = page < static_cast<unsigned>(a.cache.num_pages);
-        if (!r.ok) atomicCAS(a.err, 0, 1);  // CB_ERR_INVALID_ARG
-        r.k = page * units.k_p + slot * units.k_t;
-        r.v = same ? r.k : page * units.v_p + slot * units.v_t;
-        r.kx = page * units.kx_p + slot * units.kx_t;
-        r.vx = same_x ? r.kx : page * units.vx_p + slot * units.vx_t;
+      Place r{-1, slot};
+      const bool need = TMA ? (j | 15) >= first && (j & ~15u) < limit : j >= first && j < limit;
+      if (step < steps && need) {
+        r.page = table[pg];
+        if (static_cast<unsigned>(r.page) >= static_cast<unsigned>(a.cache.num_pages)) {
+          atomicCAS(a.err, 0, 1);  // CB_ERR_INVALID_ARG
+          r.page = -1;
+        }
       }
       j += kDecodeWarps * kStep;
       pg += adv_pg, slot += adv_slot;
       if (slot >= a.cache.page_size) slot -= a.cache.page_size, ++pg;
       return r;
     };
-    auto issue = [&](int step, int stage, const Rows& rows) {
-      const unsigned have = __ballot_sync(~0u, rows.ok);
-      if (step < steps) {
-        const uint32_t st = ring + stage * S::kStageBytes;
-        auto copies = [&](auto full) {
-          constexpr bool kFull = decltype(full)::value;
-#pragma unroll
-          for (int i = 0; i < kStep / RK; ++i) {
-            const int r = i * RK + lane / CK;
-            const long long off = 16ull * __shfl_sync(~0u, rows.k, r);
-            const bool ok = kFull || ((have >> r) & 1);
-            if (lane % CK < kq) cp_async16((st + k_dst + i * RK * S::kKeyBytes) ^ (swizzle4<S::kKeyBytes>(i * RK) * 16), ok ? kbase + off : kbase, ok);
-            if (CK == CV) {
-              const long long to = same ? off : 16ull * __shfl_sync(~0u, rows.v, r);
-              if (lane % CV < vq) cp_async16((st + v_dst + i * RV * S::kValBytes) ^ (swizzle4<S::kValBytes>(i * RV) * 16), ok ? vbase + to : vbase, ok);
+    auto issue = [&](int step, int stage, const Place& at_) {
+      const unsigned token = base + step * (kDecodeWarps * kStep) + lane;
+      const bool ok = at_.page >= 0 && (!TMA || (token >= first && token < limit));
+      const unsigned have = __ballot_sync(~0u, ok);
+      if (step < steps && alive) {
+        const uint32_t st = ring + stage * S::kStageBytes, raw = raw_ring + stage * S::kScaleBytes;
+        if constexpr (TMA) {
+          if ((lane & 15) == 0) {
+            uint64_t* bar = bars + stage;
+            if (at_.page >= 0) {
+              mbar_arrive_expect_tx(bar, 16 * (S::kKeyBytes + S::kValBytes));
+              tma_load_4d_at(st + lane * S::kKeyBytes, &maps.k, bar, 0, at_.slot, pc.hk, at_.page);
+              tma_load_4d_at(st + kStep * S::kKeyBytes + lane * S::kValBytes, &maps.v, bar, 0, at_.slot, pc.hk, at_.page);
+            } else {
+              mbar_arrive(bar);
             }
           }
-          if (CK != CV) {
+        } else {
+          const unsigned k_off = at_.page * units.k_p + at_.slot * units.k_t, v_off = same ? k_off : at_.page * units.v_p + at_.slot * units.v_t;
+          auto copies = [&](auto full) {
+            constexpr bool kFull = decltype(full)::value;
 #pragma unroll
-            for (int i = 0; i < kStep / RV; ++i) {
-              const int r = i * RV + lane / CV;
-              const long long to = 16ull * __shfl_sync(~0u, rows.v, r);
-              const bool ok = kFull || ((have >> r) & 1);
-              if (lane % CV < vq) cp_async16((st + v_dst + i * RV * S::kValBytes) ^ (swizzle4<S::kValBytes>(i * RV) * 16), ok ? vbase + to : vbase, ok);
+            for (int i = 0; i < kStep / RK; ++i) {
+              const int r = i * RK + lane / CK;
+              const long long off = 16ull * __shfl_sync(~0u, k_off, r);
+              const bool some = kFull || ((have >> r) & 1);
+              if (lane % CK < kq) cp_async16((st + k_dst + i * RK * S::kKeyBytes) ^ (swizzle4<S::kKeyBytes>(i * RK) * 16), some ? kbase + off : kbase, some);
+              if (CK == CV) {
+                const long long to = same ? off : 16ull * __shfl_sync(~0u, v_off, r);
+                if (lane % CV < vq) cp_async16((st + v_dst + i * RV * S::kValBytes) ^ (swizzle4<S::kValBytes>(i * RV) * 16), some ? vbase + to : vbase, some);
+              }
             }
-          }
-          const bool ok = kFull || rows.ok;
-          cp_async_small<2 * S::GK>(st + S::kKeyScales + lane * S::GK * 2, ok ? kxbase + static_cast<unsigned long long>(rows.kx) * S::GK : kxbase, ok);
-          cp_async_small<2 * S::GV>(st + S::kValScales + lane * S::GV * 2, ok ? vxbase + static_cast<unsigned long long>(rows.vx) * S::GV : vxbase, ok);
-        };
-        if (have == ~0u) copies(std::true_type{});
-        else copies(std::false_type{});
+            if (CK != CV) {
+#pragma unroll
+              for (int i = 0; i < kStep / RV; ++i) {
+                const int r = i * RV + lane / CV;
+                const long long to = 16ull * __shfl_sync(~0u, v_off, r);
+                const bool some = kFull || ((have >> r) & 1);
+                if (lane % CV < vq) cp_async16((st + v_dst + i * RV * S::kValBytes) ^ (swizzle4<S::kValBytes>(i * RV) * 16), some ? vbase + to : vbase, some);
+              }
+            }
+          };
+          if (have == ~0u) copies(std::true_type{});
+          else copies(std::false_type{});
+        }
+        const unsigned kx = at_.page * units.kx_p + at_.slot * units.kx_t, vx = same_x ? kx : at_.page * units.vx_p + at_.slot * units.vx_t;
+        cp_async_small<2 * S::GK>(raw + lane * S::GK * 2, ok ? kxbase + static_cast<unsigned long long>(kx) * S::GK : kxbase, ok);
+        cp_async_small<2 * S::GV>(raw + kStep * S::GK * 2 + lane * S::GV * 2, ok ? vxbase + static_cast<unsigned long long>(vx) * S::GV : vxbase, ok);
       }
       cp_async_commit();
       return have;
@@ -593,24 +664,36 @@ __global__ void __launch_bounds__(kDecodeThreads, S::kCtasPerSm) decode4_stream_
     unsigned live[kStages - 1];  // of the next steps: bit x, token x exists
 #pragma unroll
     for (int s = 0; s < kStages - 1; ++s) live[s] = issue(s, s, lookup(s));
-    Decode4Math<S> c(a, pc);  // the queries are read while the first tokens come
-    Rows rows = lookup(kStages - 1);
+    // The queries are read while the first tokens come.
+    Decode4Math<S> c(a, pc, reinterpret_cast<uint4*>(smem + S::kQueries));
+    __syncthreads();
+    Place place = lookup(kStages - 1);
     int stage = 0;
     for (int step = 0; step < steps; ++step) {
       const int fill = stage == 0 ? kStages - 1 : stage - 1;  // the stage read in the last step
       __syncwarp();
-      const unsigned lv = live[0], next = issue(step + kStages - 1, fill, rows);
+      const unsigned lv = live[0], next = issue(step + kStages - 1, fill, place);
 #pragma unroll
       for (int s = 0; s + 1 < kStages - 1; ++s) live[s] = live[s + 1];
       live[kStages - 2] = next;
-      rows = lookup(step + kStages);
+      place = lookup(step + kStages);
       cp_async_wait<kStages - 1>();
+      if constexpr (TMA) {
+        if (alive) alive = mbar_wait(bars + stage, (phases >> stage) & 1, wd);
+        phases ^= 1u << stage;
+        alive = __all_sync(~0u, alive);
+      }
       __syncwarp();
       const int far = pc.len - 1 - (base + step * (kDecodeWarps * kStep));
-      if (lv == ~0u) c.template step<true>(ring + stage * S::kStageBytes, lv, far, a, area);
-      else if (lv) c.template step<false>(ring + stage * S::kStageBytes, lv, far, a, area);
+      const uint32_t st = ring + stage * S::kStageBytes, raw = raw_ring + stage * S::kScaleBytes;
+      if (TMA && !alive) break;
+      if (lv == ~0u && direct) c.template step<true, true>(st, raw, lv, far, a, area);
+      else if (lv == ~0u) c.template step<true, false>(st, raw, lv, far, a, area);
+      else if (lv) c.template step<false, false>(st, raw, lv, far, a, area);
       stage = stage + 1 == kStages ? 0 : stage + 1;
     }
+    if (TMA && !alive)  // its copies in flight, if any land
+      for (int s = 0; s < kStages; ++s) mbar_wait_drain(bars + s, (phases >> s) & 1, kDrainNs);
     cp_async_wait<0>();
     __syncthreads();  // every warp is through with its ring: it now takes the results [warp][heads][DV]
     float* res = reinterpret_cast<float*>(smem);
@@ -679,26 +762,34 @@ __global__ void __launch_bounds__(kDecodeThreads, S::kCtasPerSm) decode4_stream_
     }
     if (!out && pc.starts && tid == 0) note_item(a, run, pc, per_seq, cta);
     at += pc.dealt;
+    if constexpr (TMA) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the results' bytes take copies again
     __syncthreads();
   }
 }
 
-template <class S>
-cudaError_t launch_decode4_shape(const DecodeArgs& a, const Units4& u, cudaStream_t s) {
+template <class S, bool TMA>
+cudaError_t launch_decode4_mode(const DecodeArgs& a, const Units4& u, const Maps4& maps, cudaStream_t s) {
   if (a.split) {
     const long long ctas = static_cast<long long>(a.B) * a.Hkv * a.chunks * a.split;
-    const cudaError_t e = smem_attr_once<decode4_stream_kernel<S, true>>(S::kSmem);
+    const size_t smem = S::kSmem + S::kAlign;
+    const cudaError_t e = smem_attr_once<decode4_stream_kernel<S, true, TMA>>(smem);
     if (e != cudaSuccess) return e;
     if (ctas >= (1LL << 31)) return cudaErrorInvalidConfiguration;
     const dim3 grid(static_cast<unsigned>(ctas));
-    if (a.split == 1) return launch_pdl(decode4_stream_kernel<S, true>, grid, dim3(kDecodeThreads), S::kSmem, s, a, u);
-    return launch_pdl_cluster(decode4_stream_kernel<S, true>, grid, dim3(kDecodeThreads), S::kSmem, s, a.split, a, u);
+    if (a.split == 1) return launch_pdl(decode4_stream_kernel<S, true, TMA>, grid, dim3(kDecodeThreads), smem, s, a, u, maps);
+    return launch_pdl_cluster(decode4_stream_kernel<S, true, TMA>, grid, dim3(kDecodeThreads), smem, s, a.split, a, u, maps);
   }
-  const size_t smem = S::kSmem + sizeof(unsigned) * (a.B + 1);
-  const cudaError_t e = smem_attr_once<decode4_stream_kernel<S, false>>(smem);
+  const size_t smem = S::kSmem + S::kAlign + sizeof(unsigned) * (a.B + 1);
+  const cudaError_t e = smem_attr_once<decode4_stream_kernel<S, false, TMA>>(smem);
   if (e != cudaSuccess) return e;
   // After the kernel before it, not among its CTAs: this wave fills the SMs exactly (decode_stream.cuh).
-  return launch_serial(decode4_stream_kernel<S, false>, dim3(a.ctas), dim3(kDecodeThreads), smem, s, a, u);
+  return launch_serial(decode4_stream_kernel<S, false, TMA>, dim3(a.ctas), dim3(kDecodeThreads), smem, s, a, u, maps);
+}
+
+template <class S>
+cudaError_t launch_decode4_shape(const DecodeArgs& a, const Units4& u, const Maps4* maps, cudaStream_t s) {
+  if (maps) return launch_decode4_mode<S, true>(a, u, *maps, s);
+  return launch_decode4_mode<S, false>(a, u, Maps4{}, s);
 }
 
 }  // namespace cb

@@ -20,4 +20,7 @@ uint64_t host_timeout_ns();
 bool host_map_bf16(CUtensorMap* out, const void* ptr, const cuuint64_t* dims, const cuuint64_t* strides_bytes,
                    const cuuint32_t* box);
 
+// The same for bytes, swizzled in 32 or 64 bytes (the box's inner extent).
+bool host_map_u8(CUtensorMap* out, const void* ptr, const cuuint64_t* dims, const cuuint64_t* strides_bytes, const cuuint32_t* box);
+
 }  // namespace cb

@@ -425,6 +425,7 @@ struct DecodeArgs {
   int* record;          // workspace: per CTA {item, pieces} of the item it starts and does not finish
   int ctas;             // grid of the main kernel
   int* err;
+  uint64_t timeout_ns;  // 4-bit caches: bound of the waits
 };
 constexpr int kDecodeSimtHeads = 8, kDecodeMmaHeads = 16;  // most query heads of one item
 // CTAs of a streaming kernel that an SM holds: by registers 4, 3 or 2 (rings of 48, 72 or 96 KB), and no more than
@@ -449,8 +450,8 @@ cudaError_t launch_decode(const DecodeArgs& a, bool bf16, bool vec, cudaStream_t
 // CTAs that an SM holds: by registers 3 or 2, and no more than its shared memory does.
 constexpr int decode4_ctas_per_sm(int dk, int dv, bool bf16, int heads, int batch) {
   const int DK = dk <= 64 ? 64 : 128, DV = dv <= 64 ? 64 : 128, hd = heads <= 8 ? 8 : 16;
-  const int most = !bf16 || hd == 16 ? 2 : 3, ring = 4 * 3 * 32 * 9 * (DK + DV) / 16, results = 4 * 5 * hd * DV;
-  const int bytes = (ring > results ? ring : results) + 4 * 1024 + 4 * (batch + 1) + 1824, fit = 233472 / bytes;
+  const int most = !bf16 || hd == 16 ? 2 : 4, ring = 4 * 2 * 32 * (DK + DV) / 2, results = 4 * 5 * hd * DV;
+  const int bytes = (ring > results ? ring : results) + 4 * 1024 + ring / 8 + (bf16 ? 1 : 2) * DK * hd * 2 + 96 + 512 + 4 * (batch + 1) + 1824, fit = 233472 / bytes;
   return fit < most ? fit : most;
 }
 constexpr int kDecode4Heads = 16, kDecode4HeadsF32 = 8;  // most query heads of one item
@@ -459,9 +460,15 @@ constexpr int kDecode4Heads = 16, kDecode4HeadsF32 = 8;  // most query heads of 
 struct Units4 {
   unsigned k_p, k_t, v_p, v_t, kx_p, kx_t, vx_p, vx_t;
 };
-cudaError_t launch_decode4_bf16(const DecodeArgs& a, const Units4& u, cudaStream_t s);
-cudaError_t launch_decode4_f32(const DecodeArgs& a, const Units4& u, cudaStream_t s);
-cudaError_t launch_decode4(const DecodeArgs& a, bool bf16, bool vec, cudaStream_t s);
+// Codes of keys and values as 4-D tensors (bytes of a row, slots, heads, pages), boxes of decode4_box.
+struct Maps4 {
+  CUtensorMap k, v;
+};
+inline int decode4_box(int dim) { return dim <= 64 ? 32 : 64; }  // bytes of a row; 16 slots; swizzled in 32 or 64 bytes
+// maps: pages of a multiple of 16 slots, or null.
+cudaError_t launch_decode4_bf16(const DecodeArgs& a, const Units4& u, const Maps4* maps, cudaStream_t s);
+cudaError_t launch_decode4_f32(const DecodeArgs& a, const Units4& u, const Maps4* maps, cudaStream_t s);
+cudaError_t launch_decode4(const DecodeArgs& a, bool bf16, bool vec, const Maps4* maps, cudaStream_t s);
 // cb_attention with few queries per key head through the streaming kernel:
 // columns are (query, head) pairs, at most kDecodeMmaHeads (bf16) or
 // kDecodeSimtHeads (fp32) of them per item.  Fills a from rw.

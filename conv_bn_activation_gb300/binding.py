@@ -224,7 +224,7 @@ def nchw(t) -> CbTensor:
 # as long to build.
 _HEADS = struct.Struct("P4i3qi4x")   # CbHeads
 _SCORE = struct.Struct("2fP2i4P")    # CbScore
-_RULE = struct.Struct("if2P3i4x3P2q")  # CbHeadRule
+_RULE, _RULE_POS = struct.Struct("if2P3i4x2P"), struct.Struct("P2q")  # CbHeadRule: what a Rotation holds, and the positions
 _raw_stream = None
 _codes = None
 
@@ -352,29 +352,32 @@ class Rotation:
     Keeps the tensors."""
 
     def __init__(self, freq=None, axis=None, axes=1, adjacent=False, norm=False, eps=1e-6, q_weight=None, k_weight=None):
-        self.freq, self.axis, self.axes, self.adjacent = freq, axis, int(axes), bool(adjacent)
-        self.norm, self.eps, self.q_weight, self.k_weight = bool(norm), float(eps), q_weight, k_weight
         if not norm and (q_weight is not None or k_weight is not None):
             raise ValueError("q_weight and k_weight are the norm's")
         if axis is not None and freq is None:
             raise ValueError("axis: the axes of freq's pairs")
+        self.freq, self.axis, self.axes, self.adjacent = freq, axis, int(axes), bool(adjacent)
+        self.norm, self.eps, self.q_weight, self.k_weight = bool(norm), float(eps), q_weight, k_weight
+        tensors = [t for t in (freq, axis, q_weight, k_weight) if t is not None]
+        self.device = _device_of(*tensors) if tensors else None
+        self.pairs = 0 if freq is None else freq.shape[0]
+        weight = next((t for t in (q_weight, k_weight) if t is not None), None)
+        self.dim = None if weight is None else weight.shape[0]
+        self._head = _RULE.pack(self.norm, self.eps, _device_array(q_weight, "q_weight", "f32", (self.dim,)),
+                                _device_array(k_weight, "k_weight", "f32", (self.dim,)), 2 * self.pairs, self.adjacent, self.axes,
+                                _device_array(freq, "freq", "f32", (self.pairs,)), _device_array(axis, "axis", "i32", (self.pairs,)))
 
     def view(self, batch, length, dim, pos=None, device=None) -> bytes:
-        """cb_head_rule for [batch, length, ., dim] heads at `pos`, packed; checks the arrays."""
-        pairs = 0 if self.freq is None else self.freq.shape[0]
-        at = sa = sb = 0
-        if pairs:
-            if _codes is None:
-                _init_codes()
-            if pos is None or pos.dtype is not _codes["i32"] or pos.shape != (self.axes, batch, length) or \
-                    (length > 1 and pos.stride(2) != 1) or device not in (None, pos.get_device()):
-                raise ValueError(f"pos: an int32 tensor of shape {(self.axes, batch, length)} on the call's device, its last dim "
-                                 "contiguous")
-            at, (sa, sb, _) = pos.data_ptr(), pos.stride()
-        return _RULE.pack(self.norm, self.eps, _device_array(self.q_weight, "q_weight", "f32", (dim,), device),
-                          _device_array(self.k_weight, "k_weight", "f32", (dim,), device), 2 * pairs, self.adjacent, self.axes,
-                          _device_array(self.freq, "freq", "f32", (pairs,), device),
-                          _device_array(self.axis, "axis", "i32", (pairs,), device), at, sa, sb)
+        """cb_head_rule for [batch, length, ., dim] heads at `pos`, packed; checks the positions."""
+        if self.dim not in (None, dim) or (self.device is not None and device not in (None, self.device)):
+            raise ValueError(f"heads of {self.dim} dims on device {self.device}, as the rule's tensors are")
+        if not self.pairs:
+            return self._head + _RULE_POS.pack(0, 0, 0)
+        if pos is None or pos.dtype is not _codes["i32"] or pos.shape != (self.axes, batch, length) or \
+                pos.get_device() != self.device or (length > 1 and pos.stride(2) != 1):
+            raise ValueError(f"pos: an int32 tensor of shape {(self.axes, batch, length)} on the rule's device, its last dim contiguous")
+        sa, sb, _ = pos.stride()
+        return self._head + _RULE_POS.pack(pos.data_ptr(), sa, sb)
 
 
 class PagedCache4:

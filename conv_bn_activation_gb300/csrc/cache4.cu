@@ -1,6 +1,14 @@
 // Tokens into the pages of a 4-bit cache and back (cb_cache4_append,
 // cb_cache4_read).  Both are bound by HBM: 16 or 32 bits an element on one side
 // and 4.5 on the other.
+//
+// Rows of whole groups and 16-byte pieces (dims that are multiples of 32): a lane
+// takes eight dims of a row, a word of codes, so four lanes share a group and its
+// scale.  A token's words of all heads, keys then values, lie side by side over
+// the lanes; which head and dims a lane's words are, and where they lie in a
+// token's row and a page's slot, is worked out once per launch, as in
+// cache_append.cu.  The reads of all a lane's words are in flight before it
+// looks the token's page up.
 #include "cache4.cuh"
 #include "launch_util.h"
 #include "ptx.cuh"
@@ -66,6 +74,181 @@ __global__ void __launch_bounds__(32 * kWarps) cache4_read_rows_kernel(const Rea
   }
 }
 
+// Eight elements of a row.
+template <typename T>
+struct Eight {
+  uint4 w[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) w[i] = reinterpret_cast<const uint4*>(p)[i];
+  }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    if constexpr (sizeof(T) == 4) {
+      unpack16<T>(w[0], *reinterpret_cast<float(*)[4]>(x));
+      unpack16<T>(w[1], *reinterpret_cast<float(*)[4]>(x + 4));
+    } else {
+      unpack16<T>(w[0], x);
+    }
+  }
+};
+
+// Where a lane's words lie: elements from the token's row of keys or values,
+// bytes from the slot's row of their codes, elements from that of their scales.
+struct Word {
+  bool is_v, writes;  // writes: the lane that stores or reads the group's scale's pair
+  int from, to, scale, group;
+};
+__device__ __forceinline__ Word word_of(int e, int keys, int kw, int vw, long long ks_h, long long vs_h, const PagedArgs& c) {
+  Word w;
+  w.is_v = e >= keys;
+  const int x = w.is_v ? e - keys : e, n = w.is_v ? vw : kw, h = x / n, i = x - h * n;
+  w.from = static_cast<int>(h * (w.is_v ? vs_h : ks_h)) + 8 * i;
+  w.to = static_cast<int>(h * (w.is_v ? c.vs_h : c.ks_h)) + 4 * i;
+  w.group = i / 4;
+  w.scale = static_cast<int>(h * (w.is_v ? c.vx_h : c.kx_h)) + w.group;
+  w.writes = i % 4 == 0;
+  return w;
+}
+
+// The token that a unit of a launch is about.
+struct Walk {
+  long long token, step, tokens;
+  int b, t, step_b, step_t, T;
+  __device__ __forceinline__ Walk(int warp, int warps, int chunks, int T_, long long tokens_) : T(T_) {
+    step = warps / chunks, token = warp / chunks, tokens = tokens_;
+    step_b = static_cast<int>(step / T), step_t = static_cast<int>(step - static_cast<long long>(step_b) * T);
+    b = static_cast<int>(token / T), t = static_cast<int>(token - static_cast<long long>(b) * T);
+  }
+  __device__ __forceinline__ bool here() const { return token < tokens; }
+  __device__ __forceinline__ void next() {
+    token += step, b += step_b, t += step_t;
+    if (t >= T) t -= T, ++b;
+  }
+};
+
+template <typename T, int U>
+__global__ void __launch_bounds__(32 * kWarps) cache4_append_kernel(const AppendArgs a, long long tokens, int chunks, int warps) {
+  const int lane = threadIdx.x & 31, warp = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const int kw = a.dk / 8, vw = a.dv / 8, keys = a.H * kw, words = a.H * (kw + vw), first = warp % chunks * (32 * U) + lane;
+  Word w[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) w[u] = word_of(min(first + 32 * u, words - 1), keys, kw, vw, a.ks_h, a.vs_h, a.cache);
+  const int spare_k = scales4(a.dk) * kGroup4 - a.dk, spare_v = scales4(a.dv) * kGroup4 - a.dv;  // a scale of zero behind the last
+  pdl_wait();
+  pdl_launch_dependents();
+  if (warp >= warps) return;
+  for (Walk at(warp, warps, chunks, a.T, tokens); at.here(); at.next()) {
+    const int b = at.b, t = at.t;
+    if (a.count && t >= a.count[b]) continue;
+    const T* ks = static_cast<const T*>(a.k) + b * a.ks_b + t * a.ks_l;
+    const T* vs = static_cast<const T*>(a.v) + b * a.vs_b + t * a.vs_l;
+    Eight<T> x[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (first + 32 * u < words) x[u].load((w[u].is_v ? vs : ks) + w[u].from);
+    int slot = 0;
+    const long long page = cache_page(a.cache, a.err, b, static_cast<long long>(a.pos[b]) + t, &slot);
+    if (page < 0) continue;
+    uint8_t* kd = const_cast<uint8_t*>(key_codes4(a.cache, page, slot, 0));
+    uint8_t* vd = const_cast<uint8_t*>(value_codes4(a.cache, page, slot, 0));
+    uint16_t* kx = const_cast<uint16_t*>(key_scales4(a.cache, page, slot, 0));
+    uint16_t* vx = const_cast<uint16_t*>(value_scales4(a.cache, page, slot, 0));
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float f[8];
+      x[u].get(f);
+      unsigned top = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(f[i]) & 0x7fffffffu);
+      top = max(top, __shfl_xor_sync(~0u, top, 1));
+      top = max(top, __shfl_xor_sync(~0u, top, 2));
+      const unsigned bits = scale4_bits(top);
+      const uint32_t code = Coder4(bits).word(f);
+      if (first + 32 * u < words) {
+        *reinterpret_cast<uint32_t*>((w[u].is_v ? vd : kd) + w[u].to) = code;
+        if (w[u].writes) {
+          uint16_t* s = (w[u].is_v ? vx : kx) + w[u].scale;
+          s[0] = static_cast<uint16_t>(bits);
+          const int last = (w[u].is_v ? a.dv : a.dk) / kGroup4 - 1;
+          if ((w[u].is_v ? spare_v : spare_k) && w[u].group == last) s[1] = 0;
+        }
+      }
+    }
+  }
+}
+
+template <typename T, int U>
+__global__ void __launch_bounds__(32 * kWarps) cache4_read_kernel(const Read4Args a, long long tokens, int chunks, int warps) {
+  const int lane = threadIdx.x & 31, warp = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const int kw = a.dk / 8, vw = a.dv / 8, keys = a.H * kw, words = a.H * (kw + vw), first = warp % chunks * (32 * U) + lane;
+  Word w[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) w[u] = word_of(min(first + 32 * u, words - 1), keys, kw, vw, a.ks_h, a.vs_h, a.cache);
+  pdl_wait();
+  pdl_launch_dependents();
+  if (warp >= warps) return;
+  for (Walk at(warp, warps, chunks, a.T, tokens); at.here(); at.next()) {
+    const int b = at.b, t = at.t;
+    if (a.count && t >= a.count[b]) continue;
+    int slot = 0;
+    const long long page = cache_page(a.cache, a.err, b, (a.first ? static_cast<long long>(a.first[b]) : 0) + t, &slot);
+    const uint8_t* ks = key_codes4(a.cache, page, slot, 0);
+    const uint8_t* vs = value_codes4(a.cache, page, slot, 0);
+    const uint16_t* kx = key_scales4(a.cache, page, slot, 0);
+    const uint16_t* vx = value_scales4(a.cache, page, slot, 0);
+    uint32_t code[U];
+    unsigned scale[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      code[u] = 0, scale[u] = 0;  // a token that has no page reads as zeros
+      if (page >= 0 && first + 32 * u < words) {
+        code[u] = *reinterpret_cast<const uint32_t*>((w[u].is_v ? vs : ks) + w[u].to);
+        scale[u] = ((w[u].is_v ? vx : kx) + w[u].scale)[0];
+      }
+    }
+    T* kd = static_cast<T*>(a.k) + b * a.ks_b + t * a.ks_l;
+    T* vd = static_cast<T*>(a.v) + b * a.vs_b + t * a.vs_l;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (first + 32 * u >= words) continue;
+      const float s = bf16_value(scale[u]);
+      float f[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)  // 2^23 + (c + 8), less 2^23 + 8
+        f[i] = page < 0 ? 0.f : (__uint_as_float(((code[u] >> (4 * i)) & 15u) | 0x4b000000u) - 8388616.f) * s;
+      uint4* y = reinterpret_cast<uint4*>((w[u].is_v ? vd : kd) + w[u].from);
+      if constexpr (sizeof(T) == 4) {
+        y[0] = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+        y[1] = make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7]));
+      } else {
+        uint32_t h[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const __nv_bfloat162 p = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+          h[i] = *reinterpret_cast<const uint32_t*>(&p);
+        }
+        y[0] = make_uint4(h[0], h[1], h[2], h[3]);
+      }
+    }
+  }
+}
+
+template <typename T, int U, class Args, class Kernel>
+cudaError_t launch_words(Kernel kernel, const Args& a, int sms, cudaStream_t s) {
+  const long long tokens = static_cast<long long>(a.B) * a.T;
+  const int words = a.H * (a.dk + a.dv) / 8, chunks = (words + 32 * U - 1) / (32 * U);
+  const long long units = tokens * chunks, most = 4LL * kWarps * sms;
+  const long long warps = units < most ? units : (most < chunks ? chunks : most / chunks * chunks);
+  return launch_pdl(kernel, dim3(static_cast<unsigned>((warps + kWarps - 1) / kWarps)), dim3(32 * kWarps), 0, s, a, tokens, chunks,
+                    static_cast<int>(warps));
+}
+
+// A CTA's worth of words per SM or fewer: one to a lane, so that a token's heads spread over the GPU; more: four.
+template <class Args>
+bool few_words(const Args& a, int sms) {
+  return static_cast<long long>(a.B) * a.T * a.H * ((a.dk + a.dv) / 8) <= 32LL * kWarps * 8 * sms;
+}
+
 unsigned grid_of(long long rows, int sms) {
   const long long ctas = (rows + kWarps - 1) / kWarps, most = 16LL * sms;
   return static_cast<unsigned>(ctas < most ? ctas : most);
@@ -74,12 +257,26 @@ unsigned grid_of(long long rows, int sms) {
 }  // namespace
 
 cudaError_t launch_cache4_append(const AppendArgs& a, bool bf16, bool vec, int sms, cudaStream_t s) {
+  if (vec) {
+    if (few_words(a, sms))
+      return bf16 ? launch_words<__nv_bfloat16, 1>(cache4_append_kernel<__nv_bfloat16, 1>, a, sms, s)
+                  : launch_words<float, 1>(cache4_append_kernel<float, 1>, a, sms, s);
+    return bf16 ? launch_words<__nv_bfloat16, 4>(cache4_append_kernel<__nv_bfloat16, 4>, a, sms, s)
+                : launch_words<float, 4>(cache4_append_kernel<float, 4>, a, sms, s);
+  }
   const long long rows = 2LL * a.B * a.T * a.H;
   return bf16 ? launch_pdl(cache4_append_rows_kernel<__nv_bfloat16>, dim3(grid_of(rows, sms)), dim3(32 * kWarps), 0, s, a, rows)
               : launch_pdl(cache4_append_rows_kernel<float>, dim3(grid_of(rows, sms)), dim3(32 * kWarps), 0, s, a, rows);
 }
 
 cudaError_t launch_cache4_read(const Read4Args& a, bool bf16, bool vec, int sms, cudaStream_t s) {
+  if (vec) {
+    if (few_words(a, sms))
+      return bf16 ? launch_words<__nv_bfloat16, 1>(cache4_read_kernel<__nv_bfloat16, 1>, a, sms, s)
+                  : launch_words<float, 1>(cache4_read_kernel<float, 1>, a, sms, s);
+    return bf16 ? launch_words<__nv_bfloat16, 4>(cache4_read_kernel<__nv_bfloat16, 4>, a, sms, s)
+                : launch_words<float, 4>(cache4_read_kernel<float, 4>, a, sms, s);
+  }
   const long long rows = 2LL * a.B * a.T * a.H;
   return bf16 ? launch_pdl(cache4_read_rows_kernel<__nv_bfloat16>, dim3(grid_of(rows, sms)), dim3(32 * kWarps), 0, s, a, rows)
               : launch_pdl(cache4_read_rows_kernel<float>, dim3(grid_of(rows, sms)), dim3(32 * kWarps), 0, s, a, rows);

@@ -49,6 +49,12 @@ struct Coder4 {
     if (a > half || (a == half && (static_cast<int>(k) & 1))) k += copysignf(1.f, r);
     return static_cast<unsigned>(static_cast<int>(fminf(fmaxf(k, -7.f), 7.f)) + 8);
   }
+  __device__ __forceinline__ uint32_t word(const float (&x)[8]) const {
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w |= nibble(x[i]) << (4 * i);
+    return w;
+  }
 };
 
 // Where token j of sequence b lies: its page, or -1 (and the error recorded).

@@ -71,6 +71,18 @@ bool streams(const cb_paged_cache4* c) {
                 {c->vs_stride_page, c->vs_stride_slot, c->vs_stride_head});
 }
 
+// Tokens and pages that the kernels for whole groups take: rows of 16-byte pieces, dims of 32, heads within 32 bits of
+// their token's or slot's first.
+bool words(const cb_heads* t, const void* codes, int dim, long long page, long long slot, long long head, long long scale_head) {
+  auto near = [&](long long stride) { return stride * (t->heads - 1) + dim < (1LL << 31); };
+  return dim % 32 == 0 && pieces16(t) && reinterpret_cast<uintptr_t>(codes) % 4 == 0 && page % 4 == 0 && slot % 4 == 0 &&
+         head % 4 == 0 && near(t->stride_h) && near(head) && near(scale_head);
+}
+bool words(const cb_heads* k, const cb_heads* v, const cb_paged_cache4* c) {
+  return words(k, c->k, c->dim_k, c->k_stride_page, c->k_stride_slot, c->k_stride_head, c->ks_stride_head) &&
+         words(v, c->v, c->dim_v, c->v_stride_page, c->v_stride_slot, c->v_stride_head, c->vs_stride_head);
+}
+
 // The codes' pages as the streaming kernels' copies take them; false where they cannot.
 bool code_map(CUtensorMap* m, const void* codes, const cb_paged_cache4* c, int dim, long long page, long long slot, long long head) {
   const cuuint64_t dims[4] = {static_cast<cuuint64_t>(dim / 2), static_cast<cuuint64_t>(c->page_size), static_cast<cuuint64_t>(c->heads),
@@ -205,7 +217,7 @@ cb_status cb_cache4_append(const cb_heads* k_new, const cb_heads* v_new, const i
   a.pos = pos, a.count = count;
   a.cache = paged_args(cache);
   a.B = k_new->batch, a.T = k_new->len, a.H = cache->heads, a.dk = cache->dim_k, a.dv = cache->dim_v;
-  return done(launch_cache4_append(a, k_new->dtype == CB_DTYPE_BF16, false, sms, static_cast<cudaStream_t>(stream)));
+  return done(launch_cache4_append(a, k_new->dtype == CB_DTYPE_BF16, words(k_new, v_new, cache), sms, static_cast<cudaStream_t>(stream)));
 }
 
 cb_status cb_cache4_read(const cb_paged_cache4* cache, const int* first, const int* count, cb_heads* k_out, cb_heads* v_out,
@@ -225,7 +237,7 @@ cb_status cb_cache4_read(const cb_paged_cache4* cache, const int* first, const i
   a.first = first, a.count = count;
   a.cache = paged_args(cache);
   a.B = k_out->batch, a.T = k_out->len, a.H = cache->heads, a.dk = cache->dim_k, a.dv = cache->dim_v;
-  return done(launch_cache4_read(a, k_out->dtype == CB_DTYPE_BF16, false, sms, static_cast<cudaStream_t>(stream)));
+  return done(launch_cache4_read(a, k_out->dtype == CB_DTYPE_BF16, words(k_out, v_out, cache), sms, static_cast<cudaStream_t>(stream)));
 }
 
 cb_status cb_attention_decode4_workspace(const cb_heads* q, const cb_paged_cache4* cache, size_t* bytes) {

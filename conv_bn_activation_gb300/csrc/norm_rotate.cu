@@ -22,6 +22,7 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kMaxPairs = 64;
+constexpr int kPiecesCtas = 5, kDepth = 3;  // resident CTAs an SM; groups copied ahead
 
 // freq / (2 pi) as a 64-bit fraction of a turn; freq is finite.
 __device__ __forceinline__ unsigned long long turn_of(float freq) {
@@ -107,9 +108,230 @@ __global__ void __launch_bounds__(32 * kWarps) rotate_rows_kernel(const RotateAr
   }
 }
 
+template <int BYTES>
+__device__ __forceinline__ void copy_ahead(void* dst, const void* src) {
+  if constexpr (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(dst)), "l"(src), "n"(BYTES) : "memory");
+}
+
+// A 16-byte piece of a row as pairs of fp32, and back.
+template <typename T>
+__device__ __forceinline__ void unpack(uint4 w, f2* x) {
+  float f[16 / sizeof(T)];
+  unpack16<T>(w, f);
+#pragma unroll
+  for (int i = 0; i < 8 / static_cast<int>(sizeof(T)); ++i) x[i] = pack2(f[2 * i], f[2 * i + 1]);
+}
+template <typename T>
+__device__ __forceinline__ uint4 pack(const f2* x) {
+  uint32_t u[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float lo, hi;
+    if constexpr (sizeof(T) == 4) {
+      unpack2(x[i / 2], lo, hi);
+      u[i] = __float_as_uint(i & 1 ? hi : lo);
+    } else {
+      unpack2(x[i], lo, hi);
+      const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+      u[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+  }
+  return make_uint4(u[0], u[1], u[2], u[3]);
+}
+
+// Rows of whole 16-byte pieces, pairs in whole pieces.  Bound by HBM.  `width`
+// lanes (a power of two) share a head, each with two pieces of it: the halves of
+// the same pairs, or, adjacent pairs, any two; what does not turn is split in
+// halves too and turns by 0.  A warp works on queries or on keys: 32 / width heads
+// of a token at a time, every `parts`-th such group of its heads, then the next
+// token's.  Each lane copies its pieces ahead through a ring of its own in shared
+// memory: kDepth groups, where two in registers left the memory waiting (84 us
+// for 16384 tokens of 40 heads of 128, so 58).  A token's angles, two to a lane,
+// go through shared memory to the lanes that need them, times the weights.
+struct Split {  // of the grid's warps: the first `warps` of a view's kind, `parts` to a token
+  unsigned warps[2], parts[2];
+};
+template <typename T, bool ADJ>
+__global__ void __launch_bounds__(32 * kWarps, kPiecesCtas) rotate_pieces_kernel(const RotateArgs a, const int width, const Split split) {
+  constexpr int E = 16 / sizeof(T), H = E / 2;  // elements of a piece; pairs of fp32
+  __shared__ __align__(16) uint4 ring_s[kWarps][kDepth][2][32];
+  __shared__ int pos_s[kWarps][kDepth][2][32];
+  __shared__ __align__(16) float weight_s[2][2 * kMaxPairs];
+  __shared__ __align__(16) float cos_s[kWarps][kMaxPairs], sin_s[kWarps][kMaxPairs];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane & (width - 1), slot = lane / width, slots = 32 / width;
+  const int half = a.rotary / 2, turning = a.rotary / (2 * E);  // lanes of a head that hold turning halves
+  int p0 = sub * E, p1 = p0 + a.dim / 2;
+  if (!ADJ) {
+    if (sub < turning) p1 = p0 + half;
+    else p0 = a.rotary + (sub - turning) * E, p1 = p0 + (a.dim - a.rotary) / 2;
+  }
+  unsigned unit = blockIdx.x * kWarps + warp;
+  const bool is_k = unit >= split.warps[0];
+  if (is_k) unit -= split.warps[0];
+  const RotateView& v = a.v[is_k];
+  const unsigned parts = max(split.parts[is_k], 1u), part = unit % parts, step = split.warps[is_k] / parts;
+  const unsigned heads = v.heads, advance = parts * slots, first = part * slots + slot;
+  const unsigned tokens = static_cast<unsigned>(a.B) * static_cast<unsigned>(a.L);
+  const bool mine = sub < a.dim / (2 * E);
+  const float inv_dim = 1.f / static_cast<float>(a.dim);
+  const unsigned xs_h = static_cast<unsigned>(v.xs_h), ys_h = static_cast<unsigned>(v.ys_h);
+  float* const cos_ = cos_s[warp];
+  float* const sin_ = sin_s[warp];
+  pdl_wait();
+  pdl_launch_dependents();
+  const Pair pair[2] = {pair_of(a, lane), pair_of(a, lane + 32)};
+  const float* const weights = weight_s[is_k];
+
+  struct Place {
+    unsigned token, head;  // this lane's; a token's last group may have none for it
+  };
+  // Where the next rows to fetch lie, and where the next results go.
+  const T* x_at = nullptr;
+  T* y_at = nullptr;
+  auto fetch = [&](const Place& r, int at) {
+    if (r.token < tokens) {
+      if (r.head == first) {  // a new token
+        const unsigned b = r.token / static_cast<unsigned>(a.L), l = r.token - b * a.L;
+        x_at = static_cast<const T*>(v.x) + b * v.xs_b + l * v.xs_l + p0;
+        const int* pos = a.pos + b * a.ps_b + l;
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          if (lane + 32 * c < half) copy_ahead<4>(&pos_s[warp][at][c][lane], pos + pair[c].axis * a.ps_a);
+      }
+      if (mine && r.head < heads) {
+        const T* x = x_at + static_cast<unsigned long long>(r.head) * xs_h;
+        copy_ahead<16>(&ring_s[warp][at][0][lane], x);
+        copy_ahead<16>(&ring_s[warp][at][1][lane], x + (p1 - p0));
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  auto next = [&](Place& r) {
+    r.head += advance;
+    if (r.head - slot >= heads) r.head = first, r.token += step;
+  };
+  // Of this lane's pairs: z1 = inv (x1 (w1 cos) - x2 (w2 sin)), z2 = inv (x2 (w2 cos) + x1 (w1 sin)); adjacent pairs as
+  // (z1, z2) = inv ((x1, x2) (w1 cos, w2 cos) + (x2, x1) (-w2 sin, w1 sin)).
+  f2 c1[H], c2[H], s1[H], s2[H];
+  auto work = [&](const Place& r, int at) {
+    if (r.head == first) {
+      const unsigned b = r.token / static_cast<unsigned>(a.L), l = r.token - b * a.L;
+      y_at = static_cast<T*>(v.y) + b * v.ys_b + l * v.ys_l + p0;
+      __syncwarp();
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        if (lane + 32 * c < half) angle_of(pos_s[warp][at][c][lane], pair[c].turn, &sin_[lane + 32 * c], &cos_[lane + 32 * c]);
+      __syncwarp();
+      auto weight = [&](int d) { return mine ? weights[d] : 0.f; };
+#pragma unroll
+      for (int i = 0; i < H; ++i) {
+        if constexpr (ADJ) {  // pairs i of either piece
+          const float ca = cos_[p0 / 2 + i], sa = sin_[p0 / 2 + i], cb = cos_[p1 / 2 + i], sb = sin_[p1 / 2 + i];
+          const float wa = weight(p0 + 2 * i), wb = weight(p0 + 2 * i + 1), wc = weight(p1 + 2 * i), wd = weight(p1 + 2 * i + 1);
+          c1[i] = pack2(wa * ca, wb * ca), s1[i] = pack2(-wb * sa, wa * sa);
+          c2[i] = pack2(wc * cb, wd * cb), s2[i] = pack2(-wd * sb, wc * sb);
+        } else {  // pairs 2 i and 2 i + 1, whose halves the pieces are
+          const float2 co = *reinterpret_cast<const float2*>(cos_ + sub * E + 2 * i), si = *reinterpret_cast<const float2*>(sin_ + sub * E + 2 * i);
+          const float wa = weight(p0 + 2 * i), wb = weight(p0 + 2 * i + 1), wc = weight(p1 + 2 * i), wd = weight(p1 + 2 * i + 1);
+          c1[i] = pack2(wa * co.x, wb * co.y), s1[i] = pack2(wa * si.x, wb * si.y);
+          c2[i] = pack2(wc * co.x, wd * co.y), s2[i] = pack2(-wc * si.x, -wd * si.y);
+        }
+      }
+    }
+    f2 x[E];  // piece 0, piece 1
+    unpack<T>(ring_s[warp][at][0][lane], x), unpack<T>(ring_s[warp][at][1][lane], x + H);
+    f2 inv = pack2(1.f, 1.f);
+    if (a.norm) {
+      f2 sums = mul2(x[0], x[0]);
+#pragma unroll
+      for (int i = 1; i < E; ++i) sums = fma2(x[i], x[i], sums);
+      float lo, hi;
+      unpack2(sums, lo, hi);
+      float sum = lo + hi;
+      for (int o = width / 2; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+      const float f = rsqrtf(fmaf(sum, inv_dim, a.eps));
+      inv = pack2(f, f);
+    }
+#pragma unroll
+    for (int i = 0; i < H; ++i) {
+      const f2 y1 = x[i], y2 = x[H + i];
+      if constexpr (ADJ) {
+        float u, w;
+        unpack2(y1, u, w);
+        x[i] = mul2(fma2(pack2(w, u), s1[i], mul2(y1, c1[i])), inv);
+        unpack2(y2, u, w);
+        x[H + i] = mul2(fma2(pack2(w, u), s2[i], mul2(y2, c2[i])), inv);
+      } else {
+        x[i] = mul2(fma2(y2, s2[i], mul2(y1, c1[i])), inv);
+        x[H + i] = mul2(fma2(y1, s1[i], mul2(y2, c2[i])), inv);
+      }
+    }
+    if (mine && r.head < heads) {
+      T* y = y_at + static_cast<unsigned long long>(r.head) * ys_h;
+      *reinterpret_cast<uint4*>(y) = pack<T>(x);
+      *reinterpret_cast<uint4*>(y + (p1 - p0)) = pack<T>(x + H);
+    }
+  };
+  if (!mine)  // what is never copied adds nothing to a norm
+    for (int at = 0; at < kDepth; ++at) ring_s[warp][at][0][lane] = ring_s[warp][at][1][lane] = make_uint4(0, 0, 0, 0);
+  Place ahead{unit < split.warps[is_k] ? unit / parts : tokens, first}, now = ahead;
+#pragma unroll
+  for (int at = 0; at < kDepth - 1; ++at) fetch(ahead, at), next(ahead);
+  cos_[lane] = cos_[lane + 32] = 1.f, sin_[lane] = sin_[lane + 32] = 0.f;  // what does not turn
+  for (int d = threadIdx.x; d < 2 * a.dim; d += 32 * kWarps) {
+    const float* w = a.v[d >= a.dim].weight;
+    weight_s[d >= a.dim][d % a.dim] = w ? w[d % a.dim] : 1.f;
+  }
+  __syncthreads();
+  int at = 0;
+  while (now.token < tokens) {
+    fetch(ahead, at == 0 ? kDepth - 1 : at - 1);
+    next(ahead);
+    asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
+    work(now, at);
+    next(now);
+    at = at + 1 == kDepth ? 0 : at + 1;
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+template <typename T>
+cudaError_t launch_pieces(const RotateArgs& a, int sms, cudaStream_t s) {
+  constexpr int E = 16 / sizeof(T);
+  int width = 1;
+  while (width * 2 * E < a.dim) width *= 2;
+  const int slots = 32 / width;
+  const long long tokens = static_cast<long long>(a.B) * a.L;
+  const long long groups[2] = {(a.v[0].heads + slots - 1) / slots, (a.v[1].heads + slots - 1) / slots};
+  // The resident warps are dealt to queries and keys by their work: their groups and, per token, its angles and
+  // weights, which cost about as much as a group.  A token's heads go to as many warps as that leaves idle.
+  const long long most = static_cast<long long>(kPiecesCtas) * kWarps * sms, work[2] = {groups[0] + 1, groups[1] ? groups[1] + 1 : 0};
+  Split split{};
+  for (int v = 0; v < 2; ++v) {
+    if (!groups[v]) continue;
+    long long warps = most * work[v] / (work[0] + work[1]);
+    if (warps < 1) warps = 1;
+    long long parts = warps / tokens;
+    parts = parts < 1 ? 1 : parts > groups[v] ? groups[v] : parts;
+    if (warps > tokens * parts) warps = tokens * parts;
+    split.parts[v] = static_cast<unsigned>(parts);
+    split.warps[v] = static_cast<unsigned>((warps + parts - 1) / parts * parts);
+  }
+  const unsigned ctas = (split.warps[0] + split.warps[1] + kWarps - 1) / kWarps;
+  auto* kernel = a.adjacent ? rotate_pieces_kernel<T, true> : rotate_pieces_kernel<T, false>;
+  return launch_pdl(kernel, dim3(ctas), dim3(32 * kWarps), 0, s, a, width, split);
+}
+
+// Whether a head's offset in its token fits the kernel's 32 bits.
+bool near_heads(const RotateView& v) { return v.xs_h < (1LL << 31) && v.ys_h < (1LL << 31); }
+
 }  // namespace
 
 cudaError_t launch_norm_rotate(const RotateArgs& a, bool bf16, bool vec, int sms, cudaStream_t s) {
+  const int two = bf16 ? 16 : 8;  // elements of two pieces
+  if (vec && a.dim % two == 0 && (a.adjacent || a.rotary % two == 0) && near_heads(a.v[0]) && near_heads(a.v[1]))
+    return bf16 ? launch_pieces<__nv_bfloat16>(a, sms, s) : launch_pieces<float>(a, sms, s);
   const long long rows = static_cast<long long>(a.B) * a.L * (a.v[0].heads + a.v[1].heads);
   const long long ctas = (rows + kWarps - 1) / kWarps, most = 16LL * sms;
   const dim3 grid(static_cast<unsigned>(ctas < most ? ctas : most)), block(32 * kWarps);

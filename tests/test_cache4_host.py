@@ -150,16 +150,20 @@ def test_packed_rule_has_the_structures_layout(cblib):
     import torch
     freq, axis = torch.zeros(16), torch.zeros(16, dtype=torch.int32)
     w, pos = torch.ones(64), torch.zeros(5, 3, 9, dtype=torch.int32)[1:3, :, 2:]
-    rot = cblib.Rotation(freq, axis=axis, axes=2, adjacent=True, norm=True, eps=0.25, k_weight=w)
     with pytest.raises(ValueError):
-        rot.view(3, 7, 64, pos)  # host tensors
+        cblib.Rotation(freq, axis=axis, axes=2)  # host tensors
 
     class Claims(torch.Tensor):
         def get_device(self):
             return 0
 
-    rot.freq, rot.axis, rot.k_weight = (t.as_subclass(Claims) for t in (freq, axis, w))
-    packed = rot.view(3, 7, 64, pos.as_subclass(Claims), 0)
+    freq, axis, w, pos = (t.as_subclass(Claims) for t in (freq, axis, w, pos))
+    rot = cblib.Rotation(freq, axis=axis, axes=2, adjacent=True, norm=True, eps=0.25, k_weight=w)
+    packed = rot.view(3, 7, 64, pos, 0)
+    for bad in ((3, 7, 32, pos, 0), (3, 7, 64, pos, 1), (3, 7, 64, None, 0), (3, 6, 64, pos, 0), (3, 7, 64, pos.long(), 0),
+                (3, 7, 64, pos.transpose(1, 2).contiguous().transpose(1, 2), 0)):
+        with pytest.raises(ValueError):
+            rot.view(*bad)
     assert len(packed) == ctypes.sizeof(cblib.CbHeadRule)
     got = cblib.CbHeadRule.from_buffer_copy(packed)
     assert (got.norm, got.eps, got.q_weight, got.k_weight) == (1, 0.25, None, w.data_ptr())

@@ -18,6 +18,7 @@ namespace cb {
 namespace {
 
 constexpr int kWarps = 4;
+constexpr long long kWordCtas = 16;  // an SM
 
 // A warp per head of a token's keys or values: a lane per dim of a group.
 template <typename T>
@@ -81,6 +82,24 @@ struct Eight {
   __device__ __forceinline__ void load(const T* p) {
 #pragma unroll
     for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) w[i] = reinterpret_cast<const uint4*>(p)[i];
+  }
+  // The largest of their bits without sign, as fp32's.
+  __device__ __forceinline__ unsigned top() const {
+    if constexpr (sizeof(T) == 4) {
+      unsigned m = 0;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        m = max(max(m, max(w[i].x & 0x7fffffffu, w[i].y & 0x7fffffffu)), max(w[i].z & 0x7fffffffu, w[i].w & 0x7fffffffu));
+      return m;
+    } else {
+      const unsigned m = max2(max2(w[0].x & 0x7fff7fffu, w[0].y & 0x7fff7fffu), max2(w[0].z & 0x7fff7fffu, w[0].w & 0x7fff7fffu));
+      return max(m & 0xffff0000u, m << 16);
+    }
+  }
+  static __device__ __forceinline__ unsigned max2(unsigned a, unsigned b) {
+    unsigned m;
+    asm("max.s16x2 %0, %1, %2;" : "=r"(m) : "r"(a), "r"(b));
+    return m;
   }
   __device__ __forceinline__ void get(float (&x)[8]) const {
     if constexpr (sizeof(T) == 4) {
@@ -157,13 +176,11 @@ __global__ void __launch_bounds__(32 * kWarps) cache4_append_kernel(const Append
     for (int u = 0; u < U; ++u) {
       float f[8];
       x[u].get(f);
-      unsigned top = 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(f[i]) & 0x7fffffffu);
+      unsigned top = x[u].top();
       top = max(top, __shfl_xor_sync(~0u, top, 1));
       top = max(top, __shfl_xor_sync(~0u, top, 2));
       const unsigned bits = scale4_bits(top);
-      const uint32_t code = Coder4(bits).word(f);
+      const uint32_t code = Coder4(bits).word<sizeof(T) == 2>(f);
       if (first + 32 * u < words) {
         *reinterpret_cast<uint32_t*>((w[u].is_v ? vd : kd) + w[u].to) = code;
         if (w[u].writes) {
@@ -200,7 +217,7 @@ __global__ void __launch_bounds__(32 * kWarps) cache4_read_kernel(const Read4Arg
     unsigned scale[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      code[u] = 0, scale[u] = 0;  // a token that has no page reads as zeros
+      code[u] = 0x88888888u, scale[u] = 0;  // a token that has no page reads as zeros
       if (page >= 0 && first + 32 * u < words) {
         code[u] = *reinterpret_cast<const uint32_t*>((w[u].is_v ? vs : ks) + w[u].to);
         scale[u] = ((w[u].is_v ? vx : kx) + w[u].scale)[0];
@@ -211,23 +228,28 @@ __global__ void __launch_bounds__(32 * kWarps) cache4_read_kernel(const Read4Arg
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (first + 32 * u >= words) continue;
-      const float s = bf16_value(scale[u]);
-      float f[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i)  // 2^23 + (c + 8), less 2^23 + 8
-        f[i] = page < 0 ? 0.f : (__uint_as_float(((code[u] >> (4 * i)) & 15u) | 0x4b000000u) - 8388616.f) * s;
       uint4* y = reinterpret_cast<uint4*>((w[u].is_v ? vd : kd) + w[u].from);
       if constexpr (sizeof(T) == 4) {
+        const float s = bf16_value(scale[u]);
+        float f[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)  // 2^23 + (c + 8), less 2^23 + 8
+          f[i] = (__uint_as_float(((code[u] >> (4 * i)) & 15u) | 0x4b000000u) - 8388616.f) * s;
         y[0] = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
         y[1] = make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7]));
       } else {
-        uint32_t h[4];
+        // Dims i and i + 4 as bf16: 128 + (c + 8), less 136, times s: one rounding, the product's.
+        const uint32_t ss = scale[u] | (scale[u] << 16), base = 0xc308c308u;
+        uint32_t p[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const __nv_bfloat162 p = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-          h[i] = *reinterpret_cast<const uint32_t*>(&p);
+          const uint32_t n = ((code[u] >> (4 * i)) & 0x000f000fu) | 0x43004300u;
+          const __nv_bfloat162 c = __hadd2(*reinterpret_cast<const __nv_bfloat162*>(&n), *reinterpret_cast<const __nv_bfloat162*>(&base));
+          const __nv_bfloat162 v = __hmul2(c, *reinterpret_cast<const __nv_bfloat162*>(&ss));
+          p[i] = *reinterpret_cast<const uint32_t*>(&v);
         }
-        y[0] = make_uint4(h[0], h[1], h[2], h[3]);
+        y[0] = make_uint4(__byte_perm(p[0], p[1], 0x5410), __byte_perm(p[2], p[3], 0x5410), __byte_perm(p[0], p[1], 0x7632),
+                          __byte_perm(p[2], p[3], 0x7632));
       }
     }
   }
@@ -237,7 +259,7 @@ template <typename T, int U, class Args, class Kernel>
 cudaError_t launch_words(Kernel kernel, const Args& a, int sms, cudaStream_t s) {
   const long long tokens = static_cast<long long>(a.B) * a.T;
   const int words = a.H * (a.dk + a.dv) / 8, chunks = (words + 32 * U - 1) / (32 * U);
-  const long long units = tokens * chunks, most = 4LL * kWarps * sms;
+  const long long units = tokens * chunks, most = kWordCtas * kWarps * sms;
   const long long warps = units < most ? units : (most < chunks ? chunks : most / chunks * chunks);
   return launch_pdl(kernel, dim3(static_cast<unsigned>((warps + kWarps - 1) / kWarps)), dim3(32 * kWarps), 0, s, a, tokens, chunks,
                     static_cast<int>(warps));
@@ -274,8 +296,8 @@ cudaError_t launch_cache4_read(const Read4Args& a, bool bf16, bool vec, int sms,
     if (few_words(a, sms))
       return bf16 ? launch_words<__nv_bfloat16, 1>(cache4_read_kernel<__nv_bfloat16, 1>, a, sms, s)
                   : launch_words<float, 1>(cache4_read_kernel<float, 1>, a, sms, s);
-    return bf16 ? launch_words<__nv_bfloat16, 4>(cache4_read_kernel<__nv_bfloat16, 4>, a, sms, s)
-                : launch_words<float, 4>(cache4_read_kernel<float, 4>, a, sms, s);
+    return bf16 ? launch_words<__nv_bfloat16, 8>(cache4_read_kernel<__nv_bfloat16, 8>, a, sms, s)
+                : launch_words<float, 8>(cache4_read_kernel<float, 8>, a, sms, s);
   }
   const long long rows = 2LL * a.B * a.T * a.H;
   return bf16 ? launch_pdl(cache4_read_rows_kernel<__nv_bfloat16>, dim3(grid_of(rows, sms)), dim3(32 * kWarps), 0, s, a, rows)

@@ -13,19 +13,20 @@ constexpr int kGroup4 = 32;
 __host__ __device__ constexpr int scales4(int dim) { return 2 * ((dim + 2 * kGroup4 - 1) / (2 * kGroup4)); }
 constexpr unsigned kNanScale = 0x7fc0u;
 
-// max|x| / 7 rounded to bf16, as its bits; a maximum that is not finite (top:
-// the largest of the elements' bits without sign) gives NaN.  The quotient
-// rounded to 24 bits lies on the same side of a tie as the exact one unless it
-// is the tie: then the remainder decides.
-__device__ __forceinline__ unsigned scale4_bits(unsigned top) {
-  if (top >= 0x7f800000u) return kNanScale;
-  const float amax = __uint_as_float(top), q = __fdiv_rn(amax, 7.f);
-  const unsigned bits = __float_as_uint(q), low = bits & 0xffffu, hi = bits >> 16;
-  if (low != 0x8000u) return hi + (low > 0x8000u);
-  const float rest = fmaf(-7.f, q, amax);
-  return hi + (rest > 0.f || (rest == 0.f && (hi & 1)));
-}
 __device__ __forceinline__ float bf16_value(unsigned bits) { return __uint_as_float(bits << 16); }
+
+// max|x| / 7 rounded to bf16, as its bits; a maximum that is not finite (top:
+// the largest of the elements' bits without sign) gives NaN.  A quotient that is
+// off by a few 2^-24 names the right bf16 numbers around it, or is so near one of
+// them that either neighbour leads to it; 7 times their middle is exact, and the
+// remainder's sign with it.
+__device__ __forceinline__ unsigned scale4_bits(unsigned top) {
+  const float amax = __uint_as_float(top);
+  const unsigned lo = __float_as_uint(amax * (1.f / 7.f)) >> 16;
+  const float rest = fmaf(-7.f, __uint_as_float((lo << 16) | 0x8000u), amax);
+  const unsigned bits = lo + (rest > 0.f || (rest == 0.f && (lo & 1)));
+  return top >= 0x7f800000u ? kNanScale : bits;
+}
 
 // x / s rounded to the nearest whole number, ties to even, for a group's scale.
 // The product with 1 / s can miss a tie: the remainder x - k s, which is exact
@@ -33,27 +34,50 @@ __device__ __forceinline__ float bf16_value(unsigned bits) { return __uint_as_fl
 // says so.
 struct Coder4 {
   float s, inv, half, up;
-  __device__ __forceinline__ explicit Coder4(unsigned scale_bits) {
+  unsigned bits;
+  __device__ __forceinline__ explicit Coder4(unsigned scale_bits) : bits(scale_bits) {
     s = bf16_value(scale_bits);
     up = s < 0x1p-64f ? 0x1p64f : 1.f;  // 1 / s stays finite; both products are exact
     s *= up;
     const bool some = s > 0.f;  // neither 0 nor NaN
-    inv = some ? __fdividef(1.f, s) : 0.f;
-    if (!some) s = 0.f, up = 0.f;
-    half = some ? 0.5f * s : 1.f;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));  // s <= max / 7: 1 / s is no subnormal
+    if (!some) s = inv = 0.f;
+    half = some ? 0.5f * s : __builtin_huge_valf();
   }
   __device__ __forceinline__ unsigned nibble(float x) const {
-    x = up == 0.f ? 0.f : x * up;
+    if (s == 0.f) return 8;
+    x *= up;
     float k = rintf(x * inv);
     const float r = fmaf(-k, s, x), a = fabsf(r);
     if (a > half || (a == half && (static_cast<int>(k) & 1))) k += copysignf(1.f, r);
     return static_cast<unsigned>(static_cast<int>(fminf(fmaxf(k, -7.f), 7.f)) + 8);
   }
+  // Eight elements, for scales that are no subnormals: k = 7 is the most then (max / s < 7.02), and x / s + 8 comes out
+  // of one FMA with 1.5 * 2^23 as that number's low bits.  Twice, with 1 / s a little too large and a little too small:
+  // the two differ where x / s is a tie, or within 2^-18 of one.  bf16 elements, of 8 bits as the scale, have none of
+  // those but the ties (the others are 2^-12 away), whose even side is the one that is even; fp32 ones ask nibble().
+  template <bool BF16>
   __device__ __forceinline__ uint32_t word(const float (&x)[8]) const {
+    constexpr float kBase = 12582920.f;  // 1.5 * 2^23 + 8
+    const float more = inv * (1.f + 0x1p-19f), less = inv * (1.f - 0x1p-19f);
+    uint32_t q[8];
+    bool near = up != 1.f && s != 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t away = __float_as_uint(fmaf(x[i], more, kBase)), in = __float_as_uint(fmaf(x[i], less, kBase));
+      if (BF16) q[i] = away & 1 ? in : away;
+      else q[i] = away, near |= away != in;
+    }
     uint32_t w = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w |= nibble(x[i]) << (4 * i);
-    return w;
+    for (int i = 7; i >= 0; --i) w = w * 16u + q[i];
+    w -= 0x4b400000u * 0x11111111u;
+    if (near) {
+      w = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w |= nibble(x[i]) << (4 * i);
+    }
+    return s == 0.f ? 0x88888888u : w;
   }
 };
 

@@ -88,7 +88,7 @@ bool code_map(CUtensorMap* m, const void* codes, const cb_paged_cache4* c, int d
   const cuuint64_t dims[4] = {static_cast<cuuint64_t>(dim / 2), static_cast<cuuint64_t>(c->page_size), static_cast<cuuint64_t>(c->heads),
                               static_cast<cuuint64_t>(c->num_pages)};
   const cuuint64_t strides[3] = {static_cast<cuuint64_t>(slot), static_cast<cuuint64_t>(head), static_cast<cuuint64_t>(page)};
-  const cuuint32_t box[4] = {static_cast<cuuint32_t>(decode4_box(dim)), 16, 1, 1};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(decode4_box(c->dim_k, c->dim_v)), 16, 1, 1};
   return host_map_u8(m, codes, dims, strides, box);
 }
 

@@ -43,12 +43,47 @@ template <int BYTES>
 __device__ __forceinline__ void cp_async_small(uint32_t dst, const void* src, bool valid) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(valid ? BYTES : 0) : "memory");
 }
+__device__ __forceinline__ void copy_scales(uint32_t dst, const uint16_t* src, const uint16_t* any, int count, bool valid) {
+  if (count == 4) cp_async_small<8>(dst, valid ? src : any, valid);
+  else cp_async_small<4>(dst, valid ? src : any, valid);
+}
 __device__ __forceinline__ void tma_load_4d_at(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2, int c3) {
   asm volatile(
       "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
       " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
       : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 lds_f4(uint32_t at) {
+  const uint4 v = lds128(at);
+  return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
+}
+__device__ __forceinline__ float lds_f(uint32_t at) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts128(uint32_t at, float4 v) {
+  asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
+}
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<unsigned>(127 + e) << 23); }  // -126 <= e <= 127
+// mbar_wait for waits of microseconds: the hardware may hold the warp for as long, so that it takes no issue slots from
+// the others.
+__device__ __forceinline__ bool mbar_wait_long(uint64_t* bar, uint32_t parity, const Watchdog& wd) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(20000)
+      : "memory");
+  return ok || mbar_wait(bar, parity, wd);
 }
 __device__ __forceinline__ void ldsm4_4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -95,6 +130,10 @@ __device__ __forceinline__ uint32_t half2_times(uint32_t x, float bits) {  // bi
   const __half2 h = __hmul2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&y));
   return *reinterpret_cast<const uint32_t*>(&h);
 }
+__device__ __forceinline__ uint32_t half2_less(uint32_t x, uint32_t y) {
+  const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&y));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
 // What f16 rounding left of a pair: another pair of f16 numbers.
 __device__ __forceinline__ uint32_t half2_rest(float lo, float hi, uint32_t bits) {
   const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&bits));
@@ -102,7 +141,7 @@ __device__ __forceinline__ uint32_t half2_rest(float lo, float hi, uint32_t bits
 }
 
 constexpr uint32_t kLowNibble = 0x000f000fu, kHighNibble = 0x00f000f0u;  // times 2^-24, 2^-20
-constexpr uint32_t kLowMinus8 = 0x80088008u, kHighMinus8 = 0x80808080u;  // -8 in their units
+constexpr uint32_t kByte = 0x00ff00ffu, kByteMinus = 0x80888088u, kHighMinus8 = 0x80808080u;  // -8 (1 + 16), -8 in their units
 // Codes as f16 numbers of their own: 1024 + c + 8, then 1024 + 16 (c + 8).
 __device__ __forceinline__ uint32_t low_codes(uint32_t w) {
   const uint32_t x = (w & kLowNibble) | 0x64006400u;
@@ -143,17 +182,15 @@ __device__ __forceinline__ constexpr int swizzle4(int row) {
   return BYTES == 64 ? (row >> 1) & 3 : (row >> 2) & 1;
 }
 
-template <class S>
+template <class S, bool DIRECT>
 struct Decode4Math {
   using T = typename S::T;
   static constexpr int GK = S::GK, GV = S::GV, NB = S::NB;
-  DecodeScore score;
-
   int g, t4, heads, top_exp;
   uint32_t k_src, v_src;  // this lane's ldmatrix rows
   // Queries as the MMAs' B operand, for each part and group: head g, dims 8 t4 + (0, 4) and (1, 5) / 16, then (2, 6) and
   // (3, 7) / 16.  In shared memory, one copy for the CTA: in registers they would cost it a neighbour.
-  const uint4* queries;
+  uint32_t queries;
   // The offsets -8 sum q. bf16: of group t4 and head 8 nb + g, as two tf32 numbers: with a key's scales as A, one MMA
   // makes a score's share of them. fp32: of every group and this thread's heads 8 nb + 2 t4 and the one after.
   float offset[NB][2], first[S::kParts == 2 ? 2 : 1][S::kParts == 2 ? GK : 1][NB][2];
@@ -161,10 +198,11 @@ struct Decode4Math {
   // neg = kWeightBits - maximum (+infinity before the first token): weights are 2^(x + neg).
   float slope[NB][2], neg[NB][2], l[NB][2], o[2 * GV][NB][4];
 
-  __device__ __forceinline__ Decode4Math(const DecodeArgs& a, const Piece& pc, uint4* q_area) : score(a), queries(q_area + (threadIdx.x & 31)) {
+  __device__ __forceinline__ Decode4Math(const DecodeArgs& a, const Piece& pc, uint4* q_area) {
+    queries = smem_u32(q_area + (threadIdx.x & 31));
+    const DecodeScore score(a);
     const int lane = threadIdx.x & 31;
     g = lane >> 2, t4 = lane & 3, heads = pc.heads, top_exp = kMinTopExp;
-
     const int row = (lane & 7) + 8 * ((lane >> 3) & 1);
     k_src = row * S::kKeyBytes + (((lane >> 4) ^ swizzle4<S::kKeyBytes>(row)) * 16);
     v_src = row * S::kValBytes + (((lane >> 4) ^ swizzle4<S::kValBytes>(row)) * 16);
@@ -178,24 +216,34 @@ struct Decode4Math {
       const T* q = static_cast<const T*>(a.q) + pc.b * a.qs_b + (pc.h0 + (hd < heads ? hd : 0)) * a.qs_h;
       float x[GK][8], big = 0.f;
 #pragma unroll
-      for (int i = 0; i < GK; ++i)
+      for (int i = 0; i < GK; ++i) {
+        const T* at = q + 32 * i + 8 * t4;
+        if (hd >= heads || 32 * i >= a.dk) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int d = 32 * i + 8 * t4 + e;
-          x[i][e] = hd < heads && d < a.dk ? to_f32(q[d]) : 0.f;
-          big = fmaxf(big, fabsf(x[i][e]));
+          for (int e = 0; e < 8; ++e) x[i][e] = 0.f;
+        } else if (reinterpret_cast<uintptr_t>(q) % 16 == 0) {
+          constexpr int kPer = 16 / static_cast<int>(sizeof(T));
+#pragma unroll
+          for (int e = 0; e < 8; e += kPer) unpack16<T>(*reinterpret_cast<const uint4*>(at + e), *reinterpret_cast<float(*)[kPer]>(&x[i][e]));
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[i][e] = to_f32(at[e]);
         }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) big = fmaxf(big, fabsf(x[i][e]));
+      }
       big = fmaxf(big, __shfl_xor_sync(~0u, big, 1));
       big = fmaxf(big, __shfl_xor_sync(~0u, big, 2));
-      int e2 = 0;
-      if (big > 0.f && big < __builtin_huge_valf()) frexpf(big, &e2);
+      // below 2^e2; 0 for what is no number
+      const int e2 = big > 0.f && big < __builtin_huge_valf() ? max(static_cast<int>(__float_as_uint(big) >> 23), 1) - 126 : 0;
+      const float p1 = pow2((kBits - e2) / 2), p2 = pow2(kBits - e2 - (kBits - e2) / 2);
       exponent[nb] = e2 - kBits;
       if (big > 0.f) top = max(top, exponent[nb]);
 #pragma unroll
       for (int i = 0; i < GK; ++i) {
         float y[8], sum[S::kParts] = {};
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = ldexpf(x[i][e], kBits - e2);
+        for (int e = 0; e < 8; ++e) y[e] = x[i][e] * p1 * p2;
         if constexpr (S::kParts == 1) {
           uint32_t qf[4];
 #pragma unroll
@@ -231,14 +279,14 @@ struct Decode4Math {
     }
     for (int s = 4; s < 32; s <<= 1) top = max(top, __shfl_xor_sync(~0u, top, s));
     const int k_exp = min(max(top + kCodeBits, -126), 127);
-    k_mul = ldexpf(1.f, k_exp);
+    k_mul = pow2(k_exp);
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int from = 4 * (2 * t4 + e), hd = 8 * nb + 2 * t4 + e;
         const int he = __shfl_sync(~0u, exponent[nb], from);
-        head_mul[nb][e] = ldexpf(1.f, min(he + kCodeBits - k_exp, 16)) * (score.cap ? 1.f : score.c_scale);
+        head_mul[nb][e] = pow2(max(min(he + kCodeBits - k_exp, 16), -126)) * (score.cap ? 1.f : score.c_scale);
 #pragma unroll
         for (int p = 0; p < S::kParts && S::kParts == 2; ++p)
 #pragma unroll
@@ -268,63 +316,50 @@ struct Decode4Math {
         for (int r = 0; r < 4; ++r) o[d][nb][r] *= f[nb][r & 1];
   }
 
-  // Scores of 32 tokens before the heads' factors: element r of half h is key 16 h + g + 8 (r >> 1), head
-  // 8 nb + 2 t4 + (r & 1).
-  __device__ __forceinline__ void scores(float (&s)[2][NB][4], uint32_t keys, const float4* area) const {
-    float ks[2][2][4];
+  // Scores of 16 tokens before the heads' factors: element r is key g + 8 (r >> 1), head 8 nb + 2 t4 + (r & 1).
+  __device__ __forceinline__ void scores(float (&s)[NB][4], uint32_t keys, uint32_t area) const {
+    const float4 x0 = lds_f4(area + 16 * g), x1 = lds_f4(area + 16 * (g + 8));
+    const float k0[4] = {x0.x, x0.y, x0.z, x0.w}, k1[4] = {x1.x, x1.y, x1.z, x1.w};
+    if constexpr (S::kParts == 1) {  // a scale has bf16's 8 bits
+      const float y0 = lds_f(area + 16 * g + 4 * t4), y1 = lds_f(area + 16 * (g + 8) + 4 * t4);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float4 x = area[16 * h + 8 * e + g];
-        ks[h][e][0] = x.x, ks[h][e][1] = x.y, ks[h][e][2] = x.z, ks[h][e][3] = x.w;
-      }
-      if constexpr (S::kParts == 1) {  // a scale has bf16's 8 bits
-        const float* x = reinterpret_cast<const float*>(area + 16 * h + g) + t4;
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) mma_tf32(s[h][nb], x[0], x[32], x[0], x[32], offset[nb][0], offset[nb][1]);
-      }
+      for (int nb = 0; nb < NB; ++nb) mma_tf32(s[nb], y0, y1, y0, y1, offset[nb][0], offset[nb][1]);
     }
 #pragma unroll
     for (int i = 0; i < GK; i += 2) {
-      uint32_t w[2][4];  // groups i and i + 1: a word of key g and of key g + 8
-#pragma unroll
-      for (int h = 0; h < 2; ++h) ldsm4_4((keys + 16 * h * S::kKeyBytes + k_src) ^ (i * 16), w[h]);
+      uint32_t w[4];  // groups i and i + 1: a word of key g and of key g + 8
+      ldsm4_4((keys + k_src) ^ (i * 16), w);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
+        const uint32_t u = w[2 * j], v = w[2 * j + 1], ub = __byte_perm(u, 0, 0x4341), vb = __byte_perm(v, 0, 0x4341);
+        const uint32_t uh = u & kHighNibble, vh = v & kHighNibble, ubh = ub & kHighNibble, vbh = vb & kHighNibble;
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-          float acc[S::kParts][2][4];
+          float acc[S::kParts][4];
 #pragma unroll
           for (int p = 0; p < S::kParts; ++p) {
-            const uint4 q = queries[((p * GK + i + j) * NB + nb) * 32];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t u = w[h][2 * j], v = w[h][2 * j + 1];
-              const uint32_t u8 = u >> 8, v8 = v >> 8;
-              float f0 = 0.f, f1 = 0.f;
-              if constexpr (S::kParts == 2) f0 = first[p][i + j][nb][0], f1 = first[p][i + j][nb][1];
-              mma_f16(acc[p][h], f0, f1, f0, f1, u & kLowNibble, v & kLowNibble, u & kHighNibble, v & kHighNibble, q.x, q.y);
-              mma_f16(acc[p][h], u8 & kLowNibble, v8 & kLowNibble, u8 & kHighNibble, v8 & kHighNibble, q.z, q.w);
-            }
+            const uint4 q = lds128(queries + ((p * GK + i + j) * NB + nb) * 512);
+            float f0 = 0.f, f1 = 0.f;
+            if constexpr (S::kParts == 2) f0 = first[p][i + j][nb][0], f1 = first[p][i + j][nb][1];
+            mma_f16(acc[p], f0, f1, f0, f1, u & kLowNibble, v & kLowNibble, uh, vh, q.x, q.y);
+            mma_f16(acc[p], half2_less(ub, ubh), half2_less(vb, vbh), ubh, vbh, q.z, q.w);
           }
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const float k = ks[h][r >> 1][i + j], sum = S::kParts == 2 ? fmaf(acc[S::kParts - 1][h][r], 0x1p-12f, acc[0][h][r]) : acc[0][h][r];
-              s[h][nb][r] = S::kParts == 2 && i + j == 0 ? sum * k : fmaf(sum, k, s[h][nb][r]);
-            }
+          for (int r = 0; r < 4; ++r) {
+            const float k = r < 2 ? k0[i + j] : k1[i + j], sum = S::kParts == 2 ? fmaf(acc[S::kParts - 1][r], 0x1p-12f, acc[0][r]) : acc[0][r];
+            s[nb][r] = S::kParts == 2 && i + j == 0 ? sum * k : fmaf(sum, k, s[nb][r]);
+          }
         }
       }
     }
   }
 
-  // O += weights (of 16 tokens, in s) times values.  area: S::kParts == 1, [token pair][group] pairs of f16 scales;
+  // O += weights (of 16 tokens, in s) times values; bf16: rows g of a tile take whole bytes, c + 16 c', rows g + 8 the
+  // high nibble 16 c' alone, for an AND less than the low one alone; store() subtracts.  area: S::kParts == 1, [token pair][group] pairs of f16 scales;
   // else [token] four fp32 scales.
-  __device__ __forceinline__ void outputs(const float (&s)[NB][4], uint32_t vals, const float4* area) {
+  __device__ __forceinline__ void outputs(const float (&s)[NB][4], uint32_t vals, uint32_t area) {
     constexpr bool kF16 = S::kParts == 1;
-    const float4 x0 = area[kF16 ? t4 : g], x1 = area[kF16 ? t4 + 4 : g + 8];
+    const float4 x0 = lds_f4(area + 16 * (kF16 ? t4 : g)), x1 = lds_f4(area + 16 * (kF16 ? t4 + 4 : g + 8));
     const float c0[4] = {x0.x, x0.y, x0.z, x0.w}, c1[4] = {x1.x, x1.y, x1.z, x1.w};
     uint32_t b[NB][2];
     if constexpr (kF16)
@@ -344,10 +379,11 @@ struct Decode4Math {
           float(&d0)[4] = o[2 * (i + j)][nb], (&d1)[4] = o[2 * (i + j) + 1][nb];
           if constexpr (kF16) {
             const uint32_t b0 = half2_times(b[nb][0], c0[i + j]), b1 = half2_times(b[nb][1], c1[i + j]);
-            mma_f16(d0, u & kLowNibble, u & kHighNibble, v & kLowNibble, v & kHighNibble, b0, b1);
-            mma_f16(d1, u8 & kLowNibble, u8 & kHighNibble, v8 & kLowNibble, v8 & kHighNibble, b0, b1);
-            mma_f16(d0, kLowMinus8, kHighMinus8, kLowMinus8, kHighMinus8, b0, b1);
-            mma_f16(d1, kLowMinus8, kHighMinus8, kLowMinus8, kHighMinus8, b0, b1);
+            const uint32_t ub = __byte_perm(u, 0, 0x4341), vb = __byte_perm(v, 0, 0x4341);
+            mma_f16(d0, u & kByte, u & kHighNibble, v & kByte, v & kHighNibble, b0, b1);
+            mma_f16(d1, ub, ub & kHighNibble, vb, vb & kHighNibble, b0, b1);
+            mma_f16(d0, kByteMinus, kHighMinus8, kByteMinus, kHighMinus8, b0, b1);
+            mma_f16(d1, kByteMinus, kHighMinus8, kByteMinus, kHighMinus8, b0, b1);
           } else {
             const float p0 = s[nb][0] * c0[i + j], p1 = s[nb][1] * c0[i + j], p2 = s[nb][2] * c1[i + j], p3 = s[nb][3] * c1[i + j];
             uint32_t lo = half2_bits(p0, p1), hi = half2_bits(p2, p3);
@@ -369,7 +405,7 @@ struct Decode4Math {
 
   // The step's scales as the products take them, a token per lane: area [32] keys', then values'.
   template <bool FULL>
-  __device__ __forceinline__ void scales(uint32_t raw, unsigned lv, const DecodeArgs& a, float4* area) {
+  __device__ __forceinline__ void scales(uint32_t raw, unsigned lv, const DecodeArgs& a, uint32_t area) {
     const int lane = threadIdx.x & 31;
     const bool live = FULL || ((lv >> lane) & 1);
     auto load = [&](uint32_t at, int groups, int dim) {
@@ -377,14 +413,14 @@ struct Decode4Math {
       if (groups == 4) asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w0), "=r"(w1) : "r"(at) : "memory");
       else asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w0) : "r"(at) : "memory");
       if (!live) w0 = w1 = 0;
-      if (groups == 2 && dim <= 32) w0 &= 0xffffu;
-      if (groups == 4 && dim <= 96) w1 &= 0xffffu;
+      if (dim <= 32) w0 &= 0xffffu;  // behind the last group's: none
+      if (dim <= 96) w1 = dim <= 64 ? 0 : w1 & 0xffffu;
       return make_float4(__uint_as_float(w0 << 16), __uint_as_float(w0 & 0xffff0000u), __uint_as_float(w1 << 16),
                          __uint_as_float(w1 & 0xffff0000u));
     };
     float4 k = load(raw + lane * GK * 2, GK, a.dk), v = load(raw + S::kStep * GK * 2 + lane * GV * 2, GV, a.dv);
     k.x *= k_mul, k.y *= k_mul, k.z *= k_mul, k.w *= k_mul;
-    area[lane] = k;
+    sts128(area + 16 * lane, k);
     float big = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w));  // NaN only where all are
     if (!(big < __builtin_huge_valf())) big = 0.f;
     const int e = static_cast<int>(__reduce_max_sync(~0u, __float_as_uint(big)) >> 23) - 126;  // below 2^e
@@ -399,14 +435,16 @@ struct Decode4Math {
     const float mul = __uint_as_float(static_cast<unsigned>(127 - top_exp) << 23);
     v.x *= mul, v.y *= mul, v.z *= mul, v.w *= mul;
     if constexpr (S::kParts == 2) {
-      area[32 + lane] = v;
+      sts128(area + 512 + 16 * lane, v);
     } else {
       // Tokens' pairs side by side: an even lane takes groups 0 and 1 of the pair, an odd one 2 and 3.
       const uint32_t h01 = half2_bits(v.x, v.y), h23 = half2_bits(v.z, v.w);
       const bool odd = lane & 1;
       const uint32_t own = odd ? h23 : h01, other = __shfl_xor_sync(~0u, odd ? h01 : h23, 1);
       const uint32_t lo = odd ? other : own, hi = odd ? own : other;
-      reinterpret_cast<uint2*>(area + 32)[lane] = make_uint2(__byte_perm(lo, hi, 0x5410), __byte_perm(lo, hi, 0x7632));
+      asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(area + 512 + 8 * lane), "r"(__byte_perm(lo, hi, 0x5410)),
+                   "r"(__byte_perm(lo, hi, 0x7632))
+                   : "memory");
     }
     __syncwarp();
   }
@@ -414,14 +452,16 @@ struct Decode4Math {
   // 32 tokens of a stage, codes at st, scales at raw; bit x of lv: token x exists (FULL: all do); far: the first one's
   // distance from the query.
   // DIRECT: no cap and no bias.
-  template <bool FULL, bool DIRECT>
-  __device__ __forceinline__ void step(uint32_t st, uint32_t raw, unsigned lv, int far, const DecodeArgs& a, float4* area) {
+  template <bool FULL>
+  __device__ __forceinline__ void step(uint32_t st, uint32_t raw, unsigned lv, int far, const DecodeArgs& a, uint32_t area) {
     scales<FULL>(raw, lv, a, area);
     float s[2][NB][4];
-    scores(s, st, area);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) scores(s[h], st + h * 16 * S::kKeyBytes, area + 256 * h);
     // What the exponential takes: x + neg, x = log2(e) * score.
     float y[2][NB][4];
     if constexpr (!DIRECT) {
+      const DecodeScore score(a);
       const float dist = static_cast<float>(far - g);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -487,7 +527,7 @@ struct Decode4Math {
         l[nb][0] += y[h][nb][0] + y[h][nb][2];
         l[nb][1] += y[h][nb][1] + y[h][nb][3];
       }
-      outputs(y[h], st + S::kStep * S::kKeyBytes + h * 16 * S::kValBytes, area + 32 + (S::kParts == 1 ? 8 : 16) * h);
+      outputs(y[h], st + S::kStep * S::kKeyBytes + h * 16 * S::kValBytes, area + 512 + (S::kParts == 1 ? 128 : 256) * h);
     }
   }
 
@@ -508,9 +548,11 @@ struct Decode4Math {
         if (hd < heads)
 #pragma unroll
           for (int d = 0; d < 2 * GV; ++d)
-            *reinterpret_cast<float2*>(res + hd * S::DV + 16 * (d & ~1) + 4 * g + 2 * (d & 1)) =
-                make_float2(ldexpf(o[d][nb][e] * inv, top_exp + (S::kParts == 1 ? 24 : 0)),
-                            ldexpf(o[d][nb][2 + e] * inv, top_exp + (S::kParts == 1 ? 20 : 0)));
+            {
+              const float hi = o[d][nb][2 + e] * inv, lo = S::kParts == 1 ? o[d][nb][e] * inv - hi : o[d][nb][e] * inv;
+              *reinterpret_cast<float2*>(res + hd * S::DV + 16 * (d & ~1) + 4 * g + 2 * (d & 1)) =
+                  make_float2(ldexpf(lo, top_exp + (S::kParts == 1 ? 24 : 0)), ldexpf(hi, top_exp + (S::kParts == 1 ? 20 : 0)));
+            }
       }
   }
 };
@@ -518,7 +560,7 @@ struct Decode4Math {
 // TMA: pages of a multiple of 16 slots, whose codes come in boxes of 16 rows (maps: bytes of a row, slots, heads,
 // pages; swizzled as swizzle4 says); else each lane copies 16-byte pieces.  Scales, a token per lane, come by
 // cp.async in either case.
-template <class S, bool WHOLE, bool TMA>
+template <class S, bool WHOLE, bool TMA, bool DIRECT>
 __global__ void __launch_bounds__(kDecodeThreads, S::kCtasPerSm)
     decode4_stream_kernel(const DecodeArgs a, const Units4 units, const __grid_constant__ Maps4 maps) {
   using T = typename S::T;
@@ -561,14 +603,14 @@ __global__ void __launch_bounds__(kDecodeThreads, S::kCtasPerSm)
   }
   const uint32_t ring = smem_u32(smem + warp * kStages * S::kStageBytes);
   const uint32_t raw_ring = smem_u32(smem + S::kScales + warp * kStages * S::kScaleBytes);
-  float4* area = reinterpret_cast<float4*>(smem + S::kMain + warp * S::kArea);
+  const uint32_t area = smem_u32(smem + S::kMain + warp * S::kArea);
   const uint32_t k_dst = (lane / CK) * S::kKeyBytes + (((lane % CK) ^ swizzle4<S::kKeyBytes>(lane / CK)) * 16);
   const uint32_t v_dst = kStep * S::kKeyBytes + (lane / CV) * S::kValBytes + (((lane % CV) ^ swizzle4<S::kValBytes>(lane / CV)) * 16);
+  const int kg = scales4(a.dk), vg = scales4(a.dv);  // scales of a row, 2 or 4; a row of the ring has room for GK, GV
   const bool same = units.k_p == units.v_p && units.k_t == units.v_t;  // one offset serves both
   const bool same_x = units.kx_p == units.vx_p && units.kx_t == units.vx_t;
   // from a lane's token to its next one, without a division per step
   const int adv_pg = kDecodeWarps * kStep / a.cache.page_size, adv_slot = kDecodeWarps * kStep - adv_pg * a.cache.page_size;
-  const bool direct = a.softcap == 0.f && !a.slopes;
   const Watchdog wd{a.err, &abort_flag, a.timeout_ns};
   unsigned phases = 0;  // bit s: the parity that stage s's barrier is waited for with
   bool alive = true;    // no wait has run out: else the warp copies and computes nothing more
@@ -654,8 +696,8 @@ __global__ void __launch_bounds__(kDecodeThreads, S::kCtasPerSm)
           else copies(std::false_type{});
         }
         const unsigned kx = at_.page * units.kx_p + at_.slot * units.kx_t, vx = same_x ? kx : at_.page * units.vx_p + at_.slot * units.vx_t;
-        cp_async_small<2 * S::GK>(raw + lane * S::GK * 2, ok ? kxbase + static_cast<unsigned long long>(kx) * S::GK : kxbase, ok);
-        cp_async_small<2 * S::GV>(raw + kStep * S::GK * 2 + lane * S::GV * 2, ok ? vxbase + static_cast<unsigned long long>(vx) * S::GV : vxbase, ok);
+        copy_scales(raw + lane * S::GK * 2, kxbase + static_cast<unsigned long long>(kx) * kg, kxbase, kg, ok);
+        copy_scales(raw + kStep * S::GK * 2 + lane * S::GV * 2, vxbase + static_cast<unsigned long long>(vx) * vg, vxbase, vg, ok);
       }
       cp_async_commit();
       return have;
@@ -665,7 +707,7 @@ __global__ void __launch_bounds__(kDecodeThreads, S::kCtasPerSm)
 #pragma unroll
     for (int s = 0; s < kStages - 1; ++s) live[s] = issue(s, s, lookup(s));
     // The queries are read while the first tokens come.
-    Decode4Math<S> c(a, pc, reinterpret_cast<uint4*>(smem + S::kQueries));
+    Decode4Math<S, DIRECT> c(a, pc, reinterpret_cast<uint4*>(smem + S::kQueries));
     __syncthreads();
     Place place = lookup(kStages - 1);
     int stage = 0;
@@ -679,7 +721,7 @@ __global__ void __launch_bounds__(kDecodeThreads, S::kCtasPerSm)
       place = lookup(step + kStages);
       cp_async_wait<kStages - 1>();
       if constexpr (TMA) {
-        if (alive) alive = mbar_wait(bars + stage, (phases >> stage) & 1, wd);
+        if (alive) alive = mbar_wait_long(bars + stage, (phases >> stage) & 1, wd);
         phases ^= 1u << stage;
         alive = __all_sync(~0u, alive);
       }
@@ -687,9 +729,8 @@ __global__ void __launch_bounds__(kDecodeThreads, S::kCtasPerSm)
       const int far = pc.len - 1 - (base + step * (kDecodeWarps * kStep));
       const uint32_t st = ring + stage * S::kStageBytes, raw = raw_ring + stage * S::kScaleBytes;
       if (TMA && !alive) break;
-      if (lv == ~0u && direct) c.template step<true, true>(st, raw, lv, far, a, area);
-      else if (lv == ~0u) c.template step<true, false>(st, raw, lv, far, a, area);
-      else if (lv) c.template step<false, false>(st, raw, lv, far, a, area);
+      if (lv == ~0u) c.template step<true>(st, raw, lv, far, a, area);
+      else if (lv) c.template step<false>(st, raw, lv, far, a, area);
       stage = stage + 1 == kStages ? 0 : stage + 1;
     }
     if (TMA && !alive)  // its copies in flight, if any land
@@ -767,29 +808,28 @@ __global__ void __launch_bounds__(kDecodeThreads, S::kCtasPerSm)
   }
 }
 
-template <class S, bool TMA>
-cudaError_t launch_decode4_mode(const DecodeArgs& a, const Units4& u, const Maps4& maps, cudaStream_t s) {
-  if (a.split) {
-    const long long ctas = static_cast<long long>(a.B) * a.Hkv * a.chunks * a.split;
-    const size_t smem = S::kSmem + S::kAlign;
-    const cudaError_t e = smem_attr_once<decode4_stream_kernel<S, true, TMA>>(smem);
-    if (e != cudaSuccess) return e;
-    if (ctas >= (1LL << 31)) return cudaErrorInvalidConfiguration;
-    const dim3 grid(static_cast<unsigned>(ctas));
-    if (a.split == 1) return launch_pdl(decode4_stream_kernel<S, true, TMA>, grid, dim3(kDecodeThreads), smem, s, a, u, maps);
-    return launch_pdl_cluster(decode4_stream_kernel<S, true, TMA>, grid, dim3(kDecodeThreads), smem, s, a.split, a, u, maps);
-  }
-  const size_t smem = S::kSmem + S::kAlign + sizeof(unsigned) * (a.B + 1);
-  const cudaError_t e = smem_attr_once<decode4_stream_kernel<S, false, TMA>>(smem);
+template <class S, bool WHOLE, bool TMA>
+cudaError_t launch_decode4_kernel(const DecodeArgs& a, const Units4& u, const Maps4& maps, cudaStream_t s) {
+  const bool direct = a.softcap == 0.f && !a.slopes;
+  auto* kernel = direct ? decode4_stream_kernel<S, WHOLE, TMA, true> : decode4_stream_kernel<S, WHOLE, TMA, false>;
+  const size_t smem = S::kSmem + S::kAlign + (WHOLE ? 0 : sizeof(unsigned) * (a.B + 1));
+  const cudaError_t e = direct ? smem_attr_once<decode4_stream_kernel<S, WHOLE, TMA, true>>(smem)
+                               : smem_attr_once<decode4_stream_kernel<S, WHOLE, TMA, false>>(smem);
   if (e != cudaSuccess) return e;
-  // After the kernel before it, not among its CTAs: this wave fills the SMs exactly (decode_stream.cuh).
-  return launch_serial(decode4_stream_kernel<S, false, TMA>, dim3(a.ctas), dim3(kDecodeThreads), smem, s, a, u, maps);
+  // Runs go after the kernel before them, not among its CTAs: this wave fills the SMs exactly (decode_stream.cuh).
+  if (!WHOLE) return launch_serial(kernel, dim3(a.ctas), dim3(kDecodeThreads), smem, s, a, u, maps);
+  const long long ctas = static_cast<long long>(a.B) * a.Hkv * a.chunks * a.split;
+  if (ctas >= (1LL << 31)) return cudaErrorInvalidConfiguration;
+  const dim3 grid(static_cast<unsigned>(ctas));
+  if (a.split == 1) return launch_pdl(kernel, grid, dim3(kDecodeThreads), smem, s, a, u, maps);
+  return launch_pdl_cluster(kernel, grid, dim3(kDecodeThreads), smem, s, a.split, a, u, maps);
 }
 
+// maps: runs over pages whose codes TMA can copy; else null.
 template <class S>
 cudaError_t launch_decode4_shape(const DecodeArgs& a, const Units4& u, const Maps4* maps, cudaStream_t s) {
-  if (maps) return launch_decode4_mode<S, true>(a, u, *maps, s);
-  return launch_decode4_mode<S, false>(a, u, Maps4{}, s);
+  if (a.split) return launch_decode4_kernel<S, true, false>(a, u, Maps4{}, s);
+  return maps ? launch_decode4_kernel<S, false, true>(a, u, *maps, s) : launch_decode4_kernel<S, false, false>(a, u, Maps4{}, s);
 }
 
 }  // namespace cb

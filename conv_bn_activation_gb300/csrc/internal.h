@@ -448,8 +448,9 @@ cudaError_t launch_decode_fma(const DecodeArgs& a, cudaStream_t s);  // fp32, ro
 cudaError_t launch_decode(const DecodeArgs& a, bool bf16, bool vec, cudaStream_t s);
 // 4-bit caches (decode4.cuh: rows of whole 16-byte pieces; decode.cu: the others).
 // CTAs that an SM holds: by registers 3 or 2, and no more than its shared memory does.
+constexpr int decode4_dim(int dk, int dv) { return dk <= 64 && dv <= 64 ? 64 : 128; }  // the kernel's shape
 constexpr int decode4_ctas_per_sm(int dk, int dv, bool bf16, int heads, int batch) {
-  const int DK = dk <= 64 ? 64 : 128, DV = dv <= 64 ? 64 : 128, hd = heads <= 8 ? 8 : 16;
+  const int DK = decode4_dim(dk, dv), DV = DK, hd = heads <= 8 ? 8 : 16;
   const int most = !bf16 || hd == 16 ? 2 : 4, ring = 4 * 2 * 32 * (DK + DV) / 2, results = 4 * 5 * hd * DV;
   const int bytes = (ring > results ? ring : results) + 4 * 1024 + ring / 8 + (bf16 ? 1 : 2) * DK * hd * 2 + 96 + 512 + 4 * (batch + 1) + 1824, fit = 233472 / bytes;
   return fit < most ? fit : most;
@@ -464,7 +465,7 @@ struct Units4 {
 struct Maps4 {
   CUtensorMap k, v;
 };
-inline int decode4_box(int dim) { return dim <= 64 ? 32 : 64; }  // bytes of a row; 16 slots; swizzled in 32 or 64 bytes
+inline int decode4_box(int dk, int dv) { return decode4_dim(dk, dv) / 2; }  // bytes of a row; 16 slots; swizzled in as many
 // maps: pages of a multiple of 16 slots, or null.
 cudaError_t launch_decode4_bf16(const DecodeArgs& a, const Units4& u, const Maps4* maps, cudaStream_t s);
 cudaError_t launch_decode4_f32(const DecodeArgs& a, const Units4& u, const Maps4* maps, cudaStream_t s);

@@ -277,7 +277,7 @@ cb_status cb_attention_decode4(const cb_heads* q, const cb_paged_cache4* cache, 
   a.B = q->batch, a.Hq = q->heads, a.Hkv = cache->heads, a.group = q->heads / cache->heads;
   a.dk = cache->dim_k, a.dv = cache->dim_v;
   a.chunks = p.chunks, a.item_heads = p.heads, a.split = p.split;
-  a.item_cost = decode_item_cost(q->dtype == CB_DTYPE_BF16);
+  a.item_cost = decode4_item_cost(q->dtype == CB_DTYPE_BF16);
   a.record = static_cast<int*>(workspace);
   a.part = reinterpret_cast<float*>(a.record + 2 * p.ctas);
   a.ctas = p.ctas;

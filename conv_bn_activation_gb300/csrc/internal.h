@@ -455,6 +455,9 @@ constexpr int decode4_ctas_per_sm(int dk, int dv, bool bf16, int heads, int batc
   const int bytes = (ring > results ? ring : results) + 4 * 1024 + ring / 8 + (bf16 ? 1 : 2) * DK * hd * 2 + 96 + 512 + 4 * (batch + 1) + 1824, fit = 233472 / bytes;
   return fit < most ? fit : most;
 }
+// What an item's start costs a CTA, in tiles (64 sequences of 130 to 4000 tokens, 8 key heads of 128: 73.3 us with 1,
+// 63.6, 61.5 and 65.5 with 3, 5 and 8). An fp32 tile takes longer.
+constexpr int decode4_item_cost(bool bf16) { return bf16 ? 5 : 3; }
 constexpr int kDecode4Heads = 16, kDecode4HeadsF32 = 8;  // most query heads of one item
 // The streaming kernels' strides of pages and slots, of codes in 16 bytes and of scales in rows' scales (2 for
 // dims up to 64, else 4): 32 bits reach 64 GB of codes.

@@ -239,9 +239,17 @@ class MapReader:
     steps the cache has room for (at least: the last page is used up); a page holds `page` tokens.  A step
     that the cache has no room for raises ValueError.  Replays of a captured step are not seen here: past
     the room their token is not stored, and cb.get_device_error() says so; after a captured read no step is
-    refused here."""
+    refused here.
 
-    def __init__(self, params, batch, hw, tokens, page=16, device="cuda", dtype=torch.float32):
+    params may hold q_norm and k_norm (weights of an RMS norm of each query and key head) and rope (the freq
+    and axis of each pair of dims, axes and adjacent of a cb.Rotation).  Positions are (time, row, column), of
+    which a rule with fewer axes takes the last ones: a map's are (0, y, x), the i-th token's max(H, W) + i on
+    every axis; with one axis, the place in the sequence.  cache_bits 4: keys and values are cached in 4 bits,
+    which the steps see; None: in `dtype`."""
+
+    def __init__(self, params, batch, hw, tokens, page=16, device="cuda", dtype=torch.float32, cache_bits=None):
+        if cache_bits not in (None, 4):
+            raise ValueError("cache_bits: None (the dtype's) or 4")
         self.hq, self.hkv, self.dim = params["heads"], params["kv_heads"], params["dim"]
         self.batch, self.hw, (H, W) = batch, hw, hw
         kw = dict(device=device, dtype=dtype)
@@ -253,15 +261,47 @@ class MapReader:
         self.tok_ctx = torch.empty(batch, 1, 1, self.hq * self.dim, **kw)
         self.map_out, self.tok_out = torch.empty(batch, H, W, C, **kw), torch.empty(batch, 1, 1, C, **kw)
         pages = -(-(H * W + tokens) // page)
-        self.pages = [torch.zeros(batch * pages, page, self.hkv, self.dim, **kw) for _ in range(2)]
         self.room, self.filled = pages * page, 0  # tokens per sequence; filled None: replays of `read` are not seen
         self.table = torch.arange(batch * pages, dtype=torch.int32, device=device).view(batch, pages)
-        self.cache = cb.PagedCache(*self.pages, self.table)
+        if cache_bits == 4:
+            self.cache = cb.PagedCache4.empty(batch * pages, page, self.hkv, self.dim, self.dim, self.table)
+            self._append, self._decode, space = cb.cache4_append, cb.attention_decode4, cb.attention_decode4_workspace
+        else:
+            self.pages = [torch.zeros(batch * pages, page, self.hkv, self.dim, **kw) for _ in range(2)]
+            self.cache = cb.PagedCache(*self.pages, self.table)
+            self._append, self._decode, space = cb.cache_append, cb.attention_decode, cb.attention_decode_workspace
         self.start = torch.zeros(batch, dtype=torch.int32, device=device)
         self.length = torch.zeros(batch, dtype=torch.int32, device=device)
         self.score = cb.Score(self.dim ** -0.5)
         q = self._split(self.tok_qkv)[0][:, 0]
-        self.workspace = torch.empty(cb.attention_decode_workspace(q, self.cache), dtype=torch.uint8, device=device)
+        self.workspace = torch.empty(space(q, self.cache), dtype=torch.uint8, device=device)
+        self.rule = self._rule(params, device)
+        if self.rule is not None:
+            axes = self.rule.axes
+            y, x = torch.meshgrid(torch.arange(H), torch.arange(W), indexing="ij")
+            at = torch.stack([torch.zeros_like(y), y, x]) if axes > 1 else torch.arange(H * W)
+            at = at.reshape(-1, 1, H * W)[-axes:].to(torch.int32).to(device)
+            self.map_pos = at.expand(axes, batch, H * W)
+            self.tok_first = max(H, W) if axes > 1 else H * W
+            self.tok_pos = torch.full((axes, batch, 1), self.tok_first, dtype=torch.int32, device=device)
+
+    @staticmethod
+    def _rule(params, device):
+        """The cb.Rotation that params ask for, or None."""
+        rope, norms = params.get("rope"), [params.get("q_norm"), params.get("k_norm")]
+        norm = any(w is not None for w in norms)
+        if rope is None and not norm:
+            return None
+        rope = rope or {}
+
+        def on(a, dtype):
+            return None if a is None else torch.as_tensor(a, dtype=dtype).to(device).contiguous()
+
+        if not 1 <= rope.get("axes", 1) <= 3:
+            raise ValueError("rope: one to three axes")
+        return cb.Rotation(on(rope.get("freq"), torch.float32), axis=on(rope.get("axis"), torch.int32), axes=rope.get("axes", 1),
+                           adjacent=rope.get("adjacent", False), norm=norm, eps=params.get("norm_eps", 1e-6),
+                           q_weight=on(norms[0], torch.float32), k_weight=on(norms[1], torch.float32))
 
     def _split(self, qkv):
         """Queries, keys and values [B, L, heads, dim]: slices of the projection, read in place."""
@@ -278,11 +318,15 @@ class MapReader:
         self.filled = None if self.filled is None or self._capturing(stream) else self.hw[0] * self.hw[1]
         self.qkv(x, self.map_qkv, stream=stream)
         q, k, v = self._split(self.map_qkv)
+        if self.rule is not None:
+            cb.norm_rotate(q, k, self.map_pos, self.rule, stream=stream)
         cb.attention(q, k, v, self.map_ctx.view(*q.shape), self.score, stream=stream)
-        cb.cache_append(k, v, self.cache, self.start, stream=stream)
+        self._append(k, v, self.cache, self.start, stream=stream)
         self.out(self.map_ctx, self.map_out, residual=x, res_mode=cb.RES_POST_ACT, stream=stream)
         with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(x.device)):
             self.length.fill_(self.hw[0] * self.hw[1])
+            if self.rule is not None:
+                self.tok_pos.fill_(self.tok_first)
         return self.map_out
 
     def step(self, tok, stream=None):
@@ -293,10 +337,14 @@ class MapReader:
         x = tok.view(self.batch, 1, 1, -1)
         self.qkv(x, self.tok_qkv, stream=stream)
         q, k, v = self._split(self.tok_qkv)
-        cb.cache_append(k, v, self.cache, self.length, stream=stream)
+        if self.rule is not None:
+            cb.norm_rotate(q, k, self.tok_pos, self.rule, stream=stream)
+        self._append(k, v, self.cache, self.length, stream=stream)
         with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(x.device)):
             self.length.add_(1)
-        cb.attention_decode(q[:, 0], self.cache, self.length, self.tok_ctx.view(self.batch, self.hq, self.dim), self.workspace,
+            if self.rule is not None:
+                self.tok_pos.add_(1)
+        self._decode(q[:, 0], self.cache, self.length, self.tok_ctx.view(self.batch, self.hq, self.dim), self.workspace,
                             self.score.scale, stream=stream)
         self.out(self.tok_ctx, self.tok_out, residual=x, res_mode=cb.RES_POST_ACT, stream=stream)
         return self.tok_out.view(self.batch, -1)

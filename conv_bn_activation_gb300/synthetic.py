@@ -140,10 +140,18 @@ def stem_params(seed: int = SEED_BASE + 4):
     return kaiming(g, 16, 3, 3, 3), bn_params(g, 16)
 
 
-def map_reader_params(channels=64, heads=8, kv_heads=2, dim=32, seed: int = SEED_BASE + 5):
-    """An attention layer over feature maps: 1x1 conv to queries, keys and values, 1x1 conv back, each with BN."""
+def map_reader_params(channels=64, heads=8, kv_heads=2, dim=32, seed: int = SEED_BASE + 5, axes=0, norm=False, adjacent=False):
+    """An attention layer over feature maps: 1x1 conv to queries, keys and values, 1x1 conv back, each with BN.
+    axes > 0: rotary positions, the pairs of dims dealt to the axes in turn; norm: norms of the query and key heads."""
     g = rng(seed)
     wide = (heads + 2 * kv_heads) * dim
-    return {"heads": heads, "kv_heads": kv_heads, "dim": dim,
-            "qkv_w": kaiming(g, wide, channels, 1, 1), "qkv_bn": bn_params(g, wide),
-            "out_w": kaiming(g, channels, heads * dim, 1, 1), "out_bn": bn_params(g, channels)}
+    p = {"heads": heads, "kv_heads": kv_heads, "dim": dim,
+         "qkv_w": kaiming(g, wide, channels, 1, 1), "qkv_bn": bn_params(g, wide),
+         "out_w": kaiming(g, channels, heads * dim, 1, 1), "out_bn": bn_params(g, channels)}
+    if axes:
+        pairs = np.arange(dim // 2)
+        p["rope"] = {"freq": (10000.0 ** (-pairs / max(dim // 2, 1))).astype(np.float32), "axis": (pairs % axes).astype(np.int32),
+                     "axes": axes, "adjacent": adjacent}
+    if norm:
+        p["q_norm"], p["k_norm"] = (uniform01(g, (dim,)) + 0.5 for _ in range(2))
+    return p

@@ -2,9 +2,9 @@
 // cb_cache4_read).  Both are bound by HBM: 16 or 32 bits an element on one side
 // and 4.5 on the other.
 //
-// Rows of whole groups and 16-byte pieces (dims that are multiples of 32): a lane
+// Rows of whole words (dims that are multiples of 8) and 16-byte pieces: a lane
 // takes eight dims of a row, a word of codes, so four lanes share a group and its
-// scale.  A token's words of all heads, keys then values, lie side by side over
+// scale (the last one's may have nothing).  A token's words of all heads, keys then values, lie side by side over
 // the lanes; which head and dims a lane's words are, and where they lie in a
 // token's row and a page's slot, is worked out once per launch, as in
 // cache_append.cu.  The reads of all a lane's words are in flight before it
@@ -114,10 +114,12 @@ struct Eight {
 // Where a lane's words lie: elements from the token's row of keys or values,
 // bytes from the slot's row of their codes, elements from that of their scales.
 struct Word {
-  bool is_v, writes;  // writes: the lane that stores or reads the group's scale's pair
+  bool is_v, real, writes;  // real: there are such dims; writes: the lane that stores the group's scale
   int from, to, scale, group;
 };
-__device__ __forceinline__ Word word_of(int e, int keys, int kw, int vw, long long ks_h, long long vs_h, const PagedArgs& c) {
+__device__ __forceinline__ int words4(int dim) { return (dim + kGroup4 - 1) / kGroup4 * 4; }
+__device__ __forceinline__ Word word_of(int e, int keys, int dk, int dv, long long ks_h, long long vs_h, const PagedArgs& c) {
+  const int kw = words4(dk), vw = words4(dv);
   Word w;
   w.is_v = e >= keys;
   const int x = w.is_v ? e - keys : e, n = w.is_v ? vw : kw, h = x / n, i = x - h * n;
@@ -125,6 +127,7 @@ __device__ __forceinline__ Word word_of(int e, int keys, int kw, int vw, long lo
   w.to = static_cast<int>(h * (w.is_v ? c.vs_h : c.ks_h)) + 4 * i;
   w.group = i / 4;
   w.scale = static_cast<int>(h * (w.is_v ? c.vx_h : c.kx_h)) + w.group;
+  w.real = 8 * i < (w.is_v ? dv : dk);
   w.writes = i % 4 == 0;
   return w;
 }
@@ -148,11 +151,11 @@ struct Walk {
 template <typename T, int U>
 __global__ void __launch_bounds__(32 * kWarps) cache4_append_kernel(const AppendArgs a, long long tokens, int chunks, int warps) {
   const int lane = threadIdx.x & 31, warp = blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int kw = a.dk / 8, vw = a.dv / 8, keys = a.H * kw, words = a.H * (kw + vw), first = warp % chunks * (32 * U) + lane;
+  const int keys = a.H * words4(a.dk), words = keys + a.H * words4(a.dv), first = warp % chunks * (32 * U) + lane;
   Word w[U];
 #pragma unroll
-  for (int u = 0; u < U; ++u) w[u] = word_of(min(first + 32 * u, words - 1), keys, kw, vw, a.ks_h, a.vs_h, a.cache);
-  const int spare_k = scales4(a.dk) * kGroup4 - a.dk, spare_v = scales4(a.dv) * kGroup4 - a.dv;  // a scale of zero behind the last
+  for (int u = 0; u < U; ++u) w[u] = word_of(min(first + 32 * u, words - 1), keys, a.dk, a.dv, a.ks_h, a.vs_h, a.cache);
+  const int last_k = words4(a.dk) / 4 - 1, last_v = words4(a.dv) / 4 - 1;  // groups; behind an even one a scale of zero
   pdl_wait();
   pdl_launch_dependents();
   if (warp >= warps) return;
@@ -163,8 +166,10 @@ __global__ void __launch_bounds__(32 * kWarps) cache4_append_kernel(const Append
     const T* vs = static_cast<const T*>(a.v) + b * a.vs_b + t * a.vs_l;
     Eight<T> x[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (first + 32 * u < words) x[u].load((w[u].is_v ? vs : ks) + w[u].from);
+    for (int u = 0; u < U; ++u) {
+      x[u] = {};
+      if (first + 32 * u < words && w[u].real) x[u].load((w[u].is_v ? vs : ks) + w[u].from);
+    }
     int slot = 0;
     const long long page = cache_page(a.cache, a.err, b, static_cast<long long>(a.pos[b]) + t, &slot);
     if (page < 0) continue;
@@ -182,12 +187,11 @@ __global__ void __launch_bounds__(32 * kWarps) cache4_append_kernel(const Append
       const unsigned bits = scale4_bits(top);
       const uint32_t code = Coder4(bits).word<sizeof(T) == 2>(f);
       if (first + 32 * u < words) {
-        *reinterpret_cast<uint32_t*>((w[u].is_v ? vd : kd) + w[u].to) = code;
+        if (w[u].real) *reinterpret_cast<uint32_t*>((w[u].is_v ? vd : kd) + w[u].to) = code;
         if (w[u].writes) {
           uint16_t* s = (w[u].is_v ? vx : kx) + w[u].scale;
           s[0] = static_cast<uint16_t>(bits);
-          const int last = (w[u].is_v ? a.dv : a.dk) / kGroup4 - 1;
-          if ((w[u].is_v ? spare_v : spare_k) && w[u].group == last) s[1] = 0;
+          if (w[u].group % 2 == 0 && w[u].group == (w[u].is_v ? last_v : last_k)) s[1] = 0;
         }
       }
     }
@@ -197,10 +201,10 @@ __global__ void __launch_bounds__(32 * kWarps) cache4_append_kernel(const Append
 template <typename T, int U>
 __global__ void __launch_bounds__(32 * kWarps) cache4_read_kernel(const Read4Args a, long long tokens, int chunks, int warps) {
   const int lane = threadIdx.x & 31, warp = blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int kw = a.dk / 8, vw = a.dv / 8, keys = a.H * kw, words = a.H * (kw + vw), first = warp % chunks * (32 * U) + lane;
+  const int keys = a.H * words4(a.dk), words = keys + a.H * words4(a.dv), first = warp % chunks * (32 * U) + lane;
   Word w[U];
 #pragma unroll
-  for (int u = 0; u < U; ++u) w[u] = word_of(min(first + 32 * u, words - 1), keys, kw, vw, a.ks_h, a.vs_h, a.cache);
+  for (int u = 0; u < U; ++u) w[u] = word_of(min(first + 32 * u, words - 1), keys, a.dk, a.dv, a.ks_h, a.vs_h, a.cache);
   pdl_wait();
   pdl_launch_dependents();
   if (warp >= warps) return;
@@ -218,7 +222,7 @@ __global__ void __launch_bounds__(32 * kWarps) cache4_read_kernel(const Read4Arg
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       code[u] = 0x88888888u, scale[u] = 0;  // a token that has no page reads as zeros
-      if (page >= 0 && first + 32 * u < words) {
+      if (page >= 0 && first + 32 * u < words && w[u].real) {
         code[u] = *reinterpret_cast<const uint32_t*>((w[u].is_v ? vs : ks) + w[u].to);
         scale[u] = ((w[u].is_v ? vx : kx) + w[u].scale)[0];
       }
@@ -227,7 +231,7 @@ __global__ void __launch_bounds__(32 * kWarps) cache4_read_kernel(const Read4Arg
     T* vd = static_cast<T*>(a.v) + b * a.vs_b + t * a.vs_l;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (first + 32 * u >= words) continue;
+      if (first + 32 * u >= words || !w[u].real) continue;
       uint4* y = reinterpret_cast<uint4*>((w[u].is_v ? vd : kd) + w[u].from);
       if constexpr (sizeof(T) == 4) {
         const float s = bf16_value(scale[u]);
@@ -258,7 +262,7 @@ __global__ void __launch_bounds__(32 * kWarps) cache4_read_kernel(const Read4Arg
 template <typename T, int U, class Args, class Kernel>
 cudaError_t launch_words(Kernel kernel, const Args& a, int sms, cudaStream_t s) {
   const long long tokens = static_cast<long long>(a.B) * a.T;
-  const int words = a.H * (a.dk + a.dv) / 8, chunks = (words + 32 * U - 1) / (32 * U);
+  const int words = a.H * 4 * ((a.dk + kGroup4 - 1) / kGroup4 + (a.dv + kGroup4 - 1) / kGroup4), chunks = (words + 32 * U - 1) / (32 * U);
   const long long units = tokens * chunks, most = kWordCtas * kWarps * sms;
   const long long warps = units < most ? units : (most < chunks ? chunks : most / chunks * chunks);
   return launch_pdl(kernel, dim3(static_cast<unsigned>((warps + kWarps - 1) / kWarps)), dim3(32 * kWarps), 0, s, a, tokens, chunks,

@@ -47,35 +47,40 @@ bool aligned(const cb_paged_cache4* c) {
   return reinterpret_cast<uintptr_t>(c->k_scale) % 2 == 0 && reinterpret_cast<uintptr_t>(c->v_scale) % 2 == 0;
 }
 
-// Rows of whole 16-byte pieces of codes, and a row's scales one word: what the streaming kernels copy, at offsets of
-// 32 bits in those units.
-bool pieces(const cb_paged_cache4* c, const void* codes, const void* scales, int dim, std::initializer_list<long long> code_strides,
+// Rows of whole pieces of `piece` bytes of codes, and a row's scales one word: what the streaming kernels copy, at
+// offsets of 32 bits in those units.
+bool pieces(const cb_paged_cache4* c, int piece, const void* codes, const void* scales, int dim, std::initializer_list<long long> code_strides,
             std::initializer_list<long long> scale_strides) {
   const int unit = dim <= 64 ? 2 : 4;
   auto reach = [&](const std::initializer_list<long long>& s, long long per) {  // of pages and slots
     const double last = static_cast<double>(s.begin()[0]) * c->num_pages + static_cast<double>(s.begin()[1]) * c->page_size;
     return last / static_cast<double>(per) < 4294967296.0;
   };
-  if (!reach(code_strides, 16) || !reach(scale_strides, unit)) return false;
-  if (dim % 32 != 0 || reinterpret_cast<uintptr_t>(codes) % 16 != 0 || reinterpret_cast<uintptr_t>(scales) % (2 * unit) != 0) return false;
+  if (!reach(code_strides, piece) || !reach(scale_strides, unit)) return false;
+  if (dim % (2 * piece) != 0 || reinterpret_cast<uintptr_t>(codes) % piece != 0 || reinterpret_cast<uintptr_t>(scales) % (2 * unit) != 0)
+    return false;
   for (const long long s : code_strides)
-    if (s % 16 != 0) return false;
+    if (s % piece != 0) return false;
   for (const long long s : scale_strides)
     if (s % unit != 0) return false;
   return true;
 }
-bool streams(const cb_paged_cache4* c) {
-  return pieces(c, c->k, c->k_scale, c->dim_k, {c->k_stride_page, c->k_stride_slot, c->k_stride_head},
-                {c->ks_stride_page, c->ks_stride_slot, c->ks_stride_head}) &&
-         pieces(c, c->v, c->v_scale, c->dim_v, {c->v_stride_page, c->v_stride_slot, c->v_stride_head},
-                {c->vs_stride_page, c->vs_stride_slot, c->vs_stride_head});
+// The largest pieces that rows of keys and values are made of: 16 bytes, 4 or none.
+int pieces(const cb_paged_cache4* c) {
+  for (const int piece : {16, 4})
+    if (pieces(c, piece, c->k, c->k_scale, c->dim_k, {c->k_stride_page, c->k_stride_slot, c->k_stride_head},
+               {c->ks_stride_page, c->ks_stride_slot, c->ks_stride_head}) &&
+        pieces(c, piece, c->v, c->v_scale, c->dim_v, {c->v_stride_page, c->v_stride_slot, c->v_stride_head},
+               {c->vs_stride_page, c->vs_stride_slot, c->vs_stride_head}))
+      return piece;
+  return 0;
 }
 
-// Tokens and pages that the kernels for whole groups take: rows of 16-byte pieces, dims of 32, heads within 32 bits of
-// their token's or slot's first.
+// Tokens and pages that the kernels for whole words take: rows of 16-byte pieces, dims that are multiples of 8, heads
+// within 32 bits of their token's or slot's first.
 bool words(const cb_heads* t, const void* codes, int dim, long long page, long long slot, long long head, long long scale_head) {
   auto near = [&](long long stride) { return stride * (t->heads - 1) + dim < (1LL << 31); };
-  return dim % 32 == 0 && pieces16(t) && reinterpret_cast<uintptr_t>(codes) % 4 == 0 && page % 4 == 0 && slot % 4 == 0 &&
+  return dim % 8 == 0 && pieces16(t) && reinterpret_cast<uintptr_t>(codes) % 4 == 0 && page % 4 == 0 && slot % 4 == 0 &&
          head % 4 == 0 && near(t->stride_h) && near(head) && near(scale_head);
 }
 bool words(const cb_heads* k, const cb_heads* v, const cb_paged_cache4* c) {
@@ -133,23 +138,23 @@ cb_status check_decode(const cb_heads* q, const cb_paged_cache4* cache) {
 struct Decode4Plan {
   int sms = 0, ctas = 0, chunks = 0, heads = 0, split = 0;
   int* err = nullptr;
-  bool vec = false;
+  int piece = 0;
 };
 cb_status plan_decode(const cb_heads* q, const cb_paged_cache4* cache, Decode4Plan* p) {
   const cb_status st = host_device(&p->sms, &p->err);
   if (st != CB_OK) return st;
-  p->vec = streams(cache);
+  p->piece = pieces(cache);
   const bool bf16 = q->dtype == CB_DTYPE_BF16;
-  const int group = q->heads / cache->heads, most = !p->vec ? kDecodeSimtHeads : bf16 ? kDecode4Heads : kDecode4HeadsF32;
+  const int group = q->heads / cache->heads, most = !p->piece ? kDecodeSimtHeads : bf16 ? kDecode4Heads : kDecode4HeadsF32;
   p->chunks = (group + most - 1) / most;
   p->heads = (group + p->chunks - 1) / p->chunks;
-  p->ctas = p->sms * (p->vec ? decode4_ctas_per_sm(cache->dim_k, cache->dim_v, bf16, p->heads, q->batch) : 4);
+  p->ctas = p->sms * (p->piece ? decode4_ctas_per_sm(cache->dim_k, cache->dim_v, bf16, p->heads, q->batch) : 4);
   // Whole items on clusters where a CTA then walks at most 16 tiles, as for other caches (cb_attention_decode).
   const long long items = static_cast<long long>(q->batch) * cache->heads * p->chunks;
   const long long tiles = (static_cast<long long>(cache->max_pages) * cache->page_size + 63) / 64;
   p->split = 1;
   while (p->split < 8 && items * p->split * 2 <= p->ctas && p->split < tiles) p->split *= 2;
-  if (!p->vec || tiles > 16LL * p->split) p->split = 0;
+  if (!p->piece || tiles > 16LL * p->split) p->split = 0;
   return CB_OK;
 }
 
@@ -184,7 +189,6 @@ cb_status cb_norm_rotate(const cb_heads* q, const cb_heads* k, const cb_head_rul
   int sms = 0;
   const cb_status st = host_device(&sms, &a.err);
   if (st != CB_OK) return st;
-  bool vec = true;
   for (int i = 0; i < views; ++i) {
     RotateView& v = a.v[i];
     v.x = in[i]->data, v.y = out[i]->data;
@@ -192,13 +196,12 @@ cb_status cb_norm_rotate(const cb_heads* q, const cb_heads* k, const cb_head_rul
     v.ys_b = out[i]->stride_b, v.ys_l = out[i]->stride_l, v.ys_h = out[i]->stride_h;
     v.weight = i == 0 ? rule->q_weight : rule->k_weight;
     v.heads = in[i]->heads;
-    vec = vec && pieces16(in[i]) && pieces16(out[i]);
   }
   a.B = q->batch, a.L = q->len, a.dim = q->dim, a.rotary = rule->rotary;
   a.adjacent = rule->adjacent != 0, a.norm = rule->norm != 0, a.axes = rule->axes, a.eps = rule->eps;
   a.freq = rule->freq, a.axis = rule->axis, a.pos = rule->pos;
   a.ps_a = rule->pos_stride_axis, a.ps_b = rule->pos_stride_b;
-  return done(launch_norm_rotate(a, q->dtype == CB_DTYPE_BF16, vec, sms, static_cast<cudaStream_t>(stream)));
+  return done(launch_norm_rotate(a, q->dtype == CB_DTYPE_BF16, sms, static_cast<cudaStream_t>(stream)));
 }
 
 cb_status cb_cache4_append(const cb_heads* k_new, const cb_heads* v_new, const int* pos, const int* count,
@@ -284,10 +287,10 @@ cb_status cb_attention_decode4(const cb_heads* q, const cb_paged_cache4* cache, 
   a.err = p.err;
   a.timeout_ns = host_timeout_ns();
   Maps4 maps;
-  const bool mapped = p.vec && !p.split && cache->num_pages > 0 && cache->page_size % 16 == 0 &&
+  const bool mapped = p.piece == 16 && !p.split && cache->num_pages > 0 && cache->page_size % 16 == 0 &&
                       code_map(&maps.k, cache->k, cache, cache->dim_k, cache->k_stride_page, cache->k_stride_slot, cache->k_stride_head) &&
                       code_map(&maps.v, cache->v, cache, cache->dim_v, cache->v_stride_page, cache->v_stride_slot, cache->v_stride_head);
-  return done(launch_decode4(a, q->dtype == CB_DTYPE_BF16, p.vec, mapped ? &maps : nullptr, static_cast<cudaStream_t>(stream)));
+  return done(launch_decode4(a, q->dtype == CB_DTYPE_BF16, p.piece, mapped ? &maps : nullptr, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -292,14 +292,14 @@ cudaError_t launch_decode(const DecodeArgs& a, bool bf16, bool vec, cudaStream_t
   return bf16 ? launch_join<__nv_bfloat16>(a, s) : launch_join<float>(a, s);
 }
 
-cudaError_t launch_decode4(const DecodeArgs& a, bool bf16, bool vec, const Maps4* maps, cudaStream_t s) {
+cudaError_t launch_decode4(const DecodeArgs& a, bool bf16, int piece, const Maps4* maps, cudaStream_t s) {
   cudaError_t e;
-  if (vec) {
+  if (piece) {
     const PagedArgs& c = a.cache;
     const int gk = scales4(a.dk), gv = scales4(a.dv);
-    const Units4 u{static_cast<unsigned>(c.ks_p / 16), static_cast<unsigned>(c.ks_t / 16), static_cast<unsigned>(c.vs_p / 16),
-                   static_cast<unsigned>(c.vs_t / 16), static_cast<unsigned>(c.kx_p / gk), static_cast<unsigned>(c.kx_t / gk),
-                   static_cast<unsigned>(c.vx_p / gv), static_cast<unsigned>(c.vx_t / gv)};
+    auto in = [](long long stride, int unit) { return static_cast<unsigned>(stride / unit); };
+    const Units4 u{static_cast<unsigned>(piece), in(c.ks_p, piece), in(c.ks_t, piece), in(c.vs_p, piece), in(c.vs_t, piece),
+                   in(c.kx_p, gk), in(c.kx_t, gk), in(c.vx_p, gv), in(c.vx_t, gv)};
     e = bf16 ? launch_decode4_bf16(a, u, maps, s) : launch_decode4_f32(a, u, maps, s);
   } else
     e = bf16 ? launch_simt<__nv_bfloat16, Elements4>(a, s) : launch_simt<float, Elements4>(a, s);

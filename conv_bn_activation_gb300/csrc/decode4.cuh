@@ -1,6 +1,6 @@
 // The streaming kernel of attention over a 4-bit cache (cb_attention_decode4),
-// for rows of whole 16-byte pieces (dims that are multiples of 32).  Tokens are
-// dealt as in decode_common.cuh; a CTA's four warps walk a piece together, each
+// for rows of whole words (dims that are multiples of 8; of 32: 16-byte pieces).
+// Tokens are dealt as in decode_common.cuh; a CTA's four warps walk a piece together, each
 // its own 32 tokens of every 128 through its own ring of cp.async copies, as in
 // decode_stream.cuh.
 //
@@ -218,10 +218,10 @@ struct Decode4Math {
 #pragma unroll
       for (int i = 0; i < GK; ++i) {
         const T* at = q + 32 * i + 8 * t4;
-        if (hd >= heads || 32 * i >= a.dk) {
+        if (hd >= heads || 32 * i + 8 * t4 >= a.dk) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) x[i][e] = 0.f;
-        } else if (reinterpret_cast<uintptr_t>(q) % 16 == 0) {
+        } else if (reinterpret_cast<uintptr_t>(at) % 16 == 0) {
           constexpr int kPer = 16 / static_cast<int>(sizeof(T));
 #pragma unroll
           for (int e = 0; e < 8; e += kPer) unpack16<T>(*reinterpret_cast<const uint4*>(at + e), *reinterpret_cast<float(*)[kPer]>(&x[i][e]));
@@ -573,7 +573,7 @@ __global__ void __launch_bounds__(kDecodeThreads, S::kCtasPerSm)
   uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & (S::kAlign - 1));
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int kq = a.dk / kGroup4, vq = a.dv / kGroup4;  // real pieces per row; what the others hold meets queries of 0
+  const int kq = a.dk / kGroup4, vq = a.dv / kGroup4;  // 16-byte pieces per row; what the ring's others hold meets queries of 0
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kBars) + warp * kStages;
   if constexpr (TMA) {
     if (tid == 0) abort_flag = 0;
@@ -692,8 +692,30 @@ __global__ void __launch_bounds__(kDecodeThreads, S::kCtasPerSm)
               }
             }
           };
-          if (have == ~0u) copies(std::true_type{});
-          else copies(std::false_type{});
+          if (units.bytes == 4) {  // words, where rows are no 16-byte pieces
+            constexpr int WK = S::kKeyBytes / 4, WV = S::kValBytes / 4;
+            const char* kw = kbase - (lane % CK) * 16;
+            const char* vw = vbase - (lane % CV) * 16;
+#pragma unroll 4
+            for (int i = 0; i < WK; ++i) {
+              const int r = (i * 32 + lane) / WK, w = lane % WK;
+              const unsigned long long off = 4ull * __shfl_sync(~0u, k_off, r);
+              const bool some = (have >> r) & 1;
+              if (w < a.dk / 8) cp_async_small<4>(st + r * S::kKeyBytes + (((w >> 2) ^ swizzle4<S::kKeyBytes>(r)) * 16) + (w & 3) * 4, some ? kw + off + w * 4 : kw, some);
+            }
+#pragma unroll 4
+            for (int i = 0; i < WV; ++i) {
+              const int r = (i * 32 + lane) / WV, w = lane % WV;
+              const unsigned long long off = 4ull * __shfl_sync(~0u, v_off, r);
+              const bool some = (have >> r) & 1;
+              if (w < a.dv / 8)
+                cp_async_small<4>(st + kStep * S::kKeyBytes + r * S::kValBytes + (((w >> 2) ^ swizzle4<S::kValBytes>(r)) * 16) + (w & 3) * 4, some ? vw + off + w * 4 : vw, some);
+            }
+          } else if (have == ~0u) {
+            copies(std::true_type{});
+          } else {
+            copies(std::false_type{});
+          }
         }
         const unsigned kx = at_.page * units.kx_p + at_.slot * units.kx_t, vx = same_x ? kx : at_.page * units.vx_p + at_.slot * units.vx_t;
         copy_scales(raw + lane * S::GK * 2, kxbase + static_cast<unsigned long long>(kx) * kg, kxbase, kg, ok);

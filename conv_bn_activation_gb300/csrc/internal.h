@@ -385,8 +385,7 @@ struct Read4Args {
 cudaError_t launch_cache4_append(const AppendArgs& a, bool bf16, bool vec, int sms, cudaStream_t s);
 cudaError_t launch_cache4_read(const Read4Args& a, bool bf16, bool vec, int sms, cudaStream_t s);
 
-// cb_norm_rotate (norm_rotate.cu): queries, then keys (no heads: none).  vec:
-// every view's rows are 16-byte pieces, and pairs lie in whole pieces.
+// cb_norm_rotate (norm_rotate.cu): queries, then keys (no heads: none).
 struct RotateView {
   const void* x;
   void* y;
@@ -405,7 +404,7 @@ struct RotateArgs {
   long long ps_a, ps_b;
   int* err;
 };
-cudaError_t launch_norm_rotate(const RotateArgs& a, bool bf16, bool vec, int sms, cudaStream_t s);
+cudaError_t launch_norm_rotate(const RotateArgs& a, bool bf16, int sms, cudaStream_t s);
 
 struct DecodeArgs {
   const void* q;
@@ -446,7 +445,7 @@ size_t decode_workspace_bytes(int ctas, int heads, int dv);
 cudaError_t launch_decode_mma(const DecodeArgs& a, cudaStream_t s);  // bf16, rows of whole 16-byte pieces
 cudaError_t launch_decode_fma(const DecodeArgs& a, cudaStream_t s);  // fp32, rows of whole 16-byte pieces
 cudaError_t launch_decode(const DecodeArgs& a, bool bf16, bool vec, cudaStream_t s);
-// 4-bit caches (decode4.cuh: rows of whole 16-byte pieces; decode.cu: the others).
+// 4-bit caches (decode4.cuh: rows of whole 4-byte words; decode.cu: the others).
 // CTAs that an SM holds: by registers 3 or 2, and no more than its shared memory does.
 constexpr int decode4_dim(int dk, int dv) { return dk <= 64 && dv <= 64 ? 64 : 128; }  // the kernel's shape
 constexpr int decode4_ctas_per_sm(int dk, int dv, bool bf16, int heads, int batch) {
@@ -459,10 +458,10 @@ constexpr int decode4_ctas_per_sm(int dk, int dv, bool bf16, int heads, int batc
 // 63.6, 61.5 and 65.5 with 3, 5 and 8). An fp32 tile takes longer.
 constexpr int decode4_item_cost(bool bf16) { return bf16 ? 5 : 3; }
 constexpr int kDecode4Heads = 16, kDecode4HeadsF32 = 8;  // most query heads of one item
-// The streaming kernels' strides of pages and slots, of codes in 16 bytes and of scales in rows' scales (2 for
-// dims up to 64, else 4): 32 bits reach 64 GB of codes.
+// The streaming kernels' strides of pages and slots, of codes in `bytes` (16, or 4: rows that are not whole 16-byte
+// pieces) and of scales in rows' scales (2 for dims up to 64, else 4): 32 bits reach 64 or 16 GB of codes.
 struct Units4 {
-  unsigned k_p, k_t, v_p, v_t, kx_p, kx_t, vx_p, vx_t;
+  unsigned bytes, k_p, k_t, v_p, v_t, kx_p, kx_t, vx_p, vx_t;
 };
 // Codes of keys and values as 4-D tensors (bytes of a row, slots, heads, pages), boxes of decode4_box.
 struct Maps4 {
@@ -472,7 +471,8 @@ inline int decode4_box(int dk, int dv) { return decode4_dim(dk, dv) / 2; }  // b
 // maps: pages of a multiple of 16 slots, or null.
 cudaError_t launch_decode4_bf16(const DecodeArgs& a, const Units4& u, const Maps4* maps, cudaStream_t s);
 cudaError_t launch_decode4_f32(const DecodeArgs& a, const Units4& u, const Maps4* maps, cudaStream_t s);
-cudaError_t launch_decode4(const DecodeArgs& a, bool bf16, bool vec, const Maps4* maps, cudaStream_t s);
+// piece: bytes that rows are whole pieces of (16 or 4, dims multiples of 32 or 8), or 0.
+cudaError_t launch_decode4(const DecodeArgs& a, bool bf16, int piece, const Maps4* maps, cudaStream_t s);
 // cb_attention with few queries per key head through the streaming kernel:
 // columns are (query, head) pairs, at most kDecodeMmaHeads (bf16) or
 // kDecodeSimtHeads (fp32) of them per item.  Fills a from rw.

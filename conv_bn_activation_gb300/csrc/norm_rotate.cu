@@ -12,6 +12,8 @@
 // 10^5 is off by 2^-8 radians.  What is left, in [-1/2, 1/2) turn, goes to sincospif.
 #include <cuda_bf16.h>
 
+#include <initializer_list>
+
 #include "attention_common.cuh"
 #include "launch_util.h"
 #include "ptx.cuh"
@@ -114,33 +116,35 @@ __device__ __forceinline__ void copy_ahead(void* dst, const void* src) {
   else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(dst)), "l"(src), "n"(BYTES) : "memory");
 }
 
-// A 16-byte piece of a row as pairs of fp32, and back.
-template <typename T>
-__device__ __forceinline__ void unpack(uint4 w, f2* x) {
-  float f[16 / sizeof(T)];
-  unpack16<T>(w, f);
+// E elements of a row, and as pairs of fp32.
+template <typename T, int E>
+struct alignas(E * sizeof(T)) Piece {
+  static constexpr int kBytes = E * static_cast<int>(sizeof(T)), kWords = kBytes / 4;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void get(f2* x) const {
 #pragma unroll
-  for (int i = 0; i < 8 / static_cast<int>(sizeof(T)); ++i) x[i] = pack2(f[2 * i], f[2 * i + 1]);
-}
-template <typename T>
-__device__ __forceinline__ uint4 pack(const f2* x) {
-  uint32_t u[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float lo, hi;
-    if constexpr (sizeof(T) == 4) {
-      unpack2(x[i / 2], lo, hi);
-      u[i] = __float_as_uint(i & 1 ? hi : lo);
-    } else {
-      unpack2(x[i], lo, hi);
-      const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-      u[i] = *reinterpret_cast<const uint32_t*>(&h);
+    for (int i = 0; i < E / 2; ++i) {
+      if constexpr (sizeof(T) == 4) x[i] = pack2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+      else x[i] = pack2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
     }
   }
-  return make_uint4(u[0], u[1], u[2], u[3]);
-}
+  __device__ __forceinline__ void set(const f2* x) {
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) {
+      float lo, hi;
+      unpack2(x[i], lo, hi);
+      if constexpr (sizeof(T) == 4) {
+        w[2 * i] = __float_as_uint(lo), w[2 * i + 1] = __float_as_uint(hi);
+      } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+    }
+  }
+};
 
-// Rows of whole 16-byte pieces, pairs in whole pieces.  Bound by HBM.  `width`
+// Rows of whole pieces of E elements, 16 bytes where dims and strides allow them,
+// else 8 or 4, and pairs in whole pieces.  Bound by HBM.  `width`
 // lanes (a power of two) share a head, each with two pieces of it: the halves of
 // the same pairs, or, adjacent pairs, any two; what does not turn is split in
 // halves too and turns by 0.  A warp works on queries or on keys: 32 / width heads
@@ -152,10 +156,11 @@ __device__ __forceinline__ uint4 pack(const f2* x) {
 struct Split {  // of the grid's warps: the first `warps` of a view's kind, `parts` to a token
   unsigned warps[2], parts[2];
 };
-template <typename T, bool ADJ>
+template <typename T, int E, bool ADJ>
 __global__ void __launch_bounds__(32 * kWarps, kPiecesCtas) rotate_pieces_kernel(const RotateArgs a, const int width, const Split split) {
-  constexpr int E = 16 / sizeof(T), H = E / 2;  // elements of a piece; pairs of fp32
-  __shared__ __align__(16) uint4 ring_s[kWarps][kDepth][2][32];
+  constexpr int H = E / 2;  // pairs of fp32 in a piece
+  using Part = Piece<T, E>;
+  __shared__ __align__(16) Part ring_s[kWarps][kDepth][2][32];
   __shared__ int pos_s[kWarps][kDepth][2][32];
   __shared__ __align__(16) float weight_s[2][2 * kMaxPairs];
   __shared__ __align__(16) float cos_s[kWarps][kMaxPairs], sin_s[kWarps][kMaxPairs];
@@ -201,8 +206,8 @@ __global__ void __launch_bounds__(32 * kWarps, kPiecesCtas) rotate_pieces_kernel
       }
       if (mine && r.head < heads) {
         const T* x = x_at + static_cast<unsigned long long>(r.head) * xs_h;
-        copy_ahead<16>(&ring_s[warp][at][0][lane], x);
-        copy_ahead<16>(&ring_s[warp][at][1][lane], x + (p1 - p0));
+        copy_ahead<Part::kBytes>(&ring_s[warp][at][0][lane], x);
+        copy_ahead<Part::kBytes>(&ring_s[warp][at][1][lane], x + (p1 - p0));
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -240,7 +245,7 @@ __global__ void __launch_bounds__(32 * kWarps, kPiecesCtas) rotate_pieces_kernel
       }
     }
     f2 x[E];  // piece 0, piece 1
-    unpack<T>(ring_s[warp][at][0][lane], x), unpack<T>(ring_s[warp][at][1][lane], x + H);
+    ring_s[warp][at][0][lane].get(x), ring_s[warp][at][1][lane].get(x + H);
     f2 inv = pack2(1.f, 1.f);
     if (a.norm) {
       f2 sums = mul2(x[0], x[0]);
@@ -269,12 +274,15 @@ __global__ void __launch_bounds__(32 * kWarps, kPiecesCtas) rotate_pieces_kernel
     }
     if (mine && r.head < heads) {
       T* y = y_at + static_cast<unsigned long long>(r.head) * ys_h;
-      *reinterpret_cast<uint4*>(y) = pack<T>(x);
-      *reinterpret_cast<uint4*>(y + (p1 - p0)) = pack<T>(x + H);
+      Part out;
+      out.set(x);
+      *reinterpret_cast<Part*>(y) = out;
+      out.set(x + H);
+      *reinterpret_cast<Part*>(y + (p1 - p0)) = out;
     }
   };
   if (!mine)  // what is never copied adds nothing to a norm
-    for (int at = 0; at < kDepth; ++at) ring_s[warp][at][0][lane] = ring_s[warp][at][1][lane] = make_uint4(0, 0, 0, 0);
+    for (int at = 0; at < kDepth; ++at) ring_s[warp][at][0][lane] = ring_s[warp][at][1][lane] = Part{};
   Place ahead{unit < split.warps[is_k] ? unit / parts : tokens, first}, now = ahead;
 #pragma unroll
   for (int at = 0; at < kDepth - 1; ++at) fetch(ahead, at), next(ahead);
@@ -296,9 +304,8 @@ __global__ void __launch_bounds__(32 * kWarps, kPiecesCtas) rotate_pieces_kernel
   asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-template <typename T>
+template <typename T, int E>
 cudaError_t launch_pieces(const RotateArgs& a, int sms, cudaStream_t s) {
-  constexpr int E = 16 / sizeof(T);
   int width = 1;
   while (width * 2 * E < a.dim) width *= 2;
   const int slots = 32 / width;
@@ -319,19 +326,35 @@ cudaError_t launch_pieces(const RotateArgs& a, int sms, cudaStream_t s) {
     split.warps[v] = static_cast<unsigned>((warps + parts - 1) / parts * parts);
   }
   const unsigned ctas = (split.warps[0] + split.warps[1] + kWarps - 1) / kWarps;
-  auto* kernel = a.adjacent ? rotate_pieces_kernel<T, true> : rotate_pieces_kernel<T, false>;
+  auto* kernel = a.adjacent ? rotate_pieces_kernel<T, E, true> : rotate_pieces_kernel<T, E, false>;
   return launch_pdl(kernel, dim3(ctas), dim3(32 * kWarps), 0, s, a, width, split);
 }
 
-// Whether a head's offset in its token fits the kernel's 32 bits.
-bool near_heads(const RotateView& v) { return v.xs_h < (1LL << 31) && v.ys_h < (1LL << 31); }
+// Whether rows are pieces of E elements, pairs lie in whole ones, and a head's offset in its token fits 32 bits.
+template <typename T, int E>
+bool pieces(const RotateArgs& a) {
+  if (a.dim % (2 * E) != 0 || (!a.adjacent && a.rotary % (2 * E) != 0)) return false;
+  for (const RotateView& v : a.v) {
+    if (!v.heads) continue;
+    if ((reinterpret_cast<uintptr_t>(v.x) | reinterpret_cast<uintptr_t>(v.y)) % (E * sizeof(T)) != 0) return false;
+    for (const long long stride : {v.xs_b, v.xs_l, v.xs_h, v.ys_b, v.ys_l, v.ys_h})
+      if (stride % E != 0) return false;
+    if (v.xs_h >= (1LL << 31) || v.ys_h >= (1LL << 31)) return false;
+  }
+  return true;
+}
 
 }  // namespace
 
-cudaError_t launch_norm_rotate(const RotateArgs& a, bool bf16, bool vec, int sms, cudaStream_t s) {
-  const int two = bf16 ? 16 : 8;  // elements of two pieces
-  if (vec && a.dim % two == 0 && (a.adjacent || a.rotary % two == 0) && near_heads(a.v[0]) && near_heads(a.v[1]))
-    return bf16 ? launch_pieces<__nv_bfloat16>(a, sms, s) : launch_pieces<float>(a, sms, s);
+cudaError_t launch_norm_rotate(const RotateArgs& a, bool bf16, int sms, cudaStream_t s) {
+  if (bf16) {
+    if (pieces<__nv_bfloat16, 8>(a)) return launch_pieces<__nv_bfloat16, 8>(a, sms, s);
+    if (pieces<__nv_bfloat16, 4>(a)) return launch_pieces<__nv_bfloat16, 4>(a, sms, s);
+    if (pieces<__nv_bfloat16, 2>(a)) return launch_pieces<__nv_bfloat16, 2>(a, sms, s);
+  } else {
+    if (pieces<float, 4>(a)) return launch_pieces<float, 4>(a, sms, s);
+    if (pieces<float, 2>(a)) return launch_pieces<float, 2>(a, sms, s);
+  }
   const long long rows = static_cast<long long>(a.B) * a.L * (a.v[0].heads + a.v[1].heads);
   const long long ctas = (rows + kWarps - 1) / kWarps, most = 16LL * sms;
   const dim3 grid(static_cast<unsigned>(ctas < most ? ctas : most)), block(32 * kWarps);

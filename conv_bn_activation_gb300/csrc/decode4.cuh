@@ -16,10 +16,11 @@
 //    tile, in the same step, so that no sum grows with the offset.
 //  - a group's scale: keys, one FMA per score and group on the group's sum;
 //    values, on the weights, a set of weights per group.
-//  - f16's range.  Queries are scaled by a power of two per head (2^15 above),
-//    weights by 2^7 and the values' scales by the power of two above the largest
-//    so far, which O follows when it grows, as it does a maximum.  Weights below
-//    2^-31 of the largest are lost.
+//  - f16's range.  Queries are scaled by a power of two per head (2^15 above).
+//    A token's largest scale goes into its weight in fp32, what its groups' are
+//    beside it into f16; the running maximum is that of weight times scale, so
+//    that a large value of no weight takes nothing from the others.  Products
+//    below 2^-31 of the largest are lost.
 // The MMAs add 16 products and the sum so far with all that lies 25 bits below
 // the largest exponent cut off, toward zero, and a subnormal's exponent counts as
 // 2^-14: a step's sums keep 15 bits below their largest term, besides the 11 of a
@@ -155,7 +156,7 @@ __device__ __forceinline__ uint32_t high_codes(uint32_t w) {
 }
 constexpr uint64_t kDrainNs = 20000000;
 constexpr int kWeightBits = 7;     // weights go up to 2^(kDecodeGrowth + kWeightBits) = 2^15
-constexpr int kMinTopExp = -119;  // 2^-top_exp is an fp32 number
+constexpr float kLeastScale = 0x1p-60f;  // of a token, beside its group's first: below it counts as this
 
 template <int DK_, int DV_, int NB_, typename T_>
 struct Decode4Shape {
@@ -168,9 +169,10 @@ struct Decode4Shape {
   static constexpr int kRing = kDecodeWarps * kStages * kStageBytes;
   static constexpr int kResults = 4 * (kDecodeWarps + 1) * kHeads * DV;  // the warps' and the CTA's, when a piece ends
   static constexpr int kMain = kRing > kResults ? kRing : kResults;
-  // Behind the ring of codes: a step's scales as the products take them, per warp (keys' fp32, values' fp32 or f16);
+  // Behind the ring of codes: a step's scales as the products take them, per warp (keys' fp32, values' fp32 or f16,
+  // tokens' largest);
   // the ring of scales; queries; barriers.
-  static constexpr int kArea = kStep * 2 * 16, kScales = kMain + kDecodeWarps * kArea;
+  static constexpr int kArea = kStep * (2 * 16 + 4), kScales = kMain + kDecodeWarps * kArea;
   static constexpr int kQueries = kScales + kDecodeWarps * kStages * kScaleBytes, kBars = kQueries + kParts * GK * NB * 512;
   static constexpr int kSmem = kBars + kDecodeWarps * kStages * 8, kAlign = 512;  // of the copies' swizzle
   static constexpr int kCtasPerSm = decode4_ctas_per_sm(DK, DV, sizeof(T) == 2, kHeads, 0);
@@ -186,7 +188,7 @@ template <class S, bool DIRECT>
 struct Decode4Math {
   using T = typename S::T;
   static constexpr int GK = S::GK, GV = S::GV, NB = S::NB;
-  int g, t4, heads, top_exp;
+  int g, t4, heads;
   uint32_t k_src, v_src;  // this lane's ldmatrix rows
   // Queries as the MMAs' B operand, for each part and group: head g, dims 8 t4 + (0, 4) and (1, 5) / 16, then (2, 6) and
   // (3, 7) / 16.  In shared memory, one copy for the CTA: in registers they would cost it a neighbour.
@@ -195,17 +197,23 @@ struct Decode4Math {
   // makes a score's share of them. fp32: of every group and this thread's heads 8 nb + 2 t4 and the one after.
   float offset[NB][2], first[S::kParts == 2 ? 2 : 1][S::kParts == 2 ? GK : 1][NB][2];
   float k_mul, head_mul[NB][2];
-  // neg = kWeightBits - maximum (+infinity before the first token): weights are 2^(x + neg).
+  // The values' scales are taken times v_mul, the power of two that makes a group's first ones about 1 (0: none yet;
+  // unset: of some group).  neg = kWeightBits - maximum of x + log2 of a token's largest scale (+infinity before the
+  // first token): weights are 2^(x + neg).
+  float v_mul[GV];
+  bool unset;
   float slope[NB][2], neg[NB][2], l[NB][2], o[2 * GV][NB][4];
 
   __device__ __forceinline__ Decode4Math(const DecodeArgs& a, const Piece& pc, uint4* q_area) {
     queries = smem_u32(q_area + (threadIdx.x & 31));
     const DecodeScore score(a);
     const int lane = threadIdx.x & 31;
-    g = lane >> 2, t4 = lane & 3, heads = pc.heads, top_exp = kMinTopExp;
+    g = lane >> 2, t4 = lane & 3, heads = pc.heads, unset = true;
     const int row = (lane & 7) + 8 * ((lane >> 3) & 1);
     k_src = row * S::kKeyBytes + (((lane >> 4) ^ swizzle4<S::kKeyBytes>(row)) * 16);
     v_src = row * S::kValBytes + (((lane >> 4) ^ swizzle4<S::kValBytes>(row)) * 16);
+#pragma unroll
+    for (int i = 0; i < GV; ++i) v_mul[i] = 0.f;
     int exponent[NB], top = -1000;
     float sums[S::kParts][GK][NB];
     constexpr int kBits = S::kParts == 2 ? 11 : 15;  // queries go up to 2^kBits
@@ -421,23 +429,33 @@ struct Decode4Math {
     float4 k = load(raw + lane * GK * 2, GK, a.dk), v = load(raw + S::kStep * GK * 2 + lane * GV * 2, GV, a.dv);
     k.x *= k_mul, k.y *= k_mul, k.z *= k_mul, k.w *= k_mul;
     sts128(area + 16 * lane, k);
-    float big = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w));  // NaN only where all are
-    if (!(big < __builtin_huge_valf())) big = 0.f;
-    const int e = static_cast<int>(__reduce_max_sync(~0u, __float_as_uint(big)) >> 23) - 126;  // below 2^e
-    if (e > top_exp) {
-      const float f2 = exp2_approx(static_cast<float>(top_exp - e));
-      top_exp = e;
-      float all[NB][2];
+    float vs[4] = {v.x, v.y, v.z, v.w};
+    if (unset) {
+      unset = false;
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb) all[nb][0] = all[nb][1] = f2;
-      rescale(all);
+      for (int i = 0; i < GV; ++i) {
+        if (v_mul[i] != 0.f || i * kGroup4 >= a.dv) continue;
+        const unsigned top = __reduce_max_sync(~0u, vs[i] < __builtin_huge_valf() ? __float_as_uint(vs[i]) : 0);
+        if (top) v_mul[i] = pow2(min(126 - static_cast<int>(top >> 23), 120));  // below 1 then
+        else unset = true;
+      }
     }
-    const float mul = __uint_as_float(static_cast<unsigned>(127 - top_exp) << 23);
-    v.x *= mul, v.y *= mul, v.z *= mul, v.w *= mul;
+    float most = kLeastScale;
+#pragma unroll
+    for (int i = 0; i < GV; ++i) {
+      vs[i] *= v_mul[i];
+      most = fmaxf(most, vs[i]);  // not NaN
+    }
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(area + 1024 + 4 * lane), "f"(most) : "memory");
+    v = make_float4(vs[0], vs[1], vs[2], vs[3]);
     if constexpr (S::kParts == 2) {
       sts128(area + 512 + 16 * lane, v);
     } else {
-      // Tokens' pairs side by side: an even lane takes groups 0 and 1 of the pair, an odd one 2 and 3.
+      // Beside the token's largest, which goes into the weights.  Tokens' pairs side by side: an even lane takes groups 0
+      // and 1 of the pair, an odd one 2 and 3.
+      float less;
+      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(less) : "f"(most));
+      v.x *= less, v.y *= less, v.z *= less, v.w *= less;
       const uint32_t h01 = half2_bits(v.x, v.y), h23 = half2_bits(v.z, v.w);
       const bool odd = lane & 1;
       const uint32_t own = odd ? h23 : h01, other = __shfl_xor_sync(~0u, odd ? h01 : h23, 1);
@@ -459,7 +477,7 @@ struct Decode4Math {
 #pragma unroll
     for (int h = 0; h < 2; ++h) scores(s[h], st + h * 16 * S::kKeyBytes, area + 256 * h);
     // What the exponential takes: x + neg, x = log2(e) * score.
-    float y[2][NB][4];
+    float y[2][NB][4], lsum[NB][2];
     if constexpr (!DIRECT) {
       const DecodeScore score(a);
       const float dist = static_cast<float>(far - g);
@@ -487,14 +505,29 @@ struct Decode4Math {
             if (!FULL && !((lv >> (g + 8 * (r >> 1) + 16 * h)) & 1)) y[h][nb][r] = kNegInf;
           }
     };
-    exponents(neg);
-    bool grow = false;
+    float most[2][2];  // the tokens' largest scales
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
+      for (int e = 0; e < 2; ++e) most[h][e] = lds_f(area + 1024 + 4 * (16 * h + 8 * e + g));
+    bool grow = false;
+    auto weights = [&](const float (&add)[NB][2]) {  // y: weights times the largest scales; lsum: of the weights
+      exponents(add);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) grow |= !(y[h][nb][r] <= kDecodeGrowth + kWeightBits);
+      for (int nb = 0; nb < NB; ++nb) {
+        lsum[nb][0] = lsum[nb][1] = 0.f;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const float p = exp2_approx(y[h][nb][r]), w = p * most[h][r >> 1];
+            lsum[nb][r & 1] += p;
+            grow |= !(w <= 0x1p15f);
+            y[h][nb][r] = S::kParts == 1 ? w : p;
+          }
+      }
+    };
+    weights(neg);
     if (__any_sync(~0u, grow)) {
       float zero[NB][2], f[NB][2], now[NB][2];
 #pragma unroll
@@ -504,7 +537,11 @@ struct Decode4Math {
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float x = fmaxf(fmaxf(y[0][nb][e], y[0][nb][2 + e]), fmaxf(y[1][nb][e], y[1][nb][2 + e]));
+          float x = kNegInf;
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) x = fmaxf(x, y[h][nb][2 * i + e] + __log2f(most[h][i]));
           x = fmaxf(x, __shfl_xor_sync(~0u, x, 4));
           x = fmaxf(x, __shfl_xor_sync(~0u, x, 8));
           x = fmaxf(x, __shfl_xor_sync(~0u, x, 16));
@@ -516,19 +553,13 @@ struct Decode4Math {
           l[nb][e] *= f[nb][e];
         }
       rescale(f);
-      exponents(now);
+      weights(now);
     }
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int nb = 0; nb < NB; ++nb) l[nb][0] += lsum[nb][0], l[nb][1] += lsum[nb][1];
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-#pragma unroll
-        for (int r = 0; r < 4; ++r) y[h][nb][r] = exp2_approx(y[h][nb][r]);
-        l[nb][0] += y[h][nb][0] + y[h][nb][2];
-        l[nb][1] += y[h][nb][1] + y[h][nb][3];
-      }
+    for (int h = 0; h < 2; ++h)
       outputs(y[h], st + S::kStep * S::kKeyBytes + h * 16 * S::kValBytes, area + 512 + (S::kParts == 1 ? 128 : 256) * h);
-    }
   }
 
   // This warp's results: res[heads][DV] divided by their sum of weights (so they are no larger than the values are),
@@ -547,12 +578,12 @@ struct Decode4Math {
         const float inv = y == 0.f ? 0.f : 1.f / y;
         if (hd < heads)
 #pragma unroll
-          for (int d = 0; d < 2 * GV; ++d)
-            {
-              const float hi = o[d][nb][2 + e] * inv, lo = S::kParts == 1 ? o[d][nb][e] * inv - hi : o[d][nb][e] * inv;
-              *reinterpret_cast<float2*>(res + hd * S::DV + 16 * (d & ~1) + 4 * g + 2 * (d & 1)) =
-                  make_float2(ldexpf(lo, top_exp + (S::kParts == 1 ? 24 : 0)), ldexpf(hi, top_exp + (S::kParts == 1 ? 20 : 0)));
-            }
+          for (int d = 0; d < 2 * GV; ++d) {
+            const int up = v_mul[d / 2] == 0.f ? 0 : 127 - static_cast<int>(__float_as_uint(v_mul[d / 2]) >> 23);
+            const float hi = o[d][nb][2 + e] * inv, lo = S::kParts == 1 ? o[d][nb][e] * inv - hi : o[d][nb][e] * inv;
+            *reinterpret_cast<float2*>(res + hd * S::DV + 16 * (d & ~1) + 4 * g + 2 * (d & 1)) =
+                make_float2(ldexpf(lo, up + (S::kParts == 1 ? 24 : 0)), ldexpf(hi, up + (S::kParts == 1 ? 20 : 0)));
+          }
       }
   }
 };

@@ -429,3 +429,46 @@ def test_rotated_cached_and_attended(gpu, dtype):
     sync_check()
     assert torch.equal(kc.cpu(), torch.cat(keys, 1).to(dtype)) and torch.equal(vc.cpu(), torch.cat(vals, 1).to(dtype))
     ref.check(out, ref.attention(q, kc, vc, 0.125), vc, dtype)
+
+
+@DTYPES
+@pytest.mark.parametrize("wide", [0, 3000], ids=["whole", "runs"])
+@pytest.mark.parametrize("at", [0, 5, 150], ids=lambda x: f"token{x}")
+def test_a_large_value_of_no_weight(gpu, at, wide, dtype):
+    """One token's values are 2^40 times the others', and its weight e^-100 of theirs; the second half of the dims is
+    2^-24 of the first.  Each half is as exact as without the token."""
+    n, D = 300, 64
+    x, y = (ref.randn(2, n, 1, D, seed=i, dtype=F32, device="cuda") for i in range(2))
+    y[..., 32:] *= 2.0 ** -24
+    x[0, at, 0, 0], y[0, at] = -100.0, y[0, at] * 2.0 ** 40
+    x, y = x.to(BF16), y.to(BF16)
+    table = torch.full((2, 19 + wide), -1, dtype=torch.int32)
+    table[:, :19] = torch.arange(38).view(2, 19)
+    cache = cb.PagedCache4(*pages4(38, 16, 1, D, D), table.cuda())
+    cb.cache4_append(x, y, cache, ints([0, 0]))
+    q = torch.zeros(2, 4, D, dtype=dtype, device="cuda")
+    q[..., 0] = torch.tensor([8.0, 7.0, 8.5, 9.0], dtype=dtype, device="cuda")
+    got = run(q, cache, ints([n, n]), scale=0.125)
+    sync_check()
+    k, v = (ref4.values(*ref4.store(t), D).flatten(0, 1)[:, None] for t in (x, y))
+    want = ref.decode(q, k, v, torch.arange(2 * n).view(2, n), [n, n], 0.125)
+    v[at] = 0
+    for half in (slice(0, 32), slice(32, 64)):
+        ref.check(got[..., half], want[..., half], v[..., half], dtype)
+
+
+@DTYPES
+def test_values_that_begin_with_zeros(gpu, dtype):
+    """Tokens, and groups, of zeros before the first others."""
+    n, D = 200, 64
+    x, y = (ref.randn(1, n, 1, D, seed=i, dtype=BF16, device="cuda") for i in range(2))
+    y[0, :70] = 0
+    y[0, :, 0, 32:] = 0
+    y[0, 199, 0, 40] = 3.0
+    cache = cb.PagedCache4(*pages4(13, 16, 1, D, D), torch.arange(13, dtype=torch.int32, device="cuda").view(1, 13))
+    cb.cache4_append(x, y, cache, ints([0]))
+    q = ref.randn(1, 8, D, seed=9, dtype=dtype, device="cuda")
+    got = run(q, cache, ints([n]), scale=0.125)
+    sync_check()
+    k, v = (ref4.values(*ref4.store(t), D).flatten(0, 1)[:, None] for t in (x, y))
+    ref.check(got, ref.decode(q, k, v, torch.arange(n).view(1, n), [n], 0.125), v, dtype)

@@ -578,11 +578,15 @@ struct Decode4Math {
         const float inv = y == 0.f ? 0.f : 1.f / y;
         if (hd < heads)
 #pragma unroll
-          for (int d = 0; d < 2 * GV; ++d) {
-            const int up = v_mul[d / 2] == 0.f ? 0 : 127 - static_cast<int>(__float_as_uint(v_mul[d / 2]) >> 23);
-            const float hi = o[d][nb][2 + e] * inv, lo = S::kParts == 1 ? o[d][nb][e] * inv - hi : o[d][nb][e] * inv;
-            *reinterpret_cast<float2*>(res + hd * S::DV + 16 * (d & ~1) + 4 * g + 2 * (d & 1)) =
-                make_float2(ldexpf(lo, up + (S::kParts == 1 ? 24 : 0)), ldexpf(hi, up + (S::kParts == 1 ? 20 : 0)));
+          for (int i = 0; i < GV; ++i) {
+            const int up = v_mul[i] == 0.f ? 0 : 127 - static_cast<int>(__float_as_uint(v_mul[i]) >> 23);
+            // in two steps, as the power may be no number
+            const float lo1 = pow2(up / 2) * inv, lo2 = pow2(up - up / 2 + (S::kParts == 1 ? 24 : 0)), hi2 = S::kParts == 1 ? lo2 * 0.0625f : lo2;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const float hi = o[2 * i + j][nb][2 + e], lo = S::kParts == 1 ? o[2 * i + j][nb][e] - hi : o[2 * i + j][nb][e];
+              *reinterpret_cast<float2*>(res + hd * S::DV + 32 * i + 4 * g + 2 * j) = make_float2(lo * lo1 * lo2, hi * lo1 * hi2);
+            }
           }
       }
   }

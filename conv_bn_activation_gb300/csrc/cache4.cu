@@ -114,12 +114,12 @@ struct Eight {
 // Where a lane's words lie: elements from the token's row of keys or values,
 // bytes from the slot's row of their codes, elements from that of their scales.
 struct Word {
-  bool is_v, real, writes;  // real: there are such dims; writes: the lane that stores the group's scale
+  bool is_v, real, writes;  // real: there is such a word, with such dims; writes: the lane that stores the group's scale
   int from, to, scale, group;
 };
 __device__ __forceinline__ int words4(int dim) { return (dim + kGroup4 - 1) / kGroup4 * 4; }
-__device__ __forceinline__ Word word_of(int e, int keys, int dk, int dv, long long ks_h, long long vs_h, const PagedArgs& c) {
-  const int kw = words4(dk), vw = words4(dv);
+__device__ __forceinline__ Word word_of(int at, int words, int dk, int dv, int heads, long long ks_h, long long vs_h, const PagedArgs& c) {
+  const int kw = words4(dk), vw = words4(dv), keys = heads * kw, e = min(at, words - 1);
   Word w;
   w.is_v = e >= keys;
   const int x = w.is_v ? e - keys : e, n = w.is_v ? vw : kw, h = x / n, i = x - h * n;
@@ -127,8 +127,8 @@ __device__ __forceinline__ Word word_of(int e, int keys, int dk, int dv, long lo
   w.to = static_cast<int>(h * (w.is_v ? c.vs_h : c.ks_h)) + 4 * i;
   w.group = i / 4;
   w.scale = static_cast<int>(h * (w.is_v ? c.vx_h : c.kx_h)) + w.group;
-  w.real = 8 * i < (w.is_v ? dv : dk);
-  w.writes = i % 4 == 0;
+  w.real = at < words && 8 * i < (w.is_v ? dv : dk);
+  w.writes = at < words && i % 4 == 0;
   return w;
 }
 
@@ -151,10 +151,10 @@ struct Walk {
 template <typename T, int U>
 __global__ void __launch_bounds__(32 * kWarps) cache4_append_kernel(const AppendArgs a, long long tokens, int chunks, int warps) {
   const int lane = threadIdx.x & 31, warp = blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int keys = a.H * words4(a.dk), words = keys + a.H * words4(a.dv), first = warp % chunks * (32 * U) + lane;
+  const int words = a.H * (words4(a.dk) + words4(a.dv)), first = warp % chunks * (32 * U) + lane;
   Word w[U];
 #pragma unroll
-  for (int u = 0; u < U; ++u) w[u] = word_of(min(first + 32 * u, words - 1), keys, a.dk, a.dv, a.ks_h, a.vs_h, a.cache);
+  for (int u = 0; u < U; ++u) w[u] = word_of(first + 32 * u, words, a.dk, a.dv, a.H, a.ks_h, a.vs_h, a.cache);
   const int last_k = words4(a.dk) / 4 - 1, last_v = words4(a.dv) / 4 - 1;  // groups; behind an even one a scale of zero
   pdl_wait();
   pdl_launch_dependents();
@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(32 * kWarps) cache4_append_kernel(const Append
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       x[u] = {};
-      if (first + 32 * u < words && w[u].real) x[u].load((w[u].is_v ? vs : ks) + w[u].from);
+      if (w[u].real) x[u].load((w[u].is_v ? vs : ks) + w[u].from);
     }
     int slot = 0;
     const long long page = cache_page(a.cache, a.err, b, static_cast<long long>(a.pos[b]) + t, &slot);
@@ -186,13 +186,11 @@ __global__ void __launch_bounds__(32 * kWarps) cache4_append_kernel(const Append
       top = max(top, __shfl_xor_sync(~0u, top, 2));
       const unsigned bits = scale4_bits(top);
       const uint32_t code = Coder4(bits).word<sizeof(T) == 2>(f);
-      if (first + 32 * u < words) {
-        if (w[u].real) *reinterpret_cast<uint32_t*>((w[u].is_v ? vd : kd) + w[u].to) = code;
-        if (w[u].writes) {
-          uint16_t* s = (w[u].is_v ? vx : kx) + w[u].scale;
-          s[0] = static_cast<uint16_t>(bits);
-          if (w[u].group % 2 == 0 && w[u].group == (w[u].is_v ? last_v : last_k)) s[1] = 0;
-        }
+      if (w[u].real) *reinterpret_cast<uint32_t*>((w[u].is_v ? vd : kd) + w[u].to) = code;
+      if (w[u].writes) {
+        uint16_t* s = (w[u].is_v ? vx : kx) + w[u].scale;
+        s[0] = static_cast<uint16_t>(bits);
+        if (w[u].group % 2 == 0 && w[u].group == (w[u].is_v ? last_v : last_k)) s[1] = 0;
       }
     }
   }
@@ -201,10 +199,10 @@ __global__ void __launch_bounds__(32 * kWarps) cache4_append_kernel(const Append
 template <typename T, int U>
 __global__ void __launch_bounds__(32 * kWarps) cache4_read_kernel(const Read4Args a, long long tokens, int chunks, int warps) {
   const int lane = threadIdx.x & 31, warp = blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int keys = a.H * words4(a.dk), words = keys + a.H * words4(a.dv), first = warp % chunks * (32 * U) + lane;
+  const int words = a.H * (words4(a.dk) + words4(a.dv)), first = warp % chunks * (32 * U) + lane;
   Word w[U];
 #pragma unroll
-  for (int u = 0; u < U; ++u) w[u] = word_of(min(first + 32 * u, words - 1), keys, a.dk, a.dv, a.ks_h, a.vs_h, a.cache);
+  for (int u = 0; u < U; ++u) w[u] = word_of(first + 32 * u, words, a.dk, a.dv, a.H, a.ks_h, a.vs_h, a.cache);
   pdl_wait();
   pdl_launch_dependents();
   if (warp >= warps) return;
@@ -222,7 +220,7 @@ __global__ void __launch_bounds__(32 * kWarps) cache4_read_kernel(const Read4Arg
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       code[u] = 0x88888888u, scale[u] = 0;  // a token that has no page reads as zeros
-      if (page >= 0 && first + 32 * u < words && w[u].real) {
+      if (page >= 0 && w[u].real) {
         code[u] = *reinterpret_cast<const uint32_t*>((w[u].is_v ? vs : ks) + w[u].to);
         scale[u] = ((w[u].is_v ? vx : kx) + w[u].scale)[0];
       }
@@ -231,7 +229,7 @@ __global__ void __launch_bounds__(32 * kWarps) cache4_read_kernel(const Read4Arg
     T* vd = static_cast<T*>(a.v) + b * a.vs_b + t * a.vs_l;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (first + 32 * u >= words || !w[u].real) continue;
+      if (!w[u].real) continue;
       uint4* y = reinterpret_cast<uint4*>((w[u].is_v ? vd : kd) + w[u].from);
       if constexpr (sizeof(T) == 4) {
         const float s = bf16_value(scale[u]);

@@ -60,18 +60,21 @@ struct Coder4 {
   __device__ __forceinline__ uint32_t word(const float (&x)[8]) const {
     constexpr float kBase = 12582920.f;  // 1.5 * 2^23 + 8
     const float more = inv * (1.f + 0x1p-19f), less = inv * (1.f - 0x1p-19f);
-    uint32_t q[8];
     bool near = up != 1.f && s != 0.f;
+    uint32_t away = 0, in = 0;  // the eight nibbles, above each of them the number's other bits, which the last line takes off
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t away = __float_as_uint(fmaf(x[i], more, kBase)), in = __float_as_uint(fmaf(x[i], less, kBase));
-      if (BF16) q[i] = away & 1 ? in : away;
-      else q[i] = away, near |= away != in;
+    for (int i = 7; i >= 0; --i) {
+      const uint32_t qa = __float_as_uint(fmaf(x[i], more, kBase)), qi = __float_as_uint(fmaf(x[i], less, kBase));
+      away = away * 16u + qa, in = in * 16u + qi;
     }
-    uint32_t w = 0;
-#pragma unroll
-    for (int i = 7; i >= 0; --i) w = w * 16u + q[i];
-    w -= 0x4b400000u * 0x11111111u;
+    away -= 0x4b400000u * 0x11111111u, in -= 0x4b400000u * 0x11111111u;
+    uint32_t w = away;
+    if (BF16) {
+      const uint32_t odd = (away & 0x11111111u) * 15u;
+      w = (in & odd) | (away & ~odd);
+    } else {
+      near |= away != in;
+    }
     if (near) {
       w = 0;
 #pragma unroll
@@ -83,14 +86,16 @@ struct Coder4 {
 
 // Where token j of sequence b lies: its page, or -1 (and the error recorded).
 __device__ __forceinline__ int cache_page(const PagedArgs& c, int* err, int b, long long j, int* slot) {
-  const long long pg = j < 0 ? -1 : j / c.page_size;
+  // 32 bits hold every place of a table (a division of 64 costs a hundred instructions)
+  const unsigned at = j < 0 || j > 0x7fffffff ? 0x7fffffffu : static_cast<unsigned>(j);
+  const unsigned pg = at / static_cast<unsigned>(c.page_size);
   int page = -1;
-  if (pg >= 0 && pg < c.max_pages) page = c.table[b * c.table_stride + pg];
+  if (pg < static_cast<unsigned>(c.max_pages)) page = c.table[b * c.table_stride + pg];
   if (page < 0 || page >= c.num_pages) {
     atomicCAS(err, 0, 1);  // CB_ERR_INVALID_ARG
     return -1;
   }
-  *slot = static_cast<int>(j - pg * c.page_size);
+  *slot = static_cast<int>(at - pg * static_cast<unsigned>(c.page_size));
   return page;
 }
 

@@ -52,8 +52,9 @@ bool aligned(const cb_paged_cache4* c) {
 bool pieces(const cb_paged_cache4* c, int piece, const void* codes, const void* scales, int dim, std::initializer_list<long long> code_strides,
             std::initializer_list<long long> scale_strides) {
   const int unit = dim <= 64 ? 2 : 4;
-  auto reach = [&](const std::initializer_list<long long>& s, long long per) {  // of pages and slots
-    const double last = static_cast<double>(s.begin()[0]) * c->num_pages + static_cast<double>(s.begin()[1]) * c->page_size;
+  auto reach = [&](const std::initializer_list<long long>& s, long long per) {  // of pages, slots and heads
+    const double last = static_cast<double>(s.begin()[0]) * c->num_pages + static_cast<double>(s.begin()[1]) * c->page_size +
+                        static_cast<double>(s.begin()[2]) * c->heads;
     return last / static_cast<double>(per) < 4294967296.0;
   };
   if (!reach(code_strides, piece) || !reach(scale_strides, unit)) return false;

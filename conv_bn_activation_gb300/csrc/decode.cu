@@ -299,7 +299,7 @@ cudaError_t launch_decode4(const DecodeArgs& a, bool bf16, int piece, const Maps
     const int gk = scales4(a.dk), gv = scales4(a.dv);
     auto in = [](long long stride, int unit) { return static_cast<unsigned>(stride / unit); };
     const Units4 u{static_cast<unsigned>(piece), in(c.ks_p, piece), in(c.ks_t, piece), in(c.vs_p, piece), in(c.vs_t, piece),
-                   in(c.kx_p, gk), in(c.kx_t, gk), in(c.vx_p, gv), in(c.vx_t, gv)};
+                   in(c.kx_p, gk), in(c.kx_t, gk), in(c.kx_h, gk), in(c.vx_p, gv), in(c.vx_t, gv), in(c.vx_h, gv)};
     e = bf16 ? launch_decode4_bf16(a, u, maps, s) : launch_decode4_f32(a, u, maps, s);
   } else
     e = bf16 ? launch_simt<__nv_bfloat16, Elements4>(a, s) : launch_simt<float, Elements4>(a, s);

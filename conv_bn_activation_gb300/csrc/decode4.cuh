@@ -170,9 +170,9 @@ struct Decode4Shape {
   static constexpr int kResults = 4 * (kDecodeWarps + 1) * kHeads * DV;  // the warps' and the CTA's, when a piece ends
   static constexpr int kMain = kRing > kResults ? kRing : kResults;
   // Behind the ring of codes: a step's scales as the products take them, per warp (keys' fp32, values' fp32 or f16,
-  // tokens' largest);
+  // tokens' largest, the values' multipliers);
   // the ring of scales; queries; barriers.
-  static constexpr int kArea = kStep * (2 * 16 + 4), kScales = kMain + kDecodeWarps * kArea;
+  static constexpr int kArea = kStep * (2 * 16 + 4) + 16, kScales = kMain + kDecodeWarps * kArea;
   static constexpr int kQueries = kScales + kDecodeWarps * kStages * kScaleBytes, kBars = kQueries + kParts * GK * NB * 512;
   static constexpr int kSmem = kBars + kDecodeWarps * kStages * 8, kAlign = 512;  // of the copies' swizzle
   static constexpr int kCtasPerSm = decode4_ctas_per_sm(DK, DV, sizeof(T) == 2, kHeads, 0);
@@ -200,11 +200,11 @@ struct Decode4Math {
   // The values' scales are taken times v_mul, the power of two that makes a group's first ones about 1 (0: none yet;
   // unset: of some group).  neg = kWeightBits - maximum of x + log2 of a token's largest scale (+infinity before the
   // first token): weights are 2^(x + neg).
-  float v_mul[GV];
+  // In shared memory, behind the scales' area.
   bool unset;
   float slope[NB][2], neg[NB][2], l[NB][2], o[2 * GV][NB][4];
 
-  __device__ __forceinline__ Decode4Math(const DecodeArgs& a, const Piece& pc, uint4* q_area) {
+  __device__ __forceinline__ Decode4Math(const DecodeArgs& a, const Piece& pc, uint4* q_area, uint32_t area) {
     queries = smem_u32(q_area + (threadIdx.x & 31));
     const DecodeScore score(a);
     const int lane = threadIdx.x & 31;
@@ -212,8 +212,8 @@ struct Decode4Math {
     const int row = (lane & 7) + 8 * ((lane >> 3) & 1);
     k_src = row * S::kKeyBytes + (((lane >> 4) ^ swizzle4<S::kKeyBytes>(row)) * 16);
     v_src = row * S::kValBytes + (((lane >> 4) ^ swizzle4<S::kValBytes>(row)) * 16);
-#pragma unroll
-    for (int i = 0; i < GV; ++i) v_mul[i] = 0.f;
+    if (lane == 0) sts128(area + 1152, make_float4(0.f, 0.f, 0.f, 0.f));
+    __syncwarp();
     int exponent[NB], top = -1000;
     float sums[S::kParts][GK][NB];
     constexpr int kBits = S::kParts == 2 ? 11 : 15;  // queries go up to 2^kBits
@@ -430,6 +430,8 @@ struct Decode4Math {
     k.x *= k_mul, k.y *= k_mul, k.z *= k_mul, k.w *= k_mul;
     sts128(area + 16 * lane, k);
     float vs[4] = {v.x, v.y, v.z, v.w};
+    float4 mul = lds_f4(area + 1152);
+    float v_mul[4] = {mul.x, mul.y, mul.z, mul.w};
     if (unset) {
       unset = false;
 #pragma unroll
@@ -439,6 +441,8 @@ struct Decode4Math {
         if (top) v_mul[i] = pow2(min(126 - static_cast<int>(top >> 23), 120));  // below 1 then
         else unset = true;
       }
+      __syncwarp();
+      if (lane == 0) sts128(area + 1152, make_float4(v_mul[0], v_mul[1], v_mul[2], v_mul[3]));
     }
     float most = kLeastScale;
 #pragma unroll
@@ -564,7 +568,9 @@ struct Decode4Math {
 
   // This warp's results: res[heads][DV] divided by their sum of weights (so they are no larger than the values are),
   // the maxima with that sum in them, and sums of 1 (0: no token).
-  __device__ __forceinline__ void store(float* res, float* ms, float* ls) {
+  __device__ __forceinline__ void store(float* res, float* ms, float* ls, uint32_t area) {
+    const float4 mul = lds_f4(area + 1152);
+    const float v_mul[4] = {mul.x, mul.y, mul.z, mul.w};
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -656,8 +662,7 @@ __global__ void __launch_bounds__(kDecodeThreads, S::kCtasPerSm)
     else pc = next_piece(a, prefix, per_seq, at, end, &b);
     const char* kbase = static_cast<const char*>(a.cache.k) + pc.hk * a.cache.ks_h + (lane % CK) * 16;
     const char* vbase = static_cast<const char*>(a.cache.v) + pc.hk * a.cache.vs_h + (lane % CV) * 16;
-    const uint16_t* kxbase = a.cache.k_scale + pc.hk * a.cache.kx_h;
-    const uint16_t* vxbase = a.cache.v_scale + pc.hk * a.cache.vx_h;
+    const unsigned kx_head = pc.hk * units.kx_h, vx_head = pc.hk * units.vx_h;
 
     const int base = pc.tile0 * kDecodeTile + warp * kStep;
     const int steps = (pc.tiles * kDecodeTile + kDecodeWarps * kStep - 1) / (kDecodeWarps * kStep);
@@ -753,8 +758,8 @@ __global__ void __launch_bounds__(kDecodeThreads, S::kCtasPerSm)
           }
         }
         const unsigned kx = at_.page * units.kx_p + at_.slot * units.kx_t, vx = same_x ? kx : at_.page * units.vx_p + at_.slot * units.vx_t;
-        copy_scales(raw + lane * S::GK * 2, kxbase + static_cast<unsigned long long>(kx) * kg, kxbase, kg, ok);
-        copy_scales(raw + kStep * S::GK * 2 + lane * S::GV * 2, vxbase + static_cast<unsigned long long>(vx) * vg, vxbase, vg, ok);
+        copy_scales(raw + lane * S::GK * 2, a.cache.k_scale + static_cast<unsigned long long>(kx + kx_head) * kg, a.cache.k_scale, kg, ok);
+        copy_scales(raw + kStep * S::GK * 2 + lane * S::GV * 2, a.cache.v_scale + static_cast<unsigned long long>(vx + vx_head) * vg, a.cache.v_scale, vg, ok);
       }
       cp_async_commit();
       return have;
@@ -764,7 +769,7 @@ __global__ void __launch_bounds__(kDecodeThreads, S::kCtasPerSm)
 #pragma unroll
     for (int s = 0; s < kStages - 1; ++s) live[s] = issue(s, s, lookup(s));
     // The queries are read while the first tokens come.
-    Decode4Math<S, DIRECT> c(a, pc, reinterpret_cast<uint4*>(smem + S::kQueries));
+    Decode4Math<S, DIRECT> c(a, pc, reinterpret_cast<uint4*>(smem + S::kQueries), area);
     __syncthreads();
     Place place = lookup(kStages - 1);
     int stage = 0;
@@ -795,7 +800,7 @@ __global__ void __launch_bounds__(kDecodeThreads, S::kCtasPerSm)
     cp_async_wait<0>();
     __syncthreads();  // every warp is through with its ring: it now takes the results [warp][heads][DV]
     float* res = reinterpret_cast<float*>(smem);
-    c.store(res + warp * pc.heads * DV, ms[warp], ls[warp]);
+    c.store(res + warp * pc.heads * DV, ms[warp], ls[warp], area);
     __syncthreads();
     // The four warps' results as one: into the output, the workspace, or (whole
     // items of a cluster) this CTA's part.

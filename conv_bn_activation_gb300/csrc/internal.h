@@ -451,17 +451,17 @@ constexpr int decode4_dim(int dk, int dv) { return dk <= 64 && dv <= 64 ? 64 : 1
 constexpr int decode4_ctas_per_sm(int dk, int dv, bool bf16, int heads, int batch) {
   const int DK = decode4_dim(dk, dv), DV = DK, hd = heads <= 8 ? 8 : 16;
   const int most = !bf16 || hd == 16 ? 2 : 4, ring = 4 * 2 * 32 * (DK + DV) / 2, results = 4 * 5 * hd * DV;
-  const int bytes = (ring > results ? ring : results) + 4 * 1152 + ring / 8 + (bf16 ? 1 : 2) * DK * hd * 2 + 96 + 512 + 4 * (batch + 1) + 1824, fit = 233472 / bytes;
+  const int bytes = (ring > results ? ring : results) + 4 * 1168 + ring / 8 + (bf16 ? 1 : 2) * DK * hd * 2 + 96 + 512 + 4 * (batch + 1) + 1824, fit = 233472 / bytes;
   return fit < most ? fit : most;
 }
 // What an item's start costs a CTA, in tiles (64 sequences of 130 to 4000 tokens, 8 key heads of 128: 73.3 us with 1,
 // 63.6, 61.5 and 65.5 with 3, 5 and 8). An fp32 tile takes longer.
 constexpr int decode4_item_cost(bool bf16) { return bf16 ? 5 : 3; }
 constexpr int kDecode4Heads = 16, kDecode4HeadsF32 = 8;  // most query heads of one item
-// The streaming kernels' strides of pages and slots, of codes in `bytes` (16, or 4: rows that are not whole 16-byte
+// The streaming kernels' strides of pages and slots (and heads, of scales), of codes in `bytes` (16, or 4: rows that are not whole 16-byte
 // pieces) and of scales in rows' scales (2 for dims up to 64, else 4): 32 bits reach 64 or 16 GB of codes.
 struct Units4 {
-  unsigned bytes, k_p, k_t, v_p, v_t, kx_p, kx_t, vx_p, vx_t;
+  unsigned bytes, k_p, k_t, v_p, v_t, kx_p, kx_t, kx_h, vx_p, vx_t, vx_h;
 };
 // Codes of keys and values as 4-D tensors (bytes of a row, slots, heads, pages), boxes of decode4_box.
 struct Maps4 {

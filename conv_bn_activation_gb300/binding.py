@@ -227,6 +227,7 @@ _SCORE = struct.Struct("2fP2i4P")    # CbScore
 _RULE, _RULE_POS = struct.Struct("if2P3i4x2P"), struct.Struct("P2q")  # CbHeadRule: what a Rotation holds, and the positions
 _raw_stream = None
 _codes = None
+_several = False  # more than one CUDA device
 
 
 def _init_codes():
@@ -234,6 +235,8 @@ def _init_codes():
     import torch
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
         (lambda device: torch.cuda.current_stream(device).cuda_stream)
+    global _several
+    _several = torch.cuda.device_count() > 1
     _codes = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16, "i32": torch.int32, "f32": torch.float32}
 
 
@@ -247,7 +250,11 @@ def _device_of(*tensors):
 
 
 def _stream_of(device, stream):
-    """The stream's handle: `stream`, or the device's current one."""
+    """The stream's handle: `stream`, or the device's current one.  The library launches on the current device."""
+    if _several:
+        import torch
+        if torch.cuda.current_device() != device:
+            raise ValueError(f"the call's tensors are on device {device}, the current one is {torch.cuda.current_device()}")
     if stream is not None:
         return stream.cuda_stream
     if _codes is None:

@@ -68,6 +68,7 @@ bool pieces(const cb_paged_cache4* c, int piece, const void* codes, const void* 
 }
 // The largest pieces that rows of keys and values are made of: 16 bytes, 4 or none.
 int pieces(const cb_paged_cache4* c) {
+  if (c->num_pages == 0) return 0;
   for (const int piece : {16, 4})
     if (pieces(c, piece, c->k, c->k_scale, c->dim_k, {c->k_stride_page, c->k_stride_slot, c->k_stride_head},
                {c->ks_stride_page, c->ks_stride_slot, c->ks_stride_head}) &&

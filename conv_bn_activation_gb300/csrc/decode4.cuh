@@ -1,19 +1,20 @@
 // The streaming kernel of attention over a 4-bit cache (cb_attention_decode4),
 // for rows of whole words (dims that are multiples of 8; of 32: 16-byte pieces).
-// Tokens are dealt as in decode_common.cuh; a CTA's four warps walk a piece together, each
-// its own 32 tokens of every 128 through its own ring of cp.async copies, as in
-// decode_stream.cuh.
+// Tokens are dealt as in decode_common.cuh; a CTA's four warps walk a piece
+// together, each its own 32 tokens of every 128 through its own ring of copies, as
+// in decode_stream.cuh.
 //
 // 4.5 bits an element: at the memory's rate an SM has 97 cycles for 16 tokens of
 // a key head with dims of 128, 388 issue slots and 194 of the integer pipe.  So
-// codes go to the MMAs (m16n8k16, f16 operands, fp32 sums) with one AND and half
-// a shift a pair: the bits of a nibble, alone in 16 bits, are the f16 number
-// code * 2^-24, and of the nibble above it code * 2^-20; ldmatrix hands each lane
-// whole bytes of a token (keys) or of two tokens' same dims (values, transposed).
-// What is left:
-//  - the nibbles hold c + 8.  Keys: -8 sum q of a group goes in as the
-//    accumulator's first value.  Values: one more MMA with -8 everywhere per
-//    tile, in the same step, so that no sum grows with the offset.
+// codes go to the MMAs (m16n8k16, f16 operands, fp32 sums) nearly as they lie:
+// the bits of a nibble, alone in 16 bits, are the f16 number code * 2^-24, and of
+// the nibble above it code * 2^-20, so that two ANDs make two pairs, of whole
+// bytes one; ldmatrix hands each lane whole bytes of a token (keys) or of two
+// tokens' same dims (values, transposed).  What is left:
+//  - the nibbles hold c + 8.  Keys: a score's share of -8 sum q comes out of one
+//    MMA over the group scales (fp32: goes in as the accumulators' first values).
+//    Values: one more MMA with -8 everywhere per tile, in the same step, so that
+//    no sum grows with the offset.
 //  - a group's scale: keys, one FMA per score and group on the group's sum;
 //    values, on the weights, a set of weights per group.
 //  - f16's range.  Queries are scaled by a power of two per head (2^15 above).
@@ -29,6 +30,14 @@
 // element), whose products and sums are exact; weights are sums of two f16
 // numbers (22 bits), codes are made f16 numbers of their own size, and a step's
 // products are added to O by FADDs.
+//
+// Measured: 16 tokens of a key head take 377 instructions, half the schedulers'
+// slots are filled, and neither memory nor a pipe is: eight sequences of up to
+// 131072 tokens, 8 key heads of 128, in 201 us, 0.66 of the copy rate (the bf16
+// cache's 466).  Three CTAs of three stages take as long as four of two (three with
+// one stage less in flight, four with fewer registers than they want).  fp8 MMAs,
+// whose e4m3 subnormals the codes are as well, run as two f16 ones after
+// conversions: 249 us where f16 took 205.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -142,7 +151,7 @@ __device__ __forceinline__ uint32_t half2_rest(float lo, float hi, uint32_t bits
 }
 
 constexpr uint32_t kLowNibble = 0x000f000fu, kHighNibble = 0x00f000f0u;  // times 2^-24, 2^-20
-constexpr uint32_t kByte = 0x00ff00ffu, kByteMinus = 0x80888088u, kHighMinus8 = 0x80808080u;  // -8 (1 + 16), -8 in their units
+constexpr uint32_t kByte = 0x00ff00ffu, kByteMinus8 = 0x80888088u, kHighMinus8 = 0x80808080u;  // -8 (1 + 16) and -8, as they count
 // Codes as f16 numbers of their own: 1024 + c + 8, then 1024 + 16 (c + 8).
 __device__ __forceinline__ uint32_t low_codes(uint32_t w) {
   const uint32_t x = (w & kLowNibble) | 0x64006400u;
@@ -154,8 +163,8 @@ __device__ __forceinline__ uint32_t high_codes(uint32_t w) {
   const __half2 h = __hfma2(*reinterpret_cast<const __half2*>(&x), __float2half2_rn(0.0625f), __float2half2_rn(-72.f));
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-constexpr uint64_t kDrainNs = 20000000;
-constexpr int kWeightBits = 7;     // weights go up to 2^(kDecodeGrowth + kWeightBits) = 2^15
+constexpr uint64_t kDrainNs = 20000000;  // a copy in flight behind a wait that ran out
+constexpr int kWeightBits = 7;           // weights times scales go up to 2^15: f16's range, 2^8 above their running maximum
 constexpr float kLeastScale = 0x1p-60f;  // of a token, beside its group's first: below it counts as this
 
 template <int DK_, int DV_, int NB_, typename T_>
@@ -170,8 +179,7 @@ struct Decode4Shape {
   static constexpr int kResults = 4 * (kDecodeWarps + 1) * kHeads * DV;  // the warps' and the CTA's, when a piece ends
   static constexpr int kMain = kRing > kResults ? kRing : kResults;
   // Behind the ring of codes: a step's scales as the products take them, per warp (keys' fp32, values' fp32 or f16,
-  // tokens' largest, the values' multipliers);
-  // the ring of scales; queries; barriers.
+  // tokens' largest, the values' multipliers); the ring of scales; queries; barriers.
   static constexpr int kArea = kStep * (2 * 16 + 4) + 16, kScales = kMain + kDecodeWarps * kArea;
   static constexpr int kQueries = kScales + kDecodeWarps * kStages * kScaleBytes, kBars = kQueries + kParts * GK * NB * 512;
   static constexpr int kSmem = kBars + kDecodeWarps * kStages * 8, kAlign = 512;  // of the copies' swizzle
@@ -363,8 +371,8 @@ struct Decode4Math {
   }
 
   // O += weights (of 16 tokens, in s) times values; bf16: rows g of a tile take whole bytes, c + 16 c', rows g + 8 the
-  // high nibble 16 c' alone, for an AND less than the low one alone; store() subtracts.  area: S::kParts == 1, [token pair][group] pairs of f16 scales;
-  // else [token] four fp32 scales.
+  // high nibble 16 c' alone, for an AND less than the low one alone; store() subtracts.  area: S::kParts == 1,
+  // [token pair][group] pairs of f16 scales; else [token] four fp32 scales.
   __device__ __forceinline__ void outputs(const float (&s)[NB][4], uint32_t vals, uint32_t area) {
     constexpr bool kF16 = S::kParts == 1;
     const float4 x0 = lds_f4(area + 16 * (kF16 ? t4 : g)), x1 = lds_f4(area + 16 * (kF16 ? t4 + 4 : g + 8));
@@ -390,8 +398,8 @@ struct Decode4Math {
             const uint32_t ub = __byte_perm(u, 0, 0x4341), vb = __byte_perm(v, 0, 0x4341);
             mma_f16(d0, u & kByte, u & kHighNibble, v & kByte, v & kHighNibble, b0, b1);
             mma_f16(d1, ub, ub & kHighNibble, vb, vb & kHighNibble, b0, b1);
-            mma_f16(d0, kByteMinus, kHighMinus8, kByteMinus, kHighMinus8, b0, b1);
-            mma_f16(d1, kByteMinus, kHighMinus8, kByteMinus, kHighMinus8, b0, b1);
+            mma_f16(d0, kByteMinus8, kHighMinus8, kByteMinus8, kHighMinus8, b0, b1);
+            mma_f16(d1, kByteMinus8, kHighMinus8, kByteMinus8, kHighMinus8, b0, b1);
           } else {
             const float p0 = s[nb][0] * c0[i + j], p1 = s[nb][1] * c0[i + j], p2 = s[nb][2] * c1[i + j], p3 = s[nb][3] * c1[i + j];
             uint32_t lo = half2_bits(p0, p1), hi = half2_bits(p2, p3);
@@ -599,14 +607,15 @@ struct Decode4Math {
 };
 
 // TMA: pages of a multiple of 16 slots, whose codes come in boxes of 16 rows (maps: bytes of a row, slots, heads,
-// pages; swizzled as swizzle4 says); else each lane copies 16-byte pieces.  Scales, a token per lane, come by
-// cp.async in either case.
+// pages; swizzled as swizzle4 says); else each lane copies 16-byte pieces, or words.  Scales, a token per lane, come
+// by cp.async in any case.
 template <class S, bool WHOLE, bool TMA, bool DIRECT>
 __global__ void __launch_bounds__(kDecodeThreads, S::kCtasPerSm)
     decode4_stream_kernel(const DecodeArgs a, const Units4 units, const __grid_constant__ Maps4 maps) {
   using T = typename S::T;
   constexpr int DV = S::DV, kStep = S::kStep, kStages = S::kStages;
-  constexpr int CK = S::kKeyBytes / 16, CV = S::kValBytes / 16, RK = 32 / CK, RV = 32 / CV;
+  static_assert(S::DK == S::DV, "keys and values lie alike in a stage");
+  constexpr int CK = S::kKeyBytes / 16, RK = 32 / CK;  // 16-byte pieces of a row; rows of a warp-wide copy
   extern __shared__ __align__(128) uint8_t smem_raw[];
   __shared__ float ms[kDecodeWarps][S::kHeads], ls[kDecodeWarps][S::kHeads];
   __shared__ float part_m[S::kHeads], part_l[S::kHeads];
@@ -646,7 +655,6 @@ __global__ void __launch_bounds__(kDecodeThreads, S::kCtasPerSm)
   const uint32_t raw_ring = smem_u32(smem + S::kScales + warp * kStages * S::kScaleBytes);
   const uint32_t area = smem_u32(smem + S::kMain + warp * S::kArea);
   const uint32_t k_dst = (lane / CK) * S::kKeyBytes + (((lane % CK) ^ swizzle4<S::kKeyBytes>(lane / CK)) * 16);
-  const uint32_t v_dst = kStep * S::kKeyBytes + (lane / CV) * S::kValBytes + (((lane % CV) ^ swizzle4<S::kValBytes>(lane / CV)) * 16);
   const int kg = scales4(a.dk), vg = scales4(a.dv);  // scales of a row, 2 or 4; a row of the ring has room for GK, GV
   const bool same = units.k_p == units.v_p && units.k_t == units.v_t;  // one offset serves both
   const bool same_x = units.kx_p == units.vx_p && units.kx_t == units.vx_t;
@@ -661,20 +669,21 @@ __global__ void __launch_bounds__(kDecodeThreads, S::kCtasPerSm)
     if constexpr (WHOLE) pc = whole_piece(a, per_seq);
     else pc = next_piece(a, prefix, per_seq, at, end, &b);
     const char* kbase = static_cast<const char*>(a.cache.k) + pc.hk * a.cache.ks_h + (lane % CK) * 16;
-    const char* vbase = static_cast<const char*>(a.cache.v) + pc.hk * a.cache.vs_h + (lane % CV) * 16;
+    const char* vbase = static_cast<const char*>(a.cache.v) + pc.hk * a.cache.vs_h + (lane % CK) * 16;
     const unsigned kx_head = pc.hk * units.kx_h, vx_head = pc.hk * units.vx_h;
 
-    const int base = pc.tile0 * kDecodeTile + warp * kStep;
+    const unsigned base = static_cast<unsigned>(pc.tile0) * kDecodeTile + warp * kStep;  // may pass 2^31
     const int steps = (pc.tiles * kDecodeTile + kDecodeWarps * kStep - 1) / (kDecodeWarps * kStep);
-    const unsigned first = pc.lo, limit = static_cast<unsigned>(min(static_cast<long long>(pc.hi), (pc.tile0 + static_cast<long long>(pc.tiles)) * kDecodeTile));
+    const unsigned first = pc.lo;
+    const unsigned limit = min(static_cast<unsigned>(pc.hi), static_cast<unsigned>(pc.tile0 + pc.tiles) * kDecodeTile);
     // Lanes look the step's tokens up, one step before their copies are issued: page (-1: none that the piece needs;
     // TMA: none that the 16 tokens around need) and slot.
     struct Place {
       int page, slot;
     };
     const int* table = a.cache.table + pc.b * a.cache.table_stride;
-    unsigned j = base + lane;  // unsigned: a token looked up past the piece's end may be past 2^31
-    int pg = static_cast<int>(j) / a.cache.page_size, slot = static_cast<int>(j) - pg * a.cache.page_size;
+    unsigned j = base + lane;
+    int pg = static_cast<int>(j / static_cast<unsigned>(a.cache.page_size)), slot = static_cast<int>(j - static_cast<unsigned>(pg) * a.cache.page_size);
     auto lookup = [&](int step) {  // once for each step, in order
       Place r{-1, slot};
       const bool need = TMA ? (j | 15) >= first && (j & ~15u) < limit : j >= first && j < limit;
@@ -708,48 +717,33 @@ __global__ void __launch_bounds__(kDecodeThreads, S::kCtasPerSm)
             }
           }
         } else {
-          const unsigned k_off = at_.page * units.k_p + at_.slot * units.k_t, v_off = same ? k_off : at_.page * units.v_p + at_.slot * units.v_t;
+          const unsigned k_off = at_.page * units.k_p + at_.slot * units.k_t;
+          const unsigned v_off = same ? k_off : at_.page * units.v_p + at_.slot * units.v_t;
           auto copies = [&](auto full) {
             constexpr bool kFull = decltype(full)::value;
 #pragma unroll
             for (int i = 0; i < kStep / RK; ++i) {
               const int r = i * RK + lane / CK;
-              const long long off = 16ull * __shfl_sync(~0u, k_off, r);
+              const unsigned long long off = 16ull * __shfl_sync(~0u, k_off, r), to = same ? off : 16ull * __shfl_sync(~0u, v_off, r);
               const bool some = kFull || ((have >> r) & 1);
-              if (lane % CK < kq) cp_async16((st + k_dst + i * RK * S::kKeyBytes) ^ (swizzle4<S::kKeyBytes>(i * RK) * 16), some ? kbase + off : kbase, some);
-              if (CK == CV) {
-                const long long to = same ? off : 16ull * __shfl_sync(~0u, v_off, r);
-                if (lane % CV < vq) cp_async16((st + v_dst + i * RV * S::kValBytes) ^ (swizzle4<S::kValBytes>(i * RV) * 16), some ? vbase + to : vbase, some);
-              }
-            }
-            if (CK != CV) {
-#pragma unroll
-              for (int i = 0; i < kStep / RV; ++i) {
-                const int r = i * RV + lane / CV;
-                const long long to = 16ull * __shfl_sync(~0u, v_off, r);
-                const bool some = kFull || ((have >> r) & 1);
-                if (lane % CV < vq) cp_async16((st + v_dst + i * RV * S::kValBytes) ^ (swizzle4<S::kValBytes>(i * RV) * 16), some ? vbase + to : vbase, some);
-              }
+              const uint32_t dst = (st + k_dst + i * RK * S::kKeyBytes) ^ (swizzle4<S::kKeyBytes>(i * RK) * 16);
+              if (lane % CK < kq) cp_async16(dst, some ? kbase + off : kbase, some);
+              if (lane % CK < vq) cp_async16(dst + kStep * S::kKeyBytes, some ? vbase + to : vbase, some);
             }
           };
           if (units.bytes == 4) {  // words, where rows are no 16-byte pieces
-            constexpr int WK = S::kKeyBytes / 4, WV = S::kValBytes / 4;
+            constexpr int WK = S::kKeyBytes / 4;
+            const int w = lane % WK;
             const char* kw = kbase - (lane % CK) * 16;
-            const char* vw = vbase - (lane % CV) * 16;
+            const char* vw = vbase - (lane % CK) * 16;
 #pragma unroll 4
             for (int i = 0; i < WK; ++i) {
-              const int r = (i * 32 + lane) / WK, w = lane % WK;
-              const unsigned long long off = 4ull * __shfl_sync(~0u, k_off, r);
+              const int r = (i * 32 + lane) / WK;
+              const unsigned long long off = 4ull * __shfl_sync(~0u, k_off, r) + 4 * w, to = 4ull * __shfl_sync(~0u, v_off, r) + 4 * w;
               const bool some = (have >> r) & 1;
-              if (w < a.dk / 8) cp_async_small<4>(st + r * S::kKeyBytes + (((w >> 2) ^ swizzle4<S::kKeyBytes>(r)) * 16) + (w & 3) * 4, some ? kw + off + w * 4 : kw, some);
-            }
-#pragma unroll 4
-            for (int i = 0; i < WV; ++i) {
-              const int r = (i * 32 + lane) / WV, w = lane % WV;
-              const unsigned long long off = 4ull * __shfl_sync(~0u, v_off, r);
-              const bool some = (have >> r) & 1;
-              if (w < a.dv / 8)
-                cp_async_small<4>(st + kStep * S::kKeyBytes + r * S::kValBytes + (((w >> 2) ^ swizzle4<S::kValBytes>(r)) * 16) + (w & 3) * 4, some ? vw + off + w * 4 : vw, some);
+              const uint32_t dst = st + r * S::kKeyBytes + (((w >> 2) ^ swizzle4<S::kKeyBytes>(r)) * 16) + (w & 3) * 4;
+              if (w < a.dk / 8) cp_async_small<4>(dst, some ? kw + off : kw, some);
+              if (w < a.dv / 8) cp_async_small<4>(dst + kStep * S::kKeyBytes, some ? vw + to : vw, some);
             }
           } else if (have == ~0u) {
             copies(std::true_type{});
@@ -757,9 +751,11 @@ __global__ void __launch_bounds__(kDecodeThreads, S::kCtasPerSm)
             copies(std::false_type{});
           }
         }
-        const unsigned kx = at_.page * units.kx_p + at_.slot * units.kx_t, vx = same_x ? kx : at_.page * units.vx_p + at_.slot * units.vx_t;
-        copy_scales(raw + lane * S::GK * 2, a.cache.k_scale + static_cast<unsigned long long>(kx + kx_head) * kg, a.cache.k_scale, kg, ok);
-        copy_scales(raw + kStep * S::GK * 2 + lane * S::GV * 2, a.cache.v_scale + static_cast<unsigned long long>(vx + vx_head) * vg, a.cache.v_scale, vg, ok);
+        const unsigned kx = at_.page * units.kx_p + at_.slot * units.kx_t;
+        const unsigned vx = same_x ? kx : at_.page * units.vx_p + at_.slot * units.vx_t;
+        const unsigned long long k_at = static_cast<unsigned long long>(kx + kx_head) * kg, v_at = static_cast<unsigned long long>(vx + vx_head) * vg;
+        copy_scales(raw + lane * S::GK * 2, a.cache.k_scale + k_at, a.cache.k_scale, kg, ok);
+        copy_scales(raw + kStep * S::GK * 2 + lane * S::GV * 2, a.cache.v_scale + v_at, a.cache.v_scale, vg, ok);
       }
       cp_async_commit();
       return have;
@@ -788,7 +784,7 @@ __global__ void __launch_bounds__(kDecodeThreads, S::kCtasPerSm)
         alive = __all_sync(~0u, alive);
       }
       __syncwarp();
-      const int far = pc.len - 1 - (base + step * (kDecodeWarps * kStep));
+      const int far = static_cast<int>(pc.len - 1 - (base + step * (kDecodeWarps * kStep)));
       const uint32_t st = ring + stage * S::kStageBytes, raw = raw_ring + stage * S::kScaleBytes;
       if (TMA && !alive) break;
       if (lv == ~0u) c.template step<true>(st, raw, lv, far, a, area);

@@ -243,3 +243,15 @@ def test_stored_values_against_whole_numbers(cblib):
             assert c.denominator == 1 and abs(c) <= 7
             d = abs(F(e) / s - c)
             assert d < F(1, 2) or (d == F(1, 2) and c % 2 == 0) or abs(c) == 7
+
+
+def test_binding_refuses_another_device_than_the_current_one(cblib, monkeypatch):
+    import torch
+    on = OnDevice(monkeypatch, cblib)
+    cblib.heads(torch.zeros(1, 1, 1, 8))  # what the first call sets up
+    monkeypatch.setattr(cblib, "_several", True)
+    k, v = on.make(2, 3, 4, 64), on.make(2, 3, 4, 64)
+    for current, wrong in ((0, AssertionError), (1, ValueError)):
+        monkeypatch.setattr(torch.cuda, "current_device", lambda: current)
+        with pytest.raises(wrong):
+            cblib.norm_rotate(k, v, None, cblib.Rotation(norm=True), stream=on.stream)

@@ -472,3 +472,58 @@ def test_values_that_begin_with_zeros(gpu, dtype):
     sync_check()
     k, v = (ref4.values(*ref4.store(t), D).flatten(0, 1)[:, None] for t in (x, y))
     ref.check(got, ref.decode(q, k, v, torch.arange(n).view(1, n), [n], 0.125), v, dtype)
+
+
+@DTYPES
+@pytest.mark.parametrize("Hq,Hkv", [(3, 3), (12, 2), (10, 1)], ids=str)
+@pytest.mark.parametrize("dk,dv", [(40, 72), (72, 40), (8, 120), (104, 8)])
+@pytest.mark.parametrize("lens", [[40, 0, 129], [3000, 1, 2100, 777]], ids=["whole", "runs"])
+def test_dims_of_whole_words(gpu, lens, dk, dv, Hq, Hkv, dtype):
+    """Rows that are multiples of 4 bytes, not of 16; a last group of 8, 16 or 24 dims."""
+    cache, k, v = filled(lens, 16, Hkv, dk, dv, seed=dk + dv, wide=3000 * (len(lens) == 4))
+    q = (ref.randn(len(lens), Hq, dk, seed=5, dtype=F32, device="cuda") * 2).to(dtype)
+    got = run(q, cache, ints(lens), scale=dk ** -0.5)
+    sync_check()
+    ref.check(got, ref.decode(q, k, v, cache.table, lens, dk ** -0.5), v, dtype)
+
+
+@DTYPES
+@pytest.mark.parametrize("gap,shift", [(4, 0), (16, 4), (3, 1), (32, 16)], ids=str)
+@pytest.mark.parametrize("wide", [0, 3000], ids=["whole", "runs"])
+def test_gaps_between_rows(gpu, wide, gap, shift, dtype):
+    """Codes that lie at any byte, scales at any bf16: append, read and decode choose by that."""
+    lens, H, D, page = [300, 45, 0], 2, 64, 32
+    count = 13
+    table = torch.full((3, 11 + wide), -1, dtype=torch.int32)
+    table[0, :10], table[1, :2] = torch.randperm(10, generator=torch.Generator().manual_seed(1)), torch.tensor([10, 12])
+    parts = []
+    for _ in range(2):
+        codes = torch.full((count, H, page, 32 + gap), 255, dtype=torch.uint8, device="cuda")
+        scales = torch.full((count, H, page, 2 + gap % 4), float("nan"), dtype=BF16, device="cuda")
+        parts += [codes, scales]
+    cut = [parts[i][..., shift:shift + 32].transpose(1, 2) if i % 2 == 0 else parts[i][..., :2].transpose(1, 2) for i in range(4)]
+    cache = cb.PagedCache4(*cut, table.cuda())
+    x, y = (ref.randn(3, 300, H, D, seed=i, dtype=dtype, device="cuda") for i in range(2))
+    cb.cache4_append(x, y, cache, ints([0] * 3), count=ints(lens))
+    out = [torch.zeros(3, 300, H, D, dtype=dtype, device="cuda") for _ in range(2)]
+    cb.cache4_read(cache, *out, count=ints(lens))
+    q = ref.randn(3, 4, D, seed=9, dtype=dtype, device="cuda")
+    got = run(q, cache, ints(lens), scale=0.125)
+    sync_check()
+    k, v = (ref4.values(*ref4.store(t), D) for t in (x, y))
+    for t, w in zip(out, (k, v)):
+        for b, n in enumerate(lens):
+            assert torch.equal(t[b, :n].cpu(), w[b, :n].to(dtype)) and (t[b, n:] == 0).all()
+    flat = [t.flatten(0, 1)[:, None] for t in (k, v)]
+    ref.check(got, ref.decode(q, *flat, torch.arange(900).view(3, 300), lens, 0.125), v, dtype)
+    for i in (0, 2):  # the gaps
+        assert (parts[i][..., :shift] == 255).all() and (parts[i][..., shift + 32:] == 255).all()
+
+
+def test_no_pages(gpu):
+    """A cache without a page: every token is absent, and said to be."""
+    cache = cb.PagedCache4.empty(0, 16, 2, 64, 64, torch.zeros(2, 3, dtype=torch.int32, device="cuda"))
+    q = ref.randn(2, 4, 64, seed=1, dtype=BF16, device="cuda")
+    got = run(q, cache, ints([5, 0]), scale=0.125)
+    assert cb.get_device_error() == cb.ERR_INVALID_ARG and cb.get_device_error() == cb.OK
+    assert (got == 0).all()

@@ -188,3 +188,19 @@ def test_captured_and_on_another_stream(gpu):
         ref4.check_rotate(qo, *ref4.norm_rotate(q, pos, rule.freq, None, norm=True))
         if shift == 0:
             assert torch.equal(qo, want[0]) and torch.equal(ko, want[1])
+
+
+@DTYPES
+@pytest.mark.parametrize("adjacent", [False, True], ids=["halves", "adjacent"])
+@pytest.mark.parametrize("dim,rotary", [(128, 128), (96, 32), (64, 64), (40, 40), (24, 12), (36, 20), (12, 4)], ids=str)
+@pytest.mark.parametrize("shift", [0, 2, 4, 1])
+def test_pieces_of_every_size(gpu, shift, dim, rotary, adjacent, dtype):
+    """Rows at 16, 8, 4 and 2 bytes, and dims that halve into pieces of those."""
+    B, L, H = 2, 19, 3
+    buf = ref.randn(B, L, 2 * H, dim + 4, seed=1, dtype=dtype, device="cuda")
+    q, k = buf[:, :, :H, shift:dim + shift] if shift else buf[:, :, :H, :dim], buf[:, :, H:, shift:dim + shift]
+    w = [ref.randn(dim, seed=i, dtype=F32, device="cuda") for i in range(2)]
+    rule = cb.Rotation(freqs(rotary // 2), adjacent=adjacent, norm=True, q_weight=w[0], k_weight=w[1])
+    rest = [buf[..., :shift].clone(), buf[..., dim + shift:].clone()]
+    both(q, k, positions(1, B, L), rule)
+    assert torch.equal(buf[..., :shift], rest[0]) and torch.equal(buf[..., dim + shift:], rest[1])

@@ -42,6 +42,7 @@
 
 #include <cuda_fp16.h>
 
+#include <cstring>
 #include <type_traits>
 
 #include "cache4.cuh"
@@ -212,7 +213,37 @@ struct Decode4Math {
   bool unset;
   float slope[NB][2], neg[NB][2], l[NB][2], o[2 * GV][NB][4];
 
-  __device__ __forceinline__ Decode4Math(const DecodeArgs& a, const Piece& pc, uint4* q_area, uint32_t area) {
+  // This lane's queries: dims 8 t4 .. + 8 of each group of heads 8 nb + g.  Read before the first tokens are looked up.
+  struct Raw {
+    T x[NB][GK][8];
+  };
+  static __device__ __forceinline__ void fetch(const DecodeArgs& a, const Piece& pc, Raw& raw) {
+    const int g = (threadIdx.x & 31) >> 2, t4 = threadIdx.x & 3;
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      const int hd = g + 8 * nb;
+      const T* q = static_cast<const T*>(a.q) + pc.b * a.qs_b + (pc.h0 + (hd < pc.heads ? hd : 0)) * a.qs_h + 8 * t4;
+#pragma unroll
+      for (int i = 0; i < GK; ++i, q += 32) {
+        constexpr int kPer = 16 / static_cast<int>(sizeof(T));
+        uint4 w[8 / kPer] = {};
+        if (hd < pc.heads && 32 * i + 8 * t4 < a.dk) {
+          if (reinterpret_cast<uintptr_t>(q) % 16 == 0) {
+#pragma unroll
+            for (int e = 0; e < 8 / kPer; ++e) w[e] = reinterpret_cast<const uint4*>(q)[e];
+          } else {
+            T x[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = q[e];
+            memcpy(w, x, sizeof(w));
+          }
+        }
+        memcpy(raw.x[nb][i], w, sizeof(w));
+      }
+    }
+  }
+
+  __device__ __forceinline__ Decode4Math(const DecodeArgs& a, const Piece& pc, const Raw& raw, uint4* q_area, uint32_t area) {
     queries = smem_u32(q_area + (threadIdx.x & 31));
     const DecodeScore score(a);
     const int lane = threadIdx.x & 31;
@@ -228,26 +259,14 @@ struct Decode4Math {
     constexpr int kCodeBits = 24;                   // codes are c + 8 times 2^-kCodeBits
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
-      const int hd = g + 8 * nb;
-      const T* q = static_cast<const T*>(a.q) + pc.b * a.qs_b + (pc.h0 + (hd < heads ? hd : 0)) * a.qs_h;
       float x[GK][8], big = 0.f;
 #pragma unroll
-      for (int i = 0; i < GK; ++i) {
-        const T* at = q + 32 * i + 8 * t4;
-        if (hd >= heads || 32 * i + 8 * t4 >= a.dk) {
+      for (int i = 0; i < GK; ++i)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[i][e] = 0.f;
-        } else if (reinterpret_cast<uintptr_t>(at) % 16 == 0) {
-          constexpr int kPer = 16 / static_cast<int>(sizeof(T));
-#pragma unroll
-          for (int e = 0; e < 8; e += kPer) unpack16<T>(*reinterpret_cast<const uint4*>(at + e), *reinterpret_cast<float(*)[kPer]>(&x[i][e]));
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[i][e] = to_f32(at[e]);
+        for (int e = 0; e < 8; ++e) {
+          x[i][e] = to_f32(raw.x[nb][i][e]);
+          big = fmaxf(big, fabsf(x[i][e]));
         }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) big = fmaxf(big, fabsf(x[i][e]));
-      }
       big = fmaxf(big, __shfl_xor_sync(~0u, big, 1));
       big = fmaxf(big, __shfl_xor_sync(~0u, big, 2));
       // below 2^e2; 0 for what is no number
@@ -761,11 +780,12 @@ __global__ void __launch_bounds__(kDecodeThreads, S::kCtasPerSm)
       return have;
     };
 
+    typename Decode4Math<S, DIRECT>::Raw queries;
+    Decode4Math<S, DIRECT>::fetch(a, pc, queries);
     unsigned live[kStages - 1];  // of the next steps: bit x, token x exists
 #pragma unroll
     for (int s = 0; s < kStages - 1; ++s) live[s] = issue(s, s, lookup(s));
-    // The queries are read while the first tokens come.
-    Decode4Math<S, DIRECT> c(a, pc, reinterpret_cast<uint4*>(smem + S::kQueries), area);
+    Decode4Math<S, DIRECT> c(a, pc, queries, reinterpret_cast<uint4*>(smem + S::kQueries), area);
     __syncthreads();
     Place place = lookup(kStages - 1);
     int stage = 0;

@@ -505,8 +505,16 @@ struct Decode4Math {
   __device__ __forceinline__ void step(uint32_t st, uint32_t raw, unsigned lv, int far, const DecodeArgs& a, uint32_t area) {
     scales<FULL>(raw, lv, a, area);
     float s[2][NB][4];
+    const bool second = FULL || (lv >> 16) != 0;  // there are tokens in the second half
+    scores(s[0], st, area);
+    if (second) {
+      scores(s[1], st + 16 * S::kKeyBytes, area + 256);
+    } else {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) scores(s[h], st + h * 16 * S::kKeyBytes, area + 256 * h);
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) s[1][nb][r] = 0.f;
+    }
     // What the exponential takes: x + neg, x = log2(e) * score.
     float y[2][NB][4], lsum[NB][2];
     if constexpr (!DIRECT) {
@@ -588,9 +596,9 @@ struct Decode4Math {
     }
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) l[nb][0] += lsum[nb][0], l[nb][1] += lsum[nb][1];
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      outputs(y[h], st + S::kStep * S::kKeyBytes + h * 16 * S::kValBytes, area + 512 + (S::kParts == 1 ? 128 : 256) * h);
+    const uint32_t vals = st + S::kStep * S::kKeyBytes;
+    outputs(y[0], vals, area + 512);
+    if (second) outputs(y[1], vals + 16 * S::kValBytes, area + 512 + (S::kParts == 1 ? 128 : 256));
   }
 
   // This warp's results: res[heads][DV] divided by their sum of weights (so they are no larger than the values are),
@@ -691,7 +699,9 @@ __global__ void __launch_bounds__(kDecodeThreads, S::kCtasPerSm)
     const char* vbase = static_cast<const char*>(a.cache.v) + pc.hk * a.cache.vs_h + (lane % CK) * 16;
     const unsigned kx_head = pc.hk * units.kx_h, vx_head = pc.hk * units.vx_h;
 
-    const unsigned base = static_cast<unsigned>(pc.tile0) * kDecodeTile + warp * kStep;  // may pass 2^31
+    // A single tile goes to all four warps, 16 tokens each, where it is all that the CTA has: half the chain.
+    const int take = WHOLE && pc.tiles == 1 ? kDecodeTile / kDecodeWarps : kStep;
+    const unsigned base = static_cast<unsigned>(pc.tile0) * kDecodeTile + warp * take;  // may pass 2^31
     const int steps = (pc.tiles * kDecodeTile + kDecodeWarps * kStep - 1) / (kDecodeWarps * kStep);
     const unsigned first = pc.lo;
     const unsigned limit = min(static_cast<unsigned>(pc.hi), static_cast<unsigned>(pc.tile0 + pc.tiles) * kDecodeTile);
@@ -705,7 +715,7 @@ __global__ void __launch_bounds__(kDecodeThreads, S::kCtasPerSm)
     int pg = static_cast<int>(j / static_cast<unsigned>(a.cache.page_size)), slot = static_cast<int>(j - static_cast<unsigned>(pg) * a.cache.page_size);
     auto lookup = [&](int step) {  // once for each step, in order
       Place r{-1, slot};
-      const bool need = TMA ? (j | 15) >= first && (j & ~15u) < limit : j >= first && j < limit;
+      const bool need = TMA ? (j | 15) >= first && (j & ~15u) < limit : j >= first && j < limit && (!WHOLE || lane < take);
       if (step < steps && need) {
         r.page = table[pg];
         if (static_cast<unsigned>(r.page) >= static_cast<unsigned>(a.cache.num_pages)) {

@@ -11,7 +11,7 @@
 // looks the token's page up.  16 prompts of up to 2048 tokens, 8 heads of 128
 // bf16: stored in 44 us, of 19 at the copy rate (bound by instructions: 0.70 of the
 // issue slots, about 100 for a word and the rest a token's addresses), 16384 such
-// tokens read in 17.6, of 12.7.  One warp per head (the kernels for other rows)
+// tokens read in 15.6, of 12.7.  One warp per head (the kernels for other rows)
 // took 4 to 6 times as long.
 #include "cache4.cuh"
 #include "launch_util.h"
@@ -22,9 +22,12 @@ namespace cb {
 namespace {
 
 constexpr int kWarps = 4;
-// CTAs for each SM, more than it holds: ragged prompts leave some with little (8: 76 us, 12: 73, 16: 71 for those above,
-// stored and read).
-constexpr long long kWordCtas = 16;
+// CTAs for each SM at most.  Counts leave some with little: more than the SM holds (stored and read as above, 6: 73 us, 8:
+// 77, 12: 69, 16: 67.5, 24: 71).  Without counts all have the same: what it holds at once when tokens are read (16 k of them,
+// 6: 15.7 us, 8: 18.3, 16: 17.7), twice that when they are stored (16 k of 4 heads, 6: 13.5, 12: 14.1, 16: 14.8; 32 k of 8,
+// 6: 52, 12: 47, 16: 49).
+constexpr int kReadCtas = 6;
+constexpr long long kCountedCtas = 16, kStoreCtas = 2 * kReadCtas;
 
 // A warp per head of a token's keys or values: a lane per dim of a group.
 template <typename T>
@@ -203,7 +206,8 @@ __global__ void __launch_bounds__(32 * kWarps) cache4_append_kernel(const Append
 }
 
 template <typename T, int U>
-__global__ void __launch_bounds__(32 * kWarps) cache4_read_kernel(const Read4Args a, long long tokens, int chunks, int warps) {
+__global__ void __launch_bounds__(32 * kWarps, kReadCtas) cache4_read_kernel(const Read4Args a, long long tokens, int chunks,
+                                                                             int warps) {
   const int lane = threadIdx.x & 31, warp = blockIdx.x * kWarps + (threadIdx.x >> 5);
   const int words = a.H * (words4(a.dk) + words4(a.dv)), first = warp % chunks * (32 * U) + lane;
   Word w[U];
@@ -264,17 +268,17 @@ __global__ void __launch_bounds__(32 * kWarps) cache4_read_kernel(const Read4Arg
 }
 
 template <typename T, int U, class Args, class Kernel>
-cudaError_t launch_words(Kernel kernel, const Args& a, int sms, cudaStream_t s) {
+cudaError_t launch_words(Kernel kernel, const Args& a, long long ctas, int sms, cudaStream_t s) {
   const long long tokens = static_cast<long long>(a.B) * a.T;
   const int words = a.H * 4 * ((a.dk + kGroup4 - 1) / kGroup4 + (a.dv + kGroup4 - 1) / kGroup4), chunks = (words + 32 * U - 1) / (32 * U);
-  const long long units = tokens * chunks, most = kWordCtas * kWarps * sms;
+  const long long units = tokens * chunks, most = (a.count ? kCountedCtas : ctas) * kWarps * sms;
   const long long warps = units < most ? units : (most < chunks ? chunks : most / chunks * chunks);
   return launch_pdl(kernel, dim3(static_cast<unsigned>((warps + kWarps - 1) / kWarps)), dim3(32 * kWarps), 0, s, a, tokens, chunks,
                     static_cast<int>(warps));
 }
 
 // Eight CTAs' worth of words per SM or fewer: one to a lane, so that a token's heads spread over the GPU; more: four to be
-// stored (two 73 us, eight 73, four 67), eight to be read (two 23 us, four 17.6, eight 16.9).
+// stored (two 73 us, eight 73, four 67), eight to be read (16 CTAs: two 23 us, four 17.6, eight 16.9).
 template <class Args>
 bool few_words(const Args& a, int sms) {
   return static_cast<long long>(a.B) * a.T * a.H * ((a.dk + a.dv) / 8) <= 32LL * kWarps * 8 * sms;
@@ -290,10 +294,10 @@ unsigned grid_of(long long rows, int sms) {
 cudaError_t launch_cache4_append(const AppendArgs& a, bool bf16, bool vec, int sms, cudaStream_t s) {
   if (vec) {
     if (few_words(a, sms))
-      return bf16 ? launch_words<__nv_bfloat16, 1>(cache4_append_kernel<__nv_bfloat16, 1>, a, sms, s)
-                  : launch_words<float, 1>(cache4_append_kernel<float, 1>, a, sms, s);
-    return bf16 ? launch_words<__nv_bfloat16, 4>(cache4_append_kernel<__nv_bfloat16, 4>, a, sms, s)
-                : launch_words<float, 4>(cache4_append_kernel<float, 4>, a, sms, s);
+      return bf16 ? launch_words<__nv_bfloat16, 1>(cache4_append_kernel<__nv_bfloat16, 1>, a, kStoreCtas, sms, s)
+                  : launch_words<float, 1>(cache4_append_kernel<float, 1>, a, kStoreCtas, sms, s);
+    return bf16 ? launch_words<__nv_bfloat16, 4>(cache4_append_kernel<__nv_bfloat16, 4>, a, kStoreCtas, sms, s)
+                : launch_words<float, 4>(cache4_append_kernel<float, 4>, a, kStoreCtas, sms, s);
   }
   const long long rows = 2LL * a.B * a.T * a.H;
   return bf16 ? launch_pdl(cache4_append_rows_kernel<__nv_bfloat16>, dim3(grid_of(rows, sms)), dim3(32 * kWarps), 0, s, a, rows)
@@ -303,10 +307,10 @@ cudaError_t launch_cache4_append(const AppendArgs& a, bool bf16, bool vec, int s
 cudaError_t launch_cache4_read(const Read4Args& a, bool bf16, bool vec, int sms, cudaStream_t s) {
   if (vec) {
     if (few_words(a, sms))
-      return bf16 ? launch_words<__nv_bfloat16, 1>(cache4_read_kernel<__nv_bfloat16, 1>, a, sms, s)
-                  : launch_words<float, 1>(cache4_read_kernel<float, 1>, a, sms, s);
-    return bf16 ? launch_words<__nv_bfloat16, 8>(cache4_read_kernel<__nv_bfloat16, 8>, a, sms, s)
-                : launch_words<float, 8>(cache4_read_kernel<float, 8>, a, sms, s);
+      return bf16 ? launch_words<__nv_bfloat16, 1>(cache4_read_kernel<__nv_bfloat16, 1>, a, kReadCtas, sms, s)
+                  : launch_words<float, 1>(cache4_read_kernel<float, 1>, a, kReadCtas, sms, s);
+    return bf16 ? launch_words<__nv_bfloat16, 8>(cache4_read_kernel<__nv_bfloat16, 8>, a, kReadCtas, sms, s)
+                : launch_words<float, 8>(cache4_read_kernel<float, 8>, a, kReadCtas, sms, s);
   }
   const long long rows = 2LL * a.B * a.T * a.H;
   return bf16 ? launch_pdl(cache4_read_rows_kernel<__nv_bfloat16>, dim3(grid_of(rows, sms)), dim3(32 * kWarps), 0, s, a, rows)

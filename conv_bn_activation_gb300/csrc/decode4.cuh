@@ -33,7 +33,7 @@
 //
 // Measured: 16 tokens of a key head take 377 instructions, half the schedulers'
 // slots are filled, and neither memory nor a pipe is: eight sequences of up to
-// 131072 tokens, 8 key heads of 128, in 201 us, 0.66 of the copy rate (the bf16
+// 131072 tokens, 8 key heads of 128, in 193 us, 0.69 of the copy rate (the bf16
 // cache's 466).  Three CTAs of three stages take as long as four of two (three with
 // one stage less in flight, four with fewer registers than they want).  fp8 MMAs,
 // whose e4m3 subnormals the codes are as well, run as two f16 ones after

@@ -446,7 +446,7 @@ cudaError_t launch_decode_mma(const DecodeArgs& a, cudaStream_t s);  // bf16, ro
 cudaError_t launch_decode_fma(const DecodeArgs& a, cudaStream_t s);  // fp32, rows of whole 16-byte pieces
 cudaError_t launch_decode(const DecodeArgs& a, bool bf16, bool vec, cudaStream_t s);
 // 4-bit caches (decode4.cuh: rows of whole 4-byte words; decode.cu: the others).
-// CTAs that an SM holds: by registers 3 or 2, and no more than its shared memory does.
+// CTAs that an SM holds: by registers 4 or 2, and no more than its shared memory does.
 constexpr int decode4_dim(int dk, int dv) { return dk <= 64 && dv <= 64 ? 64 : 128; }  // the kernel's shape
 constexpr int decode4_ctas_per_sm(int dk, int dv, bool bf16, int heads, int batch) {
   const int DK = decode4_dim(dk, dv), DV = DK, hd = heads <= 8 ? 8 : 16;

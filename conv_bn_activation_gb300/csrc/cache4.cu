@@ -271,7 +271,7 @@ template <typename T, int U, class Args, class Kernel>
 cudaError_t launch_words(Kernel kernel, const Args& a, long long ctas, int sms, cudaStream_t s) {
   const long long tokens = static_cast<long long>(a.B) * a.T;
   const int words = a.H * 4 * ((a.dk + kGroup4 - 1) / kGroup4 + (a.dv + kGroup4 - 1) / kGroup4), chunks = (words + 32 * U - 1) / (32 * U);
-  const long long units = tokens * chunks, most = (a.count ? kCountedCtas : ctas) * kWarps * sms;
+  const long long units = tokens * chunks, most = (U == 1 || a.count ? kCountedCtas : ctas) * kWarps * sms;
   const long long warps = units < most ? units : (most < chunks ? chunks : most / chunks * chunks);
   return launch_pdl(kernel, dim3(static_cast<unsigned>((warps + kWarps - 1) / kWarps)), dim3(32 * kWarps), 0, s, a, tokens, chunks,
                     static_cast<int>(warps));

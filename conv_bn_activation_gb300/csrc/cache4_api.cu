@@ -196,7 +196,7 @@ cb_status cb_norm_rotate(const cb_heads* q, const cb_heads* k, const cb_head_rul
     v.x = in[i]->data, v.y = out[i]->data;
     v.xs_b = in[i]->stride_b, v.xs_l = in[i]->stride_l, v.xs_h = in[i]->stride_h;
     v.ys_b = out[i]->stride_b, v.ys_l = out[i]->stride_l, v.ys_h = out[i]->stride_h;
-    v.weight = i == 0 ? rule->q_weight : rule->k_weight;
+    v.weight = !rule->norm ? nullptr : i == 0 ? rule->q_weight : rule->k_weight;
     v.heads = in[i]->heads;
   }
   a.B = q->batch, a.L = q->len, a.dim = q->dim, a.rotary = rule->rotary;

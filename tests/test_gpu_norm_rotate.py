@@ -124,6 +124,20 @@ def test_infinities_and_nan_stay_in_their_row(gpu, dtype):
     ref4.check_rotate(out.cpu()[~bad], want[~bad], size[~bad])
 
 
+@DTYPES
+@pytest.mark.parametrize("dim", [64, 7])
+def test_weights_are_the_norms_alone(gpu, dim, dtype):
+    """The C struct may hold weights that norm = 0 does not ask for."""
+    q = ref.randn(2, 3, 4, dim, seed=1, dtype=dtype, device="cuda")
+    w = torch.full((dim,), 3.0, device="cuda")
+    rule = cb.Rotation(norm=True, q_weight=w)
+    packed = bytes(4) + rule.view(2, 3, dim, None, q.get_device())[4:]
+    out = torch.empty_like(q)
+    assert cb.load().cb_norm_rotate(cb.heads(q), None, packed, cb.heads(out), None, torch.cuda.current_stream().cuda_stream) == cb.OK
+    sync_check()
+    assert torch.equal(out, q)
+
+
 def test_bad_pairs_do_not_turn_and_are_reported(gpu):
     q = ref.randn(1, 3, 2, 64, seed=1, dtype=F32, device="cuda")
     freq, pos = freqs(32), positions(2, 1, 3)

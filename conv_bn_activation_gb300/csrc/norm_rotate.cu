@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(32 * kWarps, kPiecesCtas) rotate_pieces_kernel
   const unsigned parts = max(split.parts[is_k], 1u), part = unit % parts, step = split.warps[is_k] / parts;
   const unsigned heads = v.heads, advance = parts * slots, first = part * slots + slot;
   const unsigned tokens = static_cast<unsigned>(a.B) * static_cast<unsigned>(a.L);
-  const bool mine = sub < a.dim / (2 * E);
+  const bool mine = sub < a.dim / (2 * E), still = a.rotary < a.dim;  // still: some dims do not turn
   const float inv_dim = 1.f / static_cast<float>(a.dim);
   const unsigned xs_h = static_cast<unsigned>(v.xs_h), ys_h = static_cast<unsigned>(v.ys_h);
   float* const cos_ = cos_s[warp];
@@ -258,18 +258,20 @@ __global__ void __launch_bounds__(32 * kWarps, kPiecesCtas) rotate_pieces_kernel
       const float f = rsqrtf(fmaf(sum, inv_dim, a.eps));
       inv = pack2(f, f);
     }
+    // What does not turn takes nothing from the other dim of its pair, an infinity or NaN neither.
+    auto other = [&](f2 y, int i) { return still && i >= half ? pack2(0.f, 0.f) : y; };
 #pragma unroll
     for (int i = 0; i < H; ++i) {
       const f2 y1 = x[i], y2 = x[H + i];
       if constexpr (ADJ) {
         float u, w;
         unpack2(y1, u, w);
-        x[i] = mul2(fma2(pack2(w, u), s1[i], mul2(y1, c1[i])), inv);
+        x[i] = mul2(fma2(other(pack2(w, u), p0 / 2 + i), s1[i], mul2(y1, c1[i])), inv);
         unpack2(y2, u, w);
-        x[H + i] = mul2(fma2(pack2(w, u), s2[i], mul2(y2, c2[i])), inv);
+        x[H + i] = mul2(fma2(other(pack2(w, u), p1 / 2 + i), s2[i], mul2(y2, c2[i])), inv);
       } else {
-        x[i] = mul2(fma2(y2, s2[i], mul2(y1, c1[i])), inv);
-        x[H + i] = mul2(fma2(y1, s1[i], mul2(y2, c2[i])), inv);
+        x[i] = mul2(fma2(other(y2, sub * E), s2[i], mul2(y1, c1[i])), inv);
+        x[H + i] = mul2(fma2(other(y1, sub * E), s1[i], mul2(y2, c2[i])), inv);
       }
     }
     if (mine && r.head < heads) {

@@ -125,6 +125,33 @@ def test_infinities_and_nan_stay_in_their_row(gpu, dtype):
 
 
 @DTYPES
+@pytest.mark.parametrize("adjacent", [False, True], ids=["halves", "adjacent"])
+@pytest.mark.parametrize("norm", [False, True], ids=["plain", "norm"])
+@pytest.mark.parametrize("dim,rotary", [(128, 64), (128, 0), (96, 32), (40, 20), (36, 12), (7, 4)], ids=str)
+def test_infinities_behind_what_turns_touch_no_other_dim(gpu, dim, rotary, norm, adjacent, dtype):
+    """Dims behind the turning ones stay y, and y of a row with an infinity is 0 but there."""
+    q = ref.randn(1, 3, 4, dim, seed=1, dtype=dtype, device="cuda")
+    far = [d for d in (rotary, rotary + 2, dim - 1) if d < dim]
+    odd = q.clone()
+    for d, x in zip(far, (float("inf"), -float("inf"), float("inf") if norm else float("nan"))):
+        odd[0, 1, 2, d] = x
+    rule = cb.Rotation(freqs(rotary // 2) if rotary else None, adjacent=adjacent, norm=norm)
+    pos = positions(1, 1, 3) if rotary else None
+    out = torch.empty_like(q)
+    cb.norm_rotate(odd, None, pos, rule, out)
+    sync_check()
+    rest = [d for d in range(dim) if d not in far]
+    row = out[0, 1, 2].clone()
+    if norm:
+        assert torch.isnan(row[far]).all() and (row[rest] == 0).all()
+        out[0, 1, 2] = odd[0, 1, 2] = 0
+    else:
+        assert torch.equal(row[far].nan_to_num(7.0, 8.0, 9.0), odd[0, 1, 2, far].nan_to_num(7.0, 8.0, 9.0))
+        out[0, 1, 2, far] = odd[0, 1, 2, far] = 0
+    ref4.check_rotate(out, *ref4.norm_rotate(odd, pos, rule.freq, None, adjacent, norm))
+
+
+@DTYPES
 @pytest.mark.parametrize("dim", [64, 7])
 def test_weights_are_the_norms_alone(gpu, dim, dtype):
     """The C struct may hold weights that norm = 0 does not ask for."""

@@ -166,7 +166,8 @@ __device__ __forceinline__ uint32_t high_codes(uint32_t w) {
 }
 constexpr uint64_t kDrainNs = 20000000;  // a copy in flight behind a wait that ran out
 constexpr int kWeightBits = 7;           // weights times scales go up to 2^15: f16's range, 2^8 above their running maximum
-constexpr float kLeastScale = 0x1p-60f;  // of a token, beside its group's first: below it counts as this
+constexpr float kLeastScale = 0x1p-80f;  // of a token, beside its group's first: below it counts as this
+constexpr int kMostUp = 60;              // the first ones are made about 1 by 2^60 at most, so that later ones, up to 2^67, stay finite
 
 template <int DK_, int DV_, int NB_, typename T_>
 struct Decode4Shape {
@@ -465,7 +466,7 @@ struct Decode4Math {
       for (int i = 0; i < GV; ++i) {
         if (v_mul[i] != 0.f || i * kGroup4 >= a.dv) continue;
         const unsigned top = __reduce_max_sync(~0u, vs[i] < __builtin_huge_valf() ? __float_as_uint(vs[i]) : 0);
-        if (top) v_mul[i] = pow2(min(126 - static_cast<int>(top >> 23), 120));  // below 1 then
+        if (top) v_mul[i] = pow2(min(126 - static_cast<int>(top >> 23), kMostUp));  // below 1 then
         else unset = true;
       }
       __syncwarp();
@@ -586,10 +587,11 @@ struct Decode4Math {
           x = fmaxf(x, __shfl_xor_sync(~0u, x, 16));
           // Before the first token the maximum is -infinity: what is multiplied then is 0.
           const float was = kWeightBits - neg[nb][e], mn = fmaxf(was, x);
-          f[nb][e] = was == kNegInf ? 1.f : exp2_approx(was - mn);
+          const float root = was == kNegInf ? 1.f : exp2_approx(0.5f * (was - mn));
+          f[nb][e] = root * root;
           neg[nb][e] = kWeightBits - mn;
           now[nb][e] = mn == kNegInf ? 0.f : neg[nb][e];
-          l[nb][e] *= f[nb][e];
+          l[nb][e] = l[nb][e] * root * root;  // in two steps: with scales far above the first ones the square may be 0
         }
       rescale(f);
       weights(now);

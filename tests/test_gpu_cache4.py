@@ -457,6 +457,60 @@ def test_a_large_value_of_no_weight(gpu, at, wide, dtype):
         ref.check(got[..., half], want[..., half], v[..., half], dtype)
 
 
+def walked(q, x, y, wide, want, v, dtype, parts):
+    """300 sequences that share two sequences' tokens x, y [2, n, 1, D]: a warp walks several steps of one."""
+    n, D = x.shape[1], x.shape[3]
+    per = (n + 15) // 16
+    table = torch.full((2, per + wide), -1, dtype=torch.int32, device="cuda")
+    table[:, :per] = torch.arange(2 * per, device="cuda").view(2, per)
+    pages = pages4(2 * per, 16, 1, D, D)
+    cb.cache4_append(x, y, cb.PagedCache4(*pages, table), ints([0, 0]))
+    got = run(q.repeat(150, 1, 1), cb.PagedCache4(*pages, table.repeat(150, 1)), ints([n] * 300), scale=0.125)
+    sync_check()
+    for part in parts:
+        ref.check(got[..., part], want.repeat(150, 1, 1)[..., part], v[..., part], dtype)
+
+
+@DTYPES
+@pytest.mark.parametrize("wide", [0, 3000], ids=["whole", "runs"])
+@pytest.mark.parametrize("early,late", [(-123, 14), (-100, 60), (-126, -126), (100, 30)], ids=str)
+def test_values_that_grow_or_shrink_by_many_powers(gpu, early, late, wide, dtype):
+    """Values of 2^early, then of 2^late; the first ones have no weight where they are the larger ones."""
+    n, D = 500, 64
+    x, y = (ref.randn(2, n, 1, D, seed=i, dtype=F32, device="cuda") for i in range(2))
+    y[:, :200] *= 2.0 ** early
+    y[:, 200:] *= 2.0 ** late
+    x[..., 0] = 0.0
+    if early > late:  # e^-100 and less
+        x[:, :200, 0, 0] = -100.0
+    x, y = x.to(BF16), y.to(BF16)
+    q = torch.zeros(2, 4, D, dtype=dtype, device="cuda")
+    q[..., 0] = torch.tensor([8.0, 9.0, 10.0, 8.5], dtype=dtype, device="cuda")
+    k, v = (ref4.values(*ref4.store(t), D).flatten(0, 1)[:, None] for t in (x, y))  # pages of one token
+    want = ref.decode(q, k, v, torch.arange(2 * n).view(2, n), [n, n], 0.125)
+    if early > late:  # 2^100 e^-100 is 2^-44: beside 2^30 nothing
+        v.view(2, n, D)[:, :200] = 0
+    walked(q, x, y, wide, want, v, dtype, [slice(None)])
+
+
+@DTYPES
+@pytest.mark.parametrize("wide", [0, 3000], ids=["whole", "runs"])
+@pytest.mark.parametrize("at", [0, 5, 150, 499], ids=lambda x: f"token{x}")
+def test_a_large_value_of_no_weight_in_a_long_walk(gpu, at, wide, dtype):
+    """As above, where a warp has other tokens before and behind that one."""
+    n, D = 500, 64
+    x, y = (ref.randn(2, n, 1, D, seed=i, dtype=F32, device="cuda") for i in range(2))
+    y[..., 32:] *= 2.0 ** -24
+    x[:, at, 0, 0], y[:, at] = -100.0, y[:, at] * 2.0 ** 40
+    x, y = x.to(BF16), y.to(BF16)
+    q = torch.zeros(2, 4, D, dtype=dtype, device="cuda")
+    q[..., 0] = torch.tensor([8.0, 7.0, 8.5, 9.0], dtype=dtype, device="cuda")
+    k, v = (ref4.values(*ref4.store(t), D).flatten(0, 1)[:, None] for t in (x, y))
+    want = ref.decode(q, k, v, torch.arange(2 * n).view(2, n), [n, n], 0.125)
+    v.view(2, n, D)[:, at] = 0
+    walked(q, x, y, wide, want, v, dtype, [slice(0, 32), slice(32, 64)])
+
+
 @DTYPES
 def test_values_that_begin_with_zeros(gpu, dtype):
     """Tokens, and groups, of zeros before the first others."""

@@ -598,8 +598,9 @@ cb_status cb_cache4_read(const cb_paged_cache4* cache, const int* first, const i
  * bf16.  Codes of dims that are multiples of 8 go to warp-level MMAs: bf16
  * queries and weights times scales are rounded to 11 bits (fp16, within its
  * range by powers of two: weights times scales below 2^-31 of their largest are
- * lost), sums are fp32; for fp32 the products keep 22 bits and more.  All else
- * is fp32 on the CUDA cores.
+ * lost, and values below 2^-80 of a sequence's earlier ones), sums are fp32;
+ * for fp32 the products keep 22 bits and more.  All else is fp32 on the CUDA
+ * cores.
  */
 cb_status cb_attention_decode4_workspace(const cb_heads* q, const cb_paged_cache4* cache, size_t* bytes);
 cb_status cb_attention_decode4(const cb_heads* q, const cb_paged_cache4* cache, const int* length, const int* first,

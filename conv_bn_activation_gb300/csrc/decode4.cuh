@@ -47,6 +47,7 @@
 
 #include "cache4.cuh"
 #include "decode_stream.cuh"
+#include "stage_ring.h"
 
 namespace cb {
 
@@ -690,7 +691,7 @@ __global__ void __launch_bounds__(kDecodeThreads, S::kCtasPerSm)
   // from a lane's token to its next one, without a division per step
   const int adv_pg = kDecodeWarps * kStep / a.cache.page_size, adv_slot = kDecodeWarps * kStep - adv_pg * a.cache.page_size;
   const Watchdog wd{a.err, &abort_flag, a.timeout_ns};
-  unsigned phases = 0;  // bit s: the parity that stage s's barrier is waited for with
+  StageRing<kStages> flight;
   bool alive = true;    // no wait has run out: else the warp copies and computes nothing more
 
   while (at < end) {
@@ -811,9 +812,11 @@ __global__ void __launch_bounds__(kDecodeThreads, S::kCtasPerSm)
       place = lookup(step + kStages);
       cp_async_wait<kStages - 1>();
       if constexpr (TMA) {
-        if (alive) alive = mbar_wait_long(bars + stage, (phases >> stage) & 1, wd);
-        phases ^= 1u << stage;
+        const bool issued = alive;  // once a wait has run out, nothing is any more
+        if (alive) alive = mbar_wait_long(bars + stage, flight.parity(stage), wd);
         alive = __all_sync(~0u, alive);
+        if (alive) flight.waited(stage);
+        else if (issued) flight.in_flight(stage, step, steps, [&](int s, unsigned parity) { mbar_wait_drain(bars + s, parity, kDrainNs); });
       }
       __syncwarp();
       const int far = static_cast<int>(pc.len - 1 - (base + step * (kDecodeWarps * kStep)));
@@ -823,8 +826,6 @@ __global__ void __launch_bounds__(kDecodeThreads, S::kCtasPerSm)
       else if (lv) c.template step<false>(st, raw, lv, far, a, area);
       stage = stage + 1 == kStages ? 0 : stage + 1;
     }
-    if (TMA && !alive)  // its copies in flight, if any land
-      for (int s = 0; s < kStages; ++s) mbar_wait_drain(bars + s, (phases >> s) & 1, kDrainNs);
     cp_async_wait<0>();
     __syncthreads();  // every warp is through with its ring: it now takes the results [warp][heads][DV]
     float* res = reinterpret_cast<float*>(smem);

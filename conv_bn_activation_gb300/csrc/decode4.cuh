@@ -168,7 +168,8 @@ __device__ __forceinline__ uint32_t high_codes(uint32_t w) {
 constexpr uint64_t kDrainNs = 20000000;  // a copy in flight behind a wait that ran out
 constexpr int kWeightBits = 7;           // weights times scales go up to 2^15: f16's range, 2^8 above their running maximum
 constexpr float kLeastScale = 0x1p-80f;  // of a token, beside its group's first: below it counts as this
-constexpr int kMostUp = 60;              // the first ones are made about 1 by 2^60 at most, so that later ones, up to 2^67, stay finite
+constexpr float kMostScale = 0x1p100f;   // and from here on the piece is done again, by redo()
+constexpr int kMostUp = 60;              // the first ones are made about 1, by 2^60 at most
 
 template <int DK_, int DV_, int NB_, typename T_>
 struct Decode4Shape {
@@ -213,6 +214,7 @@ struct Decode4Math {
   // first token): weights are 2^(x + neg).
   // In shared memory, behind the scales' area.
   bool unset;
+  bool beyond;  // the piece holds what this arithmetic does not: redo() does it
   float slope[NB][2], neg[NB][2], l[NB][2], o[2 * GV][NB][4];
 
   // This lane's queries: dims 8 t4 .. + 8 of each group of heads 8 nb + g.  Read before the first tokens are looked up.
@@ -249,7 +251,7 @@ struct Decode4Math {
     queries = smem_u32(q_area + (threadIdx.x & 31));
     const DecodeScore score(a);
     const int lane = threadIdx.x & 31;
-    g = lane >> 2, t4 = lane & 3, heads = pc.heads, unset = true;
+    g = lane >> 2, t4 = lane & 3, heads = pc.heads, unset = true, beyond = false;
     const int row = (lane & 7) + 8 * ((lane >> 3) & 1);
     k_src = row * S::kKeyBytes + (((lane >> 4) ^ swizzle4<S::kKeyBytes>(row)) * 16);
     v_src = row * S::kValBytes + (((lane >> 4) ^ swizzle4<S::kValBytes>(row)) * 16);
@@ -440,9 +442,10 @@ struct Decode4Math {
     }
   }
 
-  // The step's scales as the products take them, a token per lane: area [32] keys', then values'.
+  // The step's scales as the products take them, a token per lane: area [32] keys', then values'.  True where it set a
+  // group's multiplier.
   template <bool FULL>
-  __device__ __forceinline__ void scales(uint32_t raw, unsigned lv, const DecodeArgs& a, uint32_t area) {
+  __device__ __forceinline__ bool scales(uint32_t raw, unsigned lv, const DecodeArgs& a, uint32_t area) {
     const int lane = threadIdx.x & 31;
     const bool live = FULL || ((lv >> lane) & 1);
     auto load = [&](uint32_t at, int groups, int dim) {
@@ -461,13 +464,14 @@ struct Decode4Math {
     float vs[4] = {v.x, v.y, v.z, v.w};
     float4 mul = lds_f4(area + 1152);
     float v_mul[4] = {mul.x, mul.y, mul.z, mul.w};
+    bool fresh = false;
     if (unset) {
       unset = false;
 #pragma unroll
       for (int i = 0; i < GV; ++i) {
         if (v_mul[i] != 0.f || i * kGroup4 >= a.dv) continue;
         const unsigned top = __reduce_max_sync(~0u, vs[i] < __builtin_huge_valf() ? __float_as_uint(vs[i]) : 0);
-        if (top) v_mul[i] = pow2(min(126 - static_cast<int>(top >> 23), kMostUp));  // below 1 then
+        if (top) v_mul[i] = pow2(min(126 - static_cast<int>(top >> 23), kMostUp)), fresh = true;  // below 1 then
         else unset = true;
       }
       __syncwarp();
@@ -498,6 +502,13 @@ struct Decode4Math {
                    : "memory");
     }
     __syncwarp();
+    return fresh;
+  }
+
+  // Whether this step's weights times scales are more than f16 and the sums hold: a scale that left fp32's range beside
+  // the first ones.
+  __device__ __forceinline__ bool too_wide(uint32_t area) const {
+    return !(lds_f(area + 1024 + 4 * (threadIdx.x & 31)) < kMostScale);
   }
 
   // 32 tokens of a stage, codes at st, scales at raw; bit x of lv: token x exists (FULL: all do); far: the first one's
@@ -505,7 +516,7 @@ struct Decode4Math {
   // DIRECT: no cap and no bias.
   template <bool FULL>
   __device__ __forceinline__ void step(uint32_t st, uint32_t raw, unsigned lv, int far, const DecodeArgs& a, uint32_t area) {
-    scales<FULL>(raw, lv, a, area);
+    const bool fresh = scales<FULL>(raw, lv, a, area);
     float s[2][NB][4];
     const bool second = FULL || (lv >> 16) != 0;  // there are tokens in the second half
     scores(s[0], st, area);
@@ -569,7 +580,12 @@ struct Decode4Math {
       }
     };
     weights(neg);
-    if (__any_sync(~0u, grow)) {
+    if (__any_sync(~0u, grow || fresh)) {
+      // An infinite scale makes every weight grow (or NaN): this is where it is met.
+      if (__any_sync(~0u, too_wide(area))) {
+        beyond = true;
+        return;
+      }
       float zero[NB][2], f[NB][2], now[NB][2];
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) zero[nb][0] = zero[nb][1] = 0.f;
@@ -636,12 +652,74 @@ struct Decode4Math {
   }
 };
 
+// The tokens of one warp of a piece: 32 (the first `take` of them) of every 128 from `base` on.
+struct Share {
+  int b, hk, h0, heads, len, steps, take;
+  unsigned base, first, limit;
+};
+
+// A share from the definition, in fp32 on the CUDA cores, for what the products of f16 weights cannot hold: a token per
+// lane for the scores, four dims per lane for the values, a head at a time.  Results as Decode4Math::store() leaves
+// them.  Weights are taken times 2^-32, so that sums of the largest values stay finite.
+template <typename T>
+__device__ __noinline__ void redo(const DecodeArgs& a, const Share w, float* res, int ld, float* ms, float* ls) {
+  constexpr float kLess = 32.f;
+  const int lane = threadIdx.x & 31, dim = 4 * lane;
+  const DecodeScore score(a);
+  for (int hd = 0; hd < w.heads; ++hd) {
+    const T* q = static_cast<const T*>(a.q) + w.b * a.qs_b + (w.h0 + hd) * a.qs_h;
+    const float slope = a.slopes ? a.slopes[w.h0 + hd] * kLog2e : 0.f;
+    float m = kNegInf, mu = 0.f, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int step = 0; step < w.steps; ++step) {
+      const unsigned j = w.base + step * (kDecodeWarps * 32) + lane;
+      int page = -1, slot = 0;
+      if (lane < w.take && j >= w.first && j < w.limit) page = token_page(a, w.b, static_cast<int>(j), &slot);
+      float x[1][1] = {{0.f}};
+      if (page >= 0) {
+        const uint8_t* codes = key_codes4(a.cache, page, slot, w.hk);
+        const uint16_t* scales = key_scales4(a.cache, page, slot, w.hk);
+        for (int d = 0; d < a.dk; d += 8) {
+          const uint32_t c = *reinterpret_cast<const uint32_t*>(codes + d / 2);
+          const float s = bf16_value(scales[d / kGroup4]);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[0][0] = fmaf(to_f32(q[d + e]), (static_cast<int>((c >> (4 * e)) & 15u) - 8) * s, x[0][0]);
+        }
+      }
+      score(x);
+      const float y = page < 0 ? kNegInf : fmaf(-slope, static_cast<float>(w.len - 1 - static_cast<int>(j)), x[0][0]);
+      float top = y;
+      for (int i = 16; i; i >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, i));
+      const float was = m;
+      m = fmaxf(m, top), mu = m == kNegInf ? 0.f : m;
+      const float f = exp2_approx(was - mu), p = page < 0 ? 0.f : exp2_approx(y - mu - kLess);
+      float sum = p;
+      for (int i = 16; i; i >>= 1) sum += __shfl_xor_sync(~0u, sum, i);
+      l = fmaf(l, f, sum);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) o[c] *= f;
+      for (unsigned left = __ballot_sync(~0u, page >= 0); left; left &= left - 1) {
+        const int t = __ffs(left) - 1, pg = __shfl_sync(~0u, page, t), sl = __shfl_sync(~0u, slot, t);
+        const float pt = __shfl_sync(~0u, p, t);
+        if (dim < a.dv) {
+          const unsigned c = *reinterpret_cast<const uint16_t*>(value_codes4(a.cache, pg, sl, w.hk) + dim / 2);
+          const float s = bf16_value(value_scales4(a.cache, pg, sl, w.hk)[dim / kGroup4]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[e] = fmaf(pt, (static_cast<int>((c >> (4 * e)) & 15u) - 8) * s, o[e]);
+        }
+      }
+    }
+    if (lane == 0) ms[hd] = l == 0.f ? kNegInf : mu + kLess + log2f(l), ls[hd] = l == 0.f ? 0.f : l == l ? 1.f : l;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    if (dim < a.dv) *reinterpret_cast<float4*>(res + hd * ld + dim) = make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
+  }
+}
+
 // TMA: pages of a multiple of 16 slots, whose codes come in boxes of 16 rows (maps: bytes of a row, slots, heads,
 // pages; swizzled as swizzle4 says); else each lane copies 16-byte pieces, or words.  Scales, a token per lane, come
 // by cp.async in any case.
 template <class S, bool WHOLE, bool TMA, bool DIRECT>
 __global__ void __launch_bounds__(kDecodeThreads, S::kCtasPerSm)
-    decode4_stream_kernel(const DecodeArgs a, const Units4 units, const __grid_constant__ Maps4 maps) {
+    decode4_stream_kernel(const __grid_constant__ DecodeArgs a, const Units4 units, const __grid_constant__ Maps4 maps) {
   using T = typename S::T;
   constexpr int DV = S::DV, kStep = S::kStep, kStages = S::kStages;
   static_assert(S::DK == S::DV, "keys and values lie alike in a stage");
@@ -805,7 +883,8 @@ __global__ void __launch_bounds__(kDecodeThreads, S::kCtasPerSm)
     for (int step = 0; step < steps; ++step) {
       const int fill = stage == 0 ? kStages - 1 : stage - 1;  // the stage read in the last step
       __syncwarp();
-      const unsigned lv = live[0], next = issue(step + kStages - 1, fill, place);
+      unsigned lv = live[0];
+      const unsigned next = issue(step + kStages - 1, fill, place);
 #pragma unroll
       for (int s = 0; s + 1 < kStages - 1; ++s) live[s] = live[s + 1];
       live[kStages - 2] = next;
@@ -822,6 +901,7 @@ __global__ void __launch_bounds__(kDecodeThreads, S::kCtasPerSm)
       const int far = static_cast<int>(pc.len - 1 - (base + step * (kDecodeWarps * kStep)));
       const uint32_t st = ring + stage * S::kStageBytes, raw = raw_ring + stage * S::kScaleBytes;
       if (TMA && !alive) break;
+      if (c.beyond) lv = 0;
       if (lv == ~0u) c.template step<true>(st, raw, lv, far, a, area);
       else if (lv) c.template step<false>(st, raw, lv, far, a, area);
       stage = stage + 1 == kStages ? 0 : stage + 1;
@@ -829,7 +909,10 @@ __global__ void __launch_bounds__(kDecodeThreads, S::kCtasPerSm)
     cp_async_wait<0>();
     __syncthreads();  // every warp is through with its ring: it now takes the results [warp][heads][DV]
     float* res = reinterpret_cast<float*>(smem);
-    c.store(res + warp * pc.heads * DV, ms[warp], ls[warp], area);
+    if (c.beyond)
+      redo<T>(a, Share{pc.b, pc.hk, pc.h0, pc.heads, pc.len, steps, take, base, first, limit}, res + warp * pc.heads * DV, DV, ms[warp], ls[warp]);
+    else
+      c.store(res + warp * pc.heads * DV, ms[warp], ls[warp], area);
     __syncthreads();
     // The four warps' results as one: into the output, the workspace, or (whole
     // items of a cluster) this CTA's part.

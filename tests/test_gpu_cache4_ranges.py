@@ -1,0 +1,66 @@
+"""Attention over a 4-bit cache where sizes differ by many powers of two, between tokens, groups of dims and heads,
+against the definition in 64 bits; and how far its roundings go."""
+import pytest
+import torch
+
+import attention_ref as ref
+import cache4_ref as ref4
+from conv_bn_activation_gb300 import binding as cb
+from gpu_util import sync_check
+from test_gpu_cache4 import BF16, DTYPES, F32, ints, pages4, run
+
+pytestmark = pytest.mark.gpu
+WAYS = pytest.mark.parametrize("wide", [0, 3000], ids=["whole", "runs"])
+
+
+def stored(x, y, copies=1, wide=0, page=16):
+    """A cache of sequences with tokens x [B, n, H, dk] and y [B, n, H, dv], `copies` times over the same pages, and the
+    stored values as pages of one token with the table that names them."""
+    B, n, H, dk = x.shape
+    per = (n + page - 1) // page
+    table = torch.full((B, per + wide), -1, dtype=torch.int32, device="cuda")
+    table[:, :per] = torch.arange(B * per, device="cuda").view(B, per)
+    parts = pages4(B * per, page, H, dk, y.shape[3])
+    cb.cache4_append(x, y, cb.PagedCache4(*parts, table, dim_k=dk, dim_v=y.shape[3]), ints([0] * B))
+    cache = cb.PagedCache4(*parts, table.repeat(copies, 1), dim_k=dk, dim_v=y.shape[3])
+    k, v = (ref4.values(*ref4.store(t), t.shape[3]).flatten(0, 1)[:, None] for t in (x, y))
+    return cache, k, v, torch.arange(B * n).view(B, n)
+
+
+def scored(n, D, at, low, seed):
+    """Keys whose first dim alone is asked for: ordinary ones, and token `at` of weight e^-1000 where low."""
+    x = ref.randn(2, n, 1, D, seed=seed, dtype=F32, device="cuda")
+    x[..., 0] = 0.0
+    if low:
+        x[:, at, 0, 0] = -1000.0
+    return x
+
+
+def asking(Hq, D, dtype, copies):
+    q = torch.zeros(2, Hq, D, dtype=dtype, device="cuda")
+    q[..., 0] = torch.linspace(8.0, 10.0, Hq).to(dtype)
+    return q, q.repeat(copies, 1, 1)
+
+
+# ------------------------------------------------------------------ values
+@DTYPES
+@WAYS
+@pytest.mark.parametrize("copies", [1, 150], ids=["alone", "walk"])
+@pytest.mark.parametrize("low", [False, True], ids=["weighted", "unweighted"])
+@pytest.mark.parametrize("early,late", [(-100, 70), (-123, 100), (-126, 122)], ids=str)
+def test_finite_values_stay_finite(gpu, early, late, low, copies, wide, dtype):
+    """Values of 2^early and one token of 2^late, up to 2^248 times the others."""
+    n, D, at = 500, 64, 300
+    x, y = scored(n, D, at, low, 0), ref.randn(2, n, 1, D, seed=1, dtype=F32, device="cuda").clamp(-3, 3)
+    large = y[:, at] * 2.0 ** late
+    y *= 2.0 ** early
+    y[:, at] = large
+    x, y = x.to(BF16), y.to(BF16)
+    cache, k, v, place = stored(x, y, copies, wide)
+    q, many = asking(4, D, dtype, copies)
+    want = ref.decode(q, k, v, place, [n, n], 0.125)
+    got = run(many, cache, ints([n] * 2 * copies), scale=0.125)
+    sync_check()
+    if low:
+        v.view(2, n, D)[:, at] = 0
+    ref.check(got, want.repeat(copies, 1, 1), v, dtype)

@@ -21,7 +21,11 @@
 //    A token's largest scale goes into its weight in fp32, what its groups' are
 //    beside it into f16; the running maximum is that of weight times scale, so
 //    that a large value of no weight takes nothing from the others.  Products
-//    below 2^-31 of the largest are lost.
+//    below 2^-31 of the largest are lost; where that, or fp32's range, could
+//    show in a group (its scales far apart from the other groups' or from its
+//    first ones), the run is done again at its end by redo_run(), in fp32 on the
+//    CUDA cores.  Asking costs 1 % (196 -> 198.5 us for the sequences below, 63
+//    -> 63.5 for 64 ragged ones); the same code within the loop over pieces 8 %.
 // The MMAs add 16 products and the sum so far with all that lies 25 bits below
 // the largest exponent cut off, toward zero, and a subnormal's exponent counts as
 // 2^-14: a step's sums keep 15 bits below their largest term, besides the 11 of a
@@ -168,7 +172,7 @@ __device__ __forceinline__ uint32_t high_codes(uint32_t w) {
 constexpr uint64_t kDrainNs = 20000000;  // a copy in flight behind a wait that ran out
 constexpr int kWeightBits = 7;           // weights times scales go up to 2^15: f16's range, 2^8 above their running maximum
 constexpr float kLeastScale = 0x1p-80f;  // of a token, beside its group's first: below it counts as this
-constexpr float kMostScale = 0x1p100f;   // and from here on the piece is done again, by redo()
+constexpr float kMostScale = 0x1p100f;   // and from here on redo() has to do it
 constexpr int kMostUp = 60;              // the first ones are made about 1, by 2^60 at most
 
 template <int DK_, int DV_, int NB_, typename T_>
@@ -184,7 +188,7 @@ struct Decode4Shape {
   static constexpr int kMain = kRing > kResults ? kRing : kResults;
   // Behind the ring of codes: a step's scales as the products take them, per warp (keys' fp32, values' fp32 or f16,
   // tokens' largest, the values' multipliers); the ring of scales; queries; barriers.
-  static constexpr int kArea = kStep * (2 * 16 + 4) + 16, kScales = kMain + kDecodeWarps * kArea;
+  static constexpr int kArea = kStep * (2 * 16 + 4) + 32, kScales = kMain + kDecodeWarps * kArea;
   static constexpr int kQueries = kScales + kDecodeWarps * kStages * kScaleBytes, kBars = kQueries + kParts * GK * NB * 512;
   static constexpr int kSmem = kBars + kDecodeWarps * kStages * 8, kAlign = 512;  // of the copies' swizzle
   static constexpr int kCtasPerSm = decode4_ctas_per_sm(DK, DV, sizeof(T) == 2, kHeads, 0);
@@ -200,6 +204,9 @@ template <class S, bool DIRECT>
 struct Decode4Math {
   using T = typename S::T;
   static constexpr int GK = S::GK, GV = S::GV, NB = S::NB;
+  // What a weight rounded below 2^-14 loses is 2^-25 at most; a group's largest product of weight and scale, when the
+  // maximum is set, 2^7 times this at least.  So that is 2^-20 of it, or for fp32 2^-24.
+  static constexpr float kApart = S::kParts == 1 ? 0x1p-12f : 0x1p-8f;
   int g, t4, heads;
   uint32_t k_src, v_src;  // this lane's ldmatrix rows
   // Queries as the MMAs' B operand, for each part and group: head g, dims 8 t4 + (0, 4) and (1, 5) / 16, then (2, 6) and
@@ -213,8 +220,8 @@ struct Decode4Math {
   // unset: of some group).  neg = kWeightBits - maximum of x + log2 of a token's largest scale (+infinity before the
   // first token): weights are 2^(x + neg).
   // In shared memory, behind the scales' area.
+  // Behind them, for the whole launch: whether the warp met what this arithmetic does not hold.
   bool unset;
-  bool beyond;  // the piece holds what this arithmetic does not: redo() does it
   float slope[NB][2], neg[NB][2], l[NB][2], o[2 * GV][NB][4];
 
   // This lane's queries: dims 8 t4 .. + 8 of each group of heads 8 nb + g.  Read before the first tokens are looked up.
@@ -251,7 +258,7 @@ struct Decode4Math {
     queries = smem_u32(q_area + (threadIdx.x & 31));
     const DecodeScore score(a);
     const int lane = threadIdx.x & 31;
-    g = lane >> 2, t4 = lane & 3, heads = pc.heads, unset = true, beyond = false;
+    g = lane >> 2, t4 = lane & 3, heads = pc.heads, unset = true;
     const int row = (lane & 7) + 8 * ((lane >> 3) & 1);
     k_src = row * S::kKeyBytes + (((lane >> 4) ^ swizzle4<S::kKeyBytes>(row)) * 16);
     v_src = row * S::kValBytes + (((lane >> 4) ^ swizzle4<S::kValBytes>(row)) * 16);
@@ -442,23 +449,38 @@ struct Decode4Math {
     }
   }
 
-  // The step's scales as the products take them, a token per lane: area [32] keys', then values'.  True where it set a
-  // group's multiplier.
+  // A token's scales of a step: this lane's, 0 behind the last group's.
   template <bool FULL>
-  __device__ __forceinline__ bool scales(uint32_t raw, unsigned lv, const DecodeArgs& a, uint32_t area) {
+  static __device__ __forceinline__ float4 load_scales(uint32_t at, int groups, int dim, unsigned lv) {
+    uint32_t w0, w1 = 0;
+    if (groups == 4) asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w0), "=r"(w1) : "r"(at) : "memory");
+    else asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w0) : "r"(at) : "memory");
+    if (!FULL && !((lv >> (threadIdx.x & 31)) & 1)) w0 = w1 = 0;
+    if (dim <= 32) w0 &= 0xffffu;
+    if (dim <= 96) w1 = dim <= 64 ? 0 : w1 & 0xffffu;
+    return make_float4(__uint_as_float(w0 << 16), __uint_as_float(w0 & 0xffff0000u), __uint_as_float(w1 << 16),
+                       __uint_as_float(w1 & 0xffff0000u));
+  }
+
+  // Whether this lane's token has scales that f16 weights and the sums do not hold (s: the groups', times their
+  // multipliers; most: the largest as it goes into the weights): one that left fp32's range beside the first ones, or
+  // groups' that are far apart.  The maximum is that of weight times a token's largest scale, for all groups, so that where
+  // such a token sets it another group's products would be rounded, or lost, below f16's range.  Asked where a maximum
+  // grows or a group's multiplier is set: between those what a group loses is small beside what it had then.
+  // Its run (whole items: it) is then done again, by redo_run() or redo().
+  __device__ __forceinline__ void ask(const float (&s)[4], const float (&mul)[4], float most, uint32_t area) const {
+    float least = __builtin_huge_valf(), top = 0.f;
+#pragma unroll
+    for (int i = 0; i < GV; ++i)
+      if (mul[i] != 0.f) least = fminf(least, s[i]), top = fmaxf(top, s[i]);  // else nothing but zeros so far
+    if (!(most < kMostScale) || (top > 0.f && least < most * kApart)) asm volatile("st.shared.u32 [%0], %1;" ::"r"(area + 1168), "r"(0x3f800000) : "memory");
+  }
+
+  // The step's scales as the products take them, a token per lane: area [32] keys', then values'.
+  template <bool FULL>
+  __device__ __forceinline__ void scales(uint32_t raw, unsigned lv, const DecodeArgs& a, uint32_t area) {
     const int lane = threadIdx.x & 31;
-    const bool live = FULL || ((lv >> lane) & 1);
-    auto load = [&](uint32_t at, int groups, int dim) {
-      uint32_t w0, w1 = 0;
-      if (groups == 4) asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w0), "=r"(w1) : "r"(at) : "memory");
-      else asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w0) : "r"(at) : "memory");
-      if (!live) w0 = w1 = 0;
-      if (dim <= 32) w0 &= 0xffffu;  // behind the last group's: none
-      if (dim <= 96) w1 = dim <= 64 ? 0 : w1 & 0xffffu;
-      return make_float4(__uint_as_float(w0 << 16), __uint_as_float(w0 & 0xffff0000u), __uint_as_float(w1 << 16),
-                         __uint_as_float(w1 & 0xffff0000u));
-    };
-    float4 k = load(raw + lane * GK * 2, GK, a.dk), v = load(raw + S::kStep * GK * 2 + lane * GV * 2, GV, a.dv);
+    float4 k = load_scales<FULL>(raw + lane * GK * 2, GK, a.dk, lv), v = load_scales<FULL>(raw + S::kStep * GK * 2 + lane * GV * 2, GV, a.dv, lv);
     k.x *= k_mul, k.y *= k_mul, k.z *= k_mul, k.w *= k_mul;
     sts128(area + 16 * lane, k);
     float vs[4] = {v.x, v.y, v.z, v.w};
@@ -483,6 +505,7 @@ struct Decode4Math {
       vs[i] *= v_mul[i];
       most = fmaxf(most, vs[i]);  // not NaN
     }
+    if (fresh) ask(vs, v_mul, most, area);
     asm volatile("st.shared.f32 [%0], %1;" ::"r"(area + 1024 + 4 * lane), "f"(most) : "memory");
     v = make_float4(vs[0], vs[1], vs[2], vs[3]);
     if constexpr (S::kParts == 2) {
@@ -502,13 +525,6 @@ struct Decode4Math {
                    : "memory");
     }
     __syncwarp();
-    return fresh;
-  }
-
-  // Whether this step's weights times scales are more than f16 and the sums hold: a scale that left fp32's range beside
-  // the first ones.
-  __device__ __forceinline__ bool too_wide(uint32_t area) const {
-    return !(lds_f(area + 1024 + 4 * (threadIdx.x & 31)) < kMostScale);
   }
 
   // 32 tokens of a stage, codes at st, scales at raw; bit x of lv: token x exists (FULL: all do); far: the first one's
@@ -516,7 +532,7 @@ struct Decode4Math {
   // DIRECT: no cap and no bias.
   template <bool FULL>
   __device__ __forceinline__ void step(uint32_t st, uint32_t raw, unsigned lv, int far, const DecodeArgs& a, uint32_t area) {
-    const bool fresh = scales<FULL>(raw, lv, a, area);
+    scales<FULL>(raw, lv, a, area);
     float s[2][NB][4];
     const bool second = FULL || (lv >> 16) != 0;  // there are tokens in the second half
     scores(s[0], st, area);
@@ -580,11 +596,11 @@ struct Decode4Math {
       }
     };
     weights(neg);
-    if (__any_sync(~0u, grow || fresh)) {
-      // An infinite scale makes every weight grow (or NaN): this is where it is met.
-      if (__any_sync(~0u, too_wide(area))) {
-        beyond = true;
-        return;
+    if (__any_sync(~0u, grow)) {
+      {  // An infinite scale makes every weight grow (or NaN): it is met here.
+        const int lane = threadIdx.x & 31;
+        const float4 v = load_scales<FULL>(raw + S::kStep * GK * 2 + lane * GV * 2, GV, a.dv, lv), mul = lds_f4(area + 1152);
+        ask({v.x * mul.x, v.y * mul.y, v.z * mul.z, v.w * mul.w}, {mul.x, mul.y, mul.z, mul.w}, lds_f(area + 1024 + 4 * lane), area);
       }
       float zero[NB][2], f[NB][2], now[NB][2];
 #pragma unroll
@@ -656,6 +672,10 @@ struct Decode4Math {
 struct Share {
   int b, hk, h0, heads, len, steps, take;
   unsigned base, first, limit;
+  __device__ __forceinline__ Share(const Piece& pc, int warp, int take_)
+      : b(pc.b), hk(pc.hk), h0(pc.h0), heads(pc.heads), len(pc.len), steps((pc.tiles * kDecodeTile + kDecodeWarps * 32 - 1) / (kDecodeWarps * 32)),
+        take(take_), base(static_cast<unsigned>(pc.tile0) * kDecodeTile + warp * take_), first(pc.lo),
+        limit(min(static_cast<unsigned>(pc.hi), static_cast<unsigned>(pc.tile0 + pc.tiles) * kDecodeTile)) {}
 };
 
 // A share from the definition, in fp32 on the CUDA cores, for what the products of f16 weights cannot hold: a token per
@@ -714,6 +734,40 @@ __device__ __noinline__ void redo(const DecodeArgs& a, const Share w, float* res
   }
 }
 
+// All pieces of a CTA's run again, by all its threads; where a warp has met what it does not hold.
+template <typename T>
+__device__ __noinline__ void redo_run(const DecodeArgs& a, const unsigned* prefix, float* res, int ld, float* ms, float* ls, int width) {
+  const int tid = threadIdx.x, warp = tid >> 5, per_seq = a.Hkv * a.chunks;
+  const long long total = static_cast<long long>(prefix[a.B]) * per_seq, cta = blockIdx.x;
+  const Run run{total, min(static_cast<long long>(gridDim.x), total)};
+  long long at = run.begin(cta);
+  const long long end = run.begin(cta + 1);
+  int b = find_seq(a, prefix, per_seq, at);
+  while (at < end) {
+    const Piece pc = next_piece(a, prefix, per_seq, at, end, &b);
+    redo<T>(a, Share{pc, warp, 32}, res + warp * pc.heads * ld, ld, ms + warp * width, ls + warp * width);
+    __syncthreads();
+    const bool out = pc.starts && pc.ends;
+    float* part = a.part + (2 * cta + (pc.starts ? 1 : 0)) * part_floats(a.item_heads, a.dv);
+    T* o = static_cast<T*>(a.o) + pc.b * a.os_b + pc.h0 * a.os_h;
+    for (int e = tid; e < pc.heads * a.dv; e += kDecodeThreads) {
+      const int hd = e / a.dv, d = e % a.dv;
+      float m = kNegInf, l = 0.f, sum = 0.f;
+      for (int w = 0; w < kDecodeWarps; ++w) m = fmaxf(m, ms[w * width + hd]);
+      const float mu = m == kNegInf ? 0.f : m;
+      for (int w = 0; w < kDecodeWarps; ++w) l = fmaf(exp2_approx(ms[w * width + hd] - mu), ls[w * width + hd], l);
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      for (int w = 0; w < kDecodeWarps; ++w) sum = fmaf(exp2_approx(ms[w * width + hd] - mu) * inv, res[(w * pc.heads + hd) * ld + d], sum);
+      if (out) o[hd * a.os_h + d] = from_f32<T>(sum);
+      else part[2 * a.item_heads + hd * a.dv + d] = sum;
+      if (!out && d == 0) part[hd] = l == 0.f ? kNegInf : m + log2f(l), part[a.item_heads + hd] = l == 0.f ? 0.f : l == l ? 1.f : l;
+    }
+    __syncthreads();
+    at += pc.dealt;
+  }
+}
+__device__ __forceinline__ bool beyond4(uint32_t area) { return lds_f(area + 1168) != 0.f; }
+
 // TMA: pages of a multiple of 16 slots, whose codes come in boxes of 16 rows (maps: bytes of a row, slots, heads,
 // pages; swizzled as swizzle4 says); else each lane copies 16-byte pieces, or words.  Scales, a token per lane, come
 // by cp.async in any case.
@@ -771,6 +825,8 @@ __global__ void __launch_bounds__(kDecodeThreads, S::kCtasPerSm)
   const Watchdog wd{a.err, &abort_flag, a.timeout_ns};
   StageRing<kStages> flight;
   bool alive = true;    // no wait has run out: else the warp copies and computes nothing more
+
+  if (lane == 0) sts128(area + 1168, make_float4(0.f, 0.f, 0.f, 0.f));
 
   while (at < end) {
     Piece pc;
@@ -883,8 +939,7 @@ __global__ void __launch_bounds__(kDecodeThreads, S::kCtasPerSm)
     for (int step = 0; step < steps; ++step) {
       const int fill = stage == 0 ? kStages - 1 : stage - 1;  // the stage read in the last step
       __syncwarp();
-      unsigned lv = live[0];
-      const unsigned next = issue(step + kStages - 1, fill, place);
+      const unsigned lv = live[0], next = issue(step + kStages - 1, fill, place);
 #pragma unroll
       for (int s = 0; s + 1 < kStages - 1; ++s) live[s] = live[s + 1];
       live[kStages - 2] = next;
@@ -901,7 +956,6 @@ __global__ void __launch_bounds__(kDecodeThreads, S::kCtasPerSm)
       const int far = static_cast<int>(pc.len - 1 - (base + step * (kDecodeWarps * kStep)));
       const uint32_t st = ring + stage * S::kStageBytes, raw = raw_ring + stage * S::kScaleBytes;
       if (TMA && !alive) break;
-      if (c.beyond) lv = 0;
       if (lv == ~0u) c.template step<true>(st, raw, lv, far, a, area);
       else if (lv) c.template step<false>(st, raw, lv, far, a, area);
       stage = stage + 1 == kStages ? 0 : stage + 1;
@@ -909,8 +963,8 @@ __global__ void __launch_bounds__(kDecodeThreads, S::kCtasPerSm)
     cp_async_wait<0>();
     __syncthreads();  // every warp is through with its ring: it now takes the results [warp][heads][DV]
     float* res = reinterpret_cast<float*>(smem);
-    if (c.beyond)
-      redo<T>(a, Share{pc.b, pc.hk, pc.h0, pc.heads, pc.len, steps, take, base, first, limit}, res + warp * pc.heads * DV, DV, ms[warp], ls[warp]);
+    if (WHOLE && beyond4(area))
+      redo<T>(a, Share{pc, warp, take}, res + warp * pc.heads * DV, DV, ms[warp], ls[warp]);
     else
       c.store(res + warp * pc.heads * DV, ms[warp], ls[warp], area);
     __syncthreads();
@@ -979,6 +1033,11 @@ __global__ void __launch_bounds__(kDecodeThreads, S::kCtasPerSm)
     at += pc.dealt;
     if constexpr (TMA) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the results' bytes take copies again
     __syncthreads();
+  }
+  if constexpr (!WHOLE) {
+    bool again = false;
+    for (int w = 0; w < kDecodeWarps; ++w) again |= beyond4(area + (w - warp) * S::kArea);
+    if (again) redo_run<T>(a, prefix, reinterpret_cast<float*>(smem), DV, ms[0], ls[0], S::kHeads);
   }
 }
 

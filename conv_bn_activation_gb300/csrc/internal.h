@@ -451,7 +451,7 @@ constexpr int decode4_dim(int dk, int dv) { return dk <= 64 && dv <= 64 ? 64 : 1
 constexpr int decode4_ctas_per_sm(int dk, int dv, bool bf16, int heads, int batch) {
   const int DK = decode4_dim(dk, dv), DV = DK, hd = heads <= 8 ? 8 : 16;
   const int most = !bf16 || hd == 16 ? 2 : 4, ring = 4 * 2 * 32 * (DK + DV) / 2, results = 4 * 5 * hd * DV;
-  const int bytes = (ring > results ? ring : results) + 4 * 1168 + ring / 8 + (bf16 ? 1 : 2) * DK * hd * 2 + 96 + 512 + 4 * (batch + 1) + 1824, fit = 233472 / bytes;
+  const int bytes = (ring > results ? ring : results) + 4 * 1184 + ring / 8 + (bf16 ? 1 : 2) * DK * hd * 2 + 96 + 512 + 4 * (batch + 1) + 1824, fit = 233472 / bytes;
   return fit < most ? fit : most;
 }
 // What an item's start costs a CTA, in tiles (64 sequences of 130 to 4000 tokens, 8 key heads of 128: 73.3 us with 1,

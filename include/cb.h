@@ -597,10 +597,12 @@ cb_status cb_cache4_read(const cb_paged_cache4* cache, const int* first, const i
  * values c * s; no two rows of out overlap.  q and out are both fp32 or both
  * bf16.  Codes of dims that are multiples of 8 go to warp-level MMAs: bf16
  * queries and weights times scales are rounded to 11 bits (fp16, within its
- * range by powers of two: weights times scales below 2^-31 of their largest are
- * lost, and values below 2^-80 of a sequence's earlier ones), sums are fp32;
- * for fp32 the products keep 22 bits and more.  All else is fp32 on the CUDA
- * cores.
+ * range by powers of two: weights times scales below 2^-31 of their largest
+ * are lost), sums are fp32; for fp32 the products keep 22 bits and more.
+ * Where values' sizes differ by so much, between tokens or groups, that those
+ * roundings would be more than that of a group's own values, the tokens
+ * around are done in fp32 on the CUDA cores, at a tenth of the speed or less.
+ * All else is fp32 on the CUDA cores.
  */
 cb_status cb_attention_decode4_workspace(const cb_heads* q, const cb_paged_cache4* cache, size_t* bytes);
 cb_status cb_attention_decode4(const cb_heads* q, const cb_paged_cache4* cache, const int* length, const int* first,

@@ -64,3 +64,37 @@ def test_finite_values_stay_finite(gpu, early, late, low, copies, wide, dtype):
     if low:
         v.view(2, n, D)[:, at] = 0
     ref.check(got, want.repeat(copies, 1, 1), v, dtype)
+
+
+@DTYPES
+@WAYS
+@pytest.mark.parametrize("copies", [1, 150], ids=["alone", "walk"])
+@pytest.mark.parametrize("early,late", [(-61, 69), (-20, 115), (-20, 15), (-60, 60)], ids=str)
+def test_values_far_below_one_of_no_weight(gpu, early, late, copies, wide, dtype):
+    """The same where the large value has no weight, and f16, or the least scale beside it, would take the others'."""
+    test_finite_values_stay_finite(gpu, early, late, True, copies, wide, dtype)
+
+
+@DTYPES
+@WAYS
+@pytest.mark.parametrize("copies", [1, 150], ids=["alone", "walk"])
+@pytest.mark.parametrize("low", [False, True], ids=["weighted", "unweighted"])
+@pytest.mark.parametrize("at", [0, 5, 40, 130], ids=lambda x: f"token{x}")
+@pytest.mark.parametrize("power", [6, 13, 24, 32, 40, 100], ids=lambda p: f"2^{p}")
+def test_an_outlier_in_one_group(gpu, power, at, low, copies, wide, dtype):
+    """One token's first 32 values are 2^power times the others': each group of dims is as exact as its own values
+    ask for, whatever the token's weight."""
+    n, D = 140, 96
+    x, y = scored(n, D, at, low, 2), ref.randn(2, n, 1, D, seed=3, dtype=F32, device="cuda").abs() + 0.5
+    y[:, at, :, :32] *= 2.0 ** power
+    y[..., 64:] *= 2.0 ** -30
+    x, y = x.to(BF16), y.to(BF16)
+    cache, k, v, place = stored(x, y, copies, wide)
+    q, many = asking(5, D, dtype, copies)
+    want = ref.decode(q, k, v, place, [n, n], 0.125).repeat(copies, 1, 1)
+    got = run(many, cache, ints([n] * 2 * copies), scale=0.125)
+    sync_check()
+    if low:
+        v.view(2, n, D)[:, at] = 0
+    for group in (slice(0, 32), slice(32, 64), slice(64, 96)):
+        ref.check(got[..., group], want[..., group], v[..., group], dtype)

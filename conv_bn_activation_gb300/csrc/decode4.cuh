@@ -324,7 +324,9 @@ struct Decode4Math {
       }
     }
     for (int s = 4; s < 32; s <<= 1) top = max(top, __shfl_xor_sync(~0u, top, s));
-    const int k_exp = min(max(top + kCodeBits, -126), 127);
+    // The heads' powers take part in their scores at the end; the keys' scales take what is above 2^60 of the largest one's,
+    // so that neither leaves fp32's range where the scores do not.
+    const int k_exp = max(top + kCodeBits - 60, 0);
     k_mul = pow2(k_exp);
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
@@ -332,7 +334,8 @@ struct Decode4Math {
       for (int e = 0; e < 2; ++e) {
         const int from = 4 * (2 * t4 + e), hd = 8 * nb + 2 * t4 + e;
         const int he = __shfl_sync(~0u, exponent[nb], from);
-        head_mul[nb][e] = pow2(max(min(he + kCodeBits - k_exp, 16), -126)) * (score.cap ? 1.f : score.c_scale);
+        const int up = he + kCodeBits - k_exp;
+        head_mul[nb][e] = up < -126 ? 0.f : pow2(up) * (score.cap ? 1.f : score.c_scale);
 #pragma unroll
         for (int p = 0; p < S::kParts && S::kParts == 2; ++p)
 #pragma unroll

@@ -98,3 +98,23 @@ def test_an_outlier_in_one_group(gpu, power, at, low, copies, wide, dtype):
         v.view(2, n, D)[:, at] = 0
     for group in (slice(0, 32), slice(32, 64), slice(64, 96)):
         ref.check(got[..., group], want[..., group], v[..., group], dtype)
+
+
+# ------------------------------------------------------------------ scores
+@DTYPES
+@WAYS
+@pytest.mark.parametrize("cap", [30.0])
+@pytest.mark.parametrize("size", [100, 40, 0, -100], ids=lambda e: f"keys2^{e}")
+def test_heads_of_different_sizes(gpu, size, cap, wide, dtype):
+    """A head whose scores go to 2^120 beside heads of ordinary scores, whatever the keys' size.  Queries of one dim of
+    8 bits, so that scores are exact: of the large ones one token's is the largest."""
+    n, D = 120, 64
+    x, y = ref.randn(2, n, 1, D, seed=4, dtype=F32, device="cuda") * 2.0 ** size, ref.randn(2, n, 1, D, seed=5, dtype=BF16, device="cuda")
+    cache, k, v, place = stored(x.to(BF16), y, 1, wide)
+    q = torch.zeros(2, 4, D, dtype=F32, device="cuda")
+    for h, power in enumerate((118 - size if size >= 0 else 126, 3 - size, 1 - size, -size)):
+        q[:, h, 17 + h] = 1.375 * 2.0 ** power
+    q = q.to(dtype)
+    got = run(q, cache, ints([n, n]), scale=0.125, softcap=cap)
+    sync_check()
+    ref.check(got, ref.decode(q, k, v, place, [n, n], 0.125, softcap=cap), v, dtype)

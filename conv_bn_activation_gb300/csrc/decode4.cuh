@@ -173,6 +173,7 @@ constexpr uint64_t kDrainNs = 20000000;  // a copy in flight behind a wait that 
 constexpr int kWeightBits = 7;           // weights times scales go up to 2^15: f16's range, 2^8 above their running maximum
 constexpr float kLeastScale = 0x1p-80f;  // of a token, beside its group's first: below it counts as this
 constexpr float kMostScale = 0x1p100f;   // and from here on redo() has to do it
+constexpr float kMostScore = 0x1p20f;    // and beyond this maximum of scores
 constexpr int kMostUp = 60;              // the first ones are made about 1, by 2^60 at most
 
 template <int DK_, int DV_, int NB_, typename T_>
@@ -476,7 +477,10 @@ struct Decode4Math {
 #pragma unroll
     for (int i = 0; i < GV; ++i)
       if (mul[i] != 0.f) least = fminf(least, s[i]), top = fmaxf(top, s[i]);  // else nothing but zeros so far
-    if (!(most < kMostScale) || (top > 0.f && least < most * kApart)) asm volatile("st.shared.u32 [%0], %1;" ::"r"(area + 1168), "r"(0x3f800000) : "memory");
+    if (!(most < kMostScale) || (top > 0.f && least < most * kApart)) set_beyond(area);
+  }
+  static __device__ __forceinline__ void set_beyond(uint32_t area) {
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(area + 1168), "f"(1.f) : "memory");
   }
 
   // The step's scales as the products take them, a token per lane: area [32] keys', then values'.
@@ -623,6 +627,9 @@ struct Decode4Math {
           x = fmaxf(x, __shfl_xor_sync(~0u, x, 16));
           // Before the first token the maximum is -infinity: what is multiplied then is 0.
           const float was = kWeightBits - neg[nb][e], mn = fmaxf(was, x);
+          // Without a cap the exponent takes a score before its rounding, the maximum after it: more apart than f16 has room
+          // for, where scores are large.
+          if (DIRECT && mn > kNegInf && !(fabsf(mn) <= kMostScore)) set_beyond(area);
           const float root = was == kNegInf ? 1.f : exp2_approx(0.5f * (was - mn));
           f[nb][e] = root * root;
           neg[nb][e] = kWeightBits - mn;

@@ -103,7 +103,7 @@ def test_an_outlier_in_one_group(gpu, power, at, low, copies, wide, dtype):
 # ------------------------------------------------------------------ scores
 @DTYPES
 @WAYS
-@pytest.mark.parametrize("cap", [30.0])
+@pytest.mark.parametrize("cap", [0.0, 30.0])
 @pytest.mark.parametrize("size", [100, 40, 0, -100], ids=lambda e: f"keys2^{e}")
 def test_heads_of_different_sizes(gpu, size, cap, wide, dtype):
     """A head whose scores go to 2^120 beside heads of ordinary scores, whatever the keys' size.  Queries of one dim of
@@ -118,3 +118,25 @@ def test_heads_of_different_sizes(gpu, size, cap, wide, dtype):
     got = run(q, cache, ints([n, n]), scale=0.125, softcap=cap)
     sync_check()
     ref.check(got, ref.decode(q, k, v, place, [n, n], 0.125, softcap=cap), v, dtype)
+
+
+@DTYPES
+@WAYS
+@pytest.mark.parametrize("copies", [1, 150], ids=["alone", "walk"])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("power", [4, 12, 19, 20, 21, 24, 31, 33, 40, 80, 119], ids=lambda e: f"2^{e}")
+def test_scores_of_any_size(gpu, power, sign, copies, wide, dtype):
+    """Scores of up to 2^power, exact as above, all of one sign: the largest one's token is the result, or tokens of equal scores
+    are."""
+    n, D = 300, 64
+    x, y = (ref.randn(2, n, 1, D, seed=s, dtype=F32, device="cuda") for s in (6, 7))
+    x = (x.abs() + 0.5) * sign
+    cache, k, v, place = stored(x.to(BF16), y.to(BF16), copies, wide)
+    q = torch.zeros(2, 4, D, dtype=F32, device="cuda")
+    for h in range(4):
+        q[:, h, 17 + h] = 1.375 * 2.0 ** power
+    q = q.to(dtype)
+    want = ref.decode(q, k, v, place, [n, n], 0.125).repeat(copies, 1, 1)
+    got = run(q.repeat(copies, 1, 1), cache, ints([n] * 2 * copies), scale=0.125)
+    sync_check()
+    ref.check(got, want, v, dtype)

@@ -30,10 +30,11 @@
 // the largest exponent cut off, toward zero, and a subnormal's exponent counts as
 // 2^-14: a step's sums keep 15 bits below their largest term, besides the 11 of a
 // weight.  For fp32 that would show, so there queries are two whole numbers of at
-// most 2^11 on a common grid per head (hi + lo 2^-12, 24 bits below the largest
-// element), whose products and sums are exact; weights are sums of two f16
-// numbers (22 bits), codes are made f16 numbers of their own size, and a step's
-// products are added to O by FADDs.
+// most 2^11 on a common grid per head and group (hi + lo 2^-12, 24 bits below the
+// group's largest element, where that is 2^-20 of the head's or more), whose
+// products and sums are exact; weights are sums of two f16 numbers (22 bits),
+// codes are made f16 numbers of their own size, and a step's products are added
+// to O by FADDs.
 //
 // Measured: 16 tokens of a key head take 377 instructions, half the schedulers'
 // slots are filled, and neither memory nor a pipe is: eight sequences of up to
@@ -84,6 +85,7 @@ __device__ __forceinline__ float lds_f(uint32_t at) {
   asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
   return v;
 }
+__device__ __forceinline__ void sts_f(uint32_t at, float v) { asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory"); }
 __device__ __forceinline__ void sts128(uint32_t at, float4 v) {
   asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
 }
@@ -173,6 +175,7 @@ constexpr uint64_t kDrainNs = 20000000;  // a copy in flight behind a wait that 
 constexpr int kWeightBits = 7;           // weights times scales go up to 2^15: f16's range, 2^8 above their running maximum
 constexpr float kLeastScale = 0x1p-80f;  // of a token, beside its group's first: below it counts as this
 constexpr float kMostScale = 0x1p100f;   // and from here on redo() has to do it
+constexpr int kThin = 20;                // a group of queries that is 2^-20 of its head's largest has all its bits
 constexpr float kMostScore = 0x1p20f;    // and beyond this maximum of scores
 constexpr int kMostUp = 60;              // the first ones are made about 1, by 2^60 at most
 
@@ -263,26 +266,37 @@ struct Decode4Math {
     const int row = (lane & 7) + 8 * ((lane >> 3) & 1);
     k_src = row * S::kKeyBytes + (((lane >> 4) ^ swizzle4<S::kKeyBytes>(row)) * 16);
     v_src = row * S::kValBytes + (((lane >> 4) ^ swizzle4<S::kValBytes>(row)) * 16);
-    if (lane == 0) sts128(area + 1152, make_float4(0.f, 0.f, 0.f, 0.f));
+    if (lane == 0) sts128(area + 1152, make_float4(0.f, 0.f, 0.f, 0.f)), sts_f(area + 1172, __builtin_huge_valf());
     __syncwarp();
-    int exponent[NB], top = -1000;
+    int exponent[NB], top = -1000, thin = -1000;
     float sums[S::kParts][GK][NB];
     constexpr int kBits = S::kParts == 2 ? 11 : 15;  // queries go up to 2^kBits
     constexpr int kCodeBits = 24;                   // codes are c + 8 times 2^-kCodeBits
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
-      float x[GK][8], big = 0.f;
+      float x[GK][8], big = 0.f, of[GK];  // of: a group's largest (bf16: of this lane's dims)
 #pragma unroll
-      for (int i = 0; i < GK; ++i)
+      for (int i = 0; i < GK; ++i) {
+        of[i] = 0.f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           x[i][e] = to_f32(raw.x[nb][i][e]);
-          big = fmaxf(big, fabsf(x[i][e]));
+          of[i] = fmaxf(of[i], fabsf(x[i][e]));
         }
-      big = fmaxf(big, __shfl_xor_sync(~0u, big, 1));
-      big = fmaxf(big, __shfl_xor_sync(~0u, big, 2));
-      // below 2^e2; 0 for what is no number
-      const int e2 = big > 0.f && big < __builtin_huge_valf() ? max(static_cast<int>(__float_as_uint(big) >> 23), 1) - 126 : 0;
+        if constexpr (S::kParts == 2) {
+          of[i] = fmaxf(of[i], __shfl_xor_sync(~0u, of[i], 1));
+          of[i] = fmaxf(of[i], __shfl_xor_sync(~0u, of[i], 2));
+        }
+        big = fmaxf(big, of[i]);
+      }
+      if constexpr (S::kParts == 1) {
+        big = fmaxf(big, __shfl_xor_sync(~0u, big, 1));
+        big = fmaxf(big, __shfl_xor_sync(~0u, big, 2));
+      }
+      auto above = [](float m) {  // m is below 2^above; 0 for what is no number
+        return m > 0.f && m < __builtin_huge_valf() ? max(static_cast<int>(__float_as_uint(m) >> 23), 1) - 126 : 0;
+      };
+      const int e2 = above(big);
       const float p1 = pow2((kBits - e2) / 2), p2 = pow2(kBits - e2 - (kBits - e2) / 2);
       exponent[nb] = e2 - kBits;
       if (big > 0.f) top = max(top, exponent[nb]);
@@ -291,6 +305,8 @@ struct Decode4Math {
         float y[8], sum[S::kParts] = {};
 #pragma unroll
         for (int e = 0; e < 8; ++e) y[e] = x[i][e] * p1 * p2;
+        const int below = of[i] > 0.f && big < __builtin_huge_valf() ? e2 - above(of[i]) : 0;  // the head's largest
+        if (below > kThin) thin = max(thin, e2);
         if constexpr (S::kParts == 1) {
           uint32_t qf[4];
 #pragma unroll
@@ -303,14 +319,17 @@ struct Decode4Math {
           if (threadIdx.x < 32) q_area[(i * NB + nb) * 32 + lane] = make_uint4(qf[0], qf[1], qf[2], qf[3]);
         } else {
           uint32_t qf[2][4];
+          const float up = pow2(min(below, kThin)), down = pow2(-min(below, kThin));
+#pragma unroll
+          for (int e = 0; e < 8; ++e) y[e] *= up;
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            const float unit = r & 1 ? 0.0625f : 1.f;
+            const float unit = r & 1 ? 0.0625f * down : down;
             const float a0 = rintf(y[r]), a1 = rintf(y[r + 4]), b0 = rintf((y[r] - a0) * 0x1p12f), b1 = rintf((y[r + 4] - a1) * 0x1p12f);
             qf[0][r] = half2_bits(a0 * unit, a1 * unit);
             qf[1][r] = half2_bits(b0 * unit, b1 * unit);
-            sum[0] += a0 + a1;
-            sum[1] += b0 + b1;
+            sum[0] += (a0 + a1) * down;
+            sum[1] += (b0 + b1) * down;
           }
 #pragma unroll
           for (int p = 0; p < 2; ++p)
@@ -329,6 +348,13 @@ struct Decode4Math {
     // so that neither leaves fp32's range where the scores do not.
     const int k_exp = max(top + kCodeBits - 60, 0);
     k_mul = pow2(k_exp);
+    // A group whose queries are that far below their head's largest is off by 2^-36 of it (fp32: 2^-44) at most, which shows in
+    // a score only where its keys are large: beyond this scale.
+    if (__any_sync(~0u, thin != -1000)) {
+      thin = __reduce_max_sync(~0u, thin);
+      if (lane == 0) sts_f(area + 1172, 0x1p16f / a.scale * pow2(min(-thin, 126)) * k_mul);
+      __syncwarp();
+    }
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
@@ -479,9 +505,7 @@ struct Decode4Math {
       if (mul[i] != 0.f) least = fminf(least, s[i]), top = fmaxf(top, s[i]);  // else nothing but zeros so far
     if (!(most < kMostScale) || (top > 0.f && least < most * kApart)) set_beyond(area);
   }
-  static __device__ __forceinline__ void set_beyond(uint32_t area) {
-    asm volatile("st.shared.f32 [%0], %1;" ::"r"(area + 1168), "f"(1.f) : "memory");
-  }
+  static __device__ __forceinline__ void set_beyond(uint32_t area) { sts_f(area + 1168, 1.f); }
 
   // The step's scales as the products take them, a token per lane: area [32] keys', then values'.
   template <bool FULL>
@@ -495,7 +519,9 @@ struct Decode4Math {
     float v_mul[4] = {mul.x, mul.y, mul.z, mul.w};
     bool fresh = false;
     if (unset) {
-      unset = false;
+      const float most_key = lds_f(area + 1172);  // of a group of queries far below their head's largest
+      unset = most_key < __builtin_huge_valf();
+      if (fmaxf(fmaxf(k.x, k.y), fmaxf(k.z, k.w)) > most_key) set_beyond(area);
 #pragma unroll
       for (int i = 0; i < GV; ++i) {
         if (v_mul[i] != 0.f || i * kGroup4 >= a.dv) continue;
@@ -513,7 +539,7 @@ struct Decode4Math {
       most = fmaxf(most, vs[i]);  // not NaN
     }
     if (fresh) ask(vs, v_mul, most, area);
-    asm volatile("st.shared.f32 [%0], %1;" ::"r"(area + 1024 + 4 * lane), "f"(most) : "memory");
+    sts_f(area + 1024 + 4 * lane, most);
     v = make_float4(vs[0], vs[1], vs[2], vs[3]);
     if constexpr (S::kParts == 2) {
       sts128(area + 512 + 16 * lane, v);
@@ -836,7 +862,7 @@ __global__ void __launch_bounds__(kDecodeThreads, S::kCtasPerSm)
   StageRing<kStages> flight;
   bool alive = true;    // no wait has run out: else the warp copies and computes nothing more
 
-  if (lane == 0) sts128(area + 1168, make_float4(0.f, 0.f, 0.f, 0.f));
+  if (lane == 0) sts_f(area + 1168, 0.f);
 
   while (at < end) {
     Piece pc;

@@ -140,3 +140,21 @@ def test_scores_of_any_size(gpu, power, sign, copies, wide, dtype):
     got = run(q.repeat(copies, 1, 1), cache, ints([n] * 2 * copies), scale=0.125)
     sync_check()
     ref.check(got, want, v, dtype)
+
+
+@DTYPES
+@WAYS
+@pytest.mark.parametrize("power", [3, 8, 14, 20, 28, 40, 60], ids=lambda e: f"2^{e}")
+def test_queries_small_where_keys_are_large(gpu, power, wide, dtype):
+    """A group of dims whose queries are 2^-power of the others' and whose keys 2^power: it has as much to say in a score."""
+    n, D = 200, 96
+    x, y = (ref.randn(2, n, 1, D, seed=s, dtype=F32, device="cuda") for s in (8, 9))
+    q = ref.randn(2, 5, D, seed=10, dtype=F32, device="cuda")
+    x[..., 32:64] *= 2.0 ** power
+    q[..., 32:64] *= 2.0 ** -power
+    q[:, 2, 64:] = 0
+    x, y, q = x.to(BF16), y.to(BF16), q.to(dtype)
+    cache, k, v, place = stored(x, y, 1, wide)
+    got = run(q, cache, ints([n, n]), scale=0.3)
+    sync_check()
+    ref.check(got, ref.decode(q, k, v, place, [n, n], 0.3), v, dtype)

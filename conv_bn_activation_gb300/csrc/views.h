@@ -57,6 +57,19 @@ inline bool apart(long long period, long long a, long long b, long long d) {
   return at >= a && at + b <= period;
 }
 
+// Whether two views of the same strides, b's first byte d behind a's, lie with
+// their heads' rows between each other's ([..., head, part, dim] buffers): rows
+// apart in a token, and a token of both and a sequence of both no wider than
+// their strides.
+inline bool heads_between(const Region& a, const Region& b, long long d) {
+  auto stride = [](int na, long long sa, int nb, long long sb) { return na == 1 ? sb : nb == 1 || sa == sb ? sa : -1LL; };
+  const long long sh = stride(a.heads, a.sh, b.heads, b.sh), sl = stride(a.len, a.sl, b.len, b.sl), sb = stride(a.batch, a.sb, b.batch, b.sb);
+  if (sh <= 0 || !apart(sh, a.row, b.row, d)) return false;
+  auto both = [&](long long in_a, long long in_b) { return std::max(in_a, d + in_b) - std::min(0LL, d); };
+  if ((a.len > 1 || b.len > 1) && both(a.token(), b.token()) > sl) return false;
+  return (a.batch == 1 && b.batch == 1) || both(a.seq(), b.seq()) <= sb;
+}
+
 // True if the views may share a byte. Views whose ranges interleave share none
 // if one's rows or sequences lie in the gaps between the other's, at the same
 // strides (slices of a wider buffer), or one lies in a single gap.
@@ -64,6 +77,7 @@ inline bool overlap(const Region& a, const Region& b) {
   if (a.empty() || b.empty()) return false;
   const long long d = static_cast<long long>(b.at - a.at);
   if (d >= a.all() || -d >= b.all()) return false;
+  if (heads_between(a, b, d)) return false;
   auto rows_repeat = [](const Region& t) { return t.batch == 1 || (t.sl > 0 && t.sb % t.sl == 0); };
   if (a.sl == b.sl && rows_repeat(a) && rows_repeat(b) && apart(a.sl, a.token(), b.token(), d)) return false;
   if (a.sb == b.sb && apart(a.sb, a.seq(), b.seq(), d)) return false;

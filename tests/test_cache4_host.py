@@ -255,3 +255,63 @@ def test_binding_refuses_another_device_than_the_current_one(cblib, monkeypatch)
         monkeypatch.setattr(torch.cuda, "current_device", lambda: current)
         with pytest.raises(wrong):
             cblib.norm_rotate(k, v, None, cblib.Rotation(norm=True), stream=on.stream)
+
+
+@pytest.mark.parametrize("dtype", [0, 1], ids=["f32", "bf16"])
+def test_heads_that_lie_between_anothers(cblib, dtype):
+    """Queries, keys and values side by side for each head ([B, L, H, 3, D]): views that share no byte are no overlap."""
+    e = 2 if dtype else 4
+
+    def at(part, **kw):
+        a = dict(h=4, data=DATA + part * 64 * e, sh=3 * 64, sl=4 * 3 * 64, dtype=dtype)
+        a.update(kw)
+        return heads(cblib, **a)
+
+    in_place = rotate(cblib, q=at(0), k=at(1), q_out=at(0), k_out=at(1))
+    assert in_place not in (cblib.ERR_INVALID_ARG, cblib.ERR_ALIGNMENT, cblib.ERR_UNSUPPORTED)  # OK, or no GPU here
+    I = cblib.ERR_INVALID_ARG
+    assert rotate(cblib, q=at(0), k=at(1, data=DATA + 32 * e), q_out=at(0), k_out=at(1, data=DATA + 32 * e)) == I  # half over the queries
+    assert rotate(cblib, q=at(0), k=at(1, sh=2 * 64), q_out=at(0), k_out=at(1, sh=2 * 64)) == I  # another step of heads
+    gap = dict(sl=4 * 3 * 64 + 64)
+    assert rotate(cblib, q=at(0, **gap), k=at(1, **gap), q_out=at(0, **gap), k_out=at(1, **gap)) not in (I, cblib.ERR_UNSUPPORTED)
+    for near in (dict(sl=3 * 3 * 64), dict(sb=64 * 3 * 64)):  # tokens, sequences into which the heads of others reach
+        assert rotate(cblib, q=at(0, **near), k=at(1, **near), q_out=heads(cblib, data=DATA + 2 * FAR, dtype=dtype), k_out=at(0, **near)) == I
+    one = dict(h=1)
+    k = at(1, **one)
+    assert rotate(cblib, q=at(0), k=k, q_out=at(0), k_out=k) not in (I, cblib.ERR_ALIGNMENT, cblib.ERR_UNSUPPORTED)
+    far = dict(h=2, sh=2 * 64, sl=2 * 2 * 64, dtype=dtype)
+    k, v = heads(cblib, data=DATA + (1 << 26), **far), heads(cblib, data=DATA + (1 << 26) + 64 * e, **far)
+    assert tokens(cblib, "read", k=k, v=v) not in (I, cblib.ERR_ALIGNMENT, cblib.ERR_UNSUPPORTED)
+
+
+def test_views_that_are_taken_share_no_byte(cblib):
+    """Small views at random strides: what is not refused as an overlap has no element twice."""
+    import random
+
+    rng = random.Random(5)
+
+    def drawn():
+        d, h, ln, b = rng.choice((2, 4)), rng.randint(1, 3), rng.randint(1, 3), rng.randint(1, 2)
+        pick = lambda low: rng.choice((low, low + 2, 2 * low, 3 * low, rng.randint(0, 60)))  # noqa: E731
+        sh = pick(d)
+        sl = pick(max(sh * h, 1))
+        return dict(b=b, l=ln, h=h, d=d, sh=sh, sl=sl, sb=pick(max(sl * ln, 1)))
+
+    def bytes_of(v, at):
+        return [at + 4 * (b * v["sb"] + i * v["sl"] + h * v["sh"] + d) for b in range(v["b"]) for i in range(v["l"]) for h in range(v["h"])
+                for d in range(v["d"])]
+
+    taken = {True: 0, False: 0}
+    for _ in range(6000):
+        v = drawn()
+        w = dict(drawn(), b=v["b"], l=v["l"], h=v["h"], d=v["d"]) if rng.random() < 0.3 else v
+        at = DATA + 4 * rng.randint(0, 40)
+        st = rotate(cblib, q=heads(cblib, dtype=0, **v), q_out=heads(cblib, dtype=0, data=at, **w), k=None, k_out=None,
+                    rule=rule(cblib, rotary=0))
+        out = bytes_of(w, at)
+        same = at == DATA and w == v
+        free = len(set(out)) == len(out) and (same or not set(out) & set(bytes_of(v, DATA)))
+        if st != cblib.ERR_INVALID_ARG:
+            assert free, (v, w, at)
+        taken[st != cblib.ERR_INVALID_ARG] += free
+    assert taken[True] > 4 * taken[False] > 0  # most of those that could be taken are

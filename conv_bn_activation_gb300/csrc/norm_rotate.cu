@@ -216,8 +216,8 @@ __global__ void __launch_bounds__(32 * kWarps, kPiecesCtas) rotate_pieces_kernel
     r.head += advance;
     if (r.head - slot >= heads) r.head = first, r.token += step;
   };
-  // Of this lane's pairs: z1 = inv (x1 (w1 cos) - x2 (w2 sin)), z2 = inv (x2 (w2 cos) + x1 (w1 sin)); adjacent pairs as
-  // (z1, z2) = inv ((x1, x2) (w1 cos, w2 cos) + (x2, x1) (-w2 sin, w1 sin)).
+  // Of this lane's pairs, y = inv x (first: with a large weight a product could leave fp32's range): z1 = y1 (w1 cos) - y2
+  // (w2 sin), z2 = y2 (w2 cos) + y1 (w1 sin); adjacent pairs as (z1, z2) = (y1, y2) (w1 cos, w2 cos) + (y2, y1) (-w2 sin, w1 sin).
   f2 c1[H], c2[H], s1[H], s2[H];
   auto work = [&](const Place& r, int at) {
     if (r.head == first) {
@@ -262,16 +262,16 @@ __global__ void __launch_bounds__(32 * kWarps, kPiecesCtas) rotate_pieces_kernel
     auto other = [&](f2 y, int i) { return still && i >= half ? pack2(0.f, 0.f) : y; };
 #pragma unroll
     for (int i = 0; i < H; ++i) {
-      const f2 y1 = x[i], y2 = x[H + i];
+      const f2 y1 = mul2(x[i], inv), y2 = mul2(x[H + i], inv);
       if constexpr (ADJ) {
         float u, w;
         unpack2(y1, u, w);
-        x[i] = mul2(fma2(other(pack2(w, u), p0 / 2 + i), s1[i], mul2(y1, c1[i])), inv);
+        x[i] = fma2(other(pack2(w, u), p0 / 2 + i), s1[i], mul2(y1, c1[i]));
         unpack2(y2, u, w);
-        x[H + i] = mul2(fma2(other(pack2(w, u), p1 / 2 + i), s2[i], mul2(y2, c2[i])), inv);
+        x[H + i] = fma2(other(pack2(w, u), p1 / 2 + i), s2[i], mul2(y2, c2[i]));
       } else {
-        x[i] = mul2(fma2(other(y2, sub * E), s2[i], mul2(y1, c1[i])), inv);
-        x[H + i] = mul2(fma2(other(y1, sub * E), s1[i], mul2(y2, c2[i])), inv);
+        x[i] = fma2(other(y2, sub * E), s2[i], mul2(y1, c1[i]));
+        x[H + i] = fma2(other(y1, sub * E), s1[i], mul2(y2, c2[i]));
       }
     }
     if (mine && r.head < heads) {

@@ -12,6 +12,7 @@ using namespace cb;
 namespace {
 
 constexpr int kMaxAxes = 8;
+constexpr int kMaxHeads = 65536;  // heads times dims, items and lanes' words are counted in 32 bits
 
 long long code_bytes(int dim) { return (dim + 1) / 2; }
 long long scale_bytes(int dim) { return 4LL * ((dim + 63) / 64); }
@@ -125,7 +126,7 @@ cb_status check_tokens(const cb_heads* k, const cb_heads* v, const cb_paged_cach
   if (k->batch != cache->batch || v->batch != cache->batch || k->len != v->len) return CB_ERR_INVALID_ARG;
   if (k->heads != cache->heads || v->heads != cache->heads) return CB_ERR_INVALID_ARG;
   if (k->dim != cache->dim_k || v->dim != cache->dim_v || k->dtype != v->dtype) return CB_ERR_INVALID_ARG;
-  if (cache->dim_k > kMaxDim || cache->dim_v > kMaxDim) return CB_ERR_UNSUPPORTED;
+  if (cache->dim_k > kMaxDim || cache->dim_v > kMaxDim || cache->heads > kMaxHeads) return CB_ERR_UNSUPPORTED;
   if (!elem_aligned(k->data, k->dtype) || !elem_aligned(v->data, v->dtype) || !aligned(cache)) return CB_ERR_ALIGNMENT;
   return CB_OK;
 }
@@ -133,7 +134,7 @@ cb_status check_tokens(const cb_heads* k, const cb_heads* v, const cb_paged_cach
 cb_status check_decode(const cb_heads* q, const cb_paged_cache4* cache) {
   if (!heads_ok(q) || !cache_ok(cache)) return CB_ERR_INVALID_ARG;
   if (q->len != 1 || q->batch != cache->batch || q->dim != cache->dim_k || q->heads % cache->heads != 0) return CB_ERR_INVALID_ARG;
-  if (cache->dim_k > kMaxDim || cache->dim_v > kMaxDim || q->batch > kMaxBatch) return CB_ERR_UNSUPPORTED;
+  if (cache->dim_k > kMaxDim || cache->dim_v > kMaxDim || q->batch > kMaxBatch || q->heads > kMaxHeads) return CB_ERR_UNSUPPORTED;
   return CB_OK;
 }
 
@@ -184,6 +185,7 @@ cb_status cb_norm_rotate(const cb_heads* q, const cb_heads* k, const cb_head_rul
   if (rule->axes < 1 || rule->axes > kMaxAxes || rule->pos_stride_axis < 0 || rule->pos_stride_b < 0) return CB_ERR_INVALID_ARG;
   if (rule->rotary > 0 && (!rule->freq || (!rule->pos && !empty(q)))) return CB_ERR_INVALID_ARG;
   if (q->dim > kMaxDim || static_cast<long long>(q->batch) * q->len >= (1LL << 31)) return CB_ERR_UNSUPPORTED;
+  if (q->heads > kMaxHeads || (k && k->heads > kMaxHeads)) return CB_ERR_UNSUPPORTED;
   for (int i = 0; i < views; ++i)
     if (!elem_aligned(in[i]->data, q->dtype) || !elem_aligned(out[i]->data, q->dtype)) return CB_ERR_ALIGNMENT;
   if (empty(q)) return CB_OK;

@@ -535,8 +535,9 @@ typedef struct {
  * the same shape, either the very same view (in place) or overlapping no view
  * of the call; no two of an output's rows overlap (its strides nest).  All of
  * one dtype, aligned to it; arithmetic in fp32, rounded once.  dim at most
- * 128, rotary even, fewer than 2^31 tokens (else CB_ERR_UNSUPPORTED).  L and
- * batch may be 0.  One kernel, no workspace.
+ * 128, rotary even, fewer than 2^31 tokens, at most 65536 heads of a kind
+ * (else CB_ERR_UNSUPPORTED).  L and batch may be 0.  One kernel, no
+ * workspace.
  */
 cb_status cb_norm_rotate(const cb_heads* q, const cb_heads* k, const cb_head_rule* rule, cb_heads* q_out,
                          cb_heads* k_out, void* stream);
@@ -573,7 +574,8 @@ typedef struct {
 
 /*
  * cb_cache_append for a 4-bit cache: k_new and v_new are fp32 or bf16 (both
- * the same); dim_k and dim_v at most 128 (else CB_ERR_UNSUPPORTED).
+ * the same); dim_k and dim_v at most 128, at most 65536 heads (else
+ * CB_ERR_UNSUPPORTED).
  */
 cb_status cb_cache4_append(const cb_heads* k_new, const cb_heads* v_new, const int* pos, const int* count,
                            const cb_paged_cache4* cache, void* stream);
@@ -594,7 +596,7 @@ cb_status cb_cache4_read(const cb_paged_cache4* cache, const int* first, const i
 
 /*
  * cb_attention_decode over a 4-bit cache: the same arguments and rule, on the
- * values c * s; no two rows of out overlap.  q and out are both fp32 or both
+ * values c * s; no two rows of out overlap; at most 65536 query heads.  q and out are both fp32 or both
  * bf16.  Codes of dims that are multiples of 8 go to warp-level MMAs: bf16
  * queries and weights times scales are rounded to 11 bits (fp16, within its
  * range by powers of two: weights times scales below 2^-31 of their largest

@@ -315,3 +315,22 @@ def test_views_that_are_taken_share_no_byte(cblib):
             assert free, (v, w, at)
         taken[st != cblib.ERR_INVALID_ARG] += free
     assert taken[True] > 4 * taken[False] > 0  # most of those that could be taken are
+
+
+def test_counts_of_heads_that_fit_the_kernels(cblib):
+    """Heads are counted in 32 bits, with their dims and both kinds together: more than 65536 are refused, before anything
+    is worked out from them."""
+    U, big = cblib.ERR_UNSUPPORTED, 65537
+    huge = 1 << 40
+    for h in (big, (1 << 31) - 1):
+        q, out = (heads(cblib, b=1, l=1, h=h, d=8, data=DATA + i * huge) for i in (0, 1))
+        k, k_out = (heads(cblib, b=1, l=1, h=1, d=8, data=DATA + i * huge) for i in (2, 3))
+        assert rotate(cblib, q=q, k=k, q_out=out, k_out=k_out, rule=rule(cblib, rotary=8)) == U
+        assert rotate(cblib, q=k, k=q, q_out=k_out, k_out=out, rule=rule(cblib, rotary=8)) == U
+        c = cblib.CbPagedCache4(DATA + 4 * huge, DATA + 5 * huge, DATA + 6 * huge, DATA + 7 * huge, 1, 1, h, 8, 8, h * 4, h * 4, 4, h * 4, h * 4,
+                                4, h * 2, h * 2, 2, h * 2, h * 2, 2, DATA, 1, 1, 1)
+        for name in ("append", "read"):
+            assert tokens(cblib, name, k=q, v=out, c=c) == U
+        assert decode(cblib, q=q, c=c, out=out) == U
+        n = ctypes.c_size_t(0)
+        assert cblib.load().cb_attention_decode4_workspace(r(q), r(c), r(n)) == U

@@ -334,3 +334,33 @@ def test_counts_of_heads_that_fit_the_kernels(cblib):
         assert decode(cblib, q=q, c=c, out=out) == U
         n = ctypes.c_size_t(0)
         assert cblib.load().cb_attention_decode4_workspace(r(q), r(c), r(n)) == U
+
+
+def test_every_call_refuses_another_device_than_the_current_one(cblib, monkeypatch):
+    """Attention, the caches and the rotation all launch on the current device; a stream does not change that."""
+    import torch
+    on = OnDevice(monkeypatch, cblib)
+    cblib.heads(torch.zeros(1, 1, 1, 8))  # what the first call sets up
+    monkeypatch.setattr(cblib, "_several", True)
+    u8, bf, B = torch.uint8, torch.bfloat16, 2
+    q, k, v, o = (on.make(B, 3, 4, 64) for _ in range(4))
+    one, out, n = on.make(B, 4, 64), on.make(B, 4, 64), on.make(B, dtype=on.i32)
+    ws, table = on.make(4096, dtype=u8), on.make(B, 3, dtype=on.i32)
+    cache = cblib.PagedCache(on.make(5, 16, 4, 64), on.make(5, 16, 4, 64), table)
+    codes, scales = on.make(5, 16, 4, 32, dtype=u8), on.make(5, 16, 4, 2, dtype=bf)
+    cache4 = cblib.PagedCache4(codes, scales, codes, scales, table)
+    for stream in (None, on.stream):
+        if stream is None:
+            monkeypatch.setattr(cblib, "_raw_stream", lambda device: 0)
+        calls = [lambda: cblib.attention(q, k, v, o, cblib.Score(0.1), stream=stream),
+                 lambda: cblib.cache_append(k, v, cache, n, stream=stream),
+                 lambda: cblib.attention_decode(one, cache, n, out, ws, 0.1, stream=stream),
+                 lambda: cblib.norm_rotate(q, k, None, cblib.Rotation(norm=True), stream=stream),
+                 lambda: cblib.cache4_append(k, v, cache4, n, stream=stream),
+                 lambda: cblib.cache4_read(cache4, k, v, stream=stream),
+                 lambda: cblib.attention_decode4(one, cache4, n, out, ws, 0.1, stream=stream)]
+        for call in calls:
+            for current, wrong in ((0, AssertionError), (1, ValueError)):
+                monkeypatch.setattr(torch.cuda, "current_device", lambda current=current: current)
+                with pytest.raises(wrong):
+                    call()

@@ -715,58 +715,99 @@ struct Share {
 };
 
 // A share from the definition, in fp32 on the CUDA cores, for what the products of f16 weights cannot hold: a token per
-// lane for the scores, four dims per lane for the values, a head at a time.  Results as Decode4Math::store() leaves
-// them.  Weights are taken times 2^-32, so that sums of the largest values stay finite.
+// lane for the scores, four dims per lane for the values, two heads at a time.  Results as Decode4Math::store() leaves
+// them.  Weights are taken times 2^-32, so that sums of the largest values stay finite.  Where every run is done again the
+// cases below take 9 and 14 times as long (582 us, 2833; four heads at a time 432 and 2044, but the main loop, which the
+// compiler then treats otherwise, 204 us, not 198.7).
 template <typename T>
 __device__ __noinline__ void redo(const DecodeArgs& a, const Share w, float* res, int ld, float* ms, float* ls) {
+  constexpr int kAtOnce = 2, kAhead = 8;  // heads; tokens whose values are in flight
   constexpr float kLess = 32.f;
   const int lane = threadIdx.x & 31, dim = 4 * lane;
   const DecodeScore score(a);
-  for (int hd = 0; hd < w.heads; ++hd) {
-    const T* q = static_cast<const T*>(a.q) + w.b * a.qs_b + (w.h0 + hd) * a.qs_h;
-    const float slope = a.slopes ? a.slopes[w.h0 + hd] * kLog2e : 0.f;
-    float m = kNegInf, mu = 0.f, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int h = 0; h < w.heads; h += kAtOnce) {
+    const int heads = min(kAtOnce, w.heads - h);  // the others repeat the last one
+    const T* q[kAtOnce];
+    float slope[kAtOnce], m[kAtOnce], mu[kAtOnce], l[kAtOnce], o[kAtOnce][4];
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      const int hd = w.h0 + h + min(i, heads - 1);
+      q[i] = static_cast<const T*>(a.q) + w.b * a.qs_b + hd * a.qs_h;
+      slope[i] = a.slopes ? a.slopes[hd] * kLog2e : 0.f;
+      m[i] = kNegInf, mu[i] = l[i] = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+    }
     for (int step = 0; step < w.steps; ++step) {
       const unsigned j = w.base + step * (kDecodeWarps * 32) + lane;
       int page = -1, slot = 0;
       if (lane < w.take && j >= w.first && j < w.limit) page = token_page(a, w.b, static_cast<int>(j), &slot);
-      float x[1][1] = {{0.f}};
+      float x[kAtOnce][1] = {}, p[kAtOnce];
       if (page >= 0) {
         const uint8_t* codes = key_codes4(a.cache, page, slot, w.hk);
         const uint16_t* scales = key_scales4(a.cache, page, slot, w.hk);
+#pragma unroll 2
         for (int d = 0; d < a.dk; d += 8) {
           const uint32_t c = *reinterpret_cast<const uint32_t*>(codes + d / 2);
           const float s = bf16_value(scales[d / kGroup4]);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[0][0] = fmaf(to_f32(q[d + e]), (static_cast<int>((c >> (4 * e)) & 15u) - 8) * s, x[0][0]);
+          for (int e = 0; e < 8; ++e) {
+            const float k = (static_cast<int>((c >> (4 * e)) & 15u) - 8) * s;
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) x[i][0] = fmaf(to_f32(q[i][d + e]), k, x[i][0]);
+          }
         }
       }
       score(x);
-      const float y = page < 0 ? kNegInf : fmaf(-slope, static_cast<float>(w.len - 1 - static_cast<int>(j)), x[0][0]);
-      float top = y;
-      for (int i = 16; i; i >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, i));
-      const float was = m;
-      m = fmaxf(m, top), mu = m == kNegInf ? 0.f : m;
-      const float f = exp2_approx(was - mu), p = page < 0 ? 0.f : exp2_approx(y - mu - kLess);
-      float sum = p;
-      for (int i = 16; i; i >>= 1) sum += __shfl_xor_sync(~0u, sum, i);
-      l = fmaf(l, f, sum);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) o[c] *= f;
-      for (unsigned left = __ballot_sync(~0u, page >= 0); left; left &= left - 1) {
-        const int t = __ffs(left) - 1, pg = __shfl_sync(~0u, page, t), sl = __shfl_sync(~0u, slot, t);
-        const float pt = __shfl_sync(~0u, p, t);
-        if (dim < a.dv) {
-          const unsigned c = *reinterpret_cast<const uint16_t*>(value_codes4(a.cache, pg, sl, w.hk) + dim / 2);
-          const float s = bf16_value(value_scales4(a.cache, pg, sl, w.hk)[dim / kGroup4]);
+      for (int i = 0; i < kAtOnce; ++i) {
+        const float y = page < 0 ? kNegInf : fmaf(-slope[i], static_cast<float>(w.len - 1 - static_cast<int>(j)), x[i][0]);
+        float top = y;
+        for (int n = 16; n; n >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, n));
+        const float was = m[i];
+        m[i] = fmaxf(m[i], top), mu[i] = m[i] == kNegInf ? 0.f : m[i];
+        const float f = exp2_approx(was - mu[i]);
+        p[i] = page < 0 ? 0.f : exp2_approx(y - mu[i] - kLess);
+        float sum = p[i];
+        for (int n = 16; n; n >>= 1) sum += __shfl_xor_sync(~0u, sum, n);
+        l[i] = fmaf(l[i], f, sum);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o[e] = fmaf(pt, (static_cast<int>((c >> (4 * e)) & 15u) - 8) * s, o[e]);
+        for (int e = 0; e < 4; ++e) o[i][e] *= f;
+      }
+      if (!__any_sync(~0u, page >= 0)) continue;
+      for (int t0 = 0; t0 < 32; t0 += kAhead) {
+        unsigned c[kAhead], s[kAhead];
+#pragma unroll
+        for (int t = 0; t < kAhead; ++t) {
+          const int pg = __shfl_sync(~0u, page, t0 + t), sl = __shfl_sync(~0u, slot, t0 + t);
+          c[t] = s[t] = 0;  // a token that does not exist: its weight is 0 too
+          if (pg >= 0 && dim < a.dv) {
+            c[t] = *reinterpret_cast<const uint16_t*>(value_codes4(a.cache, pg, sl, w.hk) + dim / 2);
+            s[t] = value_scales4(a.cache, pg, sl, w.hk)[dim / kGroup4];
+          }
+        }
+#pragma unroll
+        for (int t = 0; t < kAhead; ++t) {
+          float v[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = (static_cast<int>((c[t] >> (4 * e)) & 15u) - 8) * bf16_value(s[t]);
+#pragma unroll
+          for (int i = 0; i < kAtOnce; ++i) {
+            const float pt = __shfl_sync(~0u, p[i], t0 + t);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[i][e] = fmaf(pt, v[e], o[i][e]);
+          }
         }
       }
     }
-    if (lane == 0) ms[hd] = l == 0.f ? kNegInf : mu + kLess + log2f(l), ls[hd] = l == 0.f ? 0.f : l == l ? 1.f : l;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    if (dim < a.dv) *reinterpret_cast<float4*>(res + hd * ld + dim) = make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      if (i >= heads) break;
+      const int hd = h + i;
+      if (lane == 0) ms[hd] = l[i] == 0.f ? kNegInf : mu[i] + kLess + log2f(l[i]), ls[hd] = l[i] == 0.f ? 0.f : l[i] == l[i] ? 1.f : l[i];
+      const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
+      if (dim < a.dv) *reinterpret_cast<float4*>(res + hd * ld + dim) = make_float4(o[i][0] * inv, o[i][1] * inv, o[i][2] * inv, o[i][3] * inv);
+    }
   }
 }
 

@@ -596,15 +596,18 @@ cb_status cb_cache4_read(const cb_paged_cache4* cache, const int* first, const i
 
 /*
  * cb_attention_decode over a 4-bit cache: the same arguments and rule, on the
- * values c * s; no two rows of out overlap; at most 65536 query heads.  q and out are both fp32 or both
- * bf16.  Codes of dims that are multiples of 8 go to warp-level MMAs: bf16
- * queries and weights times scales are rounded to 11 bits (fp16, within its
- * range by powers of two: weights times scales below 2^-31 of their largest
- * are lost), sums are fp32; for fp32 the products keep 22 bits and more.
- * Where values' sizes differ by so much, between tokens or groups, that those
- * roundings would be more than that of a group's own values, the tokens
- * around are done in fp32 on the CUDA cores, at a tenth of the speed or less.
- * All else is fp32 on the CUDA cores.
+ * values c * s; no two rows of out overlap; at most 65536 query heads.  q and
+ * out are both fp32 or both bf16.  Codes of dims that are multiples of 8 go to
+ * warp-level MMAs.  bf16: weights times scales are rounded to 11 bits (fp16,
+ * within its range by powers of two); scores are sums that keep 14 bits below
+ * a group's largest query element times its keys' scale.  fp32: weights and
+ * products keep 22 bits and more.  Sums over tokens are fp32.  Weights times
+ * scales below 2^-31 of the largest are lost, at most 2^-20 (fp32: 2^-24) of a
+ * group's own largest.  Where the sizes of values (between a token's groups,
+ * or far along a sequence), of scores (2^20 and more) or of keys whose queries
+ * are small go beyond what those roundings hold for each group by itself, the
+ * tokens that share a CTA with them are done in fp32 on the CUDA cores, in up
+ * to 15 times the time.  All else is fp32 on the CUDA cores.
  */
 cb_status cb_attention_decode4_workspace(const cb_heads* q, const cb_paged_cache4* cache, size_t* bytes);
 cb_status cb_attention_decode4(const cb_heads* q, const cb_paged_cache4* cache, const int* length, const int* first,

@@ -11,8 +11,11 @@
 // looks the token's page up.  16 prompts of up to 2048 tokens, 8 heads of 128
 // bf16: stored in 44 us, of 19 at the copy rate (bound by instructions: 0.70 of the
 // issue slots, about 100 for a word and the rest a token's addresses), 16384 such
-// tokens read in 15.6, of 12.7.  One warp per head (the kernels for other rows)
-// took 4 to 6 times as long.
+// tokens read in 18.4, of 12.7 (15.6 where the L2 still holds the codes).  One warp
+// per head (the kernels for other rows) took 4 to 6 times as long.  A lane's words
+// are of one token: with few key heads most lanes have none, and cases for many
+// words go far from their floor (32 maps of 400 tokens, 2 heads of 32, fp32: read
+// in 10.7 us, of 1.1).
 #include "cache4.cuh"
 #include "launch_util.h"
 #include "ptx.cuh"
@@ -22,8 +25,8 @@ namespace cb {
 namespace {
 
 constexpr int kWarps = 4;
-// CTAs for each SM at most.  Counts leave some with little: more than the SM holds (stored and read as above, 6: 73 us, 8:
-// 77, 12: 69, 16: 67.5, 24: 71).  Without counts all have the same: what it holds at once when tokens are read (16 k of them,
+// CTAs for each SM at most, by heads of 128 dims alone, 4 and 8 of them, on codes that the L2 may hold.  Counts leave some
+// with little: more than the SM holds (stored and read as above, 6: 73 us, 8: 77, 12: 69, 16: 67.5, 24: 71).  Without counts all have the same: what it holds at once when tokens are read (16 k of them,
 // 6: 15.7 us, 8: 18.3, 16: 17.7), twice that when they are stored (16 k of 4 heads, 6: 13.5, 12: 14.1, 16: 14.8; 32 k of 8,
 // 6: 52, 12: 47, 16: 49).
 constexpr int kReadCtas = 6;
@@ -278,7 +281,8 @@ cudaError_t launch_words(Kernel kernel, const Args& a, long long ctas, int sms, 
 }
 
 // Eight CTAs' worth of words per SM or fewer: one to a lane, so that a token's heads spread over the GPU; more: four to be
-// stored (two 73 us, eight 73, four 67), eight to be read (16 CTAs: two 23 us, four 17.6, eight 16.9).
+// stored (two 73 us, eight 73, four 67), eight to be read (16 CTAs: two 23 us, four 17.6, eight 16.9); measured with 8
+// heads of 128.
 template <class Args>
 bool few_words(const Args& a, int sms) {
   return static_cast<long long>(a.B) * a.T * a.H * ((a.dk + a.dv) / 8) <= 32LL * kWarps * 8 * sms;

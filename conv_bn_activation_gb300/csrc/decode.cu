@@ -1,6 +1,8 @@
 // Attention of one new token per sequence over a paged cache (cb_attention_decode,
 // cb_attention_decode4): the kernel for caches whose rows are not whole 16-byte
-// pieces (the others take decode_stream.cuh) and the join of split sequences.
+// pieces, or in 4 bits not whole 4-byte words with a row's scales one word, or
+// that have no page (the others take decode_stream.cuh and decode4.cuh), and the
+// join of split sequences.
 //
 // Bound by HBM: every key and value of the batch is read once, and one
 // query's 4 FLOP per element are far below the FMA rate until many heads

@@ -23,9 +23,10 @@
 //    that a large value of no weight takes nothing from the others.  Products
 //    below 2^-31 of the largest are lost; where that, or fp32's range, could
 //    show in a group (its scales far apart from the other groups' or from its
-//    first ones), the run is done again at its end by redo_run(), in fp32 on the
-//    CUDA cores.  Asking costs 1 % (196 -> 198.5 us for the sequences below, 63
-//    -> 63.5 for 64 ragged ones); the same code within the loop over pieces 8 %.
+//    first ones; so with scores and queries, below), the run is done again at its
+//    end by redo_run(), in fp32 on the CUDA cores.  Asking costs 1 % (calls of 196
+//    -> 198.7 us for the sequences below) to 4 % (63 -> 65.3 for 64 ragged ones);
+//    with that code within the loop over pieces the former took 209.
 // The MMAs add 16 products and the sum so far with all that lies 25 bits below
 // the largest exponent cut off, toward zero, and a subnormal's exponent counts as
 // 2^-14: a step's sums keep 15 bits below their largest term, besides the 11 of a
@@ -38,8 +39,9 @@
 //
 // Measured: 16 tokens of a key head take 377 instructions, half the schedulers'
 // slots are filled, and neither memory nor a pipe is: eight sequences of up to
-// 131072 tokens, 8 key heads of 128, in 193 us, 0.69 of the copy rate (the bf16
-// cache's 466).  Three CTAs of three stages take as long as four of two (three with
+// 131072 tokens, 8 key heads of 128, in 196 us, 0.68 of the copy rate (the bf16
+// cache's 466).  The bf16 kernels of 128 dims and 8 heads are held to 128 registers
+// and spill 4 to 60 bytes.  Three CTAs of three stages take as long as four of two (three with
 // one stage less in flight, four with fewer registers than they want).  fp8 MMAs,
 // whose e4m3 subnormals the codes are as well, run as two f16 ones after
 // conversions: 249 us where f16 took 205.
@@ -220,12 +222,13 @@ struct Decode4Math {
   // makes a score's share of them. fp32: of every group and this thread's heads 8 nb + 2 t4 and the one after.
   float offset[NB][2], first[S::kParts == 2 ? 2 : 1][S::kParts == 2 ? GK : 1][NB][2];
   float k_mul, head_mul[NB][2];
-  // The values' scales are taken times v_mul, the power of two that makes a group's first ones about 1 (0: none yet;
-  // unset: of some group).  neg = kWeightBits - maximum of x + log2 of a token's largest scale (+infinity before the
-  // first token): weights are 2^(x + neg).
-  // In shared memory, behind the scales' area.
-  // Behind them, for the whole launch: whether the warp met what this arithmetic does not hold.
+  // The values' scales are taken times v_mul, the power of two that makes a group's first ones about 1 (0: none yet).  Those
+  // lie in shared memory behind the scales' area; behind them whether the warp met what this arithmetic does not hold
+  // (for the whole launch), and the largest scale that a key may have where queries are small (else infinity).  unset:
+  // scales() has something to do for them.
   bool unset;
+  // neg = kWeightBits - maximum of x + log2 of a token's largest scale (+infinity before the first token): weights are
+  // 2^(x + neg).
   float slope[NB][2], neg[NB][2], l[NB][2], o[2 * GV][NB][4];
 
   // This lane's queries: dims 8 t4 .. + 8 of each group of heads 8 nb + g.  Read before the first tokens are looked up.

@@ -179,7 +179,7 @@ __device__ __forceinline__ void note_item(const DecodeArgs& a, const Run& run, c
   a.record[2 * cta + 1] = static_cast<int>(run.owner(p.last) - cta + 1);
 }
 
-// Floats of one partial result: per head m, l, then dv unnormalised sums.
+// Floats of one partial result: per head m, l, then dv sums (from a 4-bit cache divided by their weights, with l 1).
 __host__ __device__ inline size_t part_floats(int heads, int dv) { return static_cast<size_t>(heads) * (dv + 2); }
 
 // The page that entry pg of sequence b names, or -1 (and the error recorded).

@@ -370,7 +370,8 @@ struct AppendArgs {
 cudaError_t launch_cache_append(const AppendArgs& a, int elem_bytes, int piece, int sms, cudaStream_t s);
 
 // cb_cache4_append (AppendArgs: k, v fp32 or bf16 tokens) and cb_cache4_read
-// (cache4.cu).  vec: rows of 16-byte pieces on both sides.
+// (cache4.cu).  vec: dims that are multiples of 8, tokens' rows of whole 16-byte
+// pieces, codes of whole words at 4-byte boundaries.
 struct Read4Args {
   void* k;
   void* v;

@@ -41,9 +41,9 @@
 // slots are filled, and neither memory nor a pipe is: eight sequences of up to
 // 131072 tokens, 8 key heads of 128, in 196 us, 0.68 of the copy rate (the bf16
 // cache's 466).  The bf16 kernels of 128 dims and 8 heads are held to 128 registers
-// and spill 4 to 60 bytes.  Three CTAs of three stages take as long as four of two (three with
-// one stage less in flight, four with fewer registers than they want).  fp8 MMAs,
-// whose e4m3 subnormals the codes are as well, run as two f16 ones after
+// and spill 4 to 60 bytes.  Three CTAs of three stages take as long as four of two
+// (three with one stage less in flight, four with fewer registers than they want).
+// fp8 MMAs, whose e4m3 subnormals the codes are as well, run as two f16 ones after
 // conversions: 249 us where f16 took 205.
 #pragma once
 
@@ -355,7 +355,7 @@ struct Decode4Math {
     // a score only where its keys are large: beyond this scale.
     if (__any_sync(~0u, thin != -1000)) {
       thin = __reduce_max_sync(~0u, thin);
-      if (lane == 0) sts_f(area + 1172, 0x1p16f / a.scale * pow2(min(-thin, 126)) * k_mul);
+      if (lane == 0) sts_f(area + 1172, 0x1p16f / a.scale * pow2(max(min(-thin, 126), -126)) * k_mul);
       __syncwarp();
     }
 #pragma unroll
@@ -720,8 +720,8 @@ struct Share {
 // A share from the definition, in fp32 on the CUDA cores, for what the products of f16 weights cannot hold: a token per
 // lane for the scores, four dims per lane for the values, two heads at a time.  Results as Decode4Math::store() leaves
 // them.  Weights are taken times 2^-32, so that sums of the largest values stay finite.  Where every run is done again the
-// cases below take 9 and 14 times as long (582 us, 2833; four heads at a time 432 and 2044, but the main loop, which the
-// compiler then treats otherwise, 204 us, not 198.7).
+// file head's ragged and long sequences take 9 and 14 times as long (582 and 2833 us; four heads at a time 432 and 2044,
+// but the long ones' main loop, which the compiler then treats otherwise, 204, not 198.7).
 template <typename T>
 __device__ __noinline__ void redo(const DecodeArgs& a, const Share w, float* res, int ld, float* ms, float* ls) {
   constexpr int kAtOnce = 2, kAhead = 8;  // heads; tokens whose values are in flight

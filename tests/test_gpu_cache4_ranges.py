@@ -158,3 +158,24 @@ def test_queries_small_where_keys_are_large(gpu, power, wide, dtype):
     got = run(q, cache, ints([n, n]), scale=0.3)
     sync_check()
     ref.check(got, ref.decode(q, k, v, place, [n, n], 0.3), v, dtype)
+
+
+@DTYPES
+@WAYS
+@pytest.mark.parametrize("top", [127, -100], ids=lambda e: f"2^{e}")
+def test_small_groups_of_queries_at_the_ends_of_the_range(gpu, top, wide, dtype):
+    """Queries up to 2^127, or of 2^-100, with a group far below them and keys that bring both to ordinary scores."""
+    n, D = 100, 64
+    x, y = (ref.randn(2, n, 1, D, seed=s, dtype=F32, device="cuda").clamp(-3, 3) for s in (11, 12))
+    q = ref.randn(2, 5, D, seed=13, dtype=F32, device="cuda").clamp(-0.99, 0.99)
+    low = max(top - 60, -125)
+    x[..., :32] *= 2.0 ** min(-top, 120) if top < 0 else 2.0 ** -63
+    x[..., :32] *= 1.0 if top < 0 else 2.0 ** -64
+    x[..., 32:] *= 2.0 ** -low
+    q = torch.cat([q[..., :32] * 2.0 ** (top - 20) * 2.0 ** 20, q[..., 32:] * 2.0 ** low], -1)
+    x, y, q = x.to(BF16), y.to(BF16), q.to(dtype)
+    cache, k, v, place = stored(x, y, 1, wide)
+    got = run(q, cache, ints([n, n]), scale=0.3)
+    sync_check()
+    assert torch.isfinite(q).all() and (q[..., :32].abs().amax() > 2.0 ** (top - 1))
+    ref.check(got, ref.decode(q, k, v, place, [n, n], 0.3), v, dtype)
